@@ -138,7 +138,7 @@ def _codes(x, group):
     v = x.reshape(*x.shape[:-1], x.shape[-1] // group, group)
     lo = v.amin(-1, keepdim=True) + 0.0
     hi = v.amax(-1, keepdim=True) + 0.0
-    s = (hi - lo) / 15.0
+    s = (hi - lo) / torch.full_like(hi, 15.0)  # a quotient: by a plain number it may become a product
     s = torch.where(s < torch.finfo(torch.float32).tiny, torch.ones_like(s), s)
     q = torch.round((v - lo) * (1.0 / s)).clamp(0, 15).to(torch.int32)
     return q.reshape(x.shape), torch.cat([s, -lo / s], -1)
