@@ -379,6 +379,164 @@ GQ4_API gq4_status gq4_sequence_launches(const gq4_call *calls, int n_calls, int
  * other host threads) race: the caller must order them. */
 GQ4_API gq4_status gq4_run_sequence_static(const gq4_call *calls, int n_calls, cudaStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Between the QKV product and the output projection: per-head norm and
+ * rotation, a paged key/value cache held in 4 bits, and the attention that
+ * reads it.  The pages run these steps as executor kernels of their own
+ * (DualRMSNormRoPE, KVCacheAppend, paged KV with block tables, Attention);
+ * no body is shown and the pages keep the cache in f32 or f16, so the
+ * definitions below are this library's.
+ *
+ * A step's tokens are rows t of q [T][q_heads][head_dim] and k, v
+ * [T][kv_heads][head_dim], f32.  Rows may be columns of a wider matrix (the
+ * fused QKV product): ld is the distance between rows in floats, a multiple
+ * of 4, at least heads * head_dim; row bases are 16-byte aligned.  Head
+ * counts are at most GQ4_MAX_HEADS.
+ * ------------------------------------------------------------------------ */
+#define GQ4_MAX_HEADS 1024
+#define GQ4_MAX_HEAD_DIM 512
+
+/* RMSNorm of every head (optional) and the rotation by position, one pass:
+ *   y = x * 1/sqrt(sum_d x_d^2 / head_dim + eps) * gain    (gain NULL: y = x)
+ *   a_i = positions[t] * inv_freq[i], i < rot_dim / 2
+ *   (y_a, y_b) -> (y_a cos a_i - y_b sin a_i, y_b cos a_i + y_a sin a_i)
+ * with (a, b) = (i, i + rot_dim/2), or (2i, 2i + 1) when interleaved; the
+ * values from rot_dim on are not rotated.  The angle is formed and reduced
+ * in 64 bits (positions up to 2^31 - 1 lose nothing), everything else is
+ * f32.  head_dim and rot_dim are multiples of 8, 0 <= rot_dim <= head_dim <=
+ * GQ4_MAX_HEAD_DIM; positions and inv_freq may be NULL when rot_dim is 0.
+ * Either side may be absent (its head count 0).  q_out may be q itself with
+ * the same ld (in place), likewise k_out; other overlaps are rejected.
+ * T = 0 is a no-op.  A NaN or an infinity makes its own head's row NaN where
+ * the formula does. */
+typedef struct gq4_rope {
+    const float *q_gain;     /* [head_dim] or NULL: q is not normalised */
+    const float *k_gain;     /* [head_dim] or NULL */
+    float eps;               /* e.g. 1e-6f; must be >= 0 */
+    int rot_dim;
+    int interleaved;         /* 0 or 1 */
+    const float *inv_freq;   /* [rot_dim / 2], 4-byte aligned */
+} gq4_rope;
+
+GQ4_API gq4_status gq4_head_norm_rope(int T, int q_heads, int kv_heads, int head_dim,
+                                      const gq4_rope *rope, const int32_t *positions,
+                                      const float *q, int ldq, const float *k, int ldk,
+                                      float *q_out, int ldq_out, float *k_out, int ldk_out,
+                                      cudaStream_t stream);
+
+/* The paged cache.  A page holds page_size tokens of every kv head; slot
+ * number s is row s % page_size of page s / page_size.  Per row, kv head and
+ * group of group_size values along head_dim: 4-bit codes with an f32 scale
+ * and zero, value = (code - zero) * scale, as the weights.  Page-and-head
+ * tiles are contiguous:
+ *   Kq, Vq      u32 [n_pages][kv_heads][page_size][head_dim / 8]
+ *   K_sz, V_sz  f32 [n_pages][kv_heads][page_size][head_dim / group_size][2]
+ *               (scale, zero)
+ * The order of the codes within a row suits the attention's matrix
+ * instructions; with J = head_dim / 32 and u = d / 32,
+ *   key code d:   nibble d % 8 of word (d % 32 / 8) * J + u,
+ *   value code d: nibble d % 4 of 16-bit half (d % 32 / 4) * J + u (half h
+ *                 is the low half of word h / 2 when h is even).
+ * head_dim is 64, 96, 128 or 256 (other multiples of 32:
+ * GQ4_ERR_UNSUPPORTED), group_size a multiple of 32 that divides it,
+ * page_size 16, 32, 64, 128 or 256, n_pages * page_size < 2^31.  All four
+ * arrays are 16-byte aligned. */
+typedef struct gq4_kv_cache {
+    int n_pages, page_size, kv_heads, head_dim, group_size;
+    uint32_t *Kq;
+    float *K_sz;
+    uint32_t *Vq;
+    float *V_sz;
+} gq4_kv_cache;
+
+/* Quantise rows k[t], v[t] into slot slots[t] (int32 [T] on the device), by
+ * gq4_quantize's rule per group (a group with a non-finite value or range
+ * gets codes 0 and a NaN scale and zero and sets device error bit 3).  A
+ * negative slot is skipped; one outside the pool is skipped and sets bit 6.
+ * Slots must be distinct: of rows that share one, the row's groups may come
+ * from either.  T = 0 is a no-op. */
+GQ4_API gq4_status gq4_kv_append(int T, const gq4_kv_cache *cache, const float *k, int ldk,
+                                 const float *v, int ldv, const int32_t *slots,
+                                 cudaStream_t stream);
+
+/* Read rows back: k_out[t], v_out[t] (f32 [T][kv_heads][head_dim], dense) =
+ * fl(fl(code - zero) * scale) of slot slots[t].  A negative slot leaves its
+ * rows as they were; one outside the pool gives NaN rows and sets bit 6. */
+GQ4_API gq4_status gq4_kv_gather(int T, const gq4_kv_cache *cache, const int32_t *slots,
+                                 float *k_out, float *v_out, cudaStream_t stream);
+
+/* A step's book-keeping, on the device, from the requests' lengths.  Request
+ * b has past_lens[b] tokens in the cache, in the first
+ * ceil(past / page_size) pages of page_table row b, and gets new_lens[b]
+ * more.  The pages it lacks come off the end of the free list in request
+ * order: the j-th page granted in the step is
+ * free_pages[free_count - 1 - j].  Written:
+ *   page_table[b][...]  the granted pages, behind the ones it had
+ *   seq_lens[b]         past + new
+ *   query_start[b]      the requests' first token rows (query_start[B]: total)
+ *   positions[t], slots[t]  of each new token; rows from query_start[B] to T
+ *                       get position 0 and slot -1
+ *   *free_count_out     the pages left
+ * All counts are int32 and 4-byte aligned; page_table is [B][max_pages].
+ * seq_lens may be past_lens, and free_count_out free_count, themselves (a
+ * captured step then advances its own state); no other output may overlap
+ * anything.  Free pages returned by finished requests are the caller's to
+ * push: write them at free_pages[free_count...] and raise the count.
+ *
+ * A request is refused -- seq_lens[b] = past, its rows in T get position 0
+ * and slot -1, device error bit 7 is set, no page is granted --
+ * when a length is negative (taken as 0), when past + new passes
+ * max_pages * page_size, when its rows end past T (query_start is then cut
+ * at T), or when the free list runs out: from the first request on whose
+ * pages it cannot cover, no request that needs a page gets one.
+ * free_count is cut to 0..n_free.  1 <= B <= GQ4_MAX_REQUESTS; T may be 0. */
+#define GQ4_MAX_REQUESTS 65536
+GQ4_API gq4_status gq4_kv_plan(int B, int T, int page_size, int max_pages, int n_free,
+                               const int32_t *past_lens, const int32_t *new_lens,
+                               int32_t *page_table, const int32_t *free_pages,
+                               const int32_t *free_count, int32_t *free_count_out,
+                               int32_t *seq_lens, int32_t *query_start, int32_t *positions,
+                               int32_t *slots, cudaStream_t stream);
+
+/* Attention over the cache: prompts, chunks of prompts, drafted tokens and
+ * single tokens alike.  Request b's queries are rows query_start[b] ..
+ * query_start[b+1] - 1 of q, n of them; its seq_lens[b] keys (its own new
+ * ones included) are in the pages of page_table row b (int32
+ * [B][max_pages]).  Its j-th query stands at position p = seq_len - n + j
+ * and sees the keys at positions max(0, p + 1 - window) .. p (window 0: from
+ * 0).  With w_t = scale * sum_d q_d k_t,d over the query head's kv head
+ * (q head h reads kv head h / (q_heads / kv_heads)),
+ *   out[row][h][d] = sum_t exp(w_t - max w) v_t,d / sum_t exp(w_t - max w).
+ * A query that sees no key (seq_len < n) gives a row of zeros.  Rows of no
+ * request are left as they were.  Pages that hold no visible key are not
+ * looked at.
+ *
+ * max_query and max_len bound the requests' query counts and lengths (they
+ * size the launch; max_len 0: max_pages * page_size).  A request beyond
+ * them, or whose rows are not within T, or with a page id outside the pool
+ * sets device error bit 8: rows of its queries inside T are NaN (with a bad
+ * page: those that see it), nothing outside the pool or T is touched.
+ *
+ * Held to |error| <= about 1e-6 of the values' size: q and the weights are
+ * split into two fp16 pieces each (22 bits), the codes are exact, sums are
+ * f32 (prompts: the dequantised keys and values are two fp16 pieces too).
+ * How a request's keys are split over the GPU depends on the other requests
+ * and on max_len, so their change may change last bits; the same inputs give
+ * the same bits.
+ *
+ * workspace: at least gq4_kv_attention_workspace_bytes() bytes of device
+ * memory, 256-byte aligned, no argument's; contents need not be set and
+ * nothing is kept in it between calls.  Calls that may overlap on the GPU
+ * need one each.  out rows are ld_out floats apart, 16-byte aligned. */
+GQ4_API size_t gq4_kv_attention_workspace_bytes(int T, int q_heads, int kv_heads, int head_dim);
+
+GQ4_API gq4_status gq4_kv_attention(int B, int T, int q_heads, int max_pages, int max_query,
+                                    int max_len, const gq4_kv_cache *cache, const float *q,
+                                    int ldq, const int32_t *query_start, const int32_t *seq_lens,
+                                    const int32_t *page_table, float scale, int window,
+                                    float *out, int ld_out, void *workspace,
+                                    size_t workspace_bytes, cudaStream_t stream);
+
 /* Integer unpack test kernel: q[n*K + k] = q(n,k) as u8 [N][K].
  * Uses the same in-register extraction as the matvec kernels.
  * Requires K % 32 == 0. */
@@ -399,10 +557,14 @@ GQ4_API gq4_status gq4_dequant(int K, int N, int group_size, const uint32_t *Bq,
  * waiting for a copy or for the other CTAs at a call boundary (every wait
  * inside the kernels is bounded in time, so a broken copy cannot hang the
  * GPU; the outputs of that call are then invalid), bit 3 when gq4_quantize
- * met a group with a non-finite value or range, bit 4 when gq4_embedding met
+ * or gq4_kv_append met a group with a non-finite value or range, bit 4 when gq4_embedding met
  * an id outside its table, bit 5 when the 2..4-lane kernel gave up waiting
  * for a copy, its scale scratch or its warps' partial sums; bit 1 also
- * covers the GEMM kernel of gq4_gemm.  Copies the word to
+ * covers the GEMM kernel of gq4_gemm; bit 6 when gq4_kv_append or
+ * gq4_kv_gather met a slot outside the pool, bit 7 when gq4_kv_plan refused
+ * a request, bit 8 when gq4_kv_attention met a request outside its bounds or
+ * a page outside the pool, bit 9 when its prompt kernel gave up waiting for
+ * its own copies or MMAs.  Copies the word to
  * *bits (synchronous, device-wide) and clears it when clear != 0.  Not for
  * the hot path: a diagnostic to call after a suspicious result. */
 GQ4_API gq4_status gq4_device_error(unsigned int *bits, int clear);

@@ -12,58 +12,17 @@
 #include <vector>
 
 #include "gq4.h"
+#include "gq4_checks.h"
 #include "gq4_internal.h"
 
 namespace {
 
+using gq4::aligned;
+using gq4::overlap;
+using gq4::range_of;
+using gq4::RangeSet;
+
 constexpr int kMaxK = 1 << 24;  // keeps 32-code chunk indices below 2^20
-
-struct Range {
-    uintptr_t lo, hi;  // [lo, hi)
-};
-
-Range range_of(const void *p, size_t bytes)
-{
-    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-    return Range{lo, lo + bytes};
-}
-
-bool overlap(Range a, Range b)
-{
-    if (a.lo == a.hi || b.lo == b.hi) return false;
-    return a.lo < b.hi && b.lo < a.hi;
-}
-
-bool aligned(const void *p, uintptr_t a)
-{
-    return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
-}
-
-// Collects the byte ranges of a call and checks them.
-struct RangeSet {
-    Range in[16];
-    int n_in = 0;
-    Range out[8];
-    int n_out = 0;
-    void input(const void *p, size_t bytes)
-    {
-        if (p && bytes) in[n_in++] = range_of(p, bytes);
-    }
-    void output(const void *p, size_t bytes)
-    {
-        if (p && bytes) out[n_out++] = range_of(p, bytes);
-    }
-    bool disjoint() const
-    {
-        for (int i = 0; i < n_out; ++i) {
-            for (int j = 0; j < n_in; ++j)
-                if (overlap(out[i], in[j])) return false;
-            for (int j = i + 1; j < n_out; ++j)
-                if (overlap(out[i], out[j])) return false;
-        }
-        return true;
-    }
-};
 
 gq4_status check_shape(int M, int K, int N, int gs)
 {
@@ -119,12 +78,6 @@ gq4_status check_output(const float *out, size_t elems, RangeSet &rs)
     rs.output(out, elems * sizeof(float));
     return GQ4_OK;
 }
-
-#define GQ4_TRY(expr)                       \
-    do {                                    \
-        const gq4_status st_ = (expr);      \
-        if (st_ != GQ4_OK) return st_;      \
-    } while (0)
 
 gq4_status run(const gq4::Call &call, cudaStream_t stream)
 {
@@ -673,7 +626,10 @@ gq4_status gq4_device_error(unsigned int *bits, int clear)
     unsigned int f = 0, l = 0;
     if (gq4::read_gemm_device_error(&f, clear != 0) != cudaSuccess) return GQ4_ERR_CUDA;
     if (gq4::read_lanes_device_error(&l, clear != 0) != cudaSuccess) return GQ4_ERR_CUDA;
-    *bits = a | b | c | d | e | f | l;
+    unsigned int k = 0, t = 0;
+    if (gq4::read_kv_device_error(&k, clear != 0) != cudaSuccess) return GQ4_ERR_CUDA;
+    if (gq4::read_attn_device_error(&t, clear != 0) != cudaSuccess) return GQ4_ERR_CUDA;
+    *bits = a | b | c | d | e | f | l | k | t;
     return GQ4_OK;
 }
 

@@ -56,6 +56,22 @@ class Call(ctypes.Structure):
                 ("A", _vp), ("Bq", _vp * 2), ("scales", _vp * 2), ("zeros", _vp * 2),
                 ("out", _vp * 4), ("has_norm", _i), ("norm", Norm)]
 
+
+class Rope(ctypes.Structure):
+    """``gq4_rope``: the per-head norm and the rotation."""
+    _fields_ = [("q_gain", _vp), ("k_gain", _vp), ("eps", ctypes.c_float), ("rot_dim", _i),
+                ("interleaved", _i), ("inv_freq", _vp)]
+
+
+class KVCache(ctypes.Structure):
+    """``gq4_kv_cache``: the paged 4-bit key/value cache."""
+    _fields_ = [("n_pages", _i), ("page_size", _i), ("kv_heads", _i), ("head_dim", _i),
+                ("group_size", _i), ("Kq", _vp), ("K_sz", _vp), ("Vq", _vp), ("V_sz", _vp)]
+
+
+_RopeP = ctypes.POINTER(Rope)
+_CacheP = ctypes.POINTER(KVCache)
+
 _SIGS = {
     "gq4_matvec": [_i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp],
     "gq4_quad_matvec": [_i, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
@@ -73,6 +89,12 @@ _SIGS = {
     "gq4_quantize": [_i, _i, _i, _vp, _vp, _vp, _vp, _vp],
     "gq4_from_mlx": [_i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp],
     "gq4_embedding": [_i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp],
+    "gq4_head_norm_rope": [_i, _i, _i, _i, _RopeP, _vp, _vp, _i, _vp, _i, _vp, _i, _vp, _i, _vp],
+    "gq4_kv_append": [_i, _CacheP, _vp, _i, _vp, _i, _vp, _vp],
+    "gq4_kv_gather": [_i, _CacheP, _vp, _vp, _vp, _vp],
+    "gq4_kv_plan": [_i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp],
+    "gq4_kv_attention": [_i, _i, _i, _i, _i, _i, _CacheP, _vp, _i, _vp, _vp, _vp, ctypes.c_float, _i,
+                         _vp, _i, _vp, ctypes.c_size_t, _vp],
     "gq4_unpack": [_i, _i, _vp, _vp, _vp],
     "gq4_dequant": [_i, _i, _i, _vp, _vp, _vp, _vp, _vp],
 }
@@ -90,9 +112,12 @@ lib.gq4_sequence_workspace_bytes.restype = ctypes.c_size_t
 lib.gq4_sequence_workspace_bytes.argtypes = []
 lib.gq4_gemm_workspace_bytes.restype = ctypes.c_size_t
 lib.gq4_gemm_workspace_bytes.argtypes = [_i, _i]
+lib.gq4_kv_attention_workspace_bytes.restype = ctypes.c_size_t
+lib.gq4_kv_attention_workspace_bytes.argtypes = [_i, _i, _i, _i]
 
 EXPORTED = list(_SIGS) + ["gq4_status_string", "gq4_version", "gq4_device_error",
-                          "gq4_sequence_workspace_bytes", "gq4_gemm_workspace_bytes"]
+                          "gq4_sequence_workspace_bytes", "gq4_gemm_workspace_bytes",
+                          "gq4_kv_attention_workspace_bytes"]
 
 
 class GQ4Error(RuntimeError):
@@ -366,6 +391,222 @@ def embedding(ids, Bq, scales, zeros, group_size, out=None, stream=None):
 
 
 # ---------------------------------------------------------------------------
+# Between the QKV product and the output projection
+# ---------------------------------------------------------------------------
+
+_I32 = (torch.int32,)
+
+
+def _call(fn, name, t, stream, *args):
+    """fn(*args, stream) on t's device, on the given stream or that device's current one."""
+    if t.device.index != torch.cuda.current_device():
+        with torch.cuda.device(t.device):
+            return _call(fn, name, t, stream, *args)
+    _check(fn(*args, _stream(stream)), name)
+
+
+def _same_device(first, *others):
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors on {first.device} and {t.device}")
+
+
+def _rows(t, name, heads_dim=None):
+    """[T, heads, D] with dense rows (any row distance): (T, heads, D, row distance)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (no CPU path exists)")
+    if t.dtype != torch.float32:
+        raise TypeError(f"{name}: dtype {t.dtype} is not torch.float32")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [T, heads, head_dim]")
+    T, H, D = t.shape
+    if heads_dim is not None and (T, H, D) != heads_dim:
+        raise ValueError(f"{name}: shape {(T, H, D)} != {heads_dim}")
+    ld, sh, sd = t.stride()
+    if (D > 1 and sd != 1) or (H > 1 and sh != D):
+        raise ValueError(f"{name}: the heads of a row must be dense")
+    return T, H, D, (H * D if T <= 1 else ld)
+
+
+def head_norm_rope(q, k, positions, inv_freq, q_gain=None, k_gain=None, eps=1e-6, interleaved=False,
+                   q_out=None, k_out=None, stream=None):
+    """(q, k) with every head normalised (where a gain is given) and rotated by position
+    (gq4_head_norm_rope).  q [T, heads, D] and k [T, kv_heads, D], either may be None; rows may be
+    columns of a wider matrix.  inv_freq f32 [rot_dim / 2], or None for no rotation.  q_out / k_out
+    may be q / k themselves."""
+    if q is None and k is None:
+        raise ValueError("q or k must be given")
+    outs, side = [], []
+    for x, y, name in ((q, q_out, "q"), (k, k_out, "k")):
+        if x is None:
+            if y is not None:
+                raise ValueError(f"{name}_out needs {name}")
+            outs.append(None)
+            side.append((0, 0, 0, 0, 0, None, None))
+            continue
+        T, H, D, ld = _rows(x, name)
+        if y is None:
+            y = torch.empty((T, H, D), dtype=torch.float32, device=x.device)
+        ldy = _rows(y, name + "_out", (T, H, D))[3]
+        outs.append(y)
+        side.append((T, H, D, ld, ldy, x, y))
+    (T, QH, D, ldq, ldqo, _, _), (TK, KH, DK, ldk, ldko, _, _) = side
+    if q is None:
+        T, D = TK, DK
+    elif k is not None and (TK, DK) != (T, D):
+        raise ValueError(f"k: {TK} rows of {DK} != {T} rows of {D}")
+    first = q if q is not None else k
+    rot = 0
+    if inv_freq is not None:
+        _need(inv_freq, "inv_freq", _F32)
+        _need(positions, "positions", _I32, (T,))
+        rot = 2 * inv_freq.numel()
+    for g, name, x in ((q_gain, "q_gain", q), (k_gain, "k_gain", k)):
+        if g is not None:
+            _need(g, name, _F32, (D,))
+            if x is None:
+                raise ValueError(f"{name} needs {name[0]}")
+    _same_device(first, k, q_out, k_out, positions, inv_freq, q_gain, k_gain)
+    desc = Rope(_ptr(q_gain), _ptr(k_gain), float(eps), rot, int(bool(interleaved)), _ptr(inv_freq))
+    _call(lib.gq4_head_norm_rope, "gq4_head_norm_rope", first, stream, T, QH, KH, D, ctypes.byref(desc),
+          _ptr(positions), _ptr(q), ldq, _ptr(k), ldk, _ptr(outs[0]), ldqo, _ptr(outs[1]), ldko)
+    return outs[0], outs[1]
+
+
+def kv_cache(n_pages, kv_heads, page_size, head_dim, group_size, device=None):
+    """An empty cache: (Kq, K_sz, Vq, V_sz), the tensors the kv_* calls take (codes int32
+    [n_pages, kv_heads, page_size, head_dim/8], scale and zero f32 [..., head_dim/group_size, 2])."""
+    if group_size <= 0 or head_dim % group_size != 0 or head_dim % 8 != 0:
+        raise ValueError("head_dim must be a multiple of 8 and of group_size")
+    w, s = (n_pages, kv_heads, page_size, head_dim // 8), (n_pages, kv_heads, page_size, head_dim // group_size, 2)
+    device = device or "cuda"
+    return tuple(torch.zeros(x, dtype=d, device=device)
+                 for x, d in ((w, torch.int32), (s, torch.float32), (w, torch.int32), (s, torch.float32)))
+
+
+def _cache(Kq, K_sz, Vq, V_sz, group_size):
+    _need(Kq, "Kq", _WORDS)
+    if Kq.dim() != 4:
+        raise ValueError("Kq must be [n_pages, kv_heads, page_size, head_dim/8]")
+    P, H, S, W = Kq.shape
+    if group_size <= 0 or (8 * W) % group_size != 0:
+        raise ValueError("head_dim must be a multiple of group_size")
+    sz = (P, H, S, 8 * W // group_size, 2)
+    _need(K_sz, "K_sz", _F32, sz)
+    _need(Vq, "Vq", _WORDS, (P, H, S, W))
+    _need(V_sz, "V_sz", _F32, sz)
+    _same_device(Kq, K_sz, Vq, V_sz)
+    return KVCache(P, S, H, 8 * W, group_size, Kq.data_ptr(), K_sz.data_ptr(), Vq.data_ptr(), V_sz.data_ptr())
+
+
+def kv_append(k, v, slots, Kq, K_sz, Vq, V_sz, group_size, stream=None):
+    """Quantise rows k, v [T, kv_heads, D] into the cache at slots int32 [T] (gq4_kv_append;
+    negative slots are skipped)."""
+    c = _cache(Kq, K_sz, Vq, V_sz, group_size)
+    T, _, _, ldk = _rows(k, "k")
+    shape = (T, c.kv_heads, c.head_dim)
+    ldk, ldv = _rows(k, "k", shape)[3], _rows(v, "v", shape)[3]
+    _need(slots, "slots", _I32, (T,))
+    _same_device(Kq, k, v, slots)
+    _call(lib.gq4_kv_append, "gq4_kv_append", Kq, stream, T, ctypes.byref(c), _ptr(k), ldk, _ptr(v), ldv,
+          _ptr(slots))
+
+
+def kv_gather(slots, Kq, K_sz, Vq, V_sz, group_size, k_out=None, v_out=None, stream=None):
+    """(k, v) f32 [T, kv_heads, D] of the cache rows at slots (gq4_kv_gather; rows of negative slots
+    are left as they were, so pass k_out and v_out where there are some)."""
+    c = _cache(Kq, K_sz, Vq, V_sz, group_size)
+    _need(slots, "slots", _I32)
+    if slots.dim() != 1:
+        raise ValueError("slots must be [T]")
+    shape = (slots.shape[0], c.kv_heads, c.head_dim)
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=torch.float32, device=Kq.device)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=torch.float32, device=Kq.device)
+    _need(k_out, "k_out", _F32, shape)
+    _need(v_out, "v_out", _F32, shape)
+    _same_device(Kq, slots, k_out, v_out)
+    _call(lib.gq4_kv_gather, "gq4_kv_gather", Kq, stream, shape[0], ctypes.byref(c), _ptr(slots), _ptr(k_out),
+          _ptr(v_out))
+    return k_out, v_out
+
+
+def kv_plan(past_lens, new_lens, page_table, free_pages, free_count, n_tokens, page_size, seq_lens=None,
+            query_start=None, positions=None, slots=None, free_count_out=None, stream=None):
+    """A step's pages, positions and slots from the requests' lengths (gq4_kv_plan); page_table int32
+    [B, max_pages] is extended in place.  Returns (seq_lens, query_start, positions, slots,
+    free_count_out); pass seq_lens=past_lens and free_count_out=free_count to advance them in place."""
+    _need(past_lens, "past_lens", _I32)
+    if past_lens.dim() != 1:
+        raise ValueError("past_lens must be [B]")
+    B = past_lens.shape[0]
+    _need(new_lens, "new_lens", _I32, (B,))
+    _need(page_table, "page_table", _I32)
+    if page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError("page_table must be [B, max_pages]")
+    _need(free_pages, "free_pages", _I32)
+    _need(free_count, "free_count", _I32)
+    if free_count.numel() != 1:
+        raise ValueError("free_count must hold one number")
+
+    def out(t, name, n):
+        if t is None:
+            return torch.empty(n, dtype=torch.int32, device=past_lens.device)
+        _need(t, name, _I32)
+        if t.numel() != n:
+            raise ValueError(f"{name}: {t.numel()} values != {n}")
+        return t
+
+    seq_lens, query_start = out(seq_lens, "seq_lens", B), out(query_start, "query_start", B + 1)
+    positions, slots = out(positions, "positions", n_tokens), out(slots, "slots", n_tokens)
+    free_count_out = out(free_count_out, "free_count_out", 1)
+    _same_device(past_lens, new_lens, page_table, free_pages, free_count, seq_lens, query_start, positions, slots,
+                 free_count_out)
+    _call(lib.gq4_kv_plan, "gq4_kv_plan", past_lens, stream, B, n_tokens, page_size, page_table.shape[1],
+          free_pages.numel(), _ptr(past_lens), _ptr(new_lens), _ptr(page_table), _ptr(free_pages),
+          _ptr(free_count), _ptr(free_count_out), _ptr(seq_lens), _ptr(query_start), _ptr(positions), _ptr(slots))
+    return seq_lens, query_start, positions, slots, free_count_out
+
+
+def kv_attention_workspace_bytes(T, heads, kv_heads, head_dim) -> int:
+    return int(lib.gq4_kv_attention_workspace_bytes(T, heads, kv_heads, head_dim))
+
+
+def kv_attention(q, query_start, seq_lens, page_table, Kq, K_sz, Vq, V_sz, group_size, scale, max_query,
+                 max_len=0, window=0, out=None, workspace=None, stream=None):
+    """Causal attention of q [T, heads, D] over the cache (gq4_kv_attention): request b's queries are
+    rows query_start[b]..query_start[b+1], its seq_lens[b] keys are in the pages of page_table row b.
+    ``workspace``: a CUDA tensor of at least kv_attention_workspace_bytes(T, heads, kv_heads, D) bytes
+    (allocated when None).  ``out`` rows of no request are left as they were."""
+    c = _cache(Kq, K_sz, Vq, V_sz, group_size)
+    T, H, D, ldq = _rows(q, "q")
+    if D != c.head_dim:
+        raise ValueError(f"q: head_dim {D} != {c.head_dim}")
+    _need(seq_lens, "seq_lens", _I32)
+    B = seq_lens.numel()
+    _need(query_start, "query_start", _I32, (B + 1,))
+    _need(page_table, "page_table", _I32)
+    if page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError("page_table must be [B, max_pages]")
+    if out is None:
+        out = torch.empty((T, H, D), dtype=torch.float32, device=q.device)
+    ldo = _rows(out, "out", (T, H, D))[3]
+    if workspace is None:
+        workspace = torch.empty(kv_attention_workspace_bytes(T, H, c.kv_heads, D), dtype=torch.uint8,
+                                device=q.device)
+    elif not (isinstance(workspace, torch.Tensor) and workspace.is_cuda and workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    _same_device(Kq, q, query_start, seq_lens, page_table, out, workspace)
+    _call(lib.gq4_kv_attention, "gq4_kv_attention", Kq, stream, B, T, H, page_table.shape[1], max_query, max_len,
+          ctypes.byref(c), _ptr(q), ldq, _ptr(query_start), _ptr(seq_lens), _ptr(page_table), float(scale), window,
+          _ptr(out), ldo, _ptr(workspace), workspace.numel() * workspace.element_size())
+    return out
+
+
+# ---------------------------------------------------------------------------
 # Call sequences (one lane)
 # ---------------------------------------------------------------------------
 
@@ -499,8 +740,10 @@ def dequant(Bq, scales, zeros, K, group_size, W=None, stream=None):
 def device_error(clear: bool = True) -> int:
     """The library's sticky device error bits (bit 0: the one-lane kernel, bit 1: the
     tensor-core kernel, bit 2: a call sequence gave up a bounded wait; bit 3: the
-    quantizer met a non-finite group; bit 4: the embedding gather met an id outside
-    its table)."""
+    quantizer or the cache's writer met a non-finite group; bit 4: the embedding
+    gather met an id outside its table; bit 6: a cache slot outside the pool; bit 7:
+    kv_plan refused a request; bit 8: kv_attention met a request outside its bounds or
+    a page outside the pool; bit 9: its prompt kernel gave up a bounded wait)."""
     bits = ctypes.c_uint(0)
     _check(lib.gq4_device_error(ctypes.byref(bits), int(clear)), "gq4_device_error")
     return int(bits.value)
