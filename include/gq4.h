@@ -489,7 +489,8 @@ GQ4_API gq4_status gq4_kv_gather(int T, const gq4_kv_cache *cache, const int32_t
  * max_pages * page_size, when its rows end past T (query_start is then cut
  * at T), or when the free list runs out: from the first request on whose
  * pages it cannot cover, no request that needs a page gets one.
- * free_count is cut to 0..n_free.  1 <= B <= GQ4_MAX_REQUESTS; T may be 0. */
+ * free_count is cut to 0..n_free.  1 <= B <= GQ4_MAX_REQUESTS; T may be 0;
+ * max_pages * page_size is at most 2^30 (as in gq4_kv_attention). */
 #define GQ4_MAX_REQUESTS 65536
 GQ4_API gq4_status gq4_kv_plan(int B, int T, int page_size, int max_pages, int n_free,
                                const int32_t *past_lens, const int32_t *new_lens,

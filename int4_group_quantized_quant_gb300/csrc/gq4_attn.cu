@@ -1,94 +1,914 @@
 // gq4_attn.cu -- causal attention over the paged 4-bit key/value cache
-// (gq4_kv_attention).
+// (gq4_kv_attention), for single tokens and a few rows: the cache is read
+// once and the matrix instructions take its codes as they are.
 //
-// One warp per query row and head, running softmax over the keys one by one.
+// Mathematics.  A query row and the codes of its kv head:
+//   w_t = scale * sum_g s_tg (sum_{d in g} q_d c_td - z_tg sum_{d in g} q_d)
+//   out = sum_t p_t s_tg (c_td - 8) - sum_t p_t s_tg (z_tg - 8),  p_t = 2^(w_t log2 e - m)
+// The codes c enter the warp-level MMA (m16n8k16, f16 inputs, f32 sums) as
+// exact fp16 numbers; the other factor -- q, or p s -- is written as a sum of
+// two fp16 pieces (11 bits each, 2^-23 relative), which take two neighbouring
+// columns of the instruction, so that one thread holds both sums.  The keys
+// (or, in the second product, the head's values of d) are the 16 rows of the
+// instruction and the query rows its 8 columns: 4 rows of two pieces each, a
+// full instruction for the four query heads of a kv head, and one decode of
+// a code serves all of them.
+//   Keys: a word's nibbles i and i+4 are masked in place, an fp16 pair
+// c 2^-24 (c 2^-20 for odd i: q is pre-scaled by 1/16 there).
+//   Values: nibbles of two tokens are paired by a byte permute, OR-ed with
+// 1024 and shifted to c - 8 by one exact fp16 operation.  Without the 8 the
+// sums would carry the codes' mean, several times the result, and its
+// rounding.
+//   Sums in the tensor core are cut, not rounded: the second product runs
+// over 32 keys and is then added to the f32 accumulators.
+//   The running maximum m moves only when a weight passes 2^4 of it (a vote
+// per 32 keys), so that accumulators are rescaled rarely; the values'
+// scales likewise share a power of two 2^E, which keeps p s inside fp16.
+//
+// Split.  A CTA step is 256 keys of one (request, kv head, block of rows),
+// 32 for each of 8 warps; the list of all steps is cut into equal ranges, one
+// per CTA, whatever the requests' lengths.  A unit cut by a range boundary
+// leaves partial sums (m, l, sum) in the workspace, which a second kernel
+// joins in order: no atomics, the same bits every time.  The cut is computed
+// on the device from the lengths, so a captured launch follows them.
+//
+// Copies.  Each warp keeps its own ring of 32-key stages filled by 16-byte
+// cp.async, without any CTA barrier: the rows of 16 keys of one page and head
+// are contiguous.  Keys are assigned to the instruction's rows so that both
+// products read shared memory without bank conflicts (see key_of_row).
+#include <cuda_fp16.h>
+
+#include <atomic>
 #include <cstdint>
 
-#include "gq4_internal.h"
-#include "gq4_kv.cuh"
+#include "gq4_attn.cuh"
+#include "gq4_host.h"
 
 namespace gq4 {
 namespace {
 
 __device__ unsigned int g_attn_error = 0;
-constexpr unsigned int kAttnBad = 1u << 8;
+
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kStageKeys = 32;                    // per warp
+constexpr int kStepKeys = kStageKeys * kWarps;    // per CTA
+constexpr float kSlack = 4.0f;                    // log2 of how far a weight may pass the maximum
+constexpr int kPieceBits = 11;                    // p s <= 2^kSlack is held times 2^11: below 2^15
+constexpr int kMaxGrid = 512;                    // CTAs (the workspace's slots)
+
+struct SplitParams {
+    AttnCall a;
+    float *part;        // [grid][2][rows][D + 2] partial sums
+    int4 *desc;         // [grid] the cut unit that starts in this CTA
+    int grid;
+};
+
+// Key (0..15) that row i of the instruction's A operand takes.  A thread of
+// the second product reads the keys of rows 2c, 2c+1, 2c+8, 2c+9: these are
+// c, 4 + (c^3), and the same plus 8, so the four lanes of a quad read four
+// consecutive keys, and the two rows 2m, 2m+1 of one shared-memory phase of
+// the first product lie in different halves of 128 bytes (64-byte rows) or
+// in different quarters in fours (32-byte rows).
+__device__ __forceinline__ int key_of_row(int i)
+{
+    const int m = (i >> 1) & 3;
+    return (i & 8) + ((i & 1) ? 4 + (m ^ 3) : m);
+}
+
+// 16-byte piece of a row, swizzled by its key so that the second product's
+// reads (64- and 128-byte rows) meet distinct banks.
+template <int J>
+__device__ __forceinline__ int swizzle(int key)
+{
+    return J == 8 ? ((key & 3) << 1) | (key & 1) : J == 4 ? key & 2 : 0;
+}
+
+template <int J, int G>
+struct Stage {
+    static constexpr int kCodes = kStageKeys * 16 * J;    // bytes of 32 rows
+    static constexpr int kSz = kStageKeys * 8 * G;
+    static constexpr int kBytes = 2 * (kCodes + kSz);
+};
+
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
+{
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+// x as two fp16 pieces, the leading one in the low half.
+__device__ __forceinline__ uint32_t two_pieces(float x)
+{
+    const float hi = __half2float(__float2half_rn(x));
+    const __half2 r = __floats2half2_rn(x, x - hi);
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+__device__ __forceinline__ uint32_t h2_add(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+__device__ __forceinline__ uint32_t h2_fma(uint32_t a, uint32_t b, uint32_t c)
+{
+    uint32_t d;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+
+template <uint32_t MASK>
+__device__ __forceinline__ uint32_t mask_or(uint32_t x, uint32_t magic)
+{
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(x), "n"(MASK), "r"(magic));
+    return d;
+}
+
+// J consecutive words / halves of a row in shared memory.
+template <int J>
+__device__ __forceinline__ void load_words(uint32_t s, uint32_t (&w)[J])
+{
+    if constexpr (J % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < J; i += 4)
+            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
+                         : "r"(s + 4 * i));
+    } else if constexpr (J == 2) {
+        asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(s));
+    } else {
+#pragma unroll
+        for (int i = 0; i < J; ++i) asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[i]) : "r"(s + 4 * i));
+    }
+}
 
 template <int J>
-__global__ void __launch_bounds__(128) attn_rows_kernel(const __grid_constant__ AttnCall p)
+struct Halves {  // J 16-bit halves as (J + 1) / 2 registers, even ones low
+    uint32_t r[(J + 1) / 2];
+};
+
+template <int J>
+__device__ __forceinline__ Halves<J> load_halves(uint32_t s)
 {
-    const int lane = threadIdx.x & 31;
-    const int b = blockIdx.y;
-    const int h = blockIdx.x * 4 + (threadIdx.x >> 5);
-    const int D = 32 * J;
-    const int q0 = p.query_start[b], q1 = p.query_start[b + 1], len = p.seq_lens[b];
-    if (q1 <= q0 || h >= p.heads) return;
-    const int lo_row = max(q0, 0), hi_row = min(q1, p.T);
-    const bool bad = q0 < 0 || q1 > p.T || q1 - q0 > p.max_query || len < 0 || len > p.max_len;
-    if (bad && lane == 0) atomicOr(&g_attn_error, kAttnBad);
-    const int n = q1 - q0, kh = h / (p.heads / p.c.kv_heads), G = D / p.c.group_size;
-    const uint32_t *Kq = p.c.Kq;
-    const uint16_t *Vh = reinterpret_cast<const uint16_t *>(p.c.Vq);
-    const float2 *Ksz = reinterpret_cast<const float2 *>(p.c.K_sz), *Vsz = reinterpret_cast<const float2 *>(p.c.V_sz);
-    for (int row = lo_row; row < hi_row; ++row) {
-        float *out = p.out + (size_t)row * p.ldo + (size_t)h * D;
-        if (bad) {
-            for (int u = 0; u < J; ++u) out[32 * u + lane] = __int_as_float(0x7fc00000);
-            continue;
-        }
-        const int last = len - n + (row - q0);
-        const int first = p.window > 0 ? max(0, last + 1 - p.window) : 0;
-        float q[J], o[J];
-        for (int u = 0; u < J; ++u) {
-            q[u] = p.q[(size_t)row * p.ldq + (size_t)h * D + 32 * u + lane] * p.scale;
-            o[u] = 0.0f;
-        }
-        float m = -INFINITY, l = 0.0f;
-        for (int t = first; t <= last; ++t) {
-            const int page = p.page_table[(size_t)b * p.max_pages + t / p.c.page_size];
-            if (page < 0 || page >= p.c.n_pages) {
-                if (lane == 0) atomicOr(&g_attn_error, kAttnBad);
-                l = __int_as_float(0x7fc00000);
-                continue;
-            }
-            const size_t r = kv_row(p.c, page, kh, t % p.c.page_size);
-            float w = 0.0f;
-            for (int u = 0; u < J; ++u) {
-                const float2 s = Ksz[r * G + 32 * u / p.c.group_size];
-                const uint32_t x = Kq[r * (D / 8) + (lane >> 3) * J + u] >> (4 * (lane & 7));
-                w += q[u] * (((float)(x & 15u) - s.y) * s.x);
-            }
-            for (int i = 16; i > 0; i >>= 1) w += __shfl_xor_sync(0xffffffffu, w, i);
-            const float m2 = fmaxf(m, w);
-            const float keep = expf(m - m2), e = expf(w - m2);
-            l = l * keep + e;
-            for (int u = 0; u < J; ++u) {
-                const float2 s = Vsz[r * G + 32 * u / p.c.group_size];
-                const uint32_t x = (uint32_t)Vh[r * (D / 4) + (lane >> 2) * J + u] >> (4 * (lane & 3));
-                o[u] = o[u] * keep + e * (((float)(x & 15u) - s.y) * s.x);
-            }
-            m = m2;
-        }
-        for (int u = 0; u < J; ++u) out[32 * u + lane] = last < first ? 0.0f : o[u] / l;
+    Halves<J> h;
+    if constexpr (J == 8) {
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(h.r[0]), "=r"(h.r[1]), "=r"(h.r[2]), "=r"(h.r[3])
+                     : "r"(s));
+    } else if constexpr (J == 4) {
+        asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(h.r[0]), "=r"(h.r[1]) : "r"(s));
+    } else if constexpr (J == 2) {
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(h.r[0]) : "r"(s));
+    } else {
+        uint16_t a[J];
+#pragma unroll
+        for (int i = 0; i < J; ++i) asm volatile("ld.shared.u16 %0, [%1];" : "=h"(a[i]) : "r"(s + 2 * i));
+#pragma unroll
+        for (int i = 0; i < (J + 1) / 2; ++i)
+            h.r[i] = a[2 * i] | (2 * i + 1 < J ? (uint32_t)a[2 * i + 1] << 16 : 0u);
     }
+    return h;
+}
+
+__device__ __forceinline__ float2 lds_f2(uint32_t s)
+{
+    float2 v;
+    asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(s));
+    return v;
+}
+
+// A request's work: row blocks and key steps.
+struct Work {
+    int step0, steps;   // of kStepKeys keys
+    int blocks;         // row blocks of ROWS rows per kv head
+    long long total;    // steps of all its units
+};
+
+template <int ROWS>
+__device__ __forceinline__ Work work_of(const AttnCall &p, const AttnRequest &r)
+{
+    Work w{0, 0, 0, 0};
+    if (r.bad || r.n == 0 || r.len == 0) return w;
+    const int R = p.heads / p.c.kv_heads;
+    const int first = attn_first(p, max(r.len - r.n, -1));
+    w.step0 = first / kStepKeys;
+    w.steps = (r.len + kStepKeys - 1) / kStepKeys - w.step0;
+    w.blocks = (int)(((long long)r.n * R + ROWS - 1) / ROWS);
+    w.total = (long long)w.blocks * p.c.kv_heads * w.steps;
+    return w;
+}
+
+__device__ __forceinline__ long long warp_scan(long long v, int lane)
+{
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += u;
+    }
+    return v;
+}
+
+// Exclusive prefix of v over the CTA's threads and its total.
+__device__ __forceinline__ long long cta_scan(long long v, long long &total, long long *sums)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long inc = warp_scan(v, lane);
+    __syncthreads();
+    if (lane == 31) sums[warp] = inc;
+    __syncthreads();
+    long long before = 0;
+    total = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+        if (i < warp) before += sums[i];
+        total += sums[i];
+    }
+    return before + inc - v;
+}
+
+template <int J, int G, int NB, int STAGES, int MINB>
+__global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid_constant__ SplitParams p)
+{
+    constexpr int D = 32 * J, ROWS = 4 * NB, UG = J / G;   // UG: 32-value blocks per group
+    using S = Stage<J, G>;
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ long long s_sums[kWarps];
+    __shared__ long long s_at;
+    __shared__ int s_b;
+    const AttnCall &a = p.a;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int g = lane >> 2, c = lane & 3;
+    const int H = a.c.kv_heads, R = a.heads / H;
+
+    // ---- requests that need no sums: bad ones, and those without keys ----
+    for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+        const AttnRequest r = attn_request(a, b);
+        if (!r.bad && !(r.n > 0 && r.len == 0)) continue;
+        if (r.bad && threadIdx.x == 0) atomicOr(&g_attn_error, kAttnBadRequest);
+        const float v = r.bad ? quiet_nan() : 0.0f;
+        const int per = a.heads * D;
+        for (int row = r.fill0; row < r.fill1; ++row)
+            for (int i = threadIdx.x; i < per; i += kThreads) a.out[(size_t)row * a.ldo + i] = v;
+    }
+
+    // ---- this CTA's range of steps ----
+    long long total = 0, before = 0;
+    for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+        const int b = b0 + threadIdx.x;
+        const long long w = b < a.B ? work_of<ROWS>(a, attn_request(a, b)).total : 0;
+        long long t;
+        before = cta_scan(w, t, s_sums);
+        total += t;
+    }
+    if (threadIdx.x == 0) p.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    const long long chunk = (total + gridDim.x - 1) / gridDim.x;
+    const long long begin = chunk * blockIdx.x;
+    const long long end = min(begin + chunk, total);
+    if (begin >= end) return;
+    {
+        long long base = 0;
+        for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+            const int b = b0 + threadIdx.x;
+            const long long w = b < a.B ? work_of<ROWS>(a, attn_request(a, b)).total : 0;
+            long long t;
+            if (a.B > kThreads) before = cta_scan(w, t, s_sums);
+            else t = total;
+            if (begin >= base + before && begin < base + before + w) {
+                s_b = b;
+                s_at = begin - (base + before);
+            }
+            base += t;
+            if (base > begin) break;  // uniform
+        }
+        __syncthreads();
+    }
+
+    const uint32_t ring = smem_addr(smem) + (uint32_t)warp * STAGES * S::kBytes;
+    float *own = reinterpret_cast<float *>(smem + (size_t)warp * STAGES * S::kBytes);   // after a unit
+    int b = s_b;
+    AttnRequest rq = attn_request(a, b);
+    Work wk = work_of<ROWS>(a, rq);
+    long long at = s_at;              // step within the request
+    long long pos = begin;
+    while (pos < end) {
+        const int unit = (int)(at / wk.steps);
+        const int from = (int)(at - (long long)unit * wk.steps);
+        const int upto = (int)min((long long)wk.steps, from + (end - pos));
+        const int h = unit / wk.blocks, rb = unit - h * wk.blocks;
+        const int rows_all = rq.n * R;
+
+        // ---- query rows: two fp16 pieces, power-of-two scaled per row ----
+        uint32_t qf[NB][J][4];
+        float qs[NB][G], F[NB];
+        int last[NB], first[NB];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+            const int rho = rb * ROWS + nb * 4 + (g >> 1);     // the row this thread's column holds
+            float x[J][8];
+            float big = 0.0f;
+            const bool in = rho < rows_all;
+            const int j = in ? rho / R : 0, r = in ? rho - j * R : 0;
+            const float *q = a.q + (size_t)(rq.row0 + j) * a.ldq + (size_t)(h * R + r) * D + 8 * c;
+#pragma unroll
+            for (int u = 0; u < J; ++u) {
+                float4 v0 = make_float4(0.f, 0.f, 0.f, 0.f), v1 = v0;
+                if (in) {
+                    v0 = __ldg(reinterpret_cast<const float4 *>(q + 32 * u));
+                    v1 = __ldg(reinterpret_cast<const float4 *>(q + 32 * u) + 1);
+                }
+                x[u][0] = v0.x; x[u][1] = v0.y; x[u][2] = v0.z; x[u][3] = v0.w;
+                x[u][4] = v1.x; x[u][5] = v1.y; x[u][6] = v1.z; x[u][7] = v1.w;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) big = fmaxf(big, fabsf(x[u][i]));
+            }
+            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+            // 2^k times the row lies in [2^13, 2^14) at its largest
+            int e = (int)((__float_as_uint(big) >> 23) & 255u);
+            int k = 13 + 127 - e;
+            k = big > 0.0f ? min(k, 120) : 0;
+            const float up = exp2f((float)k);
+            float sum[G];
+#pragma unroll
+            for (int gr = 0; gr < G; ++gr) sum[gr] = 0.0f;
+            const bool lo = g & 1;
+#pragma unroll
+            for (int u = 0; u < J; ++u) {
+                __half v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float y = x[u][i] * up;
+                    const float hi = __half2float(__float2half_rn(y));
+                    sum[u / UG] += y;
+                    // odd nibbles are masked at 16 times their value
+                    v[i] = __float2half_rn((lo ? y - hi : hi) * ((i & 1) ? 0.0625f : 1.0f));
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const __half2 pr = __halves2half2(v[i], v[i + 4]);
+                    qf[nb][u][i] = *reinterpret_cast<const uint32_t *>(&pr);
+                }
+            }
+            // constants of row c (the row of this thread's sums), from a lane that holds it
+            const int src = 8 * c;
+#pragma unroll
+            for (int gr = 0; gr < G; ++gr) {
+                float s = sum[gr];
+                s += __shfl_xor_sync(0xffffffffu, s, 1);
+                s += __shfl_xor_sync(0xffffffffu, s, 2);
+                qs[nb][gr] = __shfl_sync(0xffffffffu, s, src) * 0x1p-24f;
+            }
+            const int kc = __shfl_sync(0xffffffffu, k, src);
+            F[nb] = ldexpf(a.scale * kLog2e, 24 - kc);
+            const int rc = rb * ROWS + nb * 4 + c;
+            last[nb] = rc < rows_all ? rq.len - rq.n + rc / R : -1;
+            first[nb] = attn_first(a, last[nb]);
+        }
+        // keys that some row of the block sees; keys that all of its rows see
+        const int row_hi = min(rb * ROWS + ROWS, rows_all) - 1;
+        const int see_hi = rq.len - rq.n + row_hi / R;                                  // inclusive
+        const int all_hi = rq.len - rq.n + rb * ROWS / R;
+        const int see_lo = attn_first(a, max(all_hi, -1)), all_lo = attn_first(a, see_hi);
+
+        float o[NB][J][4], zs[NB][G], l[NB], m[NB];
+        float vs = 0x1p111f, vref = 0x1p-100f;                 // 2^(11 - E), 2^E
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+            l[nb] = 0.0f;
+            m[nb] = -INFINITY;
+#pragma unroll
+            for (int gr = 0; gr < G; ++gr) zs[nb][gr] = 0.0f;
+#pragma unroll
+            for (int u = 0; u < J; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[nb][u][i] = 0.0f;
+        }
+
+        const int32_t *table = a.page_table + (size_t)b * a.max_pages;
+        const int shift = 31 - __clz(a.c.page_size);
+        const int key00 = (wk.step0 + from) * kStepKeys + warp * kStageKeys;
+        const int iters = upto - from;
+        // the two pages (16 keys each) of iteration i; -1 where nothing is seen
+        auto pages_of = [&](int i) {
+            int2 pg = make_int2(-1, -1);
+            if (i < iters) {
+                const int k0 = key00 + i * kStepKeys;
+                if (k0 <= see_hi && k0 + 16 > see_lo) pg.x = __ldg(table + (k0 >> shift));
+                if (k0 + 16 <= see_hi && k0 + 32 > see_lo) pg.y = __ldg(table + ((k0 + 16) >> shift));
+            }
+            return pg;
+        };
+        auto issue = [&](int i, int slot, int2 pg) {
+            const int k0 = key00 + i * kStepKeys;
+            if (i < iters && k0 <= see_hi && k0 + 32 > see_lo) {
+                const uint32_t st = ring + (uint32_t)slot * S::kBytes;
+                size_t row[2];
+                bool ok[2], seen[2];
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int page = x ? pg.y : pg.x, kx = k0 + 16 * x;
+                    seen[x] = kx <= see_hi && kx + 16 > see_lo;
+                    ok[x] = seen[x] && page >= 0 && page < a.c.n_pages;
+                    row[x] = ok[x] ? kv_row(a.c, page, h, kx & (a.c.page_size - 1)) : 0;
+                }
+#pragma unroll
+                for (int j = 0; j < J; ++j) {                  // 32 J pieces of 16 bytes, keys then values
+                    const int piece = 32 * j + lane;
+                    const int key = piece / J, pc = piece - key * J;
+                    const int x = key >> 4;
+                    const uint32_t dst = st + key * 16 * J + ((pc ^ swizzle<J>(key)) << 4);
+                    if (x ? ok[1] : ok[0]) {
+                        const size_t off = ((x ? row[1] : row[0]) + (key & 15)) * (size_t)(D / 2) + 16 * pc;
+                        cp_async_16(dst, reinterpret_cast<const char *>(a.c.Kq) + off);
+                        cp_async_16(dst + S::kCodes, reinterpret_cast<const char *>(a.c.Vq) + off);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < G; ++j) {                  // scales and zeros: 16 G pieces each
+                    const int piece = 32 * j + lane;
+                    const int side = piece >= 16 * G, pc = piece - side * 16 * G;
+                    const int x = pc >= 8 * G;
+                    const uint32_t dst = st + 2 * S::kCodes + side * S::kSz + pc * 16;
+                    if (x ? ok[1] : ok[0]) {
+                        const size_t off = (x ? row[1] : row[0]) * (size_t)(8 * G) + (pc - x * 8 * G) * 16;
+                        cp_async_16(dst, reinterpret_cast<const char *>(side ? a.c.V_sz : a.c.K_sz) + off);
+                    } else if (x ? seen[1] : seen[0]) {        // a page outside the pool: NaN rows
+                        const float nan = quiet_nan();
+                        asm volatile("st.shared.v4.f32 [%0], {%1,%1,%1,%1};" ::"r"(dst), "f"(nan) : "memory");
+                        atomicOr(&g_attn_error, kAttnBadRequest);
+                    }
+                }
+            }
+            cp_async_commit();
+        };
+        int2 pg = pages_of(0);
+#pragma unroll
+        for (int i = 0; i < STAGES - 1; ++i) {
+            const int2 nx = pages_of(i + 1);
+            issue(i, i, pg);
+            pg = nx;
+        }
+        int slot = 0, fill = STAGES - 1;
+        for (int i = 0; i < iters; ++i) {
+            {
+                const int2 nx = pages_of(i + STAGES);
+                issue(i + STAGES - 1, fill, pg);
+                pg = nx;
+                if (++fill == STAGES) fill = 0;
+            }
+            cp_async_wait<STAGES - 1>();
+            __syncwarp();
+            const int k0 = key00 + i * kStepKeys;
+            const uint32_t st = ring + (uint32_t)slot * S::kBytes;
+            if (++slot == STAGES) slot = 0;
+            if (k0 > see_hi || k0 + kStageKeys <= see_lo) continue;   // uniform in the warp
+
+            // ---- exponents: keys times query rows ----
+            float w[2][2][NB];                                 // [16 keys][key row g, g + 8][row]
+            const uint32_t magic = 0x64006400u;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int ka = 16 * x + key_of_row(g), kb = ka + 8;
+                uint32_t wa[J], wb[J];
+                if constexpr (J == 8) {                        // two swizzled 16-byte pieces
+                    uint32_t t4[4];
+                    load_words<4>(st + ka * 128 + (((2 * c) ^ swizzle<J>(ka)) << 4), t4);
+                    for (int i4 = 0; i4 < 4; ++i4) wa[i4] = t4[i4];
+                    load_words<4>(st + ka * 128 + (((2 * c + 1) ^ swizzle<J>(ka)) << 4), t4);
+                    for (int i4 = 0; i4 < 4; ++i4) wa[4 + i4] = t4[i4];
+                    load_words<4>(st + kb * 128 + (((2 * c) ^ swizzle<J>(kb)) << 4), t4);
+                    for (int i4 = 0; i4 < 4; ++i4) wb[i4] = t4[i4];
+                    load_words<4>(st + kb * 128 + (((2 * c + 1) ^ swizzle<J>(kb)) << 4), t4);
+                    for (int i4 = 0; i4 < 4; ++i4) wb[4 + i4] = t4[i4];
+                } else if constexpr (J == 4) {
+                    load_words<J>(st + ka * 64 + ((c ^ swizzle<J>(ka)) << 4), wa);
+                    load_words<J>(st + kb * 64 + ((c ^ swizzle<J>(kb)) << 4), wb);
+                } else {
+                    load_words<J>(st + ka * 16 * J + 4 * J * c, wa);
+                    load_words<J>(st + kb * 16 * J + 4 * J * c, wb);
+                }
+                float acc[NB][4];
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) w[x][0][nb] = w[x][1][nb] = 0.0f;
+#pragma unroll
+                for (int u = 0; u < J; ++u) {
+                    if (u % UG == 0) {
+#pragma unroll
+                        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                            for (int i4 = 0; i4 < 4; ++i4) acc[nb][i4] = 0.0f;
+                    }
+                    const uint32_t ha = wa[u] >> 8, hb = wb[u] >> 8;
+                    const uint32_t m0 = 0x000F000Fu, m1 = 0x00F000F0u;
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) {
+                        mma16816(acc[nb], wa[u] & m0, wb[u] & m0, wa[u] & m1, wb[u] & m1, qf[nb][u][0], qf[nb][u][1]);
+                        mma16816(acc[nb], ha & m0, hb & m0, ha & m1, hb & m1, qf[nb][u][2], qf[nb][u][3]);
+                    }
+                    if (u % UG == UG - 1) {
+                        const int gr = u / UG;
+                        const float2 sa = lds_f2(st + 2 * S::kCodes + (ka * G + gr) * 8);
+                        const float2 sb = lds_f2(st + 2 * S::kCodes + (kb * G + gr) * 8);
+#pragma unroll
+                        for (int nb = 0; nb < NB; ++nb) {
+                            const float ta = fmaf(-sa.y, qs[nb][gr], acc[nb][0] + acc[nb][1]);
+                            const float tb = fmaf(-sb.y, qs[nb][gr], acc[nb][2] + acc[nb][3]);
+                            w[x][0][nb] = fmaf(sa.x, ta, w[x][0][nb]);
+                            w[x][1][nb] = fmaf(sb.x, tb, w[x][1][nb]);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) {
+                    w[x][0][nb] *= F[nb];
+                    w[x][1][nb] *= F[nb];
+                }
+            }
+
+            // ---- values' scales; what a row does not see ----
+            float2 vz[2][2][G];
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const int key = 16 * x + key_of_row(g) + 8 * y;
+#pragma unroll
+                    for (int gr = 0; gr < G; ++gr)
+                        vz[x][y][gr] = lds_f2(st + 2 * S::kCodes + S::kSz + (key * G + gr) * 8);
+                }
+            const bool masked = k0 + kStageKeys - 1 > all_hi || k0 < all_lo;   // uniform
+            uint32_t hidden = 0;                               // bit (x, y, nb)
+            if (masked) {
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y)
+#pragma unroll
+                        for (int nb = 0; nb < NB; ++nb) {
+                            const int key = k0 + 16 * x + key_of_row(g) + 8 * y;
+                            if (key > last[nb] || key < first[nb]) {
+                                hidden |= 1u << ((x * 2 + y) * NB + nb);
+                                w[x][y][nb] = -INFINITY;
+                            }
+                        }
+            }
+            constexpr uint32_t kAllRows = (1u << NB) - 1u;
+            // ---- the references m and E still hold? ----
+            float top[NB], vtop = 0.0f;
+            bool move = false;
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+                top[nb] = fmaxf(fmaxf(w[0][0][nb], w[0][1][nb]), fmaxf(w[1][0][nb], w[1][1][nb]));
+                move |= top[nb] > m[nb] + kSlack;
+            }
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const bool none = ((hidden >> ((x * 2 + y) * NB)) & kAllRows) == kAllRows;
+#pragma unroll
+                    for (int gr = 0; gr < G; ++gr) vtop = fmaxf(vtop, none ? 0.0f : fabsf(vz[x][y][gr].x));
+                }
+            move |= vtop > vref;
+            if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+                for (int i4 = 16; i4 > 0; i4 >>= 1) vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, i4));
+                float fv = 1.0f;
+                if (vtop > vref) {
+                    const int e = min((int)(__float_as_uint(vtop) >> 23) - 126, 127);   // vtop < 2^e
+                    const float nref = ldexpf(1.0f, e);
+                    fv = vref / nref;
+                    vref = nref;
+                    vs = ldexpf(1.0f, kPieceBits - e);
+                }
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) {
+                    float t = top[nb];
+                    t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
+                    t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
+                    t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
+                    const float mn = fmaxf(m[nb], t);
+                    const float f = mn > m[nb] ? exp2_approx(m[nb] - mn) : 1.0f;
+                    m[nb] = mn;
+                    l[nb] *= f;
+                    const float fo = f * fv;
+#pragma unroll
+                    for (int gr = 0; gr < G; ++gr) zs[nb][gr] *= fo;
+#pragma unroll
+                    for (int u = 0; u < J; ++u)
+#pragma unroll
+                        for (int i4 = 0; i4 < 4; ++i4) o[nb][u][i4] *= fo;
+                }
+            }
+
+            // ---- weights, and the second product group by group ----
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+                const float ref = m[nb] == -INFINITY ? 0.0f : m[nb];
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        w[x][y][nb] = exp2_approx(w[x][y][nb] - ref);
+                        l[nb] += w[x][y][nb];
+                    }
+            }
+            Halves<J> hv[2][4];
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int key = 16 * x + key_of_row(2 * c + (k & 1)) + (k & 2) * 4;
+                    const uint32_t row = st + S::kCodes + key * 16 * J;
+                    if constexpr (J == 8) hv[x][k] = load_halves<J>(row + ((g ^ swizzle<J>(key)) << 4));
+                    else if constexpr (J == 4)
+                        hv[x][k] = load_halves<J>(row + (((g >> 1) ^ swizzle<J>(key)) << 4) + (g & 1) * 8);
+                    else hv[x][k] = load_halves<J>(row + 2 * J * g);
+                }
+#pragma unroll
+            for (int gr = 0; gr < G; ++gr) {
+                uint32_t pf[NB][2][2];
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const bool hid = masked && ((hidden >> ((x * 2 + y) * NB + nb)) & 1u);
+                            const float ps = hid ? 0.0f : w[x][y][nb] * (vz[x][y][gr].x * vs);
+                            zs[nb][gr] = hid ? zs[nb][gr] : fmaf(ps, vz[x][y][gr].y - 8.0f, zs[nb][gr]);
+                            pf[nb][x][y] = transpose8x8(two_pieces(ps));
+                        }
+#pragma unroll
+                for (int uu = 0; uu < UG; ++uu) {
+                    const int u = gr * UG + uu;
+                    float t0[NB][4], t1[NB][4];
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                        for (int i4 = 0; i4 < 4; ++i4) t0[nb][i4] = t1[nb][i4] = 0.0f;
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const uint32_t sel = (u & 1) ? 0x7632u : 0x5410u;
+                        const uint32_t x01 = __byte_perm(hv[x][0].r[u / 2], hv[x][1].r[u / 2], sel);
+                        const uint32_t x23 = __byte_perm(hv[x][2].r[u / 2], hv[x][3].r[u / 2], sel);
+                        const uint32_t y01 = x01 >> 8, y23 = x23 >> 8;
+                        const uint32_t m8 = 0xE408E408u;      // -(1024 + 8) in each half
+                        const uint32_t s16 = 0x2C002C00u;     // 1/16
+                        const uint32_t m72 = 0xD480D480u;     // -72: (1024 + 16 c)/16 - 72 = c - 8
+                        const uint32_t a0 = h2_add(mask_or<0x000F000Fu>(x01, magic), m8);
+                        const uint32_t a1 = h2_fma(mask_or<0x00F000F0u>(x01, magic), s16, m72);
+                        const uint32_t a2 = h2_add(mask_or<0x000F000Fu>(x23, magic), m8);
+                        const uint32_t a3 = h2_fma(mask_or<0x00F000F0u>(x23, magic), s16, m72);
+                        const uint32_t b0 = h2_add(mask_or<0x000F000Fu>(y01, magic), m8);
+                        const uint32_t b1 = h2_fma(mask_or<0x00F000F0u>(y01, magic), s16, m72);
+                        const uint32_t b2 = h2_add(mask_or<0x000F000Fu>(y23, magic), m8);
+                        const uint32_t b3 = h2_fma(mask_or<0x00F000F0u>(y23, magic), s16, m72);
+#pragma unroll
+                        for (int nb = 0; nb < NB; ++nb) {
+                            mma16816(t0[nb], a0, a1, a2, a3, pf[nb][x][0], pf[nb][x][1]);
+                            mma16816(t1[nb], b0, b1, b2, b3, pf[nb][x][0], pf[nb][x][1]);
+                        }
+                    }
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) {
+                        o[nb][u][0] += t0[nb][0] + t0[nb][1];
+                        o[nb][u][1] += t0[nb][2] + t0[nb][3];
+                        o[nb][u][2] += t1[nb][0] + t1[nb][1];
+                        o[nb][u][3] += t1[nb][2] + t1[nb][3];
+                    }
+                }
+            }
+            __syncwarp();   // the stage is read: the next copies may land in it
+        }
+        cp_async_wait<0>();
+        __syncwarp();
+
+        // ---- the warp's sums into its own stretch of the ring: [row][D], then m, l ----
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+            const float back = vref * 0x1p-11f;
+            float lt = l[nb];
+            lt += __shfl_xor_sync(0xffffffffu, lt, 4);
+            lt += __shfl_xor_sync(0xffffffffu, lt, 8);
+            lt += __shfl_xor_sync(0xffffffffu, lt, 16);
+            const int row = nb * 4 + c;
+#pragma unroll
+            for (int u = 0; u < J; ++u) {
+                float z = zs[nb][u / UG];
+                z += __shfl_xor_sync(0xffffffffu, z, 4);
+                z += __shfl_xor_sync(0xffffffffu, z, 8);
+                z += __shfl_xor_sync(0xffffffffu, z, 16);
+                *reinterpret_cast<float4 *>(own + row * D + 32 * u + 4 * g) =
+                    make_float4((o[nb][u][0] - z) * back, (o[nb][u][1] - z) * back, (o[nb][u][2] - z) * back,
+                                (o[nb][u][3] - z) * back);
+            }
+            if (g == 0) {
+                own[ROWS * D + 2 * row] = m[nb];
+                own[ROWS * D + 2 * row + 1] = lt;
+            }
+        }
+        __syncthreads();
+        // ---- the warps' sums joined, in order ----
+        const bool whole = from == 0 && upto == wk.steps;
+        const int first_unit = pos == begin;                   // this CTA's first unit: slot 0
+        float *part = p.part + ((size_t)blockIdx.x * 2 + (first_unit ? 0 : 1)) * ROWS * (D + 2);
+        for (int i = threadIdx.x; i < ROWS * D / 4; i += kThreads) {
+            const int row = i / (D / 4), d = 4 * (i - row * (D / 4));
+            const int rho = rb * ROWS + row;
+            if (rho >= rows_all) continue;
+            float mt = -INFINITY;
+#pragma unroll
+            for (int v = 0; v < kWarps; ++v) {
+                const float *o2 = reinterpret_cast<const float *>(smem + (size_t)v * STAGES * S::kBytes);
+                mt = fmaxf(mt, o2[ROWS * D + 2 * row]);
+            }
+            const float ref = mt == -INFINITY ? 0.0f : mt;
+            float lt = 0.0f;
+            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int v = 0; v < kWarps; ++v) {
+                const float *o2 = reinterpret_cast<const float *>(smem + (size_t)v * STAGES * S::kBytes);
+                const float f = exp2_approx(o2[ROWS * D + 2 * row] - ref);
+                const float4 t = *reinterpret_cast<const float4 *>(o2 + row * D + d);
+                lt = fmaf(f, o2[ROWS * D + 2 * row + 1], lt);
+                s.x = fmaf(f, t.x, s.x);
+                s.y = fmaf(f, t.y, s.y);
+                s.z = fmaf(f, t.z, s.z);
+                s.w = fmaf(f, t.w, s.w);
+            }
+            if (whole) {
+                const int j = rho / R, r = rho - j * R;
+                const float inv = mt == -INFINITY ? 0.0f : 1.0f / lt;
+                *reinterpret_cast<float4 *>(a.out + (size_t)(rq.row0 + j) * a.ldo + (size_t)(h * R + r) * D + d) =
+                    make_float4(s.x * inv, s.y * inv, s.z * inv, s.w * inv);
+            } else {
+                float *pr = part + (size_t)row * D + d;
+                *reinterpret_cast<float4 *>(pr) = s;
+                if (d == 0) {
+                    part[ROWS * D + 2 * row] = mt;
+                    part[ROWS * D + 2 * row + 1] = lt;
+                }
+            }
+        }
+        if (threadIdx.x == 0 && !whole && from == 0) {
+            // the unit starts here and goes on in the CTAs up to the one that holds its last step
+            const int last_cta = (int)((pos + wk.steps - 1) / chunk);
+            p.desc[blockIdx.x] = make_int4(b, unit, last_cta, first_unit ? 0 : 1);
+        }
+        __syncthreads();
+
+        pos += upto - from;
+        at += upto - from;
+        while (pos < end && at >= wk.total) {                  // the next request with work
+            ++b;
+            rq = attn_request(a, b);
+            wk = work_of<ROWS>(a, rq);
+            at = 0;
+            if (wk.total > 0) break;
+        }
+    }
+}
+
+// Joins the partial sums of the units that were cut, one CTA for each CTA of
+// the first kernel.
+template <int ROWS>
+__global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ SplitParams p, int D)
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int4 d = __ldcg(p.desc + blockIdx.x);
+    if (d.x < 0) return;
+    const AttnCall &a = p.a;
+    const AttnRequest rq = attn_request(a, d.x);
+    const int R = a.heads / a.c.kv_heads;
+    const int blocks = (int)(((long long)rq.n * R + ROWS - 1) / ROWS);
+    const int h = d.y / blocks, rb = d.y - h * blocks;
+    const size_t per = (size_t)ROWS * (D + 2);
+    auto part_of = [&](int cta) {
+        return p.part + ((size_t)cta * 2 + (cta == (int)blockIdx.x ? d.w : 0)) * per;
+    };
+    for (int i = threadIdx.x; i < ROWS * D / 4; i += 128) {
+        const int row = i / (D / 4), dd = 4 * (i - row * (D / 4));
+        const int rho = rb * ROWS + row;
+        if (rho >= rq.n * R) continue;
+        float m = -INFINITY, l = 0.0f;
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int cta = blockIdx.x; cta <= d.z; ++cta) {
+            const float *pt = part_of(cta);
+            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(pt + (size_t)ROWS * D + 2 * row));
+            const float4 t = __ldcg(reinterpret_cast<const float4 *>(pt + (size_t)row * D + dd));
+            const float mn = fmaxf(m, ml.x);
+            const float ref = mn == -INFINITY ? 0.0f : mn;
+            const float fo = exp2_approx(m - ref), fn = exp2_approx(ml.x - ref);
+            l = l * fo + ml.y * fn;
+            s.x = s.x * fo + t.x * fn;
+            s.y = s.y * fo + t.y * fn;
+            s.z = s.z * fo + t.z * fn;
+            s.w = s.w * fo + t.w * fn;
+            m = mn;
+        }
+        const int j = rho / R, r = rho - j * R;
+        const float inv = m == -INFINITY ? 0.0f : 1.0f / l;
+        *reinterpret_cast<float4 *>(a.out + (size_t)(rq.row0 + j) * a.ldo + (size_t)(h * R + r) * D + dd) =
+            make_float4(s.x * inv, s.y * inv, s.z * inv, s.w * inv);
+    }
+}
+
+template <int J, int G, int NB>
+cudaError_t launch_split(const AttnCall &call, cudaStream_t stream)
+{
+    // four query rows and heads of up to 128: registers and shared memory for
+    // two CTAs per SM; otherwise one
+    constexpr int MINB = NB == 1 && J <= 4 ? 2 : 1;
+    constexpr int room = MINB == 2 ? 110 * 1024 : 220 * 1024;
+    constexpr int fit = room / (kWarps * Stage<J, G>::kBytes);
+    constexpr int STAGES = fit < 2 ? 2 : fit > 4 ? 4 : fit;
+    static_assert(STAGES * Stage<J, G>::kBytes >= 4 * NB * (32 * J + 2) * 4, "the sums fit the ring");
+    auto kern = attn_split_kernel<J, G, NB, STAGES, MINB>;
+    constexpr int smem = kWarps * STAGES * Stage<J, G>::kBytes;
+    int dev = 0, sms = 0;
+    cudaError_t err;
+    if ((err = cudaGetDevice(&dev)) != cudaSuccess) return err;
+    static std::atomic<int> ready_dev{-1};
+    if (ready_dev.load(std::memory_order_acquire) != dev) {
+        if ((err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess)
+            return err;
+        ready_dev.store(dev, std::memory_order_release);
+    }
+    if ((err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return err;
+    SplitParams p{};
+    p.a = call;
+    // no more CTAs than steps can exist
+    const int R = call.heads / call.c.kv_heads;
+    const long long steps = (call.max_len + kStepKeys - 1) / kStepKeys;
+    const long long most_n = call.max_query < call.T ? call.max_query : call.T;
+    const long long blocks = (most_n * R + 4 * NB - 1) / (4 * NB);
+    const long long units = (call.B < call.T ? call.B : call.T) * blocks * call.c.kv_heads;
+    long long grid = (long long)sms * MINB;
+    if (grid > kMaxGrid) grid = kMaxGrid;
+    if (grid > units * steps) grid = units * steps;
+    if (grid < 1) grid = 1;
+    p.grid = (int)grid;
+    p.desc = static_cast<int4 *>(call.workspace);
+    p.part = reinterpret_cast<float *>(static_cast<char *>(call.workspace) + kMaxGrid * sizeof(int4));
+    kern<<<(unsigned)grid, kThreads, smem, stream>>>(p);
+    if ((err = cudaGetLastError()) != cudaSuccess || steps <= 1 || grid <= 1) return err;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(128);
+    cfg.stream = stream;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attn_join_kernel<4 * NB>, p, (int)(32 * J));
+}
+
+template <int J, int G>
+cudaError_t launch_rows(const AttnCall &call, cudaStream_t stream)
+{
+    const long long rows = (long long)call.max_query * (call.heads / call.c.kv_heads);
+    return rows <= 4 ? launch_split<J, G, 1>(call, stream) : launch_split<J, G, 2>(call, stream);
 }
 
 }  // namespace
 
-size_t attn_workspace_bytes(int, int, int, int)
+size_t attn_workspace_bytes(int, int, int, int D)
 {
-    return 256;
+    return kMaxGrid * (sizeof(int4) + 2 * 8 * (size_t)(D + 2) * sizeof(float));
 }
 
-cudaError_t launch_attn(const AttnCall &p, cudaStream_t stream)
+cudaError_t launch_attn(const AttnCall &call, cudaStream_t stream)
 {
-    const dim3 grid((unsigned)((p.heads + 3) / 4), (unsigned)p.B);
-    switch (p.c.head_dim) {
-    case 64: attn_rows_kernel<2><<<grid, 128, 0, stream>>>(p); break;
-    case 96: attn_rows_kernel<3><<<grid, 128, 0, stream>>>(p); break;
-    case 128: attn_rows_kernel<4><<<grid, 128, 0, stream>>>(p); break;
-    default: attn_rows_kernel<8><<<grid, 128, 0, stream>>>(p); break;
+    const int G = call.c.head_dim / call.c.group_size;
+    switch (call.c.head_dim * 16 + G) {
+    case 64 * 16 + 1: return launch_rows<2, 1>(call, stream);
+    case 64 * 16 + 2: return launch_rows<2, 2>(call, stream);
+    case 96 * 16 + 1: return launch_rows<3, 1>(call, stream);
+    case 96 * 16 + 3: return launch_rows<3, 3>(call, stream);
+    case 128 * 16 + 1: return launch_rows<4, 1>(call, stream);
+    case 128 * 16 + 2: return launch_rows<4, 2>(call, stream);
+    case 128 * 16 + 4: return launch_rows<4, 4>(call, stream);
+    case 256 * 16 + 1: return launch_rows<8, 1>(call, stream);
+    case 256 * 16 + 2: return launch_rows<8, 2>(call, stream);
+    case 256 * 16 + 4: return launch_rows<8, 4>(call, stream);
+    case 256 * 16 + 8: return launch_rows<8, 8>(call, stream);
     }
-    return cudaGetLastError();
+    return cudaErrorInvalidValue;
 }
 
 cudaError_t read_attn_device_error(unsigned int *bits, bool clear)

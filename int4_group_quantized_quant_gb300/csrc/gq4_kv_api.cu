@@ -13,6 +13,8 @@ namespace {
 using gq4::aligned;
 using gq4::RangeSet;
 
+constexpr long long kMaxKeys = 1ll << 30;  // of one request: positions stay well inside 32 bits
+
 // Rows x [T][heads][D], ld floats apart.
 gq4_status check_rows(const float *x, int heads, int D, int ld)
 {
@@ -168,7 +170,7 @@ gq4_status gq4_kv_plan(int B, int T, int page_size, int max_pages, int n_free,
         return GQ4_ERR_INVALID_ARG;
     if (page_size < 16 || page_size > 256 || (page_size & (page_size - 1)) != 0)
         return GQ4_ERR_INVALID_ARG;
-    if ((long long)max_pages * page_size > 0x7fffffffll) return GQ4_ERR_INVALID_ARG;
+    if ((long long)max_pages * page_size > kMaxKeys) return GQ4_ERR_INVALID_ARG;
     if (!past_lens || !new_lens || !page_table || !free_count || !free_count_out || !seq_lens ||
         !query_start || (T > 0 && (!positions || !slots)) || (n_free > 0 && !free_pages))
         return GQ4_ERR_INVALID_ARG;
@@ -228,7 +230,7 @@ gq4_status gq4_kv_attention(int B, int T, int q_heads, int max_pages, int max_qu
     if (q_heads < 1 || q_heads > GQ4_MAX_HEADS || q_heads % cache->kv_heads != 0)
         return GQ4_ERR_INVALID_ARG;
     const long long room = (long long)max_pages * cache->page_size;
-    if (room > 0x7fffffffll) return GQ4_ERR_INVALID_ARG;
+    if (room > kMaxKeys) return GQ4_ERR_INVALID_ARG;
     if (!(scale - scale == 0.0f)) return GQ4_ERR_INVALID_ARG;  // NaN or infinite
     if (T == 0 || max_query == 0) return GQ4_OK;
     GQ4_TRY(check_rows(q, q_heads, cache->head_dim, ldq));
