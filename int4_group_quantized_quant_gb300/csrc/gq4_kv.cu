@@ -15,219 +15,302 @@ constexpr unsigned int kKvNonFinite = 1u << 3, kKvBadSlot = 1u << 6, kKvRefused 
 
 // ---------------------------------------------------------------------------
 // Writer.  A lane holds one word's 8 values, a row takes D/8 lanes; a warp
-// takes as many rows as fit (K and V rows of a token count as rows of their
-// own), so that a group's minimum and maximum are a shuffle away.  Bound by
-// HBM: 4 bytes read and 0.5 + 8/gs written per value.
+// takes as many rows as fit, so that a group's minimum and maximum are a
+// shuffle away.  The K and V rows of a few tokens are one CTA's, numbered in
+// 32 bits; a row's loads do not wait for its slot.  Bound by HBM: 4 bytes
+// read and 0.5 + 8/gs written per value.
 // ---------------------------------------------------------------------------
 constexpr int kAppendThreads = 256;
+constexpr int kAppendUnroll = 2;   // rows per lane whose loads are issued together
 
 struct AppendParams {
     gq4_kv_cache c;
     const float *x[2];       // k, v
     int ld[2];
     const int32_t *slots;
-    long long n_rows;        // 2 * T * kv_heads
-    int wpr;                 // words (lanes) per row
-    int rpw;                 // rows per warp
+    int T, tokens;           // all, and per CTA
+    int shift;               // log2 of the page size
     int L;                   // lanes per group
 };
 
+template <int J>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendParams p)
 {
-    const int lane = threadIdx.x & 31;
-    const int in_warp = lane / p.wpr, w = lane - in_warp * p.wpr;
-    const long long warp0 = ((long long)blockIdx.x * kAppendThreads + threadIdx.x) >> 5;
-    const long long n_warps = ((long long)gridDim.x * kAppendThreads) >> 5;
-    const int H = p.c.kv_heads, J = p.c.head_dim / 32, G = p.c.head_dim / p.c.group_size;
+    constexpr int WPR = 4 * J, RPW = 32 / WPR;   // words per row, rows per warp
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int in_warp = lane / WPR, w = lane - in_warp * WPR;
+    const int H = p.c.kv_heads, G = 32 * J / p.c.group_size;
     const long long total = (long long)p.c.n_pages * p.c.page_size;
-    for (long long r0 = warp0 * p.rpw; r0 < p.n_rows; r0 += n_warps * p.rpw) {
-        const long long r = r0 + in_warp;
-        const bool in = in_warp < p.rpw && r < p.n_rows;
-        const long long th = in ? r >> 1 : 0;
-        const int side = (int)(r & 1);
-        const int t = (int)(th / H), h = (int)(th - (long long)t * H);
-        const int slot = in ? __ldg(p.slots + t) : -1;
-        if (in && slot >= total && w == 0) atomicOr(&g_kv_error, kKvBadSlot);
-        const bool live = slot >= 0 && slot < total;
-        float v[8];
+    const int t0 = blockIdx.x * p.tokens;
+    const int n_rows = min(p.tokens, p.T - t0) * 2 * H;
+    constexpr int kStep = kAppendThreads / 32 * RPW;
+    for (int r0 = warp * RPW; r0 < n_rows; r0 += kAppendUnroll * kStep) {
+        float4 va[kAppendUnroll], vb[kAppendUnroll];
+        int slot[kAppendUnroll], head[kAppendUnroll];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-        if (live) {
-            const float4 *x = reinterpret_cast<const float4 *>(p.x[side] + (size_t)t * p.ld[side] +
-                                                              (size_t)h * p.c.head_dim + 8 * w);
-            const float4 a = __ldcs(x), b = __ldcs(x + 1);
-            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+        for (int u = 0; u < kAppendUnroll; ++u) {
+            const int r = r0 + u * kStep + in_warp;
+            slot[u] = -1;
+            head[u] = 0;
+            va[u] = vb[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (in_warp < RPW && r < n_rows) {
+                // rows of a token: its K rows, then its V rows
+                const int t = r / (2 * H), sh = r - t * 2 * H;
+                const int side = sh >= H, h = side ? sh - H : sh;
+                head[u] = 2 * h + side;
+                slot[u] = __ldg(p.slots + t0 + t);
+                const float4 *x = reinterpret_cast<const float4 *>(
+                    p.x[side] + (size_t)(t0 + t) * p.ld[side] + (size_t)h * (32 * J) + 8 * w);
+                va[u] = __ldcs(x);
+                vb[u] = __ldcs(x + 1);
+            }
         }
-        float lo = v[0], hi = v[0];
 #pragma unroll
-        for (int i = 1; i < 8; ++i) {
-            lo = min_nan(lo, v[i]);
-            hi = max_nan(hi, v[i]);
-        }
-        const int pos = w % p.L;
-        segment_min_max(lo, hi, pos, lane - pos, p.L);
-        int bad;
-        const GroupMap m = group_map(lo, hi, bad);
-        if (!live) continue;
-        const uint32_t word = bad ? 0u : quantize_word(v, m);
-        const int page = slot / p.c.page_size, at = slot - page * p.c.page_size;
-        const size_t row = kv_row(p.c, page, h, at);
-        if (side == 0) {
-            p.c.Kq[row * p.wpr + k_word_index(w, J)] = word;
-        } else {
-            uint16_t *half = reinterpret_cast<uint16_t *>(p.c.Vq) + row * 2 * p.wpr;
-            half[v_half_index(2 * w, J)] = (uint16_t)word;
-            half[v_half_index(2 * w + 1, J)] = (uint16_t)(word >> 16);
-        }
-        if (pos == 0) {
-            const float nan = __int_as_float(0x7fc00000);
-            float2 *sz = reinterpret_cast<float2 *>(side ? p.c.V_sz : p.c.K_sz);
-            sz[row * G + w / p.L] = bad ? make_float2(nan, nan) : make_float2(m.s, m.z);
-            if (bad) atomicOr(&g_kv_error, kKvNonFinite);
+        for (int u = 0; u < kAppendUnroll; ++u) {
+            if (r0 + u * kStep >= n_rows) break;   // uniform in the warp
+            const float v[8] = {va[u].x, va[u].y, va[u].z, va[u].w, vb[u].x, vb[u].y, vb[u].z, vb[u].w};
+            float lo = v[0], hi = v[0];
+#pragma unroll
+            for (int i = 1; i < 8; ++i) {
+                lo = min_nan(lo, v[i]);
+                hi = max_nan(hi, v[i]);
+            }
+            const int pos = w % p.L;
+            segment_min_max(lo, hi, pos, lane - pos, p.L);
+            int bad;
+            const GroupMap m = group_map(lo, hi, bad);
+            uint32_t word = bad ? 0u : quantize_word(v, m);
+            const int side = head[u] & 1, h = head[u] >> 1;
+            // value halves of words w and w + 4 are neighbours: one lane stores
+            // the first halves of both, the other the second
+            const uint32_t other = __shfl_xor_sync(0xffffffffu, word, 4);
+            if (slot[u] < 0) continue;
+            if (slot[u] >= total) {
+                if (w == 0) atomicOr(&g_kv_error, kKvBadSlot);
+                continue;
+            }
+            const size_t row = kv_row(p.c, slot[u] >> p.shift, h, slot[u] & (p.c.page_size - 1));
+            if (side == 0) {
+                p.c.Kq[row * WPR + k_word_index(w, J)] = word;
+            } else if constexpr (J % 2 == 0) {
+                const int g = 2 * (w & 3), b = w >> 2;
+                const uint32_t both = (b & 1) ? __byte_perm(other, word, 0x7632) : __byte_perm(word, other, 0x5410);
+                p.c.Vq[row * WPR + (((g + (b & 1)) * J + (b & ~1)) >> 1)] = both;
+            } else {
+                uint16_t *half = reinterpret_cast<uint16_t *>(p.c.Vq) + row * 2 * WPR;
+                half[v_half_index(2 * w, J)] = (uint16_t)word;
+                half[v_half_index(2 * w + 1, J)] = (uint16_t)(word >> 16);
+            }
+            if (pos == 0) {
+                const float nan = __int_as_float(0x7fc00000);
+                float2 *sz = reinterpret_cast<float2 *>(side ? p.c.V_sz : p.c.K_sz);
+                sz[row * G + w / p.L] = bad ? make_float2(nan, nan) : make_float2(m.s, m.z);
+                if (bad) atomicOr(&g_kv_error, kKvNonFinite);
+            }
         }
     }
 }
 
 // ---------------------------------------------------------------------------
-// Reader: a lane dequantises 4 consecutive values (half a word), a warp
-// stores 512 contiguous bytes at a time.
+// Reader: a lane dequantises 4 consecutive values (half a word), so that a
+// warp stores 512 contiguous bytes at a time.  Bound by HBM writes.
 // ---------------------------------------------------------------------------
 struct GatherParams {
     gq4_kv_cache c;
     const int32_t *slots;
     float4 *y[2];
-    long long n_items;       // float4s per side
-    int f4;                  // float4s per row
+    int T, tokens;           // all, and per CTA
+    int shift;
 };
 
+constexpr int kGatherUnroll = 4;
+
+template <int J>
 __global__ void __launch_bounds__(256) gather_kernel(const __grid_constant__ GatherParams p)
 {
-    const int H = p.c.kv_heads, J = p.c.head_dim / 32, G = p.c.head_dim / p.c.group_size;
+    constexpr int F4 = 8 * J;   // float4s per row
+    const int H = p.c.kv_heads, G = 32 * J / p.c.group_size;
     const long long total = (long long)p.c.n_pages * p.c.page_size;
     const int side = blockIdx.y;
     const uint16_t *half = reinterpret_cast<const uint16_t *>(side ? p.c.Vq : p.c.Kq);
     const float2 *sz = reinterpret_cast<const float2 *>(side ? p.c.V_sz : p.c.K_sz);
-    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < p.n_items; i += (long long)gridDim.x * 256) {
-        const long long th = i / p.f4;
-        const int f = (int)(i - th * p.f4);
-        const int t = (int)(th / H), h = (int)(th - (long long)t * H);
-        const int slot = __ldg(p.slots + t);
-        if (slot < 0) continue;
-        if (slot >= total) {
-            const float nan = __int_as_float(0x7fc00000);
-            p.y[side][i] = make_float4(nan, nan, nan, nan);
-            if (f == 0) atomicOr(&g_kv_error, kKvBadSlot);
-            continue;
+    const int t0 = blockIdx.x * p.tokens;
+    const int n = min(p.tokens, p.T - t0) * H * F4;
+    float4 *y = p.y[side] + (size_t)t0 * H * F4;
+    for (int i0 = threadIdx.x; i0 < n; i0 += 256 * kGatherUnroll) {
+        int slot[kGatherUnroll];
+        uint32_t q[kGatherUnroll];
+        float2 m[kGatherUnroll];
+#pragma unroll
+        for (int u = 0; u < kGatherUnroll; ++u) {
+            const int i = i0 + u * 256;
+            slot[u] = i < n ? __ldg(p.slots + t0 + i / (H * F4)) : -1;
         }
-        const int page = slot / p.c.page_size, at = slot - page * p.c.page_size;
-        const size_t row = kv_row(p.c, page, h, at);
-        const int hi = side ? v_half_index(f, J) : 2 * k_word_index(f >> 1, J) + (f & 1);
-        const uint32_t q = half[row * p.f4 + hi];
-        const float2 m = sz[row * G + f * 4 / p.c.group_size];
-        p.y[side][i] = make_float4(__fmul_rn(__fsub_rn((float)(q & 15u), m.y), m.x),
-                                   __fmul_rn(__fsub_rn((float)((q >> 4) & 15u), m.y), m.x),
-                                   __fmul_rn(__fsub_rn((float)((q >> 8) & 15u), m.y), m.x),
-                                   __fmul_rn(__fsub_rn((float)((q >> 12) & 15u), m.y), m.x));
+#pragma unroll
+        for (int u = 0; u < kGatherUnroll; ++u) {
+            const int i = i0 + u * 256, th = i / F4, f = i - th * F4;
+            if (slot[u] >= 0 && slot[u] < total) {
+                const size_t row = kv_row(p.c, slot[u] >> p.shift, th % H, slot[u] & (p.c.page_size - 1));
+                q[u] = half[row * F4 + (side ? v_half_index(f, J) : 2 * k_word_index(f >> 1, J) + (f & 1))];
+                m[u] = sz[row * G + f * 4 / p.c.group_size];
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kGatherUnroll; ++u) {
+            const int i = i0 + u * 256;
+            if (slot[u] < 0) continue;
+            if (slot[u] >= total) {
+                const float nan = __int_as_float(0x7fc00000);
+                y[i] = make_float4(nan, nan, nan, nan);
+                atomicOr(&g_kv_error, kKvBadSlot);
+                continue;
+            }
+            __stcs(y + i, make_float4(__fmul_rn(__fsub_rn((float)(q[u] & 15u), m[u].y), m[u].x),
+                                      __fmul_rn(__fsub_rn((float)((q[u] >> 4) & 15u), m[u].y), m[u].x),
+                                      __fmul_rn(__fsub_rn((float)((q[u] >> 8) & 15u), m[u].y), m[u].x),
+                                      __fmul_rn(__fsub_rn((float)((q[u] >> 12) & 15u), m[u].y), m[u].x)));
+        }
     }
 }
 
 // ---------------------------------------------------------------------------
-// Book-keeping: one CTA; a scan over the requests' rows and pages in tiles
-// of the CTA's threads, then the requests' tokens and table entries.
+// Book-keeping.  Every CTA scans all requests' rows and pages itself, a tile
+// of 1024 requests at a time in shared memory, and then writes its share of
+// the tile's tokens and granted pages: a token finds its request by bisection
+// of the tile's first rows.  So no CTA waits for another, unless lengths or
+// the count are advanced in place: then the CTAs are one cluster, which meets
+// after the tile is read and before it is overwritten.
 // ---------------------------------------------------------------------------
 constexpr int kPlanThreads = 1024;
 
-// Inclusive sum over the CTA's threads.
-__device__ __forceinline__ long long scan_sum(long long v, long long *warp_sums)
+// Inclusive sum over the CTA's threads, and the total.
+__device__ __forceinline__ long long scan_sum(long long v, long long &total, long long *sums)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const long long u = __shfl_up_sync(0xffffffffu, v, o);
         if (lane >= o) v += u;
     }
-    if (lane == 31) warp_sums[warp] = v;
+    if (lane == 31) sums[warp] = v;
     __syncthreads();
-    if (warp == 0) {
-        long long s = warp_sums[lane];
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long u = __shfl_up_sync(0xffffffffu, s, o);
-            if (lane >= o) s += u;
-        }
-        warp_sums[lane] = s;
+    long long s = sums[lane];      // every warp scans the warps' sums itself
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += u;
     }
-    __syncthreads();
-    if (warp > 0) v += warp_sums[warp - 1];
-    const long long total = warp_sums[31];
-    __syncthreads();
-    if (threadIdx.x == 0) warp_sums[0] = total;
-    __syncthreads();
-    return v;
+    total = __shfl_sync(0xffffffffu, s, 31);
+    const long long before = __shfl_sync(0xffffffffu, s, (warp + 31) & 31);
+    return v + (warp > 0 ? before : 0);
 }
 
-__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ PlanCall p)
+// Last i in [0, n) with first[i] <= t, given first[0] <= t.
+__device__ __forceinline__ int find_last(const int *first, int n, int t)
 {
-    __shared__ long long sums[32];
-    const long long room = (long long)p.max_pages * p.page;
+    int lo = 0, hi = n;            // first[lo] <= t < first[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (first[mid] <= t) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+template <bool IN_PLACE>
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ PlanCall p, int shift)
+{
+    __shared__ long long sums[2][32];
+    __shared__ int s_row[kPlanThreads], s_page[kPlanThreads], s_past[kPlanThreads], s_had[kPlanThreads];
+    __shared__ int s_granted;
+    const int cta = blockIdx.x, n_cta = gridDim.x;
+    const long long room = (long long)p.max_pages << shift;
     const int avail = min(max(*p.free_count, 0), p.n_free);
     long long rows_before = 0, pages_before = 0;
-    int granted = 0;   // pages, the same in every thread
-    __shared__ int s_granted;
     if (threadIdx.x == 0) s_granted = 0;
     for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
-        const int b = b0 + threadIdx.x;
+        const int b = b0 + threadIdx.x, n = min(kPlanThreads, p.B - b0);
         const bool in = b < p.B;
         const int past0 = in ? p.past_lens[b] : 0, new0 = in ? p.new_lens[b] : 0;
         const int past = max(past0, 0), fresh = max(new0, 0);
         bool refused = past0 < 0 || new0 < 0;
-        const long long row_end = rows_before + scan_sum(fresh, sums);
-        const long long rows_total = rows_before + sums[0];
-        __syncthreads();
+        long long rows_in, pages_in;
+        const long long row_end = rows_before + scan_sum(fresh, rows_in, sums[0]);
         refused |= (long long)past + fresh > room || row_end > p.T;
         // refused requests aside, past + new stays below 2^31
-        const int had = refused ? 0 : (past + p.page - 1) / p.page;
-        const int need = refused ? 0 : (past + fresh + p.page - 1) / p.page - had;
-        const long long page_end = pages_before + scan_sum(need, sums);
-        const long long pages_total = pages_before + sums[0];
-        __syncthreads();
+        const int had = refused ? 0 : (past + p.page - 1) >> shift;
+        const int need = refused ? 0 : ((past + fresh + p.page - 1) >> shift) - had;
+        const long long page_end = pages_before + scan_sum(need, pages_in, sums[1]);
         if (need > 0 && page_end > avail) refused = true;
-        if (in) {
-            const long long start = min(row_end - fresh, (long long)p.T), end = min(row_end, (long long)p.T);
-            p.query_start[b + 1] = (int)end;
+        s_row[threadIdx.x] = (int)min(row_end - fresh, (long long)p.T);
+        s_page[threadIdx.x] = (int)min(page_end - need, (long long)0x7fffffff);
+        s_past[threadIdx.x] = refused ? -1 : past;
+        s_had[threadIdx.x] = had;
+        if (!refused && need > 0) atomicMax(&s_granted, (int)page_end);
+        if (IN_PLACE) {
+            asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+        } else {
+            __syncthreads();
+        }
+        if (cta == 0 && in) {
+            p.query_start[b + 1] = (int)min(row_end, (long long)p.T);
             if (b == 0) p.query_start[0] = 0;
             p.seq_lens[b] = refused ? past : past + fresh;
-            int32_t *table = p.page_table + (size_t)b * p.max_pages;
-            const long long page_start = page_end - need;
-            if (!refused) {
-                for (int j = 0; j < need; ++j) table[had + j] = p.free_pages[avail - 1 - (page_start + j)];
-                if (need > 0) atomicMax(&s_granted, (int)page_end);
-            } else if (fresh > 0 || past0 < 0 || new0 < 0) {
-                atomicOr(&g_kv_error, kKvRefused);
-            }
-            for (long long t = start; t < end; ++t) {
-                const int pos = refused ? 0 : past + (int)(t - start);
-                p.positions[t] = pos;
-                p.slots[t] = refused ? -1 : table[pos / p.page] * p.page + pos % p.page;
-            }
+            if (refused && (fresh > 0 || past0 < 0 || new0 < 0)) atomicOr(&g_kv_error, kKvRefused);
         }
-        rows_before = rows_total;
-        pages_before = pages_total;
+        // granted pages of this tile
+        const int granted = s_granted;
+        const int page_hi = (int)min(pages_before + pages_in, (long long)granted);
+        for (int k = (int)min(pages_before, (long long)granted) + cta * kPlanThreads + threadIdx.x; k < page_hi;
+             k += n_cta * kPlanThreads) {
+            const int i = find_last(s_page, n, k);
+            p.page_table[(size_t)(b0 + i) * p.max_pages + s_had[i] + (k - s_page[i])] = p.free_pages[avail - 1 - k];
+        }
+        // its tokens
+        const int row_hi = (int)min(rows_before + rows_in, (long long)p.T);
+        for (int t = (int)min(rows_before, (long long)p.T) + cta * kPlanThreads + threadIdx.x; t < row_hi;
+             t += n_cta * kPlanThreads) {
+            const int i = find_last(s_row, n, t);
+            int pos = 0, slot = -1;
+            if (s_past[i] >= 0) {
+                pos = s_past[i] + (t - s_row[i]);
+                const int pg = pos >> shift;
+                // a granted page from the list itself: its table entry may be another CTA's
+                const int id = pg >= s_had[i] ? p.free_pages[avail - 1 - (s_page[i] + pg - s_had[i])]
+                                              : p.page_table[(size_t)(b0 + i) * p.max_pages + pg];
+                slot = (int)((unsigned)id << shift) + (pos & (p.page - 1));
+            }
+            p.positions[t] = pos;
+            p.slots[t] = slot;
+        }
+        rows_before += rows_in;
+        pages_before += pages_in;
+        __syncthreads();
     }
-    __syncthreads();
-    granted = s_granted;
-    for (long long t = min(rows_before, (long long)p.T) + threadIdx.x; t < p.T; t += kPlanThreads) {
+    for (int t = (int)min(rows_before, (long long)p.T) + cta * kPlanThreads + threadIdx.x; t < p.T;
+         t += n_cta * kPlanThreads) {
         p.positions[t] = 0;
         p.slots[t] = -1;
     }
-    if (threadIdx.x == 0) *p.free_count_out = avail - granted;
+    if (cta == 0 && threadIdx.x == 0) *p.free_count_out = avail - s_granted;
 }
 
-cudaError_t device_sms(int &sms)
+}  // namespace
+
+namespace {
+
+int log2_of(int pow2)
 {
-    int dev = 0;
-    cudaError_t err = cudaGetDevice(&dev);
-    if (err != cudaSuccess) return err;
-    return cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    int s = 0;
+    while ((1 << s) < pow2) ++s;
+    return s;
+}
+
+// Tokens per CTA so that each of its threads has `items` of `per_token`.
+int tokens_per_cta(int per_token, int items)
+{
+    const int t = (256 * items + per_token - 1) / per_token;
+    return t < 1 ? 1 : t;
 }
 
 }  // namespace
@@ -235,9 +318,6 @@ cudaError_t device_sms(int &sms)
 cudaError_t launch_kv_append(int T, const gq4_kv_cache &c, const float *k, int ldk, const float *v,
                              int ldv, const int32_t *slots, cudaStream_t stream)
 {
-    int sms = 0;
-    cudaError_t err = device_sms(sms);
-    if (err != cudaSuccess) return err;
     AppendParams p{};
     p.c = c;
     p.x[0] = k;
@@ -245,38 +325,66 @@ cudaError_t launch_kv_append(int T, const gq4_kv_cache &c, const float *k, int l
     p.ld[0] = ldk;
     p.ld[1] = ldv;
     p.slots = slots;
-    p.n_rows = 2ll * T * c.kv_heads;
-    p.wpr = c.head_dim / 8;
-    p.rpw = 32 / p.wpr;
+    p.T = T;
+    p.shift = log2_of(c.page_size);
     p.L = c.group_size / 8;
-    const long long rows_per_block = (long long)p.rpw * (kAppendThreads / 32);
-    const long long want = (p.n_rows + rows_per_block - 1) / rows_per_block, cap = 8ll * sms;
-    append_kernel<<<(unsigned)(want < cap ? want : cap), kAppendThreads, 0, stream>>>(p);
+    // a lane takes two words of a long prompt; one while tokens are few, so
+    // that they spread over the GPU
+    p.tokens = tokens_per_cta(2 * c.kv_heads * (c.head_dim / 8), T >= 1024 ? kAppendUnroll : 1);
+    const unsigned grid = (unsigned)((T + p.tokens - 1) / p.tokens);
+    switch (c.head_dim) {
+    case 64: append_kernel<2><<<grid, kAppendThreads, 0, stream>>>(p); break;
+    case 96: append_kernel<3><<<grid, kAppendThreads, 0, stream>>>(p); break;
+    case 128: append_kernel<4><<<grid, kAppendThreads, 0, stream>>>(p); break;
+    default: append_kernel<8><<<grid, kAppendThreads, 0, stream>>>(p); break;
+    }
     return cudaGetLastError();
 }
 
 cudaError_t launch_kv_gather(int T, const gq4_kv_cache &c, const int32_t *slots, float *k_out,
                              float *v_out, cudaStream_t stream)
 {
-    int sms = 0;
-    cudaError_t err = device_sms(sms);
-    if (err != cudaSuccess) return err;
     GatherParams p{};
     p.c = c;
     p.slots = slots;
     p.y[0] = reinterpret_cast<float4 *>(k_out);
     p.y[1] = reinterpret_cast<float4 *>(v_out);
-    p.f4 = c.head_dim / 4;
-    p.n_items = (long long)T * c.kv_heads * p.f4;
-    const long long want = (p.n_items + 255) / 256, cap = 8ll * sms;
-    gather_kernel<<<dim3((unsigned)(want < cap ? want : cap), 2), 256, 0, stream>>>(p);
+    p.T = T;
+    p.shift = log2_of(c.page_size);
+    p.tokens = tokens_per_cta(c.kv_heads * (c.head_dim / 4), T >= 1024 ? kGatherUnroll : 1);
+    const dim3 grid((unsigned)((T + p.tokens - 1) / p.tokens), 2);
+    switch (c.head_dim) {
+    case 64: gather_kernel<2><<<grid, 256, 0, stream>>>(p); break;
+    case 96: gather_kernel<3><<<grid, 256, 0, stream>>>(p); break;
+    case 128: gather_kernel<4><<<grid, 256, 0, stream>>>(p); break;
+    default: gather_kernel<8><<<grid, 256, 0, stream>>>(p); break;
+    }
     return cudaGetLastError();
 }
 
 cudaError_t launch_kv_plan(const PlanCall &call, cudaStream_t stream)
 {
-    plan_kernel<<<1, kPlanThreads, 0, stream>>>(call);
-    return cudaGetLastError();
+    const int shift = log2_of(call.page);
+    const bool in_place = call.seq_lens == call.past_lens || call.free_count_out == call.free_count;
+    // a CTA for every 4096 token rows; in place at most one portable cluster
+    int grid = (call.T + 4095) / 4096;
+    const int most = in_place ? 8 : 128;
+    grid = grid < 1 ? 1 : grid > most ? most : grid;
+    if (!in_place) {
+        plan_kernel<false><<<(unsigned)grid, kPlanThreads, 0, stream>>>(call, shift);
+        return cudaGetLastError();
+    }
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kPlanThreads);
+    cfg.stream = stream;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)grid;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, plan_kernel<true>, call, shift);
 }
 
 cudaError_t read_kv_device_error(unsigned int *bits, bool clear)

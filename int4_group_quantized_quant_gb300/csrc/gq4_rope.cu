@@ -44,6 +44,42 @@ __device__ __forceinline__ float2 sin_cos_of(int pos, float inv_freq)
     return make_float2(s, c);
 }
 
+// A lane's share of one row: its float4s and, half-split, their partners'.
+template <int CH>
+struct Row {
+    float4 v[CH], w[CH];
+    float4 *y;
+    int side;    // -1: no row
+};
+
+template <int CH>
+__device__ __forceinline__ Row<CH> load_row(const RopeCall &c, int t, int row, int rows, int l)
+{
+    Row<CH> x;
+    const bool live = row < rows;
+    const int s = live && row >= c.heads[0] ? 1 : 0;
+    const int h = s ? row - c.heads[0] : row;
+    x.side = live ? s : -1;
+    x.y = reinterpret_cast<float4 *>(c.y[s] + (size_t)t * c.ldy[s] + (size_t)h * c.D);
+    const float4 *in = reinterpret_cast<const float4 *>(c.x[s] + (size_t)t * c.ldx[s] + (size_t)h * c.D);
+    const int d4 = c.D >> 2, rot4 = c.rot >> 2, half4 = c.rot >> 3;
+#pragma unroll
+    for (int j = 0; j < CH; ++j) {
+        const int i = l + j * 32;
+        x.v[j] = x.w[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (live && i < d4) {
+            x.v[j] = in[i];
+            if (!c.interleaved && i < rot4) x.w[j] = in[i < half4 ? i + half4 : i - half4];
+        }
+    }
+    return x;
+}
+
+__device__ __forceinline__ float4 scaled(float4 a, float r, float4 g)
+{
+    return make_float4(a.x * r * g.x, a.y * r * g.y, a.z * r * g.z, a.w * r * g.w);
+}
+
 // CH: float4 per lane of a row.
 template <int CH>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p)
@@ -52,39 +88,30 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     const RopeCall &c = p.c;
     const int t = blockIdx.x / p.splits, part = blockIdx.x - t * p.splits;
     const int half = c.rot >> 1;
+    const int lpr = p.lpr, per = kRopeThreads / lpr;   // rows at once
+    const int l = threadIdx.x & (lpr - 1);
+    const int stride = per * p.splits;
+    const int d4 = c.D >> 2, rot4 = c.rot >> 2, half4 = c.rot >> 3;
+    int row = part * per + threadIdx.x / lpr;
+    Row<CH> next = load_row<CH>(c, t, row, p.rows, l);
     if (half > 0) {
         const int pos = __ldg(c.positions + t);
         for (int i = threadIdx.x; i < half; i += kRopeThreads) sc[i] = sin_cos_of(pos, __ldg(c.inv_freq + i));
     }
     __syncthreads();
-    const int lpr = p.lpr, per = kRopeThreads / lpr;   // rows at once
-    const int l = threadIdx.x & (lpr - 1);
-    const int stride = per * p.splits;
-    const int d4 = c.D >> 2, rot4 = c.rot >> 2, half4 = c.rot >> 3;
-    // all rows of a warp take the same number of turns (the shuffles below)
+    // every thread takes the same number of turns (the shuffles below); the
+    // next row is on its way while this one is worked on
     for (int row0 = part * per; row0 < p.rows; row0 += stride) {
-        const int row = row0 + threadIdx.x / lpr;
-        const bool live = row < p.rows;
-        const int side = live && row >= c.heads[0];
-        const int h = side ? row - c.heads[0] : row;
-        const float4 *x = reinterpret_cast<const float4 *>(c.x[side] + (size_t)t * c.ldx[side] + (size_t)h * c.D);
-        float4 *y = reinterpret_cast<float4 *>(c.y[side] + (size_t)t * c.ldy[side] + (size_t)h * c.D);
-        const float4 *gain = reinterpret_cast<const float4 *>(c.gain[side]);
-        float4 v[CH], w[CH];
-#pragma unroll
-        for (int j = 0; j < CH; ++j) {
-            const int i = l + j * 32;
-            v[j] = w[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (live && i < d4) {
-                v[j] = x[i];
-                if (!c.interleaved && i < rot4) w[j] = x[i < half4 ? i + half4 : i - half4];
-            }
-        }
+        const Row<CH> x = next;
+        row += stride;
+        if (row0 + stride < p.rows) next = load_row<CH>(c, t, row, p.rows, l);
+        const float4 *gain = reinterpret_cast<const float4 *>(x.side < 0 ? nullptr : c.gain[x.side]);
         float r = 1.0f;
         if (c.gain[0] || c.gain[1]) {  // uniform: the whole warp shuffles
             float s = 0.0f;
 #pragma unroll
-            for (int j = 0; j < CH; ++j) s += v[j].x * v[j].x + v[j].y * v[j].y + v[j].z * v[j].z + v[j].w * v[j].w;
+            for (int j = 0; j < CH; ++j)
+                s += x.v[j].x * x.v[j].x + x.v[j].y * x.v[j].y + x.v[j].z * x.v[j].z + x.v[j].w * x.v[j].w;
             for (int o = lpr >> 1; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
             r = 1.0f / sqrtf(s / (float)c.D + c.eps);
         }
@@ -92,15 +119,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
 #pragma unroll
         for (int j = 0; j < CH; ++j) {
             const int i = l + j * 32;
-            if (!live || i >= d4) continue;
-            float4 a = v[j], b = w[j];
-            if (gain) {
-                const float4 g = __ldg(gain + i);
-                a.x = a.x * r * g.x;
-                a.y = a.y * r * g.y;
-                a.z = a.z * r * g.z;
-                a.w = a.w * r * g.w;
-            }
+            if (x.side < 0 || i >= d4) continue;
+            float4 a = gain ? scaled(x.v[j], r, __ldg(gain + i)) : x.v[j];
             if (i < rot4) {
                 if (c.interleaved) {
                     const float2 s0 = sc[2 * i], s1 = sc[2 * i + 1];
@@ -108,21 +128,15 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
                                     a.z * s1.y - a.w * s1.x, a.w * s1.y + a.z * s1.x);
                 } else {
                     const bool first = i < half4;
-                    const int f = 4 * (first ? i : i - half4);
-                    if (gain) {
-                        const float4 g = __ldg(gain + (first ? i + half4 : i - half4));
-                        b.x = b.x * r * g.x;
-                        b.y = b.y * r * g.y;
-                        b.z = b.z * r * g.z;
-                        b.w = b.w * r * g.w;
-                    }
+                    const int other = first ? i + half4 : i - half4, f = 4 * (first ? i : other);
+                    const float4 b = gain ? scaled(x.w[j], r, __ldg(gain + other)) : x.w[j];
                     const float m = first ? -1.0f : 1.0f;
                     const float2 s0 = sc[f], s1 = sc[f + 1], s2 = sc[f + 2], s3 = sc[f + 3];
                     a = make_float4(a.x * s0.y + m * b.x * s0.x, a.y * s1.y + m * b.y * s1.x,
                                     a.z * s2.y + m * b.z * s2.x, a.w * s3.y + m * b.w * s3.x);
                 }
             }
-            y[i] = a;
+            x.y[i] = a;
         }
     }
 }

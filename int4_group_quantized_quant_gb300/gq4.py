@@ -395,20 +395,32 @@ def embedding(ids, Bq, scales, zeros, group_size, out=None, stream=None):
 # ---------------------------------------------------------------------------
 
 _I32 = (torch.int32,)
+# the current stream's handle without a Stream object around it, where torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _call(fn, name, t, stream, *args):
     """fn(*args, stream) on t's device, on the given stream or that device's current one."""
-    if t.device.index != torch.cuda.current_device():
-        with torch.cuda.device(t.device):
+    index = t.get_device()
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(index):
             return _call(fn, name, t, stream, *args)
-    _check(fn(*args, _stream(stream)), name)
+    _check(fn(*args, _raw_stream(index) if stream is None else stream.cuda_stream), name)
 
 
 def _same_device(first, *others):
+    index = first.get_device()
     for t in others:
-        if t is not None and t.device != first.device:
+        if t is not None and t.get_device() != index:
             raise ValueError(f"tensors on {first.device} and {t.device}")
+
+
+def _at(t, name, dtype, shape):
+    """t's address; _need's checks (its errors), the common case in one expression."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.is_contiguous() and t.shape == shape):
+        _need(t, name, (dtype,), shape)
+    return t.data_ptr()
 
 
 def _rows(t, name, heads_dim=None):
@@ -417,7 +429,7 @@ def _rows(t, name, heads_dim=None):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (no CPU path exists)")
-    if t.dtype != torch.float32:
+    if t.dtype is not torch.float32:
         raise TypeError(f"{name}: dtype {t.dtype} is not torch.float32")
     if t.dim() != 3:
         raise ValueError(f"{name} must be [T, heads, head_dim]")
@@ -436,42 +448,41 @@ def head_norm_rope(q, k, positions, inv_freq, q_gain=None, k_gain=None, eps=1e-6
     (gq4_head_norm_rope).  q [T, heads, D] and k [T, kv_heads, D], either may be None; rows may be
     columns of a wider matrix.  inv_freq f32 [rot_dim / 2], or None for no rotation.  q_out / k_out
     may be q / k themselves."""
-    if q is None and k is None:
+    first = k if q is None else q
+    if first is None:
         raise ValueError("q or k must be given")
-    outs, side = [], []
-    for x, y, name in ((q, q_out, "q"), (k, k_out, "k")):
+    shape, args, outs, gains = None, [], [], []
+    for x, y, gain, name in ((q, q_out, q_gain, "q"), (k, k_out, k_gain, "k")):
         if x is None:
-            if y is not None:
-                raise ValueError(f"{name}_out needs {name}")
+            if y is not None or gain is not None:
+                raise ValueError(f"{name}_out and {name}_gain need {name}")
+            args.append((0, None, 0, None, 0))
             outs.append(None)
-            side.append((0, 0, 0, 0, 0, None, None))
+            gains.append(None)
             continue
         T, H, D, ld = _rows(x, name)
+        if shape is None:
+            shape = (T, D)
+        elif shape != (T, D):
+            raise ValueError(f"{name}: {T} rows of {D} != {shape[0]} rows of {shape[1]}")
         if y is None:
-            y = torch.empty((T, H, D), dtype=torch.float32, device=x.device)
-        ldy = _rows(y, name + "_out", (T, H, D))[3]
+            y, ldy = torch.empty((T, H, D), dtype=torch.float32, device=x.device), H * D
+        else:
+            ldy = _rows(y, name + "_out", (T, H, D))[3]
+        gains.append(None if gain is None else _at(gain, name + "_gain", torch.float32, (D,)))
         outs.append(y)
-        side.append((T, H, D, ld, ldy, x, y))
-    (T, QH, D, ldq, ldqo, _, _), (TK, KH, DK, ldk, ldko, _, _) = side
-    if q is None:
-        T, D = TK, DK
-    elif k is not None and (TK, DK) != (T, D):
-        raise ValueError(f"k: {TK} rows of {DK} != {T} rows of {D}")
-    first = q if q is not None else k
-    rot = 0
+        args.append((H, x.data_ptr(), ld, y.data_ptr(), ldy))
+    T, D = shape
+    rot, at_pos, at_inv = 0, None, None
     if inv_freq is not None:
-        _need(inv_freq, "inv_freq", _F32)
-        _need(positions, "positions", _I32, (T,))
         rot = 2 * inv_freq.numel()
-    for g, name, x in ((q_gain, "q_gain", q), (k_gain, "k_gain", k)):
-        if g is not None:
-            _need(g, name, _F32, (D,))
-            if x is None:
-                raise ValueError(f"{name} needs {name[0]}")
+        at_inv = _at(inv_freq, "inv_freq", torch.float32, (rot // 2,))
+        at_pos = _at(positions, "positions", torch.int32, (T,))
     _same_device(first, k, q_out, k_out, positions, inv_freq, q_gain, k_gain)
-    desc = Rope(_ptr(q_gain), _ptr(k_gain), float(eps), rot, int(bool(interleaved)), _ptr(inv_freq))
-    _call(lib.gq4_head_norm_rope, "gq4_head_norm_rope", first, stream, T, QH, KH, D, ctypes.byref(desc),
-          _ptr(positions), _ptr(q), ldq, _ptr(k), ldk, _ptr(outs[0]), ldqo, _ptr(outs[1]), ldko)
+    desc = Rope(gains[0], gains[1], eps, rot, 1 if interleaved else 0, at_inv)
+    (QH, xq, ldq, yq, ldqo), (KH, xk, ldk, yk, ldko) = args
+    _call(lib.gq4_head_norm_rope, "gq4_head_norm_rope", first, stream, T, QH, KH, D, desc, at_pos, xq, ldq, xk, ldk,
+          yq, ldqo, yk, ldko)
     return outs[0], outs[1]
 
 
@@ -490,28 +501,27 @@ def _cache(Kq, K_sz, Vq, V_sz, group_size):
     _need(Kq, "Kq", _WORDS)
     if Kq.dim() != 4:
         raise ValueError("Kq must be [n_pages, kv_heads, page_size, head_dim/8]")
-    P, H, S, W = Kq.shape
+    shape = P, H, S, W = Kq.shape
     if group_size <= 0 or (8 * W) % group_size != 0:
         raise ValueError("head_dim must be a multiple of group_size")
     sz = (P, H, S, 8 * W // group_size, 2)
-    _need(K_sz, "K_sz", _F32, sz)
-    _need(Vq, "Vq", _WORDS, (P, H, S, W))
-    _need(V_sz, "V_sz", _F32, sz)
+    c = KVCache(P, S, H, 8 * W, group_size, Kq.data_ptr(), _at(K_sz, "K_sz", torch.float32, sz),
+                _at(Vq, "Vq", Kq.dtype, shape), _at(V_sz, "V_sz", torch.float32, sz))
     _same_device(Kq, K_sz, Vq, V_sz)
-    return KVCache(P, S, H, 8 * W, group_size, Kq.data_ptr(), K_sz.data_ptr(), Vq.data_ptr(), V_sz.data_ptr())
+    return c
 
 
 def kv_append(k, v, slots, Kq, K_sz, Vq, V_sz, group_size, stream=None):
     """Quantise rows k, v [T, kv_heads, D] into the cache at slots int32 [T] (gq4_kv_append;
     negative slots are skipped)."""
     c = _cache(Kq, K_sz, Vq, V_sz, group_size)
-    T, _, _, ldk = _rows(k, "k")
-    shape = (T, c.kv_heads, c.head_dim)
-    ldk, ldv = _rows(k, "k", shape)[3], _rows(v, "v", shape)[3]
-    _need(slots, "slots", _I32, (T,))
+    T, H, D, ldk = _rows(k, "k")
+    if (H, D) != (c.kv_heads, c.head_dim):
+        raise ValueError(f"k: {H} heads of {D} != {c.kv_heads} heads of {c.head_dim}")
+    ldv = _rows(v, "v", (T, H, D))[3]
+    at_slots = _at(slots, "slots", torch.int32, (T,))
     _same_device(Kq, k, v, slots)
-    _call(lib.gq4_kv_append, "gq4_kv_append", Kq, stream, T, ctypes.byref(c), _ptr(k), ldk, _ptr(v), ldv,
-          _ptr(slots))
+    _call(lib.gq4_kv_append, "gq4_kv_append", Kq, stream, T, c, k.data_ptr(), ldk, v.data_ptr(), ldv, at_slots)
 
 
 def kv_gather(slots, Kq, K_sz, Vq, V_sz, group_size, k_out=None, v_out=None, stream=None):
@@ -526,11 +536,9 @@ def kv_gather(slots, Kq, K_sz, Vq, V_sz, group_size, k_out=None, v_out=None, str
         k_out = torch.empty(shape, dtype=torch.float32, device=Kq.device)
     if v_out is None:
         v_out = torch.empty(shape, dtype=torch.float32, device=Kq.device)
-    _need(k_out, "k_out", _F32, shape)
-    _need(v_out, "v_out", _F32, shape)
+    at_k, at_v = _at(k_out, "k_out", torch.float32, shape), _at(v_out, "v_out", torch.float32, shape)
     _same_device(Kq, slots, k_out, v_out)
-    _call(lib.gq4_kv_gather, "gq4_kv_gather", Kq, stream, shape[0], ctypes.byref(c), _ptr(slots), _ptr(k_out),
-          _ptr(v_out))
+    _call(lib.gq4_kv_gather, "gq4_kv_gather", Kq, stream, shape[0], c, slots.data_ptr(), at_k, at_v)
     return k_out, v_out
 
 
@@ -543,36 +551,33 @@ def kv_plan(past_lens, new_lens, page_table, free_pages, free_count, n_tokens, p
     if past_lens.dim() != 1:
         raise ValueError("past_lens must be [B]")
     B = past_lens.shape[0]
-    _need(new_lens, "new_lens", _I32, (B,))
     _need(page_table, "page_table", _I32)
     if page_table.dim() != 2 or page_table.shape[0] != B:
         raise ValueError("page_table must be [B, max_pages]")
+    if n_tokens < 0:
+        raise ValueError("n_tokens must not be negative")
     _need(free_pages, "free_pages", _I32)
-    _need(free_count, "free_count", _I32)
-    if free_count.numel() != 1:
-        raise ValueError("free_count must hold one number")
-
-    def out(t, name, n):
+    at_new, at_count = _at(new_lens, "new_lens", torch.int32, (B,)), _at(free_count, "free_count", torch.int32, (1,))
+    given = (("seq_lens", seq_lens, B), ("query_start", query_start, B + 1), ("positions", positions, n_tokens),
+             ("slots", slots, n_tokens), ("free_count_out", free_count_out, 1))
+    # what is not given is a stretch of one allocation
+    spare, at = torch.empty(sum(n for _, t, n in given if t is None), dtype=torch.int32, device=past_lens.device), 0
+    outs, ptrs = [], []
+    for name, t, n in given:
         if t is None:
-            return torch.empty(n, dtype=torch.int32, device=past_lens.device)
-        _need(t, name, _I32)
-        if t.numel() != n:
-            raise ValueError(f"{name}: {t.numel()} values != {n}")
-        return t
-
-    seq_lens, query_start = out(seq_lens, "seq_lens", B), out(query_start, "query_start", B + 1)
-    positions, slots = out(positions, "positions", n_tokens), out(slots, "slots", n_tokens)
-    free_count_out = out(free_count_out, "free_count_out", 1)
-    _same_device(past_lens, new_lens, page_table, free_pages, free_count, seq_lens, query_start, positions, slots,
-                 free_count_out)
+            t, at = spare[at:at + n], at + n
+        outs.append(t)
+        ptrs.append(_at(t, name, torch.int32, (n,)))
+    _same_device(past_lens, new_lens, page_table, free_pages, free_count, *outs)
+    lens, starts, pos, slt, left = ptrs
     _call(lib.gq4_kv_plan, "gq4_kv_plan", past_lens, stream, B, n_tokens, page_size, page_table.shape[1],
-          free_pages.numel(), _ptr(past_lens), _ptr(new_lens), _ptr(page_table), _ptr(free_pages),
-          _ptr(free_count), _ptr(free_count_out), _ptr(seq_lens), _ptr(query_start), _ptr(positions), _ptr(slots))
-    return seq_lens, query_start, positions, slots, free_count_out
+          free_pages.numel(), past_lens.data_ptr(), at_new, page_table.data_ptr(), free_pages.data_ptr(), at_count,
+          left, lens, starts, pos, slt)
+    return tuple(outs)
 
 
 def kv_attention_workspace_bytes(T, heads, kv_heads, head_dim) -> int:
-    return int(lib.gq4_kv_attention_workspace_bytes(T, heads, kv_heads, head_dim))
+    return lib.gq4_kv_attention_workspace_bytes(T, heads, kv_heads, head_dim)
 
 
 def kv_attention(q, query_start, seq_lens, page_table, Kq, K_sz, Vq, V_sz, group_size, scale, max_query,
@@ -586,23 +591,26 @@ def kv_attention(q, query_start, seq_lens, page_table, Kq, K_sz, Vq, V_sz, group
     if D != c.head_dim:
         raise ValueError(f"q: head_dim {D} != {c.head_dim}")
     _need(seq_lens, "seq_lens", _I32)
-    B = seq_lens.numel()
-    _need(query_start, "query_start", _I32, (B + 1,))
+    if seq_lens.dim() != 1:
+        raise ValueError("seq_lens must be [B]")
+    B = seq_lens.shape[0]
+    at_start = _at(query_start, "query_start", torch.int32, (B + 1,))
     _need(page_table, "page_table", _I32)
     if page_table.dim() != 2 or page_table.shape[0] != B:
         raise ValueError("page_table must be [B, max_pages]")
     if out is None:
-        out = torch.empty((T, H, D), dtype=torch.float32, device=q.device)
-    ldo = _rows(out, "out", (T, H, D))[3]
+        out, ldo = torch.empty((T, H, D), dtype=torch.float32, device=q.device), H * D
+    else:
+        ldo = _rows(out, "out", (T, H, D))[3]
     if workspace is None:
         workspace = torch.empty(kv_attention_workspace_bytes(T, H, c.kv_heads, D), dtype=torch.uint8,
                                 device=q.device)
     elif not (isinstance(workspace, torch.Tensor) and workspace.is_cuda and workspace.is_contiguous()):
         raise ValueError("workspace must be a contiguous CUDA tensor")
     _same_device(Kq, q, query_start, seq_lens, page_table, out, workspace)
-    _call(lib.gq4_kv_attention, "gq4_kv_attention", Kq, stream, B, T, H, page_table.shape[1], max_query, max_len,
-          ctypes.byref(c), _ptr(q), ldq, _ptr(query_start), _ptr(seq_lens), _ptr(page_table), float(scale), window,
-          _ptr(out), ldo, _ptr(workspace), workspace.numel() * workspace.element_size())
+    _call(lib.gq4_kv_attention, "gq4_kv_attention", Kq, stream, B, T, H, page_table.shape[1], max_query, max_len, c,
+          q.data_ptr(), ldq, at_start, seq_lens.data_ptr(), page_table.data_ptr(), scale, window, out.data_ptr(), ldo,
+          workspace.data_ptr(), workspace.nbytes)
     return out
 
 
