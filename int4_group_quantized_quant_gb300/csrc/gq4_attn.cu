@@ -55,6 +55,7 @@ constexpr int kStageKeys = 32;                    // per warp
 constexpr int kStepKeys = kStageKeys * kWarps;    // per CTA
 constexpr float kSlack = 4.0f;                    // log2 of how far a weight may pass the maximum
 constexpr int kPieceBits = 11;                    // p s <= 2^kSlack is held times 2^11: below 2^15
+constexpr int kCarry = 4;                         // stages summed in the tensor core
 constexpr int kMaxGrid = 512;                    // CTAs (the workspace's slots)
 
 struct SplitParams {
@@ -98,6 +99,16 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The same onto zero.
+__device__ __forceinline__ void mma16816_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
@@ -183,6 +194,23 @@ __device__ __forceinline__ Halves<J> load_halves(uint32_t s)
     return h;
 }
 
+// A lane's J words of a key row; J = 8: two 16-byte pieces whose places differ in bit 4.
+template <int J>
+__device__ __forceinline__ void load_key(uint32_t at, uint32_t (&w)[J])
+{
+    if constexpr (J == 8) {
+        uint32_t t[4];
+        load_words<4>(at, t);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = t[i];
+        load_words<4>(at ^ 16u, t);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[4 + i] = t[i];
+    } else {
+        load_words<J>(at, w);
+    }
+}
+
 __device__ __forceinline__ float2 lds_f2(uint32_t s)
 {
     float2 v;
@@ -239,6 +267,23 @@ __device__ __forceinline__ long long cta_scan(long long v, long long &total, lon
     return before + inc - v;
 }
 
+// o += the two pieces' sums, which start again at zero.
+template <int NB, int J>
+__device__ __forceinline__ void carry(float (&o)[NB][J][4], float (&t0)[NB][J][4], float (&t1)[NB][J][4])
+{
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int u = 0; u < J; ++u) {
+            o[nb][u][0] += t0[nb][u][0] + t0[nb][u][1];
+            o[nb][u][1] += t0[nb][u][2] + t0[nb][u][3];
+            o[nb][u][2] += t1[nb][u][0] + t1[nb][u][1];
+            o[nb][u][3] += t1[nb][u][2] + t1[nb][u][3];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) t0[nb][u][i] = t1[nb][u][i] = 0.0f;
+        }
+}
+
 template <int J, int G, int NB, int STAGES, int MINB>
 __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid_constant__ SplitParams p)
 {
@@ -247,46 +292,59 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ long long s_sums[kWarps];
     __shared__ long long s_at;
-    __shared__ int s_b;
+    __shared__ int s_b, s_special;
+    __shared__ float s_row[NB][4][G + 1];   // a query row's sums per group and its factor
     const AttnCall &a = p.a;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, c = lane & 3;
     const int H = a.c.kv_heads, R = a.heads / H;
 
-    // ---- requests that need no sums: bad ones, and those without keys ----
-    for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-        const AttnRequest r = attn_request(a, b);
-        if (!r.bad && !(r.n > 0 && r.len == 0)) continue;
-        if (r.bad && threadIdx.x == 0) atomicOr(&g_attn_error, kAttnBadRequest);
-        const float v = r.bad ? quiet_nan() : 0.0f;
-        const int per = a.heads * D;
-        for (int row = r.fill0; row < r.fill1; ++row)
-            for (int i = threadIdx.x; i < per; i += kThreads) a.out[(size_t)row * a.ldo + i] = v;
-    }
-
     // ---- this CTA's range of steps ----
-    long long total = 0, before = 0;
+    if (threadIdx.x == 0) {
+        s_special = 0;
+        p.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    }
+    __syncthreads();
+    long long total = 0, before = 0, mine = 0;
     for (int b0 = 0; b0 < a.B; b0 += kThreads) {
         const int b = b0 + threadIdx.x;
-        const long long w = b < a.B ? work_of<ROWS>(a, attn_request(a, b)).total : 0;
+        mine = 0;
+        if (b < a.B) {
+            const AttnRequest r = attn_request(a, b);
+            mine = work_of<ROWS>(a, r).total;
+            if (r.bad || (r.n > 0 && r.len == 0)) s_special = 1;
+        }
         long long t;
-        before = cta_scan(w, t, s_sums);
+        before = cta_scan(mine, t, s_sums);
         total += t;
     }
-    if (threadIdx.x == 0) p.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
     const long long chunk = (total + gridDim.x - 1) / gridDim.x;
     const long long begin = chunk * blockIdx.x;
     const long long end = min(begin + chunk, total);
+    // requests that need no sums: bad ones, and those without keys
+    __syncthreads();
+    if (s_special) {
+        for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+            const AttnRequest r = attn_request(a, b);
+            if (!r.bad && !(r.n > 0 && r.len == 0)) continue;
+            if (r.bad && threadIdx.x == 0) atomicOr(&g_attn_error, kAttnBadRequest);
+            const float v = r.bad ? quiet_nan() : 0.0f;
+            const int per = a.heads * D;
+            for (int row = r.fill0; row < r.fill1; ++row)
+                for (int i = threadIdx.x; i < per; i += kThreads) a.out[(size_t)row * a.ldo + i] = v;
+        }
+    }
     if (begin >= end) return;
     {
         long long base = 0;
         for (int b0 = 0; b0 < a.B; b0 += kThreads) {
             const int b = b0 + threadIdx.x;
-            const long long w = b < a.B ? work_of<ROWS>(a, attn_request(a, b)).total : 0;
-            long long t;
-            if (a.B > kThreads) before = cta_scan(w, t, s_sums);
-            else t = total;
-            if (begin >= base + before && begin < base + before + w) {
+            long long t = total;
+            if (a.B > kThreads) {
+                mine = b < a.B ? work_of<ROWS>(a, attn_request(a, b)).total : 0;
+                before = cta_scan(mine, t, s_sums);
+            }
+            if (begin >= base + before && begin < base + before + mine) {
                 s_b = b;
                 s_at = begin - (base + before);
             }
@@ -297,110 +355,55 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
     }
 
     const uint32_t ring = smem_addr(smem) + (uint32_t)warp * STAGES * S::kBytes;
+    const uint32_t q_s = smem_addr(smem) + kWarps * STAGES * S::kBytes;   // the unit's query pieces
     float *own = reinterpret_cast<float *>(smem + (size_t)warp * STAGES * S::kBytes);   // after a unit
     int b = s_b;
     AttnRequest rq = attn_request(a, b);
     Work wk = work_of<ROWS>(a, rq);
-    long long at = s_at;              // step within the request
     long long pos = begin;
+    int unit, from;                   // of the request: (kv head, row block), key step
+    {
+        const long long at = s_at;
+        unit = (int)(at / wk.steps);
+        from = (int)(at - (long long)unit * wk.steps);
+    }
+    // this lane's places in a stage: keys, values (the keys of rows 2c and 2c + 1), scales
+    const int ka0 = key_of_row(g), vk0 = c, vk1 = 4 + (c ^ 3);
+    const uint32_t kof = J == 8   ? ka0 * 128 + (((2 * c) ^ swizzle<J>(ka0)) << 4)
+                         : J == 4 ? ka0 * 64 + ((c ^ swizzle<J>(ka0)) << 4)
+                                  : ka0 * 16 * J + 4 * J * c;
+    auto v_place = [&](int key) -> uint32_t {
+        return S::kCodes + key * 16 * J +
+               (J == 8   ? (g ^ swizzle<J>(key)) << 4
+                : J == 4 ? (((g >> 1) ^ swizzle<J>(key)) << 4) + (g & 1) * 8
+                         : 2 * J * g);
+    };
+    const uint32_t vof0 = v_place(vk0), vof1 = v_place(vk1);
+    const uint32_t sof = 2 * S::kCodes + ka0 * 8 * G;
+    // where this lane's first 16-byte piece of 16 rows goes (the next ones 512 bytes on)
+    const uint32_t pof = (lane / J) * 16 * J + (((lane % J) ^ swizzle<J>(lane / J)) << 4);
+    const int shift = 31 - __clz(a.c.page_size);
+    const uint32_t page_rows = (uint32_t)(H * a.c.page_size);   // below 2^18
+    const uint32_t n_pages = (uint32_t)a.c.n_pages;
     while (pos < end) {
-        const int unit = (int)(at / wk.steps);
-        const int from = (int)(at - (long long)unit * wk.steps);
         const int upto = (int)min((long long)wk.steps, from + (end - pos));
         const int h = unit / wk.blocks, rb = unit - h * wk.blocks;
         const int rows_all = rq.n * R;
-
-        // ---- query rows: two fp16 pieces, power-of-two scaled per row ----
-        uint32_t qf[NB][J][4];
-        float qs[NB][G], F[NB];
-        int last[NB], first[NB];
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-            const int rho = rb * ROWS + nb * 4 + (g >> 1);     // the row this thread's column holds
-            float x[J][8];
-            float big = 0.0f;
-            const bool in = rho < rows_all;
-            const int j = in ? rho / R : 0, r = in ? rho - j * R : 0;
-            const float *q = a.q + (size_t)(rq.row0 + j) * a.ldq + (size_t)(h * R + r) * D + 8 * c;
-#pragma unroll
-            for (int u = 0; u < J; ++u) {
-                float4 v0 = make_float4(0.f, 0.f, 0.f, 0.f), v1 = v0;
-                if (in) {
-                    v0 = __ldg(reinterpret_cast<const float4 *>(q + 32 * u));
-                    v1 = __ldg(reinterpret_cast<const float4 *>(q + 32 * u) + 1);
-                }
-                x[u][0] = v0.x; x[u][1] = v0.y; x[u][2] = v0.z; x[u][3] = v0.w;
-                x[u][4] = v1.x; x[u][5] = v1.y; x[u][6] = v1.z; x[u][7] = v1.w;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) big = fmaxf(big, fabsf(x[u][i]));
-            }
-            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
-            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-            // 2^k times the row lies in [2^13, 2^14) at its largest
-            int e = (int)((__float_as_uint(big) >> 23) & 255u);
-            int k = 13 + 127 - e;
-            k = big > 0.0f ? min(k, 120) : 0;
-            const float up = exp2f((float)k);
-            float sum[G];
-#pragma unroll
-            for (int gr = 0; gr < G; ++gr) sum[gr] = 0.0f;
-            const bool lo = g & 1;
-#pragma unroll
-            for (int u = 0; u < J; ++u) {
-                __half v[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float y = x[u][i] * up;
-                    const float hi = __half2float(__float2half_rn(y));
-                    sum[u / UG] += y;
-                    // odd nibbles are masked at 16 times their value
-                    v[i] = __float2half_rn((lo ? y - hi : hi) * ((i & 1) ? 0.0625f : 1.0f));
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const __half2 pr = __halves2half2(v[i], v[i + 4]);
-                    qf[nb][u][i] = *reinterpret_cast<const uint32_t *>(&pr);
-                }
-            }
-            // constants of row c (the row of this thread's sums), from a lane that holds it
-            const int src = 8 * c;
-#pragma unroll
-            for (int gr = 0; gr < G; ++gr) {
-                float s = sum[gr];
-                s += __shfl_xor_sync(0xffffffffu, s, 1);
-                s += __shfl_xor_sync(0xffffffffu, s, 2);
-                qs[nb][gr] = __shfl_sync(0xffffffffu, s, src) * 0x1p-24f;
-            }
-            const int kc = __shfl_sync(0xffffffffu, k, src);
-            F[nb] = ldexpf(a.scale * kLog2e, 24 - kc);
-            const int rc = rb * ROWS + nb * 4 + c;
-            last[nb] = rc < rows_all ? rq.len - rq.n + rc / R : -1;
-            first[nb] = attn_first(a, last[nb]);
-        }
         // keys that some row of the block sees; keys that all of its rows see
         const int row_hi = min(rb * ROWS + ROWS, rows_all) - 1;
         const int see_hi = rq.len - rq.n + row_hi / R;                                  // inclusive
         const int all_hi = rq.len - rq.n + rb * ROWS / R;
         const int see_lo = attn_first(a, max(all_hi, -1)), all_lo = attn_first(a, see_hi);
 
-        float o[NB][J][4], zs[NB][G], l[NB], m[NB];
-        float vs = 0x1p111f, vref = 0x1p-100f;                 // 2^(11 - E), 2^E
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-            l[nb] = 0.0f;
-            m[nb] = -INFINITY;
-#pragma unroll
-            for (int gr = 0; gr < G; ++gr) zs[nb][gr] = 0.0f;
-#pragma unroll
-            for (int u = 0; u < J; ++u)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) o[nb][u][i] = 0.0f;
-        }
-
         const int32_t *table = a.page_table + (size_t)b * a.max_pages;
-        const int shift = 31 - __clz(a.c.page_size);
         const int key00 = (wk.step0 + from) * kStepKeys + warp * kStageKeys;
         const int iters = upto - from;
+        // this lane's first 16-byte piece of a page's rows of this head
+        const size_t head_row = (size_t)h * a.c.page_size;
+        const char *k_at = reinterpret_cast<const char *>(a.c.Kq) + head_row * (D / 2) + 16 * lane;
+        const char *v_at = reinterpret_cast<const char *>(a.c.Vq) + head_row * (D / 2) + 16 * lane;
+        const char *ks_at = reinterpret_cast<const char *>(a.c.K_sz) + head_row * (8 * G);
+        const char *vs_at = reinterpret_cast<const char *>(a.c.V_sz) + head_row * (8 * G);
         // the two pages (16 keys each) of iteration i; -1 where nothing is seen
         auto pages_of = [&](int i) {
             int2 pg = make_int2(-1, -1);
@@ -415,37 +418,35 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
             const int k0 = key00 + i * kStepKeys;
             if (i < iters && k0 <= see_hi && k0 + 32 > see_lo) {
                 const uint32_t st = ring + (uint32_t)slot * S::kBytes;
-                size_t row[2];
-                bool ok[2], seen[2];
+                const bool ok[2] = {(uint32_t)pg.x < n_pages, (uint32_t)pg.y < n_pages};
+                const uint32_t at[2] = {(uint32_t)k0 & (a.c.page_size - 1), (uint32_t)(k0 + 16) & (a.c.page_size - 1)};
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const int page = x ? pg.y : pg.x, kx = k0 + 16 * x;
-                    seen[x] = kx <= see_hi && kx + 16 > see_lo;
-                    ok[x] = seen[x] && page >= 0 && page < a.c.n_pages;
-                    row[x] = ok[x] ? kv_row(a.c, page, h, kx & (a.c.page_size - 1)) : 0;
-                }
+                for (int x = 0; x < 2; ++x) {                  // 16 J pieces of 16 rows, contiguous
+                    if (!ok[x]) continue;
+                    const size_t off = (size_t)(uint32_t)(x ? pg.y : pg.x) * (page_rows * (D / 2)) + at[x] * (D / 2);
+                    const char *ks = k_at + off, *vp = v_at + off;
 #pragma unroll
-                for (int j = 0; j < J; ++j) {                  // 32 J pieces of 16 bytes, keys then values
-                    const int piece = 32 * j + lane;
-                    const int key = piece / J, pc = piece - key * J;
-                    const int x = key >> 4;
-                    const uint32_t dst = st + key * 16 * J + ((pc ^ swizzle<J>(key)) << 4);
-                    if (x ? ok[1] : ok[0]) {
-                        const size_t off = ((x ? row[1] : row[0]) + (key & 15)) * (size_t)(D / 2) + 16 * pc;
-                        cp_async_16(dst, reinterpret_cast<const char *>(a.c.Kq) + off);
-                        cp_async_16(dst + S::kCodes, reinterpret_cast<const char *>(a.c.Vq) + off);
+                    for (int j = 0; j < (16 * J + 31) / 32; ++j) {
+                        uint32_t dst = st + x * 256 * J;
+                        dst += J % 2 == 0 ? pof + 512 * j : (32 * j + lane) * 16;   // (odd J: no swizzle)
+                        if (J % 2 == 0 || 32 * j + lane < 16 * J) {
+                            cp_async_16(dst, ks + 512 * j);
+                            cp_async_16(dst + S::kCodes, vp + 512 * j);
+                        }
                     }
                 }
 #pragma unroll
-                for (int j = 0; j < G; ++j) {                  // scales and zeros: 16 G pieces each
+                for (int j = 0; j < G; ++j) {                  // scales and zeros: 16 G pieces each side
                     const int piece = 32 * j + lane;
                     const int side = piece >= 16 * G, pc = piece - side * 16 * G;
                     const int x = pc >= 8 * G;
-                    const uint32_t dst = st + 2 * S::kCodes + side * S::kSz + pc * 16;
+                    const uint32_t dst = st + 2 * S::kCodes + piece * 16;
                     if (x ? ok[1] : ok[0]) {
-                        const size_t off = (x ? row[1] : row[0]) * (size_t)(8 * G) + (pc - x * 8 * G) * 16;
-                        cp_async_16(dst, reinterpret_cast<const char *>(side ? a.c.V_sz : a.c.K_sz) + off);
-                    } else if (x ? seen[1] : seen[0]) {        // a page outside the pool: NaN rows
+                        const size_t off = (size_t)(uint32_t)(x ? pg.y : pg.x) * (page_rows * (8 * G)) +
+                                           ((x ? at[1] : at[0]) * (8 * G) + (pc - x * 8 * G) * 16);
+                        cp_async_16(dst, (side ? vs_at : ks_at) + off);
+                    } else if (x ? k0 + 16 <= see_hi && k0 + 32 > see_lo : k0 <= see_hi && k0 + 16 > see_lo) {
+                        // a page outside the pool: NaN rows
                         const float nan = quiet_nan();
                         asm volatile("st.shared.v4.f32 [%0], {%1,%1,%1,%1};" ::"r"(dst), "f"(nan) : "memory");
                         atomicOr(&g_attn_error, kAttnBadRequest);
@@ -461,6 +462,100 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
             issue(i, i, pg);
             pg = nx;
         }
+
+        // ---- query rows, while the first keys come: two fp16 pieces, scaled
+        // by a power of two per row, for all warps in shared memory ----
+        if (warp < NB) {
+            const int nb = warp;
+            const int rho = rb * ROWS + nb * 4 + (g >> 1);     // the row this thread's column holds
+            const bool in = rho < rows_all;
+            const int j = in ? rho / R : 0, r = in ? rho - j * R : 0;
+            const float *q = a.q + (size_t)(rq.row0 + j) * a.ldq + (size_t)(h * R + r) * D + 8 * c;
+            float x[J][8];
+            float big = 0.0f;
+#pragma unroll
+            for (int u = 0; u < J; ++u) {
+                float4 v0 = make_float4(0.f, 0.f, 0.f, 0.f), v1 = v0;
+                if (in) {
+                    v0 = __ldg(reinterpret_cast<const float4 *>(q + 32 * u));
+                    v1 = __ldg(reinterpret_cast<const float4 *>(q + 32 * u) + 1);
+                }
+                x[u][0] = v0.x; x[u][1] = v0.y; x[u][2] = v0.z; x[u][3] = v0.w;
+                x[u][4] = v1.x; x[u][5] = v1.y; x[u][6] = v1.z; x[u][7] = v1.w;
+            }
+#pragma unroll
+            for (int u = 0; u < J; ++u)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) big = fmaxf(big, fabsf(x[u][i]));
+            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+            // 2^k times the row lies in [2^13, 2^14) at its largest
+            const int e = (int)((__float_as_uint(big) >> 23) & 255u);
+            const int k = big > 0.0f ? min(13 + 127 - e, 120) : 0;
+            const float up = exp2f((float)k);
+            float sum[G];
+#pragma unroll
+            for (int gr = 0; gr < G; ++gr) sum[gr] = 0.0f;
+            const bool lo = g & 1;
+#pragma unroll
+            for (int u = 0; u < J; ++u) {
+                uint32_t f[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float z[2];
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const float v = x[u][i + 4 * y] * up;
+                        const float hi = __half2float(__float2half_rn(v));
+                        sum[u / UG] += v;
+                        // odd nibbles are masked at 16 times their value
+                        z[y] = (lo ? v - hi : hi) * ((i & 1) ? 0.0625f : 1.0f);
+                    }
+                    const __half2 pr = __floats2half2_rn(z[0], z[1]);
+                    f[i] = *reinterpret_cast<const uint32_t *>(&pr);
+                }
+                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(q_s + ((nb * J + u) * 32 + lane) * 16),
+                             "r"(f[0]), "r"(f[1]), "r"(f[2]), "r"(f[3])
+                             : "memory");
+            }
+#pragma unroll
+            for (int gr = 0; gr < G; ++gr) {
+                float t = sum[gr];
+                t += __shfl_xor_sync(0xffffffffu, t, 1);
+                t += __shfl_xor_sync(0xffffffffu, t, 2);
+                if (c == 0 && !lo) s_row[nb][g >> 1][gr] = t * 0x1p-24f;
+            }
+            if (c == 0 && !lo) s_row[nb][g >> 1][G] = ldexpf(a.scale * kLog2e, 24 - k);
+        }
+        __syncthreads();
+        float qs[NB][G], F[NB];                                // of row c
+        int last[NB], first[NB];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+            for (int gr = 0; gr < G; ++gr) qs[nb][gr] = s_row[nb][c][gr];
+            F[nb] = s_row[nb][c][G];
+            const int rc = rb * ROWS + nb * 4 + c;
+            last[nb] = rc < rows_all ? rq.len - rq.n + rc / R : -1;
+            first[nb] = attn_first(a, last[nb]);
+        }
+
+        // o: f32 sums; t: the tensor core's, added to o every kCarry stages
+        float o[NB][J][4], t0[NB][J][4], t1[NB][J][4], zs[NB][G], l[NB], m[NB];
+        int carried = 0;
+        float vs = 0x1p111f, vref = 0x1p-100f;                 // 2^(11 - E), 2^E
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+            l[nb] = 0.0f;
+            m[nb] = -INFINITY;
+#pragma unroll
+            for (int gr = 0; gr < G; ++gr) zs[nb][gr] = 0.0f;
+#pragma unroll
+            for (int u = 0; u < J; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[nb][u][i] = t0[nb][u][i] = t1[nb][u][i] = 0.0f;
+        }
+
         int slot = 0, fill = STAGES - 1;
         for (int i = 0; i < iters; ++i) {
             {
@@ -478,64 +573,55 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
 
             // ---- exponents: keys times query rows ----
             float w[2][2][NB];                                 // [16 keys][key row g, g + 8][row]
-            const uint32_t magic = 0x64006400u;
+            {
+                uint32_t wa[2][J], wb[2][J];
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const int ka = 16 * x + key_of_row(g), kb = ka + 8;
-                uint32_t wa[J], wb[J];
-                if constexpr (J == 8) {                        // two swizzled 16-byte pieces
-                    uint32_t t4[4];
-                    load_words<4>(st + ka * 128 + (((2 * c) ^ swizzle<J>(ka)) << 4), t4);
-                    for (int i4 = 0; i4 < 4; ++i4) wa[i4] = t4[i4];
-                    load_words<4>(st + ka * 128 + (((2 * c + 1) ^ swizzle<J>(ka)) << 4), t4);
-                    for (int i4 = 0; i4 < 4; ++i4) wa[4 + i4] = t4[i4];
-                    load_words<4>(st + kb * 128 + (((2 * c) ^ swizzle<J>(kb)) << 4), t4);
-                    for (int i4 = 0; i4 < 4; ++i4) wb[i4] = t4[i4];
-                    load_words<4>(st + kb * 128 + (((2 * c + 1) ^ swizzle<J>(kb)) << 4), t4);
-                    for (int i4 = 0; i4 < 4; ++i4) wb[4 + i4] = t4[i4];
-                } else if constexpr (J == 4) {
-                    load_words<J>(st + ka * 64 + ((c ^ swizzle<J>(ka)) << 4), wa);
-                    load_words<J>(st + kb * 64 + ((c ^ swizzle<J>(kb)) << 4), wb);
-                } else {
-                    load_words<J>(st + ka * 16 * J + 4 * J * c, wa);
-                    load_words<J>(st + kb * 16 * J + 4 * J * c, wb);
+                for (int x = 0; x < 2; ++x) {
+                    load_key<J>(st + kof + 256 * J * x, wa[x]);
+                    load_key<J>(st + kof + 256 * J * x + 128 * J, wb[x]);
                 }
-                float acc[NB][4];
-#pragma unroll
-                for (int nb = 0; nb < NB; ++nb) w[x][0][nb] = w[x][1][nb] = 0.0f;
+                float acc[2][NB][4];
 #pragma unroll
                 for (int u = 0; u < J; ++u) {
-                    if (u % UG == 0) {
+                    uint32_t qf[NB][4];
 #pragma unroll
-                        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                            for (int i4 = 0; i4 < 4; ++i4) acc[nb][i4] = 0.0f;
-                    }
-                    const uint32_t ha = wa[u] >> 8, hb = wb[u] >> 8;
+                    for (int nb = 0; nb < NB; ++nb)
+                        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                                     : "=r"(qf[nb][0]), "=r"(qf[nb][1]), "=r"(qf[nb][2]), "=r"(qf[nb][3])
+                                     : "r"(q_s + ((nb * J + u) * 32 + lane) * 16));
                     const uint32_t m0 = 0x000F000Fu, m1 = 0x00F000F0u;
 #pragma unroll
-                    for (int nb = 0; nb < NB; ++nb) {
-                        mma16816(acc[nb], wa[u] & m0, wb[u] & m0, wa[u] & m1, wb[u] & m1, qf[nb][u][0], qf[nb][u][1]);
-                        mma16816(acc[nb], ha & m0, hb & m0, ha & m1, hb & m1, qf[nb][u][2], qf[nb][u][3]);
-                    }
-                    if (u % UG == UG - 1) {
-                        const int gr = u / UG;
-                        const float2 sa = lds_f2(st + 2 * S::kCodes + (ka * G + gr) * 8);
-                        const float2 sb = lds_f2(st + 2 * S::kCodes + (kb * G + gr) * 8);
+                    for (int x = 0; x < 2; ++x) {
+                        const uint32_t va = wa[x][u], vb = wb[x][u], ha = va >> 8, hb = vb >> 8;
 #pragma unroll
                         for (int nb = 0; nb < NB; ++nb) {
-                            const float ta = fmaf(-sa.y, qs[nb][gr], acc[nb][0] + acc[nb][1]);
-                            const float tb = fmaf(-sb.y, qs[nb][gr], acc[nb][2] + acc[nb][3]);
-                            w[x][0][nb] = fmaf(sa.x, ta, w[x][0][nb]);
-                            w[x][1][nb] = fmaf(sb.x, tb, w[x][1][nb]);
+                            if (u % UG == 0)
+                                mma16816_zero(acc[x][nb], va & m0, vb & m0, va & m1, vb & m1, qf[nb][0], qf[nb][1]);
+                            else
+                                mma16816(acc[x][nb], va & m0, vb & m0, va & m1, vb & m1, qf[nb][0], qf[nb][1]);
+                            mma16816(acc[x][nb], ha & m0, hb & m0, ha & m1, hb & m1, qf[nb][2], qf[nb][3]);
+                        }
+                        if (u % UG == UG - 1) {
+                            const int gr = u / UG;
+                            const float2 sa = lds_f2(st + sof + (16 * x * G + gr) * 8);
+                            const float2 sb = lds_f2(st + sof + ((16 * x + 8) * G + gr) * 8);
+#pragma unroll
+                            for (int nb = 0; nb < NB; ++nb) {
+                                const float ta = fmaf(-sa.y, qs[nb][gr], acc[x][nb][0] + acc[x][nb][1]);
+                                const float tb = fmaf(-sb.y, qs[nb][gr], acc[x][nb][2] + acc[x][nb][3]);
+                                w[x][0][nb] = gr == 0 ? sa.x * ta : fmaf(sa.x, ta, w[x][0][nb]);
+                                w[x][1][nb] = gr == 0 ? sb.x * tb : fmaf(sb.x, tb, w[x][1][nb]);
+                            }
                         }
                     }
                 }
 #pragma unroll
-                for (int nb = 0; nb < NB; ++nb) {
-                    w[x][0][nb] *= F[nb];
-                    w[x][1][nb] *= F[nb];
-                }
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) {
+                        w[x][0][nb] *= F[nb];
+                        w[x][1][nb] *= F[nb];
+                    }
             }
 
             // ---- values' scales; what a row does not see ----
@@ -544,10 +630,9 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
             for (int x = 0; x < 2; ++x)
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
-                    const int key = 16 * x + key_of_row(g) + 8 * y;
 #pragma unroll
                     for (int gr = 0; gr < G; ++gr)
-                        vz[x][y][gr] = lds_f2(st + 2 * S::kCodes + S::kSz + (key * G + gr) * 8);
+                        vz[x][y][gr] = lds_f2(st + sof + S::kSz + ((16 * x + 8 * y) * G + gr) * 8);
                 }
             const bool masked = k0 + kStageKeys - 1 > all_hi || k0 < all_lo;   // uniform
             uint32_t hidden = 0;                               // bit (x, y, nb)
@@ -558,14 +643,23 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
                     for (int y = 0; y < 2; ++y)
 #pragma unroll
                         for (int nb = 0; nb < NB; ++nb) {
-                            const int key = k0 + 16 * x + key_of_row(g) + 8 * y;
+                            const int key = k0 + 16 * x + ka0 + 8 * y;
                             if (key > last[nb] || key < first[nb]) {
                                 hidden |= 1u << ((x * 2 + y) * NB + nb);
                                 w[x][y][nb] = -INFINITY;
                             }
                         }
+                // scales of keys that none of this thread's rows sees may be rubbish
+                constexpr uint32_t kAllRows = (1u << NB) - 1u;
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y)
+                        if (((hidden >> ((x * 2 + y) * NB)) & kAllRows) == kAllRows) {
+#pragma unroll
+                            for (int gr = 0; gr < G; ++gr) vz[x][y][gr] = make_float2(0.0f, 0.0f);
+                        }
             }
-            constexpr uint32_t kAllRows = (1u << NB) - 1u;
             // ---- the references m and E still hold? ----
             float top[NB], vtop = 0.0f;
             bool move = false;
@@ -577,11 +671,9 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
 #pragma unroll
             for (int x = 0; x < 2; ++x)
 #pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    const bool none = ((hidden >> ((x * 2 + y) * NB)) & kAllRows) == kAllRows;
+                for (int y = 0; y < 2; ++y)
 #pragma unroll
-                    for (int gr = 0; gr < G; ++gr) vtop = fmaxf(vtop, none ? 0.0f : fabsf(vz[x][y][gr].x));
-                }
+                    for (int gr = 0; gr < G; ++gr) vtop = fmaxf(vtop, fabsf(vz[x][y][gr].x));
             move |= vtop > vref;
             if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
@@ -610,11 +702,16 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
 #pragma unroll
                     for (int u = 0; u < J; ++u)
 #pragma unroll
-                        for (int i4 = 0; i4 < 4; ++i4) o[nb][u][i4] *= fo;
+                        for (int i4 = 0; i4 < 4; ++i4) {
+                            o[nb][u][i4] *= fo;
+                            t0[nb][u][i4] *= fo;
+                            t1[nb][u][i4] *= fo;
+                        }
                 }
             }
 
             // ---- weights, and the second product group by group ----
+            const uint32_t magic = 0x64006400u;   // 1024 in each half
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
                 const float ref = m[nb] == -INFINITY ? 0.0f : m[nb];
@@ -630,14 +727,8 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
 #pragma unroll
             for (int x = 0; x < 2; ++x)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int key = 16 * x + key_of_row(2 * c + (k & 1)) + (k & 2) * 4;
-                    const uint32_t row = st + S::kCodes + key * 16 * J;
-                    if constexpr (J == 8) hv[x][k] = load_halves<J>(row + ((g ^ swizzle<J>(key)) << 4));
-                    else if constexpr (J == 4)
-                        hv[x][k] = load_halves<J>(row + (((g >> 1) ^ swizzle<J>(key)) << 4) + (g & 1) * 8);
-                    else hv[x][k] = load_halves<J>(row + 2 * J * g);
-                }
+                for (int k = 0; k < 4; ++k)
+                    hv[x][k] = load_halves<J>(st + ((k & 1) ? vof1 : vof0) + (16 * x + 4 * (k & 2)) * 16 * J);
 #pragma unroll
             for (int gr = 0; gr < G; ++gr) {
                 uint32_t pf[NB][2][2];
@@ -655,11 +746,6 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
 #pragma unroll
                 for (int uu = 0; uu < UG; ++uu) {
                     const int u = gr * UG + uu;
-                    float t0[NB][4], t1[NB][4];
-#pragma unroll
-                    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                        for (int i4 = 0; i4 < 4; ++i4) t0[nb][i4] = t1[nb][i4] = 0.0f;
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         const uint32_t sel = (u & 1) ? 0x7632u : 0x5410u;
@@ -679,23 +765,21 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
                         const uint32_t b3 = h2_fma(mask_or<0x00F000F0u>(y23, magic), s16, m72);
 #pragma unroll
                         for (int nb = 0; nb < NB; ++nb) {
-                            mma16816(t0[nb], a0, a1, a2, a3, pf[nb][x][0], pf[nb][x][1]);
-                            mma16816(t1[nb], b0, b1, b2, b3, pf[nb][x][0], pf[nb][x][1]);
+                            mma16816(t0[nb][u], a0, a1, a2, a3, pf[nb][x][0], pf[nb][x][1]);
+                            mma16816(t1[nb][u], b0, b1, b2, b3, pf[nb][x][0], pf[nb][x][1]);
                         }
                     }
-#pragma unroll
-                    for (int nb = 0; nb < NB; ++nb) {
-                        o[nb][u][0] += t0[nb][0] + t0[nb][1];
-                        o[nb][u][1] += t0[nb][2] + t0[nb][3];
-                        o[nb][u][2] += t1[nb][0] + t1[nb][1];
-                        o[nb][u][3] += t1[nb][2] + t1[nb][3];
-                    }
                 }
+            }
+            if (++carried == kCarry) {
+                carried = 0;
+                carry<NB, J>(o, t0, t1);
             }
             __syncwarp();   // the stage is read: the next copies may land in it
         }
         cp_async_wait<0>();
         __syncwarp();
+        carry<NB, J>(o, t0, t1);
 
         // ---- the warp's sums into its own stretch of the ring: [row][D], then m, l ----
 #pragma unroll
@@ -707,11 +791,14 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
             lt += __shfl_xor_sync(0xffffffffu, lt, 16);
             const int row = nb * 4 + c;
 #pragma unroll
+            for (int gr = 0; gr < G; ++gr) {
+                zs[nb][gr] += __shfl_xor_sync(0xffffffffu, zs[nb][gr], 4);
+                zs[nb][gr] += __shfl_xor_sync(0xffffffffu, zs[nb][gr], 8);
+                zs[nb][gr] += __shfl_xor_sync(0xffffffffu, zs[nb][gr], 16);
+            }
+#pragma unroll
             for (int u = 0; u < J; ++u) {
-                float z = zs[nb][u / UG];
-                z += __shfl_xor_sync(0xffffffffu, z, 4);
-                z += __shfl_xor_sync(0xffffffffu, z, 8);
-                z += __shfl_xor_sync(0xffffffffu, z, 16);
+                const float z = zs[nb][u / UG];
                 *reinterpret_cast<float4 *>(own + row * D + 32 * u + 4 * g) =
                     make_float4((o[nb][u][0] - z) * back, (o[nb][u][1] - z) * back, (o[nb][u][2] - z) * back,
                                 (o[nb][u][3] - z) * back);
@@ -772,13 +859,14 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
         __syncthreads();
 
         pos += upto - from;
-        at += upto - from;
-        while (pos < end && at >= wk.total) {                  // the next request with work
-            ++b;
-            rq = attn_request(a, b);
-            wk = work_of<ROWS>(a, rq);
-            at = 0;
-            if (wk.total > 0) break;
+        from = 0;
+        if (upto == wk.steps && ++unit == wk.blocks * H && pos < end) {
+            unit = 0;
+            do {                                               // the next request with work
+                ++b;
+                rq = attn_request(a, b);
+                wk = work_of<ROWS>(a, rq);
+            } while (wk.total == 0);
         }
     }
 }
@@ -832,13 +920,13 @@ cudaError_t launch_split(const AttnCall &call, cudaStream_t stream)
 {
     // four query rows and heads of up to 128: registers and shared memory for
     // two CTAs per SM; otherwise one
-    constexpr int MINB = NB == 1 && J <= 4 ? 2 : 1;
-    constexpr int room = MINB == 2 ? 110 * 1024 : 220 * 1024;
+    constexpr int MINB = NB * J <= 4 ? 2 : 1;
+    constexpr int room = MINB == 2 ? 109 * 1024 : 216 * 1024;
     constexpr int fit = room / (kWarps * Stage<J, G>::kBytes);
     constexpr int STAGES = fit < 2 ? 2 : fit > 4 ? 4 : fit;
     static_assert(STAGES * Stage<J, G>::kBytes >= 4 * NB * (32 * J + 2) * 4, "the sums fit the ring");
     auto kern = attn_split_kernel<J, G, NB, STAGES, MINB>;
-    constexpr int smem = kWarps * STAGES * Stage<J, G>::kBytes;
+    constexpr int smem = kWarps * STAGES * Stage<J, G>::kBytes + NB * J * 512;
     int dev = 0, sms = 0;
     cudaError_t err;
     if ((err = cudaGetDevice(&dev)) != cudaSuccess) return err;
@@ -882,7 +970,10 @@ template <int J, int G>
 cudaError_t launch_rows(const AttnCall &call, cudaStream_t stream)
 {
     const long long rows = (long long)call.max_query * (call.heads / call.c.kv_heads);
-    return rows <= 4 ? launch_split<J, G, 1>(call, stream) : launch_split<J, G, 2>(call, stream);
+    // 8 rows of 256 values do not fit a thread's registers: blocks of 4 instead
+    if constexpr (J < 8)
+        if (rows > 4) return launch_split<J, G, 2>(call, stream);
+    return launch_split<J, G, 1>(call, stream);
 }
 
 }  // namespace

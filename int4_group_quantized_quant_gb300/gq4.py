@@ -561,13 +561,16 @@ def kv_plan(past_lens, new_lens, page_table, free_pages, free_count, n_tokens, p
     given = (("seq_lens", seq_lens, B), ("query_start", query_start, B + 1), ("positions", positions, n_tokens),
              ("slots", slots, n_tokens), ("free_count_out", free_count_out, 1))
     # what is not given is a stretch of one allocation
-    spare, at = torch.empty(sum(n for _, t, n in given if t is None), dtype=torch.int32, device=past_lens.device), 0
+    spare = iter(torch.empty(sum(n for _, t, n in given if t is None), dtype=torch.int32, device=past_lens.device)
+                 .split([n for _, t, n in given if t is None]))
     outs, ptrs = [], []
     for name, t, n in given:
         if t is None:
-            t, at = spare[at:at + n], at + n
+            t = next(spare)
+            ptrs.append(t.data_ptr())
+        else:
+            ptrs.append(_at(t, name, torch.int32, (n,)))
         outs.append(t)
-        ptrs.append(_at(t, name, torch.int32, (n,)))
     _same_device(past_lens, new_lens, page_table, free_pages, free_count, *outs)
     lens, starts, pos, slt, left = ptrs
     _call(lib.gq4_kv_plan, "gq4_kv_plan", past_lens, stream, B, n_tokens, page_size, page_table.shape[1],
