@@ -229,7 +229,7 @@ template <int ROWS>
 __device__ __forceinline__ Work work_of(const AttnCall &p, const AttnRequest &r)
 {
     Work w{0, 0, 0, 0};
-    if (r.bad || r.n == 0 || r.len == 0) return w;
+    if (r.bad || r.n == 0 || r.len == 0 || prompt_takes(p, r)) return w;
     const int R = p.heads / p.c.kv_heads;
     const int first = attn_first(p, max(r.len - r.n, -1));
     w.step0 = first / kStepKeys;
@@ -983,8 +983,21 @@ size_t attn_workspace_bytes(int, int, int, int D)
     return kMaxGrid * (sizeof(int4) + 2 * 8 * (size_t)(D + 2) * sizeof(float));
 }
 
-cudaError_t launch_attn(const AttnCall &call, cudaStream_t stream)
+cudaError_t launch_attn(const AttnCall &in, cudaStream_t stream)
 {
+    // Many query rows: a 128-row tile of the prompt kernel takes as long as
+    // about 4 blocks of 8 rows here, if its tiles fill a good part of the GPU
+    // (16 tiles' rows over all heads).
+    AttnCall call = in;
+    constexpr int kPromptRows = 33, kPromptTotal = 2048;
+    const long long R = call.heads / call.c.kv_heads;
+    const bool prompt = prompt_path_supported(call) && call.max_query * R >= kPromptRows &&
+                        (long long)call.T * call.heads >= kPromptTotal;
+    call.prompt_rows = prompt ? kPromptRows : 0x7fffffff;
+    if (prompt) {
+        const cudaError_t err = launch_attn_prompt(call, stream);
+        if (err != cudaSuccess) return err;
+    }
     const int G = call.c.head_dim / call.c.group_size;
     switch (call.c.head_dim * 16 + G) {
     case 64 * 16 + 1: return launch_rows<2, 1>(call, stream);
@@ -1004,8 +1017,13 @@ cudaError_t launch_attn(const AttnCall &call, cudaStream_t stream)
 
 cudaError_t read_attn_device_error(unsigned int *bits, bool clear)
 {
-    cudaError_t err = cudaMemcpyFromSymbol(bits, g_attn_error, sizeof(unsigned int));
-    if (err != cudaSuccess || !clear) return err;
+    unsigned int more = 0;
+    cudaError_t err = read_prompt_device_error(&more, clear);
+    if (err != cudaSuccess) return err;
+    err = cudaMemcpyFromSymbol(bits, g_attn_error, sizeof(unsigned int));
+    if (err != cudaSuccess) return err;
+    *bits |= more;
+    if (!clear) return err;
     const unsigned int zero = 0;
     return cudaMemcpyToSymbol(g_attn_error, &zero, sizeof(unsigned int));
 }

@@ -4,6 +4,7 @@
 
 #include <cstdint>
 
+#include "gq4_device.cuh"
 #include "gq4_internal.h"
 #include "gq4_kv.cuh"
 #include "gq4_tma.cuh"
@@ -34,6 +35,12 @@ __device__ __forceinline__ AttnRequest attn_request(const AttnCall &p, int b)
     r.fill1 = max(min(q1, p.T), r.fill0);
     r.bad = r.n > 0 && (q0 < 0 || q1 > p.T || n > p.max_query || r.len < 0 || r.len > p.max_len);
     return r;
+}
+
+// Whether a request with keys is the prompt kernel's.
+__device__ __forceinline__ bool prompt_takes(const AttnCall &p, const AttnRequest &r)
+{
+    return !r.bad && r.len > 0 && (long long)r.n * (p.heads / p.c.kv_heads) >= p.prompt_rows;
 }
 
 // First key position that the query at position `last` sees.

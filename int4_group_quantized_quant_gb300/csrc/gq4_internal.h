@@ -155,10 +155,15 @@ struct AttnCall {
     float *out;
     int ldo;
     void *workspace;
+    int prompt_rows;   // requests of at least so many query rows per kv head go to the prompt kernel
 };
 size_t attn_workspace_bytes(int T, int heads, int kv_heads, int D);
 cudaError_t launch_attn(const AttnCall &call, cudaStream_t stream);
 cudaError_t read_attn_device_error(unsigned int *bits, bool clear);
+// Its kernel for requests with many query rows.
+bool prompt_path_supported(const AttnCall &call);
+cudaError_t launch_attn_prompt(const AttnCall &call, cudaStream_t stream);
+cudaError_t read_prompt_device_error(unsigned int *bits, bool clear);
 
 // Test kernels.
 cudaError_t launch_unpack(int K, int N, const uint32_t *Bq, uint8_t *q, cudaStream_t stream);

@@ -120,6 +120,21 @@ def test_prompts(gq4, n, past, H, KH, D, gs, page):
     assert gq4.device_error() == 0
 
 
+@pytest.mark.parametrize("H,KH,D,gs,page", [(32, 8, 128, 128, 16), (32, 8, 128, 64, 64), (32, 4, 128, 32, 256),
+                                            (64, 8, 64, 64, 16), (36, 12, 64, 32, 32), (35, 5, 96, 96, 16),
+                                            (42, 6, 96, 32, 64), (16, 1, 128, 32, 16)])
+@pytest.mark.parametrize("window", [0, 70])
+def test_many_rows(gq4, H, KH, D, gs, page, window):
+    """Enough query rows in all (2048) for the kernel of prompts, beside requests that are not its:
+    whole tiles of 128 rows and 64 keys, one row and one key more, queries without keys."""
+    news = [33, 64, 1, 130, 0, 9, 66, 40]
+    lens = [33, 200, 65, 129, 5, 9, 64, 30]
+    s = Setup(news, lens, H, KH, D, gs, page, window)
+    assert s.T * H >= 2048
+    s.check(s.run(gq4))
+    assert gq4.device_error() == 0
+
+
 @pytest.mark.parametrize("window", [33, 300])
 def test_prompt_with_window(gq4, window):
     s = Setup([400, 300], [1000, 300], 4, 2, 128, 64, 16, window)
@@ -132,27 +147,29 @@ def test_long_contexts_split(gq4, length):
     s.check(s.run(gq4))
 
 
-def test_queries_that_see_nothing(gq4):
+@pytest.mark.parametrize("H", [4, 16])
+def test_queries_that_see_nothing(gq4, H):
     """seq_len < n: the first queries have no key (their rows are zeros); length 0."""
-    s = Setup([5, 1, 200, 1], [2, 0, 30, 9], 4, 2, 64, 32, 16)
+    s = Setup([5, 1, 200, 1], [2, 0, 30, 9], H, 2, 64, 32, 16)
     got = s.run(gq4)
     s.check(got)
     assert np.all(got[:3] == 0) and np.all(got[5] == 0) and np.all(got[6:6 + 170] == 0)
 
 
-def test_sharp_and_flat_weights(gq4):
+@pytest.mark.parametrize("H", [4, 16])
+def test_sharp_and_flat_weights(gq4, H):
     """Queries that pick one key, and queries of zeros (the mean of the values)."""
-    s = Setup([1, 1, 150], [600, 600, 700], 4, 2, 128, 32, 16)
+    s = Setup([1, 1, 150], [600, 600, 700], H, 2, 128, 32, 16)
     s.q[0] *= 60
     s.q[1] = 0
     s.q[2:40] *= 30
     s.check(s.run(gq4))
 
 
-@pytest.mark.parametrize("n", [1, 150])
-def test_scales_of_unlike_size(gq4, n):
+@pytest.mark.parametrize("n,H", [(1, 4), (150, 4), (150, 16)])
+def test_scales_of_unlike_size(gq4, n, H):
     """Value scales over ten powers of two, queries of very small and very large size."""
-    s = Setup([n, n], [700, 800], 4, 1, 128, 64, 16)
+    s = Setup([n, n], [700, 800], H, 1, 128, 64, 16)
     g = I.rng(2201)
     for side, spread in ((0, 1.0), (1, 5.0)):
         sz = s.cache.sz[side]
@@ -163,7 +180,7 @@ def test_scales_of_unlike_size(gq4, n):
     live = 2 * n
     assert np.all(np.abs(got[:live] - ref[:live]) <= tol[:live])
     # queries and scale of opposite huge size give the same weights as plain ones
-    s2 = Setup([n], [700], 4, 1, 128, 64, 16)
+    s2 = Setup([n], [700], H, 1, 128, 64, 16)
     plain = s2.run(gq4)
     s2.q *= np.float32(2.0 ** 100)
     s2.scale *= 2.0 ** -100
@@ -171,17 +188,18 @@ def test_scales_of_unlike_size(gq4, n):
     assert np.allclose(plain, s2.run(gq4), rtol=1e-5, atol=1e-6)
 
 
-@pytest.mark.parametrize("n", [1, 140])
-def test_non_finite_queries_and_keys_stay_apart(gq4, n):
+@pytest.mark.parametrize("n,heads,D", [(1, 1, 64), (140, 1, 64), (140, 4, 64), (140, 3, 128), (140, 4, 96)])
+def test_non_finite_queries_and_keys_stay_apart(gq4, n, heads, D):
     """A NaN query spoils its own row; a NaN key or value only the rows that see it."""
-    s = Setup([n, n], [200, 200], 4, 2, 64, 32, 16)
+    s = Setup([n, n], [200, 200], 4 * heads, 2 * heads, D, 32, 16)
     clean = s.run(gq4)
     q = s.q.copy()
     q[0, 1, 3] = np.nan
+    q[0, 2, 5] = np.inf
     got = s.run(gq4, q=dev(q))
-    assert np.isnan(got[0, 1]).all()
+    assert np.isnan(got[0, 1]).all() and np.isnan(got[0, 2]).all()
     keep = np.ones(got.shape[:2], bool)
-    keep[0, 1] = False
+    keep[0, 1:3] = False
     assert np.array_equal(got[keep], clean[keep])
     # request 0's key 150 of kv head 1
     slot = s.table[0, 150 // 16], 150 % 16
@@ -191,9 +209,10 @@ def test_non_finite_queries_and_keys_stay_apart(gq4, n):
         got = s.run(gq4)
         s.cache.sz[side][slot[0], 1, slot[1]] = kept
         sees = np.arange(n) + 200 - n >= 150
-        assert np.isnan(got[:n][sees][:, 2:]).all()
+        assert np.isnan(got[:n][sees][:, 2:4]).all()
         assert np.array_equal(got[:n][~sees], clean[:n][~sees])
-        assert np.array_equal(got[:n, :2], clean[:n, :2]) and np.array_equal(got[n:], clean[n:])
+        others = [h for h in range(4 * heads) if h not in (2, 3)]
+        assert np.array_equal(got[:n, others], clean[:n, others]) and np.array_equal(got[n:], clean[n:])
 
 
 def test_strided_rows_and_workspace(gq4):
@@ -244,8 +263,9 @@ def test_bad_requests_are_refused(gq4):
     spoiled([0, 1], args=args, max_query=100)
 
 
-def test_a_bad_page_spoils_only_the_rows_that_see_it(gq4):
-    s = Setup([20], [40], 2, 1, 64, 32, 16, pad=0)
+@pytest.mark.parametrize("H", [2, 128])
+def test_a_bad_page_spoils_only_the_rows_that_see_it(gq4, H):
+    s = Setup([20], [40], H, 1, 64, 32, 16, pad=0)
     clean = s.run(gq4)
     s.table[0, 2] = -1          # keys 32..39: the last 8 queries
     got = s.run(gq4)
