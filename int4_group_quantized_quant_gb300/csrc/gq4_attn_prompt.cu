@@ -5,25 +5,32 @@
 // A CTA takes 128 query rows of one kv head (tokens times the head's query
 // heads, so that a dequantised key serves all of them) and walks the keys in
 // tiles of 64:
-//   S = Q K^T   (128 x 64, K dimension 128),   P = 2^(S F - m),
+//   S = Q K^T   (128 x 64, K dimension head_dim),   P = 2^(w - m),
 //   O = O f + P V   (128 x head_dim, K dimension 64).
-// Accuracy.  Every factor is two fp16 pieces (22 bits): x = xh + xl, and a
-// product is Ql Kh + Qh Kl + Qh Kh, three MMAs, the small ones first.  Powers
-// of two keep the pieces inside fp16: one per CTA for Q, one per key for K
-// (undone by the factor F_j of column j), a running one for V.  The tensor
-// core cuts its sums rather than rounding them, so a tile's P V starts at
-// zero and is added to f32 registers.
+// Two forms, by the scale groups of a row.
+//   One group (EXACT): the codes minus 8 are the operands, exact in fp16; the
+// scale and zero of key j come off outside the product,
+//   w_j = F_j S_j + G_j sum_d q_d,  F_j = scale log2(e) s_j,  G_j = -(z_j - 8) F_j,
+//   O = sum_j (p_j s_j) (c_j - 8) - sum_j (p_j s_j)(z_j - 8),
+// and Q and p s are two fp16 pieces (22 bits): two MMAs per product.
+//   Several groups: the keys and values themselves, (c - z) s, are two pieces
+// as well, x = xh + xl, and a product is xl yh + xh yl + xh yh: three MMAs, the
+// small ones first.
+// Powers of two keep the pieces inside fp16: one per CTA for Q, one per key
+// for K (undone by F_j), one per tile for V.  The tensor core cuts its sums
+// rather than rounding them, so a tile's P V starts at zero and is added to
+// f32 registers.
 //
-// Warps: 4 softmax (a thread per row), 8 that add the tiles' P V (a row and
-// half of head_dim per thread), 8 that read the cache and write the pieces of
-// K and V into shared memory, 1 that issues the MMAs.  Tensor memory (512
+// Warps: softmax (a thread per row; EXACT: two groups of 4 that take turns at
+// the tiles, each with its own maximum), 8 that add the tiles' P V (a row and
+// half of head_dim per thread), 4 or 8 that read the cache and write the K and
+// V operands into shared memory, 1 that issues the MMAs.  Tensor memory (512
 // columns): S, P and the tile's O, two slots each, so that the MMA of one
 // tile runs under the softmax of another; K and V have two slots too.
 // K is stored [key][d] (K-major), V [key][d] as well, which is the MN-major
 // form of the second product's B operand: no transposition.
-//
-// Bound: three times the formula's flops on the fp16 pipe, but the issue
-// slots of the dequantising and softmax warps come first.
+// Bound by the issue slots of the softmax and dequantising warps, not the fp16
+// pipe.
 #include <cuda_fp16.h>
 
 #include <atomic>
@@ -39,9 +46,9 @@ __device__ unsigned int g_prompt_error = 0;
 
 constexpr int kRows = 128;
 constexpr int kTile = 64;                       // keys
-constexpr int kSmWarps = 4, kCoWarps = 8, kDqWarps = 8;
-constexpr int kCo0 = kSmWarps, kDq0 = kCo0 + kCoWarps, kMma = kDq0 + kDqWarps;
-constexpr int kThreads = 32 * (kMma + 1);
+constexpr int kCoWarps = 8;
+constexpr int kWarps = 21;                      // all: the roles' warps and the MMA's
+constexpr int kThreads = 32 * kWarps;
 constexpr float kSlack = 4.0f;                  // log2 of how far a weight may pass the maximum
 constexpr int kPieceBits = 11;                  // P is held times 2^11
 constexpr uint32_t kColS = 0, kColP = 128, kColO = 256;
@@ -51,19 +58,31 @@ struct PromptParams {
     AttnCall a;
 };
 
+// The warps of a form, and its pieces of K and V.
+template <bool EXACT>
+struct Form {
+    static constexpr int kGroups = EXACT ? 2 : 1;               // softmax groups of 4 warps
+    static constexpr int kCo0 = 4 * kGroups;                    // first warp that adds
+    static constexpr int kDq0 = kCo0 + kCoWarps;                // first that reads the cache
+    static constexpr int kMma = kWarps - 1;
+    static constexpr int kDqWarps = kMma - kDq0;                // 4 or 8
+    static constexpr int kPieces = EXACT ? 1 : 2;
+    static constexpr int kTurns = 8 / kDqWarps;                 // keys per thread
+};
+
 // Shared memory of a head of DP = 64 or 128 values (96 is padded with zeros).
-template <int DP>
+template <int DP, bool EXACT>
 struct Mem {
-    static constexpr int kBlocks = DP / 64;             // 128-byte columns of 64 fp16
     static constexpr int kQ = kRows * DP * 2;           // bytes of a piece
     static constexpr int kKV = kTile * DP * 2;
+    static constexpr int kSlot = Form<EXACT>::kPieces * kKV;
     static constexpr int offQ = 0;                      // high, low
-    static constexpr int offK = offQ + 2 * kQ;          // [slot][high, low]
-    static constexpr int offV = offK + 4 * kKV;
-    static constexpr int offF = offV + 4 * kKV;         // F_j [slot][64]
-    static constexpr int offFac = offF + 2 * kTile * 4; // row factors [slot][128]
-    static constexpr int offInv = offFac + 2 * kRows * 4;   // 1 / l [128]
-    static constexpr int offVm = offInv + kRows * 4;    // V's largest per warp [2][8], its factor [2]
+    static constexpr int offK = offQ + 2 * kQ;          // [slot][pieces]
+    static constexpr int offV = offK + 2 * kSlot;
+    static constexpr int offF = offV + 2 * kSlot;       // per key (F, G) and (s, z - 8) [slot][2][64], or F [slot][64]
+    static constexpr int offM = offF + 2 * kTile * 16;  // per row (reference, sum p s (z - 8)) [slot][128]
+    static constexpr int offL = offM + 2 * kRows * 8;   // per row (reference, sum of weights) [group][128]
+    static constexpr int offVm = offL + 2 * kRows * 8;  // V's largest per warp [2][8], its factor [2]
     static constexpr int offBar = offVm + 128;
     static constexpr int kBytes = offBar + 256 + 1024;  // and room to align
 };
@@ -100,30 +119,52 @@ __device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t 
 }
 
 // Bounded wait: gives up when another thread of the CTA gave up, or after the
-// time limit (recording the error).
+// time limit (recording the error).  REST: the waiting warp sleeps between
+// looks, leaving the issue slots to the others.
+template <bool REST>
 __device__ __noinline__ bool bar_wait_slow(uint64_t *bar, uint32_t parity, volatile int *abort)
 {
     const unsigned long long t0 = global_timer_ns();
-    while (true) {
+    for (unsigned int i = 1;; ++i) {
         if (mbar_try_wait(bar, parity)) return true;
-        if (*abort) return false;
-        if (global_timer_ns() - t0 > kWaitLimitNs) {
-            *abort = 1;
-            atomicOr(&g_prompt_error, kAttnGaveUp);
-            return false;
+        if (REST) __nanosleep(32);
+        if ((i & 15u) == 0u) {
+            if (*abort) return false;
+            if (global_timer_ns() - t0 > kWaitLimitNs) {
+                *abort = 1;
+                atomicOr(&g_prompt_error, kAttnGaveUp);
+                return false;
+            }
         }
     }
 }
 
+template <bool REST = false>
 __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, volatile int *abort)
 {
-    return mbar_try_wait(bar, parity) || bar_wait_slow(bar, parity, abort);
+    return mbar_try_wait(bar, parity) || bar_wait_slow<REST>(bar, parity, abort);
 }
 
 // The whole warp waits; false in every lane when any gave up.
+template <bool REST = false>
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort)
 {
-    return __all_sync(0xffffffffu, bar_wait(bar, parity, abort));
+    return __all_sync(0xffffffffu, bar_wait<REST>(bar, parity, abort));
+}
+
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&v)[8])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "r"(taddr)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
 }
 
 // Two numbers as their leading fp16 pieces and the rest, each pair packed.
@@ -170,67 +211,120 @@ __device__ __forceinline__ void dequant_word(uint32_t w, float s, float z, uint3
     }
 }
 
-// A row's S of one tile, from tensor memory: the largest exponent.  Column x
-// counts when first <= x <= last.
-template <bool MASK>
-__device__ __forceinline__ float tile_max(uint32_t s_at, const float4 *F, int last, int first)
+__device__ __forceinline__ float4 lds_f4(uint32_t at)
 {
-    float top = -INFINITY;
-#pragma unroll
-    for (int x = 0; x < kTile / 16; ++x) {
-        uint32_t t[16];
-        tmem_ld16(s_at + 16 * x, t);
-        tmem_wait_ld();
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-            const float4 f = F[4 * x + y];
-            const float v[4] = {__uint_as_float(t[4 * y]) * f.x, __uint_as_float(t[4 * y + 1]) * f.y,
-                                __uint_as_float(t[4 * y + 2]) * f.z, __uint_as_float(t[4 * y + 3]) * f.w};
-#pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                const int c = 16 * x + 4 * y + n;
-                top = fmaxf(top, MASK && (c > last || c < first) ? -INFINITY : v[n]);
-            }
-        }
-    }
-    return top;
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
+    return v;
 }
 
-// Its weights 2^(S F - ref), two fp16 pieces of 2^11 times them to tensor
-// memory; returns their sum.
-template <bool MASK>
-__device__ __forceinline__ float tile_weights(uint32_t s_at, uint32_t p_at, const float4 *F, float ref, int last,
-                                              int first)
+// A softmax thread's row: the reference its weights are taken against (log2),
+// and their sum.
+struct RowSum {
+    float ref, l;
+    bool set;        // ref is a maximum seen
+};
+
+// One tile of a row: the weights 2^(w - ref) from S, their two fp16 pieces
+// (times s_j where EXACT, times 2^11) to tensor memory.  Column x counts when
+// first <= x <= last.  The reference moves, and the tile is done again, when a
+// weight passes 2^kSlack of it.  Returns sum_j p_j s_j (z_j - 8) of the tile.
+template <bool EXACT, bool MASK>
+__device__ __forceinline__ float tile_weights(uint32_t s_at, uint32_t p_at, uint32_t key, float qsum, RowSum &r,
+                                              int last, int first)
 {
-    float l = 0.0f;
-#pragma unroll
-    for (int x = 0; x < kTile / 32; ++x) {
-        uint32_t hi[16], lo[16];
-#pragma unroll
-        for (int z = 0; z < 2; ++z) {
-            uint32_t t[16];
-            tmem_ld16(s_at + 32 * x + 16 * z, t);
+    constexpr int kCols = 16;          // at a time: a loop, not unrolled, keeps the registers few
+    float l, z;
+    while (true) {
+        bool move = false;
+        l = z = 0.0f;
+#pragma unroll 1
+        for (int x = 0; x < kTile; x += kCols) {
+            uint32_t t[kCols];
+            tmem_ld16(s_at + x, t);
             tmem_wait_ld();
+            float top = -INFINITY;
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-                const float4 f = F[8 * x + 4 * z + y];
-                float v[4] = {fmaf(__uint_as_float(t[4 * y]), f.x, -ref), fmaf(__uint_as_float(t[4 * y + 1]), f.y, -ref),
-                              fmaf(__uint_as_float(t[4 * y + 2]), f.z, -ref),
-                              fmaf(__uint_as_float(t[4 * y + 3]), f.w, -ref)};
-#pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    const int c = 32 * x + 16 * z + 4 * y + n;
-                    v[n] = MASK && (c > last || c < first) ? 0.0f : exp2_approx(v[n]);
+            for (int y = 0; y < kCols; y += EXACT ? 2 : 4) {
+                float v[4];
+                if constexpr (EXACT) {             // (F, G) of two keys
+                    const float4 f = lds_f4(key + 8 * (x + y));
+                    v[0] = fmaf(__uint_as_float(t[y]), f.x, fmaf(f.y, qsum, -r.ref));
+                    v[1] = fmaf(__uint_as_float(t[y + 1]), f.z, fmaf(f.w, qsum, -r.ref));
+                } else {                           // F of four
+                    const float4 f = lds_f4(key + 4 * (x + y));
+                    v[0] = fmaf(__uint_as_float(t[y]), f.x, -r.ref);
+                    v[1] = fmaf(__uint_as_float(t[y + 1]), f.y, -r.ref);
+                    v[2] = fmaf(__uint_as_float(t[y + 2]), f.z, -r.ref);
+                    v[3] = fmaf(__uint_as_float(t[y + 3]), f.w, -r.ref);
                 }
-                l += (v[0] + v[1]) + (v[2] + v[3]);
-                split_pair(v[0] * 2048.0f, v[1] * 2048.0f, hi[8 * z + 2 * y], lo[8 * z + 2 * y]);
-                split_pair(v[2] * 2048.0f, v[3] * 2048.0f, hi[8 * z + 2 * y + 1], lo[8 * z + 2 * y + 1]);
+#pragma unroll
+                for (int n = 0; n < (EXACT ? 2 : 4); ++n) {
+                    if (MASK && (x + y + n > last || x + y + n < first)) v[n] = -INFINITY;
+                    top = fmaxf(top, v[n]);
+                    t[y + n] = __float_as_uint(v[n]);
+                }
             }
+            const bool mine = top > (r.set ? kSlack : -INFINITY);
+            if (__any_sync(0xffffffffu, mine)) {
+                if (mine) {
+                    r.l *= exp2_approx(-top);      // (0 while nothing is set)
+                    r.ref += top;
+                    r.set = true;
+                }
+                move = true;
+                break;
+            }
+            uint32_t hi[8], lo[8];
+#pragma unroll
+            for (int y = 0; y < kCols; y += 2) {
+                float p0 = exp2_approx(__uint_as_float(t[y])), p1 = exp2_approx(__uint_as_float(t[y + 1]));
+                l += p0 + p1;
+                if constexpr (EXACT) {             // (s, z - 8) of two keys
+                    const float4 f = lds_f4(key + 8 * kTile + 8 * (x + y));
+                    p0 *= f.x;
+                    p1 *= f.z;
+                    z = fmaf(p0, f.y, z);
+                    z = fmaf(p1, f.w, z);
+                } else {
+                    p0 *= 2048.0f;
+                    p1 *= 2048.0f;
+                }
+                split_pair(p0, p1, hi[y / 2], lo[y / 2]);
+            }
+            tmem_st8(p_at + x / 2, hi);
+            tmem_st8(p_at + 32 + x / 2, lo);
         }
-        tmem_st16(p_at + 16 * x, hi);
-        tmem_st16(p_at + 32 + 16 * x, lo);
+        if (!move) break;
     }
-    return l;
+    r.l += l;
+    return z;
+}
+
+// 8 codes of a word minus 8, exact, in the order 0, 4, 1, 5, 2, 6, 3, 7.
+__device__ __forceinline__ uint4 exact_word(uint32_t w)
+{
+    const uint32_t magic = 0x64006400u;      // 1024 in each half
+    auto lower = [&](uint32_t x) {           // (1024 + c) - 1032
+        uint32_t d, m = 0xE408E408u;
+        asm("{\n\t.reg .b32 t;\n\tlop3.b32 t, %1, 0x000F000F, %2, 0xEA;\n\tadd.rn.f16x2 %0, t, %3;\n\t}"
+            : "=r"(d) : "r"(x), "r"(magic), "r"(m));
+        return d;
+    };
+    auto upper = [&](uint32_t x) {           // (1024 + 16 c) / 16 - 72
+        uint32_t d, s = 0x2C002C00u, m = 0xD480D480u;
+        asm("{\n\t.reg .b32 t;\n\tlop3.b32 t, %1, 0x00F000F0, %2, 0xEA;\n\tfma.rn.f16x2 %0, t, %3, %4;\n\t}"
+            : "=r"(d) : "r"(x), "r"(magic), "r"(s), "r"(m));
+        return d;
+    };
+    const uint32_t y = w >> 8;
+    return make_uint4(lower(w), upper(w), lower(y), upper(y));
+}
+
+// Place i of an EXACT operand's group of 8 holds value exact_order(i).
+__host__ __device__ constexpr int exact_order(int i)
+{
+    return (i >> 1) + 4 * (i & 1);
 }
 
 template <int NW>
@@ -260,11 +354,13 @@ template <int J, int G, int DP>
 __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_constant__ PromptParams p)
 {
     constexpr int D = 32 * J, UG = J / G;
-    using M = Mem<DP>;
+    constexpr bool EXACT = G == 1;
+    using W = Form<EXACT>;
+    using M = Mem<DP, EXACT>;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     const uint32_t smem_s = smem_addr(smem);
-    __shared__ int s_sums[kMma + 1], s_req, s_tile, s_big;
+    __shared__ int s_sums[kWarps], s_req, s_tile, s_big;
     __shared__ volatile int s_abort;
     __shared__ uint32_t s_tmem;
     const AttnCall &a = p.a;
@@ -283,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         for (int b0 = 0; b0 < a.B; b0 += kThreads) {
             int t;
             mine = tiles_of(b0 + (int)threadIdx.x);
-            before = scan_ints<kMma + 1>(mine, t, s_sums);
+            before = scan_ints<kWarps>(mine, t, s_sums);
             all += t;
         }
         const int want = all - 1 - (int)(blockIdx.x / (unsigned)H);
@@ -293,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             int t = all;
             if (a.B > kThreads) {
                 mine = tiles_of(b0 + (int)threadIdx.x);
-                before = scan_ints<kMma + 1>(mine, t, s_sums);
+                before = scan_ints<kWarps>(mine, t, s_sums);
             }
             if (want >= base + before && want < base + before + mine) {
                 s_req = b0 + (int)threadIdx.x;
@@ -321,24 +417,24 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
     }
     if (threadIdx.x == 0) {
         for (int s = 0; s < 2; ++s) {
-            mbar_init(&bar.k_full[s], kDqWarps);
+            mbar_init(&bar.k_full[s], W::kDqWarps);
             mbar_init(&bar.k_empty[s], 1);
-            mbar_init(&bar.v_full[s], kDqWarps);
+            mbar_init(&bar.v_full[s], W::kDqWarps);
             mbar_init(&bar.v_empty[s], 1);
             mbar_init(&bar.s_full[s], 1);
-            mbar_init(&bar.s_empty[s], kSmWarps);
-            mbar_init(&bar.p_full[s], kSmWarps);
+            mbar_init(&bar.s_empty[s], 4);
+            mbar_init(&bar.p_full[s], 4);
             mbar_init(&bar.o_full[s], 1);
             mbar_init(&bar.o_empty[s], kCoWarps);
         }
-        mbar_init(bar.fin, kSmWarps);
+        mbar_init(bar.fin, W::kCo0);
         mbar_init(bar.drain, 1);
-        mbar_init(bar.vmax, kDqWarps);
+        mbar_init(bar.vmax, W::kDqWarps);
         s_abort = 0;
         s_big = 0;
         mbar_fence_init();
     }
-    if (warp == kMma) {
+    if (warp == W::kMma) {
         tmem_alloc(&s_tmem, kTmemCols);
         tmem_relinquish();
     }
@@ -392,10 +488,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                 const float4 *q = reinterpret_cast<const float4 *>(a.q + (size_t)(rq.row0 + j) * a.ldq +
                                                                   (size_t)(h * R + rho - j * R) * D + 8 * d8);
                 const float4 x = __ldg(q), y = __ldg(q + 1);
-                split_pair(x.x * up, x.y * up, hi[0], lo[0]);
-                split_pair(x.z * up, x.w * up, hi[1], lo[1]);
-                split_pair(y.x * up, y.y * up, hi[2], lo[2]);
-                split_pair(y.z * up, y.w * up, hi[3], lo[3]);
+                const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+                for (int n = 0; n < 4; ++n)
+                    split_pair(v[EXACT ? exact_order(2 * n) : 2 * n] * up, v[EXACT ? exact_order(2 * n + 1) : 2 * n + 1] * up,
+                               hi[n], lo[n]);
             }
             unsigned char *at = smem + M::offQ + (d8 >> 3) * (kRows * 128) + r * 128 + (((d8 & 7) ^ (r & 7)) << 4);
             *reinterpret_cast<uint4 *>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
@@ -404,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         // the padding of a 96-value head: zeros in every K and V slot, once
         if constexpr (DP > D) {
             constexpr int per = kTile * (DP - D) / 8;      // 16-byte pieces of one piece's padding
-            for (int i = threadIdx.x; i < 8 * per; i += kThreads) {
+            for (int i = threadIdx.x; i < 4 * W::kPieces * per; i += kThreads) {   // K's and V's pieces lie on end
                 const int t = i / per, k = (i - t * per) / ((DP - D) / 8), d8 = D / 8 + (i - t * per) % ((DP - D) / 8);
                 *reinterpret_cast<uint4 *>(smem + M::offK + t * M::kKV + (d8 >> 3) * (kTile * 128) + k * 128 +
                                            (((d8 & 7) ^ (k & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
@@ -415,121 +512,139 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
     __syncthreads();
 
     bool ok = true;
-    if (warp < kSmWarps) {
-        // ===== softmax: a thread per row =====
-        const int row = 32 * warp + lane;
-        const uint32_t lanes = (uint32_t)(32 * warp) << 16;
-        const int last = row0 + row < rows_all ? pos0 + (row0 + row) / R : -1;
+    if (warp < W::kCo0) {
+        // ===== softmax: a thread per row, a group of 4 warps per tile =====
+        const int group = warp >> 2;
+        const int row = 32 * (warp & 3) + lane;
+        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+        const int rho = row0 + row, j = rho / R;
+        const int last = rho < rows_all ? pos0 + j : -1;
         const int first = attn_first(a, max(last, -1));
-        float *fac = reinterpret_cast<float *>(smem + M::offFac);
-        float m = -INFINITY, l = 0.0f;
-        for (int i = 0; i < n_tiles; ++i) {
+        float qsum = 0.0f;
+        if (EXACT && rho < rows_all) {
+            const float4 *q = reinterpret_cast<const float4 *>(a.q + (size_t)(rq.row0 + j) * a.ldq +
+                                                              (size_t)(h * R + rho - j * R) * D);
+#pragma unroll 8
+            for (int d = 0; d < D / 4; ++d) {
+                const float4 v = __ldg(q + d);
+                qsum += (v.x + v.y) + (v.z + v.w);
+            }
+            qsum *= pow2(kq);
+        }
+        RowSum r{0.0f, 0.0f, false};
+        float2 *mz = reinterpret_cast<float2 *>(smem + M::offM);
+        for (int i = group; i < n_tiles; i += W::kGroups) {
             const int s = i & 1, k = i >> 1;
-            if (!warp_wait(&bar.s_full[s], k & 1, abort)) {
+            // S is there; the tile before last is done with (its reference is read, its P used up)
+            if (!warp_wait(&bar.s_full[s], k & 1, abort) || (i >= 2 && !warp_wait(&bar.o_empty[s], (k - 1) & 1, abort))) {
                 ok = false;
                 break;
             }
             tc_fence_after_sync();
-            // two passes over S in tensor memory (the maximum, then the weights)
-            // keep the registers few
-            const float4 *F = reinterpret_cast<const float4 *>(smem + M::offF) + s * (kTile / 4);
+            const uint32_t key = smem_s + M::offF + s * (EXACT ? 16 : 4) * kTile;
             const int k0 = (tile_lo + i) * kTile;
             const bool masked = k0 + kTile - 1 > all_hi || k0 < all_lo;   // uniform
             const uint32_t s_at = tmem + lanes + kColS + s * kTile, p_at = tmem + lanes + kColP + s * 64;
-            const float top = masked ? tile_max<true>(s_at, F, last - k0, first - k0) : tile_max<false>(s_at, F, 0, 0);
-            float f = 1.0f;
-            if (top > m + kSlack) {
-                f = exp2_approx(m - top);
-                m = top;
-                l *= f;
-            }
-            const float ref = m == -INFINITY ? 0.0f : m;
-            // the tile before last: its factors are read, its P is used up
-            if (i >= 2 && !warp_wait(&bar.o_empty[s], (k - 1) & 1, abort)) {
-                ok = false;
-                break;
-            }
-            tc_fence_after_sync();
-            fac[s * kRows + row] = f;
-            l += masked ? tile_weights<true>(s_at, p_at, F, ref, last - k0, first - k0)
-                        : tile_weights<false>(s_at, p_at, F, ref, 0, 0);
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar.s_empty[s]);
+            const float z = masked ? tile_weights<EXACT, true>(s_at, p_at, key, qsum, r, last - k0, first - k0)
+                                   : tile_weights<EXACT, false>(s_at, p_at, key, qsum, r, 0, 0);
+            mz[s * kRows + row] = make_float2(r.set ? r.ref : -INFINITY, z);
             tmem_wait_st();
             tc_fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bar.p_full[s]);
+            if (lane == 0) {
+                mbar_arrive(&bar.s_empty[s]);
+                mbar_arrive(&bar.p_full[s]);
+            }
         }
-        reinterpret_cast<float *>(smem + M::offInv)[row] = m == -INFINITY ? 0.0f : 1.0f / l;
+        reinterpret_cast<float2 *>(smem + M::offL)[group * kRows + row] = make_float2(r.set ? r.ref : -INFINITY, r.l);
         __syncwarp();
         if (lane == 0) mbar_arrive(bar.fin);
-    } else if (warp < kDq0) {
+    } else if (warp < W::kDq0) {
         // ===== the tiles' P V added up: a row and half of the values per thread =====
         constexpr int C = DP / 2;
-        const int q4 = warp & 3, half = (warp - kCo0) >> 2;
+        const int q4 = warp & 3, half = (warp - W::kCo0) >> 2;
         const int row = 32 * q4 + lane;
         const uint32_t lanes = (uint32_t)(32 * q4) << 16;
-        const float *fac = reinterpret_cast<const float *>(smem + M::offFac);
+        const float2 *mz = reinterpret_cast<const float2 *>(smem + M::offM);
         const float *vfac = reinterpret_cast<const float *>(smem + M::offVm) + 16;
-        const int *vexp = reinterpret_cast<const int *>(smem + M::offVm) + 18;
         float o[C];
 #pragma unroll
         for (int d = 0; d < C; ++d) o[d] = 0.0f;
-        int e = 0;
+        float m = -INFINITY, zs = 0.0f;    // o and zs are relative to 2^m
         for (int i = 0; i < n_tiles; ++i) {
             const int s = i & 1, k = i >> 1;
-            // the factors come with P and with V
-            if (!warp_wait(&bar.p_full[s], k & 1, abort) || !warp_wait(&bar.v_full[s], k & 1, abort) ||
-                !warp_wait(&bar.o_full[s], k & 1, abort)) {
+            // the row's reference comes with P, V's power of two with V
+            if (!warp_wait<true>(&bar.v_full[s], k & 1, abort) || !warp_wait<true>(&bar.p_full[s], k & 1, abort) ||
+                !warp_wait<true>(&bar.o_full[s], k & 1, abort)) {
                 ok = false;
                 break;
             }
             tc_fence_after_sync();
-            const float f = fac[s * kRows + row] * vfac[s];
-            e = vexp[s];
+            const float2 t2 = mz[s * kRows + row];
+            const float mn = fmaxf(m, t2.x), ref = mn == -INFINITY ? 0.0f : mn;
+            const float ft = exp2_approx(t2.x - ref) * vfac[s];
+            if (__any_sync(0xffffffffu, mn > m)) {
+                const float fo = exp2_approx(m - ref);
+                zs *= fo;
 #pragma unroll
-            for (int x = 0; x < C / 16; ++x) {
-                uint32_t t[16];
-                tmem_ld16(tmem + lanes + kColO + s * 128 + half * C + 16 * x, t);
+                for (int d = 0; d < C; ++d) o[d] *= fo;
+                m = mn;
+            }
+            zs = fmaf(t2.y, ft, zs);
+#pragma unroll
+            for (int x = 0; x < C / 8; ++x) {
+                uint32_t t[8];
+                tmem_ld8(tmem + lanes + kColO + s * 128 + half * C + 8 * x, t);
                 tmem_wait_ld();
 #pragma unroll
-                for (int y = 0; y < 16; ++y) o[16 * x + y] = fmaf(o[16 * x + y], f, __uint_as_float(t[y]));
+                for (int y = 0; y < 8; ++y) o[8 * x + y] = fmaf(__uint_as_float(t[y]), ft, o[8 * x + y]);
             }
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.o_empty[s]);
         }
-        if (ok) ok = warp_wait(bar.fin, 0, abort);
+        if (ok) ok = warp_wait<true>(bar.fin, 0, abort);
         const int rho = row0 + row;
         if (rho < rows_all) {
             const int j = rho / R;
             float *out = a.out + (size_t)(rq.row0 + j) * a.ldo + (size_t)(h * R + rho - j * R) * D + half * C;
-            const float inv = ok ? reinterpret_cast<const float *>(smem + M::offInv)[row] * pow2(-kPieceBits)
-                                 : quiet_nan();
-            const float back = pow2(-e);   // V's power of two
+            float inv = quiet_nan();
+            if (ok) {
+                const float2 *gl = reinterpret_cast<const float2 *>(smem + M::offL);
+                float l = 0.0f;
 #pragma unroll
-            for (int d = 0; d < C; d += 4)
-                if (half * C + d < D)
-                    *reinterpret_cast<float4 *>(out + d) =
-                        make_float4(o[d] * inv * back, o[d + 1] * inv * back, o[d + 2] * inv * back, o[d + 3] * inv * back);
+                for (int x = 0; x < W::kGroups; ++x) {
+                    const float2 v = gl[x * kRows + row];
+                    if (v.x != -INFINITY) l = fmaf(v.y, exp2_approx(v.x - m), l);
+                }
+                inv = m == -INFINITY ? 0.0f : 1.0f / l;
+            }
+#pragma unroll
+            for (int d = 0; d < C; d += 8) {
+                if (half * C + d >= D) break;
+                float v[8];
+#pragma unroll
+                for (int n = 0; n < 8; ++n) v[EXACT ? exact_order(n) : n] = (o[d + n] - zs) * inv;
+                *reinterpret_cast<float4 *>(out + d) = make_float4(v[0], v[1], v[2], v[3]);
+                *reinterpret_cast<float4 *>(out + d + 4) = make_float4(v[4], v[5], v[6], v[7]);
+            }
         }
-    } else if (warp < kMma) {
-        // ===== the cache: codes, scales and zeros to fp16 pieces =====
-        // lane: key lane % 8 of the warp's eight, values 32 u + 8 (lane / 8) ..
-        // + 7 (eight keys of one shared-memory phase meet eight distinct banks)
-        const int w = warp - kDq0, key = 8 * w + (lane & 7), c = lane >> 3;
+    } else if (warp < W::kMma) {
+        // ===== the cache: codes, scales and zeros to the operands =====
+        // lane: key lane % 8 of eight, values 32 u + 8 (lane / 8) .. + 7 (eight
+        // keys of one shared-memory phase meet eight distinct banks)
+        constexpr int TN = W::kTurns;
+        const int w = warp - W::kDq0, key0 = 8 * w + (lane & 7), c = lane >> 3;
         const int shift = 31 - __clz(a.c.page_size);
         const int32_t *table = a.page_table + (size_t)b * a.max_pages;
         float *vm = reinterpret_cast<float *>(smem + M::offVm);
-        int *vexp = reinterpret_cast<int *>(vm + 18);
-        const float Fq = a.scale * kLog2e;
+        const float Fq = ldexpf(a.scale * kLog2e, -kq);
         struct Loaded {
             uint32_t kw[J], vw[J];
             float2 ks[G], vs[G];
             bool here, bad;
         };
-        auto fetch = [&](int i) {
+        auto fetch = [&](int i, int key) {
             Loaded x;
             const int t = (tile_lo + i) * kTile + key;
             x.here = i < n_tiles && t <= see_hi && t >= see_lo;
@@ -540,6 +655,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                 x.bad = (uint32_t)page >= (uint32_t)a.c.n_pages;
                 if (!x.bad) row = kv_row(a.c, page, h, t & (a.c.page_size - 1));
             }
+#pragma unroll
+            for (int u = 0; u < J; ++u) x.kw[u] = x.vw[u] = 0u;
+#pragma unroll
+            for (int g = 0; g < G; ++g) x.ks[g] = x.vs[g] = make_float2(0.0f, 0.0f);
             if (x.here && !x.bad) {
                 const uint32_t *kp = a.c.Kq + row * (4 * J) + c * J, *vp = a.c.Vq + row * (4 * J) + c * J;
                 if constexpr (J == 4) {
@@ -558,11 +677,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                     x.ks[g] = __ldg(reinterpret_cast<const float2 *>(a.c.K_sz) + row * G + g);
                     x.vs[g] = __ldg(reinterpret_cast<const float2 *>(a.c.V_sz) + row * G + g);
                 }
-            } else {
-#pragma unroll
-                for (int u = 0; u < J; ++u) x.kw[u] = x.vw[u] = 0u;
-#pragma unroll
-                for (int g = 0; g < G; ++g) x.ks[g] = x.vs[g] = make_float2(0.0f, 0.0f);
             }
             return x;
         };
@@ -574,99 +688,141 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             return m;
         };
         auto finite_of = [](const float2 (&sz)[G]) {
-            float s = 0.0f;
+            float t = 0.0f;
 #pragma unroll
-            for (int g = 0; g < G; ++g) s += 0.0f * sz[g].x + 0.0f * sz[g].y;
-            return s == 0.0f;
+            for (int g = 0; g < G; ++g) t += 0.0f * sz[g].x + 0.0f * sz[g].y;
+            return t == 0.0f;
         };
-        auto store_row = [&](uint32_t base, int u, const uint32_t (&hi)[4], const uint32_t (&lo)[4]) {
+        auto place = [&](uint32_t base, int u, int key) {
             const int d8 = 4 * u + c;
-            const uint32_t at = base + (d8 >> 3) * (kTile * 128) + key * 128 + (((d8 & 7) ^ (key & 7)) << 4);
-            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(hi[0]), "r"(hi[1]), "r"(hi[2]), "r"(hi[3])
-                         : "memory");
-            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + M::kKV), "r"(lo[0]), "r"(lo[1]), "r"(lo[2]),
-                         "r"(lo[3])
-                         : "memory");
+            return base + (d8 >> 3) * (kTile * 128) + key * 128 + (((d8 & 7) ^ (key & 7)) << 4);
         };
-        int ve = 120;                                      // V is held times 2^ve
-        Loaded cur = fetch(0);
+        auto store16 = [](uint32_t at, uint32_t x0, uint32_t x1, uint32_t x2, uint32_t x3) {
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(x0), "r"(x1), "r"(x2), "r"(x3) : "memory");
+        };
+        // the 8 value codes of block u, in order (halves 2c and 2c + 1 lie J halves apart)
+        auto value_word = [](const uint32_t (&vw)[J], int u) {
+            if constexpr (J == 4) return __byte_perm(vw[u / 2], vw[2 + u / 2], (u & 1) ? 0x7632 : 0x5410);
+            else if constexpr (J == 2) return __byte_perm(vw[0], vw[1], u ? 0x7632 : 0x5410);
+            else
+                return u == 0   ? __byte_perm(vw[0], vw[1], 0x7610)
+                       : u == 1 ? __byte_perm(vw[0], vw[2], 0x5432)
+                                : __byte_perm(vw[1], vw[2], 0x7610);
+        };
+        Loaded cur[TN];
+#pragma unroll
+        for (int y = 0; y < TN; ++y) cur[y] = fetch(0, key0 + 8 * W::kDqWarps * y);
         for (int i = 0; i < n_tiles; ++i) {
             const int s = i & 1, k = i >> 1;
-            const Loaded x = cur;
-            cur = fetch(i + 1);
-            if (x.bad && lane < 8) atomicOr(&g_prompt_error, kAttnBadRequest);
-            // ---- K ----
-            const float kb = bound_of(x.ks);
-            const int kk = kb < INFINITY ? scale_exponent(kb) : 0;
-            // a value that is not finite spoils the rows that see it: through the key's factor
-            const bool vfine = finite_of(x.vs);
-            if (i >= 2 && (!warp_wait(&bar.k_empty[s], (k - 1) & 1, abort) ||
-                           !warp_wait(&bar.s_empty[s], (k - 1) & 1, abort))) {
-                ok = false;
-                break;
-            }
-            {
-                const float up = pow2(kk);
-                const uint32_t base = smem_s + M::offK + s * 2 * M::kKV;
+            Loaded x[TN];
 #pragma unroll
-                for (int u = 0; u < J; ++u) {
-                    uint32_t hi[4], lo[4];
-                    dequant_word(x.kw[u], x.ks[u / UG].x * up, x.ks[u / UG].y, hi, lo);
-                    store_row(base, u, hi, lo);
-                }
-                if (c == 0) {
-                    const float f = ldexpf(Fq, -kq - kk);
-                    reinterpret_cast<float *>(smem + M::offF)[s * kTile + key] = x.bad || !vfine ? quiet_nan() : f;
-                }
+            for (int y = 0; y < TN; ++y) {
+                x[y] = cur[y];
+                cur[y] = fetch(i + 1, key0 + 8 * W::kDqWarps * y);
+                if (x[y].bad && c == 0) atomicOr(&g_prompt_error, kAttnBadRequest);
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar.k_full[s]);
-            // ---- V: a power of two for the tile, never growing ----
-            float vb = vfine ? bound_of(x.vs) : 0.0f;
+            // V's largest, for the tile's power of two; a value that is not
+            // finite spoils the rows that see it through its key's factor
+            float vb = 0.0f;
+            bool vfine[TN];
+#pragma unroll
+            for (int y = 0; y < TN; ++y) {
+                vfine[y] = finite_of(x[y].vs);
+                if (vfine[y]) vb = fmaxf(vb, EXACT ? fabsf(x[y].vs[0].x) : bound_of(x[y].vs));
+            }
 #pragma unroll
             for (int o = 4; o > 0; o >>= 1) vb = fmaxf(vb, __shfl_xor_sync(0xffffffffu, vb, o));
             if (lane == 0) {
                 vm[8 * s + w] = vb;
                 mbar_arrive(bar.vmax);
             }
-            if (!warp_wait(bar.vmax, i & 1, abort)) {
+            // ---- K ----
+            if (i >= 2 && (!warp_wait<true>(&bar.k_empty[s], (k - 1) & 1, abort) ||
+                           !warp_wait<true>(&bar.s_empty[s], (k - 1) & 1, abort))) {
+                ok = false;
+                break;
+            }
+            if constexpr (!EXACT) {
+#pragma unroll
+                for (int y = 0; y < TN; ++y) {
+                    const int key = key0 + 8 * W::kDqWarps * y;
+                    const float kb = bound_of(x[y].ks);
+                    const int kk = kb < INFINITY ? scale_exponent(kb) : 0;
+                    const float up = pow2(kk);
+                    const uint32_t base = smem_s + M::offK + s * M::kSlot;
+#pragma unroll
+                    for (int u = 0; u < J; ++u) {
+                        uint32_t hi[4], lo[4];
+                        dequant_word(x[y].kw[u], x[y].ks[u / UG].x * up, x[y].ks[u / UG].y, hi, lo);
+                        const uint32_t at = place(base, u, key);
+                        store16(at, hi[0], hi[1], hi[2], hi[3]);
+                        store16(at + M::kKV, lo[0], lo[1], lo[2], lo[3]);
+                    }
+                    if (c == 0)
+                        reinterpret_cast<float *>(smem + M::offF)[s * kTile + key] =
+                            x[y].bad || !vfine[y] ? quiet_nan() : Fq * pow2(-kk);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.k_full[s]);
+            }
+            if (!warp_wait<true>(bar.vmax, i & 1, abort)) {
                 ok = false;
                 break;
             }
 #pragma unroll
-            for (int y = 0; y < kDqWarps; ++y) vb = fmaxf(vb, vm[8 * s + y]);
-            const int ne = vb > 0.0f ? min(ve, scale_exponent(vb < INFINITY ? vb : 1.0f)) : ve;
-            const float vf = pow2(max(ne - ve, -126));     // what the sums so far are scaled by
-            ve = ne;
-            if (i >= 2 && (!warp_wait(&bar.v_empty[s], (k - 1) & 1, abort) ||
-                           !warp_wait(&bar.o_empty[s], (k - 1) & 1, abort))) {
+            for (int y = 0; y < W::kDqWarps; ++y) vb = fmaxf(vb, vm[8 * s + y]);
+            const int ve = min(scale_exponent(vb < INFINITY ? vb : 1.0f), 110);   // 2^-(ve + 11) is a number
+            if constexpr (EXACT) {
+                // p s 2^(ve - 12) <= 2^kSlack, times 2^11
+#pragma unroll
+                for (int y = 0; y < TN; ++y) {
+                    const int key = key0 + 8 * W::kDqWarps * y;
+                    const uint32_t base = smem_s + M::offK + s * M::kSlot;
+#pragma unroll
+                    for (int u = 0; u < J; ++u) {
+                        const uint4 e = exact_word(x[y].kw[u]);
+                        store16(place(base, u, key), e.x, e.y, e.z, e.w);
+                    }
+                    if (c == 0) {
+                        const float2 ks = x[y].ks[0], vs = x[y].vs[0];
+                        const float F = x[y].bad || !vfine[y] ? quiet_nan() : Fq * ks.x;
+                        float2 *at = reinterpret_cast<float2 *>(smem + M::offF) + s * 2 * kTile + key;
+                        at[0] = make_float2(F, (8.0f - ks.y) * F);
+                        at[kTile] = vfine[y] ? make_float2(vs.x * pow2(ve - 2), vs.y - 8.0f) : make_float2(0.0f, 0.0f);
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.k_full[s]);
+            }
+            // ---- V ----
+            if (i >= 2 && (!warp_wait<true>(&bar.v_empty[s], (k - 1) & 1, abort) ||
+                           !warp_wait<true>(&bar.o_empty[s], (k - 1) & 1, abort))) {
                 ok = false;
                 break;
             }
-            {
-                const float up = vfine ? pow2(ve) : 0.0f;
-                const uint32_t base = smem_s + M::offV + s * 2 * M::kKV;
+#pragma unroll
+            for (int y = 0; y < TN; ++y) {
+                const int key = key0 + 8 * W::kDqWarps * y;
+                const uint32_t base = smem_s + M::offV + s * M::kSlot;
 #pragma unroll
                 for (int u = 0; u < J; ++u) {
-                    // halves 2c and 2c+1 of block u lie J halves apart
-                    uint32_t word;
-                    if constexpr (J == 4) word = __byte_perm(x.vw[u / 2], x.vw[2 + u / 2], (u & 1) ? 0x7632 : 0x5410);
-                    else if constexpr (J == 2) word = __byte_perm(x.vw[0], x.vw[1], u ? 0x7632 : 0x5410);
-                    else
-                        word = u == 0   ? __byte_perm(x.vw[0], x.vw[1], 0x7610)
-                               : u == 1 ? __byte_perm(x.vw[0], x.vw[2], 0x5432)
-                                        : __byte_perm(x.vw[1], x.vw[2], 0x7610);
-                    uint32_t hi[4], lo[4];
-                    const float z = x.vs[u / UG].y, sv = x.vs[u / UG].x;
-                    dequant_word(word, vfine ? sv * up : 0.0f, vfine ? z : 0.0f, hi, lo);
-                    store_row(base, u, hi, lo);
-                }
-                if (w == 0 && lane == 0) {
-                    vm[16 + s] = vf;
-                    vexp[s] = ve;
+                    const uint32_t word = value_word(x[y].vw, u), at = place(base, u, key);
+                    if constexpr (EXACT) {
+                        const uint4 e = exact_word(word);
+                        store16(at, e.x, e.y, e.z, e.w);
+                    } else {
+                        uint32_t hi[4], lo[4];
+                        dequant_word(word, vfine[y] ? x[y].vs[u / UG].x * pow2(ve) : 0.0f,
+                                     vfine[y] ? x[y].vs[u / UG].y : 0.0f, hi, lo);
+                        store16(at, hi[0], hi[1], hi[2], hi[3]);
+                        store16(at + M::kKV, lo[0], lo[1], lo[2], lo[3]);
+                    }
                 }
             }
+            // what takes the tile's P V back: V's power of two and P's
+            if (w == 0 && lane == 0) vm[16 + s] = EXACT ? pow2(2 - ve) : pow2(-ve - kPieceBits);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.v_full[s]);
@@ -675,17 +831,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         // ===== MMA =====
         const uint32_t id_s = idesc_f16_f32(kRows, kTile, false), id_o = idesc_f16_f32(kRows, DP, true);
         const uint32_t qh = smem_s + M::offQ, ql = qh + M::kQ;
+        constexpr int kProducts = EXACT ? 2 : 3;
         bool any = false;
         auto pv = [&](int i) {
             const int s = i & 1, k = i >> 1;
             if (!bar_wait(&bar.p_full[s], k & 1, abort) || !bar_wait(&bar.v_full[s], k & 1, abort)) return false;
             if (i >= 2 && !bar_wait(&bar.o_empty[s], (k - 1) & 1, abort)) return false;
             tc_fence_after_sync();
-            const uint32_t vh = smem_s + M::offV + s * 2 * M::kKV, vl = vh + M::kKV;
+            const uint32_t vh = smem_s + M::offV + s * M::kSlot, vl = vh + M::kKV;
             const uint32_t d = tmem + kColO + s * 128, ph = tmem + kColP + s * 64, pl = ph + 32;
 #pragma unroll
-            for (int x = 0; x < 3; ++x) {
-                const uint32_t at = x == 0 ? pl : ph, bt = x == 1 ? vl : vh;
+            for (int x = 0; x < kProducts; ++x) {
+                const uint32_t at = x == 0 ? pl : ph, bt = !EXACT && x == 1 ? vl : vh;
 #pragma unroll
                 for (int y = 0; y < kTile / 16; ++y)
                     tc_mma_ts(d, at + 8 * y, smem_desc_mn_sw128(bt + 2048 * y, kTile * 128, 1024), id_o,
@@ -701,11 +858,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             ok = bar_wait(&bar.k_full[s], k & 1, abort) && (i < 2 || bar_wait(&bar.s_empty[s], (k - 1) & 1, abort));
             if (!ok) break;
             tc_fence_after_sync();
-            const uint32_t kh = smem_s + M::offK + s * 2 * M::kKV, kl = kh + M::kKV;
+            const uint32_t kh = smem_s + M::offK + s * M::kSlot, kl = kh + M::kKV;
             const uint32_t d = tmem + kColS + s * kTile;
 #pragma unroll
-            for (int x = 0; x < 3; ++x) {
-                const uint32_t at = x == 0 ? ql : qh, bt = x == 1 ? kl : kh;
+            for (int x = 0; x < kProducts; ++x) {
+                const uint32_t at = x == 0 ? ql : qh, bt = !EXACT && x == 1 ? kl : kh;
 #pragma unroll
                 for (int y = 0; y < DP / 16; ++y)
                     tc_mma_ss(d, smem_desc_sw128(at + (y >> 2) * (kRows * 128) + (y & 3) * 32, 1024),
@@ -728,14 +885,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    if (warp == kMma) tmem_dealloc(tmem, kTmemCols);
+    if (warp == W::kMma) tmem_dealloc(tmem, kTmemCols);
 }
 
 template <int J, int G, int DP>
 cudaError_t launch_prompt_t(const AttnCall &call, cudaStream_t stream)
 {
     auto kern = attn_prompt_kernel<J, G, DP>;
-    constexpr int smem = Mem<DP>::kBytes;
+    constexpr int smem = Mem<DP, G == 1>::kBytes;
     int dev = 0;
     cudaError_t err;
     if ((err = cudaGetDevice(&dev)) != cudaSuccess) return err;
