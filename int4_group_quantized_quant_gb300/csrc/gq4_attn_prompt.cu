@@ -25,8 +25,10 @@
 // the tiles, each with its own maximum), 8 that add the tiles' P V (a row and
 // half of head_dim per thread), 4 or 8 that read the cache and write the K and
 // V operands into shared memory, 1 that issues the MMAs.  Tensor memory (512
-// columns): S, P and the tile's O, two slots each, so that the MMA of one
-// tile runs under the softmax of another; K and V have two slots too.
+// columns): S in four slots, whose columns P takes over 16 by 16 as S is read,
+// and the tile's O in two; K and V have four slots in shared memory (EXACT;
+// else two).  The MMA thread runs S ahead of P V, so that no role waits for
+// the next one's tile.
 // K is stored [key][d] (K-major), V [key][d] as well, which is the MN-major
 // form of the second product's B operand: no transposition.
 // Bound by the issue slots of the softmax and dequantising warps, not the fp16
@@ -51,7 +53,9 @@ constexpr int kWarps = 21;                      // all: the roles' warps and the
 constexpr int kThreads = 32 * kWarps;
 constexpr float kSlack = 4.0f;                  // log2 of how far a weight may pass the maximum
 constexpr int kPieceBits = 11;                  // P is held times 2^11
-constexpr uint32_t kColS = 0, kColP = 128, kColO = 256;
+constexpr int kSP = 4;                          // slots of S, which P replaces in place
+constexpr int kTab = 8;                         // slots of the key and row tables
+constexpr uint32_t kColS = 0, kColO = 256;      // S/P: 64 columns a slot; O: 128, two slots
 constexpr uint32_t kTmemCols = 512;
 
 struct PromptParams {
@@ -68,6 +72,8 @@ struct Form {
     static constexpr int kDqWarps = kMma - kDq0;                // 4 or 8
     static constexpr int kPieces = EXACT ? 1 : 2;
     static constexpr int kTurns = 8 / kDqWarps;                 // keys per thread
+    static constexpr int kSlots = EXACT ? 4 : 2;                // of K and of V
+    static constexpr int kAhead = EXACT ? 2 : 1;                // tiles that S runs ahead of P V
 };
 
 // Shared memory of a head of DP = 64 or 128 values (96 is padded with zeros).
@@ -78,17 +84,19 @@ struct Mem {
     static constexpr int kSlot = Form<EXACT>::kPieces * kKV;
     static constexpr int offQ = 0;                      // high, low
     static constexpr int offK = offQ + 2 * kQ;          // [slot][pieces]
-    static constexpr int offV = offK + 2 * kSlot;
-    static constexpr int offF = offV + 2 * kSlot;       // per key (F, G) and (s, z - 8) [slot][2][64], or F [slot][64]
-    static constexpr int offM = offF + 2 * kTile * 16;  // per row (reference, sum p s (z - 8)) [slot][128]
-    static constexpr int offL = offM + 2 * kRows * 8;   // per row (reference, sum of weights) [group][128]
-    static constexpr int offVm = offL + 2 * kRows * 8;  // V's largest per warp [2][8], its factor [2]
-    static constexpr int offBar = offVm + 128;
-    static constexpr int kBytes = offBar + 256 + 1024;  // and room to align
+    static constexpr int offV = offK + Form<EXACT>::kSlots * kSlot;
+    static constexpr int offF = offV + Form<EXACT>::kSlots * kSlot;       // per key (F, G) and (s, z - 8) [slot][2][64], or F [slot][64]
+    static constexpr int offM = offF + kTab * kTile * (EXACT ? 16 : 4);   // per row (reference, sum p s (z - 8)) [slot][128]
+    static constexpr int offL = offM + kTab * kRows * 8;    // per row (reference, sum of weights) [group][128]
+    static constexpr int offQs = offL + 2 * kRows * 8;      // Q's sums over 8 values [128][DP / 8] (EXACT)
+    static constexpr int offVe = offQs + (EXACT ? kRows * DP / 2 : 0);   // V's power of two [slot]
+    static constexpr int offVm = offVe + kTab * 4;          // V's largest per warp [2][8]
+    static constexpr int offBar = offVm + 64;
+    static constexpr int kBytes = offBar + 320 + 1024;  // and room to align
 };
 
 struct Bars {
-    uint64_t *k_full, *k_empty, *v_full, *v_empty, *s_full, *s_empty, *p_full, *o_full, *o_empty, *vmax, *fin, *drain;
+    uint64_t *k_full, *k_empty, *v_full, *v_empty, *s_full, *p_full, *o_full, *o_empty, *vmax, *fin, *drain;
 };
 
 // One MMA, A and B from shared memory (descriptors), D in tensor memory.
@@ -143,6 +151,31 @@ template <bool REST = false>
 __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, volatile int *abort)
 {
     return mbar_try_wait(bar, parity) || bar_wait_slow<REST>(bar, parity, abort);
+}
+
+// The MMA thread's wait: bounded polling without suspension.
+__device__ __forceinline__ bool poll_wait(uint64_t *bar, uint32_t parity, volatile int *abort)
+{
+    const unsigned long long t0 = global_timer_ns();
+    for (unsigned int i = 1;; ++i) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(smem_addr(bar)), "r"(parity)
+            : "memory");
+        if (done) return true;
+        if ((i & 255u) == 0u) {
+            if (*abort) return false;
+            if (global_timer_ns() - t0 > kWaitLimitNs) {
+                *abort = 1;
+                atomicOr(&g_prompt_error, kAttnGaveUp);
+                return false;
+            }
+        }
+    }
 }
 
 // The whole warp waits; false in every lane when any gave up.
@@ -226,76 +259,91 @@ struct RowSum {
 };
 
 // One tile of a row: the weights 2^(w - ref) from S, their two fp16 pieces
-// (times s_j where EXACT, times 2^11) to tensor memory.  Column x counts when
-// first <= x <= last.  The reference moves, and the tile is done again, when a
-// weight passes 2^kSlack of it.  Returns sum_j p_j s_j (z_j - 8) of the tile.
+// (times s_j where EXACT, times 2^11) back into the same columns of tensor
+// memory, 8 of leading pieces and 8 of rests for every 16 keys.  Column x
+// counts when first <= x <= last.  When a weight passes 2^kSlack of it the
+// reference moves by a whole power of two, by which the pieces already
+// written are scaled.  Returns sum_j p_j s_j (z_j - 8) of the tile.
 template <bool EXACT, bool MASK>
-__device__ __forceinline__ float tile_weights(uint32_t s_at, uint32_t p_at, uint32_t key, float qsum, RowSum &r,
-                                              int last, int first)
+__device__ __forceinline__ float tile_weights(uint32_t s_at, uint32_t key, float qsum, RowSum &r, int last, int first)
 {
     constexpr int kCols = 16;          // at a time: a loop, not unrolled, keeps the registers few
-    float l, z;
-    while (true) {
-        bool move = false;
-        l = z = 0.0f;
+    float l = 0.0f, z = 0.0f;
 #pragma unroll 1
-        for (int x = 0; x < kTile; x += kCols) {
-            uint32_t t[kCols];
-            tmem_ld16(s_at + x, t);
-            tmem_wait_ld();
-            float top = -INFINITY;
+    for (int x = 0; x < kTile; x += kCols) {
+        uint32_t t[kCols];
+        tmem_ld16(s_at + x, t);
+        tmem_wait_ld();
+        float top = -INFINITY;
 #pragma unroll
-            for (int y = 0; y < kCols; y += EXACT ? 2 : 4) {
-                float v[4];
-                if constexpr (EXACT) {             // (F, G) of two keys
-                    const float4 f = lds_f4(key + 8 * (x + y));
-                    v[0] = fmaf(__uint_as_float(t[y]), f.x, fmaf(f.y, qsum, -r.ref));
-                    v[1] = fmaf(__uint_as_float(t[y + 1]), f.z, fmaf(f.w, qsum, -r.ref));
-                } else {                           // F of four
-                    const float4 f = lds_f4(key + 4 * (x + y));
-                    v[0] = fmaf(__uint_as_float(t[y]), f.x, -r.ref);
-                    v[1] = fmaf(__uint_as_float(t[y + 1]), f.y, -r.ref);
-                    v[2] = fmaf(__uint_as_float(t[y + 2]), f.z, -r.ref);
-                    v[3] = fmaf(__uint_as_float(t[y + 3]), f.w, -r.ref);
-                }
+        for (int y = 0; y < kCols; y += EXACT ? 2 : 4) {
+            float v[4];
+            if constexpr (EXACT) {             // (F, G) of two keys
+                const float4 f = lds_f4(key + 8 * (x + y));
+                v[0] = fmaf(__uint_as_float(t[y]), f.x, fmaf(f.y, qsum, -r.ref));
+                v[1] = fmaf(__uint_as_float(t[y + 1]), f.z, fmaf(f.w, qsum, -r.ref));
+            } else {                           // F of four
+                const float4 f = lds_f4(key + 4 * (x + y));
+                v[0] = fmaf(__uint_as_float(t[y]), f.x, -r.ref);
+                v[1] = fmaf(__uint_as_float(t[y + 1]), f.y, -r.ref);
+                v[2] = fmaf(__uint_as_float(t[y + 2]), f.z, -r.ref);
+                v[3] = fmaf(__uint_as_float(t[y + 3]), f.w, -r.ref);
+            }
 #pragma unroll
-                for (int n = 0; n < (EXACT ? 2 : 4); ++n) {
-                    if (MASK && (x + y + n > last || x + y + n < first)) v[n] = -INFINITY;
-                    top = fmaxf(top, v[n]);
-                    t[y + n] = __float_as_uint(v[n]);
-                }
+            for (int n = 0; n < (EXACT ? 2 : 4); ++n) {
+                if (MASK && (x + y + n > last || x + y + n < first)) v[n] = -INFINITY;
+                top = fmaxf(top, v[n]);
+                t[y + n] = __float_as_uint(v[n]);
             }
-            const bool mine = top > (r.set ? kSlack : -INFINITY);
-            if (__any_sync(0xffffffffu, mine)) {
-                if (mine) {
-                    r.l *= exp2_approx(-top);      // (0 while nothing is set)
-                    r.ref += top;
-                    r.set = true;
-                }
-                move = true;
-                break;
-            }
-            uint32_t hi[8], lo[8];
-#pragma unroll
-            for (int y = 0; y < kCols; y += 2) {
-                float p0 = exp2_approx(__uint_as_float(t[y])), p1 = exp2_approx(__uint_as_float(t[y + 1]));
-                l += p0 + p1;
-                if constexpr (EXACT) {             // (s, z - 8) of two keys
-                    const float4 f = lds_f4(key + 8 * kTile + 8 * (x + y));
-                    p0 *= f.x;
-                    p1 *= f.z;
-                    z = fmaf(p0, f.y, z);
-                    z = fmaf(p1, f.w, z);
-                } else {
-                    p0 *= 2048.0f;
-                    p1 *= 2048.0f;
-                }
-                split_pair(p0, p1, hi[y / 2], lo[y / 2]);
-            }
-            tmem_st8(p_at + x / 2, hi);
-            tmem_st8(p_at + 32 + x / 2, lo);
         }
-        if (!move) break;
+        const bool mine = top > (r.set ? kSlack : -INFINITY);
+        if (__any_sync(0xffffffffu, mine)) {
+            const float by = mine ? ceilf(top) : 0.0f;
+            const float shrink = mine && r.set ? exp2_approx(fmaxf(-by, -24.0f)) : 1.0f;
+            if (mine) {
+                const float f = exp2_approx(-by);
+                r.l = r.set ? r.l * f : 0.0f;
+                l = r.set ? l * f : 0.0f;
+                z = r.set ? z * f : 0.0f;
+                r.ref += by;
+                r.set = true;
+            }
+            if (x > 0) {                       // pieces of this tile under the old reference
+                const __half2 f2 = __float2half2_rn(shrink);
+                tmem_wait_st();
+                for (int y = 0; y < x; y += kCols) {
+                    uint32_t u[kCols];
+                    tmem_ld16(s_at + y, u);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int n = 0; n < kCols; ++n) {
+                        const __half2 v = __hmul2(*reinterpret_cast<const __half2 *>(&u[n]), f2);
+                        u[n] = *reinterpret_cast<const uint32_t *>(&v);
+                    }
+                    tmem_st16(s_at + y, u);
+                }
+            }
+#pragma unroll
+            for (int y = 0; y < kCols; ++y) t[y] = __float_as_uint(__uint_as_float(t[y]) - by);
+        }
+        uint32_t pc[kCols];                    // leading pieces, rests
+#pragma unroll
+        for (int y = 0; y < kCols; y += 2) {
+            float p0 = exp2_approx(__uint_as_float(t[y])), p1 = exp2_approx(__uint_as_float(t[y + 1]));
+            l += p0 + p1;
+            if constexpr (EXACT) {             // (s, z - 8) of two keys
+                const float4 f = lds_f4(key + 8 * kTile + 8 * (x + y));
+                p0 *= f.x;
+                p1 *= f.z;
+                z = fmaf(p0, f.y, z);
+                z = fmaf(p1, f.w, z);
+            } else {
+                p0 *= 2048.0f;
+                p1 *= 2048.0f;
+            }
+            split_pair(p0, p1, pc[y / 2], pc[8 + y / 2]);
+        }
+        tmem_st16(s_at + x, pc);
     }
     r.l += l;
     return z;
@@ -403,30 +451,30 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
     {
         uint64_t *b = reinterpret_cast<uint64_t *>(smem + M::offBar);
         bar.k_full = b;
-        bar.k_empty = b + 2;
-        bar.v_full = b + 4;
-        bar.v_empty = b + 6;
-        bar.s_full = b + 8;
-        bar.s_empty = b + 10;
-        bar.p_full = b + 12;
-        bar.o_full = b + 14;
-        bar.o_empty = b + 16;
-        bar.fin = b + 18;
-        bar.drain = b + 19;
-        bar.vmax = b + 20;
+        bar.k_empty = b + 4;
+        bar.v_full = b + 8;
+        bar.v_empty = b + 12;
+        bar.o_full = b + 16;
+        bar.o_empty = b + 18;
+        bar.s_full = b + 20;
+        bar.p_full = b + 20 + kSP;
+        bar.fin = b + 20 + kSP + kTab;
+        bar.drain = bar.fin + 1;
+        bar.vmax = bar.fin + 2;
     }
     if (threadIdx.x == 0) {
-        for (int s = 0; s < 2; ++s) {
+        for (int s = 0; s < W::kSlots; ++s) {
             mbar_init(&bar.k_full[s], W::kDqWarps);
             mbar_init(&bar.k_empty[s], 1);
             mbar_init(&bar.v_full[s], W::kDqWarps);
             mbar_init(&bar.v_empty[s], 1);
-            mbar_init(&bar.s_full[s], 1);
-            mbar_init(&bar.s_empty[s], 4);
-            mbar_init(&bar.p_full[s], 4);
+        }
+        for (int s = 0; s < 2; ++s) {
             mbar_init(&bar.o_full[s], 1);
             mbar_init(&bar.o_empty[s], kCoWarps);
         }
+        for (int s = 0; s < kSP; ++s) mbar_init(&bar.s_full[s], 1);
+        for (int s = 0; s < kTab; ++s) mbar_init(&bar.p_full[s], 4);
         mbar_init(bar.fin, W::kCo0);
         mbar_init(bar.drain, 1);
         mbar_init(bar.vmax, W::kDqWarps);
@@ -483,12 +531,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         for (int i = threadIdx.x; i < kRows * (DP / 8); i += kThreads) {
             const int r = i / (DP / 8), d8 = i - r * (DP / 8);
             uint32_t hi[4] = {0u, 0u, 0u, 0u}, lo[4] = {0u, 0u, 0u, 0u};
+            float part = 0.0f;
             if (row0 + r < rows_all && 8 * d8 < D) {
                 const int rho = row0 + r, j = rho / R;
                 const float4 *q = reinterpret_cast<const float4 *>(a.q + (size_t)(rq.row0 + j) * a.ldq +
                                                                   (size_t)(h * R + rho - j * R) * D + 8 * d8);
                 const float4 x = __ldg(q), y = __ldg(q + 1);
                 const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+                part = (((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]))) * up;
 #pragma unroll
                 for (int n = 0; n < 4; ++n)
                     split_pair(v[EXACT ? exact_order(2 * n) : 2 * n] * up, v[EXACT ? exact_order(2 * n + 1) : 2 * n + 1] * up,
@@ -497,11 +547,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             unsigned char *at = smem + M::offQ + (d8 >> 3) * (kRows * 128) + r * 128 + (((d8 & 7) ^ (r & 7)) << 4);
             *reinterpret_cast<uint4 *>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
             *reinterpret_cast<uint4 *>(at + M::kQ) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            if (EXACT) reinterpret_cast<float *>(smem + M::offQs)[r * (DP / 8) + d8] = part;
         }
         // the padding of a 96-value head: zeros in every K and V slot, once
         if constexpr (DP > D) {
             constexpr int per = kTile * (DP - D) / 8;      // 16-byte pieces of one piece's padding
-            for (int i = threadIdx.x; i < 4 * W::kPieces * per; i += kThreads) {   // K's and V's pieces lie on end
+            for (int i = threadIdx.x; i < 2 * W::kSlots * W::kPieces * per; i += kThreads) {   // K's and V's pieces lie on end
                 const int t = i / per, k = (i - t * per) / ((DP - D) / 8), d8 = D / 8 + (i - t * per) % ((DP - D) / 8);
                 *reinterpret_cast<uint4 *>(smem + M::offK + t * M::kKV + (d8 >> 3) * (kTile * 128) + k * 128 +
                                            (((d8 & 7) ^ (k & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
@@ -521,40 +572,32 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         const int last = rho < rows_all ? pos0 + j : -1;
         const int first = attn_first(a, max(last, -1));
         float qsum = 0.0f;
-        if (EXACT && rho < rows_all) {
-            const float4 *q = reinterpret_cast<const float4 *>(a.q + (size_t)(rq.row0 + j) * a.ldq +
-                                                              (size_t)(h * R + rho - j * R) * D);
-#pragma unroll 8
-            for (int d = 0; d < D / 4; ++d) {
-                const float4 v = __ldg(q + d);
-                qsum += (v.x + v.y) + (v.z + v.w);
-            }
-            qsum *= pow2(kq);
+        if (EXACT) {
+#pragma unroll
+            for (int d = 0; d < DP / 8; ++d) qsum += reinterpret_cast<const float *>(smem + M::offQs)[row * (DP / 8) + d];
         }
         RowSum r{0.0f, 0.0f, false};
         float2 *mz = reinterpret_cast<float2 *>(smem + M::offM);
         for (int i = group; i < n_tiles; i += W::kGroups) {
-            const int s = i & 1, k = i >> 1;
-            // S is there; the tile before last is done with (its reference is read, its P used up)
-            if (!warp_wait(&bar.s_full[s], k & 1, abort) || (i >= 2 && !warp_wait(&bar.o_empty[s], (k - 1) & 1, abort))) {
+            const int s = i % kSP, tab = i % kTab;
+            if (!warp_wait(&bar.s_full[s], (i / kSP) & 1, abort)) {
                 ok = false;
                 break;
             }
             tc_fence_after_sync();
-            const uint32_t key = smem_s + M::offF + s * (EXACT ? 16 : 4) * kTile;
+            const uint32_t key = smem_s + M::offF + tab * (EXACT ? 16 : 4) * kTile;
             const int k0 = (tile_lo + i) * kTile;
             const bool masked = k0 + kTile - 1 > all_hi || k0 < all_lo;   // uniform
-            const uint32_t s_at = tmem + lanes + kColS + s * kTile, p_at = tmem + lanes + kColP + s * 64;
-            const float z = masked ? tile_weights<EXACT, true>(s_at, p_at, key, qsum, r, last - k0, first - k0)
-                                   : tile_weights<EXACT, false>(s_at, p_at, key, qsum, r, 0, 0);
-            mz[s * kRows + row] = make_float2(r.set ? r.ref : -INFINITY, z);
+            const uint32_t s_at = tmem + lanes + kColS + s * kTile;
+            const float z = masked ? tile_weights<EXACT, true>(s_at, key, qsum, r, last - k0, first - k0)
+                                   : tile_weights<EXACT, false>(s_at, key, qsum, r, 0, 0);
+            // what the tile's P V is relative to: P's reference and both powers of two
+            const int e = reinterpret_cast<const int *>(smem + M::offVe)[tab];
+            mz[tab * kRows + row] = make_float2(r.set ? r.ref - (float)e : -INFINITY, z);
             tmem_wait_st();
             tc_fence_before_sync();
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&bar.s_empty[s]);
-                mbar_arrive(&bar.p_full[s]);
-            }
+            if (lane == 0) mbar_arrive(&bar.p_full[tab]);
         }
         reinterpret_cast<float2 *>(smem + M::offL)[group * kRows + row] = make_float2(r.set ? r.ref : -INFINITY, r.l);
         __syncwarp();
@@ -566,23 +609,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         const int row = 32 * q4 + lane;
         const uint32_t lanes = (uint32_t)(32 * q4) << 16;
         const float2 *mz = reinterpret_cast<const float2 *>(smem + M::offM);
-        const float *vfac = reinterpret_cast<const float *>(smem + M::offVm) + 16;
         float o[C];
 #pragma unroll
         for (int d = 0; d < C; ++d) o[d] = 0.0f;
         float m = -INFINITY, zs = 0.0f;    // o and zs are relative to 2^m
         for (int i = 0; i < n_tiles; ++i) {
             const int s = i & 1, k = i >> 1;
-            // the row's reference comes with P, V's power of two with V
-            if (!warp_wait<true>(&bar.v_full[s], k & 1, abort) || !warp_wait<true>(&bar.p_full[s], k & 1, abort) ||
-                !warp_wait<true>(&bar.o_full[s], k & 1, abort)) {
+            const int tab = i % kTab;
+            // the row's reference comes with P
+            if (!warp_wait<true>(&bar.p_full[tab], (i / kTab) & 1, abort) || !warp_wait<true>(&bar.o_full[s], k & 1, abort)) {
                 ok = false;
                 break;
             }
             tc_fence_after_sync();
-            const float2 t2 = mz[s * kRows + row];
+            const float2 t2 = mz[tab * kRows + row];
             const float mn = fmaxf(m, t2.x), ref = mn == -INFINITY ? 0.0f : mn;
-            const float ft = exp2_approx(t2.x - ref) * vfac[s];
+            const float ft = exp2_approx(t2.x - ref);
             if (__any_sync(0xffffffffu, mn > m)) {
                 const float fo = exp2_approx(m - ref);
                 zs *= fo;
@@ -642,24 +684,23 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         struct Loaded {
             uint32_t kw[J], vw[J];
             float2 ks[G], vs[G];
-            bool here, bad;
+            bool bad;
         };
-        auto fetch = [&](int i, int key) {
+        // a tile's page is asked for two tiles ahead, its codes one
+        auto page_of = [&](int i, int key) {
+            const int t = (tile_lo + i) * kTile + key;
+            return i < n_tiles && t <= see_hi && t >= see_lo ? __ldg(table + (t >> shift)) : -2;   // -2: not seen
+        };
+        auto fetch = [&](int i, int key, int page) {
             Loaded x;
             const int t = (tile_lo + i) * kTile + key;
-            x.here = i < n_tiles && t <= see_hi && t >= see_lo;
-            x.bad = false;
-            size_t row = 0;
-            if (x.here) {
-                const int page = __ldg(table + (t >> shift));
-                x.bad = (uint32_t)page >= (uint32_t)a.c.n_pages;
-                if (!x.bad) row = kv_row(a.c, page, h, t & (a.c.page_size - 1));
-            }
+            x.bad = page != -2 && (uint32_t)page >= (uint32_t)a.c.n_pages;
 #pragma unroll
             for (int u = 0; u < J; ++u) x.kw[u] = x.vw[u] = 0u;
 #pragma unroll
             for (int g = 0; g < G; ++g) x.ks[g] = x.vs[g] = make_float2(0.0f, 0.0f);
-            if (x.here && !x.bad) {
+            if (page != -2 && !x.bad) {
+                const size_t row = kv_row(a.c, page, h, t & (a.c.page_size - 1));
                 const uint32_t *kp = a.c.Kq + row * (4 * J) + c * J, *vp = a.c.Vq + row * (4 * J) + c * J;
                 if constexpr (J == 4) {
                     const uint4 k4 = __ldg(reinterpret_cast<const uint4 *>(kp)), v4 = __ldg(reinterpret_cast<const uint4 *>(vp));
@@ -710,15 +751,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                                 : __byte_perm(vw[1], vw[2], 0x7610);
         };
         Loaded cur[TN];
+        int page[TN];
 #pragma unroll
-        for (int y = 0; y < TN; ++y) cur[y] = fetch(0, key0 + 8 * W::kDqWarps * y);
+        for (int y = 0; y < TN; ++y) {
+            const int key = key0 + 8 * W::kDqWarps * y;
+            cur[y] = fetch(0, key, page_of(0, key));
+            page[y] = page_of(1, key);
+        }
         for (int i = 0; i < n_tiles; ++i) {
-            const int s = i & 1, k = i >> 1;
+            const int s = i % W::kSlots, k = i / W::kSlots;
             Loaded x[TN];
 #pragma unroll
             for (int y = 0; y < TN; ++y) {
+                const int key = key0 + 8 * W::kDqWarps * y;
                 x[y] = cur[y];
-                cur[y] = fetch(i + 1, key0 + 8 * W::kDqWarps * y);
+                cur[y] = fetch(i + 1, key, page[y]);
+                page[y] = page_of(i + 2, key);
                 if (x[y].bad && c == 0) atomicOr(&g_prompt_error, kAttnBadRequest);
             }
             // V's largest, for the tile's power of two; a value that is not
@@ -733,14 +781,26 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
 #pragma unroll
             for (int o = 4; o > 0; o >>= 1) vb = fmaxf(vb, __shfl_xor_sync(0xffffffffu, vb, o));
             if (lane == 0) {
-                vm[8 * s + w] = vb;
+                vm[8 * (i & 1) + w] = vb;
                 mbar_arrive(bar.vmax);
             }
-            // ---- K ----
-            if (i >= 2 && (!warp_wait<true>(&bar.k_empty[s], (k - 1) & 1, abort) ||
-                           !warp_wait<true>(&bar.s_empty[s], (k - 1) & 1, abort))) {
+            // ---- K (its tables have slots to spare: once the product of the
+            // tile kSlots back is done, the softmax of the one 8 back is) ----
+            const int tab = i % kTab;
+            if (i >= W::kSlots && !warp_wait<true>(&bar.k_empty[s], (k - 1) & 1, abort)) {
                 ok = false;
                 break;
+            }
+            if constexpr (EXACT) {
+#pragma unroll
+                for (int y = 0; y < TN; ++y) {
+                    const uint32_t base = smem_s + M::offK + s * M::kSlot;
+#pragma unroll
+                    for (int u = 0; u < J; ++u) {
+                        const uint4 e = exact_word(x[y].kw[u]);
+                        store16(place(base, u, key0 + 8 * W::kDqWarps * y), e.x, e.y, e.z, e.w);
+                    }
+                }
             }
             if constexpr (!EXACT) {
 #pragma unroll
@@ -759,46 +819,35 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                         store16(at + M::kKV, lo[0], lo[1], lo[2], lo[3]);
                     }
                     if (c == 0)
-                        reinterpret_cast<float *>(smem + M::offF)[s * kTile + key] =
+                        reinterpret_cast<float *>(smem + M::offF)[tab * kTile + key] =
                             x[y].bad || !vfine[y] ? quiet_nan() : Fq * pow2(-kk);
                 }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.k_full[s]);
             }
             if (!warp_wait<true>(bar.vmax, i & 1, abort)) {
                 ok = false;
                 break;
             }
 #pragma unroll
-            for (int y = 0; y < W::kDqWarps; ++y) vb = fmaxf(vb, vm[8 * s + y]);
-            const int ve = min(scale_exponent(vb < INFINITY ? vb : 1.0f), 110);   // 2^-(ve + 11) is a number
-            if constexpr (EXACT) {
+            for (int y = 0; y < W::kDqWarps; ++y) vb = fmaxf(vb, vm[8 * (i & 1) + y]);
+            const int ve = min(scale_exponent(vb < INFINITY ? vb : 1.0f), 80);
+            // what takes the tile's P V back: V's power of two and P's
+            if (w == 0 && lane == 0) reinterpret_cast<int *>(smem + M::offVe)[tab] = EXACT ? ve - 2 : ve + kPieceBits;
+            if (EXACT && c == 0) {
                 // p s 2^(ve - 12) <= 2^kSlack, times 2^11
 #pragma unroll
                 for (int y = 0; y < TN; ++y) {
-                    const int key = key0 + 8 * W::kDqWarps * y;
-                    const uint32_t base = smem_s + M::offK + s * M::kSlot;
-#pragma unroll
-                    for (int u = 0; u < J; ++u) {
-                        const uint4 e = exact_word(x[y].kw[u]);
-                        store16(place(base, u, key), e.x, e.y, e.z, e.w);
-                    }
-                    if (c == 0) {
-                        const float2 ks = x[y].ks[0], vs = x[y].vs[0];
-                        const float F = x[y].bad || !vfine[y] ? quiet_nan() : Fq * ks.x;
-                        float2 *at = reinterpret_cast<float2 *>(smem + M::offF) + s * 2 * kTile + key;
-                        at[0] = make_float2(F, (8.0f - ks.y) * F);
-                        at[kTile] = vfine[y] ? make_float2(vs.x * pow2(ve - 2), vs.y - 8.0f) : make_float2(0.0f, 0.0f);
-                    }
+                    const float2 ks = x[y].ks[0], vs = x[y].vs[0];
+                    const float F = x[y].bad || !vfine[y] ? quiet_nan() : Fq * ks.x;
+                    float2 *at = reinterpret_cast<float2 *>(smem + M::offF) + tab * 2 * kTile + key0 + 8 * W::kDqWarps * y;
+                    at[0] = make_float2(F, (8.0f - ks.y) * F);
+                    at[kTile] = vfine[y] ? make_float2(vs.x * pow2(ve - 2), vs.y - 8.0f) : make_float2(0.0f, 0.0f);
                 }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.k_full[s]);
             }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.k_full[s]);
             // ---- V ----
-            if (i >= 2 && (!warp_wait<true>(&bar.v_empty[s], (k - 1) & 1, abort) ||
-                           !warp_wait<true>(&bar.o_empty[s], (k - 1) & 1, abort))) {
+            if (i >= W::kSlots && !warp_wait<true>(&bar.v_empty[s], (k - 1) & 1, abort)) {
                 ok = false;
                 break;
             }
@@ -821,8 +870,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                     }
                 }
             }
-            // what takes the tile's P V back: V's power of two and P's
-            if (w == 0 && lane == 0) vm[16 + s] = EXACT ? pow2(2 - ve) : pow2(-ve - kPieceBits);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.v_full[s]);
@@ -830,51 +877,57 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
     } else if (lane == 0) {
         // ===== MMA =====
         const uint32_t id_s = idesc_f16_f32(kRows, kTile, false), id_o = idesc_f16_f32(kRows, DP, true);
-        const uint32_t qh = smem_s + M::offQ, ql = qh + M::kQ;
+        // descriptors advance by sixteenths of their byte offsets
+        const uint64_t q_d = smem_desc_sw128(smem_s + M::offQ, 1024), k_d = smem_desc_sw128(smem_s + M::offK, 1024);
+        const uint64_t v_d = smem_desc_mn_sw128(smem_s + M::offV, kTile * 128, 1024);
         constexpr int kProducts = EXACT ? 2 : 3;
         bool any = false;
         auto pv = [&](int i) {
-            const int s = i & 1, k = i >> 1;
-            if (!bar_wait(&bar.p_full[s], k & 1, abort) || !bar_wait(&bar.v_full[s], k & 1, abort)) return false;
-            if (i >= 2 && !bar_wait(&bar.o_empty[s], (k - 1) & 1, abort)) return false;
+            const int s = i & 1, k = i >> 1, vslot = i % W::kSlots;
+            if (!poll_wait(&bar.p_full[i % kTab], (i / kTab) & 1, abort) ||
+                !poll_wait(&bar.v_full[vslot], (i / W::kSlots) & 1, abort))
+                return false;
+            if (i >= 2 && !poll_wait(&bar.o_empty[s], (k - 1) & 1, abort)) return false;
             tc_fence_after_sync();
-            const uint32_t vh = smem_s + M::offV + s * M::kSlot, vl = vh + M::kKV;
-            const uint32_t d = tmem + kColO + s * 128, ph = tmem + kColP + s * 64, pl = ph + 32;
+            const uint64_t vh = v_d + (uint64_t)(vslot * (M::kSlot / 16));
+            const uint32_t d = tmem + kColO + s * 128, ph = tmem + kColS + (i % kSP) * kTile;
 #pragma unroll
-            for (int x = 0; x < kProducts; ++x) {
-                const uint32_t at = x == 0 ? pl : ph, bt = !EXACT && x == 1 ? vl : vh;
+            for (int x = 0; x < kProducts; ++x)
 #pragma unroll
                 for (int y = 0; y < kTile / 16; ++y)
-                    tc_mma_ts(d, at + 8 * y, smem_desc_mn_sw128(bt + 2048 * y, kTile * 128, 1024), id_o,
-                              (x | y) != 0 ? 1u : 0u);
-            }
+                    tc_mma_ts(d, ph + (x == 0 ? 8 : 0) + 16 * y,
+                              vh + (uint64_t)((!EXACT && x == 1 ? M::kKV / 16 : 0) + 128 * y), id_o, (x | y) != 0 ? 1u : 0u);
             tc_commit(&bar.o_full[s]);
-            tc_commit(&bar.v_empty[s]);
+            tc_commit(&bar.v_empty[vslot]);
             any = true;
             return true;
         };
-        for (int i = 0; ok && i < n_tiles; ++i) {
-            const int s = i & 1, k = i >> 1;
-            ok = bar_wait(&bar.k_full[s], k & 1, abort) && (i < 2 || bar_wait(&bar.s_empty[s], (k - 1) & 1, abort));
-            if (!ok) break;
-            tc_fence_after_sync();
-            const uint32_t kh = smem_s + M::offK + s * M::kSlot, kl = kh + M::kKV;
-            const uint32_t d = tmem + kColS + s * kTile;
+        // S of tile i goes into the columns of tile i - 4, whose P V must be
+        // done.  One tile ahead it is: P V of i - 2 has been issued, after its
+        // wait for what was added of i - 4.  Two ahead it is waited for (its
+        // barrier's next phase, i - 2, cannot have begun).
+        for (int i = 0; ok && i < n_tiles + W::kAhead; ++i) {
+            if (i < n_tiles) {
+                const int kslot = i % W::kSlots;
+                ok = poll_wait(&bar.k_full[kslot], (i / W::kSlots) & 1, abort) &&
+                     (W::kAhead == 1 || i < kSP || poll_wait(&bar.o_full[i & 1], ((i - kSP) >> 1) & 1, abort));
+                if (!ok) break;
+                tc_fence_after_sync();
+                const uint64_t kh = k_d + (uint64_t)(kslot * (M::kSlot / 16));
+                const uint32_t d = tmem + kColS + (i % kSP) * kTile;
 #pragma unroll
-            for (int x = 0; x < kProducts; ++x) {
-                const uint32_t at = x == 0 ? ql : qh, bt = !EXACT && x == 1 ? kl : kh;
+                for (int x = 0; x < kProducts; ++x)
 #pragma unroll
-                for (int y = 0; y < DP / 16; ++y)
-                    tc_mma_ss(d, smem_desc_sw128(at + (y >> 2) * (kRows * 128) + (y & 3) * 32, 1024),
-                              smem_desc_sw128(bt + (y >> 2) * (kTile * 128) + (y & 3) * 32, 1024), id_s,
-                              (x | y) != 0 ? 1u : 0u);
+                    for (int y = 0; y < DP / 16; ++y)
+                        tc_mma_ss(d, q_d + (uint64_t)((x == 0 ? M::kQ / 16 : 0) + (y >> 2) * (kRows * 8) + (y & 3) * 2),
+                                  kh + (uint64_t)((!EXACT && x == 1 ? M::kKV / 16 : 0) + (y >> 2) * (kTile * 8) + (y & 3) * 2),
+                                  id_s, (x | y) != 0 ? 1u : 0u);
+                tc_commit(&bar.s_full[i % kSP]);
+                tc_commit(&bar.k_empty[kslot]);
+                any = true;
             }
-            tc_commit(&bar.s_full[s]);
-            tc_commit(&bar.k_empty[s]);
-            any = true;
-            if (i > 0) ok = pv(i - 1);
+            if (i >= W::kAhead) ok = pv(i - W::kAhead);
         }
-        if (ok && n_tiles > 0) ok = pv(n_tiles - 1);
         if (any) {
             // every MMA done before tensor memory and shared memory go
             tc_commit(bar.drain);
