@@ -26,9 +26,10 @@
 // half of head_dim per thread), 4 or 8 that read the cache and write the K and
 // V operands into shared memory, 1 that issues the MMAs.  Tensor memory (512
 // columns): S in four slots, whose columns P takes over 16 by 16 as S is read,
-// and the tile's O in two; K and V have four slots in shared memory (EXACT;
-// else two).  The MMA thread runs S ahead of P V, so that no role waits for
-// the next one's tile.
+// and the tile's O in two; K and V have three slots in shared memory (EXACT;
+// else two), and their warps keep four (two) tiles of the cache as it is on
+// their way there by cp.async.  The MMA warp runs S ahead of P V, so that no
+// role waits for the next one's tile.
 // K is stored [key][d] (K-major), V [key][d] as well, which is the MN-major
 // form of the second product's B operand: no transposition.
 // Bound by the issue slots of the softmax and dequantising warps, not the fp16
@@ -72,13 +73,15 @@ struct Form {
     static constexpr int kDqWarps = kMma - kDq0;                // 4 or 8
     static constexpr int kPieces = EXACT ? 1 : 2;
     static constexpr int kTurns = 8 / kDqWarps;                 // keys per thread
-    static constexpr int kSlots = EXACT ? 4 : 2;                // of K and of V
+    static constexpr int kSlots = EXACT ? 3 : 2;                // of K and of V
+    static constexpr int kRaw = EXACT ? 4 : 2;                  // tiles of the cache as it is
     static constexpr int kAhead = EXACT ? 2 : 1;                // tiles that S runs ahead of P V
 };
 
 // Shared memory of a head of DP = 64 or 128 values (96 is padded with zeros).
-template <int DP, bool EXACT>
+template <int J, int G, int DP>
 struct Mem {
+    static constexpr bool EXACT = G == 1;
     static constexpr int kQ = kRows * DP * 2;           // bytes of a piece
     static constexpr int kKV = kTile * DP * 2;
     static constexpr int kSlot = Form<EXACT>::kPieces * kKV;
@@ -86,13 +89,16 @@ struct Mem {
     static constexpr int offK = offQ + 2 * kQ;          // [slot][pieces]
     static constexpr int offV = offK + Form<EXACT>::kSlots * kSlot;
     static constexpr int offF = offV + Form<EXACT>::kSlots * kSlot;       // per key (F, G) and (s, z - 8) [slot][2][64], or F [slot][64]
-    static constexpr int offM = offF + kTab * kTile * (EXACT ? 16 : 4);   // per row (reference, sum p s (z - 8)) [slot][128]
-    static constexpr int offL = offM + kTab * kRows * 8;    // per row (reference, sum of weights) [group][128]
-    static constexpr int offQs = offL + 2 * kRows * 8;      // Q's sums over 8 values [128][DP / 8] (EXACT)
+    static constexpr int offM = offF + kTab * kTile * (EXACT ? 16 : 4);   // per row: reference, sum p s (z - 8) [2][slot][128]
+    static constexpr int offL = offM + kTab * kRows * (EXACT ? 8 : 4);    // per row (reference, sum of weights) [group][128]
+    static constexpr int offQs = offL + Form<EXACT>::kGroups * kRows * 8;      // Q's sums over 8 values [128][DP / 8] (EXACT)
     static constexpr int offVe = offQs + (EXACT ? kRows * DP / 2 : 0);   // V's power of two [slot]
     static constexpr int offVm = offVe + kTab * 4;          // V's largest per warp [2][8]
     static constexpr int offBar = offVm + 64;
-    static constexpr int kBytes = offBar + 320 + 1024;  // and room to align
+    static constexpr int kRawCodes = kTile * 16 * J, kRawSz = kTile * 8 * G;
+    static constexpr int kRawSlot = 2 * (kRawCodes + kRawSz);
+    static constexpr int offRaw = offBar + 320;         // [slot](key codes, value codes, key (s, z), value (s, z))
+    static constexpr int kBytes = offRaw + Form<EXACT>::kRaw * kRawSlot + 1024;  // and room to align
 };
 
 struct Bars {
@@ -132,12 +138,13 @@ __device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t 
 template <bool REST>
 __device__ __noinline__ bool bar_wait_slow(uint64_t *bar, uint32_t parity, volatile int *abort)
 {
-    const unsigned long long t0 = global_timer_ns();
+    unsigned long long t0 = 0;
     for (unsigned int i = 1;; ++i) {
         if (mbar_try_wait(bar, parity)) return true;
-        if (REST) __nanosleep(32);
+        if (REST) __nanosleep(100);
         if ((i & 15u) == 0u) {
             if (*abort) return false;
+            if (t0 == 0) t0 = global_timer_ns();
             if (global_timer_ns() - t0 > kWaitLimitNs) {
                 *abort = 1;
                 atomicOr(&g_prompt_error, kAttnGaveUp);
@@ -156,7 +163,7 @@ __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, volatil
 // The MMA thread's wait: bounded polling without suspension.
 __device__ __forceinline__ bool poll_wait(uint64_t *bar, uint32_t parity, volatile int *abort)
 {
-    const unsigned long long t0 = global_timer_ns();
+    unsigned long long t0 = 0;     // (the timer is slow to read: not on the short waits)
     for (unsigned int i = 1;; ++i) {
         uint32_t done;
         asm volatile(
@@ -169,6 +176,7 @@ __device__ __forceinline__ bool poll_wait(uint64_t *bar, uint32_t parity, volati
         if (done) return true;
         if ((i & 255u) == 0u) {
             if (*abort) return false;
+            if (t0 == 0) t0 = global_timer_ns();
             if (global_timer_ns() - t0 > kWaitLimitNs) {
                 *abort = 1;
                 atomicOr(&g_prompt_error, kAttnGaveUp);
@@ -251,6 +259,36 @@ __device__ __forceinline__ float4 lds_f4(uint32_t at)
     return v;
 }
 
+__device__ __forceinline__ float2 lds_f2(uint32_t at)
+{
+    float2 v;
+    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
+    return v;
+}
+
+template <int J>
+__device__ __forceinline__ void lds_words(uint32_t at, uint32_t (&w)[J])
+{
+    if constexpr (J == 4) {
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at) : "memory");
+    } else if constexpr (J == 2) {
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at) : "memory");
+    } else {
+#pragma unroll
+        for (int i = 0; i < J; ++i) asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[i]) : "r"(at + 4 * i) : "memory");
+    }
+}
+
+// Asynchronous copy of N = 4, 8 or 16 bytes; zeros (nothing is read) unless ok.
+template <int N>
+__device__ __forceinline__ void cp_async_zfill(uint32_t dst, const void *src, bool ok)
+{
+    if constexpr (N == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(ok ? N : 0) : "memory");
+}
+
 // A softmax thread's row: the reference its weights are taken against (log2),
 // and their sum.
 struct RowSum {
@@ -268,13 +306,16 @@ template <bool EXACT, bool MASK>
 __device__ __forceinline__ float tile_weights(uint32_t s_at, uint32_t key, float qsum, RowSum &r, int last, int first)
 {
     constexpr int kCols = 16;          // at a time: a loop, not unrolled, keeps the registers few
-    float l = 0.0f, z = 0.0f;
+    float l = 0.0f, l2 = 0.0f, z = 0.0f, z2 = 0.0f;
+    uint32_t t[kCols], next[kCols];
+    tmem_ld16(s_at, next);
 #pragma unroll 1
     for (int x = 0; x < kTile; x += kCols) {
-        uint32_t t[kCols];
-        tmem_ld16(s_at + x, t);
         tmem_wait_ld();
-        float top = -INFINITY;
+#pragma unroll
+        for (int y = 0; y < kCols; ++y) t[y] = next[y];
+        if (x + kCols < kTile) tmem_ld16(s_at + x + kCols, next);   // on its way meanwhile
+        float top = -INFINITY, top2 = -INFINITY;
 #pragma unroll
         for (int y = 0; y < kCols; y += EXACT ? 2 : 4) {
             float v[4];
@@ -292,10 +333,12 @@ __device__ __forceinline__ float tile_weights(uint32_t s_at, uint32_t key, float
 #pragma unroll
             for (int n = 0; n < (EXACT ? 2 : 4); ++n) {
                 if (MASK && (x + y + n > last || x + y + n < first)) v[n] = -INFINITY;
-                top = fmaxf(top, v[n]);
+                if (n & 1) top2 = fmaxf(top2, v[n]);
+                else top = fmaxf(top, v[n]);
                 t[y + n] = __float_as_uint(v[n]);
             }
         }
+        top = fmaxf(top, top2);
         const bool mine = top > (r.set ? kSlack : -INFINITY);
         if (__any_sync(0xffffffffu, mine)) {
             const float by = mine ? ceilf(top) : 0.0f;
@@ -303,8 +346,9 @@ __device__ __forceinline__ float tile_weights(uint32_t s_at, uint32_t key, float
             if (mine) {
                 const float f = exp2_approx(-by);
                 r.l = r.set ? r.l * f : 0.0f;
-                l = r.set ? l * f : 0.0f;
-                z = r.set ? z * f : 0.0f;
+                l = r.set ? (l + l2) * f : 0.0f;
+                z = r.set ? (z + z2) * f : 0.0f;
+                l2 = z2 = 0.0f;
                 r.ref += by;
                 r.set = true;
             }
@@ -330,13 +374,14 @@ __device__ __forceinline__ float tile_weights(uint32_t s_at, uint32_t key, float
 #pragma unroll
         for (int y = 0; y < kCols; y += 2) {
             float p0 = exp2_approx(__uint_as_float(t[y])), p1 = exp2_approx(__uint_as_float(t[y + 1]));
-            l += p0 + p1;
+            l += p0;
+            l2 += p1;
             if constexpr (EXACT) {             // (s, z - 8) of two keys
                 const float4 f = lds_f4(key + 8 * kTile + 8 * (x + y));
                 p0 *= f.x;
                 p1 *= f.z;
                 z = fmaf(p0, f.y, z);
-                z = fmaf(p1, f.w, z);
+                z2 = fmaf(p1, f.w, z2);
             } else {
                 p0 *= 2048.0f;
                 p1 *= 2048.0f;
@@ -345,8 +390,8 @@ __device__ __forceinline__ float tile_weights(uint32_t s_at, uint32_t key, float
         }
         tmem_st16(s_at + x, pc);
     }
-    r.l += l;
-    return z;
+    r.l += l + l2;
+    return z + z2;
 }
 
 // 8 codes of a word minus 8, exact, in the order 0, 4, 1, 5, 2, 6, 3, 7.
@@ -404,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
     constexpr int D = 32 * J, UG = J / G;
     constexpr bool EXACT = G == 1;
     using W = Form<EXACT>;
-    using M = Mem<DP, EXACT>;
+    using M = Mem<J, G, DP>;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     const uint32_t smem_s = smem_addr(smem);
@@ -577,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             for (int d = 0; d < DP / 8; ++d) qsum += reinterpret_cast<const float *>(smem + M::offQs)[row * (DP / 8) + d];
         }
         RowSum r{0.0f, 0.0f, false};
-        float2 *mz = reinterpret_cast<float2 *>(smem + M::offM);
+        float *ms = reinterpret_cast<float *>(smem + M::offM);
         for (int i = group; i < n_tiles; i += W::kGroups) {
             const int s = i % kSP, tab = i % kTab;
             if (!warp_wait(&bar.s_full[s], (i / kSP) & 1, abort)) {
@@ -593,7 +638,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                                    : tile_weights<EXACT, false>(s_at, key, qsum, r, 0, 0);
             // what the tile's P V is relative to: P's reference and both powers of two
             const int e = reinterpret_cast<const int *>(smem + M::offVe)[tab];
-            mz[tab * kRows + row] = make_float2(r.set ? r.ref - (float)e : -INFINITY, z);
+            ms[tab * kRows + row] = r.set ? r.ref - (float)e : -INFINITY;
+            if (EXACT) ms[(kTab + tab) * kRows + row] = z;
             tmem_wait_st();
             tc_fence_before_sync();
             __syncwarp();
@@ -608,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         const int q4 = warp & 3, half = (warp - W::kCo0) >> 2;
         const int row = 32 * q4 + lane;
         const uint32_t lanes = (uint32_t)(32 * q4) << 16;
-        const float2 *mz = reinterpret_cast<const float2 *>(smem + M::offM);
+        const float *ms = reinterpret_cast<const float *>(smem + M::offM);
         float o[C];
 #pragma unroll
         for (int d = 0; d < C; ++d) o[d] = 0.0f;
@@ -622,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                 break;
             }
             tc_fence_after_sync();
-            const float2 t2 = mz[tab * kRows + row];
+            const float2 t2 = make_float2(ms[tab * kRows + row], EXACT ? ms[(kTab + tab) * kRows + row] : 0.0f);
             const float mn = fmaxf(m, t2.x), ref = mn == -INFINITY ? 0.0f : mn;
             const float ft = exp2_approx(t2.x - ref);
             if (__any_sync(0xffffffffu, mn > m)) {
@@ -684,40 +730,45 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         struct Loaded {
             uint32_t kw[J], vw[J];
             float2 ks[G], vs[G];
-            bool bad;
         };
-        // a tile's page is asked for two tiles ahead, its codes one
+        // A tile's page is asked for one tile before its codes, and these
+        // kRaw - 1 tiles before their use.  A lane copies its own words; a
+        // key's 2 G scale-and-zero pairs are shared among its four lanes.
         auto page_of = [&](int i, int key) {
             const int t = (tile_lo + i) * kTile + key;
             return i < n_tiles && t <= see_hi && t >= see_lo ? __ldg(table + (t >> shift)) : -2;   // -2: not seen
         };
         auto fetch = [&](int i, int key, int page) {
-            Loaded x;
             const int t = (tile_lo + i) * kTile + key;
-            x.bad = page != -2 && (uint32_t)page >= (uint32_t)a.c.n_pages;
+            const bool ok = (uint32_t)page < (uint32_t)a.c.n_pages;    // else zeros
+            const size_t row = ok ? kv_row(a.c, page, h, t & (a.c.page_size - 1)) : 0;
+            const uint32_t raw = smem_s + M::offRaw + (uint32_t)(i % W::kRaw) * M::kRawSlot;
+            const size_t words = row * (4 * J) + c * J;
+            const uint32_t at = raw + key * 16 * J + c * 4 * J;
+            constexpr int kBytes = J == 3 ? 4 : 4 * J;
 #pragma unroll
-            for (int u = 0; u < J; ++u) x.kw[u] = x.vw[u] = 0u;
+            for (int u = 0; u < J; u += kBytes / 4) {
+                cp_async_zfill<kBytes>(at + 4 * u, a.c.Kq + words + u, ok);
+                cp_async_zfill<kBytes>(at + M::kRawCodes + 4 * u, a.c.Vq + words + u, ok);
+            }
 #pragma unroll
-            for (int g = 0; g < G; ++g) x.ks[g] = x.vs[g] = make_float2(0.0f, 0.0f);
-            if (page != -2 && !x.bad) {
-                const size_t row = kv_row(a.c, page, h, t & (a.c.page_size - 1));
-                const uint32_t *kp = a.c.Kq + row * (4 * J) + c * J, *vp = a.c.Vq + row * (4 * J) + c * J;
-                if constexpr (J == 4) {
-                    const uint4 k4 = __ldg(reinterpret_cast<const uint4 *>(kp)), v4 = __ldg(reinterpret_cast<const uint4 *>(vp));
-                    x.kw[0] = k4.x; x.kw[1] = k4.y; x.kw[2] = k4.z; x.kw[3] = k4.w;
-                    x.vw[0] = v4.x; x.vw[1] = v4.y; x.vw[2] = v4.z; x.vw[3] = v4.w;
-                } else {
+            for (int n = 0; n < 2 * G; n += 4) {
+                const int pc = n + c, side = pc >= G, g = pc - side * G;
+                if (pc < 2 * G)
+                    cp_async_zfill<8>(raw + 2 * M::kRawCodes + side * M::kRawSz + (key * G + g) * 8,
+                                      (side ? a.c.V_sz : a.c.K_sz) + (row * G + g) * 2, ok);
+            }
+            return page != -2 && !ok;      // a page outside the pool
+        };
+        auto read = [&](int i, int key) {
+            Loaded x;
+            const uint32_t raw = smem_s + M::offRaw + (uint32_t)(i % W::kRaw) * M::kRawSlot;
+            lds_words<J>(raw + key * 16 * J + c * 4 * J, x.kw);
+            lds_words<J>(raw + M::kRawCodes + key * 16 * J + c * 4 * J, x.vw);
 #pragma unroll
-                    for (int u = 0; u < J; ++u) {
-                        x.kw[u] = __ldg(kp + u);
-                        x.vw[u] = __ldg(vp + u);
-                    }
-                }
-#pragma unroll
-                for (int g = 0; g < G; ++g) {
-                    x.ks[g] = __ldg(reinterpret_cast<const float2 *>(a.c.K_sz) + row * G + g);
-                    x.vs[g] = __ldg(reinterpret_cast<const float2 *>(a.c.V_sz) + row * G + g);
-                }
+            for (int g = 0; g < G; ++g) {
+                x.ks[g] = lds_f2(raw + 2 * M::kRawCodes + (key * G + g) * 8);
+                x.vs[g] = lds_f2(raw + 2 * M::kRawCodes + M::kRawSz + (key * G + g) * 8);
             }
             return x;
         };
@@ -750,25 +801,34 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                        : u == 1 ? __byte_perm(vw[0], vw[2], 0x5432)
                                 : __byte_perm(vw[1], vw[2], 0x7610);
         };
-        Loaded cur[TN];
         int page[TN];
-#pragma unroll
-        for (int y = 0; y < TN; ++y) {
-            const int key = key0 + 8 * W::kDqWarps * y;
-            cur[y] = fetch(0, key, page_of(0, key));
-            page[y] = page_of(1, key);
-        }
-        for (int i = 0; i < n_tiles; ++i) {
-            const int s = i % W::kSlots, k = i / W::kSlots;
-            Loaded x[TN];
+        uint32_t bad = 0u;                 // bit (tile % kRaw, turn)
+        auto fetch_tile = [&](int i) {
 #pragma unroll
             for (int y = 0; y < TN; ++y) {
                 const int key = key0 + 8 * W::kDqWarps * y;
-                x[y] = cur[y];
-                cur[y] = fetch(i + 1, key, page[y]);
-                page[y] = page_of(i + 2, key);
-                if (x[y].bad && c == 0) atomicOr(&g_prompt_error, kAttnBadRequest);
+                const uint32_t bit = 1u << (i % W::kRaw * TN + y);
+                bad = fetch(i, key, page[y]) ? bad | bit : bad & ~bit;
+                page[y] = page_of(i + 1, key);
             }
+            cp_async_commit();
+        };
+#pragma unroll
+        for (int y = 0; y < TN; ++y) page[y] = page_of(0, key0 + 8 * W::kDqWarps * y);
+        for (int i = 0; i < W::kRaw - 1; ++i) fetch_tile(i);
+        for (int i = 0; i < n_tiles; ++i) {
+            const int s = i % W::kSlots, k = i / W::kSlots;
+            cp_async_wait<W::kRaw - 2>();
+            __syncwarp();
+            Loaded x[TN];
+            bool xbad[TN];
+#pragma unroll
+            for (int y = 0; y < TN; ++y) {
+                x[y] = read(i, key0 + 8 * W::kDqWarps * y);
+                xbad[y] = (bad >> (i % W::kRaw * TN + y)) & 1u;
+                if (xbad[y] && c == 0) atomicOr(&g_prompt_error, kAttnBadRequest);
+            }
+            fetch_tile(i + W::kRaw - 1);   // into the slot of tile i - 1
             // V's largest, for the tile's power of two; a value that is not
             // finite spoils the rows that see it through its key's factor
             float vb = 0.0f;
@@ -820,7 +880,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                     }
                     if (c == 0)
                         reinterpret_cast<float *>(smem + M::offF)[tab * kTile + key] =
-                            x[y].bad || !vfine[y] ? quiet_nan() : Fq * pow2(-kk);
+                            xbad[y] || !vfine[y] ? quiet_nan() : Fq * pow2(-kk);
                 }
             }
             if (!warp_wait<true>(bar.vmax, i & 1, abort)) {
@@ -837,7 +897,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
 #pragma unroll
                 for (int y = 0; y < TN; ++y) {
                     const float2 ks = x[y].ks[0], vs = x[y].vs[0];
-                    const float F = x[y].bad || !vfine[y] ? quiet_nan() : Fq * ks.x;
+                    const float F = xbad[y] || !vfine[y] ? quiet_nan() : Fq * ks.x;
                     float2 *at = reinterpret_cast<float2 *>(smem + M::offF) + tab * 2 * kTile + key0 + 8 * W::kDqWarps * y;
                     at[0] = make_float2(F, (8.0f - ks.y) * F);
                     at[kTile] = vfine[y] ? make_float2(vs.x * pow2(ve - 2), vs.y - 8.0f) : make_float2(0.0f, 0.0f);
@@ -874,8 +934,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.v_full[s]);
         }
+        cp_async_wait<0>();
     } else if (lane == 0) {
-        // ===== MMA =====
+        // ===== MMA: one lane issues =====
         const uint32_t id_s = idesc_f16_f32(kRows, kTile, false), id_o = idesc_f16_f32(kRows, DP, true);
         // descriptors advance by sixteenths of their byte offsets
         const uint64_t q_d = smem_desc_sw128(smem_s + M::offQ, 1024), k_d = smem_desc_sw128(smem_s + M::offK, 1024);
@@ -945,7 +1006,8 @@ template <int J, int G, int DP>
 cudaError_t launch_prompt_t(const AttnCall &call, cudaStream_t stream)
 {
     auto kern = attn_prompt_kernel<J, G, DP>;
-    constexpr int smem = Mem<DP, G == 1>::kBytes;
+    constexpr int smem = Mem<J, G, DP>::kBytes;
+    static_assert(smem + 1024 <= 227 * 1024, "shared memory");
     int dev = 0;
     cudaError_t err;
     if ((err = cudaGetDevice(&dev)) != cudaSuccess) return err;
