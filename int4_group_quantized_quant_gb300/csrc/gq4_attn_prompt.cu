@@ -24,12 +24,13 @@
 // Warps: softmax (a thread per row; EXACT: two groups of 4 that take turns at
 // the tiles, each with its own maximum), 8 that add the tiles' P V (a row and
 // half of head_dim per thread), 4 or 8 that read the cache and write the K and
-// V operands into shared memory, 1 that issues the MMAs.  Tensor memory (512
+// V operands into shared memory, 2 of which a lane issues the MMAs of S and of
+// P V (an MMA's operands cost its thread as much time as the MMA takes).  Tensor memory (512
 // columns): S in four slots, whose columns P takes over 16 by 16 as S is read,
 // and the tile's O in two; K and V have three slots in shared memory (EXACT;
 // else two), and their warps keep four (two) tiles of the cache as it is on
-// their way there by cp.async.  The MMA warp runs S ahead of P V, so that no
-// role waits for the next one's tile.
+// their way there by cp.async.  S runs ahead of P V by as many tiles as it has
+// slots.
 // K is stored [key][d] (K-major), V [key][d] as well, which is the MN-major
 // form of the second product's B operand: no transposition.
 // Bound by the issue slots of the softmax and dequantising warps, not the fp16
@@ -50,7 +51,7 @@ __device__ unsigned int g_prompt_error = 0;
 constexpr int kRows = 128;
 constexpr int kTile = 64;                       // keys
 constexpr int kCoWarps = 8;
-constexpr int kWarps = 21;                      // all: the roles' warps and the MMA's
+constexpr int kWarps = 22;                      // all: the roles' warps and the two MMA warps
 constexpr int kThreads = 32 * kWarps;
 constexpr float kSlack = 4.0f;                  // log2 of how far a weight may pass the maximum
 constexpr int kPieceBits = 11;                  // P is held times 2^11
@@ -69,13 +70,12 @@ struct Form {
     static constexpr int kGroups = EXACT ? 2 : 1;               // softmax groups of 4 warps
     static constexpr int kCo0 = 4 * kGroups;                    // first warp that adds
     static constexpr int kDq0 = kCo0 + kCoWarps;                // first that reads the cache
-    static constexpr int kMma = kWarps - 1;
+    static constexpr int kMma = kWarps - 2;                     // issues S; the next warp P V
     static constexpr int kDqWarps = kMma - kDq0;                // 4 or 8
     static constexpr int kPieces = EXACT ? 1 : 2;
     static constexpr int kTurns = 8 / kDqWarps;                 // keys per thread
     static constexpr int kSlots = EXACT ? 3 : 2;                // of K and of V
     static constexpr int kRaw = EXACT ? 4 : 2;                  // tiles of the cache as it is
-    static constexpr int kAhead = EXACT ? 2 : 1;                // tiles that S runs ahead of P V
 };
 
 // Shared memory of a head of DP = 64 or 128 values (96 is padded with zeros).
@@ -97,23 +97,40 @@ struct Mem {
     static constexpr int offBar = offVm + 64;
     static constexpr int kRawCodes = kTile * 16 * J, kRawSz = kTile * 8 * G;
     static constexpr int kRawSlot = 2 * (kRawCodes + kRawSz);
-    static constexpr int offRaw = offBar + 320;         // [slot](key codes, value codes, key (s, z), value (s, z))
+    static constexpr int offRaw = offBar + 384;         // [slot](key codes, value codes, key (s, z), value (s, z))
     static constexpr int kBytes = offRaw + Form<EXACT>::kRaw * kRawSlot + 1024;  // and room to align
 };
 
 struct Bars {
-    uint64_t *k_full, *k_empty, *v_full, *v_empty, *s_full, *p_full, *o_full, *o_empty, *vmax, *fin, *drain;
+    uint64_t *k_full, *k_empty, *v_full, *v_empty, *s_full, *sp_empty, *p_full, *o_full, *o_empty, *vmax, *fin, *drain;
 };
 
-// One MMA, A and B from shared memory (descriptors), D in tensor memory.
-__device__ __forceinline__ void tc_mma_ss(uint32_t d_taddr, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                          uint32_t accumulate)
+// One MMA, A and B from shared memory, D in tensor memory: the low words of
+// the descriptors, which hold the addresses, and their common high word.
+// ACC: D += (else D =).
+template <bool ACC>
+__device__ __forceinline__ void mma_ss(uint32_t d_taddr, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-        ::"r"(d_taddr), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "mov.b64 a, {%1, %3};\n\t"
+        "mov.b64 b, {%2, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}"
+        ::"r"(d_taddr), "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "n"(ACC ? 1 : 0)
+        : "memory");
+}
+
+// The same with A in tensor memory.
+template <bool ACC>
+__device__ __forceinline__ void mma_ts(uint32_t d_taddr, uint32_t a_taddr, uint32_t b_lo, uint32_t hi, uint32_t idesc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "mov.b64 b, {%2, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}"
+        ::"r"(d_taddr), "r"(a_taddr), "r"(b_lo), "r"(hi), "r"(idesc), "n"(ACC ? 1 : 0)
         : "memory");
 }
 
@@ -502,10 +519,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         bar.o_full = b + 16;
         bar.o_empty = b + 18;
         bar.s_full = b + 20;
-        bar.p_full = b + 20 + kSP;
-        bar.fin = b + 20 + kSP + kTab;
+        bar.sp_empty = b + 20 + kSP;
+        bar.p_full = b + 20 + 2 * kSP;
+        bar.fin = b + 20 + 2 * kSP + kTab;
         bar.drain = bar.fin + 1;
-        bar.vmax = bar.fin + 2;
+        bar.vmax = bar.fin + 3;
     }
     if (threadIdx.x == 0) {
         for (int s = 0; s < W::kSlots; ++s) {
@@ -518,10 +536,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             mbar_init(&bar.o_full[s], 1);
             mbar_init(&bar.o_empty[s], kCoWarps);
         }
-        for (int s = 0; s < kSP; ++s) mbar_init(&bar.s_full[s], 1);
+        for (int s = 0; s < kSP; ++s) {
+            mbar_init(&bar.s_full[s], 1);
+            mbar_init(&bar.sp_empty[s], 1);
+        }
         for (int s = 0; s < kTab; ++s) mbar_init(&bar.p_full[s], 4);
         mbar_init(bar.fin, W::kCo0);
         mbar_init(bar.drain, 1);
+        mbar_init(bar.drain + 1, 1);
         mbar_init(bar.vmax, W::kDqWarps);
         s_abort = 0;
         s_big = 0;
@@ -721,7 +743,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         // ===== the cache: codes, scales and zeros to the operands =====
         // lane: key lane % 8 of eight, values 32 u + 8 (lane / 8) .. + 7 (eight
         // keys of one shared-memory phase meet eight distinct banks)
-        constexpr int TN = W::kTurns;
+        constexpr int TN = W::kTurns, kStep = 8 * W::kDqWarps;   // keys between a lane's turns
         const int w = warp - W::kDq0, key0 = 8 * w + (lane & 7), c = lane >> 3;
         const int shift = 31 - __clz(a.c.page_size);
         const int32_t *table = a.page_table + (size_t)b * a.max_pages;
@@ -734,41 +756,46 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         // A tile's page is asked for one tile before its codes, and these
         // kRaw - 1 tiles before their use.  A lane copies its own words; a
         // key's 2 G scale-and-zero pairs are shared among its four lanes.
-        auto page_of = [&](int i, int key) {
-            const int t = (tile_lo + i) * kTile + key;
+        auto page_of = [&](int i, int y) {
+            const int t = (tile_lo + i) * kTile + key0 + kStep * y;
             return i < n_tiles && t <= see_hi && t >= see_lo ? __ldg(table + (t >> shift)) : -2;   // -2: not seen
         };
-        auto fetch = [&](int i, int key, int page) {
-            const int t = (tile_lo + i) * kTile + key;
-            const bool ok = (uint32_t)page < (uint32_t)a.c.n_pages;    // else zeros
-            const size_t row = ok ? kv_row(a.c, page, h, t & (a.c.page_size - 1)) : 0;
-            const uint32_t raw = smem_s + M::offRaw + (uint32_t)(i % W::kRaw) * M::kRawSlot;
-            const size_t words = row * (4 * J) + c * J;
-            const uint32_t at = raw + key * 16 * J + c * 4 * J;
+        const size_t head_row = (size_t)h * a.c.page_size;
+        const char *k_at = reinterpret_cast<const char *>(a.c.Kq) + head_row * (16 * J) + c * 4 * J;
+        const char *v_at = reinterpret_cast<const char *>(a.c.Vq) + head_row * (16 * J) + c * 4 * J;
+        const char *ks_at = reinterpret_cast<const char *>(a.c.K_sz) + head_row * (8 * G);
+        const char *vs_at = reinterpret_cast<const char *>(a.c.V_sz) + head_row * (8 * G);
+        const uint32_t page_rows = (uint32_t)(H * a.c.page_size), n_pages = (uint32_t)a.c.n_pages;
+        const uint32_t raw0 = smem_s + M::offRaw, raw_w = raw0 + key0 * 16 * J + c * 4 * J, raw_z = raw0 + 2 * M::kRawCodes + key0 * 8 * G;
+        auto fetch = [&](int i, uint32_t slot, int y, int page) {
+            const int t = (tile_lo + i) * kTile + key0 + kStep * y;
+            const bool ok = (uint32_t)page < n_pages;                  // else zeros
+            const size_t row = ok ? (size_t)(uint32_t)page * page_rows + (t & (a.c.page_size - 1)) : 0;
+            const uint32_t at = raw_w + slot + y * kStep * 16 * J;
+            const char *kp = k_at + row * (16 * J), *vp = v_at + row * (16 * J);
             constexpr int kBytes = J == 3 ? 4 : 4 * J;
 #pragma unroll
-            for (int u = 0; u < J; u += kBytes / 4) {
-                cp_async_zfill<kBytes>(at + 4 * u, a.c.Kq + words + u, ok);
-                cp_async_zfill<kBytes>(at + M::kRawCodes + 4 * u, a.c.Vq + words + u, ok);
+            for (int u = 0; u < 4 * J; u += kBytes) {
+                cp_async_zfill<kBytes>(at + u, kp + u, ok);
+                cp_async_zfill<kBytes>(at + M::kRawCodes + u, vp + u, ok);
             }
 #pragma unroll
             for (int n = 0; n < 2 * G; n += 4) {
                 const int pc = n + c, side = pc >= G, g = pc - side * G;
                 if (pc < 2 * G)
-                    cp_async_zfill<8>(raw + 2 * M::kRawCodes + side * M::kRawSz + (key * G + g) * 8,
-                                      (side ? a.c.V_sz : a.c.K_sz) + (row * G + g) * 2, ok);
+                    cp_async_zfill<8>(raw_z + slot + y * kStep * 8 * G + side * M::kRawSz + g * 8,
+                                      (side ? vs_at : ks_at) + row * (8 * G) + g * 8, ok);
             }
             return page != -2 && !ok;      // a page outside the pool
         };
-        auto read = [&](int i, int key) {
+        auto read = [&](uint32_t slot, int y) {
             Loaded x;
-            const uint32_t raw = smem_s + M::offRaw + (uint32_t)(i % W::kRaw) * M::kRawSlot;
-            lds_words<J>(raw + key * 16 * J + c * 4 * J, x.kw);
-            lds_words<J>(raw + M::kRawCodes + key * 16 * J + c * 4 * J, x.vw);
+            lds_words<J>(raw_w + slot + y * kStep * 16 * J, x.kw);
+            lds_words<J>(raw_w + slot + y * kStep * 16 * J + M::kRawCodes, x.vw);
 #pragma unroll
             for (int g = 0; g < G; ++g) {
-                x.ks[g] = lds_f2(raw + 2 * M::kRawCodes + (key * G + g) * 8);
-                x.vs[g] = lds_f2(raw + 2 * M::kRawCodes + M::kRawSz + (key * G + g) * 8);
+                x.ks[g] = lds_f2(raw_z + slot + y * kStep * 8 * G + g * 8);
+                x.vs[g] = lds_f2(raw_z + slot + y * kStep * 8 * G + M::kRawSz + g * 8);
             }
             return x;
         };
@@ -785,9 +812,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             for (int g = 0; g < G; ++g) t += 0.0f * sz[g].x + 0.0f * sz[g].y;
             return t == 0.0f;
         };
-        auto place = [&](uint32_t base, int u, int key) {
-            const int d8 = 4 * u + c;
-            return base + (d8 >> 3) * (kTile * 128) + key * 128 + (((d8 & 7) ^ (key & 7)) << 4);
+        // block u of 32 values of key key0 + kStep y: 16-byte piece 4 u + c of
+        // its row, swizzled by the key (the same for every turn)
+        const uint32_t place0 = key0 * 128 + ((c ^ (key0 & 7)) << 4), place1 = place0 ^ 64u;
+        auto place = [&](uint32_t base, int u, int y) {
+            return base + ((u & 1) ? place1 : place0) + (u >> 1) * (kTile * 128) + y * kStep * 128;
         };
         auto store16 = [](uint32_t at, uint32_t x0, uint32_t x1, uint32_t x2, uint32_t x3) {
             asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(x0), "r"(x1), "r"(x2), "r"(x3) : "memory");
@@ -804,27 +833,27 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         int page[TN];
         uint32_t bad = 0u;                 // bit (tile % kRaw, turn)
         auto fetch_tile = [&](int i) {
+            const uint32_t slot = (uint32_t)(i % W::kRaw) * M::kRawSlot;
 #pragma unroll
             for (int y = 0; y < TN; ++y) {
-                const int key = key0 + 8 * W::kDqWarps * y;
                 const uint32_t bit = 1u << (i % W::kRaw * TN + y);
-                bad = fetch(i, key, page[y]) ? bad | bit : bad & ~bit;
-                page[y] = page_of(i + 1, key);
+                bad = fetch(i, slot, y, page[y]) ? bad | bit : bad & ~bit;
+                page[y] = page_of(i + 1, y);
             }
             cp_async_commit();
         };
 #pragma unroll
-        for (int y = 0; y < TN; ++y) page[y] = page_of(0, key0 + 8 * W::kDqWarps * y);
+        for (int y = 0; y < TN; ++y) page[y] = page_of(0, y);
         for (int i = 0; i < W::kRaw - 1; ++i) fetch_tile(i);
+        int s = 0, phase = 1;              // slot of K and V, parity of the phase before
         for (int i = 0; i < n_tiles; ++i) {
-            const int s = i % W::kSlots, k = i / W::kSlots;
             cp_async_wait<W::kRaw - 2>();
             __syncwarp();
             Loaded x[TN];
             bool xbad[TN];
 #pragma unroll
             for (int y = 0; y < TN; ++y) {
-                x[y] = read(i, key0 + 8 * W::kDqWarps * y);
+                x[y] = read((uint32_t)(i % W::kRaw) * M::kRawSlot, y);
                 xbad[y] = (bad >> (i % W::kRaw * TN + y)) & 1u;
                 if (xbad[y] && c == 0) atomicOr(&g_prompt_error, kAttnBadRequest);
             }
@@ -847,7 +876,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             // ---- K (its tables have slots to spare: once the product of the
             // tile kSlots back is done, the softmax of the one 8 back is) ----
             const int tab = i % kTab;
-            if (i >= W::kSlots && !warp_wait<true>(&bar.k_empty[s], (k - 1) & 1, abort)) {
+            if (i >= W::kSlots && !warp_wait<true>(&bar.k_empty[s], phase, abort)) {
                 ok = false;
                 break;
             }
@@ -858,14 +887,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
 #pragma unroll
                     for (int u = 0; u < J; ++u) {
                         const uint4 e = exact_word(x[y].kw[u]);
-                        store16(place(base, u, key0 + 8 * W::kDqWarps * y), e.x, e.y, e.z, e.w);
+                        store16(place(base, u, y), e.x, e.y, e.z, e.w);
                     }
                 }
             }
             if constexpr (!EXACT) {
 #pragma unroll
                 for (int y = 0; y < TN; ++y) {
-                    const int key = key0 + 8 * W::kDqWarps * y;
+                    const int key = key0 + kStep * y;
                     const float kb = bound_of(x[y].ks);
                     const int kk = kb < INFINITY ? scale_exponent(kb) : 0;
                     const float up = pow2(kk);
@@ -874,7 +903,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                     for (int u = 0; u < J; ++u) {
                         uint32_t hi[4], lo[4];
                         dequant_word(x[y].kw[u], x[y].ks[u / UG].x * up, x[y].ks[u / UG].y, hi, lo);
-                        const uint32_t at = place(base, u, key);
+                        const uint32_t at = place(base, u, y);
                         store16(at, hi[0], hi[1], hi[2], hi[3]);
                         store16(at + M::kKV, lo[0], lo[1], lo[2], lo[3]);
                     }
@@ -898,7 +927,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                 for (int y = 0; y < TN; ++y) {
                     const float2 ks = x[y].ks[0], vs = x[y].vs[0];
                     const float F = xbad[y] || !vfine[y] ? quiet_nan() : Fq * ks.x;
-                    float2 *at = reinterpret_cast<float2 *>(smem + M::offF) + tab * 2 * kTile + key0 + 8 * W::kDqWarps * y;
+                    float2 *at = reinterpret_cast<float2 *>(smem + M::offF) + tab * 2 * kTile + key0 + kStep * y;
                     at[0] = make_float2(F, (8.0f - ks.y) * F);
                     at[kTile] = vfine[y] ? make_float2(vs.x * pow2(ve - 2), vs.y - 8.0f) : make_float2(0.0f, 0.0f);
                 }
@@ -907,17 +936,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.k_full[s]);
             // ---- V ----
-            if (i >= W::kSlots && !warp_wait<true>(&bar.v_empty[s], (k - 1) & 1, abort)) {
+            if (i >= W::kSlots && !warp_wait<true>(&bar.v_empty[s], phase, abort)) {
                 ok = false;
                 break;
             }
 #pragma unroll
             for (int y = 0; y < TN; ++y) {
-                const int key = key0 + 8 * W::kDqWarps * y;
                 const uint32_t base = smem_s + M::offV + s * M::kSlot;
 #pragma unroll
                 for (int u = 0; u < J; ++u) {
-                    const uint32_t word = value_word(x[y].vw, u), at = place(base, u, key);
+                    const uint32_t word = value_word(x[y].vw, u), at = place(base, u, y);
                     if constexpr (EXACT) {
                         const uint4 e = exact_word(word);
                         store16(at, e.x, e.y, e.z, e.w);
@@ -933,67 +961,80 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.v_full[s]);
+            if (++s == W::kSlots) {
+                s = 0;
+                phase ^= 1;
+            }
         }
         cp_async_wait<0>();
-    } else if (lane == 0) {
-        // ===== MMA: one lane issues =====
-        const uint32_t id_s = idesc_f16_f32(kRows, kTile, false), id_o = idesc_f16_f32(kRows, DP, true);
-        // descriptors advance by sixteenths of their byte offsets
-        const uint64_t q_d = smem_desc_sw128(smem_s + M::offQ, 1024), k_d = smem_desc_sw128(smem_s + M::offK, 1024);
-        const uint64_t v_d = smem_desc_mn_sw128(smem_s + M::offV, kTile * 128, 1024);
+    } else if (lane == 0 && warp == W::kMma) {
+        // ===== S = Q K^T: one lane issues =====
+        constexpr uint32_t id_s = idesc_f16_f32(kRows, kTile, false);
         constexpr int kProducts = EXACT ? 2 : 3;
-        bool any = false;
-        auto pv = [&](int i) {
-            const int s = i & 1, k = i >> 1, vslot = i % W::kSlots;
-            if (!poll_wait(&bar.p_full[i % kTab], (i / kTab) & 1, abort) ||
-                !poll_wait(&bar.v_full[vslot], (i / W::kSlots) & 1, abort))
-                return false;
-            if (i >= 2 && !poll_wait(&bar.o_empty[s], (k - 1) & 1, abort)) return false;
+        const uint64_t q_d = smem_desc_sw128(smem_s + M::offQ, 1024), k_d = smem_desc_sw128(smem_s + M::offK, 1024);
+        const uint32_t hi = (uint32_t)(q_d >> 32), q_lo = (uint32_t)q_d, k_lo = (uint32_t)k_d;
+        int slot = 0, phase = 0;
+        for (int i = 0; i < n_tiles; ++i) {
+            if (!poll_wait(&bar.k_full[slot], phase, abort) ||
+                (i >= kSP && !poll_wait(&bar.sp_empty[i % kSP], ((i / kSP) - 1) & 1, abort)))
+                break;
             tc_fence_after_sync();
-            const uint64_t vh = v_d + (uint64_t)(vslot * (M::kSlot / 16));
+            const uint32_t kh = k_lo + (uint32_t)(slot * (M::kSlot / 16));
+            const uint32_t d = tmem + kColS + (i % kSP) * kTile;
+#pragma unroll
+            for (int x = 0; x < kProducts; ++x)
+#pragma unroll
+                for (int y = 0; y < DP / 16; ++y) {
+                    const uint32_t qa = q_lo + (x == 0 ? M::kQ / 16 : 0) + (y >> 2) * (kRows * 8) + (y & 3) * 2;
+                    const uint32_t ka = kh + (!EXACT && x == 1 ? M::kKV / 16 : 0) + (y >> 2) * (kTile * 8) + (y & 3) * 2;
+                    if (x == 0 && y == 0) mma_ss<false>(d, qa, ka, hi, id_s);
+                    else mma_ss<true>(d, qa, ka, hi, id_s);
+                }
+            tc_commit(&bar.s_full[i % kSP]);
+            tc_commit(&bar.k_empty[slot]);
+            if (++slot == W::kSlots) {
+                slot = 0;
+                phase ^= 1;
+            }
+        }
+        // every MMA done before tensor memory and shared memory go
+        tc_commit(bar.drain);
+        (void)mbar_wait(bar.drain, 0);
+    } else if (lane == 0) {
+        // ===== O = P V =====
+        constexpr uint32_t id_o = idesc_f16_f32(kRows, DP, true);
+        constexpr int kProducts = EXACT ? 2 : 3;
+        const uint64_t v_d = smem_desc_mn_sw128(smem_s + M::offV, kTile * 128, 1024);
+        const uint32_t hi = (uint32_t)(v_d >> 32), v_lo = (uint32_t)v_d;
+        int slot = 0, phase = 0;
+        for (int i = 0; i < n_tiles; ++i) {
+            const int s = i & 1;
+            if (!poll_wait(&bar.v_full[slot], phase, abort) ||
+                (i >= 2 && !poll_wait(&bar.o_empty[s], ((i >> 1) - 1) & 1, abort)) ||
+                !poll_wait(&bar.p_full[i % kTab], (i / kTab) & 1, abort))
+                break;
+            tc_fence_after_sync();
+            const uint32_t vh = v_lo + (uint32_t)(slot * (M::kSlot / 16));
             const uint32_t d = tmem + kColO + s * 128, ph = tmem + kColS + (i % kSP) * kTile;
 #pragma unroll
             for (int x = 0; x < kProducts; ++x)
 #pragma unroll
-                for (int y = 0; y < kTile / 16; ++y)
-                    tc_mma_ts(d, ph + (x == 0 ? 8 : 0) + 16 * y,
-                              vh + (uint64_t)((!EXACT && x == 1 ? M::kKV / 16 : 0) + 128 * y), id_o, (x | y) != 0 ? 1u : 0u);
+                for (int y = 0; y < kTile / 16; ++y) {
+                    const uint32_t pa = ph + (x == 0 ? 8 : 0) + 16 * y;
+                    const uint32_t va = vh + (!EXACT && x == 1 ? M::kKV / 16 : 0) + 128 * y;
+                    if (x == 0 && y == 0) mma_ts<false>(d, pa, va, hi, id_o);
+                    else mma_ts<true>(d, pa, va, hi, id_o);
+                }
             tc_commit(&bar.o_full[s]);
-            tc_commit(&bar.v_empty[vslot]);
-            any = true;
-            return true;
-        };
-        // S of tile i goes into the columns of tile i - 4, whose P V must be
-        // done.  One tile ahead it is: P V of i - 2 has been issued, after its
-        // wait for what was added of i - 4.  Two ahead it is waited for (its
-        // barrier's next phase, i - 2, cannot have begun).
-        for (int i = 0; ok && i < n_tiles + W::kAhead; ++i) {
-            if (i < n_tiles) {
-                const int kslot = i % W::kSlots;
-                ok = poll_wait(&bar.k_full[kslot], (i / W::kSlots) & 1, abort) &&
-                     (W::kAhead == 1 || i < kSP || poll_wait(&bar.o_full[i & 1], ((i - kSP) >> 1) & 1, abort));
-                if (!ok) break;
-                tc_fence_after_sync();
-                const uint64_t kh = k_d + (uint64_t)(kslot * (M::kSlot / 16));
-                const uint32_t d = tmem + kColS + (i % kSP) * kTile;
-#pragma unroll
-                for (int x = 0; x < kProducts; ++x)
-#pragma unroll
-                    for (int y = 0; y < DP / 16; ++y)
-                        tc_mma_ss(d, q_d + (uint64_t)((x == 0 ? M::kQ / 16 : 0) + (y >> 2) * (kRows * 8) + (y & 3) * 2),
-                                  kh + (uint64_t)((!EXACT && x == 1 ? M::kKV / 16 : 0) + (y >> 2) * (kTile * 8) + (y & 3) * 2),
-                                  id_s, (x | y) != 0 ? 1u : 0u);
-                tc_commit(&bar.s_full[i % kSP]);
-                tc_commit(&bar.k_empty[kslot]);
-                any = true;
+            tc_commit(&bar.v_empty[slot]);
+            tc_commit(&bar.sp_empty[i % kSP]);
+            if (++slot == W::kSlots) {
+                slot = 0;
+                phase ^= 1;
             }
-            if (i >= W::kAhead) ok = pv(i - W::kAhead);
         }
-        if (any) {
-            // every MMA done before tensor memory and shared memory go
-            tc_commit(bar.drain);
-            (void)mbar_wait(bar.drain, 0);
-        }
+        tc_commit(bar.drain + 1);
+        (void)mbar_wait(bar.drain + 1, 0);
     }
     __syncwarp();
     tc_fence_before_sync();
