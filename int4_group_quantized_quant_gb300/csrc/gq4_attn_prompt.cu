@@ -17,20 +17,21 @@
 // as well, x = xh + xl, and a product is xl yh + xh yl + xh yh: three MMAs, the
 // small ones first.
 // Powers of two keep the pieces inside fp16: one per CTA for Q, one per key
-// for K (undone by F_j), one per tile for V.  The tensor core cuts its sums
+// for K (undone by F_j) and for V (undone in P, against the tile's largest).
+// The tensor core cuts its sums
 // rather than rounding them, so a tile's P V starts at zero and is added to
 // f32 registers.
 //
 // Warps: softmax (a thread per row; EXACT: two groups of 4 that take turns at
 // the tiles, each with its own maximum), 8 that add the tiles' P V (a row and
-// half of head_dim per thread), 4 or 8 that read the cache and write the K and
-// V operands into shared memory, 2 of which a lane issues the MMAs of S and of
-// P V (an MMA's operands cost its thread as much time as the MMA takes).  Tensor memory (512
+// half of head_dim per thread), 2 that fetch the cache's codes, scales and
+// zeros into shared memory by cp.async, 4 or 8 that turn them into the K and V
+// operands, 2 of which a lane issues the MMAs of S and of P V (an MMA's
+// operands cost its thread as much time as the MMA takes).  Tensor memory (512
 // columns): S in four slots, whose columns P takes over 16 by 16 as S is read,
 // and the tile's O in two; K and V have three slots in shared memory (EXACT;
-// else two), and their warps keep four (two) tiles of the cache as it is on
-// their way there by cp.async.  S runs ahead of P V by as many tiles as it has
-// slots.
+// else two), the cache as it is four (two).  S runs ahead of P V by as many
+// tiles as it has slots.
 // K is stored [key][d] (K-major), V [key][d] as well, which is the MN-major
 // form of the second product's B operand: no transposition.
 // Bound by the issue slots of the softmax and dequantising warps, not the fp16
@@ -51,7 +52,7 @@ __device__ unsigned int g_prompt_error = 0;
 constexpr int kRows = 128;
 constexpr int kTile = 64;                       // keys
 constexpr int kCoWarps = 8;
-constexpr int kWarps = 22;                      // all: the roles' warps and the two MMA warps
+constexpr int kWarps = 24;                      // all
 constexpr int kThreads = 32 * kWarps;
 constexpr float kSlack = 4.0f;                  // log2 of how far a weight may pass the maximum
 constexpr int kPieceBits = 11;                  // P is held times 2^11
@@ -70,8 +71,9 @@ struct Form {
     static constexpr int kGroups = EXACT ? 2 : 1;               // softmax groups of 4 warps
     static constexpr int kCo0 = 4 * kGroups;                    // first warp that adds
     static constexpr int kDq0 = kCo0 + kCoWarps;                // first that reads the cache
+    static constexpr int kCopy = kWarps - 4;                    // two that fetch the cache
     static constexpr int kMma = kWarps - 2;                     // issues S; the next warp P V
-    static constexpr int kDqWarps = kMma - kDq0;                // 4 or 8
+    static constexpr int kDqWarps = kCopy - kDq0;               // 4 or 8
     static constexpr int kPieces = EXACT ? 1 : 2;
     static constexpr int kTurns = 8 / kDqWarps;                 // keys per thread
     static constexpr int kSlots = EXACT ? 3 : 2;                // of K and of V
@@ -88,21 +90,21 @@ struct Mem {
     static constexpr int offQ = 0;                      // high, low
     static constexpr int offK = offQ + 2 * kQ;          // [slot][pieces]
     static constexpr int offV = offK + Form<EXACT>::kSlots * kSlot;
-    static constexpr int offF = offV + Form<EXACT>::kSlots * kSlot;       // per key (F, G) and (s, z - 8) [slot][2][64], or F [slot][64]
-    static constexpr int offM = offF + kTab * kTile * (EXACT ? 16 : 4);   // per row: reference, sum p s (z - 8) [2][slot][128]
+    static constexpr int offF = offV + Form<EXACT>::kSlots * kSlot;       // per key (F, G) and (s, z - 8), or F and V's power of two [slot][2][64]
+    static constexpr int offM = offF + kTab * kTile * (EXACT ? 16 : 8);   // per row: reference, sum p s (z - 8) [2][slot][128]
     static constexpr int offL = offM + kTab * kRows * (EXACT ? 8 : 4);    // per row (reference, sum of weights) [group][128]
     static constexpr int offQs = offL + Form<EXACT>::kGroups * kRows * 8;      // Q's sums over 8 values [128][DP / 8] (EXACT)
-    static constexpr int offVe = offQs + (EXACT ? kRows * DP / 2 : 0);   // V's power of two [slot]
-    static constexpr int offVm = offVe + kTab * 4;          // V's largest per warp [2][8]
-    static constexpr int offBar = offVm + 64;
+    static constexpr int offVm = offQs + (EXACT ? kRows * DP / 2 : 0);   // V's largest per warp [slot][8]
+    static constexpr int offBad = offVm + kTab * 8 * 4;     // pages outside the pool, by 16 keys [raw slot][4]
+    static constexpr int offBar = offBad + 64;
     static constexpr int kRawCodes = kTile * 16 * J, kRawSz = kTile * 8 * G;
     static constexpr int kRawSlot = 2 * (kRawCodes + kRawSz);
-    static constexpr int offRaw = offBar + 384;         // [slot](key codes, value codes, key (s, z), value (s, z))
+    static constexpr int offRaw = offBar + 448;         // [slot](key codes, value codes, key (s, z), value (s, z))
     static constexpr int kBytes = offRaw + Form<EXACT>::kRaw * kRawSlot + 1024;  // and room to align
 };
 
 struct Bars {
-    uint64_t *k_full, *k_empty, *v_full, *v_empty, *s_full, *sp_empty, *p_full, *o_full, *o_empty, *vmax, *fin, *drain;
+    uint64_t *k_full, *k_empty, *v_full, *v_empty, *s_full, *sp_empty, *p_full, *o_full, *o_empty, *fin, *drain, *raw_full, *raw_empty;
 };
 
 // One MMA, A and B from shared memory, D in tensor memory: the low words of
@@ -296,16 +298,6 @@ __device__ __forceinline__ void lds_words(uint32_t at, uint32_t (&w)[J])
     }
 }
 
-// Asynchronous copy of N = 4, 8 or 16 bytes; zeros (nothing is read) unless ok.
-template <int N>
-__device__ __forceinline__ void cp_async_zfill(uint32_t dst, const void *src, bool ok)
-{
-    if constexpr (N == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(ok ? N : 0) : "memory");
-}
-
 // A softmax thread's row: the reference its weights are taken against (log2),
 // and their sum.
 struct RowSum {
@@ -314,16 +306,17 @@ struct RowSum {
 };
 
 // One tile of a row: the weights 2^(w - ref) from S, their two fp16 pieces
-// (times s_j where EXACT, times 2^11) back into the same columns of tensor
-// memory, 8 of leading pieces and 8 of rests for every 16 keys.  Column x
-// counts when first <= x <= last.  When a weight passes 2^kSlack of it the
-// reference moves by a whole power of two, by which the pieces already
-// written are scaled.  Returns sum_j p_j s_j (z_j - 8) of the tile.
+// (times 2^e and the key's s_j or V's power of two) back into the same columns
+// of tensor memory, 8 of leading pieces and 8 of rests for every 16 keys.
+// Column x counts when first <= x <= last.  When a weight passes 2^kSlack of
+// it the reference moves by a whole power of two, by which the pieces already
+// written are scaled.  Returns sum_j 2^e p_j s_j (z_j - 8) of the tile.
 template <bool EXACT, bool MASK>
-__device__ __forceinline__ float tile_weights(uint32_t s_at, uint32_t key, float qsum, RowSum &r, int last, int first)
+__device__ __forceinline__ float tile_weights(uint32_t s_at, uint32_t key, float qsum, float e, RowSum &r, int last,
+                                              int first)
 {
     constexpr int kCols = 16;          // at a time: a loop, not unrolled, keeps the registers few
-    float l = 0.0f, l2 = 0.0f, z = 0.0f, z2 = 0.0f;
+    float l = 0.0f, l2 = 0.0f, z = 0.0f, z2 = 0.0f;   // all times 2^e
     uint32_t t[kCols], next[kCols];
     tmem_ld16(s_at, next);
 #pragma unroll 1
@@ -338,14 +331,14 @@ __device__ __forceinline__ float tile_weights(uint32_t s_at, uint32_t key, float
             float v[4];
             if constexpr (EXACT) {             // (F, G) of two keys
                 const float4 f = lds_f4(key + 8 * (x + y));
-                v[0] = fmaf(__uint_as_float(t[y]), f.x, fmaf(f.y, qsum, -r.ref));
-                v[1] = fmaf(__uint_as_float(t[y + 1]), f.z, fmaf(f.w, qsum, -r.ref));
+                v[0] = fmaf(__uint_as_float(t[y]), f.x, fmaf(f.y, qsum, e - r.ref));
+                v[1] = fmaf(__uint_as_float(t[y + 1]), f.z, fmaf(f.w, qsum, e - r.ref));
             } else {                           // F of four
                 const float4 f = lds_f4(key + 4 * (x + y));
-                v[0] = fmaf(__uint_as_float(t[y]), f.x, -r.ref);
-                v[1] = fmaf(__uint_as_float(t[y + 1]), f.y, -r.ref);
-                v[2] = fmaf(__uint_as_float(t[y + 2]), f.z, -r.ref);
-                v[3] = fmaf(__uint_as_float(t[y + 3]), f.w, -r.ref);
+                v[0] = fmaf(__uint_as_float(t[y]), f.x, e - r.ref);
+                v[1] = fmaf(__uint_as_float(t[y + 1]), f.y, e - r.ref);
+                v[2] = fmaf(__uint_as_float(t[y + 2]), f.z, e - r.ref);
+                v[3] = fmaf(__uint_as_float(t[y + 3]), f.w, e - r.ref);
             }
 #pragma unroll
             for (int n = 0; n < (EXACT ? 2 : 4); ++n) {
@@ -355,7 +348,7 @@ __device__ __forceinline__ float tile_weights(uint32_t s_at, uint32_t key, float
                 t[y + n] = __float_as_uint(v[n]);
             }
         }
-        top = fmaxf(top, top2);
+        top = fmaxf(top, top2) - e;
         const bool mine = top > (r.set ? kSlack : -INFINITY);
         if (__any_sync(0xffffffffu, mine)) {
             const float by = mine ? ceilf(top) : 0.0f;
@@ -399,15 +392,16 @@ __device__ __forceinline__ float tile_weights(uint32_t s_at, uint32_t key, float
                 p1 *= f.z;
                 z = fmaf(p0, f.y, z);
                 z2 = fmaf(p1, f.w, z2);
-            } else {
-                p0 *= 2048.0f;
-                p1 *= 2048.0f;
+            } else {                           // V's powers of two
+                const float2 f = lds_f2(key + 4 * kTile + 4 * (x + y));
+                p0 *= f.x;
+                p1 *= f.y;
             }
             split_pair(p0, p1, pc[y / 2], pc[8 + y / 2]);
         }
         tmem_st16(s_at + x, pc);
     }
-    r.l += l + l2;
+    r.l = fmaf(l + l2, exp2_approx(-e), r.l);
     return z + z2;
 }
 
@@ -523,7 +517,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         bar.p_full = b + 20 + 2 * kSP;
         bar.fin = b + 20 + 2 * kSP + kTab;
         bar.drain = bar.fin + 1;
-        bar.vmax = bar.fin + 3;
+        bar.raw_full = bar.fin + 3;
+        bar.raw_empty = bar.raw_full + 4;
     }
     if (threadIdx.x == 0) {
         for (int s = 0; s < W::kSlots; ++s) {
@@ -544,7 +539,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         mbar_init(bar.fin, W::kCo0);
         mbar_init(bar.drain, 1);
         mbar_init(bar.drain + 1, 1);
-        mbar_init(bar.vmax, W::kDqWarps);
+        for (int s = 0; s < W::kRaw; ++s) {
+            mbar_init(&bar.raw_full[s], 64);       // every copying thread's copies
+            mbar_init(&bar.raw_empty[s], W::kDqWarps);
+        }
         s_abort = 0;
         s_big = 0;
         mbar_fence_init();
@@ -652,15 +650,24 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                 break;
             }
             tc_fence_after_sync();
-            const uint32_t key = smem_s + M::offF + tab * (EXACT ? 16 : 4) * kTile;
+            const uint32_t key = smem_s + M::offF + tab * (EXACT ? 16 : 8) * kTile;
+            // the tile's largest V (EXACT: its scale), as a power of two: P is
+            // held times 2^e, so that 2^kSlack of it is below 2^15
+            float vb = 0.0f;
+#pragma unroll
+            for (int x = 0; x < W::kDqWarps; x += 4) {
+                const float4 v = lds_f4(smem_s + M::offVm + (tab * 8 + x) * 4);
+                vb = fmaxf(vb, fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)));
+            }
+            const int ve = min(scale_exponent(vb), 80);
+            const float e = (float)(EXACT ? ve - 2 : ve + kPieceBits);
             const int k0 = (tile_lo + i) * kTile;
             const bool masked = k0 + kTile - 1 > all_hi || k0 < all_lo;   // uniform
             const uint32_t s_at = tmem + lanes + kColS + s * kTile;
-            const float z = masked ? tile_weights<EXACT, true>(s_at, key, qsum, r, last - k0, first - k0)
-                                   : tile_weights<EXACT, false>(s_at, key, qsum, r, 0, 0);
-            // what the tile's P V is relative to: P's reference and both powers of two
-            const int e = reinterpret_cast<const int *>(smem + M::offVe)[tab];
-            ms[tab * kRows + row] = r.set ? r.ref - (float)e : -INFINITY;
+            const float z = masked ? tile_weights<EXACT, true>(s_at, key, qsum, e, r, last - k0, first - k0)
+                                   : tile_weights<EXACT, false>(s_at, key, qsum, e, r, 0, 0);
+            // what the tile's P V is relative to
+            ms[tab * kRows + row] = r.set ? r.ref - e : -INFINITY;
             if (EXACT) ms[(kTab + tab) * kRows + row] = z;
             tmem_wait_st();
             tc_fence_before_sync();
@@ -739,66 +746,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                 *reinterpret_cast<float4 *>(out + d + 4) = make_float4(v[4], v[5], v[6], v[7]);
             }
         }
-    } else if (warp < W::kMma) {
+    } else if (warp < W::kCopy) {
         // ===== the cache: codes, scales and zeros to the operands =====
         // lane: key lane % 8 of eight, values 32 u + 8 (lane / 8) .. + 7 (eight
         // keys of one shared-memory phase meet eight distinct banks)
         constexpr int TN = W::kTurns, kStep = 8 * W::kDqWarps;   // keys between a lane's turns
         const int w = warp - W::kDq0, key0 = 8 * w + (lane & 7), c = lane >> 3;
-        const int shift = 31 - __clz(a.c.page_size);
-        const int32_t *table = a.page_table + (size_t)b * a.max_pages;
-        float *vm = reinterpret_cast<float *>(smem + M::offVm);
         const float Fq = ldexpf(a.scale * kLog2e, -kq);
-        struct Loaded {
-            uint32_t kw[J], vw[J];
-            float2 ks[G], vs[G];
-        };
-        // A tile's page is asked for one tile before its codes, and these
-        // kRaw - 1 tiles before their use.  A lane copies its own words; a
-        // key's 2 G scale-and-zero pairs are shared among its four lanes.
-        auto page_of = [&](int i, int y) {
-            const int t = (tile_lo + i) * kTile + key0 + kStep * y;
-            return i < n_tiles && t <= see_hi && t >= see_lo ? __ldg(table + (t >> shift)) : -2;   // -2: not seen
-        };
-        const size_t head_row = (size_t)h * a.c.page_size;
-        const char *k_at = reinterpret_cast<const char *>(a.c.Kq) + head_row * (16 * J) + c * 4 * J;
-        const char *v_at = reinterpret_cast<const char *>(a.c.Vq) + head_row * (16 * J) + c * 4 * J;
-        const char *ks_at = reinterpret_cast<const char *>(a.c.K_sz) + head_row * (8 * G);
-        const char *vs_at = reinterpret_cast<const char *>(a.c.V_sz) + head_row * (8 * G);
-        const uint32_t page_rows = (uint32_t)(H * a.c.page_size), n_pages = (uint32_t)a.c.n_pages;
+        // this lane's words and its key's scales in a raw slot
         const uint32_t raw0 = smem_s + M::offRaw, raw_w = raw0 + key0 * 16 * J + c * 4 * J, raw_z = raw0 + 2 * M::kRawCodes + key0 * 8 * G;
-        auto fetch = [&](int i, uint32_t slot, int y, int page) {
-            const int t = (tile_lo + i) * kTile + key0 + kStep * y;
-            const bool ok = (uint32_t)page < n_pages;                  // else zeros
-            const size_t row = ok ? (size_t)(uint32_t)page * page_rows + (t & (a.c.page_size - 1)) : 0;
-            const uint32_t at = raw_w + slot + y * kStep * 16 * J;
-            const char *kp = k_at + row * (16 * J), *vp = v_at + row * (16 * J);
-            constexpr int kBytes = J == 3 ? 4 : 4 * J;
-#pragma unroll
-            for (int u = 0; u < 4 * J; u += kBytes) {
-                cp_async_zfill<kBytes>(at + u, kp + u, ok);
-                cp_async_zfill<kBytes>(at + M::kRawCodes + u, vp + u, ok);
-            }
-#pragma unroll
-            for (int n = 0; n < 2 * G; n += 4) {
-                const int pc = n + c, side = pc >= G, g = pc - side * G;
-                if (pc < 2 * G)
-                    cp_async_zfill<8>(raw_z + slot + y * kStep * 8 * G + side * M::kRawSz + g * 8,
-                                      (side ? vs_at : ks_at) + row * (8 * G) + g * 8, ok);
-            }
-            return page != -2 && !ok;      // a page outside the pool
-        };
-        auto read = [&](uint32_t slot, int y) {
-            Loaded x;
-            lds_words<J>(raw_w + slot + y * kStep * 16 * J, x.kw);
-            lds_words<J>(raw_w + slot + y * kStep * 16 * J + M::kRawCodes, x.vw);
-#pragma unroll
-            for (int g = 0; g < G; ++g) {
-                x.ks[g] = lds_f2(raw_z + slot + y * kStep * 8 * G + g * 8);
-                x.vs[g] = lds_f2(raw_z + slot + y * kStep * 8 * G + M::kRawSz + g * 8);
-            }
-            return x;
-        };
         // the largest |(code - z) s| that the row's scales allow
         auto bound_of = [](const float2 (&sz)[G]) {
             float m = 0.0f;
@@ -830,108 +786,80 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                        : u == 1 ? __byte_perm(vw[0], vw[2], 0x5432)
                                 : __byte_perm(vw[1], vw[2], 0x7610);
         };
-        int page[TN];
-        uint32_t bad = 0u;                 // bit (tile % kRaw, turn)
-        auto fetch_tile = [&](int i) {
-            const uint32_t slot = (uint32_t)(i % W::kRaw) * M::kRawSlot;
-#pragma unroll
-            for (int y = 0; y < TN; ++y) {
-                const uint32_t bit = 1u << (i % W::kRaw * TN + y);
-                bad = fetch(i, slot, y, page[y]) ? bad | bit : bad & ~bit;
-                page[y] = page_of(i + 1, y);
-            }
-            cp_async_commit();
-        };
-#pragma unroll
-        for (int y = 0; y < TN; ++y) page[y] = page_of(0, y);
-        for (int i = 0; i < W::kRaw - 1; ++i) fetch_tile(i);
         int s = 0, phase = 1;              // slot of K and V, parity of the phase before
         for (int i = 0; i < n_tiles; ++i) {
-            cp_async_wait<W::kRaw - 2>();
-            __syncwarp();
-            Loaded x[TN];
-            bool xbad[TN];
-#pragma unroll
-            for (int y = 0; y < TN; ++y) {
-                x[y] = read((uint32_t)(i % W::kRaw) * M::kRawSlot, y);
-                xbad[y] = (bad >> (i % W::kRaw * TN + y)) & 1u;
-                if (xbad[y] && c == 0) atomicOr(&g_prompt_error, kAttnBadRequest);
-            }
-            fetch_tile(i + W::kRaw - 1);   // into the slot of tile i - 1
-            // V's largest, for the tile's power of two; a value that is not
-            // finite spoils the rows that see it through its key's factor
-            float vb = 0.0f;
-            bool vfine[TN];
-#pragma unroll
-            for (int y = 0; y < TN; ++y) {
-                vfine[y] = finite_of(x[y].vs);
-                if (vfine[y]) vb = fmaxf(vb, EXACT ? fabsf(x[y].vs[0].x) : bound_of(x[y].vs));
-            }
-#pragma unroll
-            for (int o = 4; o > 0; o >>= 1) vb = fmaxf(vb, __shfl_xor_sync(0xffffffffu, vb, o));
-            if (lane == 0) {
-                vm[8 * (i & 1) + w] = vb;
-                mbar_arrive(bar.vmax);
-            }
-            // ---- K (its tables have slots to spare: once the product of the
-            // tile kSlots back is done, the softmax of the one 8 back is) ----
-            const int tab = i % kTab;
-            if (i >= W::kSlots && !warp_wait<true>(&bar.k_empty[s], phase, abort)) {
+            const int rs = i % W::kRaw, tab = i % kTab;
+            const uint32_t raw = (uint32_t)rs * M::kRawSlot;
+            if (!warp_wait<true>(&bar.raw_full[rs], (i / W::kRaw) & 1, abort) ||
+                (i >= W::kSlots && !warp_wait<true>(&bar.k_empty[s], phase, abort))) {
                 ok = false;
                 break;
             }
-            if constexpr (EXACT) {
+            // ---- K, and the keys' tables (they have slots to spare: once the
+            // product of the tile kSlots back is done, the softmax of the one 8
+            // back is) ----
+            float vb = 0.0f;
+            float2 vs[TN][G];
+            float vup[TN];
 #pragma unroll
-                for (int y = 0; y < TN; ++y) {
-                    const uint32_t base = smem_s + M::offK + s * M::kSlot;
+            for (int y = 0; y < TN; ++y) {
+                const int key = key0 + kStep * y, t = (tile_lo + i) * kTile + key;
+                const uint32_t zat = raw_z + raw + y * kStep * 8 * G;
+                const bool here = t <= see_hi && t >= see_lo;      // else what lies there counts for nothing
+                const bool bad = here && reinterpret_cast<const int *>(smem + M::offBad)[rs * 4 + (key >> 4)] != 0;
+                float2 ks[G];
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                    ks[g] = lds_f2(zat + 8 * g);
+                    vs[y][g] = lds_f2(zat + M::kRawSz + 8 * g);
+                    if (!here || bad) ks[g] = vs[y][g] = make_float2(0.0f, 0.0f);
+                }
+                // a value that is not finite spoils the rows that see it through its key's factor
+                const bool spoilt = bad || !finite_of(vs[y]);
+                if (spoilt) {
+#pragma unroll
+                    for (int g = 0; g < G; ++g) vs[y][g] = make_float2(0.0f, 0.0f);
+                }
+                const float vk = EXACT ? fabsf(vs[y][0].x) : bound_of(vs[y]);
+                vb = fmaxf(vb, vk);
+                uint32_t kw[J];
+                lds_words<J>(raw_w + raw + y * kStep * 16 * J, kw);
+                const uint32_t base = smem_s + M::offK + s * M::kSlot;
+                if constexpr (EXACT) {
 #pragma unroll
                     for (int u = 0; u < J; ++u) {
-                        const uint4 e = exact_word(x[y].kw[u]);
+                        const uint4 e = exact_word(kw[u]);
                         store16(place(base, u, y), e.x, e.y, e.z, e.w);
                     }
-                }
-            }
-            if constexpr (!EXACT) {
-#pragma unroll
-                for (int y = 0; y < TN; ++y) {
-                    const int key = key0 + kStep * y;
-                    const float kb = bound_of(x[y].ks);
-                    const int kk = kb < INFINITY ? scale_exponent(kb) : 0;
+                    if (c == 0) {
+                        const float F = spoilt ? quiet_nan() : Fq * ks[0].x;
+                        float2 *at = reinterpret_cast<float2 *>(smem + M::offF) + tab * 2 * kTile + key;
+                        at[0] = make_float2(F, (8.0f - ks[0].y) * F);
+                        at[kTile] = make_float2(vs[y][0].x, vs[y][0].y - 8.0f);
+                    }
+                } else {
+                    const float kb = bound_of(ks);
+                    const int kk = kb < INFINITY ? scale_exponent(kb) : 0, vv = min(scale_exponent(vk), 80);
                     const float up = pow2(kk);
-                    const uint32_t base = smem_s + M::offK + s * M::kSlot;
+                    vup[y] = pow2(vv);
 #pragma unroll
                     for (int u = 0; u < J; ++u) {
                         uint32_t hi[4], lo[4];
-                        dequant_word(x[y].kw[u], x[y].ks[u / UG].x * up, x[y].ks[u / UG].y, hi, lo);
+                        dequant_word(kw[u], ks[u / UG].x * up, ks[u / UG].y, hi, lo);
                         const uint32_t at = place(base, u, y);
                         store16(at, hi[0], hi[1], hi[2], hi[3]);
                         store16(at + M::kKV, lo[0], lo[1], lo[2], lo[3]);
                     }
-                    if (c == 0)
-                        reinterpret_cast<float *>(smem + M::offF)[tab * kTile + key] =
-                            xbad[y] || !vfine[y] ? quiet_nan() : Fq * pow2(-kk);
+                    if (c == 0) {
+                        float *at = reinterpret_cast<float *>(smem + M::offF) + tab * 2 * kTile + key;
+                        at[0] = spoilt ? quiet_nan() : Fq * pow2(-kk);
+                        at[kTile] = pow2(-vv);
+                    }
                 }
             }
-            if (!warp_wait<true>(bar.vmax, i & 1, abort)) {
-                ok = false;
-                break;
-            }
 #pragma unroll
-            for (int y = 0; y < W::kDqWarps; ++y) vb = fmaxf(vb, vm[8 * (i & 1) + y]);
-            const int ve = min(scale_exponent(vb < INFINITY ? vb : 1.0f), 80);
-            // what takes the tile's P V back: V's power of two and P's
-            if (w == 0 && lane == 0) reinterpret_cast<int *>(smem + M::offVe)[tab] = EXACT ? ve - 2 : ve + kPieceBits;
-            if (EXACT && c == 0) {
-                // p s 2^(ve - 12) <= 2^kSlack, times 2^11
-#pragma unroll
-                for (int y = 0; y < TN; ++y) {
-                    const float2 ks = x[y].ks[0], vs = x[y].vs[0];
-                    const float F = xbad[y] || !vfine[y] ? quiet_nan() : Fq * ks.x;
-                    float2 *at = reinterpret_cast<float2 *>(smem + M::offF) + tab * 2 * kTile + key0 + kStep * y;
-                    at[0] = make_float2(F, (8.0f - ks.y) * F);
-                    at[kTile] = vfine[y] ? make_float2(vs.x * pow2(ve - 2), vs.y - 8.0f) : make_float2(0.0f, 0.0f);
-                }
-            }
+            for (int o = 4; o > 0; o >>= 1) vb = fmaxf(vb, __shfl_xor_sync(0xffffffffu, vb, o));
+            if (lane == 0) reinterpret_cast<float *>(smem + M::offVm)[tab * 8 + w] = vb;
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.k_full[s]);
@@ -943,16 +871,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
 #pragma unroll
             for (int y = 0; y < TN; ++y) {
                 const uint32_t base = smem_s + M::offV + s * M::kSlot;
+                uint32_t vw[J];
+                lds_words<J>(raw_w + raw + y * kStep * 16 * J + M::kRawCodes, vw);
 #pragma unroll
                 for (int u = 0; u < J; ++u) {
-                    const uint32_t word = value_word(x[y].vw, u), at = place(base, u, y);
+                    const uint32_t word = value_word(vw, u), at = place(base, u, y);
                     if constexpr (EXACT) {
                         const uint4 e = exact_word(word);
                         store16(at, e.x, e.y, e.z, e.w);
                     } else {
                         uint32_t hi[4], lo[4];
-                        dequant_word(word, vfine[y] ? x[y].vs[u / UG].x * pow2(ve) : 0.0f,
-                                     vfine[y] ? x[y].vs[u / UG].y : 0.0f, hi, lo);
+                        dequant_word(word, vs[y][u / UG].x * vup[y], vs[y][u / UG].y, hi, lo);
                         store16(at, hi[0], hi[1], hi[2], hi[3]);
                         store16(at + M::kKV, lo[0], lo[1], lo[2], lo[3]);
                     }
@@ -960,12 +889,65 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bar.v_full[s]);
+            if (lane == 0) {
+                mbar_arrive(&bar.v_full[s]);
+                mbar_arrive(&bar.raw_empty[rs]);
+            }
             if (++s == W::kSlots) {
                 s = 0;
                 phase ^= 1;
             }
         }
+    } else if (warp < W::kMma) {
+        // ===== the cache into shared memory: 16 keys of a page are contiguous =====
+        const int th = (int)threadIdx.x - 32 * W::kCopy;       // of 64
+        const int shift = 31 - __clz(a.c.page_size);
+        const int32_t *table = a.page_table + (size_t)b * a.max_pages;
+        const size_t head_row = (size_t)h * a.c.page_size;
+        const char *k_at = reinterpret_cast<const char *>(a.c.Kq) + head_row * (16 * J) + 16 * th;
+        const char *v_at = reinterpret_cast<const char *>(a.c.Vq) + head_row * (16 * J) + 16 * th;
+        // scales and zeros of 16 keys: 8 G pieces of 16 bytes each side
+        const int side = th >= 8 * G, zp = th - side * 8 * G;
+        const char *z_at = reinterpret_cast<const char *>(side ? a.c.V_sz : a.c.K_sz) + head_row * (8 * G) + 16 * zp;
+        const uint32_t page_rows = (uint32_t)(H * a.c.page_size), n_pages = (uint32_t)a.c.n_pages;
+        int *bad = reinterpret_cast<int *>(smem + M::offBad);
+        // the pages of a tile's four 16-key blocks; -2: nothing is seen there
+        auto pages_of = [&](int i, int (&pg)[4]) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const int t = (tile_lo + i) * kTile + 16 * x;
+                pg[x] = i < n_tiles && t <= see_hi && t + 16 > see_lo ? __ldg(table + (t >> shift)) : -2;
+            }
+        };
+        int pg[4], next[4];
+        pages_of(0, pg);
+        for (int i = 0; i < n_tiles; ++i) {
+            const int rs = i % W::kRaw;
+            pages_of(i + 1, next);
+            if (i >= W::kRaw && !warp_wait<true>(&bar.raw_empty[rs], ((i / W::kRaw) - 1) & 1, abort)) {
+                ok = false;
+                break;
+            }
+            const uint32_t raw = smem_s + M::offRaw + (uint32_t)rs * M::kRawSlot;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const bool in = (uint32_t)pg[x] < n_pages, out = !in && pg[x] != -2;
+                if (th == x) {
+                    bad[rs * 4 + x] = out;
+                    if (out) atomicOr(&g_prompt_error, kAttnBadRequest);
+                }
+                const size_t row = in ? (size_t)(uint32_t)pg[x] * page_rows + ((((tile_lo + i) * kTile) + 16 * x) & (a.c.page_size - 1)) : 0;
+                if (in && th < 16 * J) {
+                    cp_async_16(raw + x * 256 * J + 16 * th, k_at + row * (16 * J));
+                    cp_async_16(raw + M::kRawCodes + x * 256 * J + 16 * th, v_at + row * (16 * J));
+                }
+                if (in && th < 16 * G)
+                    cp_async_16(raw + 2 * M::kRawCodes + side * M::kRawSz + x * 128 * G + 16 * zp, z_at + row * (8 * G));
+                pg[x] = next[x];
+            }
+            cp_async_mbar_arrive(&bar.raw_full[rs]);
+        }
+        cp_async_commit();
         cp_async_wait<0>();
     } else if (lane == 0 && warp == W::kMma) {
         // ===== S = Q K^T: one lane issues =====
@@ -1048,7 +1030,7 @@ cudaError_t launch_prompt_t(const AttnCall &call, cudaStream_t stream)
 {
     auto kern = attn_prompt_kernel<J, G, DP>;
     constexpr int smem = Mem<J, G, DP>::kBytes;
-    static_assert(smem + 1024 <= 227 * 1024, "shared memory");
+    static_assert(smem + 256 <= 227 * 1024, "shared memory (and the static part)");
     int dev = 0;
     cudaError_t err;
     if ((err = cudaGetDevice(&dev)) != cudaSuccess) return err;
