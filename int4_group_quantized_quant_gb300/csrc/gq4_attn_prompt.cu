@@ -90,12 +90,12 @@ struct Mem {
     static constexpr int offQ = 0;                      // high, low
     static constexpr int offK = offQ + 2 * kQ;          // [slot][pieces]
     static constexpr int offV = offK + Form<EXACT>::kSlots * kSlot;
-    static constexpr int offF = offV + Form<EXACT>::kSlots * kSlot;       // per key (F, G) and (s, z - 8), or F and V's power of two [slot][2][64]
+    static constexpr int offF = offV + Form<EXACT>::kSlots * kSlot;       // per key F, G, s, z - 8, or F and V's power of two [slot][4 or 2][64]
     static constexpr int offM = offF + kTab * kTile * (EXACT ? 16 : 8);   // per row: reference, sum p s (z - 8) [2][slot][128]
     static constexpr int offL = offM + kTab * kRows * (EXACT ? 8 : 4);    // per row (reference, sum of weights) [group][128]
     static constexpr int offQs = offL + Form<EXACT>::kGroups * kRows * 8;      // Q's sums over 8 values [128][DP / 8] (EXACT)
-    static constexpr int offVm = offQs + (EXACT ? kRows * DP / 2 : 0);   // V's largest per warp [slot][8]
-    static constexpr int offBad = offVm + kTab * 8 * 4;     // pages outside the pool, by 16 keys [raw slot][4]
+    static constexpr int offVm = offQs + (EXACT ? kRows * DP / 2 : 0);   // V's largest, by 32 keys [slot][2]
+    static constexpr int offBad = offVm + kTab * 8;         // pages outside the pool, by 16 keys [raw slot][4]
     static constexpr int offBar = offBad + 64;
     static constexpr int kRawCodes = kTile * 16 * J, kRawSz = kTile * 8 * G;
     static constexpr int kRawSlot = 2 * (kRawCodes + kRawSz);
@@ -152,15 +152,28 @@ __device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t 
 }
 
 // Bounded wait: gives up when another thread of the CTA gave up, or after the
-// time limit (recording the error).  REST: the waiting warp sleeps between
-// looks, leaving the issue slots to the others.
-template <bool REST>
+// time limit (recording the error).  try_wait without a time hint leaves the
+// thread suspended for as long as the hardware likes, so a waiting warp takes
+// few issue slots from the others (with a hint it became a loop of looks and
+// sleeps, half of all instructions); the timer is read on long waits only.
+__device__ __forceinline__ bool try_wait_once(uint64_t *bar, uint32_t parity)
+{
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+
 __device__ __noinline__ bool bar_wait_slow(uint64_t *bar, uint32_t parity, volatile int *abort)
 {
     unsigned long long t0 = 0;
     for (unsigned int i = 1;; ++i) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if (REST) __nanosleep(100);
+        if (try_wait_once(bar, parity)) return true;
         if ((i & 15u) == 0u) {
             if (*abort) return false;
             if (t0 == 0) t0 = global_timer_ns();
@@ -173,43 +186,24 @@ __device__ __noinline__ bool bar_wait_slow(uint64_t *bar, uint32_t parity, volat
     }
 }
 
-template <bool REST = false>
 __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, volatile int *abort)
 {
-    return mbar_try_wait(bar, parity) || bar_wait_slow<REST>(bar, parity, abort);
-}
-
-// The MMA thread's wait: bounded polling without suspension.
-__device__ __forceinline__ bool poll_wait(uint64_t *bar, uint32_t parity, volatile int *abort)
-{
-    unsigned long long t0 = 0;     // (the timer is slow to read: not on the short waits)
-    for (unsigned int i = 1;; ++i) {
-        uint32_t done;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(done)
-            : "r"(smem_addr(bar)), "r"(parity)
-            : "memory");
-        if (done) return true;
-        if ((i & 255u) == 0u) {
-            if (*abort) return false;
-            if (t0 == 0) t0 = global_timer_ns();
-            if (global_timer_ns() - t0 > kWaitLimitNs) {
-                *abort = 1;
-                atomicOr(&g_prompt_error, kAttnGaveUp);
-                return false;
-            }
-        }
-    }
+    return try_wait_once(bar, parity) || bar_wait_slow(bar, parity, abort);
 }
 
 // The whole warp waits; false in every lane when any gave up.
-template <bool REST = false>
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort)
 {
-    return __all_sync(0xffffffffu, bar_wait<REST>(bar, parity, abort));
+    return __all_sync(0xffffffffu, bar_wait(bar, parity, abort));
+}
+
+// Wait for the loads, of which v's are the last: v is not to be used before.
+template <int N>
+__device__ __forceinline__ void tmem_wait_for(uint32_t (&v)[N])
+{
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+r"(v[i]));
 }
 
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&v)[8])
@@ -228,13 +222,19 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8])
 }
 
 // Two numbers as their leading fp16 pieces and the rest, each pair packed.
+// The rest is one operation, an FMA of fp16 factors onto an f32 number.
 __device__ __forceinline__ void split_pair(float a, float b, uint32_t &hi, uint32_t &lo)
 {
-    const __half2 h = __floats2half2_rn(a, b);
-    const float2 f = __half22float2(h);
-    const __half2 r = __floats2half2_rn(a - f.x, b - f.y);
-    hi = *reinterpret_cast<const uint32_t *>(&h);
-    lo = *reinterpret_cast<const uint32_t *>(&r);
+    float x, y;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(b), "f"(a));
+    asm("{\n\t.reg .b16 h, l, m;\n\t"
+        "mov.b32 {l, h}, %2;\n\t"
+        "mov.b16 m, 0xBC00;\n\t"            // -1
+        "fma.rn.f32.f16 %0, l, m, %3;\n\t"
+        "fma.rn.f32.f16 %1, h, m, %4;\n\t}"
+        : "=f"(x), "=f"(y)
+        : "r"(hi), "f"(a), "f"(b));
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(y), "f"(x));
 }
 
 // 2^k with |x| 2^k in [2^12, 2^13) for the exponent field of x (0: as it is).
@@ -264,17 +264,15 @@ __device__ __forceinline__ void dequant_word(uint32_t w, float s, float z, uint3
     for (int i = 0; i < 4; ++i) {
         const f32x2 d = add2(add2(p[i], nm), i & 1 ? zp.nz23 : zp.nz01);
         const f32x2 sc = i & 1 ? s23 : s01;
-        f32x2 v;
-        asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(d), "l"(sc));
-        const float2 f = unpack2(v);
+        const float2 f = unpack2(mul2(d, sc));
         split_pair(f.x, f.y, hi[i], lo[i]);
     }
 }
 
-__device__ __forceinline__ float4 lds_f4(uint32_t at)
+__device__ __forceinline__ float lds_f1(uint32_t at)
 {
-    float4 v;
-    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
     return v;
 }
 
@@ -298,6 +296,12 @@ __device__ __forceinline__ void lds_words(uint32_t at, uint32_t (&w)[J])
     }
 }
 
+// Four consecutive floats as two packed pairs.
+__device__ __forceinline__ void lds_pairs(uint32_t at, f32x2 (&v)[2])
+{
+    asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(v[0]), "=l"(v[1]) : "r"(at) : "memory");
+}
+
 // A softmax thread's row: the reference its weights are taken against (log2),
 // and their sum.
 struct RowSum {
@@ -305,104 +309,118 @@ struct RowSum {
     bool set;        // ref is a maximum seen
 };
 
-// One tile of a row: the weights 2^(w - ref) from S, their two fp16 pieces
-// (times 2^e and the key's s_j or V's power of two) back into the same columns
-// of tensor memory, 8 of leading pieces and 8 of rests for every 16 keys.
-// Column x counts when first <= x <= last.  When a weight passes 2^kSlack of
-// it the reference moves by a whole power of two, by which the pieces already
-// written are scaled.  Returns sum_j 2^e p_j s_j (z_j - 8) of the tile.
-template <bool EXACT, bool MASK>
-__device__ __forceinline__ float tile_weights(uint32_t s_at, uint32_t key, float qsum, float e, RowSum &r, int last,
-                                              int first)
+// The pieces of a tile's first `cols` keys times `by`, a power of two (rarely
+// needed).
+__device__ __forceinline__ void scale_pieces(uint32_t s_at, int cols, float by)
 {
-    constexpr int kCols = 16;          // at a time: a loop, not unrolled, keeps the registers few
-    float l = 0.0f, l2 = 0.0f, z = 0.0f, z2 = 0.0f;   // all times 2^e
-    uint32_t t[kCols], next[kCols];
-    tmem_ld16(s_at, next);
+    const __half2 f = __float2half2_rn(by);
+    tmem_wait_st();
 #pragma unroll 1
-    for (int x = 0; x < kTile; x += kCols) {
-        tmem_wait_ld();
+    for (int x = 0; x < cols; x += 8) {
+        uint32_t u[8];
+        tmem_ld8(s_at + x, u);
+        tmem_wait_for(u);
 #pragma unroll
-        for (int y = 0; y < kCols; ++y) t[y] = next[y];
-        if (x + kCols < kTile) tmem_ld16(s_at + x + kCols, next);   // on its way meanwhile
-        float top = -INFINITY, top2 = -INFINITY;
-#pragma unroll
-        for (int y = 0; y < kCols; y += EXACT ? 2 : 4) {
-            float v[4];
-            if constexpr (EXACT) {             // (F, G) of two keys
-                const float4 f = lds_f4(key + 8 * (x + y));
-                v[0] = fmaf(__uint_as_float(t[y]), f.x, fmaf(f.y, qsum, e - r.ref));
-                v[1] = fmaf(__uint_as_float(t[y + 1]), f.z, fmaf(f.w, qsum, e - r.ref));
-            } else {                           // F of four
-                const float4 f = lds_f4(key + 4 * (x + y));
-                v[0] = fmaf(__uint_as_float(t[y]), f.x, e - r.ref);
-                v[1] = fmaf(__uint_as_float(t[y + 1]), f.y, e - r.ref);
-                v[2] = fmaf(__uint_as_float(t[y + 2]), f.z, e - r.ref);
-                v[3] = fmaf(__uint_as_float(t[y + 3]), f.w, e - r.ref);
-            }
-#pragma unroll
-            for (int n = 0; n < (EXACT ? 2 : 4); ++n) {
-                if (MASK && (x + y + n > last || x + y + n < first)) v[n] = -INFINITY;
-                if (n & 1) top2 = fmaxf(top2, v[n]);
-                else top = fmaxf(top, v[n]);
-                t[y + n] = __float_as_uint(v[n]);
-            }
+        for (int n = 0; n < 8; ++n) {
+            const __half2 v = __hmul2(*reinterpret_cast<const __half2 *>(&u[n]), f);
+            u[n] = *reinterpret_cast<const uint32_t *>(&v);
         }
-        top = fmaxf(top, top2) - e;
-        const bool mine = top > (r.set ? kSlack : -INFINITY);
-        if (__any_sync(0xffffffffu, mine)) {
-            const float by = mine ? ceilf(top) : 0.0f;
-            const float shrink = mine && r.set ? exp2_approx(fmaxf(-by, -24.0f)) : 1.0f;
-            if (mine) {
-                const float f = exp2_approx(-by);
-                r.l = r.set ? r.l * f : 0.0f;
-                l = r.set ? (l + l2) * f : 0.0f;
-                z = r.set ? (z + z2) * f : 0.0f;
-                l2 = z2 = 0.0f;
-                r.ref += by;
-                r.set = true;
-            }
-            if (x > 0) {                       // pieces of this tile under the old reference
-                const __half2 f2 = __float2half2_rn(shrink);
-                tmem_wait_st();
-                for (int y = 0; y < x; y += kCols) {
-                    uint32_t u[kCols];
-                    tmem_ld16(s_at + y, u);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int n = 0; n < kCols; ++n) {
-                        const __half2 v = __hmul2(*reinterpret_cast<const __half2 *>(&u[n]), f2);
-                        u[n] = *reinterpret_cast<const uint32_t *>(&v);
-                    }
-                    tmem_st16(s_at + y, u);
-                }
-            }
-#pragma unroll
-            for (int y = 0; y < kCols; ++y) t[y] = __float_as_uint(__uint_as_float(t[y]) - by);
-        }
-        uint32_t pc[kCols];                    // leading pieces, rests
-#pragma unroll
-        for (int y = 0; y < kCols; y += 2) {
-            float p0 = exp2_approx(__uint_as_float(t[y])), p1 = exp2_approx(__uint_as_float(t[y + 1]));
-            l += p0;
-            l2 += p1;
-            if constexpr (EXACT) {             // (s, z - 8) of two keys
-                const float4 f = lds_f4(key + 8 * kTile + 8 * (x + y));
-                p0 *= f.x;
-                p1 *= f.z;
-                z = fmaf(p0, f.y, z);
-                z2 = fmaf(p1, f.w, z2);
-            } else {                           // V's powers of two
-                const float2 f = lds_f2(key + 4 * kTile + 4 * (x + y));
-                p0 *= f.x;
-                p1 *= f.y;
-            }
-            split_pair(p0, p1, pc[y / 2], pc[8 + y / 2]);
-        }
-        tmem_st16(s_at + x, pc);
+        tmem_st8(s_at + x, u);
     }
-    r.l = fmaf(l + l2, exp2_approx(-e), r.l);
-    return z + z2;
+}
+
+// What a tile's weights are made with.
+struct TileOf {
+    uint32_t s_at, key;     // S in tensor memory; the key tables in shared memory
+    f32x2 qsum;             // sum_d q_d, twice
+    float e;                // P is held times 2^e
+    int last, first;        // column x counts when first <= x <= last
+};
+
+// 16 keys, S in t: the weights 2^(w - ref), their two fp16 pieces (times 2^e
+// and the key's s_j or V's power of two) back into the same columns of tensor
+// memory, 8 of leading pieces and 8 of rests.  When a weight passes 2^kSlack
+// of it the reference moves by a whole power of two, by which the pieces of
+// this tile already written are scaled.  l and z: sums of the weights and of
+// p_j s_j (z_j - 8), both times 2^e, over even and odd keys.
+template <bool EXACT, bool MASK>
+__device__ __forceinline__ void keys16(const TileOf &w, int x, uint32_t (&t)[16], RowSum &r, f32x2 &l, f32x2 &z)
+{
+    float top = -INFINITY;
+    const float b = w.e - r.ref;
+    const f32x2 base = pack2(b, b);
+#pragma unroll
+    for (int y = 0; y < 16; y += 4) {
+        f32x2 f[2], g[2];
+        lds_pairs(w.key + 4 * (x + y), f);                          // F
+        if (EXACT) lds_pairs(w.key + 4 * (kTile + x + y), g);       // G
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            const int c = y + 2 * n;
+            const f32x2 a = EXACT ? fma2(g[n], w.qsum, base) : base;
+            float2 v = unpack2(fma2(pack2(__uint_as_float(t[c]), __uint_as_float(t[c + 1])), f[n], a));
+            if (MASK && (x + c > w.last || x + c < w.first)) v.x = -INFINITY;
+            if (MASK && (x + c + 1 > w.last || x + c + 1 < w.first)) v.y = -INFINITY;
+            top = fmaxf(top, fmaxf(v.x, v.y));
+            t[c] = __float_as_uint(v.x);
+            t[c + 1] = __float_as_uint(v.y);
+        }
+    }
+    top -= w.e;
+    const bool mine = top > (r.set ? kSlack : -INFINITY);
+    if (__any_sync(0xffffffffu, mine)) {
+        const float by = mine ? ceilf(top) : 0.0f;
+        const float shrink = mine && r.set ? exp2_approx(fmaxf(-by, -24.0f)) : 1.0f;
+        if (mine) {
+            const float f = r.set ? exp2_approx(-by) : 0.0f;   // (0: nothing is summed yet)
+            r.l = r.set ? r.l * f : 0.0f;
+            l = r.set ? mul2(l, pack2(f, f)) : pack2(0.0f, 0.0f);
+            z = r.set ? mul2(z, pack2(f, f)) : pack2(0.0f, 0.0f);
+            r.ref += by;
+            r.set = true;
+        }
+        if (x > 0) scale_pieces(w.s_at, x, shrink);
+#pragma unroll
+        for (int y = 0; y < 16; ++y) t[y] = __float_as_uint(__uint_as_float(t[y]) - by);
+    }
+    uint32_t pc[16];                       // leading pieces, rests
+#pragma unroll
+    for (int y = 0; y < 16; y += 4) {
+        f32x2 s[2], q[2];
+        lds_pairs(w.key + 4 * ((EXACT ? 2 : 1) * kTile + x + y), s);        // s, or V's powers of two
+        if (EXACT) lds_pairs(w.key + 4 * (3 * kTile + x + y), q);           // z - 8
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            const int c = y + 2 * n;
+            f32x2 p = pack2(exp2_approx(__uint_as_float(t[c])), exp2_approx(__uint_as_float(t[c + 1])));
+            l = add2(l, p);
+            p = mul2(p, s[n]);
+            if (EXACT) z = fma2(p, q[n], z);
+            const float2 v = unpack2(p);
+            split_pair(v.x, v.y, pc[c / 2], pc[8 + c / 2]);
+        }
+    }
+    tmem_st16(w.s_at + x, pc);
+}
+
+// One tile of a row; returns sum_j 2^e p_j s_j (z_j - 8).
+template <bool EXACT, bool MASK>
+__device__ __forceinline__ float tile_weights(const TileOf &w, RowSum &r)
+{
+    f32x2 l = pack2(0.0f, 0.0f), z = l;
+    uint32_t t[16], next[16];              // one is on its way while the other is worked on
+    tmem_ld16(w.s_at, next);
+#pragma unroll 1                               // (a small loop: the roles share the instruction cache)
+    for (int x = 0; x < kTile; x += 16) {
+        tmem_wait_for(next);
+#pragma unroll
+        for (int y = 0; y < 16; ++y) t[y] = next[y];
+        if (x + 16 < kTile) tmem_ld16(w.s_at + x + 16, next);
+        keys16<EXACT, MASK>(w, x, t, r, l, z);
+    }
+    const float2 ls = unpack2(l), zs = unpack2(z);
+    r.l = fmaf(ls.x + ls.y, exp2_approx(-w.e), r.l);
+    return zs.x + zs.y;
 }
 
 // 8 codes of a word minus 8, exact, in the order 0, 4, 1, 5, 2, 6, 3, 7.
@@ -429,6 +447,36 @@ __device__ __forceinline__ uint4 exact_word(uint32_t w)
 __host__ __device__ constexpr int exact_order(int i)
 {
     return (i >> 1) + 4 * (i & 1);
+}
+
+// A key's scales and zeros of one side: zeros where the CTA does not see it or
+// its page is outside the pool.
+template <int G>
+struct KeyOf {
+    bool bad, finite;
+    float bound;             // the largest |(code - z) s| that they allow
+    __device__ __forceinline__ int exponent() const { return bound < INFINITY ? scale_exponent(bound) : 0; }
+};
+
+template <int G>
+__device__ __forceinline__ KeyOf<G> key_of(int see_lo, int see_hi, int t, uint32_t at, uint32_t bad_at, float2 (&sz)[G])
+{
+    KeyOf<G> k;
+    int bad;
+    asm volatile("ld.shared.s32 %0, [%1];" : "=r"(bad) : "r"(bad_at) : "memory");
+    const bool here = t <= see_hi && t >= see_lo;
+    k.bad = here && bad != 0;
+    k.bound = 0.0f;
+    float f = 0.0f;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        sz[g] = lds_f2(at + 8 * g);
+        if (!here || bad != 0) sz[g] = make_float2(0.0f, 0.0f);
+        k.bound = fmaxf(k.bound, fabsf(sz[g].x) * fmaxf(fabsf(sz[g].y), fabsf(15.0f - sz[g].y)));
+        f += 0.0f * sz[g].x + 0.0f * sz[g].y;
+    }
+    k.finite = f == 0.0f;
+    return k;
 }
 
 template <int NW>
@@ -522,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
     }
     if (threadIdx.x == 0) {
         for (int s = 0; s < W::kSlots; ++s) {
-            mbar_init(&bar.k_full[s], W::kDqWarps);
+            mbar_init(&bar.k_full[s], W::kDqWarps + 2);   // and the tables'
             mbar_init(&bar.k_empty[s], 1);
             mbar_init(&bar.v_full[s], W::kDqWarps);
             mbar_init(&bar.v_empty[s], 1);
@@ -541,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         mbar_init(bar.drain + 1, 1);
         for (int s = 0; s < W::kRaw; ++s) {
             mbar_init(&bar.raw_full[s], 64);       // every copying thread's copies
-            mbar_init(&bar.raw_empty[s], W::kDqWarps);
+            mbar_init(&bar.raw_empty[s], W::kDqWarps + 2);
         }
         s_abort = 0;
         s_big = 0;
@@ -655,17 +703,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             // held times 2^e, so that 2^kSlack of it is below 2^15
             float vb = 0.0f;
 #pragma unroll
-            for (int x = 0; x < W::kDqWarps; x += 4) {
-                const float4 v = lds_f4(smem_s + M::offVm + (tab * 8 + x) * 4);
-                vb = fmaxf(vb, fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)));
-            }
+            for (int x = 0; x < 2; ++x) vb = fmaxf(vb, lds_f1(smem_s + M::offVm + (tab * 2 + x) * 4));
             const int ve = min(scale_exponent(vb), 80);
             const float e = (float)(EXACT ? ve - 2 : ve + kPieceBits);
             const int k0 = (tile_lo + i) * kTile;
             const bool masked = k0 + kTile - 1 > all_hi || k0 < all_lo;   // uniform
-            const uint32_t s_at = tmem + lanes + kColS + s * kTile;
-            const float z = masked ? tile_weights<EXACT, true>(s_at, key, qsum, e, r, last - k0, first - k0)
-                                   : tile_weights<EXACT, false>(s_at, key, qsum, e, r, 0, 0);
+            const TileOf w{tmem + lanes + kColS + s * kTile, key, pack2(qsum, qsum), e, last - k0, first - k0};
+            const float z = masked ? tile_weights<EXACT, true>(w, r) : tile_weights<EXACT, false>(w, r);
             // what the tile's P V is relative to
             ms[tab * kRows + row] = r.set ? r.ref - e : -INFINITY;
             if (EXACT) ms[(kTab + tab) * kRows + row] = z;
@@ -692,7 +736,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             const int s = i & 1, k = i >> 1;
             const int tab = i % kTab;
             // the row's reference comes with P
-            if (!warp_wait<true>(&bar.p_full[tab], (i / kTab) & 1, abort) || !warp_wait<true>(&bar.o_full[s], k & 1, abort)) {
+            if (!warp_wait(&bar.p_full[tab], (i / kTab) & 1, abort) || !warp_wait(&bar.o_full[s], k & 1, abort)) {
                 ok = false;
                 break;
             }
@@ -712,7 +756,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             for (int x = 0; x < C / 8; ++x) {
                 uint32_t t[8];
                 tmem_ld8(tmem + lanes + kColO + s * 128 + half * C + 8 * x, t);
-                tmem_wait_ld();
+                tmem_wait_for(t);
 #pragma unroll
                 for (int y = 0; y < 8; ++y) o[8 * x + y] = fmaf(__uint_as_float(t[y]), ft, o[8 * x + y]);
             }
@@ -720,7 +764,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.o_empty[s]);
         }
-        if (ok) ok = warp_wait<true>(bar.fin, 0, abort);
+        if (ok) ok = warp_wait(bar.fin, 0, abort);
         const int rho = row0 + row;
         if (rho < rows_all) {
             const int j = rho / R;
@@ -752,22 +796,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         // keys of one shared-memory phase meet eight distinct banks)
         constexpr int TN = W::kTurns, kStep = 8 * W::kDqWarps;   // keys between a lane's turns
         const int w = warp - W::kDq0, key0 = 8 * w + (lane & 7), c = lane >> 3;
-        const float Fq = ldexpf(a.scale * kLog2e, -kq);
         // this lane's words and its key's scales in a raw slot
         const uint32_t raw0 = smem_s + M::offRaw, raw_w = raw0 + key0 * 16 * J + c * 4 * J, raw_z = raw0 + 2 * M::kRawCodes + key0 * 8 * G;
-        // the largest |(code - z) s| that the row's scales allow
-        auto bound_of = [](const float2 (&sz)[G]) {
-            float m = 0.0f;
-#pragma unroll
-            for (int g = 0; g < G; ++g) m = fmaxf(m, fabsf(sz[g].x) * fmaxf(fabsf(sz[g].y), fabsf(15.0f - sz[g].y)));
-            return m;
-        };
-        auto finite_of = [](const float2 (&sz)[G]) {
-            float t = 0.0f;
-#pragma unroll
-            for (int g = 0; g < G; ++g) t += 0.0f * sz[g].x + 0.0f * sz[g].y;
-            return t == 0.0f;
-        };
         // block u of 32 values of key key0 + kStep y: 16-byte piece 4 u + c of
         // its row, swizzled by the key (the same for every turn)
         const uint32_t place0 = key0 * 128 + ((c ^ (key0 & 7)) << 4), place1 = place0 ^ 64u;
@@ -786,42 +816,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                        : u == 1 ? __byte_perm(vw[0], vw[2], 0x5432)
                                 : __byte_perm(vw[1], vw[2], 0x7610);
         };
+        const uint32_t bad_at = smem_s + M::offBad;
         int s = 0, phase = 1;              // slot of K and V, parity of the phase before
         for (int i = 0; i < n_tiles; ++i) {
-            const int rs = i % W::kRaw, tab = i % kTab;
+            const int rs = i % W::kRaw;
             const uint32_t raw = (uint32_t)rs * M::kRawSlot;
-            if (!warp_wait<true>(&bar.raw_full[rs], (i / W::kRaw) & 1, abort) ||
-                (i >= W::kSlots && !warp_wait<true>(&bar.k_empty[s], phase, abort))) {
+            if (!warp_wait(&bar.raw_full[rs], (i / W::kRaw) & 1, abort) ||
+                (i >= W::kSlots && !warp_wait(&bar.k_empty[s], phase, abort))) {
                 ok = false;
                 break;
             }
-            // ---- K, and the keys' tables (they have slots to spare: once the
-            // product of the tile kSlots back is done, the softmax of the one 8
-            // back is) ----
-            float vb = 0.0f;
-            float2 vs[TN][G];
-            float vup[TN];
+            // ---- K ----
 #pragma unroll
             for (int y = 0; y < TN; ++y) {
-                const int key = key0 + kStep * y, t = (tile_lo + i) * kTile + key;
-                const uint32_t zat = raw_z + raw + y * kStep * 8 * G;
-                const bool here = t <= see_hi && t >= see_lo;      // else what lies there counts for nothing
-                const bool bad = here && reinterpret_cast<const int *>(smem + M::offBad)[rs * 4 + (key >> 4)] != 0;
-                float2 ks[G];
-#pragma unroll
-                for (int g = 0; g < G; ++g) {
-                    ks[g] = lds_f2(zat + 8 * g);
-                    vs[y][g] = lds_f2(zat + M::kRawSz + 8 * g);
-                    if (!here || bad) ks[g] = vs[y][g] = make_float2(0.0f, 0.0f);
-                }
-                // a value that is not finite spoils the rows that see it through its key's factor
-                const bool spoilt = bad || !finite_of(vs[y]);
-                if (spoilt) {
-#pragma unroll
-                    for (int g = 0; g < G; ++g) vs[y][g] = make_float2(0.0f, 0.0f);
-                }
-                const float vk = EXACT ? fabsf(vs[y][0].x) : bound_of(vs[y]);
-                vb = fmaxf(vb, vk);
                 uint32_t kw[J];
                 lds_words<J>(raw_w + raw + y * kStep * 16 * J, kw);
                 const uint32_t base = smem_s + M::offK + s * M::kSlot;
@@ -831,17 +838,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                         const uint4 e = exact_word(kw[u]);
                         store16(place(base, u, y), e.x, e.y, e.z, e.w);
                     }
-                    if (c == 0) {
-                        const float F = spoilt ? quiet_nan() : Fq * ks[0].x;
-                        float2 *at = reinterpret_cast<float2 *>(smem + M::offF) + tab * 2 * kTile + key;
-                        at[0] = make_float2(F, (8.0f - ks[0].y) * F);
-                        at[kTile] = make_float2(vs[y][0].x, vs[y][0].y - 8.0f);
-                    }
                 } else {
-                    const float kb = bound_of(ks);
-                    const int kk = kb < INFINITY ? scale_exponent(kb) : 0, vv = min(scale_exponent(vk), 80);
-                    const float up = pow2(kk);
-                    vup[y] = pow2(vv);
+                    float2 ks[G];
+                    const KeyOf<G> k = key_of<G>(see_lo, see_hi, (tile_lo + i) * kTile + key0 + kStep * y,
+                                                 raw_z + raw + y * kStep * 8 * G, bad_at + rs * 16 + ((key0 + kStep * y) >> 4) * 4, ks);
+                    const float up = pow2(k.exponent());
 #pragma unroll
                     for (int u = 0; u < J; ++u) {
                         uint32_t hi[4], lo[4];
@@ -850,21 +851,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                         store16(at, hi[0], hi[1], hi[2], hi[3]);
                         store16(at + M::kKV, lo[0], lo[1], lo[2], lo[3]);
                     }
-                    if (c == 0) {
-                        float *at = reinterpret_cast<float *>(smem + M::offF) + tab * 2 * kTile + key;
-                        at[0] = spoilt ? quiet_nan() : Fq * pow2(-kk);
-                        at[kTile] = pow2(-vv);
-                    }
                 }
             }
-#pragma unroll
-            for (int o = 4; o > 0; o >>= 1) vb = fmaxf(vb, __shfl_xor_sync(0xffffffffu, vb, o));
-            if (lane == 0) reinterpret_cast<float *>(smem + M::offVm)[tab * 8 + w] = vb;
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.k_full[s]);
             // ---- V ----
-            if (i >= W::kSlots && !warp_wait<true>(&bar.v_empty[s], phase, abort)) {
+            if (i >= W::kSlots && !warp_wait(&bar.v_empty[s], phase, abort)) {
                 ok = false;
                 break;
             }
@@ -873,6 +866,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                 const uint32_t base = smem_s + M::offV + s * M::kSlot;
                 uint32_t vw[J];
                 lds_words<J>(raw_w + raw + y * kStep * 16 * J + M::kRawCodes, vw);
+                float2 vs[G];
+                float up = 0.0f;
+                if constexpr (!EXACT) {
+                    const KeyOf<G> k = key_of<G>(see_lo, see_hi, (tile_lo + i) * kTile + key0 + kStep * y,
+                                                 raw_z + raw + y * kStep * 8 * G + M::kRawSz,
+                                                 bad_at + rs * 16 + ((key0 + kStep * y) >> 4) * 4, vs);
+                    // what is not finite is zero here: the key's factor spoils the rows that see it
+                    up = k.finite ? pow2(min(k.exponent(), 80)) : 0.0f;
+                    if (!k.finite) {
+#pragma unroll
+                        for (int g = 0; g < G; ++g) vs[g] = make_float2(0.0f, 0.0f);
+                    }
+                }
 #pragma unroll
                 for (int u = 0; u < J; ++u) {
                     const uint32_t word = value_word(vw, u), at = place(base, u, y);
@@ -881,7 +887,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                         store16(at, e.x, e.y, e.z, e.w);
                     } else {
                         uint32_t hi[4], lo[4];
-                        dequant_word(word, vs[y][u / UG].x * vup[y], vs[y][u / UG].y, hi, lo);
+                        dequant_word(word, vs[u / UG].x * up, vs[u / UG].y, hi, lo);
                         store16(at, hi[0], hi[1], hi[2], hi[3]);
                         store16(at + M::kKV, lo[0], lo[1], lo[2], lo[3]);
                     }
@@ -899,53 +905,104 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             }
         }
     } else if (warp < W::kMma) {
-        // ===== the cache into shared memory: 16 keys of a page are contiguous =====
+        // ===== the cache into shared memory: 16 keys of a page are contiguous,
+        // 16 threads' =====
         const int th = (int)threadIdx.x - 32 * W::kCopy;       // of 64
+        const int x16 = th >> 4, l16 = th & 15;
         const int shift = 31 - __clz(a.c.page_size);
         const int32_t *table = a.page_table + (size_t)b * a.max_pages;
         const size_t head_row = (size_t)h * a.c.page_size;
-        const char *k_at = reinterpret_cast<const char *>(a.c.Kq) + head_row * (16 * J) + 16 * th;
-        const char *v_at = reinterpret_cast<const char *>(a.c.Vq) + head_row * (16 * J) + 16 * th;
-        // scales and zeros of 16 keys: 8 G pieces of 16 bytes each side
-        const int side = th >= 8 * G, zp = th - side * 8 * G;
-        const char *z_at = reinterpret_cast<const char *>(side ? a.c.V_sz : a.c.K_sz) + head_row * (8 * G) + 16 * zp;
+        const char *k_at = reinterpret_cast<const char *>(a.c.Kq) + head_row * (16 * J) + 16 * l16;
+        const char *v_at = reinterpret_cast<const char *>(a.c.Vq) + head_row * (16 * J) + 16 * l16;
+        const char *ks_at = reinterpret_cast<const char *>(a.c.K_sz) + head_row * (8 * G);
+        const char *vs_at = reinterpret_cast<const char *>(a.c.V_sz) + head_row * (8 * G);
         const uint32_t page_rows = (uint32_t)(H * a.c.page_size), n_pages = (uint32_t)a.c.n_pages;
+        const uint32_t raw_at = smem_s + M::offRaw + x16 * 256 * J + 16 * l16;
         int *bad = reinterpret_cast<int *>(smem + M::offBad);
-        // the pages of a tile's four 16-key blocks; -2: nothing is seen there
-        auto pages_of = [&](int i, int (&pg)[4]) {
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const int t = (tile_lo + i) * kTile + 16 * x;
-                pg[x] = i < n_tiles && t <= see_hi && t + 16 > see_lo ? __ldg(table + (t >> shift)) : -2;
-            }
+        // the page of a tile's block of 16 keys; -2: nothing is seen there
+        auto page_of = [&](int i) {
+            const int t = (tile_lo + i) * kTile + 16 * x16;
+            return i < n_tiles && t <= see_hi && t + 16 > see_lo ? __ldg(table + (t >> shift)) : -2;
         };
-        int pg[4], next[4];
-        pages_of(0, pg);
-        for (int i = 0; i < n_tiles; ++i) {
-            const int rs = i % W::kRaw;
-            pages_of(i + 1, next);
-            if (i >= W::kRaw && !warp_wait<true>(&bar.raw_empty[rs], ((i / W::kRaw) - 1) & 1, abort)) {
-                ok = false;
-                break;
+        int page = page_of(0);
+        auto copy_tile = [&](int i) {
+            const int rs = i % W::kRaw, next = page_of(i + 1);
+            if (i >= W::kRaw && !warp_wait(&bar.raw_empty[rs], ((i / W::kRaw) - 1) & 1, abort)) return false;
+            const bool in = (uint32_t)page < n_pages, out = !in && page != -2;
+            if (l16 == 0) {
+                bad[rs * 4 + x16] = out;
+                if (out) atomicOr(&g_prompt_error, kAttnBadRequest);
             }
-            const uint32_t raw = smem_s + M::offRaw + (uint32_t)rs * M::kRawSlot;
+            if (in) {
+                const uint32_t at = (uint32_t)((tile_lo + i) * kTile + 16 * x16) & (uint32_t)(a.c.page_size - 1);
+                const size_t off = (size_t)(uint32_t)page * (page_rows * (16 * J)) + at * (16 * J);
+                const size_t zoff = (size_t)(uint32_t)page * (page_rows * (8 * G)) + at * (8 * G);
+                const uint32_t dst = raw_at + (uint32_t)rs * M::kRawSlot;
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const bool in = (uint32_t)pg[x] < n_pages, out = !in && pg[x] != -2;
-                if (th == x) {
-                    bad[rs * 4 + x] = out;
-                    if (out) atomicOr(&g_prompt_error, kAttnBadRequest);
+                for (int n = 0; n < J; ++n) {
+                    cp_async_16(dst + 256 * n, k_at + off + 256 * n);
+                    cp_async_16(dst + M::kRawCodes + 256 * n, v_at + off + 256 * n);
                 }
-                const size_t row = in ? (size_t)(uint32_t)pg[x] * page_rows + ((((tile_lo + i) * kTile) + 16 * x) & (a.c.page_size - 1)) : 0;
-                if (in && th < 16 * J) {
-                    cp_async_16(raw + x * 256 * J + 16 * th, k_at + row * (16 * J));
-                    cp_async_16(raw + M::kRawCodes + x * 256 * J + 16 * th, v_at + row * (16 * J));
+#pragma unroll
+                for (int n = 0; n < G; ++n) {              // 8 G pieces each side
+                    const int pc = l16 + 16 * n, side = pc >= 8 * G, zp = pc - side * 8 * G;
+                    cp_async_16(smem_s + M::offRaw + (uint32_t)rs * M::kRawSlot + 2 * M::kRawCodes + side * M::kRawSz +
+                                    x16 * 128 * G + 16 * zp,
+                                (side ? vs_at : ks_at) + zoff + 16 * zp);
                 }
-                if (in && th < 16 * G)
-                    cp_async_16(raw + 2 * M::kRawCodes + side * M::kRawSz + x * 128 * G + 16 * zp, z_at + row * (8 * G));
-                pg[x] = next[x];
             }
+            page = next;
             cp_async_mbar_arrive(&bar.raw_full[rs]);
+            return true;
+        };
+        // Tables of a tile's keys, a thread each.  They have slots to spare:
+        // once the product of the tile kSlots back is done, the softmax of the
+        // one 8 back is.
+        const float Fq = ldexpf(a.scale * kLog2e, -kq);
+        const uint32_t raw_z = smem_s + M::offRaw + 2 * M::kRawCodes + th * 8 * G;
+        int slot = 0, phase = 1;
+        auto tables = [&](int i) {
+            const int rs = i % W::kRaw, tab = i % kTab;
+            if (!warp_wait(&bar.raw_full[rs], (i / W::kRaw) & 1, abort) ||
+                (i >= W::kSlots && !warp_wait(&bar.k_empty[slot], phase, abort)))
+                return false;
+            const int t = (tile_lo + i) * kTile + th;
+            const uint32_t zat = raw_z + (uint32_t)rs * M::kRawSlot, bat = smem_s + M::offBad + rs * 16 + (th >> 4) * 4;
+            float2 ks[G], vs[G];
+            const KeyOf<G> k = key_of<G>(see_lo, see_hi, t, zat, bat, ks), v = key_of<G>(see_lo, see_hi, t, zat + M::kRawSz, bat, vs);
+            // a value that is not finite spoils the rows that see it through its key's factor
+            const bool spoilt = k.bad || !v.finite;
+            float *at = reinterpret_cast<float *>(smem + M::offF) + tab * (EXACT ? 4 : 2) * kTile + th;
+            float vb = spoilt ? 0.0f : v.bound;
+            if constexpr (EXACT) {
+                const float F = spoilt ? quiet_nan() : Fq * ks[0].x;
+                at[0] = F;
+                at[kTile] = (8.0f - ks[0].y) * F;
+                at[2 * kTile] = spoilt ? 0.0f : vs[0].x;
+                at[3 * kTile] = spoilt ? 0.0f : vs[0].y - 8.0f;
+                vb = spoilt ? 0.0f : fabsf(vs[0].x);
+            } else {
+                at[0] = spoilt ? quiet_nan() : Fq * pow2(-k.exponent());
+                at[kTile] = v.finite ? pow2(-min(v.exponent(), 80)) : 0.0f;
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) vb = fmaxf(vb, __shfl_xor_sync(0xffffffffu, vb, o));
+            if (lane == 0) reinterpret_cast<float *>(smem + M::offVm)[tab * 2 + (th >> 5)] = vb;
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&bar.k_full[slot]);
+                mbar_arrive(&bar.raw_empty[rs]);
+            }
+            if (++slot == W::kSlots) {
+                slot = 0;
+                phase ^= 1;
+            }
+            return true;
+        };
+        // copies run kRaw - 1 tiles ahead of the tables
+        for (int i = 0; ok && i < n_tiles + W::kRaw - 1; ++i) {
+            if (i < n_tiles) ok = copy_tile(i);
+            if (ok && i >= W::kRaw - 1) ok = tables(i - (W::kRaw - 1));
         }
         cp_async_commit();
         cp_async_wait<0>();
@@ -957,8 +1014,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         const uint32_t hi = (uint32_t)(q_d >> 32), q_lo = (uint32_t)q_d, k_lo = (uint32_t)k_d;
         int slot = 0, phase = 0;
         for (int i = 0; i < n_tiles; ++i) {
-            if (!poll_wait(&bar.k_full[slot], phase, abort) ||
-                (i >= kSP && !poll_wait(&bar.sp_empty[i % kSP], ((i / kSP) - 1) & 1, abort)))
+            if (!bar_wait(&bar.k_full[slot], phase, abort) ||
+                (i >= kSP && !bar_wait(&bar.sp_empty[i % kSP], ((i / kSP) - 1) & 1, abort)))
                 break;
             tc_fence_after_sync();
             const uint32_t kh = k_lo + (uint32_t)(slot * (M::kSlot / 16));
@@ -991,9 +1048,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         int slot = 0, phase = 0;
         for (int i = 0; i < n_tiles; ++i) {
             const int s = i & 1;
-            if (!poll_wait(&bar.v_full[slot], phase, abort) ||
-                (i >= 2 && !poll_wait(&bar.o_empty[s], ((i >> 1) - 1) & 1, abort)) ||
-                !poll_wait(&bar.p_full[i % kTab], (i / kTab) & 1, abort))
+            if (!bar_wait(&bar.v_full[slot], phase, abort) ||
+                (i >= 2 && !bar_wait(&bar.o_empty[s], ((i >> 1) - 1) & 1, abort)) ||
+                !bar_wait(&bar.p_full[i % kTab], (i / kTab) & 1, abort))
                 break;
             tc_fence_after_sync();
             const uint32_t vh = v_lo + (uint32_t)(slot * (M::kSlot / 16));

@@ -25,13 +25,6 @@ __device__ __forceinline__ float max_nan(float a, float b)
     return r;
 }
 
-__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b)
-{
-    f32x2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-
 // min and max over the L consecutive lanes of this lane's segment (segments
 // start at multiples of L, L <= 32).  A power of two: an xor butterfly that
 // leaves the result in every lane.  Otherwise a tree towards the segment's
