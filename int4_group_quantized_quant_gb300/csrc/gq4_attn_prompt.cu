@@ -24,9 +24,9 @@
 //
 // Warps: softmax (a thread per row; EXACT: two groups of 4 that take turns at
 // the tiles, each with its own maximum), 8 that add the tiles' P V (a row and
-// half of head_dim per thread), 2 that fetch the cache's codes, scales and
-// zeros into shared memory by cp.async, 4 or 8 that turn them into the K and V
-// operands, 2 of which a lane issues the MMAs of S and of P V (an MMA's
+// half of head_dim per thread), 1 that fetches the cache's codes, scales and
+// zeros into shared memory by cp.async, 1 that makes the factors of its keys
+// from them, 4 or 8 that turn the codes into the K and V operands, 2 of which a lane issues the MMAs of S and of P V (an MMA's
 // operands cost its thread as much time as the MMA takes).  Tensor memory (512
 // columns): S in four slots, whose columns P takes over 16 by 16 as S is read,
 // and the tile's O in two; K and V have three slots in shared memory (EXACT;
@@ -71,7 +71,7 @@ struct Form {
     static constexpr int kGroups = EXACT ? 2 : 1;               // softmax groups of 4 warps
     static constexpr int kCo0 = 4 * kGroups;                    // first warp that adds
     static constexpr int kDq0 = kCo0 + kCoWarps;                // first that reads the cache
-    static constexpr int kCopy = kWarps - 4;                    // two that fetch the cache
+    static constexpr int kCopy = kWarps - 4;                    // fetches the cache; the next warp makes the keys' tables
     static constexpr int kMma = kWarps - 2;                     // issues S; the next warp P V
     static constexpr int kDqWarps = kCopy - kDq0;               // 4 or 8
     static constexpr int kPieces = EXACT ? 1 : 2;
@@ -94,7 +94,7 @@ struct Mem {
     static constexpr int offM = offF + kTab * kTile * (EXACT ? 16 : 8);   // per row: reference, sum p s (z - 8) [2][slot][128]
     static constexpr int offL = offM + kTab * kRows * (EXACT ? 8 : 4);    // per row (reference, sum of weights) [group][128]
     static constexpr int offQs = offL + Form<EXACT>::kGroups * kRows * 8;      // Q's sums over 8 values [128][DP / 8] (EXACT)
-    static constexpr int offVm = offQs + (EXACT ? kRows * DP / 2 : 0);   // V's largest, by 32 keys [slot][2]
+    static constexpr int offVm = offQs + (EXACT ? kRows * DP / 2 : 0);   // V's largest [slot]
     static constexpr int offBad = offVm + kTab * 8;         // pages outside the pool, by 16 keys [raw slot][4]
     static constexpr int offBar = offBad + 64;
     static constexpr int kRawCodes = kTile * 16 * J, kRawSz = kTile * 8 * G;
@@ -570,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
     }
     if (threadIdx.x == 0) {
         for (int s = 0; s < W::kSlots; ++s) {
-            mbar_init(&bar.k_full[s], W::kDqWarps + 2);   // and the tables'
+            mbar_init(&bar.k_full[s], W::kDqWarps + 1);   // and the tables'
             mbar_init(&bar.k_empty[s], 1);
             mbar_init(&bar.v_full[s], W::kDqWarps);
             mbar_init(&bar.v_empty[s], 1);
@@ -588,8 +588,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         mbar_init(bar.drain, 1);
         mbar_init(bar.drain + 1, 1);
         for (int s = 0; s < W::kRaw; ++s) {
-            mbar_init(&bar.raw_full[s], 64);       // every copying thread's copies
-            mbar_init(&bar.raw_empty[s], W::kDqWarps + 2);
+            mbar_init(&bar.raw_full[s], 32);       // every copying thread's copies
+            mbar_init(&bar.raw_empty[s], W::kDqWarps + 1);
         }
         s_abort = 0;
         s_big = 0;
@@ -701,9 +701,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             const uint32_t key = smem_s + M::offF + tab * (EXACT ? 16 : 8) * kTile;
             // the tile's largest V (EXACT: its scale), as a power of two: P is
             // held times 2^e, so that 2^kSlack of it is below 2^15
-            float vb = 0.0f;
-#pragma unroll
-            for (int x = 0; x < 2; ++x) vb = fmaxf(vb, lds_f1(smem_s + M::offVm + (tab * 2 + x) * 4));
+            const float vb = lds_f1(smem_s + M::offVm + tab * 4);
             const int ve = min(scale_exponent(vb), 80);
             const float e = (float)(EXACT ? ve - 2 : ve + kPieceBits);
             const int k0 = (tile_lo + i) * kTile;
@@ -904,20 +902,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                 phase ^= 1;
             }
         }
-    } else if (warp < W::kMma) {
+    } else if (warp == W::kCopy) {
         // ===== the cache into shared memory: 16 keys of a page are contiguous,
-        // 16 threads' =====
-        const int th = (int)threadIdx.x - 32 * W::kCopy;       // of 64
-        const int x16 = th >> 4, l16 = th & 15;
+        // 8 lanes' =====
+        const int x16 = lane >> 3, l8 = lane & 7;
         const int shift = 31 - __clz(a.c.page_size);
         const int32_t *table = a.page_table + (size_t)b * a.max_pages;
         const size_t head_row = (size_t)h * a.c.page_size;
-        const char *k_at = reinterpret_cast<const char *>(a.c.Kq) + head_row * (16 * J) + 16 * l16;
-        const char *v_at = reinterpret_cast<const char *>(a.c.Vq) + head_row * (16 * J) + 16 * l16;
-        const char *ks_at = reinterpret_cast<const char *>(a.c.K_sz) + head_row * (8 * G);
-        const char *vs_at = reinterpret_cast<const char *>(a.c.V_sz) + head_row * (8 * G);
+        const char *k_at = reinterpret_cast<const char *>(a.c.Kq) + head_row * (16 * J) + 16 * l8;
+        const char *v_at = reinterpret_cast<const char *>(a.c.Vq) + head_row * (16 * J) + 16 * l8;
+        const char *ks_at = reinterpret_cast<const char *>(a.c.K_sz) + head_row * (8 * G) + 16 * l8;
+        const char *vs_at = reinterpret_cast<const char *>(a.c.V_sz) + head_row * (8 * G) + 16 * l8;
         const uint32_t page_rows = (uint32_t)(H * a.c.page_size), n_pages = (uint32_t)a.c.n_pages;
-        const uint32_t raw_at = smem_s + M::offRaw + x16 * 256 * J + 16 * l16;
+        const uint32_t raw_at = smem_s + M::offRaw + x16 * 256 * J + 16 * l8;
+        const uint32_t raw_z = smem_s + M::offRaw + 2 * M::kRawCodes + x16 * 128 * G + 16 * l8;
         int *bad = reinterpret_cast<int *>(smem + M::offBad);
         // the page of a tile's block of 16 keys; -2: nothing is seen there
         auto page_of = [&](int i) {
@@ -925,11 +923,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             return i < n_tiles && t <= see_hi && t + 16 > see_lo ? __ldg(table + (t >> shift)) : -2;
         };
         int page = page_of(0);
-        auto copy_tile = [&](int i) {
+        for (int i = 0; i < n_tiles; ++i) {
             const int rs = i % W::kRaw, next = page_of(i + 1);
-            if (i >= W::kRaw && !warp_wait(&bar.raw_empty[rs], ((i / W::kRaw) - 1) & 1, abort)) return false;
+            if (i >= W::kRaw && !warp_wait(&bar.raw_empty[rs], ((i / W::kRaw) - 1) & 1, abort)) {
+                ok = false;
+                break;
+            }
             const bool in = (uint32_t)page < n_pages, out = !in && page != -2;
-            if (l16 == 0) {
+            if (l8 == 0) {
                 bad[rs * 4 + x16] = out;
                 if (out) atomicOr(&g_prompt_error, kAttnBadRequest);
             }
@@ -937,57 +938,64 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                 const uint32_t at = (uint32_t)((tile_lo + i) * kTile + 16 * x16) & (uint32_t)(a.c.page_size - 1);
                 const size_t off = (size_t)(uint32_t)page * (page_rows * (16 * J)) + at * (16 * J);
                 const size_t zoff = (size_t)(uint32_t)page * (page_rows * (8 * G)) + at * (8 * G);
-                const uint32_t dst = raw_at + (uint32_t)rs * M::kRawSlot;
+                const uint32_t dst = raw_at + (uint32_t)rs * M::kRawSlot, zdst = raw_z + (uint32_t)rs * M::kRawSlot;
 #pragma unroll
-                for (int n = 0; n < J; ++n) {
-                    cp_async_16(dst + 256 * n, k_at + off + 256 * n);
-                    cp_async_16(dst + M::kRawCodes + 256 * n, v_at + off + 256 * n);
+                for (int n = 0; n < 2 * J; ++n) {
+                    cp_async_16(dst + 128 * n, k_at + off + 128 * n);
+                    cp_async_16(dst + M::kRawCodes + 128 * n, v_at + off + 128 * n);
                 }
 #pragma unroll
-                for (int n = 0; n < G; ++n) {              // 8 G pieces each side
-                    const int pc = l16 + 16 * n, side = pc >= 8 * G, zp = pc - side * 8 * G;
-                    cp_async_16(smem_s + M::offRaw + (uint32_t)rs * M::kRawSlot + 2 * M::kRawCodes + side * M::kRawSz +
-                                    x16 * 128 * G + 16 * zp,
-                                (side ? vs_at : ks_at) + zoff + 16 * zp);
+                for (int n = 0; n < G; ++n) {
+                    cp_async_16(zdst + 128 * n, ks_at + zoff + 128 * n);
+                    cp_async_16(zdst + M::kRawSz + 128 * n, vs_at + zoff + 128 * n);
                 }
             }
             page = next;
             cp_async_mbar_arrive(&bar.raw_full[rs]);
-            return true;
-        };
-        // Tables of a tile's keys, a thread each.  They have slots to spare:
+        }
+        cp_async_commit();
+        cp_async_wait<0>();
+    } else if (warp < W::kMma) {
+        // ===== tables of a tile's keys, two a lane.  They have slots to spare:
         // once the product of the tile kSlots back is done, the softmax of the
-        // one 8 back is.
+        // one 8 back is =====
         const float Fq = ldexpf(a.scale * kLog2e, -kq);
-        const uint32_t raw_z = smem_s + M::offRaw + 2 * M::kRawCodes + th * 8 * G;
         int slot = 0, phase = 1;
-        auto tables = [&](int i) {
+        for (int i = 0; i < n_tiles; ++i) {
             const int rs = i % W::kRaw, tab = i % kTab;
             if (!warp_wait(&bar.raw_full[rs], (i / W::kRaw) & 1, abort) ||
-                (i >= W::kSlots && !warp_wait(&bar.k_empty[slot], phase, abort)))
-                return false;
-            const int t = (tile_lo + i) * kTile + th;
-            const uint32_t zat = raw_z + (uint32_t)rs * M::kRawSlot, bat = smem_s + M::offBad + rs * 16 + (th >> 4) * 4;
-            float2 ks[G], vs[G];
-            const KeyOf<G> k = key_of<G>(see_lo, see_hi, t, zat, bat, ks), v = key_of<G>(see_lo, see_hi, t, zat + M::kRawSz, bat, vs);
-            // a value that is not finite spoils the rows that see it through its key's factor
-            const bool spoilt = k.bad || !v.finite;
-            float *at = reinterpret_cast<float *>(smem + M::offF) + tab * (EXACT ? 4 : 2) * kTile + th;
-            float vb = spoilt ? 0.0f : v.bound;
-            if constexpr (EXACT) {
-                const float F = spoilt ? quiet_nan() : Fq * ks[0].x;
-                at[0] = F;
-                at[kTile] = (8.0f - ks[0].y) * F;
-                at[2 * kTile] = spoilt ? 0.0f : vs[0].x;
-                at[3 * kTile] = spoilt ? 0.0f : vs[0].y - 8.0f;
-                vb = spoilt ? 0.0f : fabsf(vs[0].x);
-            } else {
-                at[0] = spoilt ? quiet_nan() : Fq * pow2(-k.exponent());
-                at[kTile] = v.finite ? pow2(-min(v.exponent(), 80)) : 0.0f;
+                (i >= W::kSlots && !warp_wait(&bar.k_empty[slot], phase, abort))) {
+                ok = false;
+                break;
             }
+            float vb = 0.0f;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) vb = fmaxf(vb, __shfl_xor_sync(0xffffffffu, vb, o));
-            if (lane == 0) reinterpret_cast<float *>(smem + M::offVm)[tab * 2 + (th >> 5)] = vb;
+            for (int y = 0; y < 2; ++y) {
+                const int key = lane + 32 * y, t = (tile_lo + i) * kTile + key;
+                const uint32_t zat = smem_s + M::offRaw + 2 * M::kRawCodes + (uint32_t)rs * M::kRawSlot + key * 8 * G;
+                const uint32_t bat = smem_s + M::offBad + rs * 16 + (key >> 4) * 4;
+                float2 ks[G], vs[G];
+                const KeyOf<G> k = key_of<G>(see_lo, see_hi, t, zat, bat, ks),
+                               v = key_of<G>(see_lo, see_hi, t, zat + M::kRawSz, bat, vs);
+                // a value that is not finite spoils the rows that see it through its key's factor
+                const bool spoilt = k.bad || !v.finite;
+                float *at = reinterpret_cast<float *>(smem + M::offF) + tab * (EXACT ? 4 : 2) * kTile + key;
+                if constexpr (EXACT) {
+                    const float F = spoilt ? quiet_nan() : Fq * ks[0].x;
+                    at[0] = F;
+                    at[kTile] = (8.0f - ks[0].y) * F;
+                    at[2 * kTile] = spoilt ? 0.0f : vs[0].x;
+                    at[3 * kTile] = spoilt ? 0.0f : vs[0].y - 8.0f;
+                    if (!spoilt) vb = fmaxf(vb, fabsf(vs[0].x));
+                } else {
+                    at[0] = spoilt ? quiet_nan() : Fq * pow2(-k.exponent());
+                    at[kTile] = v.finite ? pow2(-min(v.exponent(), 80)) : 0.0f;
+                    if (!spoilt) vb = fmaxf(vb, v.bound);
+                }
+            }
+            // (numbers of one sign order as their bits do)
+            const unsigned int top = __reduce_max_sync(0xffffffffu, __float_as_uint(vb));
+            if (lane == 0) reinterpret_cast<unsigned int *>(smem + M::offVm)[tab] = top;
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(&bar.k_full[slot]);
@@ -997,15 +1005,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                 slot = 0;
                 phase ^= 1;
             }
-            return true;
-        };
-        // copies run kRaw - 1 tiles ahead of the tables
-        for (int i = 0; ok && i < n_tiles + W::kRaw - 1; ++i) {
-            if (i < n_tiles) ok = copy_tile(i);
-            if (ok && i >= W::kRaw - 1) ok = tables(i - (W::kRaw - 1));
         }
-        cp_async_commit();
-        cp_async_wait<0>();
     } else if (lane == 0 && warp == W::kMma) {
         // ===== S = Q K^T: one lane issues =====
         constexpr uint32_t id_s = idesc_f16_f32(kRows, kTile, false);
