@@ -528,7 +528,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             return prompt_takes(a, r) ? (r.n * R + kRows - 1) / kRows : 0;
         };
         int all = 0, mine = 0, before = 0;
-        for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+        if (a.B == 1) all = mine = tiles_of(0);
+        else for (int b0 = 0; b0 < a.B; b0 += kThreads) {
             int t;
             mine = tiles_of(b0 + (int)threadIdx.x);
             before = scan_ints<kWarps>(mine, t, s_sums);
@@ -543,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                 mine = tiles_of(b0 + (int)threadIdx.x);
                 before = scan_ints<kWarps>(mine, t, s_sums);
             }
-            if (want >= base + before && want < base + before + mine) {
+            if (want >= base + before && want < base + before + mine && (a.B > 1 || threadIdx.x == 0)) {
                 s_req = b0 + (int)threadIdx.x;
                 s_tile = want - (base + before);
             }
@@ -616,64 +617,67 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
     const int tile_lo = see_lo / kTile;
     const int n_tiles = see_hi >= see_lo ? see_hi / kTile - tile_lo + 1 : 0;
 
-    // ---- Q: two fp16 pieces with one power of two for the CTA ----
-    {
-        auto row_at = [&](int r) {
-            const int rho = row0 + r, j = rho / R;
-            return a.q + (size_t)(rq.row0 + j) * a.ldq + (size_t)(h * R + rho - j * R) * D;
-        };
+    // ---- Q: two fp16 pieces with one power of two for the CTA; the copying
+    // warp is under way meanwhile ----
+    int kq = 0;
+    if (warp != W::kCopy) {
+        constexpr int kStaging = kThreads - 32, kTurns = (kRows * (DP / 8) + kStaging - 1) / kStaging;
+        const int th = (int)threadIdx.x - (warp > W::kCopy ? 32 : 0);
+        float4 q[kTurns][2];
         float big = 0.0f;
-        for (int i = threadIdx.x; i < kRows * (D / 8); i += kThreads) {
-            const int r = i / (D / 8), d8 = i - r * (D / 8);
-            if (row0 + r >= rows_all) continue;
-            const float4 *q = reinterpret_cast<const float4 *>(row_at(r) + 8 * d8);
-            const float4 x = __ldg(q), y = __ldg(q + 1);
-            const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
-            for (int n = 0; n < 8; ++n)   // an infinity is left to its own row
-                if (fabsf(v[n]) < INFINITY) big = fmaxf(big, fabsf(v[n]));
+        for (int n = 0; n < kTurns; ++n) {
+            const int i = th + n * kStaging, r = i / (DP / 8), d8 = i - r * (DP / 8);
+            q[n][0] = q[n][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (r < kRows && row0 + r < rows_all && 8 * d8 < D) {
+                const int rho = row0 + r, j = rho / R;
+                const float4 *at = reinterpret_cast<const float4 *>(a.q + (size_t)(rq.row0 + j) * a.ldq +
+                                                                   (size_t)(h * R + rho - j * R) * D + 8 * d8);
+                q[n][0] = __ldg(at);
+                q[n][1] = __ldg(at + 1);
+            }
         }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-        if (lane == 0) atomicMax(&s_big, __float_as_int(big));
-    }
-    __syncthreads();
-    const int kq = scale_exponent(__int_as_float(s_big));
-    {
-        const float up = pow2(kq);
-        for (int i = threadIdx.x; i < kRows * (DP / 8); i += kThreads) {
-            const int r = i / (DP / 8), d8 = i - r * (DP / 8);
-            uint32_t hi[4] = {0u, 0u, 0u, 0u}, lo[4] = {0u, 0u, 0u, 0u};
-            float part = 0.0f;
-            if (row0 + r < rows_all && 8 * d8 < D) {
-                const int rho = row0 + r, j = rho / R;
-                const float4 *q = reinterpret_cast<const float4 *>(a.q + (size_t)(rq.row0 + j) * a.ldq +
-                                                                  (size_t)(h * R + rho - j * R) * D + 8 * d8);
-                const float4 x = __ldg(q), y = __ldg(q + 1);
-                const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-                part = (((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]))) * up;
+        for (int n = 0; n < kTurns; ++n) {
+            const float v[8] = {q[n][0].x, q[n][0].y, q[n][0].z, q[n][0].w, q[n][1].x, q[n][1].y, q[n][1].z, q[n][1].w};
 #pragma unroll
-                for (int n = 0; n < 4; ++n)
-                    split_pair(v[EXACT ? exact_order(2 * n) : 2 * n] * up, v[EXACT ? exact_order(2 * n + 1) : 2 * n + 1] * up,
-                               hi[n], lo[n]);
-            }
+            for (int m = 0; m < 8; ++m)   // an infinity is left to its own row
+                if (fabsf(v[m]) < INFINITY) big = fmaxf(big, fabsf(v[m]));
+        }
+        const unsigned int top = __reduce_max_sync(0xffffffffu, __float_as_uint(big));
+        if (lane == 0) atomicMax(&s_big, (int)top);
+        asm volatile("bar.sync 1, %0;" ::"n"(kStaging) : "memory");
+        kq = scale_exponent(__int_as_float(s_big));
+        const float up = pow2(kq);
+#pragma unroll
+        for (int n = 0; n < kTurns; ++n) {
+            const int i = th + n * kStaging, r = i / (DP / 8), d8 = i - r * (DP / 8);
+            if (r >= kRows) break;
+            const float v[8] = {q[n][0].x, q[n][0].y, q[n][0].z, q[n][0].w, q[n][1].x, q[n][1].y, q[n][1].z, q[n][1].w};
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+                split_pair(v[EXACT ? exact_order(2 * m) : 2 * m] * up, v[EXACT ? exact_order(2 * m + 1) : 2 * m + 1] * up,
+                           hi[m], lo[m]);
             unsigned char *at = smem + M::offQ + (d8 >> 3) * (kRows * 128) + r * 128 + (((d8 & 7) ^ (r & 7)) << 4);
             *reinterpret_cast<uint4 *>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
             *reinterpret_cast<uint4 *>(at + M::kQ) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-            if (EXACT) reinterpret_cast<float *>(smem + M::offQs)[r * (DP / 8) + d8] = part;
+            if (EXACT)
+                reinterpret_cast<float *>(smem + M::offQs)[r * (DP / 8) + d8] =
+                    (((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]))) * up;
         }
         // the padding of a 96-value head: zeros in every K and V slot, once
         if constexpr (DP > D) {
             constexpr int per = kTile * (DP - D) / 8;      // 16-byte pieces of one piece's padding
-            for (int i = threadIdx.x; i < 2 * W::kSlots * W::kPieces * per; i += kThreads) {   // K's and V's pieces lie on end
+            for (int i = th; i < 2 * W::kSlots * W::kPieces * per; i += kStaging) {   // K's and V's pieces lie on end
                 const int t = i / per, k = (i - t * per) / ((DP - D) / 8), d8 = D / 8 + (i - t * per) % ((DP - D) / 8);
                 *reinterpret_cast<uint4 *>(smem + M::offK + t * M::kKV + (d8 >> 3) * (kTile * 128) + k * 128 +
                                            (((d8 & 7) ^ (k & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
             }
         }
         fence_proxy_async_smem();
+        asm volatile("bar.sync 1, %0;" ::"n"(kStaging) : "memory");
     }
-    __syncthreads();
 
     bool ok = true;
     if (warp < W::kCo0) {
