@@ -518,9 +518,11 @@ GQ4_API gq4_status gq4_kv_plan(int B, int T, int page_size, int max_pages, int n
  * sets device error bit 8: rows of its queries inside T are NaN (with a bad
  * page: those that see it), nothing outside the pool or T is touched.
  *
- * Held to |error| <= about 1e-6 of the values' size: q and the weights are
- * split into two fp16 pieces each (22 bits), the codes are exact, sums are
- * f32 (prompts: the dequantised keys and values are two fp16 pieces too).
+ * Held to |error| of about 1e-6 of the values' size: queries and weights are
+ * two fp16 pieces each (22 bits; for requests of few rows a query row is
+ * fixed-point with a power-of-two scale, each value within 2^-22 of the
+ * row's largest magnitude), the codes are exact, sums are f32 (requests of
+ * many rows and several groups: the keys and values are two pieces too).
  * How a request's keys are split over the GPU depends on the other requests
  * and on max_len, so their change may change last bits; the same inputs give
  * the same bits.

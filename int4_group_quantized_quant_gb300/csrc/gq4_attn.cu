@@ -6,21 +6,25 @@
 //   w_t = scale * sum_g s_tg (sum_{d in g} q_d c_td - z_tg sum_{d in g} q_d)
 //   out = sum_t p_t s_tg (c_td - 8) - sum_t p_t s_tg (z_tg - 8),  p_t = 2^(w_t log2 e - m)
 // The codes c enter the warp-level MMA (m16n8k16, f16 inputs, f32 sums) as
-// exact fp16 numbers; the other factor -- q, or p s -- is written as a sum of
-// two fp16 pieces (11 bits each, 2^-23 relative), which take two neighbouring
-// columns of the instruction, so that one thread holds both sums.  The keys
-// (or, in the second product, the head's values of d) are the 16 rows of the
-// instruction and the query rows its 8 columns: 4 rows of two pieces each, a
-// full instruction for the four query heads of a kv head, and one decode of
-// a code serves all of them.
+// exact fp16 numbers; the other factor is written as two fp16 pieces, which
+// take two neighbouring columns of the instruction, so that one thread holds
+// both sums.  A query row is a 22-bit fixed-point number 2048 h + l (whole
+// numbers, a power of two per row), so that every sum of the first product is
+// exact: the tensor core cuts what it cannot hold.  The weights p s are
+// xh + xl, 11 bits each (2^-23 relative): a small weight keeps its digits.
+// The keys (or, in the second product, the head's values of d) are the 16 rows
+// of the instruction and the query rows its 8 columns: 4 rows of two pieces
+// each, a full instruction for the four query heads of a kv head, and one
+// decode of a code serves all of them.
 //   Keys: a word's nibbles i and i+4 are masked in place, an fp16 pair
 // c 2^-24 (c 2^-20 for odd i: q is pre-scaled by 1/16 there).
 //   Values: nibbles of two tokens are paired by a byte permute, OR-ed with
 // 1024 and shifted to c - 8 by one exact fp16 operation.  Without the 8 the
 // sums would carry the codes' mean, several times the result, and its
 // rounding.
-//   Sums in the tensor core are cut, not rounded: the second product runs
-// over 32 keys and is then added to the f32 accumulators.
+//   The second product stays in the tensor core for 4 stages (128 keys of a
+// warp) and is then added to f32 sums: cut sums of a whole context would be
+// off by 2.6e-6 at 131072 keys instead of 1.1e-6.
 //   The running maximum m moves only when a weight passes 2^4 of it (a vote
 // per 32 keys), so that accumulators are rescaled rarely; the values'
 // scales likewise share a power of two 2^E, which keeps p s inside fp16.
@@ -54,6 +58,7 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kStageKeys = 32;                    // per warp
 constexpr int kStepKeys = kStageKeys * kWarps;    // per CTA
 constexpr float kSlack = 4.0f;                    // log2 of how far a weight may pass the maximum
+constexpr float kRadix = 2048.0f;                 // a query is 2048 h + l, whole numbers
 constexpr int kPieceBits = 11;                    // p s <= 2^kSlack is held times 2^11: below 2^15
 constexpr int kCarry = 4;                         // stages summed in the tensor core
 constexpr int kMaxGrid = 512;                    // CTAs (the workspace's slots)
@@ -489,9 +494,9 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
                 for (int i = 0; i < 8; ++i) big = fmaxf(big, fabsf(x[u][i]));
             big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
             big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-            // 2^k times the row lies in [2^13, 2^14) at its largest
+            // 2^k times the row lies in [2^21, 2^22) at its largest
             const int e = (int)((__float_as_uint(big) >> 23) & 255u);
-            const int k = big > 0.0f ? min(13 + 127 - e, 120) : 0;
+            const int k = big > 0.0f ? min(21 + 127 - e, 120) : 0;
             const float up = exp2f((float)k);
             float sum[G];
 #pragma unroll
@@ -505,11 +510,11 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
                     float z[2];
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
-                        const float v = x[u][i + 4 * y] * up;
-                        const float hi = __half2float(__float2half_rn(v));
+                        const float v = rintf(x[u][i + 4 * y] * up);
+                        const float hi = rintf(v * (1.0f / kRadix));
                         sum[u / UG] += v;
                         // odd nibbles are masked at 16 times their value
-                        z[y] = (lo ? v - hi : hi) * ((i & 1) ? 0.0625f : 1.0f);
+                        z[y] = (lo ? fmaf(-kRadix, hi, v) : hi) * ((i & 1) ? 0.0625f : 1.0f);
                     }
                     const __half2 pr = __floats2half2_rn(z[0], z[1]);
                     f[i] = *reinterpret_cast<const uint32_t *>(&pr);
@@ -607,8 +612,8 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
                             const float2 sb = lds_f2(st + sof + ((16 * x + 8) * G + gr) * 8);
 #pragma unroll
                             for (int nb = 0; nb < NB; ++nb) {
-                                const float ta = fmaf(-sa.y, qs[nb][gr], acc[x][nb][0] + acc[x][nb][1]);
-                                const float tb = fmaf(-sb.y, qs[nb][gr], acc[x][nb][2] + acc[x][nb][3]);
+                                const float ta = fmaf(-sa.y, qs[nb][gr], fmaf(kRadix, acc[x][nb][0], acc[x][nb][1]));
+                                const float tb = fmaf(-sb.y, qs[nb][gr], fmaf(kRadix, acc[x][nb][2], acc[x][nb][3]));
                                 w[x][0][nb] = gr == 0 ? sa.x * ta : fmaf(sa.x, ta, w[x][0][nb]);
                                 w[x][1][nb] = gr == 0 ? sb.x * tb : fmaf(sb.x, tb, w[x][1][nb]);
                             }
