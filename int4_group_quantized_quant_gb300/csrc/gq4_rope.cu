@@ -4,14 +4,19 @@
 //   y = x / sqrt(mean(x^2) + eps) * gain,  (y_a, y_b) -> rotation by
 //   positions[t] * inv_freq[i].
 //
-// Bound by HBM: 8 bytes per element.  A CTA takes one token and a share of
-// its heads: its threads first form the token's rot/2 sines and cosines in
-// shared memory (each once for all heads of the CTA; the loads of the rows
-// are already in flight), then a row is handled by the smallest power of two
-// of lanes that holds it in float4s (16 lanes at 64 dims, 32 at 128, 32
-// lanes with 2 or 4 float4 each above).  A half-split pair's partner is
-// loaded a second time (a first-level cache hit) rather than shuffled, as
-// rot/2 may fall anywhere.
+// Bound by HBM: 8 bytes per element, and a float4 in and out per lane.  A
+// CTA takes one token and a share of its heads: its threads load their first
+// row, form the token's rot/2 sines and cosines in shared memory meanwhile
+// (each once for all heads of the CTA), then handle a row with the smallest
+// power of two of lanes that holds it in float4s (16 lanes at 64 dims, 32 at
+// 128, 32 lanes with 2 or 4 float4 each above).  Half-split pairs are
+// exchanged by shuffles within 32 lanes; above 128 dims the partner lies in
+// another register of another lane and is loaded a second time (a
+// first-level cache hit).
+//   8191 tokens of 40 heads of 128: 63 us, 335 MB at 5.3 TB/s (0.78 of a
+// copy's).  Occupancy is what counts: one row per thread under way, 8 CTAs
+// on an SM; two rows under way take 72 us, four 82 us, and without sines and
+// cosines it still takes 62 us.
 //
 // Angles: pos * inv_freq is a 31-bit by 24-bit product; in binary64 its error
 // is below 2^-22 of a radian at any position.  It is reduced modulo 2 pi in
@@ -44,32 +49,26 @@ __device__ __forceinline__ float2 sin_cos_of(int pos, float inv_freq)
     return make_float2(s, c);
 }
 
-// A lane's share of one row: its float4s and, half-split, their partners'.
+// A lane's share of one row: its float4s and, half-split above 128 dims,
+// their partners'.
 template <int CH>
 struct Row {
     float4 v[CH], w[CH];
-    float4 *y;
-    int side;    // -1: no row
 };
 
 template <int CH>
-__device__ __forceinline__ Row<CH> load_row(const RopeCall &c, int t, int row, int rows, int l)
+__device__ __forceinline__ Row<CH> load_row(const RopeCall &c, const float *row, bool live, int l)
 {
-    Row<CH> x;
-    const bool live = row < rows;
-    const int s = live && row >= c.heads[0] ? 1 : 0;
-    const int h = s ? row - c.heads[0] : row;
-    x.side = live ? s : -1;
-    x.y = reinterpret_cast<float4 *>(c.y[s] + (size_t)t * c.ldy[s] + (size_t)h * c.D);
-    const float4 *in = reinterpret_cast<const float4 *>(c.x[s] + (size_t)t * c.ldx[s] + (size_t)h * c.D);
+    const float4 *in = reinterpret_cast<const float4 *>(row);
     const int d4 = c.D >> 2, rot4 = c.rot >> 2, half4 = c.rot >> 3;
+    Row<CH> x;
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
         const int i = l + j * 32;
         x.v[j] = x.w[j] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (live && i < d4) {
             x.v[j] = in[i];
-            if (!c.interleaved && i < rot4) x.w[j] = in[i < half4 ? i + half4 : i - half4];
+            if (CH > 1 && !c.interleaved && i < rot4) x.w[j] = in[i < half4 ? i + half4 : i - half4];
         }
     }
     return x;
@@ -84,34 +83,40 @@ __device__ __forceinline__ float4 scaled(float4 a, float r, float4 g)
 template <int CH>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p)
 {
-    __shared__ float2 sc[GQ4_MAX_HEAD_DIM / 2];
+    __shared__ alignas(16) float2 sc[GQ4_MAX_HEAD_DIM / 2];
     const RopeCall &c = p.c;
     const int t = blockIdx.x / p.splits, part = blockIdx.x - t * p.splits;
     const int half = c.rot >> 1;
     const int lpr = p.lpr, per = kRopeThreads / lpr;   // rows at once
     const int l = threadIdx.x & (lpr - 1);
-    const int stride = per * p.splits;
     const int d4 = c.D >> 2, rot4 = c.rot >> 2, half4 = c.rot >> 3;
-    int row = part * per + threadIdx.x / lpr;
-    Row<CH> next = load_row<CH>(c, t, row, p.rows, l);
-    if (half > 0) {
-        const int pos = __ldg(c.positions + t);
-        for (int i = threadIdx.x; i < half; i += kRopeThreads) sc[i] = sin_cos_of(pos, __ldg(c.inv_freq + i));
-    }
-    __syncthreads();
-    // every thread takes the same number of turns (the shuffles below); the
-    // next row is on its way while this one is worked on
-    for (int row0 = part * per; row0 < p.rows; row0 += stride) {
-        const Row<CH> x = next;
-        row += stride;
-        if (row0 + stride < p.rows) next = load_row<CH>(c, t, row, p.rows, l);
-        const float4 *gain = reinterpret_cast<const float4 *>(x.side < 0 ? nullptr : c.gain[x.side]);
+    bool first_rows = true;
+    // every thread takes the same number of turns (the shuffles below)
+    for (int row0 = part * per; row0 < p.rows; row0 += per * p.splits) {
+        const int row = row0 + threadIdx.x / lpr;
+        const int side = row >= p.rows ? -1 : row >= c.heads[0] ? 1 : 0;   // q, k or no row
+        const bool k = side == 1;
+        const size_t head = (size_t)(k ? row - c.heads[0] : row) * c.D;
+        const Row<CH> x = load_row<CH>(c, (k ? c.x[1] + (size_t)t * c.ldx[1] : c.x[0] + (size_t)t * c.ldx[0]) + head,
+                                       side >= 0, l);
+        if (first_rows) {
+            if (half > 0) {
+                const int pos = __ldg(c.positions + t);
+                for (int i = threadIdx.x; i < half; i += kRopeThreads) sc[i] = sin_cos_of(pos, __ldg(c.inv_freq + i));
+            }
+            __syncthreads();
+            first_rows = false;
+        }
+        const float4 *gain = reinterpret_cast<const float4 *>(k ? c.gain[1] : c.gain[0]);
+        float4 *y = reinterpret_cast<float4 *>((k ? c.y[1] + (size_t)t * c.ldy[1] : c.y[0] + (size_t)t * c.ldy[0]) + head);
         float r = 1.0f;
         if (c.gain[0] || c.gain[1]) {  // uniform: the whole warp shuffles
             float s = 0.0f;
 #pragma unroll
-            for (int j = 0; j < CH; ++j)
-                s += x.v[j].x * x.v[j].x + x.v[j].y * x.v[j].y + x.v[j].z * x.v[j].z + x.v[j].w * x.v[j].w;
+            for (int j = 0; j < CH; ++j) {
+                const float4 v = x.v[j];
+                s += v.x * v.x + v.y * v.y + v.z * v.z + v.w * v.w;
+            }
             for (int o = lpr >> 1; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
             r = 1.0f / sqrtf(s / (float)c.D + c.eps);
         }
@@ -119,24 +124,35 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
 #pragma unroll
         for (int j = 0; j < CH; ++j) {
             const int i = l + j * 32;
-            if (x.side < 0 || i >= d4) continue;
-            float4 a = gain ? scaled(x.v[j], r, __ldg(gain + i)) : x.v[j];
-            if (i < rot4) {
-                if (c.interleaved) {
-                    const float2 s0 = sc[2 * i], s1 = sc[2 * i + 1];
-                    a = make_float4(a.x * s0.y - a.y * s0.x, a.y * s0.y + a.x * s0.x,
-                                    a.z * s1.y - a.w * s1.x, a.w * s1.y + a.z * s1.x);
+            const bool live = side >= 0 && i < d4, turned = live && i < rot4;
+            float4 a = gain && live ? scaled(x.v[j], r, __ldg(gain + i)) : x.v[j];
+            if (c.interleaved) {
+                if (turned) {
+                    const float4 s = reinterpret_cast<const float4 *>(sc)[i];
+                    a = make_float4(a.x * s.y - a.y * s.x, a.y * s.y + a.x * s.x,
+                                    a.z * s.w - a.w * s.z, a.w * s.w + a.z * s.z);
+                }
+            } else {
+                const bool first = i < half4;
+                const int other = first ? i + half4 : i - half4;
+                float4 b;
+                if (CH == 1) {  // the whole warp shuffles
+                    b.x = __shfl_sync(0xffffffffu, a.x, other, lpr);
+                    b.y = __shfl_sync(0xffffffffu, a.y, other, lpr);
+                    b.z = __shfl_sync(0xffffffffu, a.z, other, lpr);
+                    b.w = __shfl_sync(0xffffffffu, a.w, other, lpr);
                 } else {
-                    const bool first = i < half4;
-                    const int other = first ? i + half4 : i - half4, f = 4 * (first ? i : other);
-                    const float4 b = gain ? scaled(x.w[j], r, __ldg(gain + other)) : x.w[j];
+                    b = gain && turned ? scaled(x.w[j], r, __ldg(gain + other)) : x.w[j];
+                }
+                if (turned) {
                     const float m = first ? -1.0f : 1.0f;
-                    const float2 s0 = sc[f], s1 = sc[f + 1], s2 = sc[f + 2], s3 = sc[f + 3];
-                    a = make_float4(a.x * s0.y + m * b.x * s0.x, a.y * s1.y + m * b.y * s1.x,
-                                    a.z * s2.y + m * b.z * s2.x, a.w * s3.y + m * b.w * s3.x);
+                    const float4 *s = reinterpret_cast<const float4 *>(sc + 4 * (first ? i : other));
+                    const float4 s0 = s[0], s1 = s[1];
+                    a = make_float4(a.x * s0.y + m * b.x * s0.x, a.y * s0.w + m * b.y * s0.z,
+                                    a.z * s1.y + m * b.z * s1.x, a.w * s1.w + m * b.w * s1.z);
                 }
             }
-            x.y[i] = a;
+            if (live) y[i] = a;
         }
     }
 }
