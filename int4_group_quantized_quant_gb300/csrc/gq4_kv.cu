@@ -13,6 +13,18 @@ namespace {
 __device__ unsigned int g_kv_error = 0;
 constexpr unsigned int kKvNonFinite = 1u << 3, kKvBadSlot = 1u << 6, kKvRefused = 1u << 7;
 
+// r / d for 0 <= r, r d < 2^31, by multiplying with ceil(2^31 / d): that is
+// too large by less than d, which adds less than r d / (2^31 d) < 1 / d.
+__device__ __forceinline__ int quotient(int r, uint32_t per_d)
+{
+    return (int)__umulhi(2u * (uint32_t)r, per_d);
+}
+
+uint32_t divide_by(int d)
+{
+    return (uint32_t)((0x80000000ull + (uint32_t)d - 1) / (uint32_t)d);
+}
+
 // ---------------------------------------------------------------------------
 // Writer.  A lane holds one word's 8 values, a row takes D/8 lanes; a warp
 // takes as many rows as fit, so that a group's minimum and maximum are a
@@ -31,6 +43,8 @@ struct AppendParams {
     int T, tokens;           // all, and per CTA
     int shift;               // log2 of the page size
     int L;                   // lanes per group
+    int total;               // slots of the pool
+    uint32_t per_2h;         // divides a CTA's rows by 2 heads
 };
 
 template <int J>
@@ -39,8 +53,8 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
     constexpr int WPR = 4 * J, RPW = 32 / WPR;   // words per row, rows per warp
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int in_warp = lane / WPR, w = lane - in_warp * WPR;
-    const int H = p.c.kv_heads, G = 32 * J / p.c.group_size;
-    const long long total = (long long)p.c.n_pages * p.c.page_size;
+    const int H = p.c.kv_heads, G = 8 * WPR / p.c.group_size;
+    const int group = w / p.L, pos = w - group * p.L;
     const int t0 = blockIdx.x * p.tokens;
     const int n_rows = min(p.tokens, p.T - t0) * 2 * H;
     constexpr int kStep = kAppendThreads / 32 * RPW;
@@ -55,12 +69,13 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
             va[u] = vb[u] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (in_warp < RPW && r < n_rows) {
                 // rows of a token: its K rows, then its V rows
-                const int t = r / (2 * H), sh = r - t * 2 * H;
-                const int side = sh >= H, h = side ? sh - H : sh;
+                const int t = quotient(r, p.per_2h), sh = r - t * 2 * H;
+                const bool side = sh >= H;
+                const int h = side ? sh - H : sh;
                 head[u] = 2 * h + side;
                 slot[u] = __ldg(p.slots + t0 + t);
                 const float4 *x = reinterpret_cast<const float4 *>(
-                    p.x[side] + (size_t)(t0 + t) * p.ld[side] + (size_t)h * (32 * J) + 8 * w);
+                    (side ? p.x[1] : p.x[0]) + (size_t)(t0 + t) * (side ? p.ld[1] : p.ld[0]) + h * (32 * J) + 8 * w);
                 va[u] = __ldcs(x);
                 vb[u] = __ldcs(x + 1);
             }
@@ -75,7 +90,6 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
                 lo = min_nan(lo, v[i]);
                 hi = max_nan(hi, v[i]);
             }
-            const int pos = w % p.L;
             segment_min_max(lo, hi, pos, lane - pos, p.L);
             int bad;
             const GroupMap m = group_map(lo, hi, bad);
@@ -85,7 +99,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
             // the first halves of both, the other the second
             const uint32_t other = __shfl_xor_sync(0xffffffffu, word, 4);
             if (slot[u] < 0) continue;
-            if (slot[u] >= total) {
+            if (slot[u] >= p.total) {
                 if (w == 0) atomicOr(&g_kv_error, kKvBadSlot);
                 continue;
             }
@@ -104,7 +118,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
             if (pos == 0) {
                 const float nan = __int_as_float(0x7fc00000);
                 float2 *sz = reinterpret_cast<float2 *>(side ? p.c.V_sz : p.c.K_sz);
-                sz[row * G + w / p.L] = bad ? make_float2(nan, nan) : make_float2(m.s, m.z);
+                sz[row * G + group] = bad ? make_float2(nan, nan) : make_float2(m.s, m.z);
                 if (bad) atomicOr(&g_kv_error, kKvNonFinite);
             }
         }
@@ -113,7 +127,8 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
 
 // ---------------------------------------------------------------------------
 // Reader: a lane dequantises 4 consecutive values (half a word), so that a
-// warp stores 512 contiguous bytes at a time.  Bound by HBM writes.
+// warp stores 512 contiguous bytes at a time; the same 4 of every row that it
+// takes.  Bound by HBM writes.
 // ---------------------------------------------------------------------------
 struct GatherParams {
     gq4_kv_cache c;
@@ -121,54 +136,66 @@ struct GatherParams {
     float4 *y[2];
     int T, tokens;           // all, and per CTA
     int shift;
+    int total;               // slots of the pool
+    uint32_t per_h;          // divides a CTA's rows by the heads
 };
 
 constexpr int kGatherUnroll = 4;
 
 template <int J>
-__global__ void __launch_bounds__(256) gather_kernel(const __grid_constant__ GatherParams p)
+constexpr int kGatherThreads = J == 3 ? 192 : 256;   // whole rows
+
+// The codes q & 15 and (q >> 4) & 15 as floats: exact, below 2^23 + 16.
+__device__ __forceinline__ float2 codes_of(uint32_t q)
 {
-    constexpr int F4 = 8 * J;   // float4s per row
+    return make_float2(__fsub_rn(__uint_as_float((q & 15u) | 0x4b000000u), 8388608.0f),
+                       __fsub_rn(__uint_as_float(((q >> 4) & 15u) | 0x4b000000u), 8388608.0f));
+}
+
+template <int J>
+__global__ void __launch_bounds__(kGatherThreads<J>) gather_kernel(const __grid_constant__ GatherParams p)
+{
+    constexpr int F4 = 8 * J, ROWS = kGatherThreads<J> / F4;   // float4s per row, rows at once
     const int H = p.c.kv_heads, G = 32 * J / p.c.group_size;
-    const long long total = (long long)p.c.n_pages * p.c.page_size;
     const int side = blockIdx.y;
-    const uint16_t *half = reinterpret_cast<const uint16_t *>(side ? p.c.Vq : p.c.Kq);
-    const float2 *sz = reinterpret_cast<const float2 *>(side ? p.c.V_sz : p.c.K_sz);
+    const int f = threadIdx.x % F4;
+    const uint16_t *half = reinterpret_cast<const uint16_t *>(side ? p.c.Vq : p.c.Kq) +
+                           (side ? v_half_index(f, J) : 2 * k_word_index(f >> 1, J) + (f & 1));
+    const float2 *sz = reinterpret_cast<const float2 *>(side ? p.c.V_sz : p.c.K_sz) + f * 4 / p.c.group_size;
     const int t0 = blockIdx.x * p.tokens;
-    const int n = min(p.tokens, p.T - t0) * H * F4;
-    float4 *y = p.y[side] + (size_t)t0 * H * F4;
-    for (int i0 = threadIdx.x; i0 < n; i0 += 256 * kGatherUnroll) {
+    const int n = min(p.tokens, p.T - t0) * H;
+    float4 *y = p.y[side] + (size_t)t0 * H * F4 + f;
+    for (int r0 = threadIdx.x / F4; r0 < n; r0 += ROWS * kGatherUnroll) {
         int slot[kGatherUnroll];
         uint32_t q[kGatherUnroll];
         float2 m[kGatherUnroll];
 #pragma unroll
         for (int u = 0; u < kGatherUnroll; ++u) {
-            const int i = i0 + u * 256;
-            slot[u] = i < n ? __ldg(p.slots + t0 + i / (H * F4)) : -1;
+            const int r = r0 + u * ROWS;
+            slot[u] = r < n ? __ldg(p.slots + t0 + quotient(r, p.per_h)) : -1;
         }
 #pragma unroll
         for (int u = 0; u < kGatherUnroll; ++u) {
-            const int i = i0 + u * 256, th = i / F4, f = i - th * F4;
-            if (slot[u] >= 0 && slot[u] < total) {
-                const size_t row = kv_row(p.c, slot[u] >> p.shift, th % H, slot[u] & (p.c.page_size - 1));
-                q[u] = half[row * F4 + (side ? v_half_index(f, J) : 2 * k_word_index(f >> 1, J) + (f & 1))];
-                m[u] = sz[row * G + f * 4 / p.c.group_size];
+            const int r = r0 + u * ROWS, h = r - quotient(r, p.per_h) * H;
+            if (slot[u] >= 0 && slot[u] < p.total) {
+                const size_t row = kv_row(p.c, slot[u] >> p.shift, h, slot[u] & (p.c.page_size - 1));
+                q[u] = half[row * F4];
+                m[u] = sz[row * G];
             }
         }
 #pragma unroll
         for (int u = 0; u < kGatherUnroll; ++u) {
-            const int i = i0 + u * 256;
+            float4 *to = y + (r0 + u * ROWS) * F4;
             if (slot[u] < 0) continue;
-            if (slot[u] >= total) {
+            if (slot[u] >= p.total) {
                 const float nan = __int_as_float(0x7fc00000);
-                y[i] = make_float4(nan, nan, nan, nan);
+                *to = make_float4(nan, nan, nan, nan);
                 atomicOr(&g_kv_error, kKvBadSlot);
                 continue;
             }
-            __stcs(y + i, make_float4(__fmul_rn(__fsub_rn((float)(q[u] & 15u), m[u].y), m[u].x),
-                                      __fmul_rn(__fsub_rn((float)((q[u] >> 4) & 15u), m[u].y), m[u].x),
-                                      __fmul_rn(__fsub_rn((float)((q[u] >> 8) & 15u), m[u].y), m[u].x),
-                                      __fmul_rn(__fsub_rn((float)((q[u] >> 12) & 15u), m[u].y), m[u].x)));
+            const float2 a = codes_of(q[u]), b = codes_of(q[u] >> 8);
+            __stcs(to, make_float4(__fmul_rn(__fsub_rn(a.x, m[u].y), m[u].x), __fmul_rn(__fsub_rn(a.y, m[u].y), m[u].x),
+                                   __fmul_rn(__fsub_rn(b.x, m[u].y), m[u].x), __fmul_rn(__fsub_rn(b.y, m[u].y), m[u].x)));
         }
     }
 }
@@ -327,10 +354,12 @@ cudaError_t launch_kv_append(int T, const gq4_kv_cache &c, const float *k, int l
     p.slots = slots;
     p.T = T;
     p.shift = log2_of(c.page_size);
+    p.total = c.n_pages * c.page_size;
+    p.per_2h = divide_by(2 * c.kv_heads);
     p.L = c.group_size / 8;
     // a lane takes two words of a long prompt; one while tokens are few, so
     // that they spread over the GPU
-    p.tokens = tokens_per_cta(2 * c.kv_heads * (c.head_dim / 8), T >= 1024 ? kAppendUnroll : 1);
+    p.tokens = tokens_per_cta(2 * c.kv_heads * (c.head_dim / 8), T >= 1024 ? 2 * kAppendUnroll : 1);
     const unsigned grid = (unsigned)((T + p.tokens - 1) / p.tokens);
     switch (c.head_dim) {
     case 64: append_kernel<2><<<grid, kAppendThreads, 0, stream>>>(p); break;
@@ -351,13 +380,15 @@ cudaError_t launch_kv_gather(int T, const gq4_kv_cache &c, const int32_t *slots,
     p.y[1] = reinterpret_cast<float4 *>(v_out);
     p.T = T;
     p.shift = log2_of(c.page_size);
-    p.tokens = tokens_per_cta(c.kv_heads * (c.head_dim / 4), T >= 1024 ? kGatherUnroll : 1);
+    p.total = c.n_pages * c.page_size;
+    p.per_h = divide_by(c.kv_heads);
+    p.tokens = tokens_per_cta(c.kv_heads * (c.head_dim / 4), T >= 1024 ? 2 * kGatherUnroll : 1);
     const dim3 grid((unsigned)((T + p.tokens - 1) / p.tokens), 2);
     switch (c.head_dim) {
-    case 64: gather_kernel<2><<<grid, 256, 0, stream>>>(p); break;
-    case 96: gather_kernel<3><<<grid, 256, 0, stream>>>(p); break;
-    case 128: gather_kernel<4><<<grid, 256, 0, stream>>>(p); break;
-    default: gather_kernel<8><<<grid, 256, 0, stream>>>(p); break;
+    case 64: gather_kernel<2><<<grid, kGatherThreads<2>, 0, stream>>>(p); break;
+    case 96: gather_kernel<3><<<grid, kGatherThreads<3>, 0, stream>>>(p); break;
+    case 128: gather_kernel<4><<<grid, kGatherThreads<4>, 0, stream>>>(p); break;
+    default: gather_kernel<8><<<grid, kGatherThreads<8>, 0, stream>>>(p); break;
     }
     return cudaGetLastError();
 }
