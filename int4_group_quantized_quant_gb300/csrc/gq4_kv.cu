@@ -25,12 +25,33 @@ uint32_t divide_by(int d)
     return (uint32_t)((0x80000000ull + (uint32_t)d - 1) / (uint32_t)d);
 }
 
+// Where a row of the pool lies, in 32-bit steps and one 64-bit sum: the pages
+// of all heads are fewer than 2^32 (each is 640 bytes or more).
+struct RowAt {
+    uint32_t page_head, at;
+
+    __device__ __forceinline__ RowAt(const gq4_kv_cache &c, int slot, int shift, int head)
+        : page_head((uint32_t)(slot >> shift) * (uint32_t)c.kv_heads + (uint32_t)head),
+          at((uint32_t)slot & (uint32_t)(c.page_size - 1))
+    {
+    }
+    // in an array of `bytes` per row, `page_bytes` per page and head
+    template <typename P>
+    __device__ __forceinline__ P *in(P *array, uint32_t page_bytes, uint32_t bytes) const
+    {
+        const char *base = reinterpret_cast<const char *>(array);
+        return reinterpret_cast<P *>(const_cast<char *>(base + (uint64_t)page_head * page_bytes + at * bytes));
+    }
+};
+
 // ---------------------------------------------------------------------------
 // Writer.  A lane holds one word's 8 values, a row takes D/8 lanes; a warp
 // takes as many rows as fit, so that a group's minimum and maximum are a
 // shuffle away.  The K and V rows of a few tokens are one CTA's, numbered in
-// 32 bits; a row's loads do not wait for its slot.  Bound by HBM: 4 bytes
-// read and 0.5 + 8/gs written per value.
+// 32 bits; a row's loads do not wait for its slot.  Floor: 4 bytes read and
+// 0.5 + 8/gs written per value; 16381 tokens of 8 heads of 128 take 35 us
+// (153 MB, 4.4 TB/s).  What is left is instructions: 225 per word and warp,
+// a fifth of them the group's two divisions and reciprocal.
 // ---------------------------------------------------------------------------
 constexpr int kAppendThreads = 256;
 constexpr int kAppendUnroll = 2;   // rows per lane whose loads are issued together
@@ -44,6 +65,7 @@ struct AppendParams {
     int shift;               // log2 of the page size
     int L;                   // lanes per group
     int total;               // slots of the pool
+    uint32_t page_codes, page_sz;   // bytes per page and head
     uint32_t per_2h;         // divides a CTA's rows by 2 heads
 };
 
@@ -103,22 +125,22 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
                 if (w == 0) atomicOr(&g_kv_error, kKvBadSlot);
                 continue;
             }
-            const size_t row = kv_row(p.c, slot[u] >> p.shift, h, slot[u] & (p.c.page_size - 1));
+            const RowAt row(p.c, slot[u], p.shift, h);
             if (side == 0) {
-                p.c.Kq[row * WPR + k_word_index(w, J)] = word;
+                row.in(p.c.Kq, p.page_codes, 4 * WPR)[k_word_index(w, J)] = word;
             } else if constexpr (J % 2 == 0) {
                 const int g = 2 * (w & 3), b = w >> 2;
                 const uint32_t both = (b & 1) ? __byte_perm(other, word, 0x7632) : __byte_perm(word, other, 0x5410);
-                p.c.Vq[row * WPR + (((g + (b & 1)) * J + (b & ~1)) >> 1)] = both;
+                row.in(p.c.Vq, p.page_codes, 4 * WPR)[((g + (b & 1)) * J + (b & ~1)) >> 1] = both;
             } else {
-                uint16_t *half = reinterpret_cast<uint16_t *>(p.c.Vq) + row * 2 * WPR;
+                uint16_t *half = reinterpret_cast<uint16_t *>(row.in(p.c.Vq, p.page_codes, 4 * WPR));
                 half[v_half_index(2 * w, J)] = (uint16_t)word;
                 half[v_half_index(2 * w + 1, J)] = (uint16_t)(word >> 16);
             }
             if (pos == 0) {
                 const float nan = __int_as_float(0x7fc00000);
                 float2 *sz = reinterpret_cast<float2 *>(side ? p.c.V_sz : p.c.K_sz);
-                sz[row * G + group] = bad ? make_float2(nan, nan) : make_float2(m.s, m.z);
+                row.in(sz, p.page_sz, 8 * G)[group] = bad ? make_float2(nan, nan) : make_float2(m.s, m.z);
                 if (bad) atomicOr(&g_kv_error, kKvNonFinite);
             }
         }
@@ -128,7 +150,8 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
 // ---------------------------------------------------------------------------
 // Reader: a lane dequantises 4 consecutive values (half a word), so that a
 // warp stores 512 contiguous bytes at a time; the same 4 of every row that it
-// takes.  Bound by HBM writes.
+// takes.  Bound by HBM writes: 16381 tokens of 8 heads of 128 take 22 us
+// (153 MB, 7.0 TB/s; the codes come from L2 when just written).
 // ---------------------------------------------------------------------------
 struct GatherParams {
     gq4_kv_cache c;
@@ -137,6 +160,7 @@ struct GatherParams {
     int T, tokens;           // all, and per CTA
     int shift;
     int total;               // slots of the pool
+    uint32_t page_codes, page_sz;   // bytes per page and head
     uint32_t per_h;          // divides a CTA's rows by the heads
 };
 
@@ -145,11 +169,11 @@ constexpr int kGatherUnroll = 4;
 template <int J>
 constexpr int kGatherThreads = J == 3 ? 192 : 256;   // whole rows
 
-// The codes q & 15 and (q >> 4) & 15 as floats: exact, below 2^23 + 16.
-__device__ __forceinline__ float2 codes_of(uint32_t q)
+// The codes q & 15 and (q >> 4) & 15 as floats: 2^23 + code, less 2^23.
+__device__ __forceinline__ f32x2 codes_of(uint32_t q)
 {
-    return make_float2(__fsub_rn(__uint_as_float((q & 15u) | 0x4b000000u), 8388608.0f),
-                       __fsub_rn(__uint_as_float(((q >> 4) & 15u) | 0x4b000000u), 8388608.0f));
+    return add2(pack2(__uint_as_float((q & 15u) | 0x4b000000u), __uint_as_float(((q >> 4) & 15u) | 0x4b000000u)),
+                pack2(-8388608.0f, -8388608.0f));
 }
 
 template <int J>
@@ -178,14 +202,14 @@ __global__ void __launch_bounds__(kGatherThreads<J>) gather_kernel(const __grid_
         for (int u = 0; u < kGatherUnroll; ++u) {
             const int r = r0 + u * ROWS, h = r - quotient(r, p.per_h) * H;
             if (slot[u] >= 0 && slot[u] < p.total) {
-                const size_t row = kv_row(p.c, slot[u] >> p.shift, h, slot[u] & (p.c.page_size - 1));
-                q[u] = half[row * F4];
-                m[u] = sz[row * G];
+                const RowAt row(p.c, slot[u], p.shift, h);
+                q[u] = *row.in(half, p.page_codes, 2 * F4);
+                m[u] = *row.in(sz, p.page_sz, 8 * G);
             }
         }
 #pragma unroll
         for (int u = 0; u < kGatherUnroll; ++u) {
-            float4 *to = y + (r0 + u * ROWS) * F4;
+            float4 *to = y + (uint32_t)(r0 + u * ROWS) * F4;
             if (slot[u] < 0) continue;
             if (slot[u] >= p.total) {
                 const float nan = __int_as_float(0x7fc00000);
@@ -193,9 +217,10 @@ __global__ void __launch_bounds__(kGatherThreads<J>) gather_kernel(const __grid_
                 atomicOr(&g_kv_error, kKvBadSlot);
                 continue;
             }
-            const float2 a = codes_of(q[u]), b = codes_of(q[u] >> 8);
-            __stcs(to, make_float4(__fmul_rn(__fsub_rn(a.x, m[u].y), m[u].x), __fmul_rn(__fsub_rn(a.y, m[u].y), m[u].x),
-                                   __fmul_rn(__fsub_rn(b.x, m[u].y), m[u].x), __fmul_rn(__fsub_rn(b.y, m[u].y), m[u].x)));
+            const f32x2 z = pack2(-m[u].y, -m[u].y), scale = pack2(m[u].x, m[u].x);
+            const float2 a = unpack2(mul2(add2(codes_of(q[u]), z), scale));
+            const float2 b = unpack2(mul2(add2(codes_of(q[u] >> 8), z), scale));
+            __stcs(to, make_float4(a.x, a.y, b.x, b.y));
         }
     }
 }
@@ -355,6 +380,8 @@ cudaError_t launch_kv_append(int T, const gq4_kv_cache &c, const float *k, int l
     p.T = T;
     p.shift = log2_of(c.page_size);
     p.total = c.n_pages * c.page_size;
+    p.page_codes = (uint32_t)(c.page_size * c.head_dim / 2);
+    p.page_sz = (uint32_t)(c.page_size * (c.head_dim / c.group_size) * 8);
     p.per_2h = divide_by(2 * c.kv_heads);
     p.L = c.group_size / 8;
     // a lane takes two words of a long prompt; one while tokens are few, so
@@ -381,6 +408,8 @@ cudaError_t launch_kv_gather(int T, const gq4_kv_cache &c, const int32_t *slots,
     p.T = T;
     p.shift = log2_of(c.page_size);
     p.total = c.n_pages * c.page_size;
+    p.page_codes = (uint32_t)(c.page_size * c.head_dim / 2);
+    p.page_sz = (uint32_t)(c.page_size * (c.head_dim / c.group_size) * 8);
     p.per_h = divide_by(c.kv_heads);
     p.tokens = tokens_per_cta(c.kv_heads * (c.head_dim / 4), T >= 1024 ? 2 * kGatherUnroll : 1);
     const dim3 grid((unsigned)((T + p.tokens - 1) / p.tokens), 2);
