@@ -388,7 +388,8 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
     // where this lane's first 16-byte piece of 16 rows goes (the next ones 512 bytes on)
     const uint32_t pof = (lane / J) * 16 * J + (((lane % J) ^ swizzle<J>(lane / J)) << 4);
     const int shift = 31 - __clz(a.c.page_size);
-    const uint32_t page_rows = (uint32_t)(H * a.c.page_size);   // below 2^18
+    // stretches of 16 rows (640 bytes or more each): a pool holds fewer than 2^32
+    const uint32_t page_stretches = (uint32_t)H * (uint32_t)(a.c.page_size >> 4), page_mask = a.c.page_size - 1;
     const uint32_t n_pages = (uint32_t)a.c.n_pages;
     while (pos < end) {
         const int upto = (int)min((long long)wk.steps, from + (end - pos));
@@ -424,12 +425,11 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
             if (i < iters && k0 <= see_hi && k0 + 32 > see_lo) {
                 const uint32_t st = ring + (uint32_t)slot * S::kBytes;
                 const bool ok[2] = {(uint32_t)pg.x < n_pages, (uint32_t)pg.y < n_pages};
-                const uint32_t at[2] = {(uint32_t)k0 & (a.c.page_size - 1), (uint32_t)(k0 + 16) & (a.c.page_size - 1)};
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {                  // 16 J pieces of 16 rows, contiguous
-                    if (!ok[x]) continue;
-                    const size_t off = (size_t)(uint32_t)(x ? pg.y : pg.x) * (page_rows * (D / 2)) + at[x] * (D / 2);
-                    const char *ks = k_at + off, *vp = v_at + off;
+                // the two stretches of 16 rows, in the order of the pool
+                const uint32_t at[2] = {(uint32_t)pg.x * page_stretches + (((uint32_t)k0 & page_mask) >> 4),
+                                        (uint32_t)pg.y * page_stretches + (((uint32_t)(k0 + 16) & page_mask) >> 4)};
+                auto codes = [&](int x) {                      // 16 J pieces, contiguous
+                    const char *ks = k_at + (uint64_t)at[x] * (8 * D), *vp = v_at + (uint64_t)at[x] * (8 * D);
 #pragma unroll
                     for (int j = 0; j < (16 * J + 31) / 32; ++j) {
                         uint32_t dst = st + x * 256 * J;
@@ -439,23 +439,34 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
                             cp_async_16(dst + S::kCodes, vp + 512 * j);
                         }
                     }
-                }
+                };
+                auto scales = [&](auto use) {                  // 16 G pieces each side
 #pragma unroll
-                for (int j = 0; j < G; ++j) {                  // scales and zeros: 16 G pieces each side
-                    const int piece = 32 * j + lane;
-                    const int side = piece >= 16 * G, pc = piece - side * 16 * G;
-                    const int x = pc >= 8 * G;
-                    const uint32_t dst = st + 2 * S::kCodes + piece * 16;
-                    if (x ? ok[1] : ok[0]) {
-                        const size_t off = (size_t)(uint32_t)(x ? pg.y : pg.x) * (page_rows * (8 * G)) +
-                                           ((x ? at[1] : at[0]) * (8 * G) + (pc - x * 8 * G) * 16);
-                        cp_async_16(dst, (side ? vs_at : ks_at) + off);
-                    } else if (x ? k0 + 16 <= see_hi && k0 + 32 > see_lo : k0 <= see_hi && k0 + 16 > see_lo) {
-                        // a page outside the pool: NaN rows
-                        const float nan = quiet_nan();
-                        asm volatile("st.shared.v4.f32 [%0], {%1,%1,%1,%1};" ::"r"(dst), "f"(nan) : "memory");
-                        atomicOr(&g_attn_error, kAttnBadRequest);
+                    for (int j = 0; j < G; ++j) {
+                        const int piece = 32 * j + lane;
+                        const int side = piece >= 16 * G, pc = piece - side * 16 * G;
+                        const int x = pc >= 8 * G;
+                        use(x, st + 2 * S::kCodes + piece * 16,
+                            (side ? vs_at : ks_at) + (uint64_t)(x ? at[1] : at[0]) * (128 * G) + (pc - x * 8 * G) * 16);
                     }
+                };
+                if (ok[0] && ok[1]) {                          // as nearly always: no more questions
+                    codes(0);
+                    codes(1);
+                    scales([](int, uint32_t dst, const char *src) { cp_async_16(dst, src); });
+                } else {
+                    if (ok[0]) codes(0);
+                    if (ok[1]) codes(1);
+                    scales([&](int x, uint32_t dst, const char *src) {
+                        if (x ? ok[1] : ok[0]) {
+                            cp_async_16(dst, src);
+                        } else if (x ? k0 + 16 <= see_hi && k0 + 32 > see_lo : k0 <= see_hi && k0 + 16 > see_lo) {
+                            // a page outside the pool: NaN rows
+                            const float nan = quiet_nan();
+                            asm volatile("st.shared.v4.f32 [%0], {%1,%1,%1,%1};" ::"r"(dst), "f"(nan) : "memory");
+                            atomicOr(&g_attn_error, kAttnBadRequest);
+                        }
+                    });
                 }
             }
             cp_async_commit();
@@ -743,7 +754,8 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
                     for (int x = 0; x < 2; ++x)
 #pragma unroll
                         for (int y = 0; y < 2; ++y) {
-                            const bool hid = masked && ((hidden >> ((x * 2 + y) * NB + nb)) & 1u);
+                            // (one row per thread: its hidden keys have scale 0 already)
+                            const bool hid = NB > 1 && masked && ((hidden >> ((x * 2 + y) * NB + nb)) & 1u);
                             const float ps = hid ? 0.0f : w[x][y][nb] * (vz[x][y][gr].x * vs);
                             zs[nb][gr] = hid ? zs[nb][gr] : fmaf(ps, vz[x][y][gr].y - 8.0f, zs[nb][gr]);
                             pf[nb][x][y] = transpose8x8(two_pieces(ps));
