@@ -56,16 +56,17 @@ __device__ unsigned int g_attn_error = 0;
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kStageKeys = 32;                    // per warp
-constexpr int kStepKeys = kStageKeys * kWarps;    // per CTA
 constexpr float kSlack = 4.0f;                    // log2 of how far a weight may pass the maximum
 constexpr float kRadix = 2048.0f;                 // a query is 2048 h + l, whole numbers
 constexpr int kPieceBits = 11;                    // p s <= 2^kSlack is held times 2^11: below 2^15
 constexpr int kCarry = 4;                         // stages summed in the tensor core
-constexpr int kMaxGrid = 512;                    // CTAs (the workspace's slots)
+constexpr int kWholeStages = 4;                   // units of so few stages are one warp's
+constexpr int kMaxGrid = 304;                     // CTAs (the workspace's slots)
 
 struct SplitParams {
     AttnCall a;
     float *part;        // [grid][2][rows][D + 2] partial sums
+    float *head;        // [grid][8 warps][rows][D + 2] a warp's first, cut unit
     int4 *desc;         // [grid] the cut unit that starts in this CTA
     int grid;
 };
@@ -225,7 +226,7 @@ __device__ __forceinline__ float2 lds_f2(uint32_t s)
 
 // A request's work: row blocks and key steps.
 struct Work {
-    int step0, steps;   // of kStepKeys keys
+    int step0, steps;   // stages of kStageKeys keys
     int blocks;         // row blocks of ROWS rows per kv head
     long long total;    // steps of all its units
 };
@@ -237,8 +238,8 @@ __device__ __forceinline__ Work work_of(const AttnCall &p, const AttnRequest &r)
     if (r.bad || r.n == 0 || r.len == 0 || prompt_takes(p, r)) return w;
     const int R = p.heads / p.c.kv_heads;
     const int first = attn_first(p, max(r.len - r.n, -1));
-    w.step0 = first / kStepKeys;
-    w.steps = (r.len + kStepKeys - 1) / kStepKeys - w.step0;
+    w.step0 = first / kStageKeys;
+    w.steps = (r.len + kStageKeys - 1) / kStageKeys - w.step0;
     w.blocks = (int)(((long long)r.n * R + ROWS - 1) / ROWS);
     w.total = (long long)w.blocks * p.c.kv_heads * w.steps;
     return w;
@@ -289,16 +290,30 @@ __device__ __forceinline__ void carry(float (&o)[NB][J][4], float (&t0)[NB][J][4
         }
 }
 
+// A warp's part of a cut unit: the position of the unit's first stage (-1:
+// none), and which it is.
+struct Segment {
+    long long start;
+    int b, unit, steps;      // request, unit of it, stages of the unit
+    int row0, rows;          // the request's first token and its query rows per kv head
+    int h, rb;               // kv head, row block
+};
+
 template <int J, int G, int NB, int STAGES, int MINB>
 __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid_constant__ SplitParams p)
 {
     constexpr int D = 32 * J, ROWS = 4 * NB, UG = J / G;   // UG: 32-value blocks per group
     using S = Stage<J, G>;
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ long long s_sums[kWarps];
-    __shared__ long long s_at;
-    __shared__ int s_b, s_special;
-    __shared__ float s_row[NB][4][G + 1];   // a query row's sums per group and its factor
+    constexpr int kSums = ROWS * (D + 2);   // floats of a unit's sums: [row][D], then m, l of each row
+    __shared__ union {
+        struct {
+            long long sums[kWarps];
+            long long pos[kWarps + 1], at[kWarps + 1];   // where warps start: of all stages, of request b's
+            int b[kWarps + 1], special;
+        } start;
+        Segment seg[2 * kWarps];            // a warp's first and last segment, where cut
+    } s;
     const AttnCall &a = p.a;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, c = lane & 3;
@@ -306,29 +321,31 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
 
     // ---- this CTA's range of steps ----
     if (threadIdx.x == 0) {
-        s_special = 0;
+        s.start.special = 0;
         p.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
     }
     __syncthreads();
-    long long total = 0, before = 0, mine = 0;
+    long long total = 0, before = 0, mine = 0;   // stages: all, of requests before, of request b
+    int steps = 1;                               // of a unit of request b
     for (int b0 = 0; b0 < a.B; b0 += kThreads) {
         const int b = b0 + threadIdx.x;
         mine = 0;
         if (b < a.B) {
             const AttnRequest r = attn_request(a, b);
-            mine = work_of<ROWS>(a, r).total;
-            if (r.bad || (r.n > 0 && r.len == 0)) s_special = 1;
+            const Work w = work_of<ROWS>(a, r);
+            mine = w.total;
+            steps = w.steps;
+            if (r.bad || (r.n > 0 && r.len == 0)) s.start.special = 1;
         }
         long long t;
-        before = cta_scan(mine, t, s_sums);
+        before = cta_scan(mine, t, s.start.sums);
         total += t;
     }
     const long long chunk = (total + gridDim.x - 1) / gridDim.x;
-    const long long begin = chunk * blockIdx.x;
-    const long long end = min(begin + chunk, total);
+    const long long raw0 = chunk * blockIdx.x, raw1 = min(raw0 + chunk, total);
     // requests that need no sums: bad ones, and those without keys
     __syncthreads();
-    if (s_special) {
+    if (s.start.special) {
         for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
             const AttnRequest r = attn_request(a, b);
             if (!r.bad && !(r.n > 0 && r.len == 0)) continue;
@@ -339,39 +356,56 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
                 for (int i = threadIdx.x; i < per; i += kThreads) a.out[(size_t)row * a.ldo + i] = v;
         }
     }
-    if (begin >= end) return;
+    if (raw0 >= raw1) return;
+    if (threadIdx.x <= kWarps) s.start.pos[threadIdx.x] = total;
+    __syncthreads();
     {
         long long base = 0;
         for (int b0 = 0; b0 < a.B; b0 += kThreads) {
             const int b = b0 + threadIdx.x;
             long long t = total;
             if (a.B > kThreads) {
-                mine = b < a.B ? work_of<ROWS>(a, attn_request(a, b)).total : 0;
-                before = cta_scan(mine, t, s_sums);
+                const Work w = b < a.B ? work_of<ROWS>(a, attn_request(a, b)) : Work{0, 0, 0, 0};
+                mine = w.total;
+                steps = w.steps;
+                before = cta_scan(mine, t, s.start.sums);
             }
-            if (begin >= base + before && begin < base + before + mine) {
-                s_b = b;
-                s_at = begin - (base + before);
-            }
+            if (mine > 0)
+                for (int w = 0; w <= kWarps; ++w) {
+                    long long at = raw0 + (raw1 - raw0) * w / kWarps - (base + before);
+                    if (at >= 0 && at < mine) {
+                        if (steps <= kWholeStages) at -= at % steps;
+                        s.start.b[w] = b;
+                        s.start.at[w] = at;
+                        s.start.pos[w] = base + before + at;
+                    }
+                }
             base += t;
-            if (base > begin) break;  // uniform
+            if (base > raw1) break;  // uniform
         }
         __syncthreads();
     }
 
     const uint32_t ring = smem_addr(smem) + (uint32_t)warp * STAGES * S::kBytes;
-    const uint32_t q_s = smem_addr(smem) + kWarps * STAGES * S::kBytes;   // the unit's query pieces
-    float *own = reinterpret_cast<float *>(smem + (size_t)warp * STAGES * S::kBytes);   // after a unit
-    int b = s_b;
-    AttnRequest rq = attn_request(a, b);
-    Work wk = work_of<ROWS>(a, rq);
-    long long pos = begin;
-    int unit, from;                   // of the request: (kv head, row block), key step
-    {
-        const long long at = s_at;
+    float *own = reinterpret_cast<float *>(smem + (size_t)warp * STAGES * S::kBytes);   // when the warp is done
+    const uint32_t q_s = smem_addr(smem) + kWarps * STAGES * S::kBytes + warp * NB * J * 512;   // query pieces
+    // this warp's range, and where it starts
+    const long long begin = s.start.pos[0], end = s.start.pos[kWarps];
+    const long long wb = s.start.pos[warp], we = s.start.pos[warp + 1];
+    long long pos = wb;
+    int b = 0, unit = 0, from = 0;    // of the request: (kv head, row block), stage
+    AttnRequest rq{};
+    Work wk{0, 1, 1, 0};
+    if (wb < we) {
+        b = s.start.b[warp];
+        rq = attn_request(a, b);
+        wk = work_of<ROWS>(a, rq);
+        const long long at = s.start.at[warp];
         unit = (int)(at / wk.steps);
         from = (int)(at - (long long)unit * wk.steps);
     }
+    __syncthreads();
+    if (lane < 2) s.seg[2 * warp + lane] = Segment{-1, 0, 0, 0, 0, 0, 0, 0};
     // this lane's places in a stage: keys, values (the keys of rows 2c and 2c + 1), scales
     const int ka0 = key_of_row(g), vk0 = c, vk1 = 4 + (c ^ 3);
     const uint32_t kof = J == 8   ? ka0 * 128 + (((2 * c) ^ swizzle<J>(ka0)) << 4)
@@ -391,8 +425,8 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
     // stretches of 16 rows (640 bytes or more each): a pool holds fewer than 2^32
     const uint32_t page_stretches = (uint32_t)H * (uint32_t)(a.c.page_size >> 4), page_mask = a.c.page_size - 1;
     const uint32_t n_pages = (uint32_t)a.c.n_pages;
-    while (pos < end) {
-        const int upto = (int)min((long long)wk.steps, from + (end - pos));
+    while (pos < we) {
+        const int upto = (int)min((long long)wk.steps, from + (we - pos));
         const int h = unit / wk.blocks, rb = unit - h * wk.blocks;
         const int rows_all = rq.n * R;
         // keys that some row of the block sees; keys that all of its rows see
@@ -402,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
         const int see_lo = attn_first(a, max(all_hi, -1)), all_lo = attn_first(a, see_hi);
 
         const int32_t *table = a.page_table + (size_t)b * a.max_pages;
-        const int key00 = (wk.step0 + from) * kStepKeys + warp * kStageKeys;
+        const int key00 = (wk.step0 + from) * kStageKeys;
         const int iters = upto - from;
         // this lane's first 16-byte piece of a page's rows of this head
         const size_t head_row = (size_t)h * a.c.page_size;
@@ -414,14 +448,14 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
         auto pages_of = [&](int i) {
             int2 pg = make_int2(-1, -1);
             if (i < iters) {
-                const int k0 = key00 + i * kStepKeys;
+                const int k0 = key00 + i * kStageKeys;
                 if (k0 <= see_hi && k0 + 16 > see_lo) pg.x = __ldg(table + (k0 >> shift));
                 if (k0 + 16 <= see_hi && k0 + 32 > see_lo) pg.y = __ldg(table + ((k0 + 16) >> shift));
             }
             return pg;
         };
         auto issue = [&](int i, int slot, int2 pg) {
-            const int k0 = key00 + i * kStepKeys;
+            const int k0 = key00 + i * kStageKeys;
             if (i < iters && k0 <= see_hi && k0 + 32 > see_lo) {
                 const uint32_t st = ring + (uint32_t)slot * S::kBytes;
                 const bool ok[2] = {(uint32_t)pg.x < n_pages, (uint32_t)pg.y < n_pages};
@@ -480,9 +514,11 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
         }
 
         // ---- query rows, while the first keys come: two fp16 pieces, scaled
-        // by a power of two per row, for all warps in shared memory ----
-        if (warp < NB) {
-            const int nb = warp;
+        // by a power of two per row, in shared memory ----
+        __syncwarp();
+        float qs[NB][G], F[NB];                                // of row c: sums per group, factor
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
             const int rho = rb * ROWS + nb * 4 + (g >> 1);     // the row this thread's column holds
             const bool in = rho < rows_all;
             const int j = in ? rho / R : 0, r = in ? rho - j * R : 0;
@@ -539,18 +575,14 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
                 float t = sum[gr];
                 t += __shfl_xor_sync(0xffffffffu, t, 1);
                 t += __shfl_xor_sync(0xffffffffu, t, 2);
-                if (c == 0 && !lo) s_row[nb][g >> 1][gr] = t * 0x1p-24f;
+                qs[nb][gr] = __shfl_sync(0xffffffffu, t, 8 * c) * 0x1p-24f;
             }
-            if (c == 0 && !lo) s_row[nb][g >> 1][G] = ldexpf(a.scale * kLog2e, 24 - k);
+            F[nb] = ldexpf(a.scale * kLog2e, 24 - __shfl_sync(0xffffffffu, k, 8 * c));
         }
-        __syncthreads();
-        float qs[NB][G], F[NB];                                // of row c
+        __syncwarp();
         int last[NB], first[NB];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-#pragma unroll
-            for (int gr = 0; gr < G; ++gr) qs[nb][gr] = s_row[nb][c][gr];
-            F[nb] = s_row[nb][c][G];
             const int rc = rb * ROWS + nb * 4 + c;
             last[nb] = rc < rows_all ? rq.len - rq.n + rc / R : -1;
             first[nb] = attn_first(a, last[nb]);
@@ -582,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
             }
             cp_async_wait<STAGES - 1>();
             __syncwarp();
-            const int k0 = key00 + i * kStepKeys;
+            const int k0 = key00 + i * kStageKeys;
             const uint32_t st = ring + (uint32_t)slot * S::kBytes;
             if (++slot == STAGES) slot = 0;
             if (k0 > see_hi || k0 + kStageKeys <= see_lo) continue;   // uniform in the warp
@@ -798,92 +830,116 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
         __syncwarp();
         carry<NB, J>(o, t0, t1);
 
-        // ---- the warp's sums into its own stretch of the ring: [row][D], then m, l ----
+        // ---- a whole unit is finished; the sums of a cut one go to the CTA's join ----
+        const bool whole = from == 0 && upto == wk.steps, done = pos + iters >= we;
+        float *to = done ? own : p.head + ((size_t)blockIdx.x * kWarps + warp) * kSums;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-            const float back = vref * 0x1p-11f;
             float lt = l[nb];
             lt += __shfl_xor_sync(0xffffffffu, lt, 4);
             lt += __shfl_xor_sync(0xffffffffu, lt, 8);
             lt += __shfl_xor_sync(0xffffffffu, lt, 16);
-            const int row = nb * 4 + c;
+            const int row = nb * 4 + c, rho = rb * ROWS + row;
+            float back = vref * 0x1p-11f;
+            if (whole) {
+                back *= m[nb] == -INFINITY ? 0.0f : 1.0f / lt;
+                const int j = rho / R, r = rho - j * R;
+                to = a.out + (size_t)(rq.row0 + j) * a.ldo + (size_t)(h * R + r) * D - row * D;
+            } else if (g == 0) {
+                to[ROWS * D + 2 * row] = m[nb];
+                to[ROWS * D + 2 * row + 1] = lt;
+            }
 #pragma unroll
             for (int gr = 0; gr < G; ++gr) {
                 zs[nb][gr] += __shfl_xor_sync(0xffffffffu, zs[nb][gr], 4);
                 zs[nb][gr] += __shfl_xor_sync(0xffffffffu, zs[nb][gr], 8);
                 zs[nb][gr] += __shfl_xor_sync(0xffffffffu, zs[nb][gr], 16);
             }
+            if (!whole || rho < rows_all) {
 #pragma unroll
-            for (int u = 0; u < J; ++u) {
-                const float z = zs[nb][u / UG];
-                *reinterpret_cast<float4 *>(own + row * D + 32 * u + 4 * g) =
-                    make_float4((o[nb][u][0] - z) * back, (o[nb][u][1] - z) * back, (o[nb][u][2] - z) * back,
-                                (o[nb][u][3] - z) * back);
-            }
-            if (g == 0) {
-                own[ROWS * D + 2 * row] = m[nb];
-                own[ROWS * D + 2 * row + 1] = lt;
-            }
-        }
-        __syncthreads();
-        // ---- the warps' sums joined, in order ----
-        const bool whole = from == 0 && upto == wk.steps;
-        const int first_unit = pos == begin;                   // this CTA's first unit: slot 0
-        float *part = p.part + ((size_t)blockIdx.x * 2 + (first_unit ? 0 : 1)) * ROWS * (D + 2);
-        for (int i = threadIdx.x; i < ROWS * D / 4; i += kThreads) {
-            const int row = i / (D / 4), d = 4 * (i - row * (D / 4));
-            const int rho = rb * ROWS + row;
-            if (rho >= rows_all) continue;
-            float mt = -INFINITY;
-#pragma unroll
-            for (int v = 0; v < kWarps; ++v) {
-                const float *o2 = reinterpret_cast<const float *>(smem + (size_t)v * STAGES * S::kBytes);
-                mt = fmaxf(mt, o2[ROWS * D + 2 * row]);
-            }
-            const float ref = mt == -INFINITY ? 0.0f : mt;
-            float lt = 0.0f;
-            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int v = 0; v < kWarps; ++v) {
-                const float *o2 = reinterpret_cast<const float *>(smem + (size_t)v * STAGES * S::kBytes);
-                const float f = exp2_approx(o2[ROWS * D + 2 * row] - ref);
-                const float4 t = *reinterpret_cast<const float4 *>(o2 + row * D + d);
-                lt = fmaf(f, o2[ROWS * D + 2 * row + 1], lt);
-                s.x = fmaf(f, t.x, s.x);
-                s.y = fmaf(f, t.y, s.y);
-                s.z = fmaf(f, t.z, s.z);
-                s.w = fmaf(f, t.w, s.w);
-            }
-            if (whole) {
-                const int j = rho / R, r = rho - j * R;
-                const float inv = mt == -INFINITY ? 0.0f : 1.0f / lt;
-                *reinterpret_cast<float4 *>(a.out + (size_t)(rq.row0 + j) * a.ldo + (size_t)(h * R + r) * D + d) =
-                    make_float4(s.x * inv, s.y * inv, s.z * inv, s.w * inv);
-            } else {
-                float *pr = part + (size_t)row * D + d;
-                *reinterpret_cast<float4 *>(pr) = s;
-                if (d == 0) {
-                    part[ROWS * D + 2 * row] = mt;
-                    part[ROWS * D + 2 * row + 1] = lt;
+                for (int u = 0; u < J; ++u) {
+                    const float z = zs[nb][u / UG];
+                    *reinterpret_cast<float4 *>(to + row * D + 32 * u + 4 * g) =
+                        make_float4((o[nb][u][0] - z) * back, (o[nb][u][1] - z) * back, (o[nb][u][2] - z) * back,
+                                    (o[nb][u][3] - z) * back);
                 }
             }
         }
-        if (threadIdx.x == 0 && !whole && from == 0) {
-            // the unit starts here and goes on in the CTAs up to the one that holds its last step
-            const int last_cta = (int)((pos + wk.steps - 1) / chunk);
-            p.desc[blockIdx.x] = make_int4(b, unit, last_cta, first_unit ? 0 : 1);
-        }
-        __syncthreads();
+        if (!whole && lane == 0) s.seg[2 * warp + (done ? 1 : 0)] = Segment{pos - from, b, unit, wk.steps, rq.row0, rows_all, h, rb};
 
-        pos += upto - from;
+        pos += iters;
         from = 0;
-        if (upto == wk.steps && ++unit == wk.blocks * H && pos < end) {
+        if (upto == wk.steps && ++unit == wk.blocks * H && pos < we) {
             unit = 0;
             do {                                               // the next request with work
                 ++b;
                 rq = attn_request(a, b);
                 wk = work_of<ROWS>(a, rq);
             } while (wk.total == 0);
+        }
+    }
+    __syncthreads();
+
+    // ---- the warps' segments of one unit joined, in order ----
+    const long long start_of = lane < 2 * kWarps ? s.seg[lane].start : -1;
+    uint32_t left = __ballot_sync(0xffffffffu, start_of >= 0);
+    while (left) {
+        const Segment seg = s.seg[__ffs(left) - 1];
+        const uint32_t mine_of = __ballot_sync(0xffffffffu, start_of == seg.start);
+        left &= ~mine_of;
+        const bool whole = seg.start >= begin && seg.start + seg.steps <= end;
+        const int slot = seg.start > begin ? 1 : 0;
+        float *part = p.part + ((size_t)blockIdx.x * 2 + slot) * kSums;
+        for (int i = threadIdx.x; i < ROWS * D / 4; i += kThreads) {
+            const int row = i / (D / 4), d = 4 * (i - row * (D / 4));
+            const int rho = seg.rb * ROWS + row;
+            if (rho >= seg.rows) continue;
+            auto sums_of = [&](int e) {
+                return e & 1 ? reinterpret_cast<const float *>(smem + (size_t)(e >> 1) * STAGES * S::kBytes)
+                             : p.head + ((size_t)blockIdx.x * kWarps + (e >> 1)) * kSums;
+            };
+            float2 ml[2 * kWarps];
+            float4 t[2 * kWarps];
+            float mt = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < 2 * kWarps; ++e) {
+                ml[e] = make_float2(-INFINITY, 0.0f);
+                t[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if ((mine_of >> e) & 1u) {
+                    ml[e] = *reinterpret_cast<const float2 *>(sums_of(e) + ROWS * D + 2 * row);
+                    t[e] = *reinterpret_cast<const float4 *>(sums_of(e) + row * D + d);
+                }
+                mt = fmaxf(mt, ml[e].x);
+            }
+            const float ref = mt == -INFINITY ? 0.0f : mt;
+            float lt = 0.0f;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int e = 0; e < 2 * kWarps; ++e) {
+                const float f = exp2_approx(ml[e].x - ref);
+                lt = fmaf(f, ml[e].y, lt);
+                v.x = fmaf(f, t[e].x, v.x);
+                v.y = fmaf(f, t[e].y, v.y);
+                v.z = fmaf(f, t[e].z, v.z);
+                v.w = fmaf(f, t[e].w, v.w);
+            }
+            if (whole) {
+                const int j = rho / R, r = rho - j * R;
+                const float inv = mt == -INFINITY ? 0.0f : 1.0f / lt;
+                *reinterpret_cast<float4 *>(a.out + (size_t)(seg.row0 + j) * a.ldo + (size_t)(seg.h * R + r) * D + d) =
+                    make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+            } else {
+                *reinterpret_cast<float4 *>(part + (size_t)row * D + d) = v;
+                if (d == 0) {
+                    part[ROWS * D + 2 * row] = mt;
+                    part[ROWS * D + 2 * row + 1] = lt;
+                }
+            }
+        }
+        if (threadIdx.x == 0 && !whole && seg.start >= begin) {
+            // the unit starts here and goes on in the CTAs up to the one that holds its last stage
+            const int last_cta = (int)((seg.start + seg.steps - 1) / chunk);
+            p.desc[blockIdx.x] = make_int4(seg.b, seg.unit, last_cta, slot);
         }
     }
 }
@@ -938,12 +994,13 @@ cudaError_t launch_split(const AttnCall &call, cudaStream_t stream)
     // four query rows and heads of up to 128: registers and shared memory for
     // two CTAs per SM; otherwise one
     constexpr int MINB = NB * J <= 4 ? 2 : 1;
-    constexpr int room = MINB == 2 ? 109 * 1024 : 216 * 1024;
+    constexpr int kQ = kWarps * NB * J * 512;
+    constexpr int room = (MINB == 2 ? 112 * 1024 : 216 * 1024) - kQ;
     constexpr int fit = room / (kWarps * Stage<J, G>::kBytes);
     constexpr int STAGES = fit < 2 ? 2 : fit > 4 ? 4 : fit;
     static_assert(STAGES * Stage<J, G>::kBytes >= 4 * NB * (32 * J + 2) * 4, "the sums fit the ring");
     auto kern = attn_split_kernel<J, G, NB, STAGES, MINB>;
-    constexpr int smem = kWarps * STAGES * Stage<J, G>::kBytes + NB * J * 512;
+    constexpr int smem = kWarps * STAGES * Stage<J, G>::kBytes + kQ;
     int dev = 0, sms = 0;
     cudaError_t err;
     if ((err = cudaGetDevice(&dev)) != cudaSuccess) return err;
@@ -956,21 +1013,22 @@ cudaError_t launch_split(const AttnCall &call, cudaStream_t stream)
     if ((err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return err;
     SplitParams p{};
     p.a = call;
-    // no more CTAs than steps can exist
+    // a stage for every warp at the least
     const int R = call.heads / call.c.kv_heads;
-    const long long steps = (call.max_len + kStepKeys - 1) / kStepKeys;
+    const long long steps = (call.max_len + kStageKeys - 1) / kStageKeys;
     const long long most_n = call.max_query < call.T ? call.max_query : call.T;
     const long long blocks = (most_n * R + 4 * NB - 1) / (4 * NB);
     const long long units = (call.B < call.T ? call.B : call.T) * blocks * call.c.kv_heads;
     long long grid = (long long)sms * MINB;
-    if (grid > kMaxGrid) grid = kMaxGrid;
-    if (grid > units * steps) grid = units * steps;
+    if (grid > kMaxGrid / 2 * MINB) grid = kMaxGrid / 2 * MINB;
+    if (grid > (units * steps + kWarps - 1) / kWarps) grid = (units * steps + kWarps - 1) / kWarps;
     if (grid < 1) grid = 1;
     p.grid = (int)grid;
     p.desc = static_cast<int4 *>(call.workspace);
     p.part = reinterpret_cast<float *>(static_cast<char *>(call.workspace) + kMaxGrid * sizeof(int4));
+    p.head = p.part + (size_t)grid * 2 * 4 * NB * (32 * J + 2);
     kern<<<(unsigned)grid, kThreads, smem, stream>>>(p);
-    if ((err = cudaGetLastError()) != cudaSuccess || steps <= 1 || grid <= 1) return err;
+    if ((err = cudaGetLastError()) != cudaSuccess || steps <= kWholeStages || grid <= 1) return err;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     cfg.gridDim = dim3((unsigned)grid);
@@ -997,7 +1055,9 @@ cudaError_t launch_rows(const AttnCall &call, cudaStream_t stream)
 
 size_t attn_workspace_bytes(int, int, int, int D)
 {
-    return kMaxGrid * (sizeof(int4) + 2 * 8 * (size_t)(D + 2) * sizeof(float));
+    // rows of sums of all CTAs: 304 of 8 rows at 64 dims, above that 304 of 4 or 152 of 8
+    const size_t rows = D <= 64 ? kMaxGrid * 8 : kMaxGrid * 4;
+    return kMaxGrid * sizeof(int4) + rows * (2 + kWarps) * (size_t)(D + 2) * sizeof(float);
 }
 
 cudaError_t launch_attn(const AttnCall &in, cudaStream_t stream)
