@@ -29,17 +29,29 @@
 // per 32 keys), so that accumulators are rescaled rarely; the values'
 // scales likewise share a power of two 2^E, which keeps p s inside fp16.
 //
-// Split.  A CTA step is 256 keys of one (request, kv head, block of rows),
-// 32 for each of 8 warps; the list of all steps is cut into equal ranges, one
-// per CTA, whatever the requests' lengths.  A unit cut by a range boundary
-// leaves partial sums (m, l, sum) in the workspace, which a second kernel
-// joins in order: no atomics, the same bits every time.  The cut is computed
-// on the device from the lengths, so a captured launch follows them.
+// Split.  A stage is 32 keys of one (request, kv head, block of rows), a
+// unit; the list of all stages is cut into equal ranges, one per CTA, and
+// those into one per warp, whatever the requests' lengths (units of up to 4
+// stages are not cut).  So each warp goes its own way through its keys, with
+// its own sums, query pieces and copies, and a CTA meets once, at the end: it
+// joins its warps' sums of the same unit, and a unit cut by the range of the
+// CTA leaves (m, l, sum) in the workspace, which a second kernel joins: no
+// atomics, always in order, the same bits every time.  (8 warps that share a
+// 256-key step and meet at each unit's end took 62 us where this takes 50.)
+// The cut is computed on the device from the lengths, so a captured launch
+// follows them.
 //
 // Copies.  Each warp keeps its own ring of 32-key stages filled by 16-byte
-// cp.async, without any CTA barrier: the rows of 16 keys of one page and head
-// are contiguous.  Keys are assigned to the instruction's rows so that both
-// products read shared memory without bank conflicts (see key_of_row).
+// cp.async: the rows of 16 keys of one page and head are contiguous.  Keys
+// are assigned to the instruction's rows so that both products read shared
+// memory without bank conflicts (see key_of_row).
+//
+// Measured: 48 requests of 500 to 8192 keys, 32 heads over 8 of 128, one
+// group: 50 us, 215 MB at 4.3 TB/s; two of 125k keys, two groups: 69 us, 319
+// MB at 4.6 TB/s; 16 drafts of 5 tokens, 16 heads of 64, two groups: 32 us.
+// Bound by instructions: 685 per stage and warp, 32 of them matrix
+// instructions and 240 the decoding of codes, issued in 60% of the cycles by
+// the 16 warps that registers allow (128 per thread).
 #include <cuda_fp16.h>
 
 #include <atomic>
@@ -245,6 +257,12 @@ __device__ __forceinline__ Work work_of(const AttnCall &p, const AttnRequest &r)
     return w;
 }
 
+// a / d of nonnegative numbers, in 32 bits where they allow it.
+__device__ __forceinline__ long long quotient(long long a, int d)
+{
+    return (a >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)d) : a / d;
+}
+
 __device__ __forceinline__ long long warp_scan(long long v, int lane)
 {
 #pragma unroll
@@ -341,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
         before = cta_scan(mine, t, s.start.sums);
         total += t;
     }
-    const long long chunk = (total + gridDim.x - 1) / gridDim.x;
+    const long long chunk = quotient(total + gridDim.x - 1, (int)gridDim.x);
     const long long raw0 = chunk * blockIdx.x, raw1 = min(raw0 + chunk, total);
     // requests that need no sums: bad ones, and those without keys
     __syncthreads();
@@ -372,9 +390,9 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
             }
             if (mine > 0)
                 for (int w = 0; w <= kWarps; ++w) {
-                    long long at = raw0 + (raw1 - raw0) * w / kWarps - (base + before);
+                    long long at = raw0 + (((raw1 - raw0) * w) / kWarps) - (base + before);
                     if (at >= 0 && at < mine) {
-                        if (steps <= kWholeStages) at -= at % steps;
+                        if (steps <= kWholeStages) at -= at - quotient(at, steps) * steps;
                         s.start.b[w] = b;
                         s.start.at[w] = at;
                         s.start.pos[w] = base + before + at;
@@ -401,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
         rq = attn_request(a, b);
         wk = work_of<ROWS>(a, rq);
         const long long at = s.start.at[warp];
-        unit = (int)(at / wk.steps);
+        unit = (int)quotient(at, wk.steps);
         from = (int)(at - (long long)unit * wk.steps);
     }
     __syncthreads();
@@ -938,7 +956,7 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
         }
         if (threadIdx.x == 0 && !whole && seg.start >= begin) {
             // the unit starts here and goes on in the CTAs up to the one that holds its last stage
-            const int last_cta = (int)((seg.start + seg.steps - 1) / chunk);
+            const int last_cta = (int)((uint64_t)(seg.start + seg.steps - 1) / (uint64_t)chunk);
             p.desc[blockIdx.x] = make_int4(seg.b, seg.unit, last_cta, slot);
         }
     }
@@ -967,18 +985,39 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ 
         if (rho >= rq.n * R) continue;
         float m = -INFINITY, l = 0.0f;
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int cta = blockIdx.x; cta <= d.z; ++cta) {
-            const float *pt = part_of(cta);
-            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(pt + (size_t)ROWS * D + 2 * row));
-            const float4 t = __ldcg(reinterpret_cast<const float4 *>(pt + (size_t)row * D + dd));
-            const float mn = fmaxf(m, ml.x);
+        constexpr int kAhead = 8;    // partial sums on their way at once
+        for (int cta0 = blockIdx.x; cta0 <= d.z; cta0 += kAhead) {
+            float2 ml[kAhead];
+            float4 t[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                ml[k] = make_float2(-INFINITY, 0.0f);
+                t[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (cta0 + k <= d.z) {
+                    const float *pt = part_of(cta0 + k);
+                    ml[k] = __ldcg(reinterpret_cast<const float2 *>(pt + (size_t)ROWS * D + 2 * row));
+                    t[k] = __ldcg(reinterpret_cast<const float4 *>(pt + (size_t)row * D + dd));
+                }
+            }
+            float mn = m;
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) mn = fmaxf(mn, ml[k].x);
             const float ref = mn == -INFINITY ? 0.0f : mn;
-            const float fo = exp2_approx(m - ref), fn = exp2_approx(ml.x - ref);
-            l = l * fo + ml.y * fn;
-            s.x = s.x * fo + t.x * fn;
-            s.y = s.y * fo + t.y * fn;
-            s.z = s.z * fo + t.z * fn;
-            s.w = s.w * fo + t.w * fn;
+            const float fo = exp2_approx(m - ref);
+            l *= fo;
+            s.x *= fo;
+            s.y *= fo;
+            s.z *= fo;
+            s.w *= fo;
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const float fn = exp2_approx(ml[k].x - ref);
+                l = fmaf(fn, ml[k].y, l);
+                s.x = fmaf(fn, t[k].x, s.x);
+                s.y = fmaf(fn, t[k].y, s.y);
+                s.z = fmaf(fn, t[k].z, s.z);
+                s.w = fmaf(fn, t[k].w, s.w);
+            }
             m = mn;
         }
         const int j = rho / R, r = rho - j * R;
@@ -1062,11 +1101,15 @@ size_t attn_workspace_bytes(int, int, int, int D)
 
 cudaError_t launch_attn(const AttnCall &in, cudaStream_t stream)
 {
-    // Many query rows: a 128-row tile of the prompt kernel takes as long as
-    // about 4 blocks of 8 rows here, if its tiles fill a good part of the GPU
-    // (16 tiles' rows over all heads).
+    // Requests of many query rows go to the prompt kernel, whose tiles hold
+    // 128 rows, if there are enough rows in all to fill its CTAs.  Measured
+    // with 4096 keys and more behind 32 heads over 8 of 128, one group:
+    // 16 requests of 8 tokens (32 rows each, 4096 in all) 88 us there and 83
+    // here, of 12 (48, 6144) 88 and 116, of 16 89 and 150; one request of 64
+    // tokens (256, 2048) 90 and 50.  Four groups: of 12 169 and 150, of 16
+    // 170 and 197.
     AttnCall call = in;
-    constexpr int kPromptRows = 33, kPromptTotal = 2048;
+    constexpr int kPromptRows = 48, kPromptTotal = 5120;
     const long long R = call.heads / call.c.kv_heads;
     const bool prompt = prompt_path_supported(call) && call.max_query * R >= kPromptRows &&
                         (long long)call.T * call.heads >= kPromptTotal;

@@ -166,6 +166,23 @@ def test_sharp_and_flat_weights(gq4, H):
     s.check(s.run(gq4))
 
 
+def test_prompts_of_many_heads(gq4):
+    """Queries without keys, that pick one key and that weigh all alike, scales over ten powers
+    of two: 9000 and more query rows in all."""
+    s = Setup([5, 1, 200, 1], [2, 0, 30, 9], 48, 4, 64, 32, 16)
+    got = s.run(gq4)
+    s.check(got)
+    assert np.all(got[:3] == 0) and np.all(got[5] == 0) and np.all(got[6:6 + 170] == 0)
+    for gs in (32, 128):
+        s = Setup([1, 90, 150], [600, 600, 700], 40, 2, 128, gs, 16)
+        s.q[0] *= 60
+        s.q[1:30] = 0
+        s.q[91:130] *= 30
+        s.cache.sz[1][..., 0] *= np.exp2(np.random.default_rng(3).integers(-5, 6, s.cache.sz[1].shape[:-1]))
+        s.check(s.run(gq4))
+    assert gq4.device_error() == 0
+
+
 @pytest.mark.parametrize("n,H", [(1, 4), (150, 4), (150, 16)])
 def test_scales_of_unlike_size(gq4, n, H):
     """Value scales over ten powers of two, queries of very small and very large size."""
