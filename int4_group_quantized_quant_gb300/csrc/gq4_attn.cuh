@@ -5,7 +5,7 @@
 #include <cstdint>
 
 #include "gq4_device.cuh"
-#include "gq4_internal.h"
+#include "gq4_kv_internal.h"
 #include "gq4_kv.cuh"
 #include "gq4_tma.cuh"
 

@@ -42,6 +42,7 @@
 #include <cstdint>
 
 #include "gq4_attn.cuh"
+#include "gq4_quant.cuh"
 #include "gq4_tcgen05.cuh"
 
 namespace gq4 {

@@ -3,7 +3,7 @@
 // layout is stated in gq4.h.
 #include <cstdint>
 
-#include "gq4_internal.h"
+#include "gq4_kv_internal.h"
 #include "gq4_kv.cuh"
 #include "gq4_quant.cuh"
 

@@ -6,7 +6,7 @@
 
 #include "gq4.h"
 #include "gq4_checks.h"
-#include "gq4_internal.h"
+#include "gq4_kv_internal.h"
 
 namespace {
 

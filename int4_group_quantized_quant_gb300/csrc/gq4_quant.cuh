@@ -9,6 +9,13 @@
 
 namespace gq4 {
 
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b)
+{
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
 // min and max that return NaN when either input is NaN, so that a NaN
 // anywhere in a group reaches its range.
 __device__ __forceinline__ float min_nan(float a, float b)

@@ -24,7 +24,7 @@
 // to sincosf as a value in [-pi, pi].
 #include <cstdint>
 
-#include "gq4_internal.h"
+#include "gq4_kv_internal.h"
 
 namespace gq4 {
 namespace {
