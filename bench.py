@@ -906,6 +906,92 @@ def run_reference(args, rank, world):
 # Profile cases (small, for ncu): a few launches of one kernel
 # ---------------------------------------------------------------------------
 
+CACHE_CASES = {"rope": "norm and rotation of 8192 tokens, 40 heads of 128",
+               "append": "cache writer, 16384 tokens, 8 heads of 128",
+               "gather": "cache reader, 16384 tokens, 8 heads of 128",
+               "attention": "decode attention, 48 requests of 501 to 8162 keys, 32 heads over 8 of 128",
+               "prompt": "prompt attention, 4096 tokens, 32 heads over 8 of 128"}
+
+
+class CacheStep:
+    """What lies between the QKV product and the output projection, at 32
+    heads over 8 of 128 values and pages of 16: `past` tokens per request
+    already in a 4-bit cache whose pages are shuffled, `new` each to come."""
+
+    HEADS, KV_HEADS, DIM, PAGE = 32, 8, 128, 16
+
+    def __init__(self, gq4, past, new, gs=GS, seed=1700):
+        import torch
+        self.gq4, self.gs, self.new = gq4, gs, new
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        B, T = len(past), len(past) * new
+        KH, D, page = self.KV_HEADS, self.DIM, self.PAGE
+        self.T, self.most = T, max(past) + new
+        pages = [-(-(p + new) // page) for p in past]
+        dev = {"device": "cuda"}
+        self.cache = gq4.kv_cache(sum(pages), KH, page, D, gs)
+        for codes in self.cache[0::2]:
+            codes.copy_(torch.randint(-2 ** 31, 2 ** 31 - 1, codes.shape, generator=g, dtype=torch.int32, **dev))
+        for sz in self.cache[1::2]:
+            sz[..., 0] = 0.1
+            sz[..., 1] = 7.5
+        ids = torch.randperm(sum(pages), generator=g, **dev).to(torch.int32)
+        self.table = torch.full((B, max(pages)), -1, dtype=torch.int32, **dev)
+        at = 0
+        for b, n in enumerate(pages):
+            self.table[b, :n] = ids[at:at + n]
+            at += n
+        self.past = torch.tensor(past, dtype=torch.int32, **dev)
+        self.fresh = torch.full((B,), new, dtype=torch.int32, **dev)
+        self.seq_lens = self.past + self.fresh
+        self.starts = torch.arange(0, T + 1, new, dtype=torch.int32, **dev)
+        self.positions = torch.cat([torch.arange(p, p + new) for p in past]).to(torch.int32).cuda()
+        of = torch.arange(B, **dev).repeat_interleave(new)
+        where = self.positions.long()
+        self.slots = (self.table[of, where // page] * page + where % page).to(torch.int32)
+        self.inv_freq = 10000.0 ** (-torch.arange(0, D, 2, **dev) / D)
+        self.gain = torch.rand(D, generator=g, **dev) + 0.5
+        self.q = torch.randn((T, self.HEADS, D), generator=g, **dev)
+        self.k = torch.randn((T, KH, D), generator=g, **dev)
+        self.v = torch.randn((T, KH, D), generator=g, **dev)
+        self.q_out, self.k_out, self.v_out = (torch.empty_like(x) for x in (self.q, self.k, self.v))
+        self.out = torch.empty_like(self.q)
+        self.ws = torch.empty(gq4.kv_attention_workspace_bytes(T, self.HEADS, KH, D), dtype=torch.uint8, **dev)
+        row = KH * (D // 2 + 8 * D // gs)                      # bytes of a token's keys, or values
+        self.bytes = {
+            "rope": 2 * 4 * T * (self.HEADS + KH) * D,
+            "append": 2 * T * (4 * KH * D + row),
+            "gather": 2 * T * (4 * KH * D + row),
+            "attention": 2 * row * sum(p + new for p in past) + 2 * 4 * T * self.HEADS * D,
+        }
+        seen = sum(p * new + new * (new + 1) // 2 for p in past)
+        self.flops = 4 * D * self.HEADS * seen
+
+    def rope(self, s):
+        self.gq4.head_norm_rope(self.q, self.k, self.positions, self.inv_freq, self.gain, self.gain,
+                                q_out=self.q_out, k_out=self.k_out, stream=s)
+
+    def append(self, s):
+        self.gq4.kv_append(self.k, self.v, self.slots, *self.cache, self.gs, stream=s)
+
+    def gather(self, s):
+        self.gq4.kv_gather(self.slots, *self.cache, self.gs, k_out=self.k_out, v_out=self.v_out, stream=s)
+
+    def attention(self, s):
+        self.gq4.kv_attention(self.q, self.starts, self.seq_lens, self.table, *self.cache, self.gs,
+                              self.DIM ** -0.5, self.new, max_len=self.most, out=self.out, workspace=self.ws,
+                              stream=s)
+
+
+def cache_steps(gq4):
+    """name -> (workload, call): the calls that --extras times and --profile launches."""
+    decode = CacheStep(gq4, [500 + 163 * b for b in range(48)], 1)
+    prompt = CacheStep(gq4, [0], 4096)
+    rows, more = CacheStep(gq4, [0], 8192), CacheStep(gq4, [0], 16384)
+    return {"rope": (rows, rows.rope), "append": (more, more.append), "gather": (more, more.gather),
+            "attention": (decode, decode.attention), "prompt": (prompt, prompt.attention)}
+
+
 def run_profile_case(args):
     import torch
     from int4_group_quantized_quant_gb300 import build as b
@@ -926,6 +1012,13 @@ def run_profile_case(args):
             gq4.gemm(A, *Wd, GS, C=C, workspace=ws)
         torch.cuda.synchronize()
         print(json.dumps({"profile_case": "gemm", "rows": Mg, "launch_rounds": args.steps}))
+        return
+    if args.profile in CACHE_CASES:
+        call = cache_steps(gq4)[args.profile][1]
+        for _ in range(args.steps):
+            call(torch.cuda.current_stream())
+        torch.cuda.synchronize()
+        print(json.dumps({"profile_case": args.profile, "launch_rounds": args.steps}))
         return
     stack = Stack(gq4, args.layers, args.lanes)
     stream = torch.cuda.current_stream()
@@ -957,7 +1050,8 @@ def run_extras(args):
     and the gated-input matvecs (one lane, 4096 x 4096, in a CUDA graph over
     rotating weight sets larger than 4x L2, against the plain matvec), the
     prefill GEMM (512 and 2048 rows through 4096 x 4096, against the bf16
-    peak), the quantizer and the MLX converter (4096 x 11008) and the
+    peak), the calls between the QKV product and the output projection
+    (rotation, cache writer and reader, attention), the quantizer and the MLX converter (4096 x 11008) and the
     embedding gather (8192 ids from a 32000 x 4096 table)."""
     import torch
     from int4_group_quantized_quant_gb300 import build as b
@@ -1108,6 +1202,19 @@ def run_extras(args):
                           "TFLOP/s": round(tf, 1), "frac_of_bf16_peak": round(tf / tpeak, 4),
                           "peak": tpeak, "peak_source": tpeak_src, "weight_sets": 2,
                           "timing": "CUDA graph of 2 calls, CUDA events"}))
+    for tag, (step, call) in cache_steps(gq4).items():
+        us = time_graph(lambda s, call=call: [call(s) for _ in range(4)]) / 4
+        row = {"extra": CACHE_CASES[tag] + " (gs %d)" % gs, "group_size": gs, "us_per_call": round(us, 3)}
+        if tag == "prompt":
+            tf = step.flops / (us * 1e-6) / 1e12
+            row.update({"TFLOP/s": round(tf, 1), "frac_of_bf16_peak": round(tf / tpeak, 4), "peak": tpeak,
+                        "peak_source": tpeak_src})
+        else:
+            gbs = step.bytes[tag] / (us * 1e-6) / 1e9
+            row.update({"bytes_per_call": step.bytes[tag], "GB/s": round(gbs, 1),
+                        "frac_of_hbm_peak": round(gbs / peak, 4), "peak": peak, "peak_source": peak_src})
+        print(json.dumps({**row, "timing": "CUDA graph of 4 calls, CUDA events, same inputs (beyond L2 but for "
+                                           "the prompt's)"}))
     for name, us, nbytes, extra in rows:
         gbs = nbytes / (us * 1e-6) / 1e9
         print(json.dumps({"extra": name, "lanes": 1, "group_size": gs, "us_per_call": round(us, 3),
@@ -1134,7 +1241,7 @@ def main():
                          "the prefill GEMM, the sequence kernel)")
     ap.add_argument("--stack-lanes", type=int, nargs="*", default=[4, 16, 32],
                     help="lane counts of the extra stack entries")
-    ap.add_argument("--profile", choices=["gated", "down", "quad", "o", "step", "gemm"], default=None,
+    ap.add_argument("--profile", choices=["gated", "down", "quad", "o", "step", "gemm", *CACHE_CASES], default=None,
                     help="run a small launch sequence of one kernel for ncu (no timing)")
     ap.add_argument("--extras", action="store_true",
                     help="time the dual, gated-input, GEMM, quantizer, MLX and embedding "

@@ -605,7 +605,8 @@ def kv_attention(q, query_start, seq_lens, page_table, Kq, K_sz, Vq, V_sz, group
         out, ldo = torch.empty((T, H, D), dtype=torch.float32, device=q.device), H * D
     else:
         ldo = _rows(out, "out", (T, H, D))[3]
-    if workspace is None:
+    ours = workspace is None
+    if ours:
         workspace = torch.empty(kv_attention_workspace_bytes(T, H, c.kv_heads, D), dtype=torch.uint8,
                                 device=q.device)
     elif not (isinstance(workspace, torch.Tensor) and workspace.is_cuda and workspace.is_contiguous()):
@@ -614,6 +615,8 @@ def kv_attention(q, query_start, seq_lens, page_table, Kq, K_sz, Vq, V_sz, group
     _call(lib.gq4_kv_attention, "gq4_kv_attention", Kq, stream, B, T, H, page_table.shape[1], max_query, max_len, c,
           q.data_ptr(), ldq, at_start, seq_lens.data_ptr(), page_table.data_ptr(), scale, window, out.data_ptr(), ldo,
           workspace.data_ptr(), workspace.nbytes)
+    if ours and stream is not None and stream.cuda_stream != _raw_stream(q.get_device()):
+        workspace.record_stream(stream)   # freed here, in use there
     return out
 
 

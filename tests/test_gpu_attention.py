@@ -166,6 +166,25 @@ def test_sharp_and_flat_weights(gq4, H):
     s.check(s.run(gq4))
 
 
+def test_own_workspace_outlives_the_call_on_another_stream(gq4):
+    """The workspace that a call allocates is not handed out again while its stream still uses it."""
+    s = Setup([1, 1], [3000, 900], 8, 2, 128, 128, 16)
+    clean = s.run(gq4)
+    size = gq4.kv_attention_workspace_bytes(s.T, 8, 2, 128)
+    args, q, out = s.dev(), dev(s.q), torch.full(s.q.shape, FILL, device="cuda")
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    at = torch.empty(size, dtype=torch.uint8, device="cuda").data_ptr()   # what the call will get
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)
+    gq4.kv_attention(q, *args, scale=s.scale, max_query=1, max_len=3000, out=out, stream=side)
+    again = torch.empty(size, dtype=torch.uint8, device="cuda").data_ptr()
+    assert again != at
+    torch.cuda.synchronize()
+    assert np.array_equal(host(out), clean)
+
+
 def test_prompts_of_many_heads(gq4):
     """Queries without keys, that pick one key and that weigh all alike, scales over ten powers
     of two: 9000 and more query rows in all."""
