@@ -523,9 +523,9 @@ GQ4_API gq4_status gq4_kv_plan(int B, int T, int page_size, int max_pages, int n
  * fixed-point with a power-of-two scale, each value within 2^-22 of the
  * row's largest magnitude), the codes are exact, sums are f32 (requests of
  * many rows and several groups: the keys and values are two pieces too).
- * How a request's keys are split over the GPU depends on the other requests
- * and on max_len, so their change may change last bits (not of a request of
- * few rows and up to 128 keys); the same inputs give the same bits.
+ * How a request's keys are split over the GPU depends on the other requests,
+ * on max_query and on max_len, so their change may change last bits; the same
+ * inputs give the same bits.
  *
  * workspace: at least gq4_kv_attention_workspace_bytes() bytes of device
  * memory, 256-byte aligned, no argument's; contents need not be set and

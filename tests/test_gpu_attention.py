@@ -147,6 +147,20 @@ def test_long_contexts_split(gq4, length):
     s.check(s.run(gq4))
 
 
+@pytest.mark.parametrize("H,KH,D,gs", [(8, 2, 64, 32), (2, 1, 128, 128)])
+def test_more_requests_than_a_block_has_threads(gq4, H, KH, D, gs):
+    """600 requests, idle and without keys among them, whose keys end anywhere in a stage; the
+    first and the last are long, so that cuts fall inside and between requests."""
+    g = I.rng(2202, H)
+    news = g.integers(0, 4, 600).tolist()
+    lens = [0 if g.random() < 0.05 else max(n, int(x)) for n, x in zip(news, g.integers(1, 260, 600))]
+    news[0] = news[-1] = 1
+    lens[0], lens[-1] = 2500, 1333
+    s = Setup(news, lens, H, KH, D, gs, 16)
+    s.check(s.run(gq4))
+    assert gq4.device_error() == 0
+
+
 @pytest.mark.parametrize("H", [4, 16])
 def test_queries_that_see_nothing(gq4, H):
     """seq_len < n: the first queries have no key (their rows are zeros); length 0."""

@@ -193,6 +193,13 @@ def test_append_and_gather(gq4, T, KH, D, gs, page):
     assert gq4.device_error() == 0
 
 
+@pytest.mark.parametrize("T,KH,D,gs,page", [(3000, 1, 64, 64, 16), (1025, 3, 96, 32, 32), (2, 1024, 64, 32, 16),
+                                            (1500, 5, 256, 64, 64)])
+def test_append_and_gather_many_rows(gq4, T, KH, D, gs, page):
+    """Blocks that take several tokens, or a share of one with very many heads."""
+    test_append_and_gather(gq4, T, KH, D, gs, page)
+
+
 def test_append_strided_rows_skipped_and_bad_slots(gq4):
     T, KH, D, gs, page, pages = 6, 2, 64, 32, 16, 3
     g = I.rng(2111)
