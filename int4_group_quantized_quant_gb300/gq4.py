@@ -395,51 +395,68 @@ def embedding(ids, Bq, scales, zeros, group_size, out=None, stream=None):
 # ---------------------------------------------------------------------------
 
 _I32 = (torch.int32,)
-# the current stream's handle without a Stream object around it, where torch has it
+_f32, _i32 = torch.float32, torch.int32
+# the current device, and its current stream's handle without a Stream object around it, where torch has them
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _call(fn, name, t, stream, *args):
-    """fn(*args, stream) on t's device, on the given stream or that device's current one."""
-    index = t.get_device()
-    if index != torch.cuda.current_device():
+def _call(fn, name, index, stream, *args):
+    """fn(*args, stream) on device `index`, on the given stream or that device's current one."""
+    if index != _current_device():
         with torch.cuda.device(index):
-            return _call(fn, name, t, stream, *args)
-    _check(fn(*args, _raw_stream(index) if stream is None else stream.cuda_stream), name)
+            return _call(fn, name, index, stream, *args)
+    status = fn(*args, _raw_stream(index) if stream is None else stream.cuda_stream)
+    if status != OK:
+        raise GQ4Error(status, name)
 
 
-def _same_device(first, *others):
-    index = first.get_device()
-    for t in others:
-        if t is not None and t.get_device() != index:
-            raise ValueError(f"tensors on {first.device} and {t.device}")
-
-
-def _at(t, name, dtype, shape):
-    """t's address; _need's checks (its errors), the common case in one expression."""
-    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.is_contiguous() and t.shape == shape):
+def _at(t, name, dtype, shape, index):
+    """t's address; _need's checks (its errors) and the device's, the common case in one expression."""
+    if not (isinstance(t, torch.Tensor) and t.get_device() == index and t.dtype is dtype and t.shape == shape
+            and t.is_contiguous()):
         _need(t, name, (dtype,), shape)
+        raise ValueError(f"{name} is on {t.device}, the others on cuda:{index}")
     return t.data_ptr()
 
 
-def _rows(t, name, heads_dim=None):
+def _rows(t, name, index=None, heads_dim=None):
     """[T, heads, D] with dense rows (any row distance): (T, heads, D, row distance)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (no CPU path exists)")
-    if t.dtype is not torch.float32:
+    if t.dtype is not _f32:
         raise TypeError(f"{name}: dtype {t.dtype} is not torch.float32")
     if t.dim() != 3:
         raise ValueError(f"{name} must be [T, heads, head_dim]")
     T, H, D = t.shape
     if heads_dim is not None and (T, H, D) != heads_dim:
         raise ValueError(f"{name}: shape {(T, H, D)} != {heads_dim}")
+    if index is not None and t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, the others on cuda:{index}")
     ld, sh, sd = t.stride()
     if (D > 1 and sd != 1) or (H > 1 and sh != D):
         raise ValueError(f"{name}: the heads of a row must be dense")
     return T, H, D, (H * D if T <= 1 else ld)
+
+
+def _rope_side(x, y, gain, name, T, D, index):
+    """One side's heads, tensors and row distances; its output is made where none is given."""
+    if x is None:
+        if y is not None or gain is not None:
+            raise ValueError(f"{name}_out and {name}_gain need {name}")
+        return None, None, (0, None, 0, None, 0)
+    Tx, H, Dx, ld = _rows(x, name, index)
+    if (Tx, Dx) != (T, D):
+        raise ValueError(f"{name}: {Tx} rows of {Dx} != {T} rows of {D}")
+    if y is None:
+        y, ldy = torch.empty((T, H, D), dtype=_f32, device=x.device), H * D
+    else:
+        ldy = _rows(y, name + "_out", index, (T, H, D))[3]
+    at_gain = None if gain is None else _at(gain, name + "_gain", _f32, (D,), index)
+    return y, at_gain, (H, x.data_ptr(), ld, y.data_ptr(), ldy)
 
 
 def head_norm_rope(q, k, positions, inv_freq, q_gain=None, k_gain=None, eps=1e-6, interleaved=False,
@@ -451,39 +468,19 @@ def head_norm_rope(q, k, positions, inv_freq, q_gain=None, k_gain=None, eps=1e-6
     first = k if q is None else q
     if first is None:
         raise ValueError("q or k must be given")
-    shape, args, outs, gains = None, [], [], []
-    for x, y, gain, name in ((q, q_out, q_gain, "q"), (k, k_out, k_gain, "k")):
-        if x is None:
-            if y is not None or gain is not None:
-                raise ValueError(f"{name}_out and {name}_gain need {name}")
-            args.append((0, None, 0, None, 0))
-            outs.append(None)
-            gains.append(None)
-            continue
-        T, H, D, ld = _rows(x, name)
-        if shape is None:
-            shape = (T, D)
-        elif shape != (T, D):
-            raise ValueError(f"{name}: {T} rows of {D} != {shape[0]} rows of {shape[1]}")
-        if y is None:
-            y, ldy = torch.empty((T, H, D), dtype=torch.float32, device=x.device), H * D
-        else:
-            ldy = _rows(y, name + "_out", (T, H, D))[3]
-        gains.append(None if gain is None else _at(gain, name + "_gain", torch.float32, (D,)))
-        outs.append(y)
-        args.append((H, x.data_ptr(), ld, y.data_ptr(), ldy))
-    T, D = shape
+    T, _, D, _ = _rows(first, "k" if q is None else "q")
+    index = first.get_device()
+    q_out, q_gain_at, (QH, xq, ldq, yq, ldqo) = _rope_side(q, q_out, q_gain, "q", T, D, index)
+    k_out, k_gain_at, (KH, xk, ldk, yk, ldko) = _rope_side(k, k_out, k_gain, "k", T, D, index)
     rot, at_pos, at_inv = 0, None, None
     if inv_freq is not None:
         rot = 2 * inv_freq.numel()
-        at_inv = _at(inv_freq, "inv_freq", torch.float32, (rot // 2,))
-        at_pos = _at(positions, "positions", torch.int32, (T,))
-    _same_device(first, k, q_out, k_out, positions, inv_freq, q_gain, k_gain)
-    desc = Rope(gains[0], gains[1], eps, rot, 1 if interleaved else 0, at_inv)
-    (QH, xq, ldq, yq, ldqo), (KH, xk, ldk, yk, ldko) = args
-    _call(lib.gq4_head_norm_rope, "gq4_head_norm_rope", first, stream, T, QH, KH, D, desc, at_pos, xq, ldq, xk, ldk,
+        at_inv = _at(inv_freq, "inv_freq", _f32, (rot // 2,), index)
+        at_pos = _at(positions, "positions", _i32, (T,), index)
+    _call(lib.gq4_head_norm_rope, "gq4_head_norm_rope", index, stream, T, QH, KH, D,
+          Rope(q_gain_at, k_gain_at, eps, rot, 1 if interleaved else 0, at_inv), at_pos, xq, ldq, xk, ldk,
           yq, ldqo, yk, ldko)
-    return outs[0], outs[1]
+    return q_out, k_out
 
 
 def kv_cache(n_pages, kv_heads, page_size, head_dim, group_size, device=None):
@@ -498,47 +495,45 @@ def kv_cache(n_pages, kv_heads, page_size, head_dim, group_size, device=None):
 
 
 def _cache(Kq, K_sz, Vq, V_sz, group_size):
+    """The cache's descriptor and device."""
     _need(Kq, "Kq", _WORDS)
     if Kq.dim() != 4:
         raise ValueError("Kq must be [n_pages, kv_heads, page_size, head_dim/8]")
     shape = P, H, S, W = Kq.shape
     if group_size <= 0 or (8 * W) % group_size != 0:
         raise ValueError("head_dim must be a multiple of group_size")
-    sz = (P, H, S, 8 * W // group_size, 2)
-    c = KVCache(P, S, H, 8 * W, group_size, Kq.data_ptr(), _at(K_sz, "K_sz", torch.float32, sz),
-                _at(Vq, "Vq", Kq.dtype, shape), _at(V_sz, "V_sz", torch.float32, sz))
-    _same_device(Kq, K_sz, Vq, V_sz)
-    return c
+    sz, index = (P, H, S, 8 * W // group_size, 2), Kq.get_device()
+    return KVCache(P, S, H, 8 * W, group_size, Kq.data_ptr(), _at(K_sz, "K_sz", _f32, sz, index),
+                   _at(Vq, "Vq", Kq.dtype, shape, index), _at(V_sz, "V_sz", _f32, sz, index)), index
 
 
 def kv_append(k, v, slots, Kq, K_sz, Vq, V_sz, group_size, stream=None):
     """Quantise rows k, v [T, kv_heads, D] into the cache at slots int32 [T] (gq4_kv_append;
     negative slots are skipped)."""
-    c = _cache(Kq, K_sz, Vq, V_sz, group_size)
-    T, H, D, ldk = _rows(k, "k")
+    c, index = _cache(Kq, K_sz, Vq, V_sz, group_size)
+    T, H, D, ldk = _rows(k, "k", index)
     if (H, D) != (c.kv_heads, c.head_dim):
         raise ValueError(f"k: {H} heads of {D} != {c.kv_heads} heads of {c.head_dim}")
-    ldv = _rows(v, "v", (T, H, D))[3]
-    at_slots = _at(slots, "slots", torch.int32, (T,))
-    _same_device(Kq, k, v, slots)
-    _call(lib.gq4_kv_append, "gq4_kv_append", Kq, stream, T, c, k.data_ptr(), ldk, v.data_ptr(), ldv, at_slots)
+    ldv = _rows(v, "v", index, (T, H, D))[3]
+    at_slots = _at(slots, "slots", _i32, (T,), index)
+    _call(lib.gq4_kv_append, "gq4_kv_append", index, stream, T, c, k.data_ptr(), ldk, v.data_ptr(), ldv, at_slots)
 
 
 def kv_gather(slots, Kq, K_sz, Vq, V_sz, group_size, k_out=None, v_out=None, stream=None):
     """(k, v) f32 [T, kv_heads, D] of the cache rows at slots (gq4_kv_gather; rows of negative slots
     are left as they were, so pass k_out and v_out where there are some)."""
-    c = _cache(Kq, K_sz, Vq, V_sz, group_size)
+    c, index = _cache(Kq, K_sz, Vq, V_sz, group_size)
     _need(slots, "slots", _I32)
     if slots.dim() != 1:
         raise ValueError("slots must be [T]")
-    shape = (slots.shape[0], c.kv_heads, c.head_dim)
+    T = slots.shape[0]
+    at_slots, shape = _at(slots, "slots", _i32, (T,), index), (T, c.kv_heads, c.head_dim)
     if k_out is None:
-        k_out = torch.empty(shape, dtype=torch.float32, device=Kq.device)
+        k_out = torch.empty(shape, dtype=_f32, device=Kq.device)
     if v_out is None:
-        v_out = torch.empty(shape, dtype=torch.float32, device=Kq.device)
-    at_k, at_v = _at(k_out, "k_out", torch.float32, shape), _at(v_out, "v_out", torch.float32, shape)
-    _same_device(Kq, slots, k_out, v_out)
-    _call(lib.gq4_kv_gather, "gq4_kv_gather", Kq, stream, shape[0], c, slots.data_ptr(), at_k, at_v)
+        v_out = torch.empty(shape, dtype=_f32, device=Kq.device)
+    _call(lib.gq4_kv_gather, "gq4_kv_gather", index, stream, T, c, at_slots,
+          _at(k_out, "k_out", _f32, shape, index), _at(v_out, "v_out", _f32, shape, index))
     return k_out, v_out
 
 
@@ -550,32 +545,29 @@ def kv_plan(past_lens, new_lens, page_table, free_pages, free_count, n_tokens, p
     _need(past_lens, "past_lens", _I32)
     if past_lens.dim() != 1:
         raise ValueError("past_lens must be [B]")
-    B = past_lens.shape[0]
+    B, index = past_lens.shape[0], past_lens.get_device()
     _need(page_table, "page_table", _I32)
     if page_table.dim() != 2 or page_table.shape[0] != B:
         raise ValueError("page_table must be [B, max_pages]")
     if n_tokens < 0:
         raise ValueError("n_tokens must not be negative")
-    _need(free_pages, "free_pages", _I32)
-    at_new, at_count = _at(new_lens, "new_lens", torch.int32, (B,)), _at(free_count, "free_count", torch.int32, (1,))
-    given = (("seq_lens", seq_lens, B), ("query_start", query_start, B + 1), ("positions", positions, n_tokens),
-             ("slots", slots, n_tokens), ("free_count_out", free_count_out, 1))
+    at_table = _at(page_table, "page_table", _i32, page_table.shape, index)
+    at_free = _at(free_pages, "free_pages", _i32, free_pages.shape, index)
+    at_new, at_count = _at(new_lens, "new_lens", _i32, (B,), index), _at(free_count, "free_count", _i32, (1,), index)
+    sizes = [B, B + 1, n_tokens, n_tokens, 1]
+    outs = [seq_lens, query_start, positions, slots, free_count_out]
     # what is not given is a stretch of one allocation
-    spare = iter(torch.empty(sum(n for _, t, n in given if t is None), dtype=torch.int32, device=past_lens.device)
-                 .split([n for _, t, n in given if t is None]))
-    outs, ptrs = [], []
-    for name, t, n in given:
-        if t is None:
-            t = next(spare)
-            ptrs.append(t.data_ptr())
-        else:
-            ptrs.append(_at(t, name, torch.int32, (n,)))
-        outs.append(t)
-    _same_device(past_lens, new_lens, page_table, free_pages, free_count, *outs)
-    lens, starts, pos, slt, left = ptrs
-    _call(lib.gq4_kv_plan, "gq4_kv_plan", past_lens, stream, B, n_tokens, page_size, page_table.shape[1],
-          free_pages.numel(), past_lens.data_ptr(), at_new, page_table.data_ptr(), free_pages.data_ptr(), at_count,
-          left, lens, starts, pos, slt)
+    missing = [i for i in range(5) if outs[i] is None]
+    if missing:
+        lens = [sizes[i] for i in missing]
+        parts = torch.empty(sum(lens), dtype=_i32, device=past_lens.device).split_with_sizes(lens)
+        for i, part in zip(missing, parts):
+            outs[i] = part
+    lens, starts, pos, slt, left = [_at(t, name, _i32, (n,), index) for t, name, n in
+                                    zip(outs, ("seq_lens", "query_start", "positions", "slots", "free_count_out"),
+                                        sizes)]
+    _call(lib.gq4_kv_plan, "gq4_kv_plan", index, stream, B, n_tokens, page_size, page_table.shape[1],
+          free_pages.numel(), past_lens.data_ptr(), at_new, at_table, at_free, at_count, left, lens, starts, pos, slt)
     return tuple(outs)
 
 
@@ -589,33 +581,34 @@ def kv_attention(q, query_start, seq_lens, page_table, Kq, K_sz, Vq, V_sz, group
     rows query_start[b]..query_start[b+1], its seq_lens[b] keys are in the pages of page_table row b.
     ``workspace``: a CUDA tensor of at least kv_attention_workspace_bytes(T, heads, kv_heads, D) bytes
     (allocated when None).  ``out`` rows of no request are left as they were."""
-    c = _cache(Kq, K_sz, Vq, V_sz, group_size)
-    T, H, D, ldq = _rows(q, "q")
+    c, index = _cache(Kq, K_sz, Vq, V_sz, group_size)
+    T, H, D, ldq = _rows(q, "q", index)
     if D != c.head_dim:
         raise ValueError(f"q: head_dim {D} != {c.head_dim}")
     _need(seq_lens, "seq_lens", _I32)
     if seq_lens.dim() != 1:
         raise ValueError("seq_lens must be [B]")
     B = seq_lens.shape[0]
-    at_start = _at(query_start, "query_start", torch.int32, (B + 1,))
     _need(page_table, "page_table", _I32)
     if page_table.dim() != 2 or page_table.shape[0] != B:
         raise ValueError("page_table must be [B, max_pages]")
+    at_lens, at_start = _at(seq_lens, "seq_lens", _i32, (B,), index), \
+        _at(query_start, "query_start", _i32, (B + 1,), index)
+    at_table = _at(page_table, "page_table", _i32, page_table.shape, index)
     if out is None:
-        out, ldo = torch.empty((T, H, D), dtype=torch.float32, device=q.device), H * D
+        out, ldo = torch.empty((T, H, D), dtype=_f32, device=q.device), H * D
     else:
-        ldo = _rows(out, "out", (T, H, D))[3]
+        ldo = _rows(out, "out", index, (T, H, D))[3]
     ours = workspace is None
     if ours:
-        workspace = torch.empty(kv_attention_workspace_bytes(T, H, c.kv_heads, D), dtype=torch.uint8,
+        workspace = torch.empty(lib.gq4_kv_attention_workspace_bytes(T, H, c.kv_heads, D), dtype=torch.uint8,
                                 device=q.device)
-    elif not (isinstance(workspace, torch.Tensor) and workspace.is_cuda and workspace.is_contiguous()):
-        raise ValueError("workspace must be a contiguous CUDA tensor")
-    _same_device(Kq, q, query_start, seq_lens, page_table, out, workspace)
-    _call(lib.gq4_kv_attention, "gq4_kv_attention", Kq, stream, B, T, H, page_table.shape[1], max_query, max_len, c,
-          q.data_ptr(), ldq, at_start, seq_lens.data_ptr(), page_table.data_ptr(), scale, window, out.data_ptr(), ldo,
+    elif not (isinstance(workspace, torch.Tensor) and workspace.get_device() == index and workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous CUDA tensor on the others' device")
+    _call(lib.gq4_kv_attention, "gq4_kv_attention", index, stream, B, T, H, page_table.shape[1], max_query, max_len, c,
+          q.data_ptr(), ldq, at_start, at_lens, at_table, scale, window, out.data_ptr(), ldo,
           workspace.data_ptr(), workspace.nbytes)
-    if ours and stream is not None and stream.cuda_stream != _raw_stream(q.get_device()):
+    if ours and stream is not None and stream.cuda_stream != _raw_stream(index):
         workspace.record_stream(stream)   # freed here, in use there
     return out
 
