@@ -231,7 +231,9 @@ __global__ void __launch_bounds__(kGatherThreads<J>) gather_kernel(const __grid_
 // the tile's tokens and granted pages: a token finds its request by bisection
 // of the tile's first rows.  So no CTA waits for another, unless lengths or
 // the count are advanced in place: then the CTAs are one cluster, which meets
-// after the tile is read and before it is overwritten.
+// after the tile is read and before it is overwritten.  Latency-bound (a few
+// kB): 64 requests of one token 4.2 us, 2000 requests of up to 256 tokens (257k
+// tokens, 2.1 MB written) 10.5 us.
 // ---------------------------------------------------------------------------
 constexpr int kPlanThreads = 1024;
 

@@ -13,10 +13,10 @@
 // exchanged by shuffles within 32 lanes; above 128 dims the partner lies in
 // another register of another lane and is loaded a second time (a
 // first-level cache hit).
-//   8191 tokens of 40 heads of 128: 63 us, 335 MB at 5.3 TB/s (0.78 of a
-// copy's).  Occupancy is what counts: one row per thread under way, 8 CTAs
-// on an SM; two rows under way take 72 us, four 82 us, and without sines and
-// cosines it still takes 62 us.
+//   8191 tokens of 40 heads of 128: 57 us, 335 MB at 5.9 TB/s (0.87 of a
+// copy's).  What counts is few instructions (135 per float4 and warp) and full
+// occupancy: 195 instructions took 63 us, and two rows of loads under way per
+// thread, at fewer CTAs per SM, 72.
 //
 // Angles: pos * inv_freq is a 31-bit by 24-bit product; in binary64 its error
 // is below 2^-22 of a radian at any position.  It is reduced modulo 2 pi in
@@ -35,7 +35,7 @@ struct RopeParams {
     RopeCall c;
     int rows;       // q and k heads of a token
     int splits;     // CTAs per token
-    int lpr;        // lanes per row
+    float inv_d;    // 1 / D
 };
 
 __device__ __forceinline__ float2 sin_cos_of(int pos, float inv_freq)
@@ -79,26 +79,35 @@ __device__ __forceinline__ float4 scaled(float4 a, float r, float4 g)
     return make_float4(a.x * r * g.x, a.y * r * g.y, a.z * r * g.z, a.w * r * g.w);
 }
 
-// CH: float4 per lane of a row.
-template <int CH>
+// 1 / sqrt(x): the approximation (2 ulp) and a Newton step.
+__device__ __forceinline__ float inv_sqrt(float x)
+{
+    const float r = rsqrtf(x);
+    const float e = fmaf(-x * r, r, 1.0f);
+    return fabsf(e) < 0.5f ? fmaf(0.5f * r, e, r) : r;   // (x = 0, infinite: r as it is)
+}
+
+// CH: float4 per lane of a row; LPR: lanes of a row.
+template <int CH, int LPR>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p)
 {
+    constexpr int PER = kRopeThreads / LPR;            // rows at once
     __shared__ alignas(16) float2 sc[GQ4_MAX_HEAD_DIM / 2];
     const RopeCall &c = p.c;
     const int t = blockIdx.x / p.splits, part = blockIdx.x - t * p.splits;
     const int half = c.rot >> 1;
-    const int lpr = p.lpr, per = kRopeThreads / lpr;   // rows at once
-    const int l = threadIdx.x & (lpr - 1);
+    const int l = threadIdx.x & (LPR - 1);
     const int d4 = c.D >> 2, rot4 = c.rot >> 2, half4 = c.rot >> 3;
+    const float *qx = c.x[0] + (size_t)t * c.ldx[0], *kx = c.x[1] + (size_t)t * c.ldx[1];
+    float *qy = c.y[0] + (size_t)t * c.ldy[0], *ky = c.y[1] + (size_t)t * c.ldy[1];
+    const bool norm = c.gain[0] || c.gain[1];
     bool first_rows = true;
     // every thread takes the same number of turns (the shuffles below)
-    for (int row0 = part * per; row0 < p.rows; row0 += per * p.splits) {
-        const int row = row0 + threadIdx.x / lpr;
-        const int side = row >= p.rows ? -1 : row >= c.heads[0] ? 1 : 0;   // q, k or no row
-        const bool k = side == 1;
-        const size_t head = (size_t)(k ? row - c.heads[0] : row) * c.D;
-        const Row<CH> x = load_row<CH>(c, (k ? c.x[1] + (size_t)t * c.ldx[1] : c.x[0] + (size_t)t * c.ldx[0]) + head,
-                                       side >= 0, l);
+    for (int row0 = part * PER; row0 < p.rows; row0 += PER * p.splits) {
+        const int row = row0 + threadIdx.x / LPR;
+        const bool in = row < p.rows, k = row >= c.heads[0];
+        const int head = (k ? row - c.heads[0] : row) * c.D;
+        const Row<CH> x = load_row<CH>(c, (k ? kx : qx) + head, in, l);
         if (first_rows) {
             if (half > 0) {
                 const int pos = __ldg(c.positions + t);
@@ -108,23 +117,24 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
             first_rows = false;
         }
         const float4 *gain = reinterpret_cast<const float4 *>(k ? c.gain[1] : c.gain[0]);
-        float4 *y = reinterpret_cast<float4 *>((k ? c.y[1] + (size_t)t * c.ldy[1] : c.y[0] + (size_t)t * c.ldy[0]) + head);
+        float4 *y = reinterpret_cast<float4 *>((k ? ky : qy) + head);
         float r = 1.0f;
-        if (c.gain[0] || c.gain[1]) {  // uniform: the whole warp shuffles
+        if (norm) {  // uniform: the whole warp shuffles
             float s = 0.0f;
 #pragma unroll
             for (int j = 0; j < CH; ++j) {
                 const float4 v = x.v[j];
                 s += v.x * v.x + v.y * v.y + v.z * v.z + v.w * v.w;
             }
-            for (int o = lpr >> 1; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-            r = 1.0f / sqrtf(s / (float)c.D + c.eps);
+#pragma unroll
+            for (int o = LPR >> 1; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+            r = inv_sqrt(fmaf(s, p.inv_d, c.eps));
         }
         __syncwarp();  // in place: every lane of the row has read before any writes
 #pragma unroll
         for (int j = 0; j < CH; ++j) {
             const int i = l + j * 32;
-            const bool live = side >= 0 && i < d4, turned = live && i < rot4;
+            const bool live = in && i < d4, turned = live && i < rot4;
             float4 a = gain && live ? scaled(x.v[j], r, __ldg(gain + i)) : x.v[j];
             if (c.interleaved) {
                 if (turned) {
@@ -137,10 +147,10 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
                 const int other = first ? i + half4 : i - half4;
                 float4 b;
                 if (CH == 1) {  // the whole warp shuffles
-                    b.x = __shfl_sync(0xffffffffu, a.x, other, lpr);
-                    b.y = __shfl_sync(0xffffffffu, a.y, other, lpr);
-                    b.z = __shfl_sync(0xffffffffu, a.z, other, lpr);
-                    b.w = __shfl_sync(0xffffffffu, a.w, other, lpr);
+                    b.x = __shfl_sync(0xffffffffu, a.x, other, LPR);
+                    b.y = __shfl_sync(0xffffffffu, a.y, other, LPR);
+                    b.z = __shfl_sync(0xffffffffu, a.z, other, LPR);
+                    b.w = __shfl_sync(0xffffffffu, a.w, other, LPR);
                 } else {
                     b = gain && turned ? scaled(x.w[j], r, __ldg(gain + other)) : x.w[j];
                 }
@@ -167,19 +177,21 @@ cudaError_t launch_rope(const RopeCall &call, cudaStream_t stream)
     const int d4 = call.D / 4;
     int lpr = 2;
     while (lpr < d4 && lpr < 32) lpr *= 2;
-    p.lpr = lpr;
+    p.inv_d = 1.0f / (float)call.D;
     const int per = kRopeThreads / lpr;
     // few tokens: their heads over several CTAs, until the GPU has two each
     p.splits = 1;
     while (p.splits * per < p.rows && (long long)call.T * p.splits < 2 * 152) ++p.splits;
     const long long grid = (long long)call.T * p.splits;
     if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
-    if (d4 <= 32)
-        rope_kernel<1><<<(unsigned)grid, kRopeThreads, 0, stream>>>(p);
-    else if (d4 <= 64)
-        rope_kernel<2><<<(unsigned)grid, kRopeThreads, 0, stream>>>(p);
-    else
-        rope_kernel<4><<<(unsigned)grid, kRopeThreads, 0, stream>>>(p);
+    auto run = [&](auto kern) { kern<<<(unsigned)grid, kRopeThreads, 0, stream>>>(p); };
+    if (d4 > 64) run(rope_kernel<4, 32>);
+    else if (d4 > 32) run(rope_kernel<2, 32>);
+    else if (lpr == 32) run(rope_kernel<1, 32>);
+    else if (lpr == 16) run(rope_kernel<1, 16>);
+    else if (lpr == 8) run(rope_kernel<1, 8>);
+    else if (lpr == 4) run(rope_kernel<1, 4>);
+    else run(rope_kernel<1, 2>);
     return cudaGetLastError();
 }
 
