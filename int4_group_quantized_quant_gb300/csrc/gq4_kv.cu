@@ -49,9 +49,10 @@ struct RowAt {
 // takes as many rows as fit, so that a group's minimum and maximum are a
 // shuffle away.  The K and V rows of a few tokens are one CTA's, numbered in
 // 32 bits; a row's loads do not wait for its slot.  Floor: 4 bytes read and
-// 0.5 + 8/gs written per value; 16381 tokens of 8 heads of 128 take 35 us
-// (153 MB, 4.4 TB/s).  What is left is instructions: 225 per word and warp,
-// a fifth of them the group's two divisions and reciprocal.
+// 0.5 + 8/gs written per value; 16381 tokens of 8 heads of 128 take 30 us
+// (153 MB, 5.1 TB/s).  What is left is instructions: 194 per word and warp, a
+// quarter of them the group's two divisions and reciprocal (with the lanes of
+// a group a run-time number it was 225, and 35 us).
 // ---------------------------------------------------------------------------
 constexpr int kAppendThreads = 256;
 constexpr int kAppendUnroll = 2;   // rows per lane whose loads are issued together
@@ -63,20 +64,21 @@ struct AppendParams {
     const int32_t *slots;
     int T, tokens;           // all, and per CTA
     int shift;               // log2 of the page size
-    int L;                   // lanes per group
     int total;               // slots of the pool
     uint32_t page_codes, page_sz;   // bytes per page and head
     uint32_t per_2h;         // divides a CTA's rows by 2 heads
 };
 
-template <int J>
+// J = head_dim / 32; L: lanes per group.
+template <int J, int L>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendParams p)
 {
     constexpr int WPR = 4 * J, RPW = 32 / WPR;   // words per row, rows per warp
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int in_warp = lane / WPR, w = lane - in_warp * WPR;
-    const int H = p.c.kv_heads, G = 8 * WPR / p.c.group_size;
-    const int group = w / p.L, pos = w - group * p.L;
+    constexpr int G = WPR / L;
+    const int H = p.c.kv_heads;
+    const int group = w / L, pos = w - group * L;
     const int t0 = blockIdx.x * p.tokens;
     const int n_rows = min(p.tokens, p.T - t0) * 2 * H;
     constexpr int kStep = kAppendThreads / 32 * RPW;
@@ -112,7 +114,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
                 lo = min_nan(lo, v[i]);
                 hi = max_nan(hi, v[i]);
             }
-            segment_min_max(lo, hi, pos, lane - pos, p.L);
+            segment_min_max(lo, hi, pos, lane - pos, L);
             int bad;
             const GroupMap m = group_map(lo, hi, bad);
             uint32_t word = bad ? 0u : quantize_word(v, m);
@@ -385,16 +387,24 @@ cudaError_t launch_kv_append(int T, const gq4_kv_cache &c, const float *k, int l
     p.page_codes = (uint32_t)(c.page_size * c.head_dim / 2);
     p.page_sz = (uint32_t)(c.page_size * (c.head_dim / c.group_size) * 8);
     p.per_2h = divide_by(2 * c.kv_heads);
-    p.L = c.group_size / 8;
     // a lane takes two words of a long prompt; one while tokens are few, so
     // that they spread over the GPU
     p.tokens = tokens_per_cta(2 * c.kv_heads * (c.head_dim / 8), T >= 1024 ? 2 * kAppendUnroll : 1);
     const unsigned grid = (unsigned)((T + p.tokens - 1) / p.tokens);
-    switch (c.head_dim) {
-    case 64: append_kernel<2><<<grid, kAppendThreads, 0, stream>>>(p); break;
-    case 96: append_kernel<3><<<grid, kAppendThreads, 0, stream>>>(p); break;
-    case 128: append_kernel<4><<<grid, kAppendThreads, 0, stream>>>(p); break;
-    default: append_kernel<8><<<grid, kAppendThreads, 0, stream>>>(p); break;
+    auto run = [&](auto kern) { kern<<<grid, kAppendThreads, 0, stream>>>(p); };
+    switch (c.head_dim * 16 + c.group_size / 32) {
+    case 64 * 16 + 1: run(append_kernel<2, 4>); break;
+    case 64 * 16 + 2: run(append_kernel<2, 8>); break;
+    case 96 * 16 + 1: run(append_kernel<3, 4>); break;
+    case 96 * 16 + 3: run(append_kernel<3, 12>); break;
+    case 128 * 16 + 1: run(append_kernel<4, 4>); break;
+    case 128 * 16 + 2: run(append_kernel<4, 8>); break;
+    case 128 * 16 + 4: run(append_kernel<4, 16>); break;
+    case 256 * 16 + 1: run(append_kernel<8, 4>); break;
+    case 256 * 16 + 2: run(append_kernel<8, 8>); break;
+    case 256 * 16 + 4: run(append_kernel<8, 16>); break;
+    case 256 * 16 + 8: run(append_kernel<8, 32>); break;
+    default: return cudaErrorInvalidValue;
     }
     return cudaGetLastError();
 }
