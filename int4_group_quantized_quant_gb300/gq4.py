@@ -394,7 +394,6 @@ def embedding(ids, Bq, scales, zeros, group_size, out=None, stream=None):
 # Between the QKV product and the output projection
 # ---------------------------------------------------------------------------
 
-_I32 = (torch.int32,)
 _f32, _i32 = torch.float32, torch.int32
 # the current device, and its current stream's handle without a Stream object around it, where torch has them
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
@@ -419,6 +418,21 @@ def _at(t, name, dtype, shape, index):
         _need(t, name, (dtype,), shape)
         raise ValueError(f"{name} is on {t.device}, the others on cuda:{index}")
     return t.data_ptr()
+
+
+def _device(t, name):
+    """The CUDA device that a call's first tensor names."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{name} must be a CUDA tensor (no CPU path exists)")
+    return index
+
+
+def _width(t):
+    """Columns of a matrix (-1: not one, which no shape matches)."""
+    return t.shape[1] if isinstance(t, torch.Tensor) and t.dim() == 2 else -1
 
 
 def _rows(t, name, index=None, heads_dim=None):
@@ -496,15 +510,17 @@ def kv_cache(n_pages, kv_heads, page_size, head_dim, group_size, device=None):
 
 def _cache(Kq, K_sz, Vq, V_sz, group_size):
     """The cache's descriptor and device."""
-    _need(Kq, "Kq", _WORDS)
+    index, dtype = _device(Kq, "Kq"), Kq.dtype
     if Kq.dim() != 4:
         raise ValueError("Kq must be [n_pages, kv_heads, page_size, head_dim/8]")
+    if dtype is not _i32:
+        _need(Kq, "Kq", _WORDS)
     shape = P, H, S, W = Kq.shape
     if group_size <= 0 or (8 * W) % group_size != 0:
         raise ValueError("head_dim must be a multiple of group_size")
-    sz, index = (P, H, S, 8 * W // group_size, 2), Kq.get_device()
-    return KVCache(P, S, H, 8 * W, group_size, Kq.data_ptr(), _at(K_sz, "K_sz", _f32, sz, index),
-                   _at(Vq, "Vq", Kq.dtype, shape, index), _at(V_sz, "V_sz", _f32, sz, index)), index
+    sz = (P, H, S, 8 * W // group_size, 2)
+    return KVCache(P, S, H, 8 * W, group_size, _at(Kq, "Kq", dtype, shape, index), _at(K_sz, "K_sz", _f32, sz, index),
+                   _at(Vq, "Vq", dtype, shape, index), _at(V_sz, "V_sz", _f32, sz, index)), index
 
 
 def kv_append(k, v, slots, Kq, K_sz, Vq, V_sz, group_size, stream=None):
@@ -523,10 +539,8 @@ def kv_gather(slots, Kq, K_sz, Vq, V_sz, group_size, k_out=None, v_out=None, str
     """(k, v) f32 [T, kv_heads, D] of the cache rows at slots (gq4_kv_gather; rows of negative slots
     are left as they were, so pass k_out and v_out where there are some)."""
     c, index = _cache(Kq, K_sz, Vq, V_sz, group_size)
-    _need(slots, "slots", _I32)
-    if slots.dim() != 1:
-        raise ValueError("slots must be [T]")
-    T = slots.shape[0]
+    _device(slots, "slots")
+    T = slots.numel()
     at_slots, shape = _at(slots, "slots", _i32, (T,), index), (T, c.kv_heads, c.head_dim)
     if k_out is None:
         k_out = torch.empty(shape, dtype=_f32, device=Kq.device)
@@ -542,32 +556,30 @@ def kv_plan(past_lens, new_lens, page_table, free_pages, free_count, n_tokens, p
     """A step's pages, positions and slots from the requests' lengths (gq4_kv_plan); page_table int32
     [B, max_pages] is extended in place.  Returns (seq_lens, query_start, positions, slots,
     free_count_out); pass seq_lens=past_lens and free_count_out=free_count to advance them in place."""
-    _need(past_lens, "past_lens", _I32)
-    if past_lens.dim() != 1:
-        raise ValueError("past_lens must be [B]")
-    B, index = past_lens.shape[0], past_lens.get_device()
-    _need(page_table, "page_table", _I32)
-    if page_table.dim() != 2 or page_table.shape[0] != B:
-        raise ValueError("page_table must be [B, max_pages]")
+    index, B = _device(past_lens, "past_lens"), past_lens.numel()
     if n_tokens < 0:
         raise ValueError("n_tokens must not be negative")
-    at_table = _at(page_table, "page_table", _i32, page_table.shape, index)
-    at_free = _at(free_pages, "free_pages", _i32, free_pages.shape, index)
-    at_new, at_count = _at(new_lens, "new_lens", _i32, (B,), index), _at(free_count, "free_count", _i32, (1,), index)
-    sizes = [B, B + 1, n_tokens, n_tokens, 1]
+    width, n_free = _width(page_table), free_pages.numel()
+    at_past, at_new = _at(past_lens, "past_lens", _i32, (B,), index), _at(new_lens, "new_lens", _i32, (B,), index)
+    at_table = _at(page_table, "page_table", _i32, (B, width), index)
+    at_free, at_count = _at(free_pages, "free_pages", _i32, (n_free,), index), \
+        _at(free_count, "free_count", _i32, (1,), index)
+    sizes = (B, B + 1, n_tokens, n_tokens, 1)
     outs = [seq_lens, query_start, positions, slots, free_count_out]
+    ptrs = [None if t is None else _at(t, name, _i32, (n,), index) for t, name, n in
+            zip(outs, ("seq_lens", "query_start", "positions", "slots", "free_count_out"), sizes)]
     # what is not given is a stretch of one allocation
     missing = [i for i in range(5) if outs[i] is None]
     if missing:
         lens = [sizes[i] for i in missing]
-        parts = torch.empty(sum(lens), dtype=_i32, device=past_lens.device).split_with_sizes(lens)
-        for i, part in zip(missing, parts):
-            outs[i] = part
-    lens, starts, pos, slt, left = [_at(t, name, _i32, (n,), index) for t, name, n in
-                                    zip(outs, ("seq_lens", "query_start", "positions", "slots", "free_count_out"),
-                                        sizes)]
-    _call(lib.gq4_kv_plan, "gq4_kv_plan", index, stream, B, n_tokens, page_size, page_table.shape[1],
-          free_pages.numel(), past_lens.data_ptr(), at_new, at_table, at_free, at_count, left, lens, starts, pos, slt)
+        spare = torch.empty(sum(lens), dtype=_i32, device=past_lens.device)
+        at = spare.data_ptr()
+        for i, part in zip(missing, spare.split_with_sizes(lens)):
+            outs[i], ptrs[i] = part, at
+            at += 4 * sizes[i]
+    lens, starts, pos, slt, left = ptrs
+    _call(lib.gq4_kv_plan, "gq4_kv_plan", index, stream, B, n_tokens, page_size, width, n_free, at_past, at_new,
+          at_table, at_free, at_count, left, lens, starts, pos, slt)
     return tuple(outs)
 
 
@@ -585,16 +597,11 @@ def kv_attention(q, query_start, seq_lens, page_table, Kq, K_sz, Vq, V_sz, group
     T, H, D, ldq = _rows(q, "q", index)
     if D != c.head_dim:
         raise ValueError(f"q: head_dim {D} != {c.head_dim}")
-    _need(seq_lens, "seq_lens", _I32)
-    if seq_lens.dim() != 1:
-        raise ValueError("seq_lens must be [B]")
-    B = seq_lens.shape[0]
-    _need(page_table, "page_table", _I32)
-    if page_table.dim() != 2 or page_table.shape[0] != B:
-        raise ValueError("page_table must be [B, max_pages]")
+    _device(seq_lens, "seq_lens")
+    B, width = seq_lens.numel(), _width(page_table)
     at_lens, at_start = _at(seq_lens, "seq_lens", _i32, (B,), index), \
         _at(query_start, "query_start", _i32, (B + 1,), index)
-    at_table = _at(page_table, "page_table", _i32, page_table.shape, index)
+    at_table = _at(page_table, "page_table", _i32, (B, width), index)
     if out is None:
         out, ldo = torch.empty((T, H, D), dtype=_f32, device=q.device), H * D
     else:
@@ -605,7 +612,7 @@ def kv_attention(q, query_start, seq_lens, page_table, Kq, K_sz, Vq, V_sz, group
                                 device=q.device)
     elif not (isinstance(workspace, torch.Tensor) and workspace.get_device() == index and workspace.is_contiguous()):
         raise ValueError("workspace must be a contiguous CUDA tensor on the others' device")
-    _call(lib.gq4_kv_attention, "gq4_kv_attention", index, stream, B, T, H, page_table.shape[1], max_query, max_len, c,
+    _call(lib.gq4_kv_attention, "gq4_kv_attention", index, stream, B, T, H, width, max_query, max_len, c,
           q.data_ptr(), ldq, at_start, at_lens, at_table, scale, window, out.data_ptr(), ldo,
           workspace.data_ptr(), workspace.nbytes)
     if ours and stream is not None and stream.cuda_stream != _raw_stream(index):
