@@ -79,7 +79,9 @@ struct SplitParams {
     AttnCall a;
     float *part;        // [grid][2][rows][D + 2] partial sums
     float *head;        // [grid][8 warps][rows][D + 2] a warp's first, cut unit
-    int4 *desc;         // [grid] the cut unit that starts in this CTA
+    int4 *desc;         // [grid][2] the cut unit that starts in this CTA: (first token, rows, kv head,
+                        // row block), (last CTA or -1, slot)
+    int R;              // query heads per kv head
     int grid;
 };
 
@@ -244,11 +246,10 @@ struct Work {
 };
 
 template <int ROWS>
-__device__ __forceinline__ Work work_of(const AttnCall &p, const AttnRequest &r)
+__device__ __forceinline__ Work work_of(const AttnCall &p, const AttnRequest &r, int R)
 {
     Work w{0, 0, 0, 0};
     if (r.bad || r.n == 0 || r.len == 0 || prompt_takes(p, r)) return w;
-    const int R = p.heads / p.c.kv_heads;
     const int first = attn_first(p, max(r.len - r.n, -1));
     w.step0 = first / kStageKeys;
     w.steps = (r.len + kStageKeys - 1) / kStageKeys - w.step0;
@@ -312,7 +313,7 @@ __device__ __forceinline__ void carry(float (&o)[NB][J][4], float (&t0)[NB][J][4
 // none), and which it is.
 struct Segment {
     long long start;
-    int b, unit, steps;      // request, unit of it, stages of the unit
+    int steps;               // its stages
     int row0, rows;          // the request's first token and its query rows per kv head
     int h, rb;               // kv head, row block
 };
@@ -327,38 +328,45 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
     __shared__ union {
         struct {
             long long sums[kWarps];
-            long long pos[kWarps + 1], at[kWarps + 1];   // where warps start: of all stages, of request b's
-            int b[kWarps + 1], special;
+            int special;
         } start;
         Segment seg[2 * kWarps];            // a warp's first and last segment, where cut
     } s;
+    __shared__ long long s_bound[kWarps + 1];   // where the warps' ranges start and the last ends
     const AttnCall &a = p.a;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, c = lane & 3;
-    const int H = a.c.kv_heads, R = a.heads / H;
+    const int H = a.c.kv_heads, R = p.R;
+    // the requests of a tile of kThreads, until the copies start: the stages up to and with each,
+    // and (first token, queries, length, stages of a unit)
+    long long *t_end = reinterpret_cast<long long *>(smem);
+    int4 *t_req = reinterpret_cast<int4 *>(smem + 8 * kThreads);
 
-    // ---- this CTA's range of steps ----
+    // ---- this CTA's range of stages ----
     if (threadIdx.x == 0) {
         s.start.special = 0;
-        p.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+        p.desc[2 * blockIdx.x + 1] = make_int4(-1, 0, 0, 0);
     }
     __syncthreads();
-    long long total = 0, before = 0, mine = 0;   // stages: all, of requests before, of request b
-    int steps = 1;                               // of a unit of request b
-    for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+    long long total = 0;
+    // a tile's requests; returns its stages
+    auto tile = [&](int b0, bool look) {
         const int b = b0 + threadIdx.x;
-        mine = 0;
+        long long mine = 0, t;
+        int4 r4 = make_int4(0, 0, 0, 1);
         if (b < a.B) {
             const AttnRequest r = attn_request(a, b);
-            const Work w = work_of<ROWS>(a, r);
+            const Work w = work_of<ROWS>(a, r, R);
             mine = w.total;
-            steps = w.steps;
-            if (r.bad || (r.n > 0 && r.len == 0)) s.start.special = 1;
+            r4 = make_int4(r.row0, r.n, r.len, max(w.steps, 1));
+            if (look && (r.bad || (r.n > 0 && r.len == 0))) s.start.special = 1;
         }
-        long long t;
-        before = cta_scan(mine, t, s.start.sums);
-        total += t;
-    }
+        const long long before = cta_scan(mine, t, s.start.sums);
+        t_end[threadIdx.x] = before + mine;
+        t_req[threadIdx.x] = r4;
+        return t;
+    };
+    for (int b0 = 0; b0 < a.B; b0 += kThreads) total += tile(b0, true);
     const long long chunk = quotient(total + gridDim.x - 1, (int)gridDim.x);
     const long long raw0 = chunk * blockIdx.x, raw1 = min(raw0 + chunk, total);
     // requests that need no sums: bad ones, and those without keys
@@ -375,55 +383,54 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
         }
     }
     if (raw0 >= raw1) return;
-    if (threadIdx.x <= kWarps) s.start.pos[threadIdx.x] = total;
-    __syncthreads();
-    {
-        long long base = 0;
-        for (int b0 = 0; b0 < a.B; b0 += kThreads) {
-            const int b = b0 + threadIdx.x;
-            long long t = total;
-            if (a.B > kThreads) {
-                const Work w = b < a.B ? work_of<ROWS>(a, attn_request(a, b)) : Work{0, 0, 0, 0};
-                mine = w.total;
-                steps = w.steps;
-                before = cta_scan(mine, t, s.start.sums);
-            }
-            if (mine > 0)
-                for (int w = 0; w <= kWarps; ++w) {
-                    long long at = raw0 + (((raw1 - raw0) * w) / kWarps) - (base + before);
-                    if (at >= 0 && at < mine) {
-                        if (steps <= kWholeStages) at -= at - quotient(at, steps) * steps;
-                        s.start.b[w] = b;
-                        s.start.at[w] = at;
-                        s.start.pos[w] = base + before + at;
-                    }
-                }
-            base += t;
-            if (base > raw1) break;  // uniform
-        }
-        __syncthreads();
-    }
-
-    const uint32_t ring = smem_addr(smem) + (uint32_t)warp * STAGES * S::kBytes;
-    float *own = reinterpret_cast<float *>(smem + (size_t)warp * STAGES * S::kBytes);   // when the warp is done
-    const uint32_t q_s = smem_addr(smem) + kWarps * STAGES * S::kBytes + warp * NB * J * 512;   // query pieces
-    // this warp's range, and where it starts
-    const long long begin = s.start.pos[0], end = s.start.pos[kWarps];
-    const long long wb = s.start.pos[warp], we = s.start.pos[warp + 1];
-    long long pos = wb;
+    // this warp's range, from the unit that its first stage belongs to
+    long long wb = total, we = total;
     int b = 0, unit = 0, from = 0;    // of the request: (kv head, row block), stage
     AttnRequest rq{};
     Work wk{0, 1, 1, 0};
-    if (wb < we) {
-        b = s.start.b[warp];
-        rq = attn_request(a, b);
-        wk = work_of<ROWS>(a, rq);
-        const long long at = s.start.at[warp];
-        unit = (int)quotient(at, wk.steps);
-        from = (int)(at - (long long)unit * wk.steps);
+    {
+        const long long n = raw1 - raw0, raw_b = raw0 + n * warp / kWarps, raw_e = raw0 + n * (warp + 1) / kWarps;
+        long long base = 0;
+        for (int b0 = 0; b0 < a.B && base <= raw1; b0 += kThreads) {   // uniform
+            const long long t = a.B > kThreads ? tile(b0, false) : total;
+            if (a.B > kThreads) __syncthreads();
+            // where a warp starts at the earliest: its place among all stages, within request i
+            auto locate = [&](long long raw, int &i, int &u, int &f) {
+                const long long rel = raw - base;
+                const int block = __ffs(__ballot_sync(0xffffffffu, t_end[lane * 8 + 7] > rel)) - 1;
+                i = block * 8 + __ffs(__ballot_sync(0xffffffffu, t_end[block * 8 + (lane & 7)] > rel)) - 1;
+                const long long at = rel - (i > 0 ? t_end[i - 1] : 0);
+                const int steps = t_req[i].w;
+                u = (int)quotient(at, steps);
+                f = (int)(at - (long long)u * steps);
+                if (steps > kWholeStages) return raw;
+                const int whole_from = f;
+                f = 0;
+                return raw - whole_from;
+            };
+            int i, u, f;
+            if (raw_b >= base && raw_b < base + t) {
+                wb = locate(raw_b, i, unit, from);
+                const int4 r4 = t_req[i];
+                b = b0 + i;
+                rq.row0 = r4.x;
+                rq.n = r4.y;
+                rq.len = r4.z;
+                wk = work_of<ROWS>(a, rq, R);
+            }
+            if (raw_e >= base && raw_e < base + t) we = locate(raw_e, i, u, f);
+            base += t;
+        }
+        if (lane == 0) s_bound[warp] = wb;
+        if (threadIdx.x == kThreads - 1) s_bound[kWarps] = we;
     }
     __syncthreads();
-    if (lane < 2) s.seg[2 * warp + lane] = Segment{-1, 0, 0, 0, 0, 0, 0, 0};
+    const long long begin = s_bound[0], end = s_bound[kWarps];
+    long long pos = wb;
+    const uint32_t ring = smem_addr(smem) + (uint32_t)warp * STAGES * S::kBytes;
+    float *own = reinterpret_cast<float *>(smem + (size_t)warp * STAGES * S::kBytes);   // when the warp is done
+    const uint32_t q_s = smem_addr(smem) + kWarps * STAGES * S::kBytes + warp * NB * J * 512;   // query pieces
+    if (lane < 2) s.seg[2 * warp + lane] = Segment{-1, 0, 0, 0, 0, 0};
     // this lane's places in a stage: keys, values (the keys of rows 2c and 2c + 1), scales
     const int ka0 = key_of_row(g), vk0 = c, vk1 = 4 + (c ^ 3);
     const uint32_t kof = J == 8   ? ka0 * 128 + (((2 * c) ^ swizzle<J>(ka0)) << 4)
@@ -449,8 +456,9 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
         const int rows_all = rq.n * R;
         // keys that some row of the block sees; keys that all of its rows see
         const int row_hi = min(rb * ROWS + ROWS, rows_all) - 1;
-        const int see_hi = rq.len - rq.n + row_hi / R;                                  // inclusive
-        const int all_hi = rq.len - rq.n + rb * ROWS / R;
+        const bool one = rq.n == 1;                            // every row is token 0's
+        const int see_hi = rq.len - rq.n + (one ? 0 : row_hi / R);                      // inclusive
+        const int all_hi = rq.len - rq.n + (one ? 0 : rb * ROWS / R);
         const int see_lo = attn_first(a, max(all_hi, -1)), all_lo = attn_first(a, see_hi);
 
         const int32_t *table = a.page_table + (size_t)b * a.max_pages;
@@ -523,26 +531,15 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
             }
             cp_async_commit();
         };
+        // ---- the query rows' values and the first keys on their way ----
         int2 pg = pages_of(0);
-#pragma unroll
-        for (int i = 0; i < STAGES - 1; ++i) {
-            const int2 nx = pages_of(i + 1);
-            issue(i, i, pg);
-            pg = nx;
-        }
-
-        // ---- query rows, while the first keys come: two fp16 pieces, scaled
-        // by a power of two per row, in shared memory ----
-        __syncwarp();
-        float qs[NB][G], F[NB];                                // of row c: sums per group, factor
+        float x[NB][J][8];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
             const int rho = rb * ROWS + nb * 4 + (g >> 1);     // the row this thread's column holds
             const bool in = rho < rows_all;
-            const int j = in ? rho / R : 0, r = in ? rho - j * R : 0;
+            const int j = in && !one ? rho / R : 0, r = in ? rho - j * R : 0;
             const float *q = a.q + (size_t)(rq.row0 + j) * a.ldq + (size_t)(h * R + r) * D + 8 * c;
-            float x[J][8];
-            float big = 0.0f;
 #pragma unroll
             for (int u = 0; u < J; ++u) {
                 float4 v0 = make_float4(0.f, 0.f, 0.f, 0.f), v1 = v0;
@@ -550,13 +547,28 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
                     v0 = __ldg(reinterpret_cast<const float4 *>(q + 32 * u));
                     v1 = __ldg(reinterpret_cast<const float4 *>(q + 32 * u) + 1);
                 }
-                x[u][0] = v0.x; x[u][1] = v0.y; x[u][2] = v0.z; x[u][3] = v0.w;
-                x[u][4] = v1.x; x[u][5] = v1.y; x[u][6] = v1.z; x[u][7] = v1.w;
+                x[nb][u][0] = v0.x; x[nb][u][1] = v0.y; x[nb][u][2] = v0.z; x[nb][u][3] = v0.w;
+                x[nb][u][4] = v1.x; x[nb][u][5] = v1.y; x[nb][u][6] = v1.z; x[nb][u][7] = v1.w;
             }
+        }
+#pragma unroll
+        for (int i = 0; i < STAGES - 1; ++i) {
+            const int2 nx = pages_of(i + 1);
+            issue(i, i, pg);
+            pg = nx;
+        }
+
+        // ---- the query rows as two fp16 pieces, scaled by a power of two per
+        // row, in shared memory ----
+        __syncwarp();
+        float qs[NB][G], F[NB];                                // of row c: sums per group, factor
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+            float big = 0.0f;
 #pragma unroll
             for (int u = 0; u < J; ++u)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) big = fmaxf(big, fabsf(x[u][i]));
+                for (int i = 0; i < 8; ++i) big = fmaxf(big, fabsf(x[nb][u][i]));
             big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
             big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
             // 2^k times the row lies in [2^21, 2^22) at its largest
@@ -575,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
                     float z[2];
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
-                        const float v = rintf(x[u][i + 4 * y] * up);
+                        const float v = rintf(x[nb][u][i + 4 * y] * up);
                         const float hi = rintf(v * (1.0f / kRadix));
                         sum[u / UG] += v;
                         // odd nibbles are masked at 16 times their value
@@ -602,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
             const int rc = rb * ROWS + nb * 4 + c;
-            last[nb] = rc < rows_all ? rq.len - rq.n + rc / R : -1;
+            last[nb] = rc < rows_all ? rq.len - rq.n + (one ? 0 : rc / R) : -1;
             first[nb] = attn_first(a, last[nb]);
         }
 
@@ -883,7 +895,7 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
                 }
             }
         }
-        if (!whole && lane == 0) s.seg[2 * warp + (done ? 1 : 0)] = Segment{pos - from, b, unit, wk.steps, rq.row0, rows_all, h, rb};
+        if (!whole && lane == 0) s.seg[2 * warp + (done ? 1 : 0)] = Segment{pos - from, wk.steps, rq.row0, rows_all, h, rb};
 
         pos += iters;
         from = 0;
@@ -892,7 +904,7 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
             do {                                               // the next request with work
                 ++b;
                 rq = attn_request(a, b);
-                wk = work_of<ROWS>(a, rq);
+                wk = work_of<ROWS>(a, rq, R);
             } while (wk.total == 0);
         }
     }
@@ -957,7 +969,8 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
         if (threadIdx.x == 0 && !whole && seg.start >= begin) {
             // the unit starts here and goes on in the CTAs up to the one that holds its last stage
             const int last_cta = (int)((uint64_t)(seg.start + seg.steps - 1) / (uint64_t)chunk);
-            p.desc[blockIdx.x] = make_int4(seg.b, seg.unit, last_cta, slot);
+            p.desc[2 * blockIdx.x] = make_int4(seg.row0, seg.rows, seg.h, seg.rb);
+            p.desc[2 * blockIdx.x + 1] = make_int4(last_cta, slot, 0, 0);
         }
     }
 }
@@ -968,32 +981,29 @@ template <int ROWS>
 __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ SplitParams p, int D)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int4 d = __ldcg(p.desc + blockIdx.x);
+    const int4 u = __ldcg(p.desc + 2 * blockIdx.x), d = __ldcg(p.desc + 2 * blockIdx.x + 1);
     if (d.x < 0) return;
     const AttnCall &a = p.a;
-    const AttnRequest rq = attn_request(a, d.x);
-    const int R = a.heads / a.c.kv_heads;
-    const int blocks = (int)(((long long)rq.n * R + ROWS - 1) / ROWS);
-    const int h = d.y / blocks, rb = d.y - h * blocks;
+    const int R = p.R, rows = u.y, h = u.z, rb = u.w;
     const size_t per = (size_t)ROWS * (D + 2);
     auto part_of = [&](int cta) {
-        return p.part + ((size_t)cta * 2 + (cta == (int)blockIdx.x ? d.w : 0)) * per;
+        return p.part + ((size_t)cta * 2 + (cta == (int)blockIdx.x ? d.y : 0)) * per;
     };
     for (int i = threadIdx.x; i < ROWS * D / 4; i += 128) {
         const int row = i / (D / 4), dd = 4 * (i - row * (D / 4));
         const int rho = rb * ROWS + row;
-        if (rho >= rq.n * R) continue;
+        if (rho >= rows) continue;
         float m = -INFINITY, l = 0.0f;
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
         constexpr int kAhead = 8;    // partial sums on their way at once
-        for (int cta0 = blockIdx.x; cta0 <= d.z; cta0 += kAhead) {
+        for (int cta0 = blockIdx.x; cta0 <= d.x; cta0 += kAhead) {
             float2 ml[kAhead];
             float4 t[kAhead];
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
                 ml[k] = make_float2(-INFINITY, 0.0f);
                 t[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (cta0 + k <= d.z) {
+                if (cta0 + k <= d.x) {
                     const float *pt = part_of(cta0 + k);
                     ml[k] = __ldcg(reinterpret_cast<const float2 *>(pt + (size_t)ROWS * D + 2 * row));
                     t[k] = __ldcg(reinterpret_cast<const float4 *>(pt + (size_t)row * D + dd));
@@ -1022,7 +1032,7 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ 
         }
         const int j = rho / R, r = rho - j * R;
         const float inv = m == -INFINITY ? 0.0f : 1.0f / l;
-        *reinterpret_cast<float4 *>(a.out + (size_t)(rq.row0 + j) * a.ldo + (size_t)(h * R + r) * D + dd) =
+        *reinterpret_cast<float4 *>(a.out + (size_t)(u.x + j) * a.ldo + (size_t)(h * R + r) * D + dd) =
             make_float4(s.x * inv, s.y * inv, s.z * inv, s.w * inv);
     }
 }
@@ -1063,8 +1073,9 @@ cudaError_t launch_split(const AttnCall &call, cudaStream_t stream)
     if (grid > (units * steps + kWarps - 1) / kWarps) grid = (units * steps + kWarps - 1) / kWarps;
     if (grid < 1) grid = 1;
     p.grid = (int)grid;
+    p.R = R;
     p.desc = static_cast<int4 *>(call.workspace);
-    p.part = reinterpret_cast<float *>(static_cast<char *>(call.workspace) + kMaxGrid * sizeof(int4));
+    p.part = reinterpret_cast<float *>(static_cast<char *>(call.workspace) + 2 * kMaxGrid * sizeof(int4));
     p.head = p.part + (size_t)grid * 2 * 4 * NB * (32 * J + 2);
     kern<<<(unsigned)grid, kThreads, smem, stream>>>(p);
     if ((err = cudaGetLastError()) != cudaSuccess || steps <= kWholeStages || grid <= 1) return err;
@@ -1096,7 +1107,7 @@ size_t attn_workspace_bytes(int, int, int, int D)
 {
     // rows of sums of all CTAs: 304 of 8 rows at 64 dims, above that 304 of 4 or 152 of 8
     const size_t rows = D <= 64 ? kMaxGrid * 8 : kMaxGrid * 4;
-    return kMaxGrid * sizeof(int4) + rows * (2 + kWarps) * (size_t)(D + 2) * sizeof(float);
+    return 2 * kMaxGrid * sizeof(int4) + rows * (2 + kWarps) * (size_t)(D + 2) * sizeof(float);
 }
 
 cudaError_t launch_attn(const AttnCall &in, cudaStream_t stream)
