@@ -37,7 +37,7 @@
 // joins its warps' sums of the same unit, and a unit cut by the range of the
 // CTA leaves (m, l, sum) in the workspace, which a second kernel joins: no
 // atomics, always in order, the same bits every time.  (8 warps that share a
-// 256-key step and meet at each unit's end took 62 us where this takes 50.)
+// 256-key step and meet at each unit's end took 62 us where this takes 47.)
 // The cut is computed on the device from the lengths, so a captured launch
 // follows them.
 //
@@ -47,8 +47,10 @@
 // memory without bank conflicts (see key_of_row).
 //
 // Measured: 48 requests of 500 to 8192 keys, 32 heads over 8 of 128, one
-// group: 50 us, 215 MB at 4.3 TB/s; two of 125k keys, two groups: 69 us, 319
-// MB at 4.6 TB/s; 16 drafts of 5 tokens, 16 heads of 64, two groups: 32 us.
+// group: 47 us, 215 MB at 4.6 TB/s; two of 125k keys, two groups: 65 us, 319
+// MB at 4.9 TB/s; 16 drafts of 5 tokens, 16 heads of 64, two groups: 30 us; one
+// request of 776 keys: 10 us, of which 2 the ranges, 2 the first loads, 1 a
+// stage, 2 the CTA's join and 3 the second kernel.
 // Bound by instructions: 685 per stage and warp, 32 of them matrix
 // instructions and 240 the decoding of codes, issued in 60% of the cycles by
 // the 16 warps that registers allow (128 per thread).
@@ -73,6 +75,9 @@ constexpr float kRadix = 2048.0f;                 // a query is 2048 h + l, whol
 constexpr int kPieceBits = 11;                    // p s <= 2^kSlack is held times 2^11: below 2^15
 constexpr int kCarry = 4;                         // stages summed in the tensor core
 constexpr int kWholeStages = 4;                   // units of so few stages are one warp's
+// What a unit's start costs a warp, in stages, when shares are cut (0 / 2 / 4 take 31.9 / 30.1 / 29.4 us for the
+// drafts below, 48.1 / 47.0 / 47.7 for the 48 requests)
+constexpr int kStart = 2;
 constexpr int kMaxGrid = 304;                     // CTAs (the workspace's slots)
 
 struct SplitParams {
@@ -242,7 +247,7 @@ __device__ __forceinline__ float2 lds_f2(uint32_t s)
 struct Work {
     int step0, steps;   // stages of kStageKeys keys
     int blocks;         // row blocks of ROWS rows per kv head
-    long long total;    // steps of all its units
+    long long total;    // of all its units, with kStart for each one's start
 };
 
 template <int ROWS>
@@ -254,7 +259,7 @@ __device__ __forceinline__ Work work_of(const AttnCall &p, const AttnRequest &r,
     w.step0 = first / kStageKeys;
     w.steps = (r.len + kStageKeys - 1) / kStageKeys - w.step0;
     w.blocks = (int)(((long long)r.n * R + ROWS - 1) / ROWS);
-    w.total = (long long)w.blocks * p.c.kv_heads * w.steps;
+    w.total = (long long)w.blocks * p.c.kv_heads * (w.steps + kStart);
     return w;
 }
 
@@ -313,7 +318,7 @@ __device__ __forceinline__ void carry(float (&o)[NB][J][4], float (&t0)[NB][J][4
 // none), and which it is.
 struct Segment {
     long long start;
-    int steps;               // its stages
+    int length;              // with its start
     int row0, rows;          // the request's first token and its query rows per kv head
     int h, rb;               // kv head, row block
 };
@@ -401,8 +406,8 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
                 i = block * 8 + __ffs(__ballot_sync(0xffffffffu, t_end[block * 8 + (lane & 7)] > rel)) - 1;
                 const long long at = rel - (i > 0 ? t_end[i - 1] : 0);
                 const int steps = t_req[i].w;
-                u = (int)quotient(at, steps);
-                f = (int)(at - (long long)u * steps);
+                u = (int)quotient(at, steps + kStart);
+                f = (int)(at - (long long)u * (steps + kStart));
                 if (steps > kWholeStages) return raw;
                 const int whole_from = f;
                 f = 0;
@@ -451,7 +456,13 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
     const uint32_t page_stretches = (uint32_t)H * (uint32_t)(a.c.page_size >> 4), page_mask = a.c.page_size - 1;
     const uint32_t n_pages = (uint32_t)a.c.n_pages;
     while (pos < we) {
-        const int upto = (int)min((long long)wk.steps, from + (we - pos));
+        // its share of the unit: a start of kStart, then the stages
+        const int length = wk.steps + kStart, upto = (int)min((long long)length, from + (we - pos));
+        const int from_stage = max(from - kStart, 0), iters = max(upto - kStart, 0) - from_stage;
+        if (iters == 0) {                                      // the range ends within the start
+            pos += upto - from;
+            continue;
+        }
         const int h = unit / wk.blocks, rb = unit - h * wk.blocks;
         const int rows_all = rq.n * R;
         // keys that some row of the block sees; keys that all of its rows see
@@ -462,8 +473,7 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
         const int see_lo = attn_first(a, max(all_hi, -1)), all_lo = attn_first(a, see_hi);
 
         const int32_t *table = a.page_table + (size_t)b * a.max_pages;
-        const int key00 = (wk.step0 + from) * kStageKeys;
-        const int iters = upto - from;
+        const int key00 = (wk.step0 + from_stage) * kStageKeys;
         // this lane's first 16-byte piece of a page's rows of this head
         const size_t head_row = (size_t)h * a.c.page_size;
         const char *k_at = reinterpret_cast<const char *>(a.c.Kq) + head_row * (D / 2) + 16 * lane;
@@ -861,7 +871,7 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
         carry<NB, J>(o, t0, t1);
 
         // ---- a whole unit is finished; the sums of a cut one go to the CTA's join ----
-        const bool whole = from == 0 && upto == wk.steps, done = pos + iters >= we;
+        const bool whole = iters == wk.steps, done = pos + (upto - from) >= we;
         float *to = done ? own : p.head + ((size_t)blockIdx.x * kWarps + warp) * kSums;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
@@ -895,11 +905,11 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
                 }
             }
         }
-        if (!whole && lane == 0) s.seg[2 * warp + (done ? 1 : 0)] = Segment{pos - from, wk.steps, rq.row0, rows_all, h, rb};
+        if (!whole && lane == 0) s.seg[2 * warp + (done ? 1 : 0)] = Segment{pos - from, length, rq.row0, rows_all, h, rb};
 
-        pos += iters;
+        pos += upto - from;
         from = 0;
-        if (upto == wk.steps && ++unit == wk.blocks * H && pos < we) {
+        if (upto == length && ++unit == wk.blocks * H && pos < we) {
             unit = 0;
             do {                                               // the next request with work
                 ++b;
@@ -917,8 +927,9 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
         const Segment seg = s.seg[__ffs(left) - 1];
         const uint32_t mine_of = __ballot_sync(0xffffffffu, start_of == seg.start);
         left &= ~mine_of;
-        const bool whole = seg.start >= begin && seg.start + seg.steps <= end;
-        const int slot = seg.start > begin ? 1 : 0;
+        const long long first = seg.start + kStart;            // its first stage
+        const bool whole = first >= begin && seg.start + seg.length <= end;
+        const int slot = first > begin ? 1 : 0;
         float *part = p.part + ((size_t)blockIdx.x * 2 + slot) * kSums;
         for (int i = threadIdx.x; i < ROWS * D / 4; i += kThreads) {
             const int row = i / (D / 4), d = 4 * (i - row * (D / 4));
@@ -966,9 +977,9 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
                 }
             }
         }
-        if (threadIdx.x == 0 && !whole && seg.start >= begin) {
+        if (threadIdx.x == 0 && !whole && first >= begin) {
             // the unit starts here and goes on in the CTAs up to the one that holds its last stage
-            const int last_cta = (int)((uint64_t)(seg.start + seg.steps - 1) / (uint64_t)chunk);
+            const int last_cta = (int)((uint64_t)(seg.start + seg.length - 1) / (uint64_t)chunk);
             p.desc[2 * blockIdx.x] = make_int4(seg.row0, seg.rows, seg.h, seg.rb);
             p.desc[2 * blockIdx.x + 1] = make_int4(last_cta, slot, 0, 0);
         }
