@@ -905,7 +905,8 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
                 }
             }
         }
-        if (!whole && lane == 0) s.seg[2 * warp + (done ? 1 : 0)] = Segment{pos - from, length, rq.row0, rows_all, h, rb};
+        if (!whole && lane == 0)
+            s.seg[2 * warp + (done ? 1 : 0)] = Segment{pos - from, length, rq.row0, rows_all, h, rb};
 
         pos += upto - from;
         from = 0;

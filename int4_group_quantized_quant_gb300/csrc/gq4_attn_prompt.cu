@@ -27,10 +27,10 @@
 // zeros into shared memory by cp.async, 1 that makes the factors of its keys
 // from them, 4 or 8 that turn the codes into the K and V operands, 2 of which
 // a lane issues the MMAs of S and of P V (an MMA's operands cost its thread as
-// much time as the MMA takes).  Tensor memory (512 columns): S in four slots, whose columns P takes over 16 by 16 as S is read,
-// and the tile's O in two; K and V have three slots in shared memory (EXACT;
-// else two), the cache as it is four (two).  S runs ahead of P V by as many
-// tiles as it has slots.
+// much time as the MMA takes).  Tensor memory (512 columns): S in four slots,
+// whose columns P takes over 16 by 16 as S is read, and the tile's O in two; K
+// and V have three slots in shared memory (EXACT; else two), the cache as it
+// is four (two).  S runs ahead of P V by as many tiles as it has slots.
 // K is stored [key][d] (K-major), V [key][d] as well, which is the MN-major
 // form of the second product's B operand: no transposition.
 // Measured, 32 heads over 8 of 128: a prompt of 6007 tokens, one group, 674 us
