@@ -622,12 +622,23 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
     const int tile_lo = see_lo / kTile;
     const int n_tiles = see_hi >= see_lo ? see_hi / kTile - tile_lo + 1 : 0;
 
-    // ---- Q: two fp16 pieces with one power of two for the CTA; the copying
-    // warp is under way meanwhile ----
+    // ---- Q: two fp16 pieces with one power of two for the CTA, by the softmax
+    // and adding warps; the others are under way meanwhile, but the tables need
+    // the power (barrier 1) and S the pieces (barrier 2) ----
+    constexpr int kStaging = 32 * W::kDq0;
     int kq = 0;
-    if (warp != W::kCopy) {
-        constexpr int kStaging = kThreads - 32, kTurns = (kRows * (DP / 8) + kStaging - 1) / kStaging;
-        const int th = (int)threadIdx.x - (warp > W::kCopy ? 32 : 0);
+    auto meet = [&](int barrier) {
+        if (barrier == 1) asm volatile("bar.sync 1, %0;" ::"n"(kStaging + 32) : "memory");
+        else asm volatile("bar.sync 2, %0;" ::"n"(kStaging + 32) : "memory");
+    };
+    if (warp == W::kCopy + 1) {
+        meet(1);
+        kq = scale_exponent(__int_as_float(s_big));
+    } else if (warp == W::kMma) {
+        meet(2);
+    } else if (warp < W::kDq0) {
+        constexpr int kTurns = (kRows * (DP / 8) + kStaging - 1) / kStaging;
+        const int th = (int)threadIdx.x;
         float4 q[kTurns][2];
         float big = 0.0f;
 #pragma unroll
@@ -651,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         }
         const unsigned int top = __reduce_max_sync(0xffffffffu, __float_as_uint(big));
         if (lane == 0) atomicMax(&s_big, (int)top);
-        asm volatile("bar.sync 1, %0;" ::"n"(kStaging) : "memory");
+        meet(1);
         kq = scale_exponent(__int_as_float(s_big));
         const float up = pow2(kq);
 #pragma unroll
@@ -681,7 +692,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             }
         }
         fence_proxy_async_smem();
-        asm volatile("bar.sync 1, %0;" ::"n"(kStaging) : "memory");
+        meet(2);
     }
 
     bool ok = true;
