@@ -1,0 +1,177 @@
+"""GPU tests of gq4_kv_attention's kernel for requests with many query rows
+(prompts and chunks), and of both kernels on caches and queries of unlike
+sizes, against the float64 restatement of tests/kv_ref.py.
+
+Every case that is meant for the prompt kernel states so by ``prompt(...)``,
+which restates the dispatch rule: at least 48 query rows per kv head in some
+request, 5120 in all, heads of at most 128 values."""
+
+import numpy as np
+import pytest
+import torch
+
+from int4_group_quantized_quant_gb300 import inputs as I
+from tests import kv_ref as R
+from tests.gpu_util import dev, gq4_module, host, requires_cuda
+from tests.test_gpu_attention import FILL, Setup
+
+pytestmark = [pytest.mark.gpu, requires_cuda]
+
+
+@pytest.fixture(scope="module")
+def gq4():
+    g = gq4_module()
+    g.device_error(clear=True)
+    return g
+
+
+def prompt(news, lens, H, KH, D, gs, page, window=0, pad=3, seed=0):
+    """A Setup whose requests of 48 query rows per kv head and more run on the prompt kernel."""
+    s = Setup(news, lens, H, KH, D, gs, page, window, pad, seed)
+    assert max(news) * (H // KH) >= 48 and s.T * H >= 5120 and D <= 128
+    return s
+
+
+def few(news, lens, H, KH, D, gs, page, window=0, pad=3, seed=0):
+    """A Setup that runs on the kernel of few query rows."""
+    s = Setup(news, lens, H, KH, D, gs, page, window, pad, seed)
+    assert max(news) * (H // KH) < 48 or s.T * H < 5120 or D > 128
+    return s
+
+
+def close(got, s, shrink=1.0):
+    """Within the derived bound (times shrink) everywhere; returns the worst share of it."""
+    ref, tol = R.attention(s.q, s.starts, s.lens, s.table, s.cache, s.scale, s.window)
+    live = int(s.starts[-1])
+    got, ref, tol = got[:live].astype(np.float64), ref[:live], shrink * tol[:live]
+    assert np.all(np.isfinite(got))
+    err = np.abs(got - ref)
+    assert np.all(err <= tol), f"worst err/tol {float((err / np.maximum(tol, 1e-300)).max()):.3g}"
+
+
+# H, KH, D, gs: one group and several, padded heads, groups of query heads of any size
+FORMS = [(24, 6, 128, 128), (24, 6, 128, 64), (24, 3, 128, 32), (20, 4, 96, 96), (24, 8, 96, 32), (32, 4, 64, 64),
+         (20, 20, 64, 32)]
+
+
+# ---------------------------------------------------------------------------
+# The prompt kernel: masks, rows, what is not finite, pages, repetition
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("window", [1, 16, 33, 64, 300])
+@pytest.mark.parametrize("H,KH,D,gs", FORMS)
+def test_windows(gq4, H, KH, D, gs, window):
+    s = prompt([140, 60, 1, 90], [500, 60, 70, 333], H, KH, D, gs, 32, window)
+    s.check(s.run(gq4))
+    assert gq4.device_error() == 0
+
+
+@pytest.mark.parametrize("H,KH,D,gs", FORMS)
+def test_what_is_not_finite_stays_apart(gq4, H, KH, D, gs):
+    """A NaN or infinite query spoils its own row; a NaN key or value only the rows that see it."""
+    n, L, R_ = 140, 200, H // KH
+    s = prompt([n, n], [L, L], H, KH, D, gs, 16)
+    clean = s.run(gq4)
+    q = s.q.copy()
+    q[0, 1, 3] = np.nan
+    q[n - 1, 2, 5] = np.inf
+    q[5, 3, D - 1] = -np.inf
+    got = s.run(gq4, q=dev(q))
+    keep = np.ones(got.shape[:2], bool)
+    for row, h in ((0, 1), (n - 1, 2), (5, 3)):
+        assert np.isnan(got[row, h]).all()
+        keep[row, h] = False
+    assert np.array_equal(got[keep], clean[keep])
+    slot = s.table[0, 150 // 16], 150 % 16            # request 0's key 150 of kv head 1
+    sees = np.arange(n) + L - n >= 150
+    mine = list(range(R_, 2 * R_))
+    others = [h for h in range(H) if h not in mine]
+    for side in range(2):
+        kept = s.cache.sz[side][slot[0], 1, slot[1]].copy()
+        s.cache.sz[side][slot[0], 1, slot[1]] = np.nan
+        got = s.run(gq4)
+        s.cache.sz[side][slot[0], 1, slot[1]] = kept
+        assert np.isnan(got[:n][sees][:, mine]).all()
+        assert np.array_equal(got[:n][~sees], clean[:n][~sees])
+        assert np.array_equal(got[:n, others], clean[:n, others]) and np.array_equal(got[n:], clean[n:])
+    assert gq4.device_error() == 0
+
+
+@pytest.mark.parametrize("H,KH,D,gs", [(256, 1, 64, 32), (256, 2, 64, 64), (256, 4, 128, 128), (260, 5, 96, 32)])
+@pytest.mark.parametrize("page", [-1, 10**9])
+def test_a_bad_page_spoils_only_the_rows_that_see_it(gq4, H, KH, D, gs, page):
+    s = prompt([20], [40], H, KH, D, gs, 16, pad=0)
+    clean = s.run(gq4)
+    s.table[0, 2] = page        # keys 32..39: the last 8 queries
+    got = s.run(gq4)
+    assert gq4.device_error(clear=True) == 1 << 8
+    assert np.array_equal(got[:12], clean[:12]) and np.isnan(got[12:]).all()
+
+
+@pytest.mark.parametrize("H,KH,D,gs", FORMS)
+def test_same_bits_again_and_in_graphs(gq4, H, KH, D, gs):
+    """Twice, and in two graphs that share the workspace, replayed in turn; NaN in the workspace."""
+    s = prompt([1, 4, 130, 150], [900, 300, 200, 400], H, KH, D, gs, 16)
+    first = s.run(gq4)
+    assert np.array_equal(first, s.run(gq4))
+    args, q = s.dev(), dev(s.q)
+    out = torch.full(s.q.shape, FILL, device="cuda")
+    ws = torch.full((gq4.kv_attention_workspace_bytes(s.T, H, KH, D),), 255, dtype=torch.uint8, device="cuda")
+    side, graphs = torch.cuda.Stream(), []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.stream(side):
+            with torch.cuda.graph(g, stream=side):
+                gq4.kv_attention(q, *args, scale=s.scale, max_query=150, max_len=900, out=out, workspace=ws)
+        graphs.append(g)
+    for g in graphs * 2:
+        out.fill_(FILL)
+        g.replay()
+        torch.cuda.synchronize()
+        assert np.array_equal(host(out), first)
+
+
+@pytest.mark.parametrize("H,KH,D,gs", [(24, 6, 128, 128), (24, 6, 128, 32), (24, 8, 96, 96)])
+def test_strided_rows(gq4, H, KH, D, gs):
+    """q as columns of the fused QKV product, out as columns of a wider matrix."""
+    s = prompt([150, 77], [150, 333], H, KH, D, gs, 16)
+    wide = torch.full((s.T, H + 2 * KH, D), 9.0, device="cuda")
+    wide[:, :H] = dev(s.q)
+    out = torch.full((s.T, H + 1, D), FILL, device="cuda")
+    got = s.run(gq4, q=wide[:, :H], out=out[:, :H])
+    s.check(got)
+    assert torch.all(out[:, H:] == FILL)
+
+
+def test_two_streams_at_once(gq4):
+    a, b = prompt([150, 99], [500, 99], 24, 6, 128, 128, 16), prompt([1, 200], [900, 500], 32, 8, 64, 32, 16)
+    want = [s.run(gq4) for s in (a, b)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    held = [(s.dev(), dev(s.q), torch.full(s.q.shape, FILL, device="cuda")) for s in (a, b)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for s, st, (args, q, out) in zip((a, b), streams, held):
+            with torch.cuda.stream(st):
+                gq4.kv_attention(q, *args, scale=s.scale, max_query=max(s.news), max_len=int(s.lens.max()), out=out)
+    torch.cuda.synchronize()
+    for w, (_, _, out) in zip(want, held):
+        assert np.array_equal(host(out), w)
+
+
+@pytest.mark.parametrize("H,KH,D,gs", FORMS)
+def test_sizes_of_queries_and_scales(gq4, H, KH, D, gs):
+    """Value scales over ten powers of two, a request of queries 2^-100 of the other's; queries and
+    scale of opposite huge size."""
+    n = 130
+    s = prompt([n, n], [300, 400], H, KH, D, gs, 16)
+    g = I.rng(2210)
+    for side, spread in ((0, 1.0), (1, 5.0)):
+        sz = s.cache.sz[side]
+        sz[..., 0] *= np.exp2(g.uniform(-spread, spread, sz.shape[:-1])).astype(np.float32)
+    s.q[:n] *= 2.0 ** -100
+    close(s.run(gq4), s)
+    s = prompt([2 * n], [400], H, KH, D, gs, 16)
+    s.q *= np.float32(2.0 ** 100)
+    s.scale *= 2.0 ** -100
+    s.check(s.run(gq4))
+    assert gq4.device_error() == 0
