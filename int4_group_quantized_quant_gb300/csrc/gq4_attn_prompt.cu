@@ -1020,7 +1020,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                     if (!spoilt) vb = fmaxf(vb, fabsf(vs[0].x));
                 } else {
                     at[0] = spoilt ? quiet_nan() : Fq * pow2(-k.exponent());
-                    at[kTile] = v.finite ? pow2(-min(v.exponent(), 80)) : 0.0f;
+                    // (a row of zeros has no power: any but 0 would be too large beside its neighbours')
+                    at[kTile] = v.finite && v.bound > 0.0f ? pow2(-min(v.exponent(), 80)) : 0.0f;
                     if (!spoilt) vb = fmaxf(vb, v.bound);
                 }
             }

@@ -175,3 +175,31 @@ def test_sizes_of_queries_and_scales(gq4, H, KH, D, gs):
     s.scale *= 2.0 ** -100
     s.check(s.run(gq4))
     assert gq4.device_error() == 0
+
+
+# ---------------------------------------------------------------------------
+# Values, keys and queries of unlike size, on both kernels
+# ---------------------------------------------------------------------------
+
+BOTH = [(prompt, [200, 1, 64], [300, 77, 64], *f) for f in FORMS] + \
+       [(few, [5, 1, 3], [300, 77, 3], *f) for f in [*FORMS, (8, 8, 128, 128), (4, 4, 256, 64), (12, 2, 256, 256)]]
+
+
+def name_of(x):
+    return x.__name__ if callable(x) else None
+
+
+@pytest.mark.parametrize("make,news,lens,H,KH,D,gs", BOTH, ids=name_of)
+def test_rows_of_scale_zero(gq4, make, news, lens, H, KH, D, gs):
+    """Value and key rows whose scales are 0 (an unwritten slot of a zeroed pool) count as zeros."""
+    s = make(news, lens, H, KH, D, gs, 16)
+    g = I.rng(2211, H, D, gs)
+    for side in range(2):
+        live = ~np.isnan(s.cache.sz[side][..., 0, 0])
+        s.cache.sz[side][live & (g.random(live.shape) < 0.3)] = 0.0
+    s.check(s.run(gq4))
+    for side in range(2):
+        s.cache.sz[side][~np.isnan(s.cache.sz[side])] = 0.0
+    got = s.run(gq4)
+    assert np.all(got[:int(s.starts[-1])] == 0.0)
+    assert gq4.device_error() == 0
