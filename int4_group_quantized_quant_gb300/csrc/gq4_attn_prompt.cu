@@ -96,11 +96,11 @@ struct Mem {
     static constexpr int offQ = 0;                      // high, low
     static constexpr int offK = offQ + 2 * kQ;          // [slot][pieces]
     static constexpr int offV = offK + Form<EXACT>::kSlots * kSlot;
-    static constexpr int offF = offV + Form<EXACT>::kSlots * kSlot;       // per key F, G, s, z - 8, or F and V's power of two [slot][4 or 2][64]
+    static constexpr int offF = offV + Form<EXACT>::kSlots * kSlot;       // per key F, G, s and z - 8, or F and V's power of two, s and the power times P's [slot][4 or 2][64]
     static constexpr int offM = offF + kTab * kTile * (EXACT ? 16 : 8);   // per row: reference, sum p s (z - 8) [2][slot][128]
     static constexpr int offL = offM + kTab * kRows * (EXACT ? 8 : 4);    // per row (reference, sum of weights) [group][128]
     static constexpr int offQs = offL + Form<EXACT>::kGroups * kRows * 8;      // Q's sums over 8 values [128][DP / 8] (EXACT)
-    static constexpr int offVm = offQs + (EXACT ? kRows * DP / 2 : 0);   // V's largest [slot]
+    static constexpr int offVm = offQs + (EXACT ? kRows * DP / 2 : 0);   // what undoes P's power of two: the tables', the softmax's [2][slot]
     static constexpr int offBad = offVm + kTab * 8;         // pages outside the pool, by 16 keys [raw slot][4]
     static constexpr int offBar = offBad + 64;
     static constexpr int kRawCodes = kTile * 16 * J, kRawSz = kTile * 8 * G;
@@ -339,22 +339,23 @@ __device__ __forceinline__ void scale_pieces(uint32_t s_at, int cols, float by)
 struct TileOf {
     uint32_t s_at, key;     // S in tensor memory; the key tables in shared memory
     f32x2 qsum;             // sum_d q_d, twice
-    float e;                // P is held times 2^e
     int last, first;        // column x counts when first <= x <= last
 };
 
-// 16 keys, S in t: the weights 2^(w - ref), their two fp16 pieces (times 2^e
-// and the key's s_j or V's power of two) back into the same columns of tensor
-// memory, 8 of leading pieces and 8 of rests.  When a weight passes 2^kSlack
-// of it the reference moves by a whole power of two, by which the pieces of
-// this tile already written are scaled.  l and z: sums of the weights and of
-// p_j s_j (z_j - 8), both times 2^e, over even and odd keys.
+// 16 keys, S in t: the weights p_j = 2^(w - ref), two fp16 pieces of them times
+// 2^e and the key's s_j or V's power of two (the table holds the product) back
+// into the same columns of tensor memory, 8 of leading pieces and 8 of rests.
+// When a weight passes 2^kSlack of it the reference moves by a whole power of
+// two, by which the pieces of this tile already written are scaled.  From 2^23
+// on a whole step may be lost beside the reference: it moves to the largest
+// exponent itself there, and the exponents are rounded as numbers of its size
+// first, so that the weights and what is summed keep one reference.  l and z:
+// sums of the weights and of 2^e p_j s_j (z_j - 8), over even and odd keys.
 template <bool EXACT, bool MASK>
 __device__ __forceinline__ void keys16(const TileOf &w, int x, uint32_t (&t)[16], RowSum &r, f32x2 &l, f32x2 &z)
 {
     float top = -INFINITY;
-    const float b = w.e - r.ref;
-    const f32x2 base = pack2(b, b);
+    const f32x2 base = pack2(-r.ref, -r.ref);
 #pragma unroll
     for (int y = 0; y < 16; y += 4) {
         f32x2 f[2], g[2];
@@ -372,22 +373,30 @@ __device__ __forceinline__ void keys16(const TileOf &w, int x, uint32_t (&t)[16]
             t[c + 1] = __float_as_uint(v.y);
         }
     }
-    top -= w.e;
     const bool mine = top > (r.set ? kSlack : -INFINITY);
     if (__any_sync(0xffffffffu, mine)) {
-        const float by = mine ? ceilf(top) : 0.0f;
+        const float most = r.ref + top;
+        const bool large = mine && fabsf(most) >= 0x1p23f;
+        const float moved = large ? most : r.ref + ceilf(top);
+        const float by = large ? moved - r.ref : mine ? ceilf(top) : 0.0f;
+        const float up = large ? r.ref : 0.0f, down = large ? moved : by;
         const float shrink = mine && r.set ? exp2_approx(fmaxf(-by, -24.0f)) : 1.0f;
         if (mine) {
             const float f = r.set ? exp2_approx(-by) : 0.0f;   // (0: nothing is summed yet)
             r.l = r.set ? r.l * f : 0.0f;
             l = r.set ? mul2(l, pack2(f, f)) : pack2(0.0f, 0.0f);
             z = r.set ? mul2(z, pack2(f, f)) : pack2(0.0f, 0.0f);
-            r.ref += by;
+            r.ref = moved;
             r.set = true;
         }
         if (x > 0) scale_pieces(w.s_at, x, shrink);
 #pragma unroll
-        for (int y = 0; y < 16; ++y) t[y] = __float_as_uint(__uint_as_float(t[y]) - by);
+        for (int y = 0; y < 16; y += 2) {
+            const float2 v = unpack2(add2(add2(pack2(__uint_as_float(t[y]), __uint_as_float(t[y + 1])), pack2(up, up)),
+                                          pack2(-down, -down)));
+            t[y] = __float_as_uint(v.x);
+            t[y + 1] = __float_as_uint(v.y);
+        }
     }
     uint32_t pc[16];                       // leading pieces, rests
 #pragma unroll
@@ -425,7 +434,7 @@ __device__ __forceinline__ float tile_weights(const TileOf &w, RowSum &r)
         keys16<EXACT, MASK>(w, x, t, r, l, z);
     }
     const float2 ls = unpack2(l), zs = unpack2(z);
-    r.l = fmaf(ls.x + ls.y, exp2_approx(-w.e), r.l);
+    r.l += ls.x + ls.y;
     return zs.x + zs.y;
 }
 
@@ -720,17 +729,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             }
             tc_fence_after_sync();
             const uint32_t key = smem_s + M::offF + tab * (EXACT ? 16 : 8) * kTile;
-            // the tile's largest V (EXACT: its scale), as a power of two: P is
-            // held times 2^e, so that 2^kSlack of it is below 2^15
-            const float vb = lds_f1(smem_s + M::offVm + tab * 4);
-            const int ve = min(scale_exponent(vb), 80);
-            const float e = (float)(EXACT ? ve - 2 : ve + kPieceBits);
+            const float undo = lds_f1(smem_s + M::offVm + tab * 4);
             const int k0 = (tile_lo + i) * kTile;
             const bool masked = k0 + kTile - 1 > all_hi || k0 < all_lo;   // uniform
-            const TileOf w{tmem + lanes + kColS + s * kTile, key, pack2(qsum, qsum), e, last - k0, first - k0};
+            const TileOf w{tmem + lanes + kColS + s * kTile, key, pack2(qsum, qsum), last - k0, first - k0};
             const float z = masked ? tile_weights<EXACT, true>(w, r) : tile_weights<EXACT, false>(w, r);
-            // what the tile's P V is relative to
-            ms[tab * kRows + row] = r.set ? r.ref - e : -INFINITY;
+            // what the tile's P V is relative to; its power of two apart, which a
+            // large reference would swallow
+            ms[tab * kRows + row] = r.set ? r.ref : -INFINITY;
+            if (row == 0) reinterpret_cast<float *>(smem + M::offVm)[kTab + tab] = undo;
             if (EXACT) ms[(kTab + tab) * kRows + row] = z;
             tmem_wait_st();
             tc_fence_before_sync();
@@ -760,9 +767,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                 break;
             }
             tc_fence_after_sync();
+            const float undo = reinterpret_cast<const float *>(smem + M::offVm)[kTab + tab];
             const float2 t2 = make_float2(ms[tab * kRows + row], EXACT ? ms[(kTab + tab) * kRows + row] : 0.0f);
             const float mn = fmaxf(m, t2.x), ref = mn == -INFINITY ? 0.0f : mn;
-            const float ft = exp2_approx(t2.x - ref);
+            const float ft = exp2_approx(t2.x - ref) * undo;
             if (__any_sync(0xffffffffu, mn > m)) {
                 const float fo = exp2_approx(m - ref);
                 zs *= fo;
@@ -999,7 +1007,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                 ok = false;
                 break;
             }
-            float vb = 0.0f;
+            float vb = 0.0f, by[2];
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
                 const int key = lane + 32 * y, t = (tile_lo + i) * kTile + key;
@@ -1015,24 +1023,30 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                     const float F = spoilt ? quiet_nan() : Fq * ks[0].x;
                     at[0] = F;
                     at[kTile] = (8.0f - ks[0].y) * F;
-                    at[2 * kTile] = spoilt ? 0.0f : vs[0].x;
                     at[3 * kTile] = spoilt ? 0.0f : vs[0].y - 8.0f;
+                    by[y] = spoilt ? 0.0f : vs[0].x;
                     if (!spoilt) vb = fmaxf(vb, fabsf(vs[0].x));
                 } else {
                     at[0] = spoilt ? quiet_nan() : Fq * pow2(-k.exponent());
                     // (a row of zeros has no power: any but 0 would be too large beside its neighbours')
-                    at[kTile] = v.finite && v.bound > 0.0f ? pow2(-min(v.exponent(), 80)) : 0.0f;
+                    by[y] = v.finite && v.bound > 0.0f ? pow2(-min(v.exponent(), 80)) : 0.0f;
                     if (!spoilt) vb = fmaxf(vb, v.bound);
                 }
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.raw_empty[rs]);
             // (numbers of one sign order as their bits do)
             const unsigned int top = __reduce_max_sync(0xffffffffu, __float_as_uint(vb));
-            if (lane == 0) reinterpret_cast<unsigned int *>(smem + M::offVm)[tab] = top;
+            // by the tile's largest V (EXACT: its scale), as a power of two: P is
+            // held times 2^e, so that 2^kSlack of it is below 2^15
+            const int ve = min(scale_exponent(__uint_as_float(top)), 80), e = EXACT ? ve - 2 : ve + kPieceBits;
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+                reinterpret_cast<float *>(smem + M::offF)[(tab * (EXACT ? 4 : 2) + (EXACT ? 2 : 1)) * kTile + lane + 32 * y] =
+                    by[y] * pow2(e);
+            if (lane == 0) reinterpret_cast<float *>(smem + M::offVm)[tab] = pow2(-e);
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&bar.k_full[slot]);
-                mbar_arrive(&bar.raw_empty[rs]);
-            }
+            if (lane == 0) mbar_arrive(&bar.k_full[slot]);
             if (++slot == W::kSlots) {
                 slot = 0;
                 phase ^= 1;

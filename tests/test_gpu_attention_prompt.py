@@ -203,3 +203,35 @@ def test_rows_of_scale_zero(gq4, make, news, lens, H, KH, D, gs):
     got = s.run(gq4)
     assert np.all(got[:int(s.starts[-1])] == 0.0)
     assert gq4.device_error() == 0
+
+
+@pytest.mark.parametrize("make,news,lens,H,KH,D,gs", BOTH, ids=name_of)
+@pytest.mark.parametrize("power", [16, 24, 40, 100])
+def test_scores_of_any_size(gq4, make, news, lens, H, KH, D, gs, power):
+    """Queries so large that the exponents pass 2^24: an output is still a mean of the values with
+    weights that sum to 1, and the top key's value where no error of the exponents can decide."""
+    s = make(news, lens, H, KH, D, gs, 16)
+    s.q *= np.float32(2.0 ** power)
+    got = s.run(gq4).astype(np.float64)
+    R_ = H // KH
+    sure = 0
+    for b, (n, L) in enumerate(zip(news, lens)):
+        t = np.arange(L)
+        slots = s.table[b, t // 16].astype(np.int64) * 16 + t % 16
+        seen = t[None] <= (L - n + np.arange(n))[:, None]
+        for h in range(H):
+            k, v = (s.cache.rows(side, h // R_, slots) for side in range(2))
+            x = s.q[s.starts[b]:s.starts[b] + n, h].astype(np.float64)
+            w = np.where(seen, s.scale * (x @ k.T), -np.inf)
+            # twice the restated bound's error of an exponent, from a looser A: |code - z| <= 9
+            e = 2 * s.scale * np.abs(x).sum(-1) * 0.3 * 24 * (D / 8 + 9) * 2.0 ** -23
+            out = got[s.starts[b]:s.starts[b] + n, h]
+            vmax = np.abs(v).max()
+            assert np.all(np.abs(out) <= vmax * 1.001)
+            top = np.sort(w, -1)[:, -2:] if L > 1 else np.stack([np.full(n, -np.inf), w[:, 0]], -1)
+            one = top[:, 1] - top[:, 0] > 2 * e + 20
+            sure += one.sum()
+            # 2^-20 of the rest's weight and the bound's 16 units on terms of 17 scales of 0.3
+            assert np.all(np.abs(out[one] - v[np.argmax(w[one], -1)]) <= L * np.exp(-20.0) * vmax + 16 * 2.0 ** -23 * 5.1)
+    assert sure > 0
+    assert gq4.device_error() == 0
