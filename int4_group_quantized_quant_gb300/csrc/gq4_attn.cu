@@ -987,12 +987,30 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
     }
 }
 
+constexpr int kJoinThreads = 128;
+
 // Joins the partial sums of the units that were cut, one CTA for each CTA of
-// the first kernel.
-template <int ROWS>
-__global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ SplitParams p, int D)
+// the first kernel.  J, G: also computes the rows that the prompt kernel left
+// (0: there are none).
+template <int ROWS, int J, int G>
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_constant__ SplitParams p, int D)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    if constexpr (J > 0) {
+        // a thread looks at one tile in gridDim.x at a time
+        __shared__ float q[kJoinThreads / 32][32 * J];
+        const int warp = threadIdx.x >> 5;
+        for (long long n0 = blockIdx.x; n0 < p.a.n_apart; n0 += (long long)kJoinThreads * gridDim.x) {   // uniform
+            const long long n = n0 + (long long)threadIdx.x * gridDim.x;
+            uint4 rows = make_uint4(0, 0, 0, 0);
+            if (n < p.a.n_apart) rows = __ldcg(reinterpret_cast<const uint4 *>(p.a.apart + n));
+            if (!__syncthreads_or((rows.x | rows.y | rows.z | rows.w) != 0)) continue;
+            for (int x = 0; x < kJoinThreads && n0 + (long long)x * gridDim.x < p.a.n_apart; ++x) {
+                const long long m = n0 + (long long)x * gridDim.x;
+                apart_rows<J, G>(p.a, p.a.apart[m], (int)(m % p.a.c.kv_heads), warp, kJoinThreads / 32, q[warp]);
+            }
+        }
+    }
     const int4 u = __ldcg(p.desc + 2 * blockIdx.x), d = __ldcg(p.desc + 2 * blockIdx.x + 1);
     if (d.x < 0) return;
     const AttnCall &a = p.a;
@@ -1001,7 +1019,7 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ 
     auto part_of = [&](int cta) {
         return p.part + ((size_t)cta * 2 + (cta == (int)blockIdx.x ? d.y : 0)) * per;
     };
-    for (int i = threadIdx.x; i < ROWS * D / 4; i += 128) {
+    for (int i = threadIdx.x; i < ROWS * D / 4; i += kJoinThreads) {
         const int row = i / (D / 4), dd = 4 * (i - row * (D / 4));
         const int rho = rb * ROWS + row;
         if (rho >= rows) continue;
@@ -1090,17 +1108,20 @@ cudaError_t launch_split(const AttnCall &call, cudaStream_t stream)
     p.part = reinterpret_cast<float *>(static_cast<char *>(call.workspace) + 2 * kMaxGrid * sizeof(int4));
     p.head = p.part + (size_t)grid * 2 * 4 * NB * (32 * J + 2);
     kern<<<(unsigned)grid, kThreads, smem, stream>>>(p);
-    if ((err = cudaGetLastError()) != cudaSuccess || steps <= kWholeStages || grid <= 1) return err;
+    if ((err = cudaGetLastError()) != cudaSuccess || ((steps <= kWholeStages || grid <= 1) && call.n_apart == 0))
+        return err;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(128);
+    cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = stream;
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_join_kernel<4 * NB>, p, (int)(32 * J));
+    if constexpr (J <= 4)
+        if (call.n_apart > 0) return cudaLaunchKernelEx(&cfg, attn_join_kernel<4 * NB, J, G>, p, (int)(32 * J));
+    return cudaLaunchKernelEx(&cfg, attn_join_kernel<4 * NB, 0, 0>, p, (int)(32 * J));
 }
 
 template <int J, int G>
@@ -1115,11 +1136,33 @@ cudaError_t launch_rows(const AttnCall &call, cudaStream_t stream)
 
 }  // namespace
 
-size_t attn_workspace_bytes(int, int, int, int D)
+namespace {
+
+// Requests of at least so many query rows per kv head, and calls of so many
+// rows in all, are the prompt kernel's.
+constexpr int kPromptRows = 48, kPromptTotal = 5120;
+
+// The prompt kernel's CTAs: as many row tiles as its requests can have
+// together, per kv head.
+long long prompt_ctas(int B, int T, int heads, int kv_heads)
+{
+    const long long rows = (long long)T * (heads / kv_heads), most = rows / kPromptRows;
+    return ((rows + kPromptTile - 1) / kPromptTile + (B < most ? B : most)) * kv_heads;
+}
+
+size_t sums_bytes(int D)
 {
     // rows of sums of all CTAs: 304 of 8 rows at 64 dims, above that 304 of 4 or 152 of 8
     const size_t rows = D <= 64 ? kMaxGrid * 8 : kMaxGrid * 4;
     return 2 * kMaxGrid * sizeof(int4) + rows * (2 + kWarps) * (size_t)(D + 2) * sizeof(float);
+}
+
+}  // namespace
+
+size_t attn_workspace_bytes(int T, int heads, int kv_heads, int D)
+{
+    static_assert(sizeof(ApartTile) == 32, "a multiple of 16 bytes");
+    return sums_bytes(D) + (size_t)prompt_ctas(GQ4_MAX_REQUESTS, T, heads, kv_heads) * sizeof(ApartTile);
 }
 
 cudaError_t launch_attn(const AttnCall &in, cudaStream_t stream)
@@ -1132,11 +1175,12 @@ cudaError_t launch_attn(const AttnCall &in, cudaStream_t stream)
     // tokens (256, 2048) 90 and 50.  Four groups: of 12 169 and 150, of 16
     // 170 and 197.
     AttnCall call = in;
-    constexpr int kPromptRows = 48, kPromptTotal = 5120;
     const long long R = call.heads / call.c.kv_heads;
     const bool prompt = prompt_path_supported(call) && call.max_query * R >= kPromptRows &&
                         (long long)call.T * call.heads >= kPromptTotal;
     call.prompt_rows = prompt ? kPromptRows : 0x7fffffff;
+    call.apart = reinterpret_cast<ApartTile *>(static_cast<char *>(call.workspace) + sums_bytes(call.c.head_dim));
+    call.n_apart = prompt ? prompt_ctas(call.B, call.T, call.heads, call.c.kv_heads) : 0;
     if (prompt) {
         const cudaError_t err = launch_attn_prompt(call, stream);
         if (err != cudaSuccess) return err;

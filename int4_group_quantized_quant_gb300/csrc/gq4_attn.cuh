@@ -79,4 +79,95 @@ __device__ __forceinline__ float quiet_nan()
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+// Rows of a prompt tile that its pieces do not hold, in plain f32 over what the
+// tile wrote for them: one row per warp and 32 keys at a time, of which a lane
+// takes a key and then, of every key, four of the head's values.  Rare, so in
+// the call's last kernel: any such code in the prompt kernel itself, run or
+// not, cost it 1 to 6 % (its roles fill the registers and share the
+// instruction cache).  q: 32 J floats of the warp's own.
+template <int J, int G>
+__device__ __noinline__ void apart_rows(const AttnCall &a, const ApartTile &at, int h, int warp, int warps, float *q)
+{
+    constexpr int D = 32 * J, GS = D / G;
+    const int lane = threadIdx.x & 31, b = at.request;
+    const int R = a.heads / a.c.kv_heads, shift = 31 - __clz(a.c.page_size);
+    const AttnRequest rq = attn_request(a, b);
+    const int32_t *table = a.page_table + (size_t)b * a.max_pages;
+    for (int r = warp; r < kPromptTile; r += warps) {
+        if (!(at.rows[r >> 5] >> (r & 31) & 1u)) continue;
+        const int rho = at.tile * kPromptTile + r, j = rho / R, head = h * R + rho - j * R;
+        const int last = rq.len - rq.n + j, first = attn_first(a, max(last, -1));
+        const float *qg = a.q + (size_t)(rq.row0 + j) * a.ldq + (size_t)head * D;
+        float x[J], big = 0.0f;        // the row at a size of 1 to 2, undone in its factor
+#pragma unroll
+        for (int i = 0; i < J; ++i) {
+            x[i] = qg[lane + 32 * i];
+            if (fabsf(x[i]) < INFINITY) big = fmaxf(big, fabsf(x[i]));
+        }
+        const uint32_t top_q = __reduce_max_sync(0xffffffffu, __float_as_uint(big));
+        const int e = top_q == 0 ? 0 : min(max((int)(top_q >> 23) - 127, -126), 126);
+#pragma unroll
+        for (int i = 0; i < J; ++i) q[lane + 32 * i] = ldexpf(x[i], -e);
+        const float factor = ldexpf(a.scale * kLog2e, e);
+        __syncwarp();
+        float m = -INFINITY, l = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int k0 = first; k0 <= last; k0 += 32) {
+            const int t = k0 + lane;
+            size_t row = 0;
+            bool in = false;
+            float w = -INFINITY;
+            if (t <= last) {
+                const int page = __ldg(table + (t >> shift));
+                in = (uint32_t)page < (uint32_t)a.c.n_pages;
+                w = quiet_nan();       // a page outside the pool
+                if (in) {
+                    row = kv_row(a.c, page, h, t & (a.c.page_size - 1));
+                    const uint32_t *words = a.c.Kq + row * (4 * J);
+                    const float2 *sz = reinterpret_cast<const float2 *>(a.c.K_sz) + row * G;
+                    float sum = 0.0f;
+#pragma unroll 1
+                    for (int x = 0; x < 4 * J; ++x) {
+                        const uint32_t word = __ldg(words + k_word_index(x, J));
+                        const float2 s = __ldg(sz + 8 * x / GS);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            sum = fmaf(q[8 * x + i], ((float)(word >> (4 * i) & 15u) - s.y) * s.x, sum);
+                    }
+                    w = sum * factor;
+                }
+            }
+            float top = w;
+#pragma unroll
+            for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+            const float mn = fmaxf(m, top), ref = mn == -INFINITY ? 0.0f : mn;
+            const float f = exp2_approx(m - ref), p = exp2_approx(w - ref);
+            m = mn;
+            l = fmaf(l, f, p);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] *= f;
+#pragma unroll 1
+            for (int x = 0; x < min(32, last - k0 + 1); ++x) {
+                const float px = __shfl_sync(0xffffffffu, p, x);
+                const size_t rx = __shfl_sync(0xffffffffu, (unsigned long long)row, x);
+                if (!__shfl_sync(0xffffffffu, (int)in, x)) {
+                    o[0] = o[1] = o[2] = o[3] = quiet_nan();
+                    continue;
+                }
+                if (lane >= 8 * J) continue;
+                const uint32_t half = __ldg(reinterpret_cast<const uint16_t *>(a.c.Vq) + rx * (8 * J) + v_half_index(lane, J));
+                const float2 s = __ldg(reinterpret_cast<const float2 *>(a.c.V_sz) + rx * G + 4 * lane / GS);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[i] = fmaf(px, ((float)(half >> (4 * i) & 15u) - s.y) * s.x, o[i]);
+            }
+        }
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+        const float inv = last < first ? 0.0f : 1.0f / l;
+        if (lane < 8 * J)
+            *reinterpret_cast<float4 *>(a.out + (size_t)(rq.row0 + j) * a.ldo + (size_t)head * D + 4 * lane) =
+                make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
+        __syncwarp();
+    }
+}
+
 }  // namespace gq4

@@ -18,6 +18,8 @@
 // small ones first.
 // Powers of two keep the pieces inside fp16: one per CTA for Q, one per key
 // for K (undone by F_j) and for V (undone in P, against the tile's largest).
+// Query rows too small for their CTA's power are computed again in plain f32 by
+// the call's last kernel (see apart_rows).
 // The tensor core cuts its sums rather than rounding them, so a tile's P V
 // starts at zero and is added to f32 registers.
 //
@@ -55,13 +57,14 @@ namespace {
 
 __device__ unsigned int g_prompt_error = 0;
 
-constexpr int kRows = 128;
+constexpr int kRows = kPromptTile;
 constexpr int kTile = 64;                       // keys
 constexpr int kCoWarps = 8;
 constexpr int kWarps = 24;                      // all
 constexpr int kThreads = 32 * kWarps;
 constexpr float kSlack = 4.0f;                  // log2 of how far a weight may pass the maximum
 constexpr int kPieceBits = 11;                  // P is held times 2^11
+constexpr int kSpread = 12;                     // log2 of how far apart what shares a power of two may be
 constexpr int kSP = 4;                          // slots of S, which P replaces in place
 constexpr int kTab = 8;                         // slots of the key and row tables
 constexpr uint32_t kColS = 0, kColO = 256;      // S/P: 64 columns a slot; O: 128, two slots
@@ -527,7 +530,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     const uint32_t smem_s = smem_addr(smem);
-    __shared__ int s_sums[kWarps], s_req, s_tile, s_big;
+    __shared__ int s_sums[kWarps], s_big, s_small;
+    __shared__ volatile int s_req, s_tile;
+    __shared__ uint32_t s_apart[kRows / 32];               // a bit per row that is left to the last kernel
     __shared__ volatile int s_abort;
     __shared__ uint32_t s_tmem;
     const AttnCall &a = p.a;
@@ -551,7 +556,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             all += t;
         }
         const int want = all - 1 - (int)(blockIdx.x / (unsigned)H);
-        if (want < 0) return;   // uniform
+        if (want < 0) {   // uniform
+            if (threadIdx.x < kRows / 32) a.apart[blockIdx.x].rows[threadIdx.x] = 0;
+            return;
+        }
         int base = 0;
         for (int b0 = 0; b0 < a.B; b0 += kThreads) {
             int t = all;
@@ -609,6 +617,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         }
         s_abort = 0;
         s_big = 0;
+        s_small = 0x7f800000;
+#pragma unroll
+        for (int x = 0; x < kRows / 32; ++x) s_apart[x] = 0;
         mbar_fence_init();
     }
     if (warp == W::kMma) {
@@ -650,7 +661,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         constexpr int kTurns = (kRows * (DP / 8) + kStaging - 1) / kStaging;
         const int th = (int)threadIdx.x;
         float4 q[kTurns][2];
-        float big = 0.0f;
+        float big = 0.0f, small = INFINITY;
+        // the largest finite value of a turn's row, whose DP / 8 threads are
+        // neighbours (an infinity is left to its own row)
+        auto largest = [&](const float4 (&x)[2]) {
+            const float v[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
+            float m = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (fabsf(v[i]) < INFINITY) m = fmaxf(m, fabsf(v[i]));
+#pragma unroll
+            for (int o = DP / 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            return m;
+        };
 #pragma unroll
         for (int n = 0; n < kTurns; ++n) {
             const int i = th + n * kStaging, r = i / (DP / 8), d8 = i - r * (DP / 8);
@@ -665,15 +688,28 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         }
 #pragma unroll
         for (int n = 0; n < kTurns; ++n) {
-            const float v[8] = {q[n][0].x, q[n][0].y, q[n][0].z, q[n][0].w, q[n][1].x, q[n][1].y, q[n][1].z, q[n][1].w};
-#pragma unroll
-            for (int m = 0; m < 8; ++m)   // an infinity is left to its own row
-                if (fabsf(v[m]) < INFINITY) big = fmaxf(big, fabsf(v[m]));
+            const float m = largest(q[n]);
+            big = fmaxf(big, m);
+            if (m > 0.0f) small = fminf(small, m);
         }
         const unsigned int top = __reduce_max_sync(0xffffffffu, __float_as_uint(big));
-        if (lane == 0) atomicMax(&s_big, (int)top);
+        const unsigned int least = __reduce_min_sync(0xffffffffu, __float_as_uint(small));
+        if (lane == 0) {
+            atomicMax(&s_big, (int)top);
+            atomicMin(&s_small, (int)least);
+        }
         meet(1);
         kq = scale_exponent(__int_as_float(s_big));
+        if (s_small < 0x7f800000 && scale_exponent(__int_as_float(s_small)) - kq > kSpread) {
+            // rows of less than 2^-kSpread of the largest would lose digits to it
+#pragma unroll
+            for (int n = 0; n < kTurns; ++n) {
+                const int i = th + n * kStaging, r = i / (DP / 8);
+                const float m = largest(q[n]);
+                if (i % (DP / 8) == 0 && m > 0.0f && scale_exponent(m) - kq > kSpread)
+                    atomicOr(&s_apart[r >> 5], 1u << (r & 31));
+            }
+        }
         const float up = pow2(kq);
 #pragma unroll
         for (int n = 0; n < kTurns; ++n) {
@@ -1126,6 +1162,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
     __syncthreads();
     tc_fence_after_sync();
     if (warp == W::kMma) tmem_dealloc(tmem, kTmemCols);
+    // (the request is read again: in registers for so long it costs the roles)
+    if (threadIdx.x < kRows / 32) a.apart[blockIdx.x].rows[threadIdx.x] = s_apart[threadIdx.x];
+    if (threadIdx.x == kRows / 32) {
+        a.apart[blockIdx.x].request = s_req;
+        a.apart[blockIdx.x].tile = s_tile;
+    }
 }
 
 template <int J, int G, int DP>
@@ -1143,10 +1185,7 @@ cudaError_t launch_prompt_t(const AttnCall &call, cudaStream_t stream)
             return err;
         ready_dev.store(dev, std::memory_order_release);
     }
-    // as many row tiles as the requests can have together, per kv head
-    const long long R = call.heads / call.c.kv_heads;
-    const long long tiles = (call.T * R + kRows - 1) / kRows + (call.B < call.T ? call.B : call.T);
-    const long long grid = tiles * call.c.kv_heads;
+    const long long grid = call.n_apart;
     if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
     PromptParams p{};
     p.a = call;

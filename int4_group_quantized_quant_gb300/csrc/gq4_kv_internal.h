@@ -36,6 +36,12 @@ cudaError_t launch_kv_plan(const PlanCall &call, cudaStream_t stream);
 cudaError_t read_kv_device_error(unsigned int *bits, bool clear);
 
 // Attention over the cache.
+constexpr int kPromptTile = 128;   // query rows of a tile of the prompt kernel
+// What a tile of the prompt kernel leaves to the call's last kernel: a bit per row.
+struct ApartTile {
+    uint32_t rows[kPromptTile / 32];
+    int request, tile, unused[2];
+};
 struct AttnCall {
     int B, T, heads, max_pages, max_query, max_len;
     gq4_kv_cache c;
@@ -48,6 +54,8 @@ struct AttnCall {
     int ldo;
     void *workspace;
     int prompt_rows;   // requests of at least so many query rows per kv head go to the prompt kernel
+    ApartTile *apart;  // in the workspace, one for each of the prompt kernel's CTAs
+    long long n_apart;
 };
 size_t attn_workspace_bytes(int T, int heads, int kv_heads, int D);
 cudaError_t launch_attn(const AttnCall &call, cudaStream_t stream);

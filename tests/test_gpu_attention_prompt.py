@@ -235,3 +235,19 @@ def test_scores_of_any_size(gq4, make, news, lens, H, KH, D, gs, power):
             assert np.all(np.abs(out[one] - v[np.argmax(w[one], -1)]) <= L * np.exp(-20.0) * vmax + 16 * 2.0 ** -23 * 5.1)
     assert sure > 0
     assert gq4.device_error() == 0
+
+
+@pytest.mark.parametrize("make,news,lens,H,KH,D,gs", BOTH, ids=name_of)
+@pytest.mark.parametrize("low,high,by", [(0, 40, 0), (0, 13, 0), (-60, 40, 0), (-70, -30, 50), (60, 120, -80)])
+def test_queries_of_unlike_size(gq4, make, news, lens, H, KH, D, gs, low, high, by):
+    """Rows of one request spread over many powers of two (the scale taken by 2^by): every row is
+    held to the bound of its own size, whatever rows stand beside it."""
+    s = make(news, lens, H, KH, D, gs, 16)
+    g = I.rng(2212, H, D, gs)
+    size = g.integers(low, high + 1, s.q.shape[:2])
+    size[::3] = min(max(-by, low), high)         # a third of the tokens: weights of ordinary spread
+    s.q *= np.exp2(size).astype(np.float32)[..., None]
+    s.q[7 % len(s.q), 1] = 0.0
+    s.scale = np.ldexp(s.scale, by)
+    close(s.run(gq4), s)
+    assert gq4.device_error() == 0
