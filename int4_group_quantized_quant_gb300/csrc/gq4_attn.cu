@@ -26,8 +26,9 @@
 // warp) and is then added to f32 sums: cut sums of a whole context would be
 // off by 2.6e-6 at 131072 keys instead of 1.1e-6.
 //   The running maximum m moves only when a weight passes 2^4 of it (a vote
-// per 32 keys), so that accumulators are rescaled rarely; the values'
-// scales likewise share a power of two 2^E, which keeps p s inside fp16.
+// per 32 keys), so that accumulators are rescaled rarely; the scales of the
+// values that a row sees likewise share a power of two 2^E, which keeps p s
+// inside fp16.
 //
 // Split.  A stage is 32 keys of one (request, kv head, block of rows), a
 // unit; the list of all stages is cut into equal ranges, one per CTA, and
@@ -295,6 +296,12 @@ __device__ __forceinline__ long long cta_scan(long long v, long long &total, lon
         total += sums[i];
     }
     return before + inc - v;
+}
+
+// 1 / x for a power of two, 2^-126 to 2^126.
+__device__ __forceinline__ float inverse_power(float x)
+{
+    return __uint_as_float(0x7f000000u - __float_as_uint(x));
 }
 
 // o += the two pieces' sums, which start again at zero.
@@ -631,9 +638,10 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
         // o: f32 sums; t: the tensor core's, added to o every kCarry stages
         float o[NB][J][4], t0[NB][J][4], t1[NB][J][4], zs[NB][G], l[NB], m[NB];
         int carried = 0;
-        float vs = 0x1p111f, vref = 0x1p-100f;                 // 2^(11 - E), 2^E
+        float vs[NB];                                          // a row's 2^(11 - E), E by the values that it sees
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
+            vs[nb] = 0x1p111f;
             l[nb] = 0.0f;
             m[nb] = -INFINITY;
 #pragma unroll
@@ -762,18 +770,8 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
                 for (int y = 0; y < 2; ++y)
 #pragma unroll
                     for (int gr = 0; gr < G; ++gr) vtop = fmaxf(vtop, fabsf(vz[x][y][gr].x));
-            move |= vtop > vref;
+            move |= vtop * (NB == 1 ? vs[0] : fmaxf(vs[0], vs[NB - 1])) > (float)(1 << kPieceBits);   // vtop > 2^E
             if (__any_sync(0xffffffffu, move)) {
-#pragma unroll
-                for (int i4 = 16; i4 > 0; i4 >>= 1) vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, i4));
-                float fv = 1.0f;
-                if (vtop > vref) {
-                    const int e = min((int)(__float_as_uint(vtop) >> 23) - 126, 127);   // vtop < 2^e
-                    const float nref = ldexpf(1.0f, e);
-                    fv = vref / nref;
-                    vref = nref;
-                    vs = ldexpf(1.0f, kPieceBits - e);
-                }
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb) {
                     float t = top[nb];
@@ -784,6 +782,26 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
                     const float f = mn > m[nb] ? exp2_approx(m[nb] - mn) : 1.0f;
                     m[nb] = mn;
                     l[nb] *= f;
+                    float vt = vtop;
+                    if (NB > 1 && masked) {                    // (one row per thread: what it does not see is 0 already)
+                        vt = 0.0f;
+#pragma unroll 1
+                        for (int xy = 0; xy < 4; ++xy)
+#pragma unroll
+                            for (int gr = 0; gr < G; ++gr)
+                                if (!((hidden >> (xy * NB + nb)) & 1u))
+                                    vt = fmaxf(vt, fabsf(lds_f2(st + sof + S::kSz + (8 * xy * G + gr) * 8).x));
+                    }
+                    vt = fmaxf(vt, __shfl_xor_sync(0xffffffffu, vt, 4));
+                    vt = fmaxf(vt, __shfl_xor_sync(0xffffffffu, vt, 8));
+                    vt = fmaxf(vt, __shfl_xor_sync(0xffffffffu, vt, 16));
+                    float fv = 1.0f;
+                    const float vref = (float)(1 << kPieceBits) * inverse_power(vs[nb]);
+                    if (vt > vref) {
+                        const int e = min((int)(__float_as_uint(vt) >> 23) - 126, 127);   // vt < 2^e
+                        vs[nb] = __uint_as_float((uint32_t)(127 + kPieceBits - e) << 23);
+                        fv = vref * (vs[nb] * (1.0f / (1 << kPieceBits)));
+                    }
                     const float fo = f * fv;
 #pragma unroll
                     for (int gr = 0; gr < G; ++gr) zs[nb][gr] *= fo;
@@ -809,6 +827,7 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
                     for (int y = 0; y < 2; ++y) {
                         w[x][y][nb] = exp2_approx(w[x][y][nb] - ref);
                         l[nb] += w[x][y][nb];
+                        w[x][y][nb] *= vs[nb];
                     }
             }
             Halves<J> hv[2][4];
@@ -828,7 +847,7 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
                         for (int y = 0; y < 2; ++y) {
                             // (one row per thread: its hidden keys have scale 0 already)
                             const bool hid = NB > 1 && masked && ((hidden >> ((x * 2 + y) * NB + nb)) & 1u);
-                            const float ps = hid ? 0.0f : w[x][y][nb] * (vz[x][y][gr].x * vs);
+                            const float ps = hid ? 0.0f : w[x][y][nb] * vz[x][y][gr].x;
                             zs[nb][gr] = hid ? zs[nb][gr] : fmaf(ps, vz[x][y][gr].y - 8.0f, zs[nb][gr]);
                             pf[nb][x][y] = transpose8x8(two_pieces(ps));
                         }
@@ -880,7 +899,7 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
             lt += __shfl_xor_sync(0xffffffffu, lt, 8);
             lt += __shfl_xor_sync(0xffffffffu, lt, 16);
             const int row = nb * 4 + c, rho = rb * ROWS + row;
-            float back = vref * 0x1p-11f;
+            float back = inverse_power(vs[nb]);
             if (whole) {
                 back *= m[nb] == -INFINITY ? 0.0f : 1.0f / lt;
                 const int j = rho / R, r = rho - j * R;
@@ -987,8 +1006,6 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
     }
 }
 
-constexpr int kJoinThreads = 128;
-
 // Joins the partial sums of the units that were cut, one CTA for each CTA of
 // the first kernel.  J, G: also computes the rows that the prompt kernel left
 // (0: there are none).
@@ -998,16 +1015,21 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if constexpr (J > 0) {
         // a thread looks at one tile in gridDim.x at a time
-        __shared__ float q[kJoinThreads / 32][32 * J];
-        const int warp = threadIdx.x >> 5;
+        __shared__ ApartShared<J> s;
         for (long long n0 = blockIdx.x; n0 < p.a.n_apart; n0 += (long long)kJoinThreads * gridDim.x) {   // uniform
             const long long n = n0 + (long long)threadIdx.x * gridDim.x;
-            uint4 rows = make_uint4(0, 0, 0, 0);
-            if (n < p.a.n_apart) rows = __ldcg(reinterpret_cast<const uint4 *>(p.a.apart + n));
-            if (!__syncthreads_or((rows.x | rows.y | rows.z | rows.w) != 0)) continue;
+            bool some = false;
+            if (n < p.a.n_apart) {
+                const uint4 *at = reinterpret_cast<const uint4 *>(p.a.apart + n);
+                const uint4 rows = __ldcg(at), more = __ldcg(at + 1);
+                some = (rows.x | rows.y | rows.z | rows.w | more.z) != 0;
+            }
+            if (!__syncthreads_or(some)) continue;
             for (int x = 0; x < kJoinThreads && n0 + (long long)x * gridDim.x < p.a.n_apart; ++x) {
                 const long long m = n0 + (long long)x * gridDim.x;
-                apart_rows<J, G>(p.a, p.a.apart[m], (int)(m % p.a.c.kv_heads), warp, kJoinThreads / 32, q[warp]);
+                const ApartTile &at = p.a.apart[m];
+                if ((at.rows[0] | at.rows[1] | at.rows[2] | at.rows[3] | (uint32_t)at.uneven) != 0)
+                    apart_rows<J, G>(p.a, at, (int)(m % p.a.c.kv_heads), s);
             }
         }
     }

@@ -79,22 +79,89 @@ __device__ __forceinline__ float quiet_nan()
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+// 2^k with |x| 2^k in [2^12, 2^13) for the exponent field of x (0: as it is).
+__device__ __forceinline__ int scale_exponent(float x)
+{
+    const int e = (int)((__float_as_uint(x) >> 23) & 255u);
+    return x > 0.0f ? min(max(12 + 127 - e, -120), 120) : 0;
+}
+
+// log2 of how far apart what shares a power of two may be: two fp16 pieces of
+// the largest hold 2^-25 of it, so what is smaller by more would lose digits.
+constexpr int kSpread = 12;
+
+// Threads of the call's last kernel, and what it keeps in shared memory for
+// the rows that the prompt kernel left.
+constexpr int kJoinThreads = 128;
+template <int J>
+struct ApartShared {
+    float q[kJoinThreads / 32][32 * J];
+    uint32_t rows[kPromptTile / 32];
+};
+
+// Marks the rows of a tile that see, of some 64 keys, only values less than
+// 2^-kSpread of the largest.  By the whole CTA.
+template <int G>
+__device__ __noinline__ void small_rows(const AttnCall &a, const AttnRequest &rq, const ApartTile &at, int h, uint32_t *rows)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int R = a.heads / a.c.kv_heads, shift = 31 - __clz(a.c.page_size);
+    const int row0 = at.tile * kPromptTile, row_hi = min(row0 + kPromptTile, rq.n * R) - 1, pos0 = rq.len - rq.n;
+    // keys that some row sees; keys that all rows see
+    const int see_hi = pos0 + row_hi / R, all_hi = pos0 + row0 / R;
+    const int see_lo = attn_first(a, max(all_hi, -1)), all_lo = attn_first(a, max(see_hi, -1));
+    auto size_of = [&](int t) {
+        if (t < see_lo || t > see_hi) return 0.0f;
+        const int page = __ldg(a.page_table + (size_t)at.request * a.max_pages + (t >> shift));
+        if ((uint32_t)page >= (uint32_t)a.c.n_pages) return 0.0f;
+        const float2 *sz = reinterpret_cast<const float2 *>(a.c.V_sz) + kv_row(a.c, page, h, t & (a.c.page_size - 1)) * G;
+        float size = 0.0f;
+#pragma unroll 1
+        for (int g = 0; g < G; ++g) {
+            const float2 s = __ldg(sz + g);
+            const float x = fabsf(s.x) * (G == 1 ? 1.0f : fmaxf(fabsf(s.y), fabsf(15.0f - s.y)));
+            if (x < INFINITY) size = fmaxf(size, x);
+        }
+        return size;
+    };
+    auto largest = [](float x) { return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(x))); };
+    for (int k0 = (see_lo / kPromptKeys + warp) * kPromptKeys; k0 <= see_hi; k0 += kPromptKeys * (kJoinThreads / 32)) {
+        if (k0 + kPromptKeys - 1 <= all_hi && k0 >= all_lo) continue;
+        const int t0 = k0 + lane, t1 = t0 + 32;
+        const float v0 = size_of(t0), v1 = size_of(t1);
+        const int power = scale_exponent(largest(fmaxf(v0, v1)));
+        for (int j = row0 / R; j <= row_hi / R; ++j) {
+            const int last = pos0 + j, first = attn_first(a, max(last, -1));
+            const float top = largest(fmaxf(t0 <= last && t0 >= first ? v0 : 0.0f, t1 <= last && t1 >= first ? v1 : 0.0f));
+            if (top == 0.0f || scale_exponent(top) - power <= kSpread) continue;
+            for (int r = max(j * R - row0, 0) + lane; r <= min(j * R + R - 1, row_hi) - row0; r += 32)
+                atomicOr(&rows[r >> 5], 1u << (r & 31));
+        }
+    }
+}
+
 // Rows of a prompt tile that its pieces do not hold, in plain f32 over what the
 // tile wrote for them: one row per warp and 32 keys at a time, of which a lane
 // takes a key and then, of every key, four of the head's values.  Rare, so in
-// the call's last kernel: any such code in the prompt kernel itself, run or
-// not, cost it 1 to 6 % (its roles fill the registers and share the
-// instruction cache).  q: 32 J floats of the warp's own.
+// the call's last kernel: such code in the prompt kernel itself, run or not,
+// cost it 1 to 6 % (its roles fill the registers and share the instruction
+// cache).  By the whole CTA.
 template <int J, int G>
-__device__ __noinline__ void apart_rows(const AttnCall &a, const ApartTile &at, int h, int warp, int warps, float *q)
+__device__ __noinline__ void apart_rows(const AttnCall &a, const ApartTile &at, int h, ApartShared<J> &s)
 {
     constexpr int D = 32 * J, GS = D / G;
-    const int lane = threadIdx.x & 31, b = at.request;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = at.request;
     const int R = a.heads / a.c.kv_heads, shift = 31 - __clz(a.c.page_size);
     const AttnRequest rq = attn_request(a, b);
     const int32_t *table = a.page_table + (size_t)b * a.max_pages;
-    for (int r = warp; r < kPromptTile; r += warps) {
-        if (!(at.rows[r >> 5] >> (r & 31) & 1u)) continue;
+    float *q = s.q[warp];
+    __syncthreads();
+    if (threadIdx.x < kPromptTile / 32) s.rows[threadIdx.x] = at.rows[threadIdx.x];
+    __syncthreads();
+    if (at.uneven) small_rows<G>(a, rq, at, h, s.rows);
+    __syncthreads();
+    for (int r = warp; r < kPromptTile; r += kJoinThreads / 32) {
+        if (!(s.rows[r >> 5] >> (r & 31) & 1u)) continue;
         const int rho = at.tile * kPromptTile + r, j = rho / R, head = h * R + rho - j * R;
         const int last = rq.len - rq.n + j, first = attn_first(a, max(last, -1));
         const float *qg = a.q + (size_t)(rq.row0 + j) * a.ldq + (size_t)head * D;
@@ -128,10 +195,10 @@ __device__ __noinline__ void apart_rows(const AttnCall &a, const ApartTile &at, 
 #pragma unroll 1
                     for (int x = 0; x < 4 * J; ++x) {
                         const uint32_t word = __ldg(words + k_word_index(x, J));
-                        const float2 s = __ldg(sz + 8 * x / GS);
+                        const float2 kz = __ldg(sz + 8 * x / GS);
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
-                            sum = fmaf(q[8 * x + i], ((float)(word >> (4 * i) & 15u) - s.y) * s.x, sum);
+                            sum = fmaf(q[8 * x + i], ((float)(word >> (4 * i) & 15u) - kz.y) * kz.x, sum);
                     }
                     w = sum * factor;
                 }
@@ -155,9 +222,9 @@ __device__ __noinline__ void apart_rows(const AttnCall &a, const ApartTile &at, 
                 }
                 if (lane >= 8 * J) continue;
                 const uint32_t half = __ldg(reinterpret_cast<const uint16_t *>(a.c.Vq) + rx * (8 * J) + v_half_index(lane, J));
-                const float2 s = __ldg(reinterpret_cast<const float2 *>(a.c.V_sz) + rx * G + 4 * lane / GS);
+                const float2 vz = __ldg(reinterpret_cast<const float2 *>(a.c.V_sz) + rx * G + 4 * lane / GS);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) o[i] = fmaf(px, ((float)(half >> (4 * i) & 15u) - s.y) * s.x, o[i]);
+                for (int i = 0; i < 4; ++i) o[i] = fmaf(px, ((float)(half >> (4 * i) & 15u) - vz.y) * vz.x, o[i]);
             }
         }
 #pragma unroll

@@ -18,8 +18,9 @@
 // small ones first.
 // Powers of two keep the pieces inside fp16: one per CTA for Q, one per key
 // for K (undone by F_j) and for V (undone in P, against the tile's largest).
-// Query rows too small for their CTA's power are computed again in plain f32 by
-// the call's last kernel (see apart_rows).
+// Query rows too small for their CTA's power, or whose values are for a tile's
+// (some later row's are the large ones), are computed again in plain f32 by the
+// call's last kernel (see apart_rows).
 // The tensor core cuts its sums rather than rounding them, so a tile's P V
 // starts at zero and is added to f32 registers.
 //
@@ -58,13 +59,12 @@ namespace {
 __device__ unsigned int g_prompt_error = 0;
 
 constexpr int kRows = kPromptTile;
-constexpr int kTile = 64;                       // keys
+constexpr int kTile = kPromptKeys;
 constexpr int kCoWarps = 8;
 constexpr int kWarps = 24;                      // all
 constexpr int kThreads = 32 * kWarps;
 constexpr float kSlack = 4.0f;                  // log2 of how far a weight may pass the maximum
 constexpr int kPieceBits = 11;                  // P is held times 2^11
-constexpr int kSpread = 12;                     // log2 of how far apart what shares a power of two may be
 constexpr int kSP = 4;                          // slots of S, which P replaces in place
 constexpr int kTab = 8;                         // slots of the key and row tables
 constexpr uint32_t kColS = 0, kColO = 256;      // S/P: 64 columns a slot; O: 128, two slots
@@ -244,13 +244,6 @@ __device__ __forceinline__ void split_pair(float a, float b, uint32_t &hi, uint3
         : "=f"(x), "=f"(y)
         : "r"(hi), "f"(a), "f"(b));
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(y), "f"(x));
-}
-
-// 2^k with |x| 2^k in [2^12, 2^13) for the exponent field of x (0: as it is).
-__device__ __forceinline__ int scale_exponent(float x)
-{
-    const int e = (int)((__float_as_uint(x) >> 23) & 255u);
-    return x > 0.0f ? min(max(12 + 127 - e, -120), 120) : 0;
 }
 
 __device__ __forceinline__ float pow2(int k)   // |k| <= 126
@@ -533,6 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
     __shared__ int s_sums[kWarps], s_big, s_small;
     __shared__ volatile int s_req, s_tile;
     __shared__ uint32_t s_apart[kRows / 32];               // a bit per row that is left to the last kernel
+    __shared__ int s_uneven;                               // it is to look for rows that see small values only
     __shared__ volatile int s_abort;
     __shared__ uint32_t s_tmem;
     const AttnCall &a = p.a;
@@ -558,6 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         const int want = all - 1 - (int)(blockIdx.x / (unsigned)H);
         if (want < 0) {   // uniform
             if (threadIdx.x < kRows / 32) a.apart[blockIdx.x].rows[threadIdx.x] = 0;
+            if (threadIdx.x == kRows / 32) a.apart[blockIdx.x].uneven = 0;
             return;
         }
         int base = 0;
@@ -620,6 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         s_small = 0x7f800000;
 #pragma unroll
         for (int x = 0; x < kRows / 32; ++x) s_apart[x] = 0;
+        s_uneven = 0;
         mbar_fence_init();
     }
     if (warp == W::kMma) {
@@ -1081,6 +1077,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                 reinterpret_cast<float *>(smem + M::offF)[(tab * (EXACT ? 4 : 2) + (EXACT ? 2 : 1)) * kTile + lane + 32 * y] =
                     by[y] * pow2(e);
             if (lane == 0) reinterpret_cast<float *>(smem + M::offVm)[tab] = pow2(-e);
+            // where some row may not see the largest (uniform)
+            const int k0 = (tile_lo + i) * kTile;
+            if (k0 + kTile - 1 > all_hi || k0 < all_lo) {
+                // (a power of V is 2^-12 of its bound)
+                const float least = __uint_as_float(top) * (EXACT ? 0x1p-12f : 0x1p-24f);
+                if ((by[0] != 0.0f && fabsf(by[0]) < least) || (by[1] != 0.0f && fabsf(by[1]) < least)) s_uneven = 1;
+            }
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.k_full[slot]);
             if (++slot == W::kSlots) {
@@ -1167,6 +1170,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
     if (threadIdx.x == kRows / 32) {
         a.apart[blockIdx.x].request = s_req;
         a.apart[blockIdx.x].tile = s_tile;
+        a.apart[blockIdx.x].uneven = s_uneven;
     }
 }
 

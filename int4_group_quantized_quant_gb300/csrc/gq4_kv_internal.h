@@ -36,11 +36,12 @@ cudaError_t launch_kv_plan(const PlanCall &call, cudaStream_t stream);
 cudaError_t read_kv_device_error(unsigned int *bits, bool clear);
 
 // Attention over the cache.
-constexpr int kPromptTile = 128;   // query rows of a tile of the prompt kernel
-// What a tile of the prompt kernel leaves to the call's last kernel: a bit per row.
+constexpr int kPromptTile = 128, kPromptKeys = 64;   // query rows and keys of a tile of the prompt kernel
+// What a row tile of the prompt kernel leaves to the call's last kernel: a bit
+// per row, and whether to look for rows that see small values only.
 struct ApartTile {
     uint32_t rows[kPromptTile / 32];
-    int request, tile, unused[2];
+    int request, tile, uneven, unused;
 };
 struct AttnCall {
     int B, T, heads, max_pages, max_query, max_len;

@@ -251,3 +251,20 @@ def test_queries_of_unlike_size(gq4, make, news, lens, H, KH, D, gs, low, high, 
     s.scale = np.ldexp(s.scale, by)
     close(s.run(gq4), s)
     assert gq4.device_error() == 0
+
+
+@pytest.mark.parametrize("make,news,lens,H,KH,D,gs", BOTH, ids=name_of)
+@pytest.mark.parametrize("power", [20, 40, 90])
+@pytest.mark.parametrize("window", [0, 40])
+def test_unseen_values_take_no_digits(gq4, make, news, lens, H, KH, D, gs, power, window):
+    """Values 2^power of the others' size at a request's last keys, and before the window's first:
+    the rows that do not see them are held to the bound of what they see."""
+    s = make(news, lens, H, KH, D, gs, 16, window)
+    for b, n in enumerate(lens):
+        at = [n - 1, n - 30] if news[b] > 40 else [n - 1]
+        if window:
+            at.append(max(0, n - news[b] + 1 - window))     # the first query's first key
+        for t in at:
+            s.cache.sz[1][s.table[b, t // 16], :, t % 16, :, 0] *= np.float32(2.0 ** power)
+    close(s.run(gq4), s)
+    assert gq4.device_error() == 0
