@@ -376,7 +376,7 @@ __device__ __forceinline__ void keys16(const TileOf &w, int x, uint32_t (&t)[16]
         const float moved = large ? most : r.ref + ceilf(top);
         const float by = large ? moved - r.ref : mine ? ceilf(top) : 0.0f;
         const float up = large ? r.ref : 0.0f, down = large ? moved : by;
-        const float shrink = mine && r.set ? exp2_approx(fmaxf(-by, -24.0f)) : 1.0f;
+        float shrink = mine && r.set ? fminf(by, 48.0f) : 0.0f;   // (2^-48 leaves nothing of pieces below 2^16)
         if (mine) {
             const float f = r.set ? exp2_approx(-by) : 0.0f;   // (0: nothing is summed yet)
             r.l = r.set ? r.l * f : 0.0f;
@@ -385,7 +385,11 @@ __device__ __forceinline__ void keys16(const TileOf &w, int x, uint32_t (&t)[16]
             r.ref = moved;
             r.set = true;
         }
-        if (x > 0) scale_pieces(w.s_at, x, shrink);
+        if (x > 0)
+            do {                               // fp16's least power is 2^-24
+                scale_pieces(w.s_at, x, exp2_approx(-fminf(fmaxf(shrink, 0.0f), 24.0f)));
+                shrink -= 24.0f;
+            } while (__any_sync(0xffffffffu, shrink > 0.0f));
 #pragma unroll
         for (int y = 0; y < 16; y += 2) {
             const float2 v = unpack2(add2(add2(pack2(__uint_as_float(t[y]), __uint_as_float(t[y + 1])), pack2(up, up)),

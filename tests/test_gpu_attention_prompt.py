@@ -268,3 +268,28 @@ def test_unseen_values_take_no_digits(gq4, make, news, lens, H, KH, D, gs, power
             s.cache.sz[1][s.table[b, t // 16], :, t % 16, :, 0] *= np.float32(2.0 ** power)
     close(s.run(gq4), s)
     assert gq4.device_error() == 0
+
+
+@pytest.mark.parametrize("H,KH,D,gs", FORMS)
+@pytest.mark.parametrize("jump", [20, 30, 45, 100])
+def test_a_reference_that_jumps_inside_a_tile(gq4, H, KH, D, gs, jump):
+    """47 keys just below 2^4 of the first ones' weight, then one of 2^jump: what was summed before
+    shrinks by the whole jump.  The last key's value is 0 and its weight is all but everything, so
+    the result is below 48 2^(4 - jump) of the others' values (1) and its error below 16 2^-23 of
+    them, whatever the error of the exponents is (the bound's own term for them does not apply)."""
+    s = prompt([260], [330], H, KH, D, gs, 16)
+    t = np.arange(330)
+    log2w = np.where(t < 16, 0.0, np.where(t < 63, 3.875, np.where(t == 63, 3.875 + jump, -40.0)))
+    s.q[:] = 1.0
+    slots = s.table[0, t // 16], t % 16
+    # code 1, zero 0 in every key: w = scale D s
+    s.cache.codes[0][:] = 1
+    sk = (log2w / (s.scale * D * np.log2(np.e))).astype(np.float32)
+    for i in range(330):
+        pg, at = slots[0][i], slots[1][i]
+        s.cache.sz[0][pg, :, at, :] = (sk[i], 0.0)
+        s.cache.sz[1][pg, :, at, :] = (1.0 / 16, 0.0)
+        s.cache.codes[1][pg, :, at] = 0 if i == 63 else 15
+    got = s.run(gq4)[:260].astype(np.float64)
+    ref, _ = R.attention(s.q, s.starts, s.lens, s.table, s.cache, s.scale)
+    assert np.all(np.abs(got - ref[:260]) <= 16 * 2.0 ** -23 + 48 * 2.0 ** (4 - jump) * 2.0 ** -15)
