@@ -330,6 +330,37 @@ struct Segment {
     int h, rb;               // kv head, row block
 };
 
+// A stage's value groups of equal values, by scales of their size: a lane per
+// key.  st: the stage.
+template <int J, int G>
+__device__ __noinline__ void fit_equal_values(uint32_t st)
+{
+    using S = Stage<J, G>;
+    const int key = threadIdx.x & 31;
+    const uint32_t row = st + S::kCodes + key * 16 * J, at = st + 2 * S::kCodes + S::kSz + key * 8 * G;
+    __syncwarp();
+#pragma unroll 1
+    for (int gr = 0; gr < G; ++gr) {
+        const float2 sz = lds_f2(at + 8 * gr);
+        if (sz.x != 1.0f) continue;
+        uint32_t any = 0;
+#pragma unroll 1
+        for (int x = 0; x < 8 * (J / G); ++x) {
+            const int byte = 2 * ((x & 7) * J + gr * (J / G) + (x >> 3));
+            uint16_t half;
+            asm volatile("ld.shared.u16 %0, [%1];"
+                         : "=h"(half)
+                         : "r"(row + (((byte >> 4) ^ swizzle<J>(key)) << 4) + (byte & 15))
+                         : "memory");
+            any |= half;
+        }
+        if (any != 0) continue;
+        const float2 to = equal_values(sz);
+        asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(at + 8 * gr), "f"(to.x), "f"(to.y) : "memory");
+    }
+    __syncwarp();
+}
+
 template <int J, int G, int NB, int STAGES, int MINB>
 __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid_constant__ SplitParams p)
 {
@@ -722,14 +753,23 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
 
             // ---- values' scales; what a row does not see ----
             float2 vz[2][2][G];
+            bool ones = false;
+            auto load_scales = [&] {
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
+                for (int x = 0; x < 2; ++x)
 #pragma unroll
-                for (int y = 0; y < 2; ++y) {
+                    for (int y = 0; y < 2; ++y)
 #pragma unroll
-                    for (int gr = 0; gr < G; ++gr)
-                        vz[x][y][gr] = lds_f2(st + sof + S::kSz + ((16 * x + 8 * y) * G + gr) * 8);
-                }
+                        for (int gr = 0; gr < G; ++gr) {
+                            vz[x][y][gr] = lds_f2(st + sof + S::kSz + ((16 * x + 8 * y) * G + gr) * 8);
+                            ones |= vz[x][y][gr].x == 1.0f;
+                        }
+            };
+            load_scales();
+            if (__any_sync(0xffffffffu, ones)) {               // rare
+                fit_equal_values<J, G>(st);
+                load_scales();
+            }
             const bool masked = k0 + kStageKeys - 1 > all_hi || k0 < all_lo;   // uniform
             uint32_t hidden = 0;                               // bit (x, y, nb)
             if (masked) {

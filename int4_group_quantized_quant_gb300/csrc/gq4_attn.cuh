@@ -90,6 +90,20 @@ __device__ __forceinline__ int scale_exponent(float x)
 // the largest hold 2^-25 of it, so what is smaller by more would lose digits.
 constexpr int kSpread = 12;
 
+// A group of equal values has scale 1, codes 0 and the value in its zero (the
+// quantiser's rule), so its scale says nothing of its size: what is held
+// against the scale, or sums of codes minus 8 times it, would drown small
+// values.  The same value by a scale of its size: (0 - z) 1 = (0 - z / s) s for
+// a power of two s with 8 <= |z / s| < 16.
+__device__ __forceinline__ float2 equal_values(float2 sz)
+{
+    const uint32_t bits = __float_as_uint(sz.y) & 0x7fffffffu, e = bits >> 23;
+    if (bits == 0) return make_float2(0.0f, 0.0f);
+    if (e == 255) return sz;
+    const uint32_t s = e > 24 ? e - 3 : 21;
+    return make_float2(__uint_as_float(s << 23), sz.y * __uint_as_float((254 - s) << 23));
+}
+
 // Threads of the call's last kernel, and what it keeps in shared memory for
 // the rows that the prompt kernel left.
 constexpr int kJoinThreads = 128;
@@ -101,7 +115,7 @@ struct ApartShared {
 
 // Marks the rows of a tile that see, of some 64 keys, only values less than
 // 2^-kSpread of the largest.  By the whole CTA.
-template <int G>
+template <int J, int G>
 __device__ __noinline__ void small_rows(const AttnCall &a, const AttnRequest &rq, const ApartTile &at, int h, uint32_t *rows)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -114,11 +128,18 @@ __device__ __noinline__ void small_rows(const AttnCall &a, const AttnRequest &rq
         if (t < see_lo || t > see_hi) return 0.0f;
         const int page = __ldg(a.page_table + (size_t)at.request * a.max_pages + (t >> shift));
         if ((uint32_t)page >= (uint32_t)a.c.n_pages) return 0.0f;
-        const float2 *sz = reinterpret_cast<const float2 *>(a.c.V_sz) + kv_row(a.c, page, h, t & (a.c.page_size - 1)) * G;
+        const size_t row = kv_row(a.c, page, h, t & (a.c.page_size - 1));
+        const float2 *sz = reinterpret_cast<const float2 *>(a.c.V_sz) + row * G;
         float size = 0.0f;
 #pragma unroll 1
         for (int g = 0; g < G; ++g) {
-            const float2 s = __ldg(sz + g);
+            float2 s = __ldg(sz + g);
+            if (s.x == 1.0f) {
+                uint32_t any = 0;
+                for (int x = 0; x < 8 * (J / G); ++x)
+                    any |= reinterpret_cast<const uint16_t *>(a.c.Vq)[row * (8 * J) + (x & 7) * J + g * (J / G) + (x >> 3)];
+                if (any == 0) s = equal_values(s);
+            }
             const float x = fabsf(s.x) * (G == 1 ? 1.0f : fmaxf(fabsf(s.y), fabsf(15.0f - s.y)));
             if (x < INFINITY) size = fmaxf(size, x);
         }
@@ -158,11 +179,12 @@ __device__ __noinline__ void apart_rows(const AttnCall &a, const ApartTile &at, 
     __syncthreads();
     if (threadIdx.x < kPromptTile / 32) s.rows[threadIdx.x] = at.rows[threadIdx.x];
     __syncthreads();
-    if (at.uneven) small_rows<G>(a, rq, at, h, s.rows);
+    if (at.uneven) small_rows<J, G>(a, rq, at, h, s.rows);
     __syncthreads();
     for (int r = warp; r < kPromptTile; r += kJoinThreads / 32) {
         if (!(s.rows[r >> 5] >> (r & 31) & 1u)) continue;
         const int rho = at.tile * kPromptTile + r, j = rho / R, head = h * R + rho - j * R;
+        if (rho >= rq.n * R) break;
         const int last = rq.len - rq.n + j, first = attn_first(a, max(last, -1));
         const float *qg = a.q + (size_t)(rq.row0 + j) * a.ldq + (size_t)head * D;
         float x[J], big = 0.0f;        // the row at a size of 1 to 2, undone in its factor

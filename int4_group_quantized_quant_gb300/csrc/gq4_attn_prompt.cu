@@ -494,6 +494,73 @@ __device__ __forceinline__ KeyOf<G> key_of(int see_lo, int see_hi, int t, uint32
     return k;
 }
 
+// One scale group per row: a tile's rows of equal values, as it was copied, by
+// scales of their size.  raw: the keys' codes, the values', the keys' scales,
+// the values'.
+template <int J>
+__device__ __noinline__ void fit_equal_rows(uint32_t raw)
+{
+    const int lane = threadIdx.x & 31;
+    __syncwarp();
+#pragma unroll 1
+    for (int i = lane; i < 2 * kTile; i += 32) {
+        const int value = i / kTile, key = i % kTile;
+        const uint32_t row = raw + value * kTile * 16 * J + key * 16 * J;
+        const uint32_t at = raw + 2 * kTile * 16 * J + value * kTile * 8 + key * 8;
+        const float2 sz = lds_f2(at);
+        if (sz.x != 1.0f) continue;
+        uint32_t any = 0;
+#pragma unroll 1
+        for (int x = 0; x < 4 * J; ++x) {
+            uint32_t word;
+            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(word) : "r"(row + 4 * x) : "memory");
+            any |= word;
+        }
+        if (any != 0) continue;
+        const float2 to = equal_values(sz);
+        asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(at), "f"(to.x), "f"(to.y) : "memory");
+    }
+    __syncwarp();
+}
+
+// Several scale groups per row: a power of two is taken from what a key's scales
+// and zeros allow, 15 for a group of equal values (scale 1).  Where that leaves
+// too few digits for what such rows hold, all rows of the CTA are the last
+// kernel's.  zat: the keys' scales, then the values'; keys lo to hi of the tile
+// are seen by some row; every: by all.  (The codes are not looked at: a scale
+// of 1 by chance is computed there as well, and comes out the same.)
+template <int G>
+__device__ __noinline__ void leave_equal_rows(uint32_t zat, int lo, int hi, bool every, uint32_t *apart)
+{
+    constexpr float kLeast = 15.0f / (1 << kSpread);
+    const int lane = threadIdx.x & 31;
+    bool leave = false, some = false;
+    float top = 0.0f;
+#pragma unroll 1
+    for (int i = lane; i < 2 * kTile; i += 32) {
+        const int key = i % kTile;
+        bool ones = false;
+        float size = 0.0f;
+#pragma unroll 1
+        for (int g = 0; g < G && key >= lo && key <= hi; ++g) {
+            const float2 sz = lds_f2(zat + (i * G + g) * 8);
+            ones |= sz.x == 1.0f;
+            const float x = fabsf(sz.y);
+            size = fmaxf(size, sz.x == 1.0f ? x : fabsf(sz.x) * fmaxf(x, fabsf(15.0f - sz.y)));
+        }
+        const bool value = i >= kTile;
+        if (ones && size > 0.0f && size < kLeast && !(value && every)) leave = true;
+        if (value) {
+            some |= ones;
+            top = fmaxf(top, size);
+        }
+    }
+    top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+    if (every && __any_sync(0xffffffffu, some) && top > 0.0f && top < kLeast) leave = true;
+    if (__any_sync(0xffffffffu, leave) && lane < kRows / 32) apart[lane] = ~0u;
+    __syncwarp();
+}
+
 template <int NW>
 __device__ __forceinline__ int scan_ints(int v, int &total, int *sums)
 {
@@ -1044,6 +1111,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                 break;
             }
             float vb = 0.0f, by[2];
+            bool ones = false;             // a scale of 1: a group of equal values, most likely
+            if (EXACT) {
+                // (nobody else reads the scales of this form)
+                const uint32_t raw = smem_s + M::offRaw + (uint32_t)rs * M::kRawSlot, zat = raw + 2 * M::kRawCodes + lane * 8;
+#pragma unroll
+                for (int y = 0; y < 4; ++y) ones |= lds_f1(zat + (y & 1) * 256 + (y >> 1) * M::kRawSz) == 1.0f;
+                if (__any_sync(0xffffffffu, ones)) fit_equal_rows<J>(raw);   // rare
+            }
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
                 const int key = lane + 32 * y, t = (tile_lo + i) * kTile + key;
@@ -1065,11 +1140,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                 } else {
                     at[0] = spoilt ? quiet_nan() : Fq * pow2(-k.exponent());
                     // (a row of zeros has no power: any but 0 would be too large beside its neighbours')
+#pragma unroll
+                    for (int g = 0; g < G; ++g) ones |= ks[g].x == 1.0f || vs[g].x == 1.0f;
                     by[y] = v.finite && v.bound > 0.0f ? pow2(-min(v.exponent(), 80)) : 0.0f;
                     if (!spoilt) vb = fmaxf(vb, v.bound);
                 }
             }
             __syncwarp();
+            if (!EXACT && __any_sync(0xffffffffu, ones)) {   // rare
+                const int k0 = (tile_lo + i) * kTile;
+                leave_equal_rows<G>(smem_s + M::offRaw + 2 * M::kRawCodes + (uint32_t)rs * M::kRawSlot, see_lo - k0, see_hi - k0,
+                                    k0 + kTile - 1 <= all_hi && k0 >= all_lo, s_apart);
+            }
             if (lane == 0) mbar_arrive(&bar.raw_empty[rs]);
             // (numbers of one sign order as their bits do)
             const unsigned int top = __reduce_max_sync(0xffffffffu, __float_as_uint(vb));

@@ -293,3 +293,48 @@ def test_a_reference_that_jumps_inside_a_tile(gq4, H, KH, D, gs, jump):
     got = s.run(gq4)[:260].astype(np.float64)
     ref, _ = R.attention(s.q, s.starts, s.lens, s.table, s.cache, s.scale)
     assert np.all(np.abs(got - ref[:260]) <= 16 * 2.0 ** -23 + 48 * 2.0 ** (4 - jump) * 2.0 ** -15)
+
+
+@pytest.mark.parametrize("make,news,lens,H,KH,D,gs", BOTH, ids=name_of)
+@pytest.mark.parametrize("size", [1e-3, 1e-6, 1e3])
+def test_groups_of_one_value(gq4, make, news, lens, H, KH, D, gs, size):
+    """A group of equal values has scale 1, codes 0 and the value in its zero (the quantiser's rule);
+    a row of zeros among them.  Errors are held to the values' size, not to the scale's: the bound
+    with s (code + |z|), at most `top` here, in the place of s (8 + |z - 8|), 16 at least where s = 1."""
+    s = make(news, lens, H, KH, D, gs, 16)
+    g = I.rng(2213, H, D, gs)
+    sz = s.cache.sz[1]
+    live = ~np.isnan(sz[..., 0])                               # [page, head, slot, group]
+    ordinary = np.where(live[..., None], sz, 0.0)
+    const = live & (g.random(live.shape) < 0.5)
+    for b, n in enumerate(lens):                               # every row sees one: the first key
+        if n:
+            const[s.table[b, 0], :, 0] = True
+    lo = (size * g.uniform(-1, 1, live.shape)).astype(np.float32)
+    lo[g.random(live.shape) < 0.2] = 0.0
+    sz[..., 0] = np.where(const, 1.0, sz[..., 0] * np.float32(size))
+    sz[..., 1] = np.where(const, -lo, sz[..., 1])
+    s.cache.codes[1][np.repeat(const, gs, -1)] = 0
+    top = max(float(np.abs(lo).max()), size * float((ordinary[..., 0] * (15 + ordinary[..., 1])).max()))
+    # in the restated bound every row's vmax is that of some group with s = 1: 8 + |z - 8|
+    least = 16.0 if size < 1 else 8.0
+    close(s.run(gq4), s, min(1.0, top / least))
+    assert gq4.device_error() == 0
+
+
+@pytest.mark.parametrize("make,news,lens,H,KH,D,gs", BOTH, ids=name_of)
+def test_keys_of_one_value(gq4, make, news, lens, H, KH, D, gs):
+    """The same among the keys, under queries that make up for their size (the restated bound holds
+    as it is: it counts a key's codes and zero)."""
+    s = make(news, lens, H, KH, D, gs, 16)
+    g = I.rng(2214, H, D, gs)
+    sz = s.cache.sz[0]
+    live = ~np.isnan(sz[..., 0])
+    const = live & (g.random(live.shape) < 0.5)
+    lo = (1e-3 * g.uniform(-1, 1, live.shape)).astype(np.float32)
+    sz[..., 0] = np.where(const, 1.0, sz[..., 0] * np.float32(1e-3))
+    sz[..., 1] = np.where(const, -lo, sz[..., 1])
+    s.cache.codes[0][np.repeat(const, gs, -1)] = 0
+    s.q *= np.float32(1e3)
+    s.check(s.run(gq4))
+    assert gq4.device_error() == 0
