@@ -513,10 +513,11 @@ GQ4_API gq4_status gq4_kv_plan(int B, int T, int page_size, int max_pages, int n
  * looked at.
  *
  * max_query and max_len bound the requests' query counts and lengths (they
- * size the launch; max_len 0: max_pages * page_size).  A request beyond
- * them, or whose rows are not within T, or with a page id outside the pool
- * sets device error bit 8: rows of its queries inside T are NaN (with a bad
- * page: those that see it), nothing outside the pool or T is touched.
+ * size the launch; max_len 0: max_pages * page_size; T or max_query 0: there
+ * are no queries and the call is a no-op).  A request beyond them, or whose
+ * rows are not within T or end before they start, or with a page id outside
+ * the pool sets device error bit 8: rows of its queries inside T are NaN (with
+ * a bad page: those that see it), nothing outside the pool or T is touched.
  *
  * Held to |error| of about 1e-6 of the values' size: queries and weights are
  * two fp16 pieces each (22 bits; for requests of few rows a query row is

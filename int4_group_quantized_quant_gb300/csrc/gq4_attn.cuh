@@ -33,7 +33,7 @@ __device__ __forceinline__ AttnRequest attn_request(const AttnCall &p, int b)
     r.n = n > 0 ? (int)(n < 0x7fffffff ? n : 0x7fffffff) : 0;
     r.fill0 = max(q0, 0);
     r.fill1 = max(min(q1, p.T), r.fill0);
-    r.bad = r.n > 0 && (q0 < 0 || q1 > p.T || n > p.max_query || r.len < 0 || r.len > p.max_len);
+    r.bad = n < 0 || (r.n > 0 && (q0 < 0 || q1 > p.T || n > p.max_query || r.len < 0 || r.len > p.max_len));   // (n < 0: it has no rows)
     return r;
 }
 

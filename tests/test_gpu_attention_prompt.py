@@ -338,3 +338,17 @@ def test_keys_of_one_value(gq4, make, news, lens, H, KH, D, gs):
     s.q *= np.float32(1e3)
     s.check(s.run(gq4))
     assert gq4.device_error() == 0
+
+
+@pytest.mark.parametrize("make,news,lens,H,KH,D,gs", [BOTH[0], BOTH[2], BOTH[len(FORMS)]], ids=name_of)
+def test_rows_that_end_before_they_start(gq4, make, news, lens, H, KH, D, gs):
+    """query_start that decreases: that request has no rows and bit 8 is set; the others are served."""
+    s = make(news, lens, H, KH, D, gs, 16)
+    clean = s.run(gq4)
+    assert gq4.device_error(clear=True) == 0
+    args = s.dev()
+    args[0] = dev(np.array([0, news[0], news[0] - 2, s.starts[3]], np.int32))
+    got = s.run(gq4, args=args, max_query=max(news) + 4)
+    assert gq4.device_error(clear=True) == 1 << 8
+    assert np.array_equal(got[:news[0] - 2], clean[:news[0] - 2])
+    assert np.all(got[s.starts[3]:] == FILL)
