@@ -344,11 +344,13 @@ def test_keys_of_one_value(gq4, make, news, lens, H, KH, D, gs):
 def test_rows_that_end_before_they_start(gq4, make, news, lens, H, KH, D, gs):
     """query_start that decreases: that request has no rows and bit 8 is set; the others are served."""
     s = make(news, lens, H, KH, D, gs, 16)
-    clean = s.run(gq4)
     assert gq4.device_error(clear=True) == 0
     args = s.dev()
     args[0] = dev(np.array([0, news[0], news[0] - 2, s.starts[3]], np.int32))
     got = s.run(gq4, args=args, max_query=max(news) + 4)
     assert gq4.device_error(clear=True) == 1 << 8
-    assert np.array_equal(got[:news[0] - 2], clean[:news[0] - 2])
+    # (how keys are split depends on the other requests, so last bits may differ: the bound holds)
+    ref, tol = R.attention(s.q, s.starts, s.lens, s.table, s.cache, s.scale)
+    mine = slice(0, news[0] - 2)
+    assert np.all(np.abs(got[mine] - ref[mine]) <= tol[mine])
     assert np.all(got[s.starts[3]:] == FILL)
