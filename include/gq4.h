@@ -475,7 +475,9 @@ GQ4_API gq4_status gq4_kv_gather(int T, const gq4_kv_cache *cache, const int32_t
  *   seq_lens[b]         past + new
  *   query_start[b]      the requests' first token rows (query_start[B]: total)
  *   positions[t], slots[t]  of each new token; rows from query_start[B] to T
- *                       get position 0 and slot -1
+ *                       get position 0 and slot -1; a page id below 0 or
+ *                       whose slots pass 2^31 gives slot 2^31 - 1, outside
+ *                       any pool
  *   *free_count_out     the pages left
  * All counts are int32 and 4-byte aligned; page_table is [B][max_pages].
  * seq_lens may be past_lens, and free_count_out free_count, themselves (a

@@ -334,7 +334,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
                 // a granted page from the list itself: its table entry may be another CTA's
                 const int id = pg >= s_had[i] ? p.free_pages[avail - 1 - (s_page[i] + pg - s_had[i])]
                                               : p.page_table[(size_t)(b0 + i) * p.max_pages + pg];
-                slot = (int)((unsigned)id << shift) + (pos & (p.page - 1));
+                // an id without slots (they would wrap into the pool): a slot outside any
+                slot = (unsigned)id < (0x80000000u >> shift) ? (id << shift) + (pos & (p.page - 1)) : 0x7fffffff;
             }
             p.positions[t] = pos;
             p.slots[t] = slot;

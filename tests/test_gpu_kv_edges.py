@@ -1,0 +1,48 @@
+"""GPU tests of the cache calls' edges: page ids that are none, refusals that
+write nothing, the largest step, outputs allocated for another stream."""
+
+import numpy as np
+import pytest
+import torch
+
+from tests.gpu_util import dev, gq4_module, host, requires_cuda
+from tests.test_gpu_attention import FILL, Setup
+
+pytestmark = [pytest.mark.gpu, requires_cuda]
+
+
+@pytest.fixture(scope="module")
+def gq4():
+    g = gq4_module()
+    g.device_error(clear=True)
+    return g
+
+
+def plan(gq4, past, new, table, free, count, T, page, **kw):
+    d = [dev(np.asarray(a, np.int32)) for a in (past, new, table, free, [count])]
+    got = gq4.kv_plan(*d, T, page, **kw)
+    torch.cuda.synchronize()
+    return [host(t) for t in (d[2], *got)]
+
+
+@pytest.mark.parametrize("page", [16, 256])
+def test_page_ids_that_name_no_slot(gq4, page):
+    """An id below 0, or whose slots pass 2^31, on the free list or in the table: the token's slot is
+    2^31 - 1, outside any pool, which the writer reports; the largest id that has slots is used."""
+    top = 2**31 // page
+    free = [top - 1, top, 2**32 // page - 2**31 // page, -1, -2**31, 5, 2**31 - 1]
+    new = [1] * len(free)
+    # granted off the end of the list
+    table, lens, starts, pos, slots, left = plan(gq4, [0] * 7, new, np.full((7, 1), -9), free, 7, 7, page)
+    want = [2**31 - 1 if not 0 <= i < top else i * page for i in free[::-1]]
+    assert slots.tolist() == want and table[:, 0].tolist() == free[::-1] and left[0] == 0
+    # already in the table
+    table, lens, starts, pos, slots, left = plan(gq4, [3] * 7, new, np.array(free)[:, None], [1], 1, 7, page)
+    assert slots.tolist() == [2**31 - 1 if not 0 <= i < top else i * page + 3 for i in free]
+    assert gq4.device_error(clear=True) == 0
+    c = gq4.kv_cache(1, 1, page, 64, 32)
+    x = torch.ones((1, 1, 64), device="cuda")
+    gq4.kv_append(x, x, dev(np.array([2**31 - 1], np.int32)), *c, 32)
+    torch.cuda.synchronize()
+    assert gq4.device_error(clear=True) == 1 << 6
+    assert all(not bool(t.any()) for t in c)
