@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
         bool refused = past0 < 0 || new0 < 0;
         long long rows_in, pages_in;
         const long long row_end = rows_before + scan_sum(fresh, rows_in, sums[0]);
-        refused |= (long long)past + fresh > room || row_end > p.T;
+        refused |= (long long)past + fresh > room || (fresh > 0 && row_end > p.T);
         // refused requests aside, past + new stays below 2^31
         const int had = refused ? 0 : (past + p.page - 1) >> shift;
         const int need = refused ? 0 : ((past + fresh + p.page - 1) >> shift) - had;
@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
             p.query_start[b + 1] = (int)min(row_end, (long long)p.T);
             if (b == 0) p.query_start[0] = 0;
             p.seq_lens[b] = refused ? past : past + fresh;
-            if (refused && (fresh > 0 || past0 < 0 || new0 < 0)) atomicOr(&g_kv_error, kKvRefused);
+            if (refused) atomicOr(&g_kv_error, kKvRefused);
         }
         // granted pages of this tile
         const int granted = s_granted;

@@ -46,3 +46,13 @@ def test_page_ids_that_name_no_slot(gq4, page):
     torch.cuda.synchronize()
     assert gq4.device_error(clear=True) == 1 << 6
     assert all(not bool(t.any()) for t in c)
+
+
+def test_a_request_too_long_is_refused_without_new_tokens_too(gq4):
+    """past + new beyond the table's row sets bit 7, whether or not the request has new tokens."""
+    table, lens, starts, pos, slots, left = plan(gq4, [33, 5], [0, 1], [[1, 2], [3, -9]], [7], 1, 1, 16)
+    assert gq4.device_error(clear=True) == 1 << 7
+    assert lens.tolist() == [33, 6] and starts.tolist() == [0, 0, 1] and slots.tolist() == [3 * 16 + 5]
+    # at its end without new ones, or behind rows that were cut: nothing is refused there
+    plan(gq4, [32, 5], [0, 0], [[1, 2], [3, -9]], [7], 1, 0, 16)
+    assert gq4.device_error(clear=True) == 0
