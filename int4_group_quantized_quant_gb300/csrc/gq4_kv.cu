@@ -317,16 +317,16 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
         // granted pages of this tile
         const int granted = s_granted;
         const int page_hi = (int)min(pages_before + pages_in, (long long)granted);
-        for (int k = (int)min(pages_before, (long long)granted) + cta * kPlanThreads + threadIdx.x; k < page_hi;
-             k += n_cta * kPlanThreads) {
-            const int i = find_last(s_page, n, k);
+        // (unsigned: a stride past the last row or page may pass 2^31)
+        const unsigned lead = cta * kPlanThreads + threadIdx.x, step = n_cta * kPlanThreads;
+        for (unsigned u = (unsigned)min(pages_before, (long long)granted) + lead; u < (unsigned)page_hi; u += step) {
+            const int k = (int)u, i = find_last(s_page, n, k);
             p.page_table[(size_t)(b0 + i) * p.max_pages + s_had[i] + (k - s_page[i])] = p.free_pages[avail - 1 - k];
         }
         // its tokens
         const int row_hi = (int)min(rows_before + rows_in, (long long)p.T);
-        for (int t = (int)min(rows_before, (long long)p.T) + cta * kPlanThreads + threadIdx.x; t < row_hi;
-             t += n_cta * kPlanThreads) {
-            const int i = find_last(s_row, n, t);
+        for (unsigned u = (unsigned)min(rows_before, (long long)p.T) + lead; u < (unsigned)row_hi; u += step) {
+            const int t = (int)u, i = find_last(s_row, n, t);
             int pos = 0, slot = -1;
             if (s_past[i] >= 0) {
                 pos = s_past[i] + (t - s_row[i]);
@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
         pages_before += pages_in;
         __syncthreads();
     }
-    for (int t = (int)min(rows_before, (long long)p.T) + cta * kPlanThreads + threadIdx.x; t < p.T;
+    for (unsigned t = (unsigned)min(rows_before, (long long)p.T) + cta * kPlanThreads + threadIdx.x; t < (unsigned)p.T;
          t += n_cta * kPlanThreads) {
         p.positions[t] = 0;
         p.slots[t] = -1;
@@ -440,9 +440,8 @@ cudaError_t launch_kv_plan(const PlanCall &call, cudaStream_t stream)
     const int shift = log2_of(call.page);
     const bool in_place = call.seq_lens == call.past_lens || call.free_count_out == call.free_count;
     // a CTA for every 4096 token rows; in place at most one portable cluster
-    int grid = (call.T + 4095) / 4096;
-    const int most = in_place ? 8 : 128;
-    grid = grid < 1 ? 1 : grid > most ? most : grid;
+    const long long want = ((long long)call.T + 4095) / 4096, most = in_place ? 8 : 128;
+    const long long grid = want < 1 ? 1 : want > most ? most : want;
     if (!in_place) {
         plan_kernel<false><<<(unsigned)grid, kPlanThreads, 0, stream>>>(call, shift);
         return cudaGetLastError();

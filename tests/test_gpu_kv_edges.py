@@ -56,3 +56,20 @@ def test_a_request_too_long_is_refused_without_new_tokens_too(gq4):
     # at its end without new ones, or behind rows that were cut: nothing is refused there
     plan(gq4, [32, 5], [0, 0], [[1, 2], [3, -9]], [7], 1, 0, 16)
     assert gq4.device_error(clear=True) == 0
+
+
+def test_the_largest_step(gq4):
+    """2^31 - 1 token rows (17 GB of positions and slots), nearly all of them of no request."""
+    T = 2**31 - 1
+    out = [torch.empty(T, dtype=torch.int32, device="cuda") for _ in range(2)]
+    for o in out:
+        o.fill_(-77)
+    got = gq4.kv_plan(*[dev(np.asarray(a, np.int32)) for a in ([7], [3], [[4]], [1], [1])], T, 16, positions=out[0],
+                      slots=out[1])
+    torch.cuda.synchronize()
+    assert host(got[1]).tolist() == [0, 3]
+    assert host(out[0][:3]).tolist() == [7, 8, 9] and host(out[1][:3]).tolist() == [71, 72, 73]
+    for o, rest in zip(out, (0, -1)):
+        for part in o[3:].split(2**28):
+            assert int(part.min()) == rest and int(part.max()) == rest
+    assert gq4.device_error(clear=True) == 0
