@@ -503,7 +503,7 @@ def kv_cache(n_pages, kv_heads, page_size, head_dim, group_size, device=None):
     if group_size <= 0 or head_dim % group_size != 0 or head_dim % 8 != 0:
         raise ValueError("head_dim must be a multiple of 8 and of group_size")
     w, s = (n_pages, kv_heads, page_size, head_dim // 8), (n_pages, kv_heads, page_size, head_dim // group_size, 2)
-    device = device or "cuda"
+    device = "cuda" if device is None else device
     return tuple(torch.zeros(x, dtype=d, device=device)
                  for x, d in ((w, torch.int32), (s, torch.float32), (w, torch.int32), (s, torch.float32)))
 
