@@ -411,6 +411,21 @@ def _call(fn, name, index, stream, *args):
         raise GQ4Error(status, name)
 
 
+def _lend(stream, index, *made):
+    """Tensors that a call allocated (on the current stream) for use on another: that stream first waits for
+    what their memory was last used for here, and they are not handed out again while it uses them."""
+    if stream is None or not made or stream.cuda_stream == _raw_stream(index):
+        return
+    here = torch.cuda.current_stream(index)
+    capturing = torch.cuda.is_current_stream_capturing()
+    with torch.cuda.stream(stream):
+        capturing = capturing or torch.cuda.is_current_stream_capturing()
+    if not capturing:       # (a captured graph's memory is its own)
+        stream.wait_stream(here)
+    for t in made:
+        t.record_stream(stream)
+
+
 def _at(t, name, dtype, shape, index):
     """t's address; _need's checks (its errors) and the device's, the common case in one expression."""
     if not (isinstance(t, torch.Tensor) and t.get_device() == index and t.dtype is dtype and t.shape == shape
@@ -484,6 +499,7 @@ def head_norm_rope(q, k, positions, inv_freq, q_gain=None, k_gain=None, eps=1e-6
         raise ValueError("q or k must be given")
     T, _, D, _ = _rows(first, "k" if q is None else "q")
     index = first.get_device()
+    given = q_out, k_out
     q_out, q_gain_at, (QH, xq, ldq, yq, ldqo) = _rope_side(q, q_out, q_gain, "q", T, D, index)
     k_out, k_gain_at, (KH, xk, ldk, yk, ldko) = _rope_side(k, k_out, k_gain, "k", T, D, index)
     rot, at_pos, at_inv = 0, None, None
@@ -491,6 +507,8 @@ def head_norm_rope(q, k, positions, inv_freq, q_gain=None, k_gain=None, eps=1e-6
         rot = 2 * inv_freq.numel()
         at_inv = _at(inv_freq, "inv_freq", _f32, (rot // 2,), index)
         at_pos = _at(positions, "positions", _i32, (T,), index)
+    if stream is not None:
+        _lend(stream, index, *[y for y, was in zip((q_out, k_out), given) if was is None and y is not None])
     _call(lib.gq4_head_norm_rope, "gq4_head_norm_rope", index, stream, T, QH, KH, D,
           Rope(q_gain_at, k_gain_at, eps, rot, 1 if interleaved else 0, at_inv), at_pos, xq, ldq, xk, ldk,
           yq, ldqo, yk, ldko)
@@ -542,10 +560,13 @@ def kv_gather(slots, Kq, K_sz, Vq, V_sz, group_size, k_out=None, v_out=None, str
     _device(slots, "slots")
     T = slots.numel()
     at_slots, shape = _at(slots, "slots", _i32, (T,), index), (T, c.kv_heads, c.head_dim)
+    given = k_out, v_out
     if k_out is None:
         k_out = torch.empty(shape, dtype=_f32, device=Kq.device)
     if v_out is None:
         v_out = torch.empty(shape, dtype=_f32, device=Kq.device)
+    if stream is not None:
+        _lend(stream, index, *[y for y, was in zip((k_out, v_out), given) if was is None])
     _call(lib.gq4_kv_gather, "gq4_kv_gather", index, stream, T, c, at_slots,
           _at(k_out, "k_out", _f32, shape, index), _at(v_out, "v_out", _f32, shape, index))
     return k_out, v_out
@@ -577,6 +598,8 @@ def kv_plan(past_lens, new_lens, page_table, free_pages, free_count, n_tokens, p
         for i, part in zip(missing, spare.split_with_sizes(lens)):
             outs[i], ptrs[i] = part, at
             at += 4 * sizes[i]
+        if stream is not None:
+            _lend(stream, index, spare)
     lens, starts, pos, slt, left = ptrs
     _call(lib.gq4_kv_plan, "gq4_kv_plan", index, stream, B, n_tokens, page_size, width, n_free, at_past, at_new,
           at_table, at_free, at_count, left, lens, starts, pos, slt)
@@ -602,21 +625,23 @@ def kv_attention(q, query_start, seq_lens, page_table, Kq, K_sz, Vq, V_sz, group
     at_lens, at_start = _at(seq_lens, "seq_lens", _i32, (B,), index), \
         _at(query_start, "query_start", _i32, (B + 1,), index)
     at_table = _at(page_table, "page_table", _i32, (B, width), index)
+    made = []
     if out is None:
         out, ldo = torch.empty((T, H, D), dtype=_f32, device=q.device), H * D
+        made.append(out)
     else:
         ldo = _rows(out, "out", index, (T, H, D))[3]
-    ours = workspace is None
-    if ours:
+    if workspace is None:
         workspace = torch.empty(lib.gq4_kv_attention_workspace_bytes(T, H, c.kv_heads, D), dtype=torch.uint8,
                                 device=q.device)
+        made.append(workspace)
     elif not (isinstance(workspace, torch.Tensor) and workspace.get_device() == index and workspace.is_contiguous()):
         raise ValueError("workspace must be a contiguous CUDA tensor on the others' device")
+    if stream is not None:
+        _lend(stream, index, *made)
     _call(lib.gq4_kv_attention, "gq4_kv_attention", index, stream, B, T, H, width, max_query, max_len, c,
           q.data_ptr(), ldq, at_start, at_lens, at_table, scale, window, out.data_ptr(), ldo,
           workspace.data_ptr(), workspace.nbytes)
-    if ours and stream is not None and stream.cuda_stream != _raw_stream(index):
-        workspace.record_stream(stream)   # freed here, in use there
     return out
 
 

@@ -73,3 +73,48 @@ def test_the_largest_step(gq4):
         for part in o[3:].split(2**28):
             assert int(part.min()) == rest and int(part.max()) == rest
     assert gq4.device_error(clear=True) == 0
+
+
+def test_outputs_allocated_for_another_stream(gq4):
+    """What a call allocates may be memory whose last use is still under way on the current stream:
+    the call's own stream waits for it, and it is not handed out again while that stream uses it."""
+    s = Setup([1, 1], [3000, 900], 8, 2, 128, 128, 16)
+    clean = s.run(gq4)
+    live = int(s.starts[-1])
+    args, q = s.dev(), dev(s.q)
+    k = torch.ones((64, 2, 128), device="cuda")
+    slots = torch.arange(64, dtype=torch.int32, device="cuda")
+    cache = gq4.kv_cache(4, 2, 16, 128, 128)
+    gq4.kv_append(k, k, slots, *cache, 128)
+    inv = torch.ones(64, device="cuda")
+    lens, new = (torch.full((1,), n, dtype=torch.int32, device="cuda") for n in (0, 64))
+    table = torch.zeros((1, 4), dtype=torch.int32, device="cuda")
+    free, count = torch.arange(4, dtype=torch.int32, device="cuda"), torch.full((1,), 4, dtype=torch.int32,
+                                                                                device="cuda")
+    side = torch.cuda.Stream()
+    calls = {
+        "attention": lambda: (gq4.kv_attention(q, *args, scale=s.scale, max_query=1, max_len=3000, stream=side),),
+        "rope": lambda: gq4.head_norm_rope(k, None, slots, inv, stream=side)[:1],
+        "gather": lambda: gq4.kv_gather(slots, *cache, 128, stream=side),
+        "plan": lambda: gq4.kv_plan(lens, new, table, free, count, 64, 16, stream=side),
+    }
+    for name, call in calls.items():
+        torch.cuda.synchronize()
+        want = [host(t) for t in call()]
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()
+        # blocks of every size the call may ask for, freed with a write of theirs under way
+        held = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in
+                (512, 1024, 2048, 4096, 20480, 65536, gq4.kv_attention_workspace_bytes(s.T, 8, 2, 128)) for _ in "ab"]
+        torch.cuda._sleep(100_000_000)
+        for t in held:
+            t.fill_(255)
+        del held, t
+        got = call()
+        side.synchronize()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            a = host(a)
+            if name == "attention":
+                a, b = a[:live], clean[:live]
+            assert np.array_equal(a, b), name
