@@ -521,11 +521,21 @@ GQ4_API gq4_status gq4_kv_plan(int B, int T, int page_size, int max_pages, int n
  * the pool sets device error bit 8: rows of its queries inside T are NaN (with
  * a bad page: those that see it), nothing outside the pool or T is touched.
  *
- * Held to |error| of about 1e-6 of the values' size: queries and weights are
- * two fp16 pieces each (22 bits; for requests of few rows a query row is
- * fixed-point with a power-of-two scale, each value within 2^-22 of the
- * row's largest magnitude), the codes are exact, sums are f32 (requests of
- * many rows and several groups: the keys and values are two pieces too).
+ * A query, key or value that is not finite makes NaN of the rows that see it:
+ * all of the row, or with several groups per row at least the columns of a
+ * value's group.
+ *
+ * Held to |error| of about 1e-6 of the largest value that the row sees: queries
+ * and weights are two fp16 pieces each (22 bits; for requests of few rows a
+ * query row is fixed-point with a power-of-two scale, each value within 2^-22
+ * of the row's largest magnitude; for requests of many rows, within 2^-25 of
+ * it), the codes are exact, sums are f32, cut rather than rounded within 64 to
+ * 128 keys by the tensor cores (requests of many rows and several groups: the
+ * keys and values are two pieces too).  What shares a power of two of those
+ * pieces and is too small for it -- query rows, or all the values that a row
+ * sees, less than 2^-12 of their neighbours' in a tile of 128 rows and 64 keys;
+ * groups of equal values below 0.004 -- is computed in f32 at the call's end,
+ * at about a fortieth of the speed.
  * How a request's keys are split over the GPU depends on the other requests,
  * on max_query and on max_len, so their change may change last bits; the same
  * inputs give the same bits.

@@ -354,3 +354,32 @@ def test_rows_that_end_before_they_start(gq4, make, news, lens, H, KH, D, gs):
     mine = slice(0, news[0] - 2)
     assert np.all(np.abs(got[mine] - ref[mine]) <= tol[mine])
     assert np.all(got[s.starts[3]:] == FILL)
+
+
+@pytest.mark.parametrize("make,news,lens,H,KH,D,gs",
+                         [c for c in BOTH if c[5] > c[6]], ids=name_of)
+def test_a_value_group_that_is_not_finite(gq4, make, news, lens, H, KH, D, gs):
+    """A NaN scale of one group of one value row: the rows that see it are NaN in that group's
+    columns at least (all of theirs in the prompt kernel), the others as they were."""
+    s = make(news, lens, H, KH, D, gs, 16)
+    clean = s.run(gq4)
+    ref, tol = R.attention(s.q, s.starts, s.lens, s.table, s.cache, s.scale)
+    R_, n, L, at = H // KH, news[0], lens[0], lens[0] - 2
+    sees = np.arange(n) + L - n >= at
+    for group in range(D // gs):
+        kept = s.cache.sz[1][s.table[0, at // 16], 0, at % 16, group].copy()
+        s.cache.sz[1][s.table[0, at // 16], 0, at % 16, group] = np.nan
+        got = s.run(gq4)
+        s.cache.sz[1][s.table[0, at // 16], 0, at % 16, group] = kept
+        cols = np.zeros(D, bool)
+        cols[group * gs:(group + 1) * gs] = True
+        mine = got[:n][sees][:, :R_]
+        assert np.isnan(mine[..., cols]).all()
+        if make is few:
+            err = np.abs(mine - ref[:n][sees][:, :R_])[..., ~cols]
+            assert np.all(err <= tol[:n][sees][:, :R_][..., ~cols])
+        else:
+            assert np.isnan(mine).all()
+        assert np.array_equal(got[:n][~sees], clean[:n][~sees]) and np.array_equal(got[n:], clean[n:])
+        assert np.array_equal(got[:n][sees][:, R_:], clean[:n][sees][:, R_:])
+    assert gq4.device_error() == 0
