@@ -755,7 +755,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         }
 #pragma unroll
         for (int n = 0; n < kTurns; ++n) {
+            const int i = th + n * kStaging;
             const float m = largest(q[n]);
+            if (i % (DP / 8) == 0 && i < kRows * (DP / 8)) reinterpret_cast<float *>(smem + M::offL)[i / (DP / 8)] = m;
             big = fmaxf(big, m);
             if (m > 0.0f) small = fminf(small, m);
         }
@@ -769,13 +771,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         kq = scale_exponent(__int_as_float(s_big));
         if (s_small < 0x7f800000 && scale_exponent(__int_as_float(s_small)) - kq > kSpread) {
             // rows of less than 2^-kSpread of the largest would lose digits to it
-#pragma unroll
-            for (int n = 0; n < kTurns; ++n) {
-                const int i = th + n * kStaging, r = i / (DP / 8);
-                const float m = largest(q[n]);
-                if (i % (DP / 8) == 0 && m > 0.0f && scale_exponent(m) - kq > kSpread)
-                    atomicOr(&s_apart[r >> 5], 1u << (r & 31));
-            }
+            const float m = th < kRows ? reinterpret_cast<const float *>(smem + M::offL)[th] : 0.0f;
+            if (m > 0.0f && scale_exponent(m) - kq > kSpread) atomicOr(&s_apart[th >> 5], 1u << (th & 31));
         }
         const float up = pow2(kq);
 #pragma unroll
@@ -1110,7 +1107,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                 ok = false;
                 break;
             }
-            float vb = 0.0f, by[2];
+            float vb = 0.0f;
             bool ones = false;             // a scale of 1: a group of equal values, most likely
             if (EXACT) {
                 // (nobody else reads the scales of this form)
@@ -1119,7 +1116,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                 for (int y = 0; y < 4; ++y) ones |= lds_f1(zat + (y & 1) * 256 + (y >> 1) * M::kRawSz) == 1.0f;
                 if (__any_sync(0xffffffffu, ones)) fit_equal_rows<J>(raw);   // rare
             }
-#pragma unroll
+#pragma unroll EXACT ? 2 : 1
             for (int y = 0; y < 2; ++y) {
                 const int key = lane + 32 * y, t = (tile_lo + i) * kTile + key;
                 const uint32_t zat = smem_s + M::offRaw + 2 * M::kRawCodes + (uint32_t)rs * M::kRawSlot + key * 8 * G;
@@ -1135,14 +1132,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                     at[0] = F;
                     at[kTile] = (8.0f - ks[0].y) * F;
                     at[3 * kTile] = spoilt ? 0.0f : vs[0].y - 8.0f;
-                    by[y] = spoilt ? 0.0f : vs[0].x;
+                    at[2 * kTile] = spoilt ? 0.0f : vs[0].x;
                     if (!spoilt) vb = fmaxf(vb, fabsf(vs[0].x));
                 } else {
                     at[0] = spoilt ? quiet_nan() : Fq * pow2(-k.exponent());
                     // (a row of zeros has no power: any but 0 would be too large beside its neighbours')
 #pragma unroll
                     for (int g = 0; g < G; ++g) ones |= ks[g].x == 1.0f || vs[g].x == 1.0f;
-                    by[y] = v.finite && v.bound > 0.0f ? pow2(-min(v.exponent(), 80)) : 0.0f;
+                    at[kTile] = v.finite && v.bound > 0.0f ? pow2(-min(v.exponent(), 80)) : 0.0f;
                     if (!spoilt) vb = fmaxf(vb, v.bound);
                 }
             }
@@ -1158,10 +1155,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             // by the tile's largest V (EXACT: its scale), as a power of two: P is
             // held times 2^e, so that 2^kSlack of it is below 2^15
             const int ve = min(scale_exponent(__uint_as_float(top)), 80), e = EXACT ? ve - 2 : ve + kPieceBits;
-#pragma unroll
-            for (int y = 0; y < 2; ++y)
-                reinterpret_cast<float *>(smem + M::offF)[(tab * (EXACT ? 4 : 2) + (EXACT ? 2 : 1)) * kTile + lane + 32 * y] =
-                    by[y] * pow2(e);
+            float *at = reinterpret_cast<float *>(smem + M::offF) + (tab * (EXACT ? 4 : 2) + (EXACT ? 2 : 1)) * kTile + lane;
+            const float by[2] = {at[0], at[32]};
+            at[0] = by[0] * pow2(e);
+            at[32] = by[1] * pow2(e);
             if (lane == 0) reinterpret_cast<float *>(smem + M::offVm)[tab] = pow2(-e);
             // where some row may not see the largest (uniform)
             const int k0 = (tile_lo + i) * kTile;
