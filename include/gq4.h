@@ -540,8 +540,8 @@ GQ4_API gq4_status gq4_kv_plan(int B, int T, int page_size, int max_pages, int n
  * on max_query and on max_len, so their change may change last bits; the same
  * inputs give the same bits.
  *
- * workspace: at least gq4_kv_attention_workspace_bytes() bytes of device
- * memory, 256-byte aligned, no argument's; contents need not be set and
+ * workspace: at least gq4_kv_attention_workspace_bytes() bytes (more for more
+ * rows) of device memory, 256-byte aligned, no argument's; contents need not be set and
  * nothing is kept in it between calls.  Calls that may overlap on the GPU
  * need one each.  out rows are ld_out floats apart, 16-byte aligned. */
 GQ4_API size_t gq4_kv_attention_workspace_bytes(int T, int q_heads, int kv_heads, int head_dim);

@@ -19,12 +19,15 @@
 //   Keys: a word's nibbles i and i+4 are masked in place, an fp16 pair
 // c 2^-24 (c 2^-20 for odd i: q is pre-scaled by 1/16 there).
 //   Values: nibbles of two tokens are paired by a byte permute, OR-ed with
-// 1024 and shifted to c - 8 by one exact fp16 operation.  Without the 8 the
+// 1024 and shifted to c - 8 by one exact fp16 operation (conversion by the
+// exponent's bits, as Kim, Henry, Fahim and Awadalla published it in 2022).  Without the 8 the
 // sums would carry the codes' mean, several times the result, and its
 // rounding.
 //   The second product stays in the tensor core for 4 stages (128 keys of a
 // warp) and is then added to f32 sums: cut sums of a whole context would be
-// off by 2.6e-6 at 131072 keys instead of 1.1e-6.
+// off by 2.0e-6 of the result at 125k keys instead of 4.5e-7.
+//   A group of equal values (scale 1) is given a scale of its own size first,
+// in shared memory: the 8 taken off its codes would drown small ones.
 //   The running maximum m moves only when a weight passes 2^4 of it (a vote
 // per 32 keys), so that accumulators are rescaled rarely; the scales of the
 // values that a row sees likewise share a power of two 2^E, which keeps p s
@@ -47,14 +50,18 @@
 // are assigned to the instruction's rows so that both products read shared
 // memory without bank conflicts (see key_of_row).
 //
-// Measured: 48 requests of 500 to 8192 keys, 32 heads over 8 of 128, one
-// group: 47 us, 215 MB at 4.6 TB/s; two of 125k keys, two groups: 65 us, 319
-// MB at 4.9 TB/s; 16 drafts of 5 tokens, 16 heads of 64, two groups: 30 us; one
-// request of 776 keys: 10 us, of which 2 the ranges, 2 the first loads, 1 a
+// Measured in a graph: 48 requests of 500 to 8192 keys, 32 heads over 8 of 128,
+// one group: 47 us, 215 MB at 4.6 TB/s; two of 125k keys, two groups: 64 us,
+// 319 MB at 5.0 TB/s; 16 drafts of 5 tokens, 16 heads of 64, two groups: 30 us;
+// one request of 776 keys: 10 us, of which 2 the ranges, 2 the first loads, 1 a
 // stage, 2 the CTA's join and 3 the second kernel.
-// Bound by instructions: 685 per stage and warp, 32 of them matrix
-// instructions and 240 the decoding of codes, issued in 60% of the cycles by
-// the 16 warps that registers allow (128 per thread).
+// Instructions: 685 per stage and warp, 32 of them matrix instructions and 240
+// the decoding of codes, issued in 60% of the cycles by the 16 warps that
+// registers allow (128 per thread, of which the 4-row form at heads of 128
+// spills 92 bytes).
+// A row block of a prompt is given all stages up to the request's last key and
+// walks past those that it does not see, which the equal cut counts: prompts
+// that stay here lose up to half of their time to it.
 #include <cuda_fp16.h>
 
 #include <atomic>
@@ -1235,7 +1242,8 @@ cudaError_t launch_attn(const AttnCall &in, cudaStream_t stream)
     // 16 requests of 8 tokens (32 rows each, 4096 in all) 88 us there and 83
     // here, of 12 (48, 6144) 88 and 116, of 16 89 and 150; one request of 64
     // tokens (256, 2048) 90 and 50.  Four groups: of 12 169 and 150, of 16
-    // 170 and 197.
+    // 170 and 197.  (Measured at this shape only; with four groups the border
+    // lies somewhat higher, and few rows behind a long past leave SMs idle.)
     AttnCall call = in;
     const long long R = call.heads / call.c.kv_heads;
     const bool prompt = prompt_path_supported(call) && call.max_query * R >= kPromptRows &&

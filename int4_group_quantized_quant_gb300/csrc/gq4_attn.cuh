@@ -1,5 +1,6 @@
 // gq4_attn.cuh -- what the attention kernels share: a request's rows and keys,
-// the base-2 exponential, asynchronous copies into shared memory.
+// the base-2 exponential, asynchronous copies into shared memory, groups of
+// equal values, and the rows of a prompt that are computed apart.
 #pragma once
 
 #include <cstdint>

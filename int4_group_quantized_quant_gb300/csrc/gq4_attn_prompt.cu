@@ -36,14 +36,16 @@
 // is four (two).  S runs ahead of P V by as many tiles as it has slots.
 // K is stored [key][d] (K-major), V [key][d] as well, which is the MN-major
 // form of the second product's B operand: no transposition.
-// Measured, 32 heads over 8 of 128: a prompt of 6007 tokens, one group, 657 us
-// (296 GFLOP by the formula, 450 TFLOP/s; twice that in the MMAs, 0.47 of the
-// measured bf16 peak); three chunks of 1021 tokens behind 1000 to 4096 with a
-// window of 2048, four groups, 452 us (103 GFLOP, 227 TFLOP/s; three times that
-// in the MMAs).  Bound by the latency and issue slots of the softmax, adding and
+// Measured in a graph, 32 heads over 8 of 128: a prompt of 6007 tokens, one
+// group, 664 us (296 GFLOP by the formula, 446 TFLOP/s; twice that in the MMAs,
+// 0.46 of the measured bf16 peak); three chunks of 1021 tokens behind 1000 to
+// 4096 with a window of 2048, four groups, 459 us (103 GFLOP, 224 TFLOP/s;
+// three times that in the MMAs).  Bound by the latency and issue slots of the softmax, adding and
 // dequantising warps (issue active in half of the cycles, the tensor pipe in a
 // third): a tile takes 2150 cycles, its MMAs 1080; and a CTA starts and ends in
-// 18 thousand, of which the queries are 6 and the rows' way out 5.
+// 18 thousand, of which the queries are 6 and the rows' way out 5.  The roles
+// fill the registers and share the instruction cache: code for rare cases costs
+// 1 to 6 % here whether it runs or not, so it is the last kernel's.
 #include <cuda_fp16.h>
 
 #include <atomic>

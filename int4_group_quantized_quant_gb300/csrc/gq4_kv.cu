@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
 // Reader: a lane dequantises 4 consecutive values (half a word), so that a
 // warp stores 512 contiguous bytes at a time; the same 4 of every row that it
 // takes.  Bound by HBM writes: 16381 tokens of 8 heads of 128 take 22 us
-// (153 MB, 7.0 TB/s; the codes come from L2 when just written).
+// (153 MB, 7.0 TB/s) with the codes in L2, just written, and 27 cold.
 // ---------------------------------------------------------------------------
 struct GatherParams {
     gq4_kv_cache c;
@@ -234,8 +234,8 @@ __global__ void __launch_bounds__(kGatherThreads<J>) gather_kernel(const __grid_
 // of the tile's first rows.  So no CTA waits for another, unless lengths or
 // the count are advanced in place: then the CTAs are one cluster, which meets
 // after the tile is read and before it is overwritten.  Latency-bound (a few
-// kB): 64 requests of one token 4.2 us, 2000 requests of up to 256 tokens (257k
-// tokens, 2.1 MB written) 10.5 us.
+// kB): 64 requests of one token 4 us, 2000 requests of up to 256 tokens (257k
+// tokens, 2.1 MB written) 10 us.
 // ---------------------------------------------------------------------------
 constexpr int kPlanThreads = 1024;
 

@@ -21,7 +21,7 @@
 // Angles: pos * inv_freq is a 31-bit by 24-bit product; in binary64 its error
 // is below 2^-22 of a radian at any position.  It is reduced modulo 2 pi in
 // binary64 with a two-term constant (Cody and Waite's reduction) and handed
-// to sincosf as a value in [-pi, pi].
+// to sincosf as a value in [-pi, pi], rounded to f32: 1.2e-7 of a radian.
 #include <cstdint>
 
 #include "gq4_kv_internal.h"
