@@ -55,7 +55,7 @@
 // 319 MB at 5.0 TB/s; 16 drafts of 5 tokens, 16 heads of 64, two groups: 30 us;
 // one request of 776 keys: 10 us, of which 2 the ranges, 2 the first loads, 1 a
 // stage, 2 the CTA's join and 3 the second kernel.
-// Instructions: 685 per stage and warp, 32 of them matrix instructions and 240
+// Instructions: 675 per stage and warp, 32 of them matrix instructions and 240
 // the decoding of codes, issued in 60% of the cycles by the 16 warps that
 // registers allow (128 per thread, of which the 4-row form at heads of 128
 // spills 92 bytes).
