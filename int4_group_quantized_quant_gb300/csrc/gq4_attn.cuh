@@ -174,7 +174,10 @@ __device__ __noinline__ void apart_rows(const AttnCall &a, const ApartTile &at, 
     constexpr int D = 32 * J, GS = D / G;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = at.request;
     const int R = a.heads / a.c.kv_heads, shift = 31 - __clz(a.c.page_size);
+    // (marks that another call wrote over must not lead out of bounds)
+    if ((uint32_t)b >= (uint32_t)a.B) return;
     const AttnRequest rq = attn_request(a, b);
+    if (rq.bad || (uint32_t)at.tile >= (uint32_t)((rq.n * R + kPromptTile - 1) / kPromptTile)) return;
     const int32_t *table = a.page_table + (size_t)b * a.max_pages;
     float *q = s.q[warp];
     __syncthreads();

@@ -383,3 +383,20 @@ def test_a_value_group_that_is_not_finite(gq4, make, news, lens, H, KH, D, gs):
         assert np.array_equal(got[:n][~sees], clean[:n][~sees]) and np.array_equal(got[n:], clean[n:])
         assert np.array_equal(got[:n][sees][:, R_:], clean[:n][sees][:, R_:])
     assert gq4.device_error() == 0
+
+
+@pytest.mark.parametrize("n,B,idle", [(12, 40, 0), (12, 17, 300), (13, 25, 900), (33, 30, 5)])
+def test_requests_of_the_fewest_rows(gq4, n, B, idle):
+    """Requests of 48 query rows per kv head, the fewest of this kernel, and a little more, between
+    others without queries or with one: the launch has a tile for each, and a mark for each tile."""
+    g = I.rng(2215, n, B, idle)
+    news = [n] * B + g.integers(0, 2, idle).tolist()
+    lens = [n + int(x) for x in g.integers(0, 60, B)] + [1 + int(x) for x in g.integers(0, 30, idle)]
+    order = g.permutation(B + idle)
+    news, lens = [news[i] for i in order], [lens[i] for i in order]
+    for H, KH, D, gs in ((32, 8, 64, 64), (32, 8, 64, 32)):
+        s = prompt(news, lens, H, KH, D, gs, 16)
+        s.check(s.run(gq4))
+        s.q *= np.exp2(g.integers(-20, 20, s.q.shape[:2])).astype(np.float32)[..., None]
+        close(s.run(gq4), s)
+    assert gq4.device_error() == 0
