@@ -553,6 +553,38 @@ GQ4_API gq4_status gq4_kv_attention(int B, int T, int q_heads, int max_pages, in
                                     float *out, int ld_out, void *workspace,
                                     size_t workspace_bytes, cudaStream_t stream);
 
+/* The same with other keys in sight.  A row's position p is seq_len - n + j as
+ * above or, with `tree`, positions[row] (used with a window only, and taken as
+ * seq_len - n at the least and seq_len - 1 at the most).
+ *   window, sinks   a row sees, of the keys of its request up to its own (with
+ *       `tree`: before the n new ones), those from p + 1 - window on and the
+ *       first `sinks` ones, which a window does not hide (attention sinks:
+ *       Xiao, Tian, Chen, Han and Lewis, 2023).  window 0: all of them.
+ *   tree            drafted tokens that are not one line but a tree: row r's
+ *       words tree[r * tree_words ...] say which of its request's n new keys it
+ *       sees, bit i % 32 of word i / 32 for new key i, whatever the window.
+ *       Any bits do (gq4_kv_tree makes those of a tree from its parents); bits
+ *       from n on count for nothing.  A request of more than 32 * tree_words
+ *       queries is beyond the call's bounds (NaN rows, bit 8).  NULL: none.
+ * Everything else -- pages, bounds, errors, accuracy, workspace, a row that sees
+ * nothing -- is gq4_kv_attention's; without tree and sinks it is that call. */
+#define GQ4_MAX_TREE_WORDS 8
+typedef struct gq4_kv_mask {
+    int window;                 /* 0: none */
+    int sinks;                  /* >= 0 */
+    const uint32_t *tree;       /* [T][tree_words] or NULL */
+    int tree_words;             /* 1 .. GQ4_MAX_TREE_WORDS */
+    const int32_t *positions;   /* [T]; may be NULL without a tree or a window */
+} gq4_kv_mask;
+
+GQ4_API gq4_status gq4_kv_attention_masked(int B, int T, int q_heads, int max_pages, int max_query,
+                                           int max_len, const gq4_kv_cache *cache, const float *q,
+                                           int ldq, const int32_t *query_start,
+                                           const int32_t *seq_lens, const int32_t *page_table,
+                                           float scale, const gq4_kv_mask *mask, float *out,
+                                           int ld_out, void *workspace, size_t workspace_bytes,
+                                           cudaStream_t stream);
+
 /* Integer unpack test kernel: q[n*K + k] = q(n,k) as u8 [N][K].
  * Uses the same in-register extraction as the matvec kernels.
  * Requires K % 32 == 0. */

@@ -24,6 +24,7 @@ struct AttnRequest {
     int fill0, fill1;
 };
 
+template <bool MASKS>
 __device__ __forceinline__ AttnRequest attn_request(const AttnCall &p, int b)
 {
     AttnRequest r;
@@ -35,6 +36,7 @@ __device__ __forceinline__ AttnRequest attn_request(const AttnCall &p, int b)
     r.fill0 = max(q0, 0);
     r.fill1 = max(min(q1, p.T), r.fill0);
     r.bad = n < 0 || (r.n > 0 && (q0 < 0 || q1 > p.T || n > p.max_query || r.len < 0 || r.len > p.max_len));   // (n < 0: it has no rows)
+    if (MASKS && p.tree && n > 32ll * p.tree_words) r.bad = true;
     return r;
 }
 
@@ -48,6 +50,70 @@ __device__ __forceinline__ bool prompt_takes(const AttnCall &p, const AttnReques
 __device__ __forceinline__ int attn_first(const AttnCall &p, int last)
 {
     return p.window > 0 ? max(0, last + 1 - p.window) : 0;
+}
+
+// ---- What a row sees in the masked form ----
+// Without bits: keys first .. last of the causal rule, and of those up to last
+// the first p.sinks.  With them: the same of the keys before the request's new
+// ones, at the row's own position (taken as at least the first new token's and
+// at most the last's), and new key i where bit i of the row is set.
+struct RowSight {
+    int first, last;
+    int past, len;          // new keys are past .. len - 1
+    const uint32_t *bits;   // NULL: none
+};
+
+// Of the row of token j of its request.
+__device__ __forceinline__ RowSight row_sight(const AttnCall &p, const AttnRequest &r, int j)
+{
+    RowSight s;
+    s.past = r.len - r.n;
+    s.len = r.len;
+    s.bits = nullptr;
+    int at = s.last = s.past + j;
+    if (p.tree) {
+        s.bits = p.tree + (size_t)(r.row0 + j) * p.tree_words;
+        s.last = s.past - 1;
+        if (p.window > 0) at = min(max(__ldg(p.positions + r.row0 + j), s.past), s.len - 1);
+    }
+    s.first = attn_first(p, max(at, -1));
+    return s;
+}
+
+// Bit x: lo <= k0 + x <= hi.
+__device__ __forceinline__ uint32_t range_bits(int k0, int lo, int hi)
+{
+    const int a = min(max(lo - k0, 0), 32), n = min(hi - k0, 31) + 1 - a;
+    return n <= 0 ? 0u : (0xffffffffu >> (32 - n)) << a;
+}
+
+// Bit x: the row sees key k0 + x (k0 >= 0).
+__device__ __forceinline__ uint32_t sight_bits(const AttnCall &p, const RowSight &s, int k0)
+{
+    uint32_t seen = range_bits(k0, s.first, s.last);
+    if (p.window > 0) seen |= range_bits(k0, 0, min(p.sinks - 1, s.last));
+    if (s.bits && k0 + 31 >= s.past) {
+        const int o = k0 - s.past, w = o >> 5;     // bits o .. o + 31, from -31 on
+        const uint32_t lo = w >= 0 && w < p.tree_words ? __ldg(s.bits + w) : 0u;
+        const uint32_t hi = w + 1 >= 0 && w + 1 < p.tree_words ? __ldg(s.bits + w + 1) : 0u;
+        seen |= __funnelshift_r(lo, hi, o & 31) & range_bits(k0, max(s.past, 0), s.len - 1);
+    }
+    return seen;
+}
+
+// A tree's rows may all see every key before the new ones, and some the last.
+__device__ __forceinline__ void tree_bounds(const AttnCall &p, const AttnRequest &r, int &see_hi, int &all_hi)
+{
+    if (!p.tree) return;
+    see_hi = r.len - 1;
+    all_hi = r.len - r.n - 1;
+}
+
+// Blocks of `width` keys that hold the first tokens, before the one of see_lo,
+// the first key of a window.
+__device__ __forceinline__ int lead_blocks(const AttnCall &p, int see_lo, int width)
+{
+    return p.window > 0 ? min((p.sinks + width - 1) / width, see_lo / width) : 0;
 }
 
 __device__ __forceinline__ float exp2_approx(float x)
@@ -116,17 +182,19 @@ struct ApartShared {
 
 // Marks the rows of a tile that see, of some 64 keys, only values less than
 // 2^-kSpread of the largest.  By the whole CTA.
-template <int J, int G>
+template <int J, int G, bool MASKS>
 __device__ __noinline__ void small_rows(const AttnCall &a, const AttnRequest &rq, const ApartTile &at, int h, uint32_t *rows)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int R = a.heads / a.c.kv_heads, shift = 31 - __clz(a.c.page_size);
     const int row0 = at.tile * kPromptTile, row_hi = min(row0 + kPromptTile, rq.n * R) - 1, pos0 = rq.len - rq.n;
     // keys that some row sees; keys that all rows see
-    const int see_hi = pos0 + row_hi / R, all_hi = pos0 + row0 / R;
-    const int see_lo = attn_first(a, max(all_hi, -1)), all_lo = attn_first(a, max(see_hi, -1));
+    int see_hi = pos0 + row_hi / R, all_hi = pos0 + row0 / R;
+    if constexpr (MASKS) tree_bounds(a, rq, see_hi, all_hi);
+    const int see_lo = attn_first(a, max(MASKS && a.tree ? all_hi + 1 : all_hi, -1)), all_lo = attn_first(a, max(see_hi, -1));
+    const int kept = MASKS && a.window > 0 ? a.sinks : 0, lead = MASKS ? lead_blocks(a, see_lo, kPromptKeys) : 0;
     auto size_of = [&](int t) {
-        if (t < see_lo || t > see_hi) return 0.0f;
+        if ((t < see_lo && !(MASKS && t < kept)) || t > see_hi) return 0.0f;
         const int page = __ldg(a.page_table + (size_t)at.request * a.max_pages + (t >> shift));
         if ((uint32_t)page >= (uint32_t)a.c.n_pages) return 0.0f;
         const size_t row = kv_row(a.c, page, h, t & (a.c.page_size - 1));
@@ -147,14 +215,25 @@ __device__ __noinline__ void small_rows(const AttnCall &a, const AttnRequest &rq
         return size;
     };
     auto largest = [](float x) { return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(x))); };
-    for (int k0 = (see_lo / kPromptKeys + warp) * kPromptKeys; k0 <= see_hi; k0 += kPromptKeys * (kJoinThreads / 32)) {
+    for (int i = warp;; i += kJoinThreads / 32) {
+        const int k0 = (MASKS && i < lead ? i : see_lo / kPromptKeys + i - lead) * kPromptKeys;
+        if (k0 > see_hi) break;
         if (k0 + kPromptKeys - 1 <= all_hi && k0 >= all_lo) continue;
         const int t0 = k0 + lane, t1 = t0 + 32;
         const float v0 = size_of(t0), v1 = size_of(t1);
         const int power = scale_exponent(largest(fmaxf(v0, v1)));
         for (int j = row0 / R; j <= row_hi / R; ++j) {
-            const int last = pos0 + j, first = attn_first(a, max(last, -1));
-            const float top = largest(fmaxf(t0 <= last && t0 >= first ? v0 : 0.0f, t1 <= last && t1 >= first ? v1 : 0.0f));
+            bool in0, in1;
+            if constexpr (MASKS) {
+                const RowSight s = row_sight(a, rq, j);
+                in0 = sight_bits(a, s, k0) >> lane & 1u;
+                in1 = sight_bits(a, s, k0 + 32) >> lane & 1u;
+            } else {
+                const int last = pos0 + j, first = attn_first(a, max(last, -1));
+                in0 = t0 <= last && t0 >= first;
+                in1 = t1 <= last && t1 >= first;
+            }
+            const float top = largest(fmaxf(in0 ? v0 : 0.0f, in1 ? v1 : 0.0f));
             if (top == 0.0f || scale_exponent(top) - power <= kSpread) continue;
             for (int r = max(j * R - row0, 0) + lane; r <= min(j * R + R - 1, row_hi) - row0; r += 32)
                 atomicOr(&rows[r >> 5], 1u << (r & 31));
@@ -168,7 +247,7 @@ __device__ __noinline__ void small_rows(const AttnCall &a, const AttnRequest &rq
 // the call's last kernel: such code in the prompt kernel itself, run or not,
 // cost it 1 to 6 % (its roles fill the registers and share the instruction
 // cache).  By the whole CTA.
-template <int J, int G>
+template <int J, int G, bool MASKS>
 __device__ __noinline__ void apart_rows(const AttnCall &a, const ApartTile &at, int h, ApartShared<J> &s)
 {
     constexpr int D = 32 * J, GS = D / G;
@@ -176,20 +255,25 @@ __device__ __noinline__ void apart_rows(const AttnCall &a, const ApartTile &at, 
     const int R = a.heads / a.c.kv_heads, shift = 31 - __clz(a.c.page_size);
     // (marks that another call wrote over must not lead out of bounds)
     if ((uint32_t)b >= (uint32_t)a.B) return;
-    const AttnRequest rq = attn_request(a, b);
+    const AttnRequest rq = attn_request<MASKS>(a, b);
     if (rq.bad || (uint32_t)at.tile >= (uint32_t)((rq.n * R + kPromptTile - 1) / kPromptTile)) return;
     const int32_t *table = a.page_table + (size_t)b * a.max_pages;
     float *q = s.q[warp];
     __syncthreads();
     if (threadIdx.x < kPromptTile / 32) s.rows[threadIdx.x] = at.rows[threadIdx.x];
     __syncthreads();
-    if (at.uneven) small_rows<J, G>(a, rq, at, h, s.rows);
+    if (at.uneven) small_rows<J, G, MASKS>(a, rq, at, h, s.rows);
     __syncthreads();
     for (int r = warp; r < kPromptTile; r += kJoinThreads / 32) {
         if (!(s.rows[r >> 5] >> (r & 31) & 1u)) continue;
         const int rho = at.tile * kPromptTile + r, j = rho / R, head = h * R + rho - j * R;
         if (rho >= rq.n * R) break;
-        const int last = rq.len - rq.n + j, first = attn_first(a, max(last, -1));
+        // MASKS: blocks of 32 keys from the first on, those between the first tokens and the window left out
+        const RowSight sight = MASKS ? row_sight(a, rq, j) : RowSight{};
+        const int last = MASKS ? (a.tree ? rq.len - 1 : sight.last) : rq.len - rq.n + j;
+        const int first = MASKS ? (a.tree ? min(sight.first, max(sight.past, 0)) : sight.first) & ~31 : attn_first(a, max(last, -1));
+        const int lead = MASKS ? 32 * lead_blocks(a, first, 32) : 0;
+        bool some = false;
         const float *qg = a.q + (size_t)(rq.row0 + j) * a.ldq + (size_t)head * D;
         float x[J], big = 0.0f;        // the row at a size of 1 to 2, undone in its factor
 #pragma unroll
@@ -204,12 +288,15 @@ __device__ __noinline__ void apart_rows(const AttnCall &a, const ApartTile &at, 
         const float factor = ldexpf(a.scale * kLog2e, e);
         __syncwarp();
         float m = -INFINITY, l = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        for (int k0 = first; k0 <= last; k0 += 32) {
-            const int t = k0 + lane;
+        for (int k = first - lead; k <= last; k += 32) {
+            const int k0 = MASKS && k < first ? k - (first - lead) : k, t = k0 + lane;
+            const uint32_t seen = MASKS ? sight_bits(a, sight, k0) : 0u;
+            if (MASKS && seen == 0) continue;
+            some = true;
             size_t row = 0;
             bool in = false;
             float w = -INFINITY;
-            if (t <= last) {
+            if (MASKS ? seen >> lane & 1u : t <= last) {
                 const int page = __ldg(table + (t >> shift));
                 in = (uint32_t)page < (uint32_t)a.c.n_pages;
                 w = quiet_nan();       // a page outside the pool
@@ -239,7 +326,8 @@ __device__ __noinline__ void apart_rows(const AttnCall &a, const ApartTile &at, 
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[i] *= f;
 #pragma unroll 1
-            for (int x = 0; x < min(32, last - k0 + 1); ++x) {
+            for (int x = 0; x < (MASKS ? 32 : min(32, last - k0 + 1)); ++x) {
+                if (MASKS && !(seen >> x & 1u)) continue;
                 const float px = __shfl_sync(0xffffffffu, p, x);
                 const size_t rx = __shfl_sync(0xffffffffu, (unsigned long long)row, x);
                 if (!__shfl_sync(0xffffffffu, (int)in, x)) {
@@ -255,7 +343,7 @@ __device__ __noinline__ void apart_rows(const AttnCall &a, const ApartTile &at, 
         }
 #pragma unroll
         for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
-        const float inv = last < first ? 0.0f : 1.0f / l;
+        const float inv = (MASKS ? !some : last < first) ? 0.0f : 1.0f / l;
         if (lane < 8 * J)
             *reinterpret_cast<float4 *>(a.out + (size_t)(rq.row0 + j) * a.ldo + (size_t)head * D + 4 * lane) =
                 make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);

@@ -65,6 +65,73 @@ gq4_status status_of(cudaError_t err)
     return err == cudaSuccess ? GQ4_OK : GQ4_ERR_CUDA;
 }
 
+// Both forms of the attention.
+gq4_status attention(int B, int T, int q_heads, int max_pages, int max_query, int max_len, const gq4_kv_cache *cache,
+                     const float *q, int ldq, const int32_t *query_start, const int32_t *seq_lens,
+                     const int32_t *page_table, float scale, const gq4_kv_mask &mask, float *out, int ld_out,
+                     void *workspace, size_t workspace_bytes, cudaStream_t stream)
+{
+    if (B < 1 || B > GQ4_MAX_REQUESTS || T < 0 || max_pages < 1 || max_query < 0 || max_len < 0 ||
+        mask.window < 0 || mask.sinks < 0)
+        return GQ4_ERR_INVALID_ARG;
+    GQ4_TRY(check_cache(cache));
+    if (q_heads < 1 || q_heads > GQ4_MAX_HEADS || q_heads % cache->kv_heads != 0)
+        return GQ4_ERR_INVALID_ARG;
+    const long long room = (long long)max_pages * cache->page_size;
+    if (room > kMaxKeys) return GQ4_ERR_INVALID_ARG;
+    if (!(scale - scale == 0.0f)) return GQ4_ERR_INVALID_ARG;  // NaN or infinite
+    if (mask.tree && (mask.tree_words < 1 || mask.tree_words > GQ4_MAX_TREE_WORDS ||
+                      (mask.window > 0 && !mask.positions)))
+        return GQ4_ERR_INVALID_ARG;
+    if (T == 0 || max_query == 0) return GQ4_OK;
+    GQ4_TRY(check_rows(q, q_heads, cache->head_dim, ldq));
+    GQ4_TRY(check_rows(out, q_heads, cache->head_dim, ld_out));
+    if (!query_start || !seq_lens || !page_table) return GQ4_ERR_INVALID_ARG;
+    if (!aligned(query_start, 4) || !aligned(seq_lens, 4) || !aligned(page_table, 4) ||
+        !aligned(mask.tree, 4) || (mask.tree && mask.window > 0 && !aligned(mask.positions, 4)))
+        return GQ4_ERR_MISALIGNED;
+    const size_t need = gq4::attn_workspace_bytes(T, q_heads, cache->kv_heads, cache->head_dim);
+    if (!workspace || workspace_bytes < need) return GQ4_ERR_INVALID_ARG;
+    if (!aligned(workspace, 256)) return GQ4_ERR_MISALIGNED;
+    const size_t width = (size_t)q_heads * cache->head_dim * 4;
+    RangeSet rs;
+    cache_ranges(cache, false, rs);
+    rs.input_rows(q, T, width, (size_t)ldq * 4);
+    rs.input(query_start, ((size_t)B + 1) * 4);
+    rs.input(seq_lens, (size_t)B * 4);
+    rs.input(page_table, (size_t)B * max_pages * 4);
+    if (mask.tree) rs.input(mask.tree, (size_t)T * mask.tree_words * 4);
+    if (mask.tree && mask.window > 0) rs.input(mask.positions, (size_t)T * 4);
+    rs.output_rows(out, T, width, (size_t)ld_out * 4);
+    rs.output(workspace, need);
+    if (!rs.disjoint()) return GQ4_ERR_ALIAS;
+    gq4::AttnCall c{};
+    c.B = B;
+    c.T = T;
+    c.heads = q_heads;
+    c.max_pages = max_pages;
+    c.max_query = max_query;
+    c.max_len = max_len > 0 && max_len < room ? max_len : (int)room;
+    c.c = *cache;
+    c.q = q;
+    c.ldq = ldq;
+    c.query_start = query_start;
+    c.seq_lens = seq_lens;
+    c.page_table = page_table;
+    c.scale = scale;
+    c.window = mask.window;
+    // (first tokens count behind a window only)
+    c.masks = mask.tree || (mask.window > 0 && mask.sinks > 0);
+    c.sinks = mask.sinks < c.max_len ? mask.sinks : c.max_len;
+    c.tree = mask.tree;
+    c.tree_words = mask.tree_words;
+    c.positions = mask.positions;
+    c.out = out;
+    c.ldo = ld_out;
+    c.workspace = workspace;
+    return status_of(gq4::launch_attn(c, stream));
+}
+
 }  // namespace
 
 extern "C" {
@@ -223,53 +290,22 @@ gq4_status gq4_kv_attention(int B, int T, int q_heads, int max_pages, int max_qu
                             int ld_out, void *workspace, size_t workspace_bytes,
                             cudaStream_t stream)
 {
-    if (B < 1 || B > GQ4_MAX_REQUESTS || T < 0 || max_pages < 1 || max_query < 0 || max_len < 0 ||
-        window < 0)
-        return GQ4_ERR_INVALID_ARG;
-    GQ4_TRY(check_cache(cache));
-    if (q_heads < 1 || q_heads > GQ4_MAX_HEADS || q_heads % cache->kv_heads != 0)
-        return GQ4_ERR_INVALID_ARG;
-    const long long room = (long long)max_pages * cache->page_size;
-    if (room > kMaxKeys) return GQ4_ERR_INVALID_ARG;
-    if (!(scale - scale == 0.0f)) return GQ4_ERR_INVALID_ARG;  // NaN or infinite
-    if (T == 0 || max_query == 0) return GQ4_OK;
-    GQ4_TRY(check_rows(q, q_heads, cache->head_dim, ldq));
-    GQ4_TRY(check_rows(out, q_heads, cache->head_dim, ld_out));
-    if (!query_start || !seq_lens || !page_table) return GQ4_ERR_INVALID_ARG;
-    if (!aligned(query_start, 4) || !aligned(seq_lens, 4) || !aligned(page_table, 4))
-        return GQ4_ERR_MISALIGNED;
-    const size_t need = gq4::attn_workspace_bytes(T, q_heads, cache->kv_heads, cache->head_dim);
-    if (!workspace || workspace_bytes < need) return GQ4_ERR_INVALID_ARG;
-    if (!aligned(workspace, 256)) return GQ4_ERR_MISALIGNED;
-    const size_t width = (size_t)q_heads * cache->head_dim * 4;
-    RangeSet rs;
-    cache_ranges(cache, false, rs);
-    rs.input_rows(q, T, width, (size_t)ldq * 4);
-    rs.input(query_start, ((size_t)B + 1) * 4);
-    rs.input(seq_lens, (size_t)B * 4);
-    rs.input(page_table, (size_t)B * max_pages * 4);
-    rs.output_rows(out, T, width, (size_t)ld_out * 4);
-    rs.output(workspace, need);
-    if (!rs.disjoint()) return GQ4_ERR_ALIAS;
-    gq4::AttnCall c{};
-    c.B = B;
-    c.T = T;
-    c.heads = q_heads;
-    c.max_pages = max_pages;
-    c.max_query = max_query;
-    c.max_len = max_len > 0 && max_len < room ? max_len : (int)room;
-    c.c = *cache;
-    c.q = q;
-    c.ldq = ldq;
-    c.query_start = query_start;
-    c.seq_lens = seq_lens;
-    c.page_table = page_table;
-    c.scale = scale;
-    c.window = window;
-    c.out = out;
-    c.ldo = ld_out;
-    c.workspace = workspace;
-    return status_of(gq4::launch_attn(c, stream));
+    gq4_kv_mask mask{};
+    mask.window = window;
+    return attention(B, T, q_heads, max_pages, max_query, max_len, cache, q, ldq, query_start, seq_lens, page_table, scale,
+                     mask, out, ld_out, workspace, workspace_bytes, stream);
+}
+
+gq4_status gq4_kv_attention_masked(int B, int T, int q_heads, int max_pages, int max_query, int max_len,
+                                   const gq4_kv_cache *cache, const float *q, int ldq,
+                                   const int32_t *query_start, const int32_t *seq_lens,
+                                   const int32_t *page_table, float scale, const gq4_kv_mask *mask,
+                                   float *out, int ld_out, void *workspace, size_t workspace_bytes,
+                                   cudaStream_t stream)
+{
+    if (!mask) return GQ4_ERR_INVALID_ARG;
+    return attention(B, T, q_heads, max_pages, max_query, max_len, cache, q, ldq, query_start, seq_lens, page_table, scale,
+                     *mask, out, ld_out, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -51,6 +51,11 @@ struct AttnCall {
     const int32_t *query_start, *seq_lens, *page_table;
     float scale;
     int window;
+    bool masks;             // the masked form: what follows counts
+    int sinks;              // first keys that a window does not hide
+    const uint32_t *tree;   // ancestor bits [T][tree_words], or NULL
+    int tree_words;
+    const int32_t *positions;   // [T], with bits and a window
     float *out;
     int ldo;
     void *workspace;
@@ -65,5 +70,10 @@ cudaError_t read_attn_device_error(unsigned int *bits, bool clear);
 bool prompt_path_supported(const AttnCall &call);
 cudaError_t launch_attn_prompt(const AttnCall &call, cudaStream_t stream);
 cudaError_t read_prompt_device_error(unsigned int *bits, bool clear);
+// Both kernels' masked forms.
+cudaError_t launch_attn_masked(const AttnCall &call, cudaStream_t stream);
+cudaError_t read_masked_device_error(unsigned int *bits, bool clear);
+cudaError_t launch_attn_prompt_masked(const AttnCall &call, cudaStream_t stream);
+cudaError_t read_prompt_masked_device_error(unsigned int *bits, bool clear);
 
 }  // namespace gq4

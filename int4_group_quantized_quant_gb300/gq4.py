@@ -69,6 +69,11 @@ class KVCache(ctypes.Structure):
                 ("group_size", _i), ("Kq", _vp), ("K_sz", _vp), ("Vq", _vp), ("V_sz", _vp)]
 
 
+class KVMask(ctypes.Structure):
+    """``gq4_kv_mask``: what a row sees beyond the causal rule."""
+    _fields_ = [("window", _i), ("sinks", _i), ("tree", _vp), ("tree_words", _i), ("positions", _vp)]
+
+
 _RopeP = ctypes.POINTER(Rope)
 _CacheP = ctypes.POINTER(KVCache)
 
@@ -95,6 +100,8 @@ _SIGS = {
     "gq4_kv_plan": [_i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp],
     "gq4_kv_attention": [_i, _i, _i, _i, _i, _i, _CacheP, _vp, _i, _vp, _vp, _vp, ctypes.c_float, _i,
                          _vp, _i, _vp, ctypes.c_size_t, _vp],
+    "gq4_kv_attention_masked": [_i, _i, _i, _i, _i, _i, _CacheP, _vp, _i, _vp, _vp, _vp, ctypes.c_float,
+                                ctypes.POINTER(KVMask), _vp, _i, _vp, ctypes.c_size_t, _vp],
     "gq4_unpack": [_i, _i, _vp, _vp, _vp],
     "gq4_dequant": [_i, _i, _i, _vp, _vp, _vp, _vp, _vp],
 }
@@ -611,9 +618,12 @@ def kv_attention_workspace_bytes(T, heads, kv_heads, head_dim) -> int:
 
 
 def kv_attention(q, query_start, seq_lens, page_table, Kq, K_sz, Vq, V_sz, group_size, scale, max_query,
-                 max_len=0, window=0, out=None, workspace=None, stream=None):
+                 max_len=0, window=0, out=None, workspace=None, stream=None, sinks=0, tree=None, positions=None):
     """Causal attention of q [T, heads, D] over the cache (gq4_kv_attention): request b's queries are
     rows query_start[b]..query_start[b+1], its seq_lens[b] keys are in the pages of page_table row b.
+    ``sinks``: first keys that the window does not hide.  ``tree`` int32 [T, words]: which of its
+    request's new keys a row sees, bit i for new key i (kv_tree makes them; gq4_kv_attention_masked);
+    with a window the rows' ``positions`` int32 [T] are needed too.
     ``workspace``: a CUDA tensor of at least kv_attention_workspace_bytes(T, heads, kv_heads, D) bytes
     (allocated when None).  ``out`` rows of no request are left as they were."""
     c, index = _cache(Kq, K_sz, Vq, V_sz, group_size)
@@ -639,9 +649,26 @@ def kv_attention(q, query_start, seq_lens, page_table, Kq, K_sz, Vq, V_sz, group
         raise ValueError("workspace must be a contiguous CUDA tensor on the others' device")
     if stream is not None:
         _lend(stream, index, *made)
-    _call(lib.gq4_kv_attention, "gq4_kv_attention", index, stream, B, T, H, width, max_query, max_len, c,
-          q.data_ptr(), ldq, at_start, at_lens, at_table, scale, window, out.data_ptr(), ldo,
-          workspace.data_ptr(), workspace.nbytes)
+    if tree is None and not sinks:
+        if positions is not None:
+            raise ValueError("positions are a tree's")
+        _call(lib.gq4_kv_attention, "gq4_kv_attention", index, stream, B, T, H, width, max_query, max_len, c,
+              q.data_ptr(), ldq, at_start, at_lens, at_table, scale, window, out.data_ptr(), ldo,
+              workspace.data_ptr(), workspace.nbytes)
+        return out
+    words, at_tree, at_pos = 0, None, None
+    if tree is not None:
+        words = _width(tree)
+        at_tree = _at(tree, "tree", _i32, (T, words), index)
+        if positions is not None:
+            at_pos = _at(positions, "positions", _i32, (T,), index)
+        elif window:
+            raise ValueError("a tree behind a window needs positions")
+    elif positions is not None:
+        raise ValueError("positions are a tree's")
+    _call(lib.gq4_kv_attention_masked, "gq4_kv_attention_masked", index, stream, B, T, H, width, max_query, max_len, c,
+          q.data_ptr(), ldq, at_start, at_lens, at_table, scale, KVMask(window, sinks, at_tree, words, at_pos),
+          out.data_ptr(), ldo, workspace.data_ptr(), workspace.nbytes)
     return out
 
 
