@@ -459,6 +459,21 @@ GQ4_API gq4_status gq4_kv_append(int T, const gq4_kv_cache *cache, const float *
                                  const float *v, int ldv, const int32_t *slots,
                                  cudaStream_t stream);
 
+/* gq4_head_norm_rope and gq4_kv_append in one pass: q_out = q normalised and
+ * rotated, k normalised, rotated and quantised into slots[t], v quantised into
+ * it.  rope, positions, q and q_out as there (q_heads 0: no queries; q_out may
+ * be q with the same ld; rows of skipped slots are rotated all the same; any
+ * number of query heads goes with any of the cache's), k, v and slots as here.
+ * A code is that of the key's value in 64 bits (the angle's 64-bit product
+ * among them) rounded once to f32, whatever the order of its f32 operations;
+ * scales and zeros are f32's.  So of the two calls' results some codes next to a
+ * border and scales' last bits may differ. */
+GQ4_API gq4_status gq4_kv_rope_append(int T, int q_heads, const gq4_kv_cache *cache,
+                                      const gq4_rope *rope, const int32_t *positions, const float *q,
+                                      int ldq, float *q_out, int ldq_out, const float *k, int ldk,
+                                      const float *v, int ldv, const int32_t *slots,
+                                      cudaStream_t stream);
+
 /* Read rows back: k_out[t], v_out[t] (f32 [T][kv_heads][head_dim], dense) =
  * fl(fl(code - zero) * scale) of slot slots[t].  A negative slot leaves its
  * rows as they were; one outside the pool gives NaN rows and sets bit 6. */
@@ -585,6 +600,58 @@ GQ4_API gq4_status gq4_kv_attention_masked(int B, int T, int q_heads, int max_pa
                                            int ld_out, void *workspace, size_t workspace_bytes,
                                            cudaStream_t stream);
 
+/* Drafted trees.  Request b's new tokens are the nodes 0 .. n - 1 of a tree
+ * (rows query_start[b] .. query_start[b+1] - 1); parents[row] is the node that a
+ * node follows, which comes before it, or -1: the request's last token of the
+ * past (there may be several such).  Node i's depth is its number of ancestors.
+ * Written for each row:
+ *   positions[row]   seq_len - n + depth, to rotate by
+ *   tree[row][...]   bit i: node i is the row's own or an ancestor; with a
+ *                    window (> 0) those less than `window` steps up, and those
+ *                    whose position is below `sinks`
+ * as gq4_kv_attention_masked takes them.  (A step: gq4_kv_plan gives the nodes
+ * slots, one after the other; these positions replace the ones it writes.)  A
+ * request with a parent that is none, more than 32 * tree_words nodes, more
+ * nodes than seq_len or rows not within T is refused: its rows inside T get
+ * position 0 and no bits, and device error bit 10 is set.  Rows of no request
+ * are left as they were. */
+GQ4_API gq4_status gq4_kv_tree(int B, int T, int tree_words, int window, int sinks,
+                               const int32_t *parents, const int32_t *query_start,
+                               const int32_t *seq_lens, int32_t *positions, uint32_t *tree,
+                               cudaStream_t stream);
+
+/* After the verification: of request b's n new tokens, counts[b] are accepted,
+ * the nodes path[b][0 .. counts[b] - 1] (int32 [B][max_path], rising).  The
+ * cache's row of node path[b][i] moves to that of node i -- position past + i,
+ * the one that it was rotated by, if the path starts at a root and goes from
+ * parent to child -- the request's length becomes past + counts[b], past =
+ * seq_len - n, and pages that hold none of its tokens any more go back: in the
+ * order of the requests and of their tables, behind the free list's free_count
+ * entries, where gq4_kv_plan takes them again (the table's entries stay as they
+ * are).  path NULL: the first counts[b] tokens, nothing moves (a line of drafts,
+ * or a step taken back).  seq_lens_out may be seq_lens, and free_count_out
+ * free_count.
+ *
+ * A request is refused -- its length stays, nothing moves, no page goes back,
+ * device error bit 11 is set -- when n is negative or above seq_len, seq_len
+ * passes max_pages * page_size, counts[b] is not in 0 .. min(n, max_path), the
+ * path does not rise or leaves 0 .. n - 1, or a page of its new tokens is outside
+ * the pool.  Pages for which the list has no room (n_free) are lost, and bit 11
+ * is set; free_count is cut to 0 .. n_free.  Rows shared with other requests
+ * (one page in two tables) move for both.
+ *
+ * workspace: gq4_kv_accept_workspace_bytes(B) bytes of device memory, 256-byte
+ * aligned, as in gq4_kv_attention. */
+GQ4_API size_t gq4_kv_accept_workspace_bytes(int B);
+
+GQ4_API gq4_status gq4_kv_accept(int B, int max_path, int max_pages, int n_free,
+                                 const gq4_kv_cache *cache, const int32_t *path,
+                                 const int32_t *counts, const int32_t *query_start,
+                                 const int32_t *seq_lens, const int32_t *page_table,
+                                 int32_t *free_pages, const int32_t *free_count,
+                                 int32_t *free_count_out, int32_t *seq_lens_out, void *workspace,
+                                 size_t workspace_bytes, cudaStream_t stream);
+
 /* Integer unpack test kernel: q[n*K + k] = q(n,k) as u8 [N][K].
  * Uses the same in-register extraction as the matvec kernels.
  * Requires K % 32 == 0. */
@@ -612,7 +679,9 @@ GQ4_API gq4_status gq4_dequant(int K, int N, int group_size, const uint32_t *Bq,
  * gq4_kv_gather met a slot outside the pool, bit 7 when gq4_kv_plan refused
  * a request, bit 8 when gq4_kv_attention met a request outside its bounds or
  * a page outside the pool, bit 9 when its prompt kernel gave up waiting for
- * its own copies or MMAs.  Copies the word to
+ * its own copies or MMAs, bit 10 when gq4_kv_tree and bit 11 when gq4_kv_accept
+ * refused a request (or lost pages for want of room); bits 3 and 6 also cover
+ * gq4_kv_rope_append, bits 8 and 9 gq4_kv_attention_masked.  Copies the word to
  * *bits (synchronous, device-wide) and clears it when clear != 0.  Not for
  * the hot path: a diagnostic to call after a suspicious result. */
 GQ4_API gq4_status gq4_device_error(unsigned int *bits, int clear);

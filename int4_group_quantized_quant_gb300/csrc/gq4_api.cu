@@ -630,7 +630,10 @@ gq4_status gq4_device_error(unsigned int *bits, int clear)
     unsigned int k = 0, t = 0;
     if (gq4::read_kv_device_error(&k, clear != 0) != cudaSuccess) return GQ4_ERR_CUDA;
     if (gq4::read_attn_device_error(&t, clear != 0) != cudaSuccess) return GQ4_ERR_CUDA;
-    *bits = a | b | c | d | e | f | l | k | t;
+    unsigned int r = 0, w = 0;
+    if (gq4::read_kv_rope_device_error(&r, clear != 0) != cudaSuccess) return GQ4_ERR_CUDA;
+    if (gq4::read_tree_device_error(&w, clear != 0) != cudaSuccess) return GQ4_ERR_CUDA;
+    *bits = a | b | c | d | e | f | l | k | t | r | w;
     return GQ4_OK;
 }
 

@@ -4,45 +4,13 @@
 #include <cstdint>
 
 #include "gq4_kv_internal.h"
-#include "gq4_kv.cuh"
-#include "gq4_quant.cuh"
+#include "gq4_kv_write.cuh"
 
 namespace gq4 {
 namespace {
 
 __device__ unsigned int g_kv_error = 0;
-constexpr unsigned int kKvNonFinite = 1u << 3, kKvBadSlot = 1u << 6, kKvRefused = 1u << 7;
-
-// r / d for 0 <= r, r d < 2^31, by multiplying with ceil(2^31 / d): that is
-// too large by less than d, which adds less than r d / (2^31 d) < 1 / d.
-__device__ __forceinline__ int quotient(int r, uint32_t per_d)
-{
-    return (int)__umulhi(2u * (uint32_t)r, per_d);
-}
-
-uint32_t divide_by(int d)
-{
-    return (uint32_t)((0x80000000ull + (uint32_t)d - 1) / (uint32_t)d);
-}
-
-// Where a row of the pool lies, in 32-bit steps and one 64-bit sum: the pages
-// of all heads are fewer than 2^32 (each is 640 bytes or more).
-struct RowAt {
-    uint32_t page_head, at;
-
-    __device__ __forceinline__ RowAt(const gq4_kv_cache &c, int slot, int shift, int head)
-        : page_head((uint32_t)(slot >> shift) * (uint32_t)c.kv_heads + (uint32_t)head),
-          at((uint32_t)slot & (uint32_t)(c.page_size - 1))
-    {
-    }
-    // in an array of `bytes` per row, `page_bytes` per page and head
-    template <typename P>
-    __device__ __forceinline__ P *in(P *array, uint32_t page_bytes, uint32_t bytes) const
-    {
-        const char *base = reinterpret_cast<const char *>(array);
-        return reinterpret_cast<P *>(const_cast<char *>(base + (uint64_t)page_head * page_bytes + at * bytes));
-    }
-};
+constexpr unsigned int kKvRefused = 1u << 7;
 
 // ---------------------------------------------------------------------------
 // Writer.  A lane holds one word's 8 values, a row takes D/8 lanes; a warp
@@ -76,9 +44,8 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
     constexpr int WPR = 4 * J, RPW = 32 / WPR;   // words per row, rows per warp
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int in_warp = lane / WPR, w = lane - in_warp * WPR;
-    constexpr int G = WPR / L;
     const int H = p.c.kv_heads;
-    const int group = w / L, pos = w - group * L;
+    const int pos = w % L;
     const int t0 = blockIdx.x * p.tokens;
     const int n_rows = min(p.tokens, p.T - t0) * 2 * H;
     constexpr int kStep = kAppendThreads / 32 * RPW;
@@ -123,28 +90,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
             // the first halves of both, the other the second
             const uint32_t other = __shfl_xor_sync(0xffffffffu, word, 4);
             if (slot[u] < 0) continue;
-            if (slot[u] >= p.total) {
-                if (w == 0) atomicOr(&g_kv_error, kKvBadSlot);
-                continue;
-            }
-            const RowAt row(p.c, slot[u], p.shift, h);
-            if (side == 0) {
-                row.in(p.c.Kq, p.page_codes, 4 * WPR)[k_word_index(w, J)] = word;
-            } else if constexpr (J % 2 == 0) {
-                const int g = 2 * (w & 3), b = w >> 2;
-                const uint32_t both = (b & 1) ? __byte_perm(other, word, 0x7632) : __byte_perm(word, other, 0x5410);
-                row.in(p.c.Vq, p.page_codes, 4 * WPR)[((g + (b & 1)) * J + (b & ~1)) >> 1] = both;
-            } else {
-                uint16_t *half = reinterpret_cast<uint16_t *>(row.in(p.c.Vq, p.page_codes, 4 * WPR));
-                half[v_half_index(2 * w, J)] = (uint16_t)word;
-                half[v_half_index(2 * w + 1, J)] = (uint16_t)(word >> 16);
-            }
-            if (pos == 0) {
-                const float nan = __int_as_float(0x7fc00000);
-                float2 *sz = reinterpret_cast<float2 *>(side ? p.c.V_sz : p.c.K_sz);
-                row.in(sz, p.page_sz, 8 * G)[group] = bad ? make_float2(nan, nan) : make_float2(m.s, m.z);
-                if (bad) atomicOr(&g_kv_error, kKvNonFinite);
-            }
+            write_word<J, L>(p, slot[u], h, side, w, word, other, bad, m, &g_kv_error);
         }
     }
 }
@@ -355,13 +301,6 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
 }  // namespace
 
 namespace {
-
-int log2_of(int pow2)
-{
-    int s = 0;
-    while ((1 << s) < pow2) ++s;
-    return s;
-}
 
 // Tokens per CTA so that each of its threads has `items` of `per_token`.
 int tokens_per_cta(int per_token, int items)

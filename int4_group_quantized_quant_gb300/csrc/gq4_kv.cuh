@@ -28,4 +28,42 @@ __host__ __device__ __forceinline__ int v_half_index(int h, int J)
     return (h & 7) * J + (h >> 3);
 }
 
+// r / d for 0 <= r, r d < 2^31, by multiplying with ceil(2^31 / d): that is
+// too large by less than d, which adds less than r d / (2^31 d) < 1 / d.
+__device__ __forceinline__ int quotient(int r, uint32_t per_d)
+{
+    return (int)__umulhi(2u * (uint32_t)r, per_d);
+}
+
+inline uint32_t divide_by(int d)
+{
+    return (uint32_t)((0x80000000ull + (uint32_t)d - 1) / (uint32_t)d);
+}
+
+// Where a row of the pool lies, in 32-bit steps and one 64-bit sum: the pages
+// of all heads are fewer than 2^32 (each is 640 bytes or more).
+struct RowAt {
+    uint32_t page_head, at;
+
+    __device__ __forceinline__ RowAt(const gq4_kv_cache &c, int slot, int shift, int head)
+        : page_head((uint32_t)(slot >> shift) * (uint32_t)c.kv_heads + (uint32_t)head),
+          at((uint32_t)slot & (uint32_t)(c.page_size - 1))
+    {
+    }
+    // in an array of `bytes` per row, `page_bytes` per page and head
+    template <typename P>
+    __device__ __forceinline__ P *in(P *array, uint32_t page_bytes, uint32_t bytes) const
+    {
+        const char *base = reinterpret_cast<const char *>(array);
+        return reinterpret_cast<P *>(const_cast<char *>(base + (uint64_t)page_head * page_bytes + at * bytes));
+    }
+};
+
+inline int log2_of(int pow2)
+{
+    int s = 0;
+    while ((1 << s) < pow2) ++s;
+    return s;
+}
+
 }  // namespace gq4

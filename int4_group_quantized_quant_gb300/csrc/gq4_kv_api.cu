@@ -209,6 +209,67 @@ gq4_status gq4_kv_append(int T, const gq4_kv_cache *cache, const float *k, int l
     return status_of(gq4::launch_kv_append(T, *cache, k, ldk, v, ldv, slots, stream));
 }
 
+gq4_status gq4_kv_rope_append(int T, int q_heads, const gq4_kv_cache *cache, const gq4_rope *rope,
+                              const int32_t *positions, const float *q, int ldq, float *q_out,
+                              int ldq_out, const float *k, int ldk, const float *v, int ldv,
+                              const int32_t *slots, cudaStream_t stream)
+{
+    if (!rope || T < 0 || q_heads < 0 || q_heads > GQ4_MAX_HEADS) return GQ4_ERR_INVALID_ARG;
+    GQ4_TRY(check_cache(cache));
+    const int D = cache->head_dim;
+    if (rope->rot_dim < 0 || rope->rot_dim > D || rope->rot_dim % 8 != 0) return GQ4_ERR_INVALID_ARG;
+    if (rope->interleaved != 0 && rope->interleaved != 1) return GQ4_ERR_INVALID_ARG;
+    if (!(rope->eps >= 0.0f)) return GQ4_ERR_INVALID_ARG;  // also rejects NaN
+    if (T == 0) return GQ4_OK;
+    if (rope->rot_dim > 0 && (!positions || !rope->inv_freq)) return GQ4_ERR_INVALID_ARG;
+    GQ4_TRY(check_rows(k, cache->kv_heads, D, ldk));
+    GQ4_TRY(check_rows(v, cache->kv_heads, D, ldv));
+    if (!slots) return GQ4_ERR_INVALID_ARG;
+    if (!aligned(slots, 4)) return GQ4_ERR_MISALIGNED;
+    const size_t width = (size_t)cache->kv_heads * D * 4;
+    RangeSet rs;
+    if (rope->rot_dim > 0) {
+        if (!aligned(positions, 4) || !aligned(rope->inv_freq, 4)) return GQ4_ERR_MISALIGNED;
+        rs.input(positions, (size_t)T * 4);
+        rs.input(rope->inv_freq, (size_t)rope->rot_dim / 2 * 4);
+    }
+    if (rope->k_gain && !aligned(rope->k_gain, 16)) return GQ4_ERR_MISALIGNED;
+    gq4::RopeCall c{};
+    c.T = T;
+    c.D = D;
+    c.rot = rope->rot_dim;
+    c.interleaved = rope->interleaved != 0;
+    c.eps = rope->eps;
+    c.positions = positions;
+    c.inv_freq = rope->inv_freq;
+    c.x[1] = k;
+    c.ldx[1] = ldk;
+    c.gain[1] = rope->k_gain;
+    if (q_heads > 0) {
+        GQ4_TRY(check_rows(q, q_heads, D, ldq));
+        GQ4_TRY(check_rows(q_out, q_heads, D, ldq_out));
+        if (rope->q_gain && !aligned(rope->q_gain, 16)) return GQ4_ERR_MISALIGNED;
+        const size_t q_width = (size_t)q_heads * D * 4;
+        // in place: the same rows (each is read whole before it is written)
+        if (!(q == q_out && ldq == ldq_out)) rs.input_rows(q, T, q_width, (size_t)ldq * 4);
+        rs.output_rows(q_out, T, q_width, (size_t)ldq_out * 4);
+        rs.input(rope->q_gain, (size_t)D * 4);
+        c.heads[0] = q_heads;
+        c.x[0] = q;
+        c.y[0] = q_out;
+        c.gain[0] = rope->q_gain;
+        c.ldx[0] = ldq;
+        c.ldy[0] = ldq_out;
+    }
+    rs.input_rows(k, T, width, (size_t)ldk * 4);
+    rs.input_rows(v, T, width, (size_t)ldv * 4);
+    rs.input(rope->k_gain, (size_t)D * 4);
+    rs.input(slots, (size_t)T * 4);
+    cache_ranges(cache, true, rs);
+    if (!rs.disjoint()) return GQ4_ERR_ALIAS;
+    return status_of(gq4::launch_kv_rope_append(c, *cache, v, ldv, slots, stream));
+}
+
 gq4_status gq4_kv_gather(int T, const gq4_kv_cache *cache, const int32_t *slots, float *k_out,
                          float *v_out, cudaStream_t stream)
 {
@@ -275,6 +336,96 @@ gq4_status gq4_kv_plan(int B, int T, int page_size, int max_pages, int n_free,
     c.positions = positions;
     c.slots = slots;
     return status_of(gq4::launch_kv_plan(c, stream));
+}
+
+gq4_status gq4_kv_tree(int B, int T, int tree_words, int window, int sinks, const int32_t *parents,
+                       const int32_t *query_start, const int32_t *seq_lens, int32_t *positions,
+                       uint32_t *tree, cudaStream_t stream)
+{
+    if (B < 1 || B > GQ4_MAX_REQUESTS || T < 0 || tree_words < 1 || tree_words > GQ4_MAX_TREE_WORDS ||
+        window < 0 || sinks < 0)
+        return GQ4_ERR_INVALID_ARG;
+    if (T == 0) return GQ4_OK;
+    if (!parents || !query_start || !seq_lens || !positions || !tree) return GQ4_ERR_INVALID_ARG;
+    const void *all[] = {parents, query_start, seq_lens, positions, tree};
+    for (const void *p : all)
+        if (!aligned(p, 4)) return GQ4_ERR_MISALIGNED;
+    RangeSet rs;
+    rs.input(parents, (size_t)T * 4);
+    rs.input(query_start, ((size_t)B + 1) * 4);
+    rs.input(seq_lens, (size_t)B * 4);
+    rs.output(positions, (size_t)T * 4);
+    rs.output(tree, (size_t)T * tree_words * 4);
+    if (!rs.disjoint()) return GQ4_ERR_ALIAS;
+    gq4::TreeCall c{};
+    c.B = B;
+    c.T = T;
+    c.words = tree_words;
+    c.window = window;
+    c.sinks = sinks;
+    c.parents = parents;
+    c.query_start = query_start;
+    c.seq_lens = seq_lens;
+    c.positions = positions;
+    c.bits = tree;
+    return status_of(gq4::launch_kv_tree(c, stream));
+}
+
+size_t gq4_kv_accept_workspace_bytes(int B)
+{
+    return B < 1 ? 0 : ((size_t)B * 4 + 255) / 256 * 256;
+}
+
+gq4_status gq4_kv_accept(int B, int max_path, int max_pages, int n_free, const gq4_kv_cache *cache,
+                         const int32_t *path, const int32_t *counts, const int32_t *query_start,
+                         const int32_t *seq_lens, const int32_t *page_table, int32_t *free_pages,
+                         const int32_t *free_count, int32_t *free_count_out, int32_t *seq_lens_out,
+                         void *workspace, size_t workspace_bytes, cudaStream_t stream)
+{
+    if (B < 1 || B > GQ4_MAX_REQUESTS || max_path < 0 || max_pages < 1 || n_free < 0)
+        return GQ4_ERR_INVALID_ARG;
+    GQ4_TRY(check_cache(cache));
+    if ((long long)max_pages * cache->page_size > kMaxKeys) return GQ4_ERR_INVALID_ARG;
+    if (!counts || !query_start || !seq_lens || !page_table || !free_count || !free_count_out || !seq_lens_out ||
+        (n_free > 0 && !free_pages))
+        return GQ4_ERR_INVALID_ARG;
+    const void *all[] = {path, counts, query_start, seq_lens, page_table, free_pages, free_count, free_count_out,
+                         seq_lens_out};
+    for (const void *p : all)
+        if (!aligned(p, 4)) return GQ4_ERR_MISALIGNED;
+    const size_t need = gq4_kv_accept_workspace_bytes(B), b = (size_t)B * 4;
+    if (!workspace || workspace_bytes < need) return GQ4_ERR_INVALID_ARG;
+    if (!aligned(workspace, 256)) return GQ4_ERR_MISALIGNED;
+    RangeSet rs;
+    cache_ranges(cache, true, rs);
+    rs.input(path, b * (size_t)max_path);
+    rs.input(counts, b);
+    rs.input(query_start, b + 4);
+    if (seq_lens_out != seq_lens) rs.input(seq_lens, b);
+    rs.input(page_table, b * (size_t)max_pages);
+    if (free_count_out != free_count) rs.input(free_count, 4);
+    rs.output(free_pages, (size_t)n_free * 4);
+    rs.output(free_count_out, 4);
+    rs.output(seq_lens_out, b);
+    rs.output(workspace, need);
+    if (!rs.disjoint()) return GQ4_ERR_ALIAS;
+    gq4::AcceptCall c{};
+    c.B = B;
+    c.max_path = max_path;
+    c.max_pages = max_pages;
+    c.n_free = n_free;
+    c.c = *cache;
+    c.path = path;
+    c.counts = counts;
+    c.query_start = query_start;
+    c.seq_lens = seq_lens;
+    c.page_table = page_table;
+    c.free_count = free_count;
+    c.free_pages = free_pages;
+    c.free_count_out = free_count_out;
+    c.seq_lens_out = seq_lens_out;
+    c.verdict = static_cast<int32_t *>(workspace);
+    return status_of(gq4::launch_kv_accept(c, stream));
 }
 
 size_t gq4_kv_attention_workspace_bytes(int T, int q_heads, int kv_heads, int head_dim)

@@ -34,6 +34,28 @@ struct PlanCall {
 };
 cudaError_t launch_kv_plan(const PlanCall &call, cudaStream_t stream);
 cudaError_t read_kv_device_error(unsigned int *bits, bool clear);
+// Rotation and append in one: side 1 of the call is k, which has no output.
+cudaError_t launch_kv_rope_append(const RopeCall &call, const gq4_kv_cache &c, const float *v, int ldv,
+                                  const int32_t *slots, cudaStream_t stream);
+cudaError_t read_kv_rope_device_error(unsigned int *bits, bool clear);
+
+// Drafted trees: their bits, and accepting a path.
+struct TreeCall {
+    int B, T, words, window, sinks;
+    const int32_t *parents, *query_start, *seq_lens;
+    int32_t *positions;
+    uint32_t *bits;
+};
+cudaError_t launch_kv_tree(const TreeCall &call, cudaStream_t stream);
+struct AcceptCall {
+    int B, max_path, max_pages, n_free;
+    gq4_kv_cache c;
+    const int32_t *path, *counts, *query_start, *seq_lens, *page_table, *free_count;
+    int32_t *free_pages, *free_count_out, *seq_lens_out;
+    int32_t *verdict;   // [B] of the workspace: how many rows, -1: refused
+};
+cudaError_t launch_kv_accept(const AcceptCall &call, cudaStream_t stream);
+cudaError_t read_tree_device_error(unsigned int *bits, bool clear);
 
 // Attention over the cache.
 constexpr int kPromptTile = 128, kPromptKeys = 64;   // query rows and keys of a tile of the prompt kernel

@@ -96,6 +96,10 @@ _SIGS = {
     "gq4_embedding": [_i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp],
     "gq4_head_norm_rope": [_i, _i, _i, _i, _RopeP, _vp, _vp, _i, _vp, _i, _vp, _i, _vp, _i, _vp],
     "gq4_kv_append": [_i, _CacheP, _vp, _i, _vp, _i, _vp, _vp],
+    "gq4_kv_rope_append": [_i, _i, _CacheP, _RopeP, _vp, _vp, _i, _vp, _i, _vp, _i, _vp, _i, _vp, _vp],
+    "gq4_kv_tree": [_i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp],
+    "gq4_kv_accept": [_i, _i, _i, _i, _CacheP, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t,
+                      _vp],
     "gq4_kv_gather": [_i, _CacheP, _vp, _vp, _vp, _vp],
     "gq4_kv_plan": [_i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp],
     "gq4_kv_attention": [_i, _i, _i, _i, _i, _i, _CacheP, _vp, _i, _vp, _vp, _vp, ctypes.c_float, _i,
@@ -121,10 +125,12 @@ lib.gq4_gemm_workspace_bytes.restype = ctypes.c_size_t
 lib.gq4_gemm_workspace_bytes.argtypes = [_i, _i]
 lib.gq4_kv_attention_workspace_bytes.restype = ctypes.c_size_t
 lib.gq4_kv_attention_workspace_bytes.argtypes = [_i, _i, _i, _i]
+lib.gq4_kv_accept_workspace_bytes.restype = ctypes.c_size_t
+lib.gq4_kv_accept_workspace_bytes.argtypes = [_i]
 
 EXPORTED = list(_SIGS) + ["gq4_status_string", "gq4_version", "gq4_device_error",
                           "gq4_sequence_workspace_bytes", "gq4_gemm_workspace_bytes",
-                          "gq4_kv_attention_workspace_bytes"]
+                          "gq4_kv_attention_workspace_bytes", "gq4_kv_accept_workspace_bytes"]
 
 
 class GQ4Error(RuntimeError):
@@ -560,6 +566,34 @@ def kv_append(k, v, slots, Kq, K_sz, Vq, V_sz, group_size, stream=None):
     _call(lib.gq4_kv_append, "gq4_kv_append", index, stream, T, c, k.data_ptr(), ldk, v.data_ptr(), ldv, at_slots)
 
 
+def kv_rope_append(q, k, v, positions, inv_freq, slots, Kq, K_sz, Vq, V_sz, group_size, q_gain=None, k_gain=None,
+                   eps=1e-6, interleaved=False, q_out=None, stream=None):
+    """head_norm_rope and kv_append in one pass (gq4_kv_rope_append): k normalised (where k_gain is given),
+    rotated and quantised into the cache at slots int32 [T], v quantised; returns q normalised and rotated.
+    q [T, heads, D] may be None, and q_out q itself; rows may be columns of a wider matrix; inv_freq None:
+    no rotation."""
+    c, index = _cache(Kq, K_sz, Vq, V_sz, group_size)
+    T, H, D, ldk = _rows(k, "k", index)
+    if (H, D) != (c.kv_heads, c.head_dim):
+        raise ValueError(f"k: {H} heads of {D} != {c.kv_heads} heads of {c.head_dim}")
+    ldv = _rows(v, "v", index, (T, H, D))[3]
+    given = q_out
+    q_out, q_gain_at, (QH, xq, ldq, yq, ldqo) = _rope_side(q, q_out, q_gain, "q", T, D, index)
+    k_gain_at = None if k_gain is None else _at(k_gain, "k_gain", _f32, (D,), index)
+    rot, at_pos, at_inv = 0, None, None
+    if inv_freq is not None:
+        rot = 2 * inv_freq.numel()
+        at_inv = _at(inv_freq, "inv_freq", _f32, (rot // 2,), index)
+        at_pos = _at(positions, "positions", _i32, (T,), index)
+    at_slots = _at(slots, "slots", _i32, (T,), index)
+    if stream is not None and given is None and q_out is not None:
+        _lend(stream, index, q_out)
+    _call(lib.gq4_kv_rope_append, "gq4_kv_rope_append", index, stream, T, QH, c,
+          Rope(q_gain_at, k_gain_at, eps, rot, 1 if interleaved else 0, at_inv), at_pos, xq, ldq, yq, ldqo,
+          k.data_ptr(), ldk, v.data_ptr(), ldv, at_slots)
+    return q_out
+
+
 def kv_gather(slots, Kq, K_sz, Vq, V_sz, group_size, k_out=None, v_out=None, stream=None):
     """(k, v) f32 [T, kv_heads, D] of the cache rows at slots (gq4_kv_gather; rows of negative slots
     are left as they were, so pass k_out and v_out where there are some)."""
@@ -670,6 +704,74 @@ def kv_attention(q, query_start, seq_lens, page_table, Kq, K_sz, Vq, V_sz, group
           q.data_ptr(), ldq, at_start, at_lens, at_table, scale, KVMask(window, sinks, at_tree, words, at_pos),
           out.data_ptr(), ldo, workspace.data_ptr(), workspace.nbytes)
     return out
+
+
+def kv_tree(parents, query_start, seq_lens, words, window=0, sinks=0, positions=None, tree=None, stream=None):
+    """(positions int32 [T], tree int32 [T, words]) of drafted trees from their parents int32 [T], the node of
+    its request that each follows, -1 the request's last token (gq4_kv_tree), as kv_attention takes them.
+    Rows of no request are left as they were."""
+    index = _device(parents, "parents")
+    T = parents.numel()
+    _device(seq_lens, "seq_lens")
+    B = seq_lens.numel()
+    at_parents, at_lens = _at(parents, "parents", _i32, (T,), index), _at(seq_lens, "seq_lens", _i32, (B,), index)
+    at_start = _at(query_start, "query_start", _i32, (B + 1,), index)
+    if not 1 <= words <= 8:
+        raise ValueError(f"words {words} not in 1..8")
+    made = []
+    if positions is None:
+        positions = torch.empty(T, dtype=_i32, device=parents.device)
+        made.append(positions)
+    if tree is None:
+        tree = torch.empty((T, words), dtype=_i32, device=parents.device)
+        made.append(tree)
+    if stream is not None:
+        _lend(stream, index, *made)
+    _call(lib.gq4_kv_tree, "gq4_kv_tree", index, stream, B, T, words, window, sinks, at_parents, at_start, at_lens,
+          _at(positions, "positions", _i32, (T,), index), _at(tree, "tree", _i32, (T, words), index))
+    return positions, tree
+
+
+def kv_accept(path, counts, query_start, seq_lens, page_table, free_pages, free_count, Kq, K_sz, Vq, V_sz, group_size,
+              seq_lens_out=None, free_count_out=None, workspace=None, stream=None):
+    """After a verification (gq4_kv_accept): the cache's rows of the accepted nodes path int32 [B, max_path] (the
+    first counts int32 [B] of each row; None: the first new tokens) move to the end of their request, and pages
+    left over go back on free_pages.  Returns (seq_lens_out, free_count_out); pass seq_lens_out=seq_lens and
+    free_count_out=free_count to advance them in place."""
+    c, index = _cache(Kq, K_sz, Vq, V_sz, group_size)
+    _device(seq_lens, "seq_lens")
+    B, width, n_free = seq_lens.numel(), _width(page_table), free_pages.numel()
+    at_lens, at_start = _at(seq_lens, "seq_lens", _i32, (B,), index), \
+        _at(query_start, "query_start", _i32, (B + 1,), index)
+    at_counts, at_table = _at(counts, "counts", _i32, (B,), index), \
+        _at(page_table, "page_table", _i32, (B, width), index)
+    at_free, at_count = _at(free_pages, "free_pages", _i32, (n_free,), index), \
+        _at(free_count, "free_count", _i32, (1,), index)
+    most, at_path = 0, None
+    if path is not None:
+        most = _width(path)
+        at_path = _at(path, "path", _i32, (B, most), index)
+        if most == 0:
+            raise ValueError("path has no columns")
+    need = lib.gq4_kv_accept_workspace_bytes(B)
+    # what is not given is a stretch of one allocation, the workspace first
+    spare = torch.empty(need // 4 + B + 1, dtype=_i32, device=Kq.device)
+    if workspace is None:
+        at_work, work = spare.data_ptr(), need
+    elif not (isinstance(workspace, torch.Tensor) and workspace.get_device() == index and workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous CUDA tensor on the others' device")
+    else:
+        at_work, work = workspace.data_ptr(), workspace.nbytes
+    if seq_lens_out is None:
+        seq_lens_out = spare[need // 4:need // 4 + B]
+    if free_count_out is None:
+        free_count_out = spare[need // 4 + B:]
+    if stream is not None:
+        _lend(stream, index, spare)
+    _call(lib.gq4_kv_accept, "gq4_kv_accept", index, stream, B, most, width, n_free, c, at_path, at_counts, at_start,
+          at_lens, at_table, at_free, at_count, _at(free_count_out, "free_count_out", _i32, (1,), index),
+          _at(seq_lens_out, "seq_lens_out", _i32, (B,), index), at_work, work)
+    return seq_lens_out, free_count_out
 
 
 # ---------------------------------------------------------------------------
@@ -809,7 +911,8 @@ def device_error(clear: bool = True) -> int:
     quantizer or the cache's writer met a non-finite group; bit 4: the embedding
     gather met an id outside its table; bit 6: a cache slot outside the pool; bit 7:
     kv_plan refused a request; bit 8: kv_attention met a request outside its bounds or
-    a page outside the pool; bit 9: its prompt kernel gave up a bounded wait)."""
+    a page outside the pool; bit 9: its prompt kernel gave up a bounded wait; bit 10:
+    kv_tree, bit 11: kv_accept refused a request)."""
     bits = ctypes.c_uint(0)
     _check(lib.gq4_device_error(ctypes.byref(bits), int(clear)), "gq4_device_error")
     return int(bits.value)

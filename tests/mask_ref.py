@@ -17,9 +17,8 @@ def tree(parents, starts, lens, words, window=0, sinks=0):
         lo, n = int(starts[b]), int(starts[b + 1] - starts[b])
         past = int(lens[b]) - n
         own = parents[lo:lo + n]
-        if n > 32 * words or any(not -1 <= p < i for i, p in enumerate(own)):
+        if n > 32 * words or past < 0 or any(not -1 <= p < i for i, p in enumerate(own)):
             refused = True
-            pos[lo:lo + n] = past
             continue
         depth = []
         for i, p in enumerate(own):
