@@ -9,20 +9,23 @@
 // rotated keys' way to HBM and back (8 bytes per value of k).  Floor: 8 bytes
 // per value of q, 4 read and 0.5 + 8/gs written per value of k and v.
 //
-// A lane holds a word's 8 values, a row takes D/8 lanes, a warp as many rows as
-// fit; a CTA takes one token (few tokens: a share of its rows).  All rows of a
-// warp are of one kind, so that it goes one way: rows are numbered in units of a
-// warp's.  Half-split pairs are read a second time, as two float4s (a first-level
-// cache hit), which takes 2 instructions where shuffles take 8.
+// Two kinds of CTAs take turns in the grid, so that the queries', which wait for
+// HBM, and the keys', which are bound by instructions, share an SM.  A CTA of
+// queries takes one token (few tokens: a share of its heads): a row is held in
+// float4s by 16 lanes (64 values) or 32, pairs of a half-split rotation are
+// exchanged by shuffles.  A CTA of keys and values takes a few tokens: a lane
+// holds a word's 8 values, a row takes D/8 lanes, a warp as many rows as fit,
+// all K or all V; half-split partners are read a second time (a first-level
+// cache hit), 2 instructions where shuffles take 8.
 //
-// Codes next to a border.  A key's code is that of its exact value, rounded once
-// to f32, as if the rotation were computed in 64 bits: so it does not depend on
-// how sums and products were ordered.  The rotation itself is f32; what it
-// leaves of a key is off by at most kKeyError (|a| + |b|) for the pair (a, b)
-// before the rotation.  Where that could turn a code's rounding -- a value so
-// near to the border of two codes -- the warp computes its rows again, the
-// values next to a border and next to the group's two ends in 64 bits
-// (exact_unit).  With groups of 128 normal values that is one unit in 60.
+// Codes next to a border.  A key's code is that of its value in 64 bits rounded
+// once to f32: so it does not depend on the order of sums and products.  The
+// rotation itself is f32; what it leaves of a key is off by at most key_error
+// (|a| + |b|) for the pair (a, b) before the rotation.  Where that could turn a
+// code's rounding -- a value so near to the border of two codes -- the warp
+// computes its rows again, the values next to a border and next to the group's
+// two ends in 64 bits (exact_unit).  With groups of 128 normal values that is
+// one warp's 256 values in 100.
 #include <cstdint>
 
 #include "gq4_kv_internal.h"
@@ -34,21 +37,25 @@ namespace {
 
 __device__ unsigned int g_kv_rope_error = 0;
 constexpr int kRopeAppendThreads = 256, kRopeAppendWarps = kRopeAppendThreads / 32;
+constexpr int kRopeTokens = 2;         // tokens of a CTA of keys and values, at most (kv_rows counts on it)
 
 // A rotated value's error relative to |a| + |b|, in units of 2^-24 (a rounding):
-// the angle's rounding 2, the sine and cosine 2, the gain 1, the products and
-// their sum 2, the factor that the row shares 1 (its own error is the same for
-// all of the row and moves no code), and 1 that the value in 64 bits is rounded
-// by.
-constexpr float kKeyError = 9 * 0x1p-24f;
+// the angle's rounding 1, the sine and cosine 2, the products and their sum 2,
+// and 1 that the value in 64 bits is rounded by; with a norm the gain 1 and the
+// factor that the row shares 1 (its own error is the same for all of the row and
+// moves no code).
+__device__ __forceinline__ float key_error(bool norm)
+{
+    return norm ? 8 * 0x1p-24f : 6 * 0x1p-24f;
+}
 // Of a code's argument (v - lo) r, up to 15, on either side: two roundings and r's two.
 constexpr float kCodeError = 8 * 15 * 0x1p-24f;
 
 struct RopeAppendParams {
     gq4_kv_cache c;
-    const float *x[3];       // k, v, q
-    int ld[3];
-    const float *gain[3];    // k's, none, q's (NULL: not normalised)
+    const float *q, *k, *v;
+    int ldq, ldk, ldv;
+    const float *q_gain, *k_gain;   // NULL: not normalised
     float *q_out;
     int ldq_out;
     const int32_t *positions, *slots;
@@ -58,33 +65,64 @@ struct RopeAppendParams {
     bool interleaved;
     int shift, total;        // log2 of the page size; slots of the pool
     uint32_t page_codes, page_sz;   // bytes per page and head
-    int kv_units, units;     // units of k's rows, and of v's; and all (k, v, q)
-    int splits;              // CTAs per token
+    int units;               // warps' rows of K of a token, and as many of V
+    int q_parts;             // CTAs of queries per token
+    int kv_tokens, kv_parts; // tokens per CTA of keys, CTAs per such
+    int q_ctas, kv_ctas, turn;      // all of them; CTAs of queries after each of keys
 };
 
-enum { kKeyRow, kValueRow, kQueryRow };
+// pos * inv_freq less whole quarter turns (n, the nearest), in 64 bits: a 31-bit
+// by a 24-bit product, off by less than 2^-22 of a radian at any position, and a
+// quarter turn in two terms (Cody and Waite's reduction).
+struct Quarter {
+    double r;      // [-pi/4, pi/4]
+    int n;         // modulo 4
 
-// A lane's 8 values and, half-split, their partners.
-struct Words {
-    float4 v[2], w[2];
-};
-
-template <int J>
-struct Unit {
-    int kind, head;
-    bool live;
-    const float *row;
-
-    __device__ __forceinline__ Unit(const RopeAppendParams &p, int t, int u, int in_warp)
+    __device__ __forceinline__ Quarter(int pos, float inv_freq)
     {
-        constexpr int RPW = 32 / (4 * J);
-        kind = u < p.kv_units ? kKeyRow : u < 2 * p.kv_units ? kValueRow : kQueryRow;
-        head = (u - kind * p.kv_units) * RPW + in_warp;
-        live = in_warp < RPW && head < (kind == kQueryRow ? p.q_heads : p.c.kv_heads);
-        row = (kind == kKeyRow ? p.x[0] : kind == kValueRow ? p.x[1] : p.x[2]) +
-              (size_t)t * (kind == kKeyRow ? p.ld[0] : kind == kValueRow ? p.ld[1] : p.ld[2]) + (size_t)head * (32 * J);
+        const double a = (double)pos * (double)inv_freq;
+        const double whole = 6755399441055744.0;                  // 1.5 2^52: a sum's last bit counts ones
+        const double m = fma(a, 0.6366197723675814, whole), k = m - whole;   // 2 / pi
+        r = fma(k, -6.123233995736766e-17, fma(k, -1.5707963267948966, a));
+        n = __double2loint(m) & 3;
     }
 };
+
+// Sine and cosine of x in [-pi/4, pi/4] by their Taylor series, TERMS terms each
+// (f32, 5: off by 2^-28 and a rounding or two; f64, 9: by 2^-58), and n quarter
+// turns on.
+template <int TERMS, typename F>
+__device__ __forceinline__ void sin_cos_series(F x, int n, F &s, F &c)
+{
+    F inverse[2 * TERMS + 1];      // of factorials (constants)
+    inverse[0] = F(1);
+    double f = 1.0;
+#pragma unroll
+    for (int i = 1; i <= 2 * TERMS; ++i) {
+        f *= i;
+        inverse[i] = F(1.0 / f);
+    }
+    const F y = -x * x;
+    F a = inverse[2 * TERMS - 1], b = inverse[2 * TERMS];
+#pragma unroll
+    for (int i = TERMS - 2; i >= 0; --i) a = fma(a, y, inverse[2 * i + 1]);
+#pragma unroll
+    for (int i = TERMS - 1; i >= 1; --i) b = fma(b, y, inverse[2 * i]);
+    b = fma(b, y, F(1));
+    a *= x;
+    s = n & 1 ? b : a;
+    c = n & 1 ? a : b;
+    if (n & 2) s = -s;
+    if ((n + 1) & 2) c = -c;
+}
+
+__device__ __forceinline__ float2 sin_cos_at(int pos, float inv_freq)
+{
+    const Quarter turn(pos, inv_freq);
+    float2 sc;
+    sin_cos_series<5, float>((float)turn.r, turn.n, sc.x, sc.y);
+    return sc;
+}
 
 // The partner of value d (a multiple of 4) of a half-split rotation.
 __device__ __forceinline__ int partner_of(int d, int half)
@@ -92,22 +130,107 @@ __device__ __forceinline__ int partner_of(int d, int half)
     return d < half ? d + half : d - half;
 }
 
-template <int J>
-__device__ __forceinline__ Words load_words_of(const RopeAppendParams &p, const Unit<J> &u, int w)
+__device__ __forceinline__ float4 times(float4 a, float4 b)
 {
-    Words x;
+    return make_float4(a.x * b.x, a.y * b.y, a.z * b.z, a.w * b.w);
+}
+
+__device__ __forceinline__ float square_sum(float4 a)
+{
+    return (a.x * a.x + a.y * a.y) + (a.z * a.z + a.w * a.w);
+}
+
+// Values d .. d + 3 rotated (d < rot); b: their partners, half-split.  sc: the
+// token's sines and cosines.
+__device__ __forceinline__ float4 rotated(float4 a, float4 b, int d, int half, bool interleaved, const float2 *sc)
+{
+    if (interleaved) {
+        const float4 s = *reinterpret_cast<const float4 *>(sc + (d >> 1));
+        return make_float4(a.x * s.y - a.y * s.x, a.y * s.y + a.x * s.x, a.z * s.w - a.w * s.z, a.w * s.w + a.z * s.z);
+    }
+    const bool first = d < half;
+    const float m = first ? -1.0f : 1.0f;
+    const float4 *s = reinterpret_cast<const float4 *>(sc + (first ? d : d - half));
+    const float4 s0 = s[0], s1 = s[1];
+    return make_float4(a.x * s0.y + m * b.x * s0.x, a.y * s0.w + m * b.y * s0.z, a.z * s1.y + m * b.z * s1.x,
+                       a.w * s1.w + m * b.w * s1.z);
+}
+
+// ---------------------------------------------------------------------------
+// Queries
+// ---------------------------------------------------------------------------
+
+// LPR lanes hold a row, CH float4s each; two rows of a warp under way.
+template <int J>
+__device__ __forceinline__ void query_rows(const RopeAppendParams &p, int t, int part, const float2 *sc)
+{
+    constexpr int D4 = 8 * J, LPR = J == 2 ? 16 : 32, CH = J == 8 ? 2 : 1, RPW = 32 / LPR, AHEAD = CH == 1 ? 2 : 1;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane & (LPR - 1);
+    const int half4 = p.rot >> 3, rot4 = p.rot >> 2;
+    const float4 *from = reinterpret_cast<const float4 *>(p.q + (size_t)t * p.ldq);
+    float4 *to = reinterpret_cast<float4 *>(p.q_out + (size_t)t * p.ldq_out);
+    const float4 *gain = reinterpret_cast<const float4 *>(p.q_gain);
+    const int step = kRopeAppendWarps * RPW * p.q_parts;
+    bool waited = false;
+    // every warp takes the same number of turns (the barrier below)
+    for (int row0 = part * kRopeAppendWarps * RPW; row0 < p.q_heads; row0 += AHEAD * step) {
+        const int first = row0 + warp * RPW + lane / LPR;
+        float4 x[AHEAD][CH];
 #pragma unroll
-    for (int f = 0; f < 2; ++f) {
-        const int d = 8 * w + 4 * f;
-        x.v[f] = x.w[f] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (u.live) {
-            x.v[f] = *reinterpret_cast<const float4 *>(u.row + d);
-            if (u.kind != kValueRow && !p.interleaved && d < p.rot)
-                x.w[f] = *reinterpret_cast<const float4 *>(u.row + partner_of(d, p.rot >> 1));
+        for (int u = 0; u < AHEAD; ++u)
+#pragma unroll
+            for (int j = 0; j < CH; ++j) {
+                x[u][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (first + u * step < p.q_heads && l + 32 * j < D4) x[u][j] = from[(first + u * step) * D4 + l + 32 * j];
+            }
+        if (!waited) __syncthreads();      // the sines
+        waited = true;
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) {
+            if (row0 + warp * RPW + u * step >= p.q_heads) break;   // uniform in the warp
+            float r = 1.0f;
+            if (gain) {
+                float s = square_sum(x[u][0]);
+#pragma unroll
+                for (int j = 1; j < CH; ++j) s += square_sum(x[u][j]);
+#pragma unroll
+                for (int o = LPR >> 1; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+                r = inv_sqrt(fmaf(s, p.inv_d, p.eps));
+#pragma unroll
+                for (int j = 0; j < CH; ++j)
+                    if (l + 32 * j < D4) x[u][j] = times(x[u][j], __ldg(gain + l + 32 * j));
+            }
+            float4 y[CH];
+#pragma unroll
+            for (int j = 0; j < CH; ++j) {
+                const int i = l + 32 * j, other = i < half4 ? i + half4 : i - half4;
+                float4 b = x[u][j];
+                if (!p.interleaved) {      // (the whole warp shuffles)
+                    b.x = __shfl_sync(0xffffffffu, x[u][0].x, other, LPR);
+                    b.y = __shfl_sync(0xffffffffu, x[u][0].y, other, LPR);
+                    b.z = __shfl_sync(0xffffffffu, x[u][0].z, other, LPR);
+                    b.w = __shfl_sync(0xffffffffu, x[u][0].w, other, LPR);
+#pragma unroll
+                    for (int n = 1; n < CH; ++n) {
+                        const float4 c = make_float4(__shfl_sync(0xffffffffu, x[u][n].x, other), __shfl_sync(0xffffffffu, x[u][n].y, other),
+                                                     __shfl_sync(0xffffffffu, x[u][n].z, other), __shfl_sync(0xffffffffu, x[u][n].w, other));
+                        if (other >> 5 == n) b = c;
+                    }
+                }
+                y[j] = i < rot4 ? rotated(x[u][j], b, 4 * i, p.rot >> 1, p.interleaved, sc) : x[u][j];
+            }
+            __syncwarp();   // in place: every lane of the row has read before any writes
+#pragma unroll
+            for (int j = 0; j < CH; ++j)
+                if (first + u * step < p.q_heads && l + 32 * j < D4)
+                    to[(first + u * step) * D4 + l + 32 * j] = gain ? times(y[j], make_float4(r, r, r, r)) : y[j];
         }
     }
-    return x;
 }
+
+// ---------------------------------------------------------------------------
+// Keys and values
+// ---------------------------------------------------------------------------
 
 // Sum over a row's lanes, in each of them (lanes of no row: anything).
 template <int WPR, typename V>
@@ -125,52 +248,6 @@ __device__ __forceinline__ V row_sum(V s, int w, int lane)
         s = __shfl_sync(0xffffffffu, s, lane - w);
     }
     return s;
-}
-
-__device__ __forceinline__ float4 times(float4 a, float4 b)
-{
-    return make_float4(a.x * b.x, a.y * b.y, a.z * b.z, a.w * b.w);
-}
-
-// The row's values normalised and rotated.  sc: sines and cosines.
-template <int J>
-__device__ __forceinline__ void turn(const RopeAppendParams &p, int kind, const Words &x, int w, int lane, const float2 *sc,
-                                     float (&v)[8])
-{
-    const float *gain = kind == kKeyRow ? p.gain[0] : p.gain[2];
-    float r = 1.0f;
-    if (gain) {   // uniform in the warp
-        float s[2];
-#pragma unroll
-        for (int f = 0; f < 2; ++f)
-            s[f] = (x.v[f].x * x.v[f].x + x.v[f].y * x.v[f].y) + (x.v[f].z * x.v[f].z + x.v[f].w * x.v[f].w);
-        r = inv_sqrt(fmaf(row_sum<4 * J>(s[0] + s[1], w, lane), p.inv_d, p.eps));
-    }
-    const int half = p.rot >> 1;
-#pragma unroll
-    for (int f = 0; f < 2; ++f) {
-        const int d = 8 * w + 4 * f;
-        float4 a = x.v[f], b = x.w[f];
-        if (gain && d < 32 * J) a = times(a, __ldg(reinterpret_cast<const float4 *>(gain + d)));
-        if (d < p.rot) {
-            if (p.interleaved) {
-                const float4 s = *reinterpret_cast<const float4 *>(sc + (d >> 1));
-                a = make_float4(a.x * s.y - a.y * s.x, a.y * s.y + a.x * s.x, a.z * s.w - a.w * s.z, a.w * s.w + a.z * s.z);
-            } else {
-                const int other = partner_of(d, half);
-                if (gain) b = times(b, __ldg(reinterpret_cast<const float4 *>(gain + other)));
-                const float m = d < half ? -1.0f : 1.0f;
-                const float4 *s = reinterpret_cast<const float4 *>(sc + min(d, other));
-                const float4 s0 = s[0], s1 = s[1];
-                a = make_float4(a.x * s0.y + m * b.x * s0.x, a.y * s0.w + m * b.y * s0.z, a.z * s1.y + m * b.z * s1.x,
-                                a.w * s1.w + m * b.w * s1.z);
-            }
-        }
-        v[4 * f] = a.x * r;
-        v[4 * f + 1] = a.y * r;
-        v[4 * f + 2] = a.z * r;
-        v[4 * f + 3] = a.w * r;
-    }
 }
 
 // A group's ends, and how far a code's argument may be off: of the whole row,
@@ -211,123 +288,245 @@ struct Group {
     }
 };
 
-// An argument's distance to a border of two codes: 0.5 less what it is from the
-// nearest code.
+// An argument's distance to the nearest code.
 __device__ __forceinline__ float from_code(float v, const GroupMap &m)
 {
     const float t = __fmul_rn(__fsub_rn(v, m.lo), m.r);
     return fabsf(t - rintf(t));
 }
 
-__device__ __forceinline__ float code_slack(float largest, const GroupMap &m)
+// How far a code's argument t = 15 (v - lo) / (hi - lo) may be off: v, and lo
+// and hi in the parts 1 - t / 15 and t / 15, each by 2 key_error of the row's
+// largest.
+__device__ __forceinline__ float code_slack(float largest, const GroupMap &m, bool norm)
 {
-    // 2 kKeyError of the largest by the value and by the lower end each, twice that by the scale
-    return fmaf(8.0f * kKeyError * largest, m.r, kCodeError);
+    return fmaf(4.0f * key_error(norm) * largest, m.r, kCodeError);
 }
 
-// A unit of key rows whose values next to a border, and to its group's ends, are
-// computed in 64 bits.  By the whole warp.
+// The 8 codes of a word, as quantize_word's, and how far an argument is from its
+// code at most (FAR).  An argument t is rounded by a sum with 1.5 2^23, whose
+// last bits are then the code: conversions run at an eighth of the rate.  The
+// sum is an FMA with a factor of 1 that the compiler does not see, so that it
+// cannot take the product before it in, which would round that instead of t.
+template <bool FAR>
+__device__ __forceinline__ uint32_t code_word(const float (&v)[8], const GroupMap &m, float &far)
+{
+    constexpr float kOnes = 12582912.0f;
+    float unit = 1.0f;
+    asm volatile("" : "+f"(unit));
+    const f32x2 nlo = pack2(-m.lo, -m.lo), r = pack2(m.r, m.r), one = pack2(unit, unit), ones = pack2(kOnes, kOnes);
+    uint32_t b[8];
+    far = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+        const f32x2 t = mul2(add2(pack2(v[i], v[i + 1]), nlo), r), q = fma2(t, one, ones);
+        const float2 c = unpack2(q);
+        b[i] = __float_as_uint(c.x);
+        b[i + 1] = __float_as_uint(c.y);
+        if (FAR) {
+            const float2 d = unpack2(add2(add2(q, pack2(-kOnes, -kOnes)), mul2(t, pack2(-unit, -unit))));
+            far = fmaxf(far, fmaxf(fabsf(d.x), fabsf(d.y)));
+        }
+    }
+    const uint32_t even = __byte_perm(__byte_perm(b[0], b[2], 0x0040), __byte_perm(b[4], b[6], 0x0040), 0x5410);
+    const uint32_t odd = __byte_perm(__byte_perm(b[1], b[3], 0x0040), __byte_perm(b[5], b[7], 0x0040), 0x5410);
+    return even | (odd << 4);
+}
+
+// A warp's row: its kv head and where it starts.
+template <int J>
+struct KvRow {
+    int head;
+    bool live;
+    const float *at;
+
+    __device__ __forceinline__ KvRow(const RopeAppendParams &p, int t, int unit, bool value, int in_warp)
+    {
+        constexpr int RPW = 32 / (4 * J);
+        head = unit * RPW + in_warp;
+        live = in_warp < RPW && head < p.c.kv_heads;
+        at = (value ? p.v : p.k) + (size_t)t * (value ? p.ldv : p.ldk) + head * (32 * J);
+    }
+};
+
+// The scratch of a warp in exact_unit: its 256 values, and which are needed.
+struct ExactShared {
+    float v[256];
+    uint8_t list[256];
+};
+
+// A unit of key rows whose values (in s.v) next to a border, and to its group's
+// ends, are computed in 64 bits.  By the whole warp.
 template <int J, int L>
-__device__ __noinline__ void exact_unit(const RopeAppendParams &p, int t, int u, int slot, const float2 *sc)
+__device__ __noinline__ void exact_unit(const RopeAppendParams &p, int t, int unit, int slot, ExactShared &s)
 {
     constexpr int D = 32 * J, WPR = 4 * J;
     const int lane = threadIdx.x & 31, in_warp = lane / WPR, w = lane - in_warp * WPR;
-    const Unit<J> unit(p, t, u, in_warp);
-    const Words x = load_words_of(p, unit, w);
+    const KvRow<J> row(p, t, unit, false, in_warp);
+    const bool norm = p.k_gain != nullptr;
     float v[8];
-    turn<J>(p, kKeyRow, x, w, lane, sc, v);
+    auto read = [&] {
+        const float4 a = *reinterpret_cast<const float4 *>(s.v + 8 * lane), b = *reinterpret_cast<const float4 *>(s.v + 8 * lane + 4);
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    };
+    read();
+    // the values needed as a list, of which each lane takes one at a time: most
+    // often there are fewer than lanes
     uint32_t need = 0;
     {
         const Group<J, L> g(v, w, lane);
-        const float largest = g.largest(w, lane), slack = code_slack(largest, g.m), near = 4.0f * kKeyError * largest;
+        const float largest = g.largest(w, lane), slack = code_slack(largest, g.m, norm), near = 4.0f * key_error(norm) * largest;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             if (!(from_code(v[i], g.m) <= 0.5f - slack) || v[i] <= g.lo + near || v[i] >= g.hi - near) need |= 1u << i;
-        if (!unit.live || g.bad) need = 0;
+        if (!row.live || g.bad) need = 0;
     }
-    const float *gain = p.gain[0];
-    double r = 1.0;
-    if (gain) {
-        double s = 0.0;
+    int at = __popc(need);
+    const int mine = at;
 #pragma unroll
-        for (int f = 0; f < 2; ++f)
-            s += (double)x.v[f].x * x.v[f].x + (double)x.v[f].y * x.v[f].y + (double)x.v[f].z * x.v[f].z +
-                 (double)x.v[f].w * x.v[f].w;
-        r = 1.0 / sqrt(row_sum<WPR>(s, w, lane) / D + (double)p.eps);
+    for (int o = 1; o < 32; o <<= 1) {
+        const int n = __shfl_up_sync(0xffffffffu, at, o);
+        if (lane >= o) at += n;
     }
-    const int half = p.rot >> 1, pos = p.rot > 0 ? __ldg(p.positions + t) : 0;
+    const int all = __shfl_sync(0xffffffffu, at, 31);
+    at -= mine;
 #pragma unroll 1
-    for (int i = 0; i < 8; ++i) {
-        if (!(need >> i & 1u)) continue;
-        const int d = 8 * w + i;
-        auto value = [&](int n) { return (double)unit.row[n] * (gain ? (double)__ldg(gain + n) * r : 1.0); };
-        double y = value(d);
-        if (d < p.rot) {
-            const bool first = p.interleaved ? !(d & 1) : d < half;
-            const int other = p.interleaved ? d ^ 1 : partner_of(d, half);
-            const int at = p.interleaved ? d >> 1 : min(d, other);
-            double s, c;
-            sincos((double)pos * (double)__ldg(p.inv_freq + at), &s, &c);
-            y = y * c + (first ? -s : s) * value(other);
+    for (; need; need &= need - 1) s.list[at++] = (uint8_t)(8 * lane + __ffs(need) - 1);
+    double r = 1.0;
+    if (norm) {
+        double sum = 0.0;
+        if (row.live) {
+#pragma unroll 2
+            for (int i = 0; i < 8; ++i) {
+                const double x = row.at[8 * w + i];
+                sum = fma(x, x, sum);
+            }
         }
-        v[i] = (float)y;
+        sum = fma(row_sum<WPR>(sum, w, lane), 1.0 / D, (double)p.eps);
+        r = inv_sqrt((float)sum);          // and two Newton steps
+        r = fma(fma(-0.5 * sum * r, r, 0.5), r, r);
+        r = fma(fma(-0.5 * sum * r, r, 0.5), r, r);
     }
     __syncwarp();
+    const int half = p.rot >> 1, pos = p.rot > 0 ? __ldg(p.positions + t) : 0;
+    for (int n0 = 0; n0 < all; n0 += 32) {
+        const int e = n0 + lane < all ? s.list[n0 + lane] : 0, from = e >> 3;   // value e & 7 of lane `from`
+        const double factor = __shfl_sync(0xffffffffu, r, from);
+        if (n0 + lane < all) {
+            const int d = 8 * (from % WPR) + (e & 7);
+            const float *x = KvRow<J>(p, t, unit, false, from / WPR).at;
+            auto value = [&](int m) { return (double)x[m] * (norm ? (double)__ldg(p.k_gain + m) : 1.0); };
+            double y = value(d);
+            if (d < p.rot) {
+                const bool first = p.interleaved ? !(d & 1) : d < half;
+                const int other = p.interleaved ? d ^ 1 : partner_of(d, half);
+                double sine, cosine;
+                const Quarter turn(pos, __ldg(p.inv_freq + (p.interleaved ? d >> 1 : min(d, other))));
+                sin_cos_series<9, double>(turn.r, turn.n, sine, cosine);
+                y = y * cosine + (first ? -sine : sine) * value(other);
+            }
+            s.v[e] = (float)(y * factor);
+        }
+    }
+    __syncwarp();
+    read();
     const Group<J, L> g(v, w, lane);
     const uint32_t word = g.bad ? 0u : quantize_word(v, g.m);
-    if (unit.live) write_word<J, L>(p, slot, unit.head, 0, w, word, 0u, g.bad, g.m, &g_kv_rope_error);
+    if (row.live) write_word<J, L>(p, slot, row.head, 0, w, word, 0u, g.bad, g.m, &g_kv_rope_error);
+    __syncwarp();
+}
+
+template <int J, int L>
+__device__ __forceinline__ void kv_rows(const RopeAppendParams &p, int t0, int part, const float2 *sc, ExactShared *exact)
+{
+    constexpr int WPR = 4 * J;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int in_warp = lane / WPR, w = lane - in_warp * WPR;
+    const int units = min(p.kv_tokens, p.T - t0) * 2 * p.units, step = kRopeAppendWarps * p.kv_parts;
+    const int half = p.rot >> 1;
+    bool waited = false;
+    // every warp takes the same number of turns (the barrier below)
+    for (int u0 = part * kRopeAppendWarps; u0 < units; u0 += step) {
+        const int u = u0 + warp, n = u >= 2 * p.units, rest = u - n * 2 * p.units, t = t0 + n;
+        // a token's units of K and of V, of every second token the other way round: a warp gets both
+        const bool value = (rest >= p.units) != (n & 1);
+        const int unit = rest >= p.units ? rest - p.units : rest;
+        const KvRow<J> row(p, t, unit, value, in_warp);
+        const bool in = u < units && row.live;
+        const int slot = u < units ? __ldg(p.slots + t) : -1;
+        float4 a[2], b[2];
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+            const int d = 8 * w + 4 * f;
+            a[f] = b[f] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (in) {
+                a[f] = *reinterpret_cast<const float4 *>(row.at + d);
+                if (!value && !p.interleaved && d < p.rot) b[f] = *reinterpret_cast<const float4 *>(row.at + partner_of(d, half));
+            }
+        }
+        if (!waited) __syncthreads();      // the sines
+        waited = true;
+        if (slot < 0) continue;            // uniform in the warp
+        if (!value) {
+            float r = 1.0f;
+            if (p.k_gain) {
+                r = inv_sqrt(fmaf(row_sum<WPR>(square_sum(a[0]) + square_sum(a[1]), w, lane), p.inv_d, p.eps));
+#pragma unroll
+                for (int f = 0; f < 2; ++f) {
+                    const int d = 8 * w + 4 * f;
+                    a[f] = times(a[f], __ldg(reinterpret_cast<const float4 *>(p.k_gain + d)));
+                    if (!p.interleaved && d < p.rot) b[f] = times(b[f], __ldg(reinterpret_cast<const float4 *>(p.k_gain + partner_of(d, half))));
+                }
+            }
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+                const int d = 8 * w + 4 * f;
+                if (d < p.rot) a[f] = rotated(a[f], b[f], d, half, p.interleaved, sc + n * 16 * J);
+                if (p.k_gain) a[f] = times(a[f], make_float4(r, r, r, r));
+            }
+        }
+        const float v[8] = {a[0].x, a[0].y, a[0].z, a[0].w, a[1].x, a[1].y, a[1].z, a[1].w};
+        const Group<J, L> g(v, w, lane);
+        bool border = false;
+        float far;
+        uint32_t word = code_word<true>(v, g.m, far);
+        if (!value && (p.rot > 0 || p.k_gain))
+            border = !(far <= 0.5f - code_slack(g.largest(w, lane), g.m, p.k_gain != nullptr)) && row.live && !g.bad;
+        if (__any_sync(0xffffffffu, border)) {
+            float4 *to = reinterpret_cast<float4 *>(exact[warp].v + 8 * lane);
+            to[0] = a[0];
+            to[1] = a[1];
+            __syncwarp();
+            exact_unit<J, L>(p, t, unit, slot, exact[warp]);
+        } else {
+            word = g.bad ? 0u : word;
+            const uint32_t other = __shfl_xor_sync(0xffffffffu, word, 4);
+            if (row.live) write_word<J, L>(p, slot, row.head, value, w, word, other, g.bad, g.m, &g_kv_rope_error);
+        }
+    }
 }
 
 // J = head_dim / 32; L: lanes per group.
 template <int J, int L>
-__global__ void __launch_bounds__(kRopeAppendThreads) rope_append_kernel(const __grid_constant__ RopeAppendParams p)
+__global__ void __launch_bounds__(kRopeAppendThreads, 7) rope_append_kernel(const __grid_constant__ RopeAppendParams p)
 {
-    constexpr int WPR = 4 * J;
-    __shared__ alignas(16) float2 sc[16 * J];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int in_warp = lane / WPR, w = lane - in_warp * WPR;
-    const int t = blockIdx.x / p.splits, part = blockIdx.x - t * p.splits;
-    const int slot = __ldg(p.slots + t);
-    int u = part * kRopeAppendWarps + warp;
-    const int step = p.splits * kRopeAppendWarps;
-    Words x;
-    if (u < p.units) x = load_words_of(p, Unit<J>(p, t, u, in_warp), w);
-    if (p.rot > 0) {
-        const int pos = __ldg(p.positions + t);
-        for (int i = threadIdx.x; i < p.rot >> 1; i += kRopeAppendThreads) sc[i] = sin_cos_of(pos, __ldg(p.inv_freq + i));
+    __shared__ alignas(16) float2 sc[kRopeTokens * 16 * J];
+    __shared__ alignas(16) ExactShared exact[kRopeAppendWarps];
+    const int turn = blockIdx.x / (p.turn + 1), place = blockIdx.x - turn * (p.turn + 1);
+    const bool kv = place == 0;
+    const int cta = kv ? turn : turn * p.turn + place - 1;
+    if (cta >= (kv ? p.kv_ctas : p.q_ctas)) return;
+    const int parts = kv ? p.kv_parts : p.q_parts, per = kv ? p.kv_tokens : 1;
+    const int item = parts == 1 ? cta : cta / parts, t0 = item * per, part = cta - item * parts;
+    // the tokens' sines and cosines
+    const int half = p.rot >> 1, tokens = min(per, p.T - t0);
+    for (int i = threadIdx.x; i < tokens * half; i += kRopeAppendThreads) {
+        const int n = i >= half, x = i - n * half;
+        sc[n * 16 * J + x] = sin_cos_at(__ldg(p.positions + t0 + n), __ldg(p.inv_freq + x));
     }
-    __syncthreads();
-    while (u < p.units) {   // uniform in the warp
-        const Unit<J> unit(p, t, u, in_warp);
-        float v[8] = {x.v[0].x, x.v[0].y, x.v[0].z, x.v[0].w, x.v[1].x, x.v[1].y, x.v[1].z, x.v[1].w};
-        if (unit.kind != kValueRow) turn<J>(p, unit.kind, x, w, lane, sc, v);
-        if (unit.kind == kQueryRow) {
-            __syncwarp();   // in place: every lane of the row has read before any writes
-            if (unit.live) {
-                float4 *y = reinterpret_cast<float4 *>(p.q_out + (size_t)t * p.ldq_out + (size_t)unit.head * (32 * J) + 8 * w);
-                y[0] = make_float4(v[0], v[1], v[2], v[3]);
-                y[1] = make_float4(v[4], v[5], v[6], v[7]);
-            }
-        } else if (slot >= 0) {
-            const Group<J, L> g(v, w, lane);
-            bool border = false;
-            if (unit.kind == kKeyRow && (p.rot > 0 || p.gain[0])) {
-                float far = 0.0f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) far = fmaxf(far, from_code(v[i], g.m));
-                border = !(far <= 0.5f - code_slack(g.largest(w, lane), g.m)) && unit.live && !g.bad;
-            }
-            if (__any_sync(0xffffffffu, border)) {
-                exact_unit<J, L>(p, t, u, slot, sc);
-            } else {
-                const uint32_t word = g.bad ? 0u : quantize_word(v, g.m);
-                const uint32_t other = __shfl_xor_sync(0xffffffffu, word, 4);
-                if (unit.live) write_word<J, L>(p, slot, unit.head, unit.kind == kValueRow, w, word, other, g.bad, g.m, &g_kv_rope_error);
-            }
-        }
-        u += step;
-        if (u < p.units) x = load_words_of(p, Unit<J>(p, t, u, in_warp), w);
-    }
+    if (kv) kv_rows<J, L>(p, t0, part, sc, exact);
+    else query_rows<J>(p, t0, part, sc);
 }
 
 }  // namespace
@@ -337,14 +536,14 @@ cudaError_t launch_kv_rope_append(const RopeCall &call, const gq4_kv_cache &c, c
 {
     RopeAppendParams p{};
     p.c = c;
-    p.x[0] = call.x[1];
-    p.x[1] = v;
-    p.x[2] = call.x[0];
-    p.ld[0] = call.ldx[1];
-    p.ld[1] = ldv;
-    p.ld[2] = call.ldx[0];
-    p.gain[0] = call.gain[1];
-    p.gain[2] = call.gain[0];
+    p.q = call.x[0];
+    p.k = call.x[1];
+    p.v = v;
+    p.ldq = call.ldx[0];
+    p.ldk = call.ldx[1];
+    p.ldv = ldv;
+    p.q_gain = call.gain[0];
+    p.k_gain = call.gain[1];
     p.q_out = call.y[0];
     p.ldq_out = call.ldy[0];
     p.positions = call.positions;
@@ -361,12 +560,18 @@ cudaError_t launch_kv_rope_append(const RopeCall &call, const gq4_kv_cache &c, c
     p.page_codes = (uint32_t)(c.page_size * c.head_dim / 2);
     p.page_sz = (uint32_t)(c.page_size * (c.head_dim / c.group_size) * 8);
     const int per = 32 / (c.head_dim / 8);
-    p.kv_units = (c.kv_heads + per - 1) / per;
-    p.units = 2 * p.kv_units + (p.q_heads + per - 1) / per;
+    p.units = (c.kv_heads + per - 1) / per;
     // few tokens: their rows over several CTAs, until the GPU has two each
-    p.splits = 1;
-    while (p.splits * kRopeAppendWarps < p.units && (long long)call.T * p.splits < 2 * 152) ++p.splits;
-    const long long grid = (long long)call.T * p.splits;
+    const bool few = call.T < 2 * 152;
+    auto parts = [&](int rows) { return few ? (rows + kRopeAppendWarps - 1) / kRopeAppendWarps : 1; };
+    p.q_parts = parts(c.head_dim == 64 ? (p.q_heads + 1) / 2 : p.q_heads);
+    p.kv_tokens = few ? 1 : kRopeTokens;
+    p.kv_parts = parts(2 * p.units);
+    if ((long long)call.T * (p.q_parts + p.kv_parts) > 0x3fffffffll) return cudaErrorInvalidValue;
+    p.q_ctas = call.heads[0] > 0 ? call.T * p.q_parts : 0;
+    p.kv_ctas = (call.T + p.kv_tokens - 1) / p.kv_tokens * p.kv_parts;
+    p.turn = (p.q_ctas + p.kv_ctas - 1) / p.kv_ctas;
+    const long long grid = (long long)p.kv_ctas * (p.turn + 1);
     if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
     auto run = [&](auto kern) { kern<<<(unsigned)grid, kRopeAppendThreads, 0, stream>>>(p); };
     switch (c.head_dim * 16 + c.group_size / 32) {
