@@ -581,8 +581,10 @@ GQ4_API gq4_status gq4_kv_attention(int B, int T, int q_heads, int max_pages, in
  *       Any bits do (gq4_kv_tree makes those of a tree from its parents); bits
  *       from n on count for nothing.  A request of more than 32 * tree_words
  *       queries is beyond the call's bounds (NaN rows, bit 8).  NULL: none.
- * Everything else -- pages, bounds, errors, accuracy, workspace, a row that sees
- * nothing -- is gq4_kv_attention's; without tree and sinks it is that call. */
+ * Everything else -- pages, bounds, errors, accuracy, a row that sees nothing --
+ * is gq4_kv_attention's; without tree and sinks it is that call.  workspace: at
+ * least gq4_kv_attention_masked_workspace_bytes() bytes with a tree (20 MB more,
+ * for sums of shared row tiles), gq4_kv_attention_workspace_bytes() without. */
 #define GQ4_MAX_TREE_WORDS 8
 typedef struct gq4_kv_mask {
     int window;                 /* 0: none */
@@ -591,6 +593,9 @@ typedef struct gq4_kv_mask {
     int tree_words;             /* 1 .. GQ4_MAX_TREE_WORDS */
     const int32_t *positions;   /* [T]; may be NULL without a tree or a window */
 } gq4_kv_mask;
+
+GQ4_API size_t gq4_kv_attention_masked_workspace_bytes(int T, int q_heads, int kv_heads,
+                                                       int head_dim);
 
 GQ4_API gq4_status gq4_kv_attention_masked(int B, int T, int q_heads, int max_pages, int max_query,
                                            int max_len, const gq4_kv_cache *cache, const float *q,

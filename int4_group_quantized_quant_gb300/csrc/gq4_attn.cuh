@@ -246,9 +246,10 @@ __device__ __noinline__ void small_rows(const AttnCall &a, const AttnRequest &rq
 // takes a key and then, of every key, four of the head's values.  Rare, so in
 // the call's last kernel: such code in the prompt kernel itself, run or not,
 // cost it 1 to 6 % (its roles fill the registers and share the instruction
-// cache).  By the whole CTA.
+// cache).  By the whole CTA; MASKS: rows row_lo .. row_hi - 1 of the tile.
 template <int J, int G, bool MASKS>
-__device__ __noinline__ void apart_rows(const AttnCall &a, const ApartTile &at, int h, ApartShared<J> &s)
+__device__ __noinline__ void apart_rows(const AttnCall &a, const ApartTile &at, int h, ApartShared<J> &s, int row_lo = 0,
+                                        int row_hi = kPromptTile)
 {
     constexpr int D = 32 * J, GS = D / G;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = at.request;
@@ -264,7 +265,7 @@ __device__ __noinline__ void apart_rows(const AttnCall &a, const ApartTile &at, 
     __syncthreads();
     if (at.uneven) small_rows<J, G, MASKS>(a, rq, at, h, s.rows);
     __syncthreads();
-    for (int r = warp; r < kPromptTile; r += kJoinThreads / 32) {
+    for (int r = (MASKS ? row_lo : 0) + warp; r < (MASKS ? row_hi : kPromptTile); r += kJoinThreads / 32) {
         if (!(s.rows[r >> 5] >> (r & 31) & 1u)) continue;
         const int rho = at.tile * kPromptTile + r, j = rho / R, head = h * R + rho - j * R;
         if (rho >= rq.n * R) break;

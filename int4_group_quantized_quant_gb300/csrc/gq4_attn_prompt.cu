@@ -10,7 +10,7 @@ bool prompt_path_supported(const AttnCall &call)
 
 cudaError_t launch_attn_prompt(const AttnCall &call, cudaStream_t stream)
 {
-    return launch_many_rows<false>(call, stream);
+    return launch_many_rows<kCausal>(call, stream);
 }
 
 cudaError_t read_prompt_device_error(unsigned int *bits, bool clear)

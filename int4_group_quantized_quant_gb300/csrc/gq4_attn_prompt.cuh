@@ -83,6 +83,10 @@ struct PromptParams {
     AttnCall a;
 };
 
+// The forms: causal; behind first tokens that stay visible; with ancestor bits,
+// where the CTAs stay and share the tiles.
+enum { kCausal, kSinks, kTree };
+
 // The warps of a form, and its pieces of K and V.
 template <bool EXACT>
 struct Form {
@@ -123,6 +127,25 @@ struct Mem {
 
 struct Bars {
     uint64_t *k_full, *k_empty, *v_full, *v_empty, *s_full, *sp_empty, *p_full, *o_full, *o_empty, *fin, *drain, *raw_full, *raw_empty;
+
+    __device__ __forceinline__ explicit Bars(unsigned char *at)
+    {
+        uint64_t *b = reinterpret_cast<uint64_t *>(at);
+        k_full = b;
+        k_empty = b + 4;
+        v_full = b + 8;
+        v_empty = b + 12;
+        o_full = b + 16;
+        o_empty = b + 18;
+        s_full = b + 20;
+        sp_empty = b + 20 + kSP;
+        p_full = b + 20 + 2 * kSP;
+        fin = b + 20 + 2 * kSP + kTab;
+        drain = fin + 1;
+        raw_full = fin + 3;
+        raw_empty = raw_full + 4;
+    }
+    static constexpr int kAll = 20 + 2 * kSP + kTab + 3 + 8;
 };
 
 // One MMA, A and B from shared memory, D in tensor memory: the low words of
@@ -612,123 +635,265 @@ __device__ __noinline__ uint2 tile_sight(const AttnCall &a, int b, int rho, int 
     return make_uint2(sight_bits(a, s, k0), sight_bits(a, s, k0 + 32));
 }
 
-// J: 32-value blocks of a row, G: scale groups per row, DP: padded head.
-template <int J, int G, int DP, bool MASKS>
-__global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_constant__ PromptParams p)
+// kTree: what a CTA does of a row tile.
+struct Segment {
+    int req, tile, head;
+    int from, upto;                        // of the row tile's tiles
+    int slot;                              // of its sums in the workspace, -1: the row tile is the CTA's alone
+    long long entry;                       // of its marks
+};
+
+// What a CTA's threads share beside the operands.
+struct CtaShared {
+    int sums[kWarps], big, small;
+    volatile int req, tile;
+    uint32_t apart[kRows / 32];            // a bit per row that is left to the last kernel
+    int uneven;                            // it is to look for rows that see small values only
+    volatile int abort;
+    uint32_t tmem;
+};
+struct TreeShared {
+    Segment now, next;
+    volatile int more;                     // next is one
+    // the range of stages of this CTA (see walk_start), and where the next segment starts
+    long long pos, end, unit_at, share;
+    int at_req, unit, off;                 // request; of it (row tile, kv head); stage
+};
+__shared__ TreeShared walk;                // (in kTree's kernels only)
+__shared__ CtaShared cta;                  // (known addresses: pointers to it would cost registers)
+
+// The operands' memory, from a 1024-byte boundary on.
+__device__ __forceinline__ unsigned char *operands()
 {
+    extern __shared__ unsigned char smem_raw[];
+    return smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+}
+
+// Barriers, and what a row tile starts with.  By the whole CTA, between barriers
+// of its own.
+template <bool EXACT, bool AGAIN>
+__device__ __forceinline__ void set_up(unsigned char *at)
+{
+    using W = Form<EXACT>;
+    const Bars bar(at);
+    const int i = threadIdx.x;
+    if (i < Bars::kAll) {
+        uint64_t *b = bar.k_full + i;
+        const uint32_t count = b < bar.k_empty    ? W::kDqWarps + 1   // and the tables'
+                               : b < bar.v_full   ? 1
+                               : b < bar.v_empty  ? W::kDqWarps
+                               : b < bar.o_empty  ? 1
+                               : b < bar.s_full   ? kCoWarps
+                               : b < bar.p_full   ? 1
+                               : b < bar.fin      ? 4
+                               : b < bar.drain    ? W::kCo0
+                               : b < bar.raw_full ? 1
+                               : b < bar.raw_empty ? 32               // every copying thread's copies
+                                                   : W::kDqWarps + 1;
+        if (AGAIN) asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(smem_addr(b)) : "memory");
+        mbar_init(b, count);
+        mbar_fence_init();
+    }
+    if (i < kRows / 32) cta.apart[i] = 0;
+    if (i == 0) {
+        cta.abort = 0;
+        cta.big = 0;
+        cta.small = 0x7f800000;
+        cta.uneven = 0;
+    }
+}
+
+// ---- kTree: which tiles a CTA does ----
+// Its CTAs are as many as the GPU has SMs, and each takes an equal share of all
+// tiles: of the list of (request, row tile, kv head), a unit, each a start and
+// its tiles.  All row tiles of a tree see the same keys.  A unit that is cut
+// leaves its sums in the workspace, at most two of them per CTA (slot 0: of a unit
+// that began before, 1: of one that goes on after), and the last kernel joins
+// them.  kUnitStart: what a start and an end cost, in tiles.
+template <bool EXACT>
+constexpr int kUnitStart = EXACT ? 6 : 4;
+// No CTA takes less than this.
+constexpr int kLeastShare = 12;
+
+// a / b of nonnegative numbers, in 32 bits where they allow it.
+__device__ __forceinline__ long long quotient_of(long long a, long long b)
+{
+    return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+struct TreeWork {
+    int units;          // row tiles times kv heads
+    int length;         // of each, with its start
+};
+
+template <bool EXACT>
+__device__ __forceinline__ TreeWork tree_work(const AttnCall &a, int b)
+{
+    TreeWork w{0, 1};
+    if (b >= a.B) return w;
+    const AttnRequest r = attn_request<true>(a, b);
+    if (!prompt_takes(a, r)) return w;
+    const int see_lo = attn_first(a, max(r.len - r.n, -1));
+    w.units = (r.n * (a.heads / a.c.kv_heads) + kRows - 1) / kRows * a.c.kv_heads;
+    w.length = (r.len - 1) / kTile - see_lo / kTile + 1 + lead_blocks(a, see_lo, kTile) + kUnitStart<EXACT>;
+    return w;
+}
+
+// Of two numbers: what the CTA's threads before have, and all.  In scratch of
+// 2 kWarps numbers.
+struct TwoSums {
+    long long before[2], all[2];
+};
+
+__device__ __forceinline__ TwoSums scan_two(long long v0, long long v1, long long *sums)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    TwoSums s;
+    const long long v[2] = {v0, v1};
+    __syncthreads();
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        long long inc = v[x];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long u = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += u;
+        }
+        if (lane == 31) sums[x * kWarps + warp] = inc;
+        s.before[x] = inc - v[x];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        const long long of = lane < kWarps ? sums[x * kWarps + lane] : 0;
+        long long inc = of;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long u = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += u;
+        }
+        s.all[x] = __shfl_sync(0xffffffffu, inc, 31);
+        s.before[x] += __shfl_sync(0xffffffffu, inc - of, warp);
+    }
+    return s;
+}
+
+__device__ __forceinline__ void no_marks(ApartTile &to)
+{
+    to.rows[0] = to.rows[1] = to.rows[2] = to.rows[3] = 0;
+    to.uneven = 0;
+}
+
+// The segment that starts at walk.pos into walk.next, and walk.pos behind it;
+// walk.more: there is one.  (A range that ends within a unit's start ends there.)
+// By one thread.
+template <bool EXACT>
+__device__ __noinline__ void walk_on(const AttnCall &a)
+{
+    constexpr int kStart = kUnitStart<EXACT>;
+    walk.more = 0;
+    if (walk.pos >= walk.end) return;
+    TreeWork w = tree_work<EXACT>(a, walk.at_req);
+    while (walk.unit >= w.units) {          // the next request with work (there is one)
+        walk.unit = 0;
+        w = tree_work<EXACT>(a, ++walk.at_req);
+    }
+    const int off = walk.off, upto = (int)min((long long)w.length, off + (walk.end - walk.pos));
+    const int from = max(off - kStart, 0);
+    if (upto - kStart > from) {
+        const bool first = from == 0, last = upto == w.length;
+        Segment &s = walk.next;
+        s.req = walk.at_req;
+        s.tile = walk.unit / a.c.kv_heads;
+        s.head = walk.unit - s.tile * a.c.kv_heads;
+        s.from = from;
+        s.upto = upto - kStart;
+        s.slot = first && last ? -1 : first ? 1 : 0;
+        s.entry = first && last ? walk.unit_at : a.n_units + 2ll * blockIdx.x + s.slot;
+        if (first && !last) {
+            // it goes on in the CTAs up to the one that holds its last tile
+            const int until = (int)quotient_of(walk.pos - off + w.length - 1, walk.share);
+            a.cut[blockIdx.x] = make_int4(s.req, s.tile, s.head, until);
+            no_marks(a.apart[walk.unit_at]);
+        }
+        walk.more = 1;
+    }
+    walk.pos += upto - off;
+    walk.off = 0;
+    ++walk.unit;
+    ++walk.unit_at;
+}
+
+// This CTA's range and its first segment; false: it has none.
+template <bool EXACT>
+__device__ __noinline__ bool walk_start(const AttnCall &a)
+{
+    if (threadIdx.x == 0) {
+        a.cut[blockIdx.x] = make_int4(0, 0, 0, -1);
+        no_marks(a.apart[a.n_units + 2 * blockIdx.x]);
+        no_marks(a.apart[a.n_units + 2 * blockIdx.x + 1]);
+    }
+    long long total = 0, units = 0;
+    long long *sums = reinterpret_cast<long long *>(operands());   // (not in use yet)
+    TreeWork mine{0, 1};
+    TwoSums t{};
+    for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+        mine = tree_work<EXACT>(a, b0 + (int)threadIdx.x);
+        t = scan_two((long long)mine.units * mine.length, mine.units, sums);
+        total += t.all[0];
+        units += t.all[1];
+    }
+    // units that are not there leave nothing to the last kernel
+    for (long long i = units + (long long)blockIdx.x * kThreads + threadIdx.x; i < a.n_units; i += (long long)gridDim.x * kThreads)
+        no_marks(a.apart[i]);
+    const long long even = quotient_of(total + gridDim.x - 1, gridDim.x), share = max(even, (long long)kLeastShare);
+    const long long pos = share * blockIdx.x, end = min(pos + share, total);
+    if (pos >= end) return false;          // uniform
+    long long base = 0, base_units = 0;
+    for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+        if (a.B > kThreads) {
+            mine = tree_work<EXACT>(a, b0 + (int)threadIdx.x);
+            t = scan_two((long long)mine.units * mine.length, mine.units, sums);
+        }
+        const long long rel = pos - base - t.before[0];
+        if (rel >= 0 && rel < (long long)mine.units * mine.length) {
+            walk.at_req = b0 + (int)threadIdx.x;
+            walk.unit = (int)quotient_of(rel, mine.length);
+            walk.off = (int)(rel - (long long)walk.unit * mine.length);
+            walk.unit_at = base_units + t.before[1] + walk.unit;
+            walk.pos = pos;
+            walk.end = end;
+            walk.share = share;
+        }
+        base += t.all[0];
+        base_units += t.all[1];
+        if (base > pos) break;             // uniform
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        walk_on<EXACT>(a);
+        walk.now = walk.next;
+    }
+    __syncthreads();
+    return walk.more != 0;
+}
+
+// One row tile's keys, or this CTA's share of them.  By the whole CTA.
+template <int J, int G, int DP, int MODE>
+__device__ __forceinline__ void row_tile(const AttnCall &a, int h)
+{
+    constexpr bool MASKS = MODE != kCausal, TREE = MODE == kTree;
     constexpr int D = 32 * J, UG = J / G;
     constexpr bool EXACT = G == 1;
     using W = Form<EXACT>;
     using M = Mem<J, G, DP>;
-    extern __shared__ unsigned char smem_raw[];
-    unsigned char *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
-    const uint32_t smem_s = smem_addr(smem);
-    __shared__ int s_sums[kWarps], s_big, s_small;
-    __shared__ volatile int s_req, s_tile;
-    __shared__ uint32_t s_apart[kRows / 32];               // a bit per row that is left to the last kernel
-    __shared__ int s_uneven;                               // it is to look for rows that see small values only
-    __shared__ volatile int s_abort;
-    __shared__ uint32_t s_tmem;
-    const AttnCall &a = p.a;
+    unsigned char *smem = operands();
+    const uint32_t smem_s = smem_addr(smem), tmem = cta.tmem;
+    const Bars bar(smem + M::offBar);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int H = a.c.kv_heads, R = a.heads / H;
-
-    // ---- this CTA's request and row tile: the last ones (most keys) first ----
-    const int h = (int)(blockIdx.x % (unsigned)H);
-    {
-        auto tiles_of = [&](int b) {
-            if (b >= a.B) return 0;
-            const AttnRequest r = attn_request<MASKS>(a, b);
-            return prompt_takes(a, r) ? (r.n * R + kRows - 1) / kRows : 0;
-        };
-        int all = 0, mine = 0, before = 0;
-        if (a.B == 1) all = mine = tiles_of(0);
-        else for (int b0 = 0; b0 < a.B; b0 += kThreads) {
-            int t;
-            mine = tiles_of(b0 + (int)threadIdx.x);
-            before = scan_ints<kWarps>(mine, t, s_sums);
-            all += t;
-        }
-        const int want = all - 1 - (int)(blockIdx.x / (unsigned)H);
-        if (want < 0) {   // uniform
-            if (threadIdx.x < kRows / 32) a.apart[blockIdx.x].rows[threadIdx.x] = 0;
-            if (threadIdx.x == kRows / 32) a.apart[blockIdx.x].uneven = 0;
-            return;
-        }
-        int base = 0;
-        for (int b0 = 0; b0 < a.B; b0 += kThreads) {
-            int t = all;
-            if (a.B > kThreads) {
-                mine = tiles_of(b0 + (int)threadIdx.x);
-                before = scan_ints<kWarps>(mine, t, s_sums);
-            }
-            if (want >= base + before && want < base + before + mine && (a.B > 1 || threadIdx.x == 0)) {
-                s_req = b0 + (int)threadIdx.x;
-                s_tile = want - (base + before);
-            }
-            base += t;
-            if (base > want) break;   // uniform
-        }
-    }
-    Bars bar;
-    {
-        uint64_t *b = reinterpret_cast<uint64_t *>(smem + M::offBar);
-        bar.k_full = b;
-        bar.k_empty = b + 4;
-        bar.v_full = b + 8;
-        bar.v_empty = b + 12;
-        bar.o_full = b + 16;
-        bar.o_empty = b + 18;
-        bar.s_full = b + 20;
-        bar.sp_empty = b + 20 + kSP;
-        bar.p_full = b + 20 + 2 * kSP;
-        bar.fin = b + 20 + 2 * kSP + kTab;
-        bar.drain = bar.fin + 1;
-        bar.raw_full = bar.fin + 3;
-        bar.raw_empty = bar.raw_full + 4;
-    }
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < W::kSlots; ++s) {
-            mbar_init(&bar.k_full[s], W::kDqWarps + 1);   // and the tables'
-            mbar_init(&bar.k_empty[s], 1);
-            mbar_init(&bar.v_full[s], W::kDqWarps);
-            mbar_init(&bar.v_empty[s], 1);
-        }
-        for (int s = 0; s < 2; ++s) {
-            mbar_init(&bar.o_full[s], 1);
-            mbar_init(&bar.o_empty[s], kCoWarps);
-        }
-        for (int s = 0; s < kSP; ++s) {
-            mbar_init(&bar.s_full[s], 1);
-            mbar_init(&bar.sp_empty[s], 1);
-        }
-        for (int s = 0; s < kTab; ++s) mbar_init(&bar.p_full[s], 4);
-        mbar_init(bar.fin, W::kCo0);
-        mbar_init(bar.drain, 1);
-        mbar_init(bar.drain + 1, 1);
-        for (int s = 0; s < W::kRaw; ++s) {
-            mbar_init(&bar.raw_full[s], 32);       // every copying thread's copies
-            mbar_init(&bar.raw_empty[s], W::kDqWarps + 1);
-        }
-        s_abort = 0;
-        s_big = 0;
-        s_small = 0x7f800000;
-#pragma unroll
-        for (int x = 0; x < kRows / 32; ++x) s_apart[x] = 0;
-        s_uneven = 0;
-        mbar_fence_init();
-    }
-    if (warp == W::kMma) {
-        tmem_alloc(&s_tmem, kTmemCols);
-        tmem_relinquish();
-    }
-    tc_fence_before_sync();
-    __syncthreads();
-    tc_fence_after_sync();
-    const uint32_t tmem = s_tmem;
-    volatile int *abort = &s_abort;
-
-    const int b = s_req, tile = s_tile;
+    volatile int *abort = &cta.abort;
+    const int b = TREE ? walk.now.req : cta.req, tile = TREE ? walk.now.tile : cta.tile;
     const AttnRequest rq = attn_request<MASKS>(a, b);
     const int rows_all = rq.n * R, row0 = tile * kRows;
     const int pos0 = rq.len - rq.n;                        // position of the request's first query
@@ -740,9 +905,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
     // MASKS: keys before this one are seen whatever the window
     const int kept = MASKS && a.window > 0 ? a.sinks : 0;
     const int tile_lo = see_lo / kTile, lead = MASKS ? lead_blocks(a, see_lo, kTile) : 0;
-    const int n_tiles = see_hi >= see_lo ? see_hi / kTile - tile_lo + 1 + lead : 0;
+    // TREE: this CTA's share of the row tile's tiles
+    const int tile0 = TREE ? walk.now.from : 0;
+    const int n_tiles = TREE ? walk.now.upto - tile0 : see_hi >= see_lo ? see_hi / kTile - tile_lo + 1 + lead : 0;
     // the first key of tile i
-    auto key_of_tile = [&](int i) { return (MASKS && i < lead ? i : tile_lo + i - (MASKS ? lead : 0)) * kTile; };
+    auto key_of_tile = [&](int i) {
+        if (TREE) i += tile0;
+        return (MASKS && i < lead ? i : tile_lo + i - (MASKS ? lead : 0)) * kTile;
+    };
 
     // ---- Q: two fp16 pieces with one power of two for the CTA, by the softmax
     // and adding warps; the others are under way meanwhile, but the tables need
@@ -754,8 +924,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         else asm volatile("bar.sync 2, %0;" ::"n"(kStaging + 32) : "memory");
     };
     if (warp == W::kCopy + 1) {
+        // (this warp has time now)
+        if (TREE && lane == 0) walk_on<EXACT>(a);
         meet(1);
-        kq = scale_exponent(__int_as_float(s_big));
+        kq = scale_exponent(__int_as_float(cta.big));
     } else if (warp == W::kMma) {
         meet(2);
     } else if (warp < W::kDq0) {
@@ -798,15 +970,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         const unsigned int top = __reduce_max_sync(0xffffffffu, __float_as_uint(big));
         const unsigned int least = __reduce_min_sync(0xffffffffu, __float_as_uint(small));
         if (lane == 0) {
-            atomicMax(&s_big, (int)top);
-            atomicMin(&s_small, (int)least);
+            atomicMax(&cta.big, (int)top);
+            atomicMin(&cta.small, (int)least);
         }
         meet(1);
-        kq = scale_exponent(__int_as_float(s_big));
-        if (s_small < 0x7f800000 && scale_exponent(__int_as_float(s_small)) - kq > kSpread) {
+        kq = scale_exponent(__int_as_float(cta.big));
+        if (cta.small < 0x7f800000 && scale_exponent(__int_as_float(cta.small)) - kq > kSpread) {
             // rows of less than 2^-kSpread of the largest would lose digits to it
             const float m = th < kRows ? reinterpret_cast<const float *>(smem + M::offL)[th] : 0.0f;
-            if (m > 0.0f && scale_exponent(m) - kq > kSpread) atomicOr(&s_apart[th >> 5], 1u << (th & 31));
+            if (m > 0.0f && scale_exponent(m) - kq > kSpread) atomicOr(&cta.apart[th >> 5], 1u << (th & 31));
         }
         const float up = pow2(kq);
 #pragma unroll
@@ -933,16 +1105,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         // not needed any more, unless the kernel gave up.
         constexpr int X = C / 4;           // 16-byte pieces of half a row
         float4 *stage = reinterpret_cast<float4 *>(smem + M::offK) + (warp - W::kCo0) * 32 * X;
-        float inv = quiet_nan();
+        float inv = quiet_nan(), l = 0.0f;
         if (ok) {
             const float2 *gl = reinterpret_cast<const float2 *>(smem + M::offL);
-            float l = 0.0f;
 #pragma unroll
             for (int x = 0; x < W::kGroups; ++x) {
                 const float2 v = gl[x * kRows + row];
                 if (v.x != -INFINITY) l = fmaf(v.y, exp2_approx(v.x - m), l);
             }
             inv = m == -INFINITY ? 0.0f : 1.0f / l;
+            if (TREE && walk.now.slot >= 0) inv = 1.0f;
 #pragma unroll
             for (int d = 0; d < C; d += 8) {
                 float v[8];
@@ -953,14 +1125,37 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             }
         }
         __syncwarp();
+        // TREE: sums of a row tile that other CTAs have a share of go to the workspace
+        float *piece = nullptr;
+        if (TREE && walk.now.slot >= 0) {
+            piece = a.pieces + ((size_t)blockIdx.x * 2 + walk.now.slot) * (kRows * (D + 2));
+            if (half == 0) reinterpret_cast<float2 *>(piece + kRows * D)[row] = ok ? make_float2(m, l) : make_float2(0.0f, inv);
+        }
+        if constexpr (MASKS) {
+            // a small loop, whose code is fetched sooner, and where a row goes worked out once
+            // by its lane (3 instead of 8 thousand cycles of a CTA)
+            const int rho = row0 + row, j = rho / R;
+            float *mine = TREE && piece ? piece + row * D
+                                        : a.out + (size_t)(rq.row0 + j) * a.ldo + (size_t)(h * R + rho - j * R) * D;
+            mine += half * C;
+            const int rows = rows_all - row0 - 32 * q4;    // of this warp that are there
+#pragma unroll 2
+            for (int n = 0; n < X; ++n) {
+                const int r = n * (32 / X) + lane / X, x = lane % X;
+                float *to = reinterpret_cast<float *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), r));
+                if (r >= rows || half * C + 4 * x >= D) continue;
+                *reinterpret_cast<float4 *>(to + 4 * x) = ok ? stage[r * X + (x ^ (r & 7))] : make_float4(inv, inv, inv, inv);
+            }
+        } else {
 #pragma unroll
-        for (int n = 0; n < X; ++n) {
-            const int r = n * (32 / X) + lane / X, x = lane % X;
-            const int rho = row0 + 32 * q4 + r, j = rho / R;
-            if (rho >= rows_all || half * C + 4 * x >= D) continue;
-            *reinterpret_cast<float4 *>(a.out + (size_t)(rq.row0 + j) * a.ldo + (size_t)(h * R + rho - j * R) * D +
-                                        half * C + 4 * x) =
-                ok ? stage[r * X + (x ^ (r & 7))] : make_float4(inv, inv, inv, inv);
+            for (int n = 0; n < X; ++n) {
+                const int r = n * (32 / X) + lane / X, x = lane % X;
+                const int rho = row0 + 32 * q4 + r, j = rho / R;
+                if (rho >= rows_all || half * C + 4 * x >= D) continue;
+                *reinterpret_cast<float4 *>(a.out + (size_t)(rq.row0 + j) * a.ldo + (size_t)(h * R + rho - j * R) * D +
+                                            half * C + 4 * x) =
+                    ok ? stage[r * X + (x ^ (r & 7))] : make_float4(inv, inv, inv, inv);
+            }
         }
     } else if (warp < W::kCopy) {
         // ===== the cache: codes, scales and zeros to the operands =====
@@ -1182,7 +1377,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             if (!EXACT && __any_sync(0xffffffffu, ones)) {   // rare
                 const int k0 = key_of_tile(i);
                 leave_equal_rows<G, MASKS>(smem_s + M::offRaw + 2 * M::kRawCodes + (uint32_t)rs * M::kRawSlot, see_lo - k0, see_hi - k0,
-                                    kept - k0, k0 + kTile - 1 <= all_hi && k0 >= all_lo, s_apart);
+                                    kept - k0, k0 + kTile - 1 <= all_hi && k0 >= all_lo, cta.apart);
             }
             if (lane == 0) mbar_arrive(&bar.raw_empty[rs]);
             // (numbers of one sign order as their bits do)
@@ -1200,7 +1395,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             if (k0 + kTile - 1 > all_hi || k0 < all_lo) {
                 // (a power of V is 2^-12 of its bound)
                 const float least = __uint_as_float(top) * (EXACT ? 0x1p-12f : 0x1p-24f);
-                if ((by[0] != 0.0f && fabsf(by[0]) < least) || (by[1] != 0.0f && fabsf(by[1]) < least)) s_uneven = 1;
+                if ((by[0] != 0.0f && fabsf(by[0]) < least) || (by[1] != 0.0f && fabsf(by[1]) < least)) cta.uneven = 1;
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.k_full[slot]);
@@ -1242,6 +1437,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         // every MMA done before tensor memory and shared memory go
         tc_commit(bar.drain);
         (void)mbar_wait(bar.drain, 0);
+        // (TREE: the barriers are made anew; nothing may still arrive at them)
+        if (TREE)
+            for (int i = max(n_tiles - W::kSlots, 0); i < n_tiles; ++i)
+                if (!bar_wait(&bar.k_empty[i % W::kSlots], (i / W::kSlots) & 1, abort)) break;
     } else if (lane == 0) {
         // ===== O = P V =====
         constexpr uint32_t id_o = idesc_f16_f32(kRows, DP, true);
@@ -1277,27 +1476,116 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         }
         tc_commit(bar.drain + 1);
         (void)mbar_wait(bar.drain + 1, 0);
-    }
-    __syncwarp();
-    tc_fence_before_sync();
-    __syncthreads();
-    tc_fence_after_sync();
-    if (warp == W::kMma) tmem_dealloc(tmem, kTmemCols);
-    // (the request is read again: in registers for so long it costs the roles)
-    if (threadIdx.x < kRows / 32) a.apart[blockIdx.x].rows[threadIdx.x] = s_apart[threadIdx.x];
-    if (threadIdx.x == kRows / 32) {
-        a.apart[blockIdx.x].request = s_req;
-        a.apart[blockIdx.x].tile = s_tile;
-        a.apart[blockIdx.x].uneven = s_uneven;
+        if (TREE) {
+            for (int i = max(n_tiles - W::kSlots, 0); i < n_tiles; ++i)
+                if (!bar_wait(&bar.v_empty[i % W::kSlots], (i / W::kSlots) & 1, abort)) break;
+            for (int i = max(n_tiles - kSP, 0); i < n_tiles; ++i)
+                if (!bar_wait(&bar.sp_empty[i % kSP], (i / kSP) & 1, abort)) break;
+        }
     }
 }
 
-template <int J, int G, int DP, bool MASKS>
+// A row tile's marks for the last kernel.  By the whole CTA.
+__device__ __forceinline__ void write_marks(ApartTile &to, int request, int tile)
+{
+    if (threadIdx.x < kRows / 32) to.rows[threadIdx.x] = cta.apart[threadIdx.x];
+    if (threadIdx.x == kRows / 32) {
+        to.request = request;
+        to.tile = tile;
+        to.uneven = cta.uneven;
+    }
+}
+
+// J: 32-value blocks of a row, G: scale groups per row, DP: padded head.
+template <int J, int G, int DP, int MODE>
+__global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_constant__ PromptParams p)
+{
+    constexpr bool EXACT = G == 1, MASKS = MODE != kCausal;
+    using W = Form<EXACT>;
+    using M = Mem<J, G, DP>;
+    const AttnCall &a = p.a;
+    const int warp = threadIdx.x >> 5;
+    const int H = a.c.kv_heads, R = a.heads / H;
+
+    // ---- this CTA's request and row tile: the last ones (most keys) first ----
+    const int h = (int)(blockIdx.x % (unsigned)H);
+    if constexpr (MODE == kTree) {
+        if (!walk_start<EXACT>(a)) return;
+    } else {
+        auto tiles_of = [&](int b) {
+            if (b >= a.B) return 0;
+            const AttnRequest r = attn_request<MASKS>(a, b);
+            return prompt_takes(a, r) ? (r.n * R + kRows - 1) / kRows : 0;
+        };
+        int all = 0, mine = 0, before = 0;
+        if (a.B == 1) all = mine = tiles_of(0);
+        else for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+            int t;
+            mine = tiles_of(b0 + (int)threadIdx.x);
+            before = scan_ints<kWarps>(mine, t, cta.sums);
+            all += t;
+        }
+        const int want = all - 1 - (int)(blockIdx.x / (unsigned)H);
+        if (want < 0) {   // uniform
+            if (threadIdx.x < kRows / 32) a.apart[blockIdx.x].rows[threadIdx.x] = 0;
+            if (threadIdx.x == kRows / 32) a.apart[blockIdx.x].uneven = 0;
+            return;
+        }
+        int base = 0;
+        for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+            int t = all;
+            if (a.B > kThreads) {
+                mine = tiles_of(b0 + (int)threadIdx.x);
+                before = scan_ints<kWarps>(mine, t, cta.sums);
+            }
+            if (want >= base + before && want < base + before + mine && (a.B > 1 || threadIdx.x == 0)) {
+                cta.req = b0 + (int)threadIdx.x;
+                cta.tile = want - (base + before);
+            }
+            base += t;
+            if (base > want) break;   // uniform
+        }
+    }
+    set_up<EXACT, false>(operands() + M::offBar);
+    if (warp == W::kMma) {
+        tmem_alloc(&cta.tmem, kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    auto met = [] {
+        __syncwarp();
+        tc_fence_before_sync();
+        __syncthreads();
+        tc_fence_after_sync();
+    };
+    if constexpr (MODE == kTree) {
+        for (;;) {
+            row_tile<J, G, DP, MODE>(a, walk.now.head);
+            met();
+            write_marks(a.apart[walk.now.entry], walk.now.req, walk.now.tile);
+            if (walk.more == 0 || cta.abort) break;   // uniform
+            __syncthreads();
+            if (threadIdx.x == 0) walk.now = walk.next;
+            set_up<EXACT, true>(operands() + M::offBar);
+            __syncthreads();
+        }
+    } else {
+        row_tile<J, G, DP, MODE>(a, h);
+        met();
+    }
+    if (warp == W::kMma) tmem_dealloc(cta.tmem, kTmemCols);
+    // (the request is read again: in registers for so long it costs the roles)
+    if constexpr (MODE != kTree) write_marks(a.apart[blockIdx.x], cta.req, cta.tile);
+}
+
+template <int J, int G, int DP, int MODE>
 cudaError_t launch_prompt_t(const AttnCall &call, cudaStream_t stream)
 {
-    auto kern = attn_prompt_kernel<J, G, DP, MASKS>;
+    auto kern = attn_prompt_kernel<J, G, DP, MODE>;
     constexpr int smem = Mem<J, G, DP>::kBytes;
-    static_assert(smem + 256 <= 227 * 1024, "shared memory (and the static part)");
+    static_assert(smem + sizeof(CtaShared) + (MODE == kTree ? sizeof(TreeShared) : 0) <= 227 * 1024, "shared memory (and the static part)");
     int dev = 0;
     cudaError_t err;
     if ((err = cudaGetDevice(&dev)) != cudaSuccess) return err;
@@ -1307,7 +1595,7 @@ cudaError_t launch_prompt_t(const AttnCall &call, cudaStream_t stream)
             return err;
         ready_dev.store(dev, std::memory_order_release);
     }
-    const long long grid = call.n_apart;
+    const long long grid = MODE == kTree ? call.tree_ctas : call.n_apart;
     if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
     PromptParams p{};
     p.a = call;
@@ -1315,18 +1603,18 @@ cudaError_t launch_prompt_t(const AttnCall &call, cudaStream_t stream)
     return cudaGetLastError();
 }
 
-template <bool MASKS>
+template <int MODE>
 cudaError_t launch_many_rows(const AttnCall &call, cudaStream_t stream)
 {
     const int G = call.c.head_dim / call.c.group_size;
     switch (call.c.head_dim * 16 + G) {
-    case 64 * 16 + 1: return launch_prompt_t<2, 1, 64, MASKS>(call, stream);
-    case 64 * 16 + 2: return launch_prompt_t<2, 2, 64, MASKS>(call, stream);
-    case 96 * 16 + 1: return launch_prompt_t<3, 1, 128, MASKS>(call, stream);
-    case 96 * 16 + 3: return launch_prompt_t<3, 3, 128, MASKS>(call, stream);
-    case 128 * 16 + 1: return launch_prompt_t<4, 1, 128, MASKS>(call, stream);
-    case 128 * 16 + 2: return launch_prompt_t<4, 2, 128, MASKS>(call, stream);
-    case 128 * 16 + 4: return launch_prompt_t<4, 4, 128, MASKS>(call, stream);
+    case 64 * 16 + 1: return launch_prompt_t<2, 1, 64, MODE>(call, stream);
+    case 64 * 16 + 2: return launch_prompt_t<2, 2, 64, MODE>(call, stream);
+    case 96 * 16 + 1: return launch_prompt_t<3, 1, 128, MODE>(call, stream);
+    case 96 * 16 + 3: return launch_prompt_t<3, 3, 128, MODE>(call, stream);
+    case 128 * 16 + 1: return launch_prompt_t<4, 1, 128, MODE>(call, stream);
+    case 128 * 16 + 2: return launch_prompt_t<4, 2, 128, MODE>(call, stream);
+    case 128 * 16 + 4: return launch_prompt_t<4, 4, 128, MODE>(call, stream);
     }
     return cudaErrorInvalidValue;
 }

@@ -1097,6 +1097,85 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
     }
 }
 
+// CTAs of the last kernel for each row tile that the prompt kernel's CTAs share.
+constexpr int kPieceParts = 16;
+
+// Joins the sums of row tiles that are cut, a part of the rows at a time, and
+// then computes those of them that are marked.
+template <int J, int G>
+__device__ __forceinline__ void join_pieces(const AttnCall &a, ApartShared<J> &s)
+{
+    constexpr int D = 32 * J, PER = kPromptTile / kPieceParts;
+    __shared__ ApartTile marks;
+    for (int x = blockIdx.x; x < a.tree_ctas * kPieceParts; x += gridDim.x) {
+        const int c = x / kPieceParts, lo = (x - c * kPieceParts) * PER;
+        const int4 u = __ldcg(a.cut + c);              // request, tile, kv head, last CTA
+        if (u.w < 0) continue;                         // uniform
+        const AttnRequest rq = attn_request<true>(a, u.x);
+        const int R = a.heads / a.c.kv_heads, hi = min(lo + PER, rq.n * R - u.y * kPromptTile);
+        auto piece_of = [&](int k) { return a.pieces + ((size_t)k * 2 + (k == c)) * (kPromptTile * (D + 2)); };
+        for (int i = threadIdx.x; i < (hi - lo) * (D / 4); i += kJoinThreads) {
+            const int row = lo + i / (D / 4), d = 4 * (i % (D / 4));
+            float m = -INFINITY, l = 0.0f;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            constexpr int kAhead = 4;                  // sums on their way at once
+            for (int k0 = c; k0 <= u.w; k0 += kAhead) {
+                float2 ml[kAhead];
+                float4 t[kAhead];
+                float mn = m;
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) {
+                    ml[k] = make_float2(-INFINITY, 0.0f);
+                    t[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (k0 + k <= u.w) {
+                        const float *from = piece_of(k0 + k);
+                        ml[k] = __ldcg(reinterpret_cast<const float2 *>(from + kPromptTile * D) + row);
+                        t[k] = __ldcg(reinterpret_cast<const float4 *>(from + row * D + d));
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) mn = fmaxf(mn, ml[k].x);
+                const float ref = mn == -INFINITY ? 0.0f : mn, fo = exp2_approx(m - ref);
+                l *= fo;
+                v.x *= fo;
+                v.y *= fo;
+                v.z *= fo;
+                v.w *= fo;
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) {
+                    const float f = exp2_approx(ml[k].x - ref);
+                    l = fmaf(f, ml[k].y, l);
+                    v.x = fmaf(f, t[k].x, v.x);
+                    v.y = fmaf(f, t[k].y, v.y);
+                    v.z = fmaf(f, t[k].z, v.z);
+                    v.w = fmaf(f, t[k].w, v.w);
+                }
+                m = mn;
+            }
+            const int rho = u.y * kPromptTile + row, j = rho / R;
+            const float inv = m == -INFINITY ? 0.0f : 1.0f / l;
+            *reinterpret_cast<float4 *>(a.out + (size_t)(rq.row0 + j) * a.ldo + (size_t)(u.z * R + rho - j * R) * D + d) =
+                make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+        }
+        if (threadIdx.x <= kPromptTile / 32) {         // a thread per word of marks, and one
+            uint32_t any = 0;
+            for (int k = c; k <= u.w; ++k) {
+                const ApartTile &from = a.apart[a.n_units + 2 * k + (k == c)];
+                any |= threadIdx.x < kPromptTile / 32 ? from.rows[threadIdx.x] : (uint32_t)from.uneven;
+            }
+            if (threadIdx.x < kPromptTile / 32) marks.rows[threadIdx.x] = any;
+            else {
+                marks.uneven = (int)any;
+                marks.request = u.x;
+                marks.tile = u.y;
+            }
+        }
+        __syncthreads();
+        if ((marks.rows[lo >> 5] | (uint32_t)marks.uneven) != 0) apart_rows<J, G, true>(a, marks, u.z, s, lo, lo + PER);
+        __syncthreads();
+    }
+}
+
 // Joins the partial sums of the units that were cut, one CTA for each CTA of
 // the first kernel.  J, G: also computes the rows that the prompt kernel left
 // (0: there are none).
@@ -1107,22 +1186,27 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
     if constexpr (J > 0) {
         // a thread looks at one tile in gridDim.x at a time
         __shared__ ApartShared<J> s;
-        for (long long n0 = blockIdx.x; n0 < p.a.n_apart; n0 += (long long)kJoinThreads * gridDim.x) {   // uniform
+        const long long n_apart = MASKS ? p.a.n_units : p.a.n_apart;   // (the others are join_pieces')
+        for (long long n0 = blockIdx.x; n0 < n_apart; n0 += (long long)kJoinThreads * gridDim.x) {   // uniform
             const long long n = n0 + (long long)threadIdx.x * gridDim.x;
             bool some = false;
-            if (n < p.a.n_apart) {
+            if (n < n_apart) {
                 const uint4 *at = reinterpret_cast<const uint4 *>(p.a.apart + n);
                 const uint4 rows = __ldcg(at), more = __ldcg(at + 1);
                 some = (rows.x | rows.y | rows.z | rows.w | more.z) != 0;
             }
             if (!__syncthreads_or(some)) continue;
-            for (int x = 0; x < kJoinThreads && n0 + (long long)x * gridDim.x < p.a.n_apart; ++x) {
+            for (int x = 0; x < kJoinThreads && n0 + (long long)x * gridDim.x < n_apart; ++x) {
                 const long long m = n0 + (long long)x * gridDim.x;
                 const ApartTile &at = p.a.apart[m];
                 if ((at.rows[0] | at.rows[1] | at.rows[2] | at.rows[3] | (uint32_t)at.uneven) != 0)
                     apart_rows<J, G, MASKS>(p.a, at, (int)(m % p.a.c.kv_heads), s);
             }
         }
+        if constexpr (MASKS) join_pieces<J, G>(p.a, s);
+    }
+    if constexpr (J > 0 && MASKS) {
+        if ((int)blockIdx.x >= p.grid) return;
     }
     const int4 u = __ldcg(p.desc + 2 * blockIdx.x), d = __ldcg(p.desc + 2 * blockIdx.x + 1);
     if (d.x < 0) return;
@@ -1237,6 +1321,7 @@ cudaError_t launch_split(const AttnCall &call, cudaStream_t stream)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    if (MASKS && call.tree_ctas * kPieceParts > grid) cfg.gridDim = dim3((unsigned)(call.tree_ctas * kPieceParts));
     if constexpr (J <= 4)
         if (call.n_apart > 0) return cudaLaunchKernelEx(&cfg, attn_join_kernel<4 * NB, J, G, MASKS>, p, (int)(32 * J));
     return cudaLaunchKernelEx(&cfg, attn_join_kernel<4 * NB, 0, 0, MASKS>, p, (int)(32 * J));

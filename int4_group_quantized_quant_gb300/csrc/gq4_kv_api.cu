@@ -90,7 +90,7 @@ gq4_status attention(int B, int T, int q_heads, int max_pages, int max_query, in
     if (!aligned(query_start, 4) || !aligned(seq_lens, 4) || !aligned(page_table, 4) ||
         !aligned(mask.tree, 4) || (mask.tree && mask.window > 0 && !aligned(mask.positions, 4)))
         return GQ4_ERR_MISALIGNED;
-    const size_t need = gq4::attn_workspace_bytes(T, q_heads, cache->kv_heads, cache->head_dim);
+    const size_t need = gq4::attn_workspace_bytes(T, q_heads, cache->kv_heads, cache->head_dim, mask.tree != nullptr);
     if (!workspace || workspace_bytes < need) return GQ4_ERR_INVALID_ARG;
     if (!aligned(workspace, 256)) return GQ4_ERR_MISALIGNED;
     const size_t width = (size_t)q_heads * cache->head_dim * 4;
@@ -431,7 +431,13 @@ gq4_status gq4_kv_accept(int B, int max_path, int max_pages, int n_free, const g
 size_t gq4_kv_attention_workspace_bytes(int T, int q_heads, int kv_heads, int head_dim)
 {
     if (T < 0 || q_heads < 1 || kv_heads < 1 || head_dim < 1) return 0;
-    return gq4::attn_workspace_bytes(T, q_heads, kv_heads, head_dim);
+    return gq4::attn_workspace_bytes(T, q_heads, kv_heads, head_dim, false);
+}
+
+size_t gq4_kv_attention_masked_workspace_bytes(int T, int q_heads, int kv_heads, int head_dim)
+{
+    if (T < 0 || q_heads < 1 || kv_heads < 1 || head_dim < 1) return 0;
+    return gq4::attn_workspace_bytes(T, q_heads, kv_heads, head_dim, true);
 }
 
 gq4_status gq4_kv_attention(int B, int T, int q_heads, int max_pages, int max_query, int max_len,

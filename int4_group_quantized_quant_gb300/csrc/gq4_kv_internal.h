@@ -84,8 +84,14 @@ struct AttnCall {
     int prompt_rows;   // requests of at least so many query rows per kv head go to the prompt kernel
     ApartTile *apart;  // in the workspace, one for each of the prompt kernel's CTAs
     long long n_apart;
+    // Trees: the prompt kernel's CTAs share the tiles (gq4_attn_prompt.cuh).  Marks 0 .. n_units - 1 are then the row
+    // tiles', behind them two for each CTA's sums of row tiles that are cut.
+    int tree_ctas;
+    long long n_units;
+    float *pieces;     // [tree_ctas][2][kPromptTile][D + 2] sums: the rows', then the maximum and the weights' sum of each
+    int4 *cut;         // [tree_ctas] the row tile that starts in the CTA and is cut: request, tile, kv head, last CTA or -1
 };
-size_t attn_workspace_bytes(int T, int heads, int kv_heads, int D);
+size_t attn_workspace_bytes(int T, int heads, int kv_heads, int D, bool masks);
 cudaError_t launch_attn(const AttnCall &call, cudaStream_t stream);
 cudaError_t read_attn_device_error(unsigned int *bits, bool clear);
 // Its kernel for requests with many query rows.
@@ -97,5 +103,7 @@ cudaError_t launch_attn_masked(const AttnCall &call, cudaStream_t stream);
 cudaError_t read_masked_device_error(unsigned int *bits, bool clear);
 cudaError_t launch_attn_prompt_masked(const AttnCall &call, cudaStream_t stream);
 cudaError_t read_prompt_masked_device_error(unsigned int *bits, bool clear);
+cudaError_t launch_attn_prompt_tree(const AttnCall &call, cudaStream_t stream);
+cudaError_t read_prompt_tree_device_error(unsigned int *bits, bool clear);
 
 }  // namespace gq4

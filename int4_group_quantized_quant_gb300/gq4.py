@@ -125,12 +125,15 @@ lib.gq4_gemm_workspace_bytes.restype = ctypes.c_size_t
 lib.gq4_gemm_workspace_bytes.argtypes = [_i, _i]
 lib.gq4_kv_attention_workspace_bytes.restype = ctypes.c_size_t
 lib.gq4_kv_attention_workspace_bytes.argtypes = [_i, _i, _i, _i]
+lib.gq4_kv_attention_masked_workspace_bytes.restype = ctypes.c_size_t
+lib.gq4_kv_attention_masked_workspace_bytes.argtypes = [_i, _i, _i, _i]
 lib.gq4_kv_accept_workspace_bytes.restype = ctypes.c_size_t
 lib.gq4_kv_accept_workspace_bytes.argtypes = [_i]
 
 EXPORTED = list(_SIGS) + ["gq4_status_string", "gq4_version", "gq4_device_error",
                           "gq4_sequence_workspace_bytes", "gq4_gemm_workspace_bytes",
-                          "gq4_kv_attention_workspace_bytes", "gq4_kv_accept_workspace_bytes"]
+                          "gq4_kv_attention_workspace_bytes", "gq4_kv_attention_masked_workspace_bytes",
+                          "gq4_kv_accept_workspace_bytes"]
 
 
 class GQ4Error(RuntimeError):
@@ -647,8 +650,9 @@ def kv_plan(past_lens, new_lens, page_table, free_pages, free_count, n_tokens, p
     return tuple(outs)
 
 
-def kv_attention_workspace_bytes(T, heads, kv_heads, head_dim) -> int:
-    return lib.gq4_kv_attention_workspace_bytes(T, heads, kv_heads, head_dim)
+def kv_attention_workspace_bytes(T, heads, kv_heads, head_dim, tree=False) -> int:
+    fn = lib.gq4_kv_attention_masked_workspace_bytes if tree else lib.gq4_kv_attention_workspace_bytes
+    return fn(T, heads, kv_heads, head_dim)
 
 
 def kv_attention(q, query_start, seq_lens, page_table, Kq, K_sz, Vq, V_sz, group_size, scale, max_query,
@@ -658,8 +662,8 @@ def kv_attention(q, query_start, seq_lens, page_table, Kq, K_sz, Vq, V_sz, group
     ``sinks``: first keys that the window does not hide.  ``tree`` int32 [T, words]: which of its
     request's new keys a row sees, bit i for new key i (kv_tree makes them; gq4_kv_attention_masked);
     with a window the rows' ``positions`` int32 [T] are needed too.
-    ``workspace``: a CUDA tensor of at least kv_attention_workspace_bytes(T, heads, kv_heads, D) bytes
-    (allocated when None).  ``out`` rows of no request are left as they were."""
+    ``workspace``: a CUDA tensor of at least kv_attention_workspace_bytes(T, heads, kv_heads, D, tree=...)
+    bytes (allocated when None).  ``out`` rows of no request are left as they were."""
     c, index = _cache(Kq, K_sz, Vq, V_sz, group_size)
     T, H, D, ldq = _rows(q, "q", index)
     if D != c.head_dim:
@@ -676,8 +680,8 @@ def kv_attention(q, query_start, seq_lens, page_table, Kq, K_sz, Vq, V_sz, group
     else:
         ldo = _rows(out, "out", index, (T, H, D))[3]
     if workspace is None:
-        workspace = torch.empty(lib.gq4_kv_attention_workspace_bytes(T, H, c.kv_heads, D), dtype=torch.uint8,
-                                device=q.device)
+        need = lib.gq4_kv_attention_workspace_bytes if tree is None else lib.gq4_kv_attention_masked_workspace_bytes
+        workspace = torch.empty(need(T, H, c.kv_heads, D), dtype=torch.uint8, device=q.device)
         made.append(workspace)
     elif not (isinstance(workspace, torch.Tensor) and workspace.get_device() == index and workspace.is_contiguous()):
         raise ValueError("workspace must be a contiguous CUDA tensor on the others' device")

@@ -23,9 +23,11 @@ def gq4():
 
 
 class Setup:
-    """Requests over a pool with scattered pages; slots that no row sees hold NaN, pages without a seen slot lead nowhere."""
+    """Requests over a pool with scattered pages; slots that no row sees hold NaN, pages without a seen slot lead nowhere.
+    room: the length that the call is bounded by, and its tables wide enough for (trees of many heads go to the kernel of
+    many rows by their rows times that)."""
 
-    def __init__(self, news, lens, H, KH, D, gs, page, window=0, sinks=0, words=0, bits=None, pad=3, seed=0):
+    def __init__(self, news, lens, H, KH, D, gs, page, window=0, sinks=0, words=0, bits=None, pad=3, seed=0, room=None):
         g = I.rng(2400, sum(news), sum(lens), H, KH, D, gs, page, window, sinks, words, seed)
         self.news, self.lens = news, np.asarray(lens, np.int32)
         self.window, self.sinks, self.gs, self.scale = window, sinks, gs, 1.0 / np.sqrt(D)
@@ -41,7 +43,8 @@ class Setup:
         pages = sum(per) + 3
         self.cache = R.Cache(g, pages, KH, page, D, gs)
         order = g.permutation(pages)
-        self.table = np.full((len(lens), max(max(per), 1) + 1), -5, np.int32)
+        self.room = room or (32768 if words and H >= 48 else int(max(lens)))
+        self.table = np.full((len(lens), max(max(per) + 1, self.room // page)), -5, np.int32)
         used = np.zeros((pages, page), bool)
         at = 0
         for b, n in enumerate(per):
@@ -67,7 +70,7 @@ class Setup:
         return [dev(self.starts), dev(self.lens), dev(self.table), *[dev(a) for a in self.cache.arrays()], self.gs]
 
     def opts(self, **kw):
-        o = dict(scale=self.scale, max_query=max(self.news), max_len=int(self.lens.max()), window=self.window,
+        o = dict(scale=self.scale, max_query=max(self.news), max_len=self.room, window=self.window,
                  sinks=self.sinks)
         if self.bits is not None:
             o["tree"] = dev(self.bits)
@@ -142,13 +145,13 @@ def test_trees(gq4, H, KH, D, gs, page, window, sinks):
     assert gq4.device_error() == 0
 
 
-@pytest.mark.parametrize("window,sinks", [(0, 0), (30, 4), (100, 70)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (900, 4), (1000, 70)])
 @pytest.mark.parametrize("H,KH,D,gs,page", MANY)
 def test_trees_of_many_rows(gq4, H, KH, D, gs, page, window, sinks):
     """For the kernel of many rows: words in use and to spare, trees over several tiles of rows and of keys."""
-    news, lens = [64, 33, 1, 100, 48], [64, 333, 65, 230, 47 + 128]
+    news, lens = [64, 33, 1, 100, 48], [64, 1333, 65, 1230, 47 + 128]
     s = Setup(news, lens, H, KH, D, gs, page, window, sinks, words=5)
-    assert s.T * H >= 5120
+    assert s.T * H * (window + sinks + 100 if window else s.room) >= 8 << 20
     s.check(s.run(gq4))
     assert gq4.device_error() == 0
 
@@ -158,6 +161,33 @@ def test_the_largest_trees(gq4, H, KH):
     s = Setup([256, 250], [256 + 19, 250 + 700], H, KH, 64, 32, 16, words=8)
     s.check(s.run(gq4))
     assert gq4.device_error() == 0
+
+
+@pytest.mark.parametrize("H,KH,D,gs", [(16, 2, 128, 128), (16, 2, 128, 64), (24, 2, 64, 32), (16, 1, 96, 96)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (700, 20)])
+def test_row_tiles_that_are_shared(gq4, H, KH, D, gs, window, sinks):
+    """Trees behind long pasts: row tiles cut over two and over many CTAs, whole ones between them, small requests of the
+    other kernel, and idle ones; lengths that are not those that the call is bounded by."""
+    for news, lens in (([40], [6000]), ([33, 0, 40, 1, 64, 50, 20, 64], [5000, 9, 41, 700, 2000, 333, 1500, 64]),
+                       ([64] * 20, [64 + 97 * i for i in range(20)])):
+        s = Setup(news, lens, H, KH, D, gs, 16, window, sinks, words=2, room=32768)
+        s.check(s.run(gq4))
+        assert gq4.device_error() == 0
+
+
+@pytest.mark.parametrize("gs", [128, 64])
+def test_shared_row_tiles_of_unlike_size(gq4, gs):
+    """Rows that their tile's pieces do not hold, in tiles that several CTAs share: each CTA sees a part of the keys."""
+    s = Setup([64, 64], [5000, 3001], 8, 1, 128, gs, 16, words=2, room=32768)
+    g = I.rng(2403)
+    sz = s.cache.sz[1]
+    sz[..., 0] *= np.exp2(g.uniform(-5, 5, sz.shape[:-1])).astype(np.float32)
+    s.q[:128:7] *= np.float32(2.0 ** -60)
+    big = 5000 - 64 + 3
+    s.cache.sz[1][s.table[0, big // 16], :, big % 16, :, 0] *= np.float32(2.0 ** 20)
+    s.check(s.run(gq4))
+    first = s.run(gq4)
+    assert np.array_equal(first, s.run(gq4)) and gq4.device_error() == 0
 
 
 @pytest.mark.parametrize("H,KH,D,gs,page", [SHAPES[0], SHAPES[1], SHAPES[5], MANY[1], MANY[4]])
@@ -302,7 +332,7 @@ def test_same_bits_again_and_in_a_graph(gq4, words, window, sinks):
     assert np.array_equal(first, s.run(gq4))
     args, q = s.dev(), dev(s.q)
     out = torch.full(s.q.shape, FILL, device="cuda")
-    ws = torch.empty(gq4.kv_attention_workspace_bytes(s.T, 128, 4, 128), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(gq4.kv_attention_workspace_bytes(s.T, 128, 4, 128, tree=True), dtype=torch.uint8, device="cuda")
     opts = s.opts(out=out, workspace=ws)
     side = torch.cuda.Stream()
     graphs = []
@@ -341,7 +371,7 @@ def test_strided_rows_and_workspace(gq4):
     wide = torch.full((s.T, H + 2 * KH, D), 9.0, device="cuda")
     wide[:, :H] = dev(s.q)
     out = torch.full((s.T, H + 1, D), FILL, device="cuda")
-    ws = torch.full((gq4.kv_attention_workspace_bytes(s.T, H, KH, D),), 255, dtype=torch.uint8, device="cuda")
+    ws = torch.full((gq4.kv_attention_workspace_bytes(s.T, H, KH, D, tree=True),), 255, dtype=torch.uint8, device="cuda")
     s.check(s.run(gq4, q=wide[:, :H], out=out[:, :H], workspace=ws))
     assert torch.all(out[:, H:] == FILL)
 

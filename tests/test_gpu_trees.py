@@ -387,7 +387,7 @@ def test_speculative_loop(gq4, window, sinks, graph):
     xin, parents = torch.zeros((T, H + 2 * KH, D), device="cuda"), torch.zeros(T, dtype=torch.int32, device="cuda")
     path, counts = torch.zeros((B, n), dtype=torch.int32, device="cuda"), torch.zeros(B, dtype=torch.int32, device="cuda")
     kept = {}
-    ws = torch.empty(gq4.kv_attention_workspace_bytes(T, H, KH, D), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(gq4.kv_attention_workspace_bytes(T, H, KH, D, tree=True), dtype=torch.uint8, device="cuda")
 
     def draft():
         _, st, _, slt, _ = gq4.kv_plan(lens, new, table, free, count, T, page, seq_lens=lens, free_count_out=count)

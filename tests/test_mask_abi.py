@@ -47,7 +47,7 @@ int main(void) {
 @no_gpu_only
 def test_attention_checks(gq4):
     lib, bad = gq4.lib, gq4.ERR_INVALID_ARG
-    need = gq4.kv_attention_workspace_bytes(4, 8, 2, 64)
+    need = gq4.kv_attention_workspace_bytes(4, 8, 2, 64, tree=True)
     c = cache(gq4)
 
     def attn(B=2, T=4, mq=2, q=None, table=None, scale=0.1, out=None, ws=None, wb=need, window=0, sinks=0, tree=addr(7),
