@@ -140,20 +140,37 @@ __device__ __forceinline__ float square_sum(float4 a)
     return (a.x * a.x + a.y * a.y) + (a.z * a.z + a.w * a.w);
 }
 
-// Values d .. d + 3 rotated (d < rot); b: their partners, half-split.  sc: the
-// token's sines and cosines.
-__device__ __forceinline__ float4 rotated(float4 a, float4 b, int d, int half, bool interleaved, const float2 *sc)
+// A token's rotation with the gain taken in: value d of a row becomes x_d A_d +
+// x_d' B_d, d' its partner, A_d = g_d cos and B_d = -+ g_d' sin.
+template <int J>
+struct alignas(16) Turn {
+    float A[32 * J], B[32 * J];
+};
+
+// Pair i of a token's table.  gain: NULL for ones.
+template <int J>
+__device__ __forceinline__ void make_turn(const RopeAppendParams &p, int pos, int i, const float *gain, Turn<J> &t)
 {
-    if (interleaved) {
-        const float4 s = *reinterpret_cast<const float4 *>(sc + (d >> 1));
-        return make_float4(a.x * s.y - a.y * s.x, a.y * s.y + a.x * s.x, a.z * s.w - a.w * s.z, a.w * s.w + a.z * s.z);
-    }
-    const bool first = d < half;
-    const float m = first ? -1.0f : 1.0f;
-    const float4 *s = reinterpret_cast<const float4 *>(sc + (first ? d : d - half));
-    const float4 s0 = s[0], s1 = s[1];
-    return make_float4(a.x * s0.y + m * b.x * s0.x, a.y * s0.w + m * b.y * s0.z, a.z * s1.y + m * b.z * s1.x,
-                       a.w * s1.w + m * b.w * s1.z);
+    const float2 sc = sin_cos_at(pos, __ldg(p.inv_freq + i));
+    const int a = p.interleaved ? 2 * i : i, b = p.interleaved ? 2 * i + 1 : i + (p.rot >> 1);
+    const float ga = gain ? __ldg(gain + a) : 1.0f, gb = gain ? __ldg(gain + b) : 1.0f;
+    t.A[a] = ga * sc.y;
+    t.B[a] = -gb * sc.x;
+    t.A[b] = gb * sc.y;
+    t.B[b] = ga * sc.x;
+}
+
+// Values d .. d + 3 rotated (d < rot); b: their partners.
+template <int J>
+__device__ __forceinline__ float4 rotated(float4 a, float4 b, int d, const Turn<J> &t)
+{
+    const float4 A = *reinterpret_cast<const float4 *>(t.A + d), B = *reinterpret_cast<const float4 *>(t.B + d);
+    return make_float4(a.x * A.x + b.x * B.x, a.y * A.y + b.y * B.y, a.z * A.z + b.z * B.z, a.w * A.w + b.w * B.w);
+}
+
+__device__ __forceinline__ float4 swapped(float4 a)
+{
+    return make_float4(a.y, a.x, a.w, a.z);
 }
 
 // ---------------------------------------------------------------------------
@@ -162,7 +179,7 @@ __device__ __forceinline__ float4 rotated(float4 a, float4 b, int d, int half, b
 
 // LPR lanes hold a row, CH float4s each; two rows of a warp under way.
 template <int J>
-__device__ __forceinline__ void query_rows(const RopeAppendParams &p, int t, int part, const float2 *sc)
+__device__ __forceinline__ void query_rows(const RopeAppendParams &p, int t, int part, const Turn<J> &turn)
 {
     constexpr int D4 = 8 * J, LPR = J == 2 ? 16 : 32, CH = J == 8 ? 2 : 1, RPW = 32 / LPR, AHEAD = CH == 1 ? 2 : 1;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane & (LPR - 1);
@@ -183,7 +200,7 @@ __device__ __forceinline__ void query_rows(const RopeAppendParams &p, int t, int
                 x[u][j] = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (first + u * step < p.q_heads && l + 32 * j < D4) x[u][j] = from[(first + u * step) * D4 + l + 32 * j];
             }
-        if (!waited) __syncthreads();      // the sines
+        if (!waited) __syncthreads();      // the rotation
         waited = true;
 #pragma unroll
         for (int u = 0; u < AHEAD; ++u) {
@@ -196,15 +213,12 @@ __device__ __forceinline__ void query_rows(const RopeAppendParams &p, int t, int
 #pragma unroll
                 for (int o = LPR >> 1; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
                 r = inv_sqrt(fmaf(s, p.inv_d, p.eps));
-#pragma unroll
-                for (int j = 0; j < CH; ++j)
-                    if (l + 32 * j < D4) x[u][j] = times(x[u][j], __ldg(gain + l + 32 * j));
             }
             float4 y[CH];
 #pragma unroll
             for (int j = 0; j < CH; ++j) {
                 const int i = l + 32 * j, other = i < half4 ? i + half4 : i - half4;
-                float4 b = x[u][j];
+                float4 b = swapped(x[u][j]);
                 if (!p.interleaved) {      // (the whole warp shuffles)
                     b.x = __shfl_sync(0xffffffffu, x[u][0].x, other, LPR);
                     b.y = __shfl_sync(0xffffffffu, x[u][0].y, other, LPR);
@@ -217,7 +231,9 @@ __device__ __forceinline__ void query_rows(const RopeAppendParams &p, int t, int
                         if (other >> 5 == n) b = c;
                     }
                 }
-                y[j] = i < rot4 ? rotated(x[u][j], b, 4 * i, p.rot >> 1, p.interleaved, sc) : x[u][j];
+                y[j] = x[u][j];
+                if (i < rot4) y[j] = rotated(y[j], b, 4 * i, turn);
+                else if (gain && i < D4) y[j] = times(y[j], __ldg(gain + i));
             }
             __syncwarp();   // in place: every lane of the row has read before any writes
 #pragma unroll
@@ -438,7 +454,7 @@ __device__ __noinline__ void exact_unit(const RopeAppendParams &p, int t, int un
 }
 
 template <int J, int L>
-__device__ __forceinline__ void kv_rows(const RopeAppendParams &p, int t0, int part, const float2 *sc, ExactShared *exact)
+__device__ __forceinline__ void kv_rows(const RopeAppendParams &p, int t0, int part, const Turn<J> *turns, ExactShared *exact)
 {
     constexpr int WPR = 4 * J;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -465,24 +481,17 @@ __device__ __forceinline__ void kv_rows(const RopeAppendParams &p, int t0, int p
                 if (!value && !p.interleaved && d < p.rot) b[f] = *reinterpret_cast<const float4 *>(row.at + partner_of(d, half));
             }
         }
-        if (!waited) __syncthreads();      // the sines
+        if (!waited) __syncthreads();      // the rotation
         waited = true;
         if (slot < 0) continue;            // uniform in the warp
         if (!value) {
             float r = 1.0f;
-            if (p.k_gain) {
-                r = inv_sqrt(fmaf(row_sum<WPR>(square_sum(a[0]) + square_sum(a[1]), w, lane), p.inv_d, p.eps));
-#pragma unroll
-                for (int f = 0; f < 2; ++f) {
-                    const int d = 8 * w + 4 * f;
-                    a[f] = times(a[f], __ldg(reinterpret_cast<const float4 *>(p.k_gain + d)));
-                    if (!p.interleaved && d < p.rot) b[f] = times(b[f], __ldg(reinterpret_cast<const float4 *>(p.k_gain + partner_of(d, half))));
-                }
-            }
+            if (p.k_gain) r = inv_sqrt(fmaf(row_sum<WPR>(square_sum(a[0]) + square_sum(a[1]), w, lane), p.inv_d, p.eps));
 #pragma unroll
             for (int f = 0; f < 2; ++f) {
                 const int d = 8 * w + 4 * f;
-                if (d < p.rot) a[f] = rotated(a[f], b[f], d, half, p.interleaved, sc + n * 16 * J);
+                if (d < p.rot) a[f] = rotated(a[f], p.interleaved ? swapped(a[f]) : b[f], d, turns[n]);
+                else if (p.k_gain) a[f] = times(a[f], __ldg(reinterpret_cast<const float4 *>(p.k_gain + d)));
                 if (p.k_gain) a[f] = times(a[f], make_float4(r, r, r, r));
             }
         }
@@ -509,9 +518,9 @@ __device__ __forceinline__ void kv_rows(const RopeAppendParams &p, int t0, int p
 
 // J = head_dim / 32; L: lanes per group.
 template <int J, int L>
-__global__ void __launch_bounds__(kRopeAppendThreads, 7) rope_append_kernel(const __grid_constant__ RopeAppendParams p)
+__global__ void __launch_bounds__(kRopeAppendThreads, 8) rope_append_kernel(const __grid_constant__ RopeAppendParams p)
 {
-    __shared__ alignas(16) float2 sc[kRopeTokens * 16 * J];
+    __shared__ Turn<J> turns[kRopeTokens];
     __shared__ alignas(16) ExactShared exact[kRopeAppendWarps];
     const int turn = blockIdx.x / (p.turn + 1), place = blockIdx.x - turn * (p.turn + 1);
     const bool kv = place == 0;
@@ -519,14 +528,14 @@ __global__ void __launch_bounds__(kRopeAppendThreads, 7) rope_append_kernel(cons
     if (cta >= (kv ? p.kv_ctas : p.q_ctas)) return;
     const int parts = kv ? p.kv_parts : p.q_parts, per = kv ? p.kv_tokens : 1;
     const int item = parts == 1 ? cta : cta / parts, t0 = item * per, part = cta - item * parts;
-    // the tokens' sines and cosines
+    // the tokens' rotations
     const int half = p.rot >> 1, tokens = min(per, p.T - t0);
     for (int i = threadIdx.x; i < tokens * half; i += kRopeAppendThreads) {
-        const int n = i >= half, x = i - n * half;
-        sc[n * 16 * J + x] = sin_cos_at(__ldg(p.positions + t0 + n), __ldg(p.inv_freq + x));
+        const int n = i >= half;
+        make_turn<J>(p, __ldg(p.positions + t0 + n), i - n * half, kv ? p.k_gain : p.q_gain, turns[n]);
     }
-    if (kv) kv_rows<J, L>(p, t0, part, sc, exact);
-    else query_rows<J>(p, t0, part, sc);
+    if (kv) kv_rows<J, L>(p, t0, part, turns, exact);
+    else query_rows<J>(p, t0, part, turns[0]);
 }
 
 }  // namespace
