@@ -642,8 +642,8 @@ GQ4_API gq4_status gq4_kv_tree(int B, int T, int tree_words, int window, int sin
  * passes max_pages * page_size, counts[b] is not in 0 .. min(n, max_path), the
  * path does not rise or leaves 0 .. n - 1, or a page of its new tokens is outside
  * the pool.  Pages for which the list has no room (n_free) are lost, and bit 11
- * is set; free_count is cut to 0 .. n_free.  Rows shared with other requests
- * (one page in two tables) move for both.
+ * is set; free_count is cut to 0 .. n_free.  No two requests of a call may have
+ * new tokens in the same page.
  *
  * workspace: gq4_kv_accept_workspace_bytes(B) bytes of device memory, 256-byte
  * aligned, as in gq4_kv_attention. */

@@ -640,7 +640,7 @@ struct Segment {
     int req, tile, head;
     int from, upto;                        // of the row tile's tiles
     int slot;                              // of its sums in the workspace, -1: the row tile is the CTA's alone
-    long long entry;                       // of its marks
+    long long entry;                       // of its marks, -1: none
 };
 
 // What a CTA's threads share beside the operands.
@@ -809,12 +809,13 @@ __device__ __noinline__ void walk_on(const AttnCall &a)
         s.from = from;
         s.upto = upto - kStart;
         s.slot = first && last ? -1 : first ? 1 : 0;
-        s.entry = first && last ? walk.unit_at : a.n_units + 2ll * blockIdx.x + s.slot;
+        // (requests that share rows, between which one ends before it starts, may be more units than marks)
+        s.entry = !(first && last) ? a.n_units + 2ll * blockIdx.x + s.slot : walk.unit_at < a.n_units ? walk.unit_at : -1;
         if (first && !last) {
             // it goes on in the CTAs up to the one that holds its last tile
             const int until = (int)quotient_of(walk.pos - off + w.length - 1, walk.share);
             a.cut[blockIdx.x] = make_int4(s.req, s.tile, s.head, until);
-            no_marks(a.apart[walk.unit_at]);
+            if (walk.unit_at < a.n_units) no_marks(a.apart[walk.unit_at]);
         }
         walk.more = 1;
     }
@@ -1564,7 +1565,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         for (;;) {
             row_tile<J, G, DP, MODE>(a, walk.now.head);
             met();
-            write_marks(a.apart[walk.now.entry], walk.now.req, walk.now.tile);
+            if (walk.now.entry >= 0) write_marks(a.apart[walk.now.entry], walk.now.req, walk.now.tile);
             if (walk.more == 0 || cta.abort) break;   // uniform
             __syncthreads();
             if (threadIdx.x == 0) walk.now = walk.next;

@@ -1110,9 +1110,12 @@ __device__ __forceinline__ void join_pieces(const AttnCall &a, ApartShared<J> &s
     for (int x = blockIdx.x; x < a.tree_ctas * kPieceParts; x += gridDim.x) {
         const int c = x / kPieceParts, lo = (x - c * kPieceParts) * PER;
         const int4 u = __ldcg(a.cut + c);              // request, tile, kv head, last CTA
-        if (u.w < 0) continue;                         // uniform
+        // (uniform; what another call wrote over must not lead out of bounds)
+        if (u.w < c || u.w >= a.tree_ctas || (uint32_t)u.x >= (uint32_t)a.B || (uint32_t)u.z >= (uint32_t)a.c.kv_heads) continue;
         const AttnRequest rq = attn_request<true>(a, u.x);
-        const int R = a.heads / a.c.kv_heads, hi = min(lo + PER, rq.n * R - u.y * kPromptTile);
+        const int R = a.heads / a.c.kv_heads;
+        if (rq.bad || (uint32_t)u.y >= (uint32_t)((rq.n * R + kPromptTile - 1) / kPromptTile)) continue;
+        const int hi = min(lo + PER, rq.n * R - u.y * kPromptTile);
         auto piece_of = [&](int k) { return a.pieces + ((size_t)k * 2 + (k == c)) * (kPromptTile * (D + 2)); };
         for (int i = threadIdx.x; i < (hi - lo) * (D / 4); i += kJoinThreads) {
             const int row = lo + i / (D / 4), d = 4 * (i % (D / 4));

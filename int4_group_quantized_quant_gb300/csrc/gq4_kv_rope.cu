@@ -420,9 +420,11 @@ __device__ __noinline__ void exact_unit(const RopeAppendParams &p, int t, int un
             }
         }
         sum = fma(row_sum<WPR>(sum, w, lane), 1.0 / D, (double)p.eps);
-        r = inv_sqrt((float)sum);          // and two Newton steps
-        r = fma(fma(-0.5 * sum * r, r, 0.5), r, r);
-        r = fma(fma(-0.5 * sum * r, r, 0.5), r, r);
+        r = inv_sqrt((float)sum);
+        if (r > 0.0 && r < 1e30) {         // and two Newton steps
+            r = fma(fma(-0.5 * sum * r, r, 0.5), r, r);
+            r = fma(fma(-0.5 * sum * r, r, 0.5), r, r);
+        }
     }
     __syncwarp();
     const int half = p.rot >> 1, pos = p.rot > 0 ? __ldg(p.positions + t) : 0;

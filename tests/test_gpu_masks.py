@@ -224,6 +224,56 @@ def test_a_line_is_the_causal_rule(gq4, H, KH):
     assert np.all(np.abs(got[:live].astype(np.float64) - want[:live]) <= 2 * tol[:live])
 
 
+def test_sinks_without_a_window_hide_nothing(gq4):
+    s = Setup([1, 30], [700, 90], 8, 2, 128, 64, 16)
+    want = s.run(gq4)
+    s.sinks = 7
+    assert np.array_equal(s.run(gq4), want)
+
+
+@pytest.mark.parametrize("gs", [64, 32])
+def test_trees_of_more_requests_than_a_block_has_threads(gq4, gs):
+    """900 requests for the kernel of many rows: trees of one to three nodes of 64 heads, idle ones among them."""
+    g = I.rng(2404, gs)
+    news = g.integers(0, 4, 900).tolist()
+    lens = [n + int(x) for n, x in zip(news, g.integers(0, 60, 900))]
+    lens[450] += 3000
+    s = Setup(news, lens, 64, 1, 64, gs, 16, words=1)
+    s.check(s.run(gq4))
+    assert gq4.device_error() == 0
+
+
+@pytest.mark.parametrize("gs", [128, 64])
+def test_non_finite_queries_in_shared_row_tiles(gq4, gs):
+    """A NaN or infinite query spoils its own row, in tiles that several CTAs share."""
+    s = Setup([60], [7000], 16, 2, 128, gs, 16, words=2, room=32768)
+    clean = s.run(gq4)
+    s.check(clean)
+    q = s.q.copy()
+    q[3, 5, 7], q[40, 0, 100] = np.nan, np.inf
+    got = s.run(gq4, q=dev(q))
+    bad = np.zeros(got.shape[:2], bool)
+    bad[3, 5] = bad[40, 0] = True
+    assert np.isnan(got[bad]).all() and np.array_equal(got[~bad], clean[~bad])
+    assert gq4.device_error() == 0
+
+
+def test_requests_that_share_rows_stay_in_bounds(gq4):
+    """Requests over the same rows, between which one ends before it starts: more units than the call counts on."""
+    s = Setup([64], [400], 64, 1, 64, 64, 16, words=2, pad=0)
+    B = 301
+    args = s.dev()
+    args[0] = dev(np.array([0, 64] * (B // 2) + [0, 64], np.int32))
+    args[1] = dev(np.full(B, 400, np.int32))
+    args[2] = dev(np.repeat(s.table, B, 0))
+    size = gq4.kv_attention_workspace_bytes(64, 64, 1, 64, tree=True)
+    ws = torch.zeros(size + (1 << 20), dtype=torch.uint8, device="cuda")
+    got = s.run(gq4, args=args, workspace=ws[:size])
+    assert gq4.device_error(clear=True) == 1 << 8        # those that end before they start
+    s.check(got)        # (how keys are split goes by the other requests: not to the bit)
+    assert not ws[size:].any()
+
+
 @pytest.mark.parametrize("H", [4, 64])
 def test_queries_that_see_nothing(gq4, H):
     """seq_len < n with sinks and with bits; length 0."""
