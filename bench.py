@@ -910,7 +910,11 @@ CACHE_CASES = {"rope": "norm and rotation of 8192 tokens, 40 heads of 128",
                "append": "cache writer, 16384 tokens, 8 heads of 128",
                "gather": "cache reader, 16384 tokens, 8 heads of 128",
                "attention": "decode attention, 48 requests of 501 to 8162 keys, 32 heads over 8 of 128",
-               "prompt": "prompt attention, 4096 tokens, 32 heads over 8 of 128"}
+               "prompt": "prompt attention, 4096 tokens, 32 heads over 8 of 128",
+               "rope_append": "rotation and append in one pass, 16384 tokens, 32 + 8 heads of 128",
+               "tree": "attention of drafted trees, 32 requests of 26 nodes behind 500 to 4003 keys, 32 heads over 8 of 128",
+               "sinks": "decode attention behind a window of 4096 and 4 first tokens, 64 requests of 501 to 60035 keys, "
+                        "32 heads over 8 of 128"}
 
 
 class CacheStep:
@@ -920,7 +924,7 @@ class CacheStep:
 
     HEADS, KV_HEADS, DIM, PAGE = 32, 8, 128, 16
 
-    def __init__(self, gq4, past, new, gs=GS, seed=1700):
+    def __init__(self, gq4, past, new, gs=GS, seed=1700, window=0, sinks=0, tree=False):
         import torch
         self.gq4, self.gs, self.new = gq4, gs, new
         g = torch.Generator(device="cuda").manual_seed(seed)
@@ -956,14 +960,24 @@ class CacheStep:
         self.v = torch.randn((T, KH, D), generator=g, **dev)
         self.q_out, self.k_out, self.v_out = (torch.empty_like(x) for x in (self.q, self.k, self.v))
         self.out = torch.empty_like(self.q)
-        self.ws = torch.empty(gq4.kv_attention_workspace_bytes(T, self.HEADS, KH, D), dtype=torch.uint8, **dev)
+        self.ws = torch.empty(gq4.kv_attention_workspace_bytes(T, self.HEADS, KH, D, tree=tree), dtype=torch.uint8, **dev)
+        self.masks = {}
+        if window:
+            self.masks = {"window": window, "sinks": sinks}
+        if tree:                # binary trees
+            parents = ((torch.arange(new) - 1) // 2).repeat(B).to(torch.int32).cuda()
+            self.positions, bits = gq4.kv_tree(parents, self.starts, self.seq_lens, -(-new // 32))
+            self.masks["tree"] = bits
         row = KH * (D // 2 + 8 * D // gs)                      # bytes of a token's keys, or values
         self.bytes = {
             "rope": 2 * 4 * T * (self.HEADS + KH) * D,
             "append": 2 * T * (4 * KH * D + row),
             "gather": 2 * T * (4 * KH * D + row),
             "attention": 2 * row * sum(p + new for p in past) + 2 * 4 * T * self.HEADS * D,
+            "rope_append": T * (8 * self.HEADS * D + 8 * KH * D + 2 * row),
         }
+        self.bytes["tree"] = self.bytes["attention"]
+        self.bytes["sinks"] = 2 * row * sum(min(p + new, window + sinks) for p in past) + 2 * 4 * T * self.HEADS * D
         seen = sum(p * new + new * (new + 1) // 2 for p in past)
         self.flops = 4 * D * self.HEADS * seen
 
@@ -980,7 +994,11 @@ class CacheStep:
     def attention(self, s):
         self.gq4.kv_attention(self.q, self.starts, self.seq_lens, self.table, *self.cache, self.gs,
                               self.DIM ** -0.5, self.new, max_len=self.most, out=self.out, workspace=self.ws,
-                              stream=s)
+                              stream=s, **self.masks)
+
+    def rope_append(self, s):
+        self.gq4.kv_rope_append(self.q, self.k, self.v, self.positions, self.inv_freq, self.slots, *self.cache, self.gs,
+                                q_gain=self.gain, k_gain=self.gain, q_out=self.q_out, stream=s)
 
 
 def cache_steps(gq4):
@@ -988,8 +1006,11 @@ def cache_steps(gq4):
     decode = CacheStep(gq4, [500 + 163 * b for b in range(48)], 1)
     prompt = CacheStep(gq4, [0], 4096)
     rows, more = CacheStep(gq4, [0], 8192), CacheStep(gq4, [0], 16384)
+    trees = CacheStep(gq4, [500 + 113 * b for b in range(32)], 26, tree=True)
+    sinks = CacheStep(gq4, [500 + 945 * b for b in range(64)], 1, window=4096, sinks=4)
     return {"rope": (rows, rows.rope), "append": (more, more.append), "gather": (more, more.gather),
-            "attention": (decode, decode.attention), "prompt": (prompt, prompt.attention)}
+            "attention": (decode, decode.attention), "prompt": (prompt, prompt.attention),
+            "rope_append": (more, more.rope_append), "tree": (trees, trees.attention), "sinks": (sinks, sinks.attention)}
 
 
 def run_profile_case(args):
@@ -1051,7 +1072,8 @@ def run_extras(args):
     rotating weight sets larger than 4x L2, against the plain matvec), the
     prefill GEMM (512 and 2048 rows through 4096 x 4096, against the bf16
     peak), the calls between the QKV product and the output projection
-    (rotation, cache writer and reader, attention), the quantizer and the MLX converter (4096 x 11008) and the
+    (rotation, cache writer and reader, attention, the two first in one pass, attention of
+    drafted trees and behind a window with first tokens), the quantizer and the MLX converter (4096 x 11008) and the
     embedding gather (8192 ids from a 32000 x 4096 table)."""
     import torch
     from int4_group_quantized_quant_gb300 import build as b

@@ -547,6 +547,15 @@ def _cache(Kq, K_sz, Vq, V_sz, group_size):
     index, dtype = _device(Kq, "Kq"), Kq.dtype
     if Kq.dim() != 4:
         raise ValueError("Kq must be [n_pages, kv_heads, page_size, head_dim/8]")
+    if dtype is _i32 and group_size > 0 and type(K_sz) is type(Vq) is type(V_sz) is type(Kq):
+        # the checks below in one expression, for the common case
+        shape = P, H, S, W = Kq.shape
+        sz = (P, H, S, 8 * W // group_size, 2)
+        if (8 * W % group_size == 0 and Vq.shape == shape and K_sz.shape == sz and V_sz.shape == sz
+                and Vq.dtype is _i32 and K_sz.dtype is _f32 and V_sz.dtype is _f32
+                and K_sz.get_device() == index and Vq.get_device() == index and V_sz.get_device() == index
+                and Kq.is_contiguous() and K_sz.is_contiguous() and Vq.is_contiguous() and V_sz.is_contiguous()):
+            return KVCache(P, S, H, 8 * W, group_size, Kq.data_ptr(), K_sz.data_ptr(), Vq.data_ptr(), V_sz.data_ptr()), index
     if dtype is not _i32:
         _need(Kq, "Kq", _WORDS)
     shape = P, H, S, W = Kq.shape
@@ -759,22 +768,26 @@ def kv_accept(path, counts, query_start, seq_lens, page_table, free_pages, free_
             raise ValueError("path has no columns")
     need = lib.gq4_kv_accept_workspace_bytes(B)
     # what is not given is a stretch of one allocation, the workspace first
-    spare = torch.empty(need // 4 + B + 1, dtype=_i32, device=Kq.device)
-    if workspace is None:
-        at_work, work = spare.data_ptr(), need
-    elif not (isinstance(workspace, torch.Tensor) and workspace.get_device() == index and workspace.is_contiguous()):
-        raise ValueError("workspace must be a contiguous CUDA tensor on the others' device")
-    else:
+    at_len_out = None if seq_lens_out is None else _at(seq_lens_out, "seq_lens_out", _i32, (B,), index)
+    at_count_out = None if free_count_out is None else _at(free_count_out, "free_count_out", _i32, (1,), index)
+    if workspace is None or at_len_out is None or at_count_out is None:
+        _, lens, count = parts = torch.empty(need // 4 + B + 1, dtype=_i32, device=Kq.device).split_with_sizes(
+            [need // 4, B, 1])
+        at = parts[0].data_ptr()
+        if workspace is None:
+            at_work, work = at, need
+        if at_len_out is None:
+            seq_lens_out, at_len_out = lens, at + need
+        if at_count_out is None:
+            free_count_out, at_count_out = count, at + need + 4 * B
+        if stream is not None:
+            _lend(stream, index, parts[0])
+    if workspace is not None:
+        if not (isinstance(workspace, torch.Tensor) and workspace.get_device() == index and workspace.is_contiguous()):
+            raise ValueError("workspace must be a contiguous CUDA tensor on the others' device")
         at_work, work = workspace.data_ptr(), workspace.nbytes
-    if seq_lens_out is None:
-        seq_lens_out = spare[need // 4:need // 4 + B]
-    if free_count_out is None:
-        free_count_out = spare[need // 4 + B:]
-    if stream is not None:
-        _lend(stream, index, spare)
     _call(lib.gq4_kv_accept, "gq4_kv_accept", index, stream, B, most, width, n_free, c, at_path, at_counts, at_start,
-          at_lens, at_table, at_free, at_count, _at(free_count_out, "free_count_out", _i32, (1,), index),
-          _at(seq_lens_out, "seq_lens_out", _i32, (B,), index), at_work, work)
+          at_lens, at_table, at_free, at_count, at_count_out, at_len_out, at_work, work)
     return seq_lens_out, free_count_out
 
 
