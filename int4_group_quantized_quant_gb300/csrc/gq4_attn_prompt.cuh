@@ -39,7 +39,7 @@
 // Measured in a graph, 32 heads over 8 of 128: a prompt of 6007 tokens, one
 // group, 664 us (296 GFLOP by the formula, 446 TFLOP/s; twice that in the MMAs,
 // 0.46 of the measured bf16 peak); three chunks of 1021 tokens behind 1000 to
-// 4096 with a window of 2048, four groups, 459 us (103 GFLOP, 224 TFLOP/s;
+// 4096 with a window of 2048, four groups, 445 us (103 GFLOP, 231 TFLOP/s;
 // three times that in the MMAs).  Bound by the latency and issue slots of the softmax, adding and
 // dequantising warps (issue active in half of the cycles, the tensor pipe in a
 // third): a tile takes 2150 cycles, its MMAs 1080; and a CTA starts and ends in
@@ -50,7 +50,11 @@
 // MASKS: the form with first tokens that stay visible behind a window, and
 // with ancestor bits of drafted trees (gq4_attn.cuh says what a row sees): the
 // tiles between the first tokens and the window are left out, and a tile where
-// not every row sees every key is masked by 64 bits per row.
+// not every row sees every key is masked by 64 bits per row.  The same three
+// chunks behind 1000 to 16000 with 64 first tokens: 473 us.  Trees: the CTAs
+// stay and share all tiles (see kUnitStart); 32 of 26 nodes behind 500 to 4096
+// keys, one group, 138 us (29 GFLOP; a tile takes 2400 cycles, a row tile's
+// start and end 17 thousand), 4 of 64 behind 8000 to 16000, two groups, 188.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -1185,6 +1189,17 @@ __device__ __forceinline__ void row_tile(const AttnCall &a, int h)
                                 : __byte_perm(vw[1], vw[2], 0x7610);
         };
         const uint32_t bad_at = smem_s + M::offBad;
+        // Several groups: the blocks of 32 values in small loops, a word at a time.  Instructions that
+        // are fetched anew hold up all roles: the trees above 205 -> 188 us (unrolled by 2: 195), the
+        // chunks 494 -> 473 (by 1: 488).  (One group, whose blocks are short: 5 to 10 % slower that way.)
+        constexpr int kBlocks = UG == 1 ? 2 : 1;
+        auto scale_of = [](const float2 (&z)[G], int u) {
+            float2 x = z[0];
+#pragma unroll
+            for (int g = 1; g < G; ++g)
+                if (u / UG == g) x = z[g];
+            return x;
+        };
         int s = 0, phase = 1;              // slot of K and V, parity of the phase before
         for (int i = 0; i < n_tiles; ++i) {
             const int rs = i % W::kRaw;
@@ -1197,10 +1212,10 @@ __device__ __forceinline__ void row_tile(const AttnCall &a, int h)
             // ---- K ----
 #pragma unroll
             for (int y = 0; y < TN; ++y) {
-                uint32_t kw[J];
-                lds_words<J>(raw_w + raw + y * kStep * 16 * J, kw);
                 const uint32_t base = smem_s + M::offK + s * M::kSlot;
                 if constexpr (EXACT) {
+                    uint32_t kw[J];
+                    lds_words<J>(raw_w + raw + y * kStep * 16 * J, kw);
 #pragma unroll
                     for (int u = 0; u < J; ++u) {
                         const uint4 e = exact_word(kw[u]);
@@ -1211,10 +1226,12 @@ __device__ __forceinline__ void row_tile(const AttnCall &a, int h)
                     const KeyOf<G> k = key_of<G, MASKS>(see_lo, see_hi, kept, key_of_tile(i) + key0 + kStep * y,
                                                  raw_z + raw + y * kStep * 8 * G, bad_at + rs * 16 + ((key0 + kStep * y) >> 4) * 4, ks);
                     const float up = pow2(k.exponent());
-#pragma unroll
+#pragma unroll kBlocks
                     for (int u = 0; u < J; ++u) {
-                        uint32_t hi[4], lo[4];
-                        dequant_word(kw[u], ks[u / UG].x * up, ks[u / UG].y, hi, lo);
+                        uint32_t hi[4], lo[4], word;
+                        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(word) : "r"(raw_w + raw + y * kStep * 16 * J + 4 * u) : "memory");
+                        const float2 z = scale_of(ks, u);
+                        dequant_word(word, z.x * up, z.y, hi, lo);
                         const uint32_t at = place(base, u, y);
                         store16(at, hi[0], hi[1], hi[2], hi[3]);
                         store16(at + M::kKV, lo[0], lo[1], lo[2], lo[3]);
@@ -1232,30 +1249,36 @@ __device__ __forceinline__ void row_tile(const AttnCall &a, int h)
 #pragma unroll
             for (int y = 0; y < TN; ++y) {
                 const uint32_t base = smem_s + M::offV + s * M::kSlot;
-                uint32_t vw[J];
-                lds_words<J>(raw_w + raw + y * kStep * 16 * J + M::kRawCodes, vw);
-                float2 vs[G];
-                float up = 0.0f;
-                if constexpr (!EXACT) {
+                if constexpr (EXACT) {
+                    uint32_t vw[J];
+                    lds_words<J>(raw_w + raw + y * kStep * 16 * J + M::kRawCodes, vw);
+#pragma unroll
+                    for (int u = 0; u < J; ++u) {
+                        const uint4 e = exact_word(value_word(vw, u));
+                        store16(place(base, u, y), e.x, e.y, e.z, e.w);
+                    }
+                } else {
+                    float2 vs[G];
                     const KeyOf<G> k = key_of<G, MASKS>(see_lo, see_hi, kept, key_of_tile(i) + key0 + kStep * y,
-                                                 raw_z + raw + y * kStep * 8 * G + M::kRawSz,
-                                                 bad_at + rs * 16 + ((key0 + kStep * y) >> 4) * 4, vs);
+                                                        raw_z + raw + y * kStep * 8 * G + M::kRawSz,
+                                                        bad_at + rs * 16 + ((key0 + kStep * y) >> 4) * 4, vs);
                     // what is not finite is zero here: the key's factor spoils the rows that see it
-                    up = k.finite ? pow2(min(k.exponent(), 80)) : 0.0f;
+                    const float up = k.finite ? pow2(min(k.exponent(), 80)) : 0.0f;
                     if (!k.finite) {
 #pragma unroll
                         for (int g = 0; g < G; ++g) vs[g] = make_float2(0.0f, 0.0f);
                     }
-                }
-#pragma unroll
-                for (int u = 0; u < J; ++u) {
-                    const uint32_t word = value_word(vw, u), at = place(base, u, y);
-                    if constexpr (EXACT) {
-                        const uint4 e = exact_word(word);
-                        store16(at, e.x, e.y, e.z, e.w);
-                    } else {
+#pragma unroll kBlocks
+                    for (int u = 0; u < J; ++u) {
+                        // the block's 8 codes: halves 2c and 2c + 1, J halves apart
+                        const uint32_t from = raw_w + raw + y * kStep * 16 * J + M::kRawCodes + 2 * u;
+                        uint16_t h0, h1;
+                        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h0) : "r"(from) : "memory");
+                        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h1) : "r"(from + 2 * J) : "memory");
+                        const float2 z = scale_of(vs, u);
                         uint32_t hi[4], lo[4];
-                        dequant_word(word, vs[u / UG].x * up, vs[u / UG].y, hi, lo);
+                        dequant_word(h0 | (uint32_t)h1 << 16, z.x * up, z.y, hi, lo);
+                        const uint32_t at = place(base, u, y);
                         store16(at, hi[0], hi[1], hi[2], hi[3]);
                         store16(at + M::kKV, lo[0], lo[1], lo[2], lo[3]);
                     }

