@@ -68,7 +68,9 @@ cudaError_t launch_attn(const AttnCall &in, cudaStream_t stream)
     const long long seen = call.tree && call.window > 0 ? (long long)call.window + call.sinks + call.max_query : call.max_len;
     const bool enough = call.tree ? (long long)call.T * call.heads * (seen < call.max_len ? seen : call.max_len) >= kTreeScores
                                   : (long long)call.T * call.heads >= kPromptTotal;
-    const bool prompt = prompt_path_supported(call) && call.max_query * R >= least && enough;
+    // (the workspace of a tree call goes by T: no request has more rows than that)
+    const long long most = call.tree && call.T < call.max_query ? call.T : call.max_query;
+    const bool prompt = prompt_path_supported(call) && most * R >= least && enough;
     call.prompt_rows = prompt ? least : 0x7fffffff;
     call.apart = reinterpret_cast<ApartTile *>(static_cast<char *>(call.workspace) + sums_bytes(call.c.head_dim));
     call.n_units = call.n_apart = prompt ? prompt_ctas(call.B, call.T, call.heads, call.c.kv_heads) : 0;

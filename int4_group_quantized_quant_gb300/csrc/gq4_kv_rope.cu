@@ -90,6 +90,7 @@ struct Quarter {
         const double whole = 6755399441055744.0;                  // 1.5 2^52: a sum's last bit counts ones
         const double m = fma(a, 0.6366197723675814, whole), k = m - whole;   // 2 / pi
         r = fma(k, -6.123233995736766e-17, fma(k, -1.5707963267948966, a));
+        if (fabsf((float)r) >= 1.0f) r = 0.0;          // (angles from 2^50 on, which mean nothing, stay bounded)
         n = __double2loint(m) & 3;
     }
 };

@@ -274,6 +274,21 @@ def test_requests_that_share_rows_stay_in_bounds(gq4):
     assert not ws[size:].any()
 
 
+def test_a_bound_above_the_rows_of_the_call(gq4):
+    """Fewer rows than max_query: the kernel and the workspace go by the rows."""
+    s = Setup([2], [3000], 32, 8, 128, 128, 16, words=2, pad=0, room=1 << 20)
+    size = gq4.kv_attention_workspace_bytes(2, 32, 8, 128, tree=True)
+    ws = torch.zeros(size + (1 << 25), dtype=torch.uint8, device="cuda")
+    s.check(s.run(gq4, max_query=64, workspace=ws[:size]))
+    assert not ws[size:].any() and gq4.device_error() == 0
+    for T, H, KH, D in ((16, 32, 8, 128), (64, 1, 1, 64), (1, 64, 1, 96), (8, 128, 8, 64)):     # the fewest rows of a tree call
+        s = Setup([T], [3000], H, KH, D, D, 16, words=2, pad=0, room=1 << 20)
+        size = gq4.kv_attention_workspace_bytes(T, H, KH, D, tree=True)
+        ws = torch.zeros(size + (1 << 25), dtype=torch.uint8, device="cuda")
+        s.check(s.run(gq4, workspace=ws[:size]))
+        assert not ws[size:].any() and gq4.device_error() == 0
+
+
 @pytest.mark.parametrize("H", [4, 64])
 def test_queries_that_see_nothing(gq4, H):
     """seq_len < n with sinks and with bits; length 0."""

@@ -62,6 +62,8 @@ APPENDS = [
     (25, 0, 4, 128, 32, 16, 128, False, False, True), (30, 16, 3, 256, 32, 16, 8, False, True, True),
     (700, 4, 5, 128, 128, 16, 128, False, True, True), (650, 9, 3, 64, 32, 16, 32, True, False, False),
     (50, 2, 2, 128, 32, 16, 0, False, True, True), (31, 1, 7, 96, 32, 16, 88, False, False, False),
+    (401, 3, 2, 64, 64, 16, 64, False, True, True), (307, 0, 1, 256, 128, 32, 128, True, False, False),
+    (305, 33, 17, 96, 96, 16, 48, False, False, True), (3, 200, 65, 64, 32, 16, 64, False, True, True),
 ]
 
 
@@ -142,6 +144,31 @@ def test_rope_append_like_the_two_calls(gq4):
     used[slots[slots >= 0]] = True
     assert np.all(host(one[1]).transpose(0, 2, 1, 3, 4).reshape(80, -1)[~used] == 0)
     assert gq4.device_error() == 0
+
+
+def test_far_positions_and_huge_frequencies(gq4):
+    """Positions up to 2^31 - 1: queries and values hold; frequencies beyond all sense stay bounded, NaN ones are NaN."""
+    T, D = 5, 64
+    g = I.rng(2504)
+    pos = np.array([2**31 - 1, 2**30 + 12345, 2**20 + 1, 7, 0], np.int32)
+    q, k, v = (g.standard_normal((T, 2, D)).astype(np.float32) for _ in range(3))
+    cache = gq4.kv_cache(1, 2, 16, D, 32)
+    slots = np.arange(T, dtype=np.int32)
+    qr = gq4.kv_rope_append(dev(q), dev(k), dev(v), dev(pos), dev(inv_freq(D)), dev(slots), *cache, 32)
+    y, size = R.norm_rope(q, None, 0, pos, inv_freq(D), False)
+    # an angle is a 64-bit product, off by 2^-53 of it: 2^-22 at 2^31
+    assert np.all(np.abs(host(qr) - y) <= (16 * 2.0 ** -24 + pos[:, None, None] * 2.0 ** -53) * size)
+    kr = host(gq4.kv_gather(dev(slots), *cache, 32)[0])
+    y, size = R.norm_rope(k, None, 0, pos, inv_freq(D), False)
+    step = host(cache[1])[0, :, :T, :, 0].transpose(1, 0, 2).repeat(32, -1)
+    assert np.all(np.abs(kr - y) <= 0.5 * step + 64 * 2.0 ** -22 * size)
+    inv = inv_freq(D)
+    inv[3], inv[5] = 1e30, np.nan
+    qr = host(gq4.kv_rope_append(dev(q), dev(k), dev(v), dev(pos), dev(inv), dev(slots), *cache, 32))
+    bad = np.zeros(D, bool)
+    bad[[5, 5 + D // 2]] = True
+    assert np.isnan(qr[..., bad]).all() and np.all(np.abs(qr[..., ~bad]) <= 2 * np.abs(q).max())
+    assert gq4.device_error(clear=True) == 1 << 3
 
 
 def test_rope_append_marks_what_is_wrong(gq4):
