@@ -9,7 +9,7 @@
 // rotated keys' way to HBM and back (8 bytes per value of k).  Floor: 8 bytes
 // per value of q, 4 read and 0.5 + 8/gs written per value of k and v.  16381
 // tokens, 32 + 8 heads of 128: 118 us, 692 MB at 5.9 TB/s (0.86 of a copy's;
-// normalised 128; the two calls 138 and 147), of which exact_unit is 10; 61
+// normalised 128; the two calls 138 and 147), of which exact_values is 10; 61
 // tokens 5.7 us, of which it is 2.
 //
 // Two kinds of CTAs take turns in the grid, so that the queries', which wait for
@@ -30,7 +30,7 @@
 // (|a| + |b|) for the pair (a, b) before the rotation.  Where that could turn a
 // code's rounding -- a value so near to the border of two codes -- the warp
 // computes its rows again, the values next to a border and next to the group's
-// two ends in 64 bits (exact_unit).  With groups of 128 normal values that is
+// two ends in 64 bits (exact_values).  With groups of 128 normal values that is
 // one warp's 256 values in 100.
 #include <cstdint>
 
@@ -311,13 +311,6 @@ struct Group {
     }
 };
 
-// An argument's distance to the nearest code.
-__device__ __forceinline__ float from_code(float v, const GroupMap &m)
-{
-    const float t = __fmul_rn(__fsub_rn(v, m.lo), m.r);
-    return fabsf(t - rintf(t));
-}
-
 // How far a code's argument t = 15 (v - lo) / (hi - lo) may be off: v, and lo
 // and hi in the parts 1 - t / 15 and t / 15, each by 2 key_error of the row's
 // largest.
@@ -372,38 +365,33 @@ struct KvRow {
     }
 };
 
-// The scratch of a warp in exact_unit: its 256 values, and which are needed.
+// The scratch of a warp for exact_values: its 256 values, and which are needed.
 struct ExactShared {
     float v[256];
     uint8_t list[256];
 };
 
-// A unit of key rows whose values (in s.v) next to a border, and to its group's
-// ends, are computed in 64 bits.  By the whole warp.
-template <int J, int L>
-__device__ __noinline__ void exact_unit(const RopeAppendParams &p, int t, int unit, int slot, ExactShared &s)
+// Of a unit of key rows, whose values are in s.v, those next to a border of two
+// codes and to their group's ends, in 64 bits.  lo, hi, r32, slack, near: of the
+// lane's group, its ends, its factor and how far its arguments and values may be
+// off; wanted: it has codes.  By the whole warp.
+template <int J>
+__device__ __noinline__ void exact_values(const RopeAppendParams &p, int t, int unit, bool wanted, float lo, float hi, float r32,
+                                          float slack, float near, ExactShared &s)
 {
     constexpr int D = 32 * J, WPR = 4 * J;
     const int lane = threadIdx.x & 31, in_warp = lane / WPR, w = lane - in_warp * WPR;
     const KvRow<J> row(p, t, unit, false, in_warp);
     const bool norm = p.k_gain != nullptr;
-    float v[8];
-    auto read = [&] {
-        const float4 a = *reinterpret_cast<const float4 *>(s.v + 8 * lane), b = *reinterpret_cast<const float4 *>(s.v + 8 * lane + 4);
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    };
-    read();
     // the values needed as a list, of which each lane takes one at a time: most
     // often there are fewer than lanes
     uint32_t need = 0;
-    {
-        const Group<J, L> g(v, w, lane);
-        const float largest = g.largest(w, lane), slack = code_slack(largest, g.m, norm), near = 4.0f * key_error(norm) * largest;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (!(from_code(v[i], g.m) <= 0.5f - slack) || v[i] <= g.lo + near || v[i] >= g.hi - near) need |= 1u << i;
-        if (!row.live || g.bad) need = 0;
+    if (wanted) {
+#pragma unroll 2
+        for (int i = 0; i < 8; ++i) {
+            const float v = s.v[8 * lane + i], x = __fmul_rn(__fsub_rn(v, lo), r32);
+            if (!(fabsf(x - rintf(x)) <= 0.5f - slack) || v <= lo + near || v >= hi - near) need |= 1u << i;
+        }
     }
     int at = __popc(need);
     const int mine = at;
@@ -455,15 +443,10 @@ __device__ __noinline__ void exact_unit(const RopeAppendParams &p, int t, int un
         }
     }
     __syncwarp();
-    read();
-    const Group<J, L> g(v, w, lane);
-    const uint32_t word = g.bad ? 0u : quantize_word(v, g.m);
-    if (row.live) write_word<J, L>(p, slot, row.head, 0, w, word, 0u, g.bad, g.m, &g_kv_rope_error);
-    __syncwarp();
 }
 
 template <int J, int L>
-__device__ __forceinline__ void kv_rows(const RopeAppendParams &p, int t0, int part, const Turn<J> *turns, ExactShared *exact)
+__device__ __forceinline__ void kv_rows(const RopeAppendParams &p, int t0, int part, const Turn<J> *turns, ExactShared *scratch)
 {
     constexpr int WPR = 4 * J;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -504,23 +487,33 @@ __device__ __forceinline__ void kv_rows(const RopeAppendParams &p, int t0, int p
                 if (p.k_gain) a[f] = times(a[f], make_float4(r, r, r, r));
             }
         }
-        const float v[8] = {a[0].x, a[0].y, a[0].z, a[0].w, a[1].x, a[1].y, a[1].z, a[1].w};
-        const Group<J, L> g(v, w, lane);
-        bool border = false;
-        float far;
-        uint32_t word = code_word<true>(v, g.m, far);
-        if (!value && (p.rot > 0 || p.k_gain))
-            border = !(far <= 0.5f - code_slack(g.largest(w, lane), g.m, p.k_gain != nullptr)) && row.live && !g.bad;
-        if (__any_sync(0xffffffffu, border)) {
-            float4 *to = reinterpret_cast<float4 *>(exact[warp].v + 8 * lane);
-            to[0] = a[0];
-            to[1] = a[1];
-            __syncwarp();
-            exact_unit<J, L>(p, t, unit, slot, exact[warp]);
-        } else {
-            word = g.bad ? 0u : word;
-            const uint32_t other = __shfl_xor_sync(0xffffffffu, word, 4);
+        bool exact = value || (p.rot == 0 && !p.k_gain);
+#pragma unroll 1
+        for (;;) {
+            const float v[8] = {a[0].x, a[0].y, a[0].z, a[0].w, a[1].x, a[1].y, a[1].z, a[1].w};
+            const Group<J, L> g(v, w, lane);
+            float far;
+            const uint32_t code = code_word<true>(v, g.m, far);
+            if (!exact) {
+                const float largest = g.largest(w, lane), slack = code_slack(largest, g.m, p.k_gain != nullptr);
+                if (__any_sync(0xffffffffu, !(far <= 0.5f - slack) && row.live && !g.bad)) {
+                    // once more with the values that count in 64 bits (a group that is not finite stays so)
+                    float4 *at = reinterpret_cast<float4 *>(scratch[warp].v + 8 * lane);
+                    at[0] = a[0];
+                    at[1] = a[1];
+                    __syncwarp();
+                    exact_values<J>(p, t, unit, row.live && !g.bad, g.lo, g.hi, g.m.r, slack,
+                                    4.0f * key_error(p.k_gain != nullptr) * largest, scratch[warp]);
+                    a[0] = at[0];
+                    a[1] = at[1];
+                    __syncwarp();
+                    exact = true;
+                    continue;
+                }
+            }
+            const uint32_t word = g.bad ? 0u : code, other = __shfl_xor_sync(0xffffffffu, word, 4);
             if (row.live) write_word<J, L>(p, slot, row.head, value, w, word, other, g.bad, g.m, &g_kv_rope_error);
+            break;
         }
     }
 }
@@ -530,7 +523,7 @@ template <int J, int L>
 __global__ void __launch_bounds__(kRopeAppendThreads, 8) rope_append_kernel(const __grid_constant__ RopeAppendParams p)
 {
     __shared__ Turn<J> turns[kRopeTokens];
-    __shared__ alignas(16) ExactShared exact[kRopeAppendWarps];
+    __shared__ alignas(16) ExactShared scratch[kRopeAppendWarps];
     const int turn = blockIdx.x / (p.turn + 1), place = blockIdx.x - turn * (p.turn + 1);
     const bool kv = place == 0;
     const int cta = kv ? turn : turn * p.turn + place - 1;
@@ -543,7 +536,7 @@ __global__ void __launch_bounds__(kRopeAppendThreads, 8) rope_append_kernel(cons
         const int n = i >= half;
         make_turn<J>(p, __ldg(p.positions + t0 + n), i - n * half, kv ? p.k_gain : p.q_gain, turns[n]);
     }
-    if (kv) kv_rows<J, L>(p, t0, part, turns, exact);
+    if (kv) kv_rows<J, L>(p, t0, part, turns, scratch);
     else query_rows<J>(p, t0, part, turns[0]);
 }
 
