@@ -95,6 +95,7 @@ constexpr int kWholeStages = 4;                   // units of so few stages are 
 // What a unit's start costs a warp, in stages, when shares are cut (0 / 2 / 4 take 31.9 / 30.1 / 29.4 us for the
 // drafts below, 48.1 / 47.0 / 47.7 for the 48 requests)
 constexpr int kStart = 2;
+constexpr int kWholeUnit = 32;                    // MASKS: units of so few stages are one CTA's (see launch_split)
 constexpr int kMaxGrid = 304;                     // CTAs (the workspace's slots)
 
 struct SplitParams {
@@ -105,6 +106,7 @@ struct SplitParams {
                         // row block), (last CTA or -1, slot)
     int R;              // query heads per kv head
     int grid;
+    int whole;          // MASKS: no unit is cut between CTAs (up to kThreads requests)
 };
 
 // Key (0..15) that row i of the instruction's A operand takes.  A thread of
@@ -436,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
     };
     for (int b0 = 0; b0 < a.B; b0 += kThreads) total += tile(b0, true);
     const long long chunk = quotient(total + gridDim.x - 1, (int)gridDim.x);
-    const long long raw0 = chunk * blockIdx.x, raw1 = min(raw0 + chunk, total);
+    long long raw0 = chunk * blockIdx.x, raw1 = min(raw0 + chunk, total);
     // requests that need no sums: bad ones, and those without keys
     __syncthreads();
     if (s.start.special) {
@@ -451,6 +453,20 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
         }
     }
     if (raw0 >= raw1) return;
+    if (MASKS && p.whole) {
+        // from the start of the unit that the range starts in to that of the one that it ends in
+        auto unit_start = [&](long long raw) {
+            if (raw >= total) return total;
+            const int block = __ffs(__ballot_sync(0xffffffffu, t_end[lane * 8 + 7] > raw)) - 1;
+            const int i = block * 8 + __ffs(__ballot_sync(0xffffffffu, t_end[block * 8 + (lane & 7)] > raw)) - 1;
+            const long long at = raw - (i > 0 ? t_end[i - 1] : 0);
+            const int length = t_req[i].w + kStart;
+            return raw - (at - quotient(at, length) * length);
+        };
+        raw0 = unit_start(raw0);
+        raw1 = unit_start(raw1);
+        if (raw0 >= raw1) return;          // uniform
+    }
     // this warp's range, from the unit that its first stage belongs to
     long long wb = total, we = total;
     int b = 0, unit = 0, from = 0;    // of the request: (kv head, row block), stage
@@ -1306,6 +1322,17 @@ cudaError_t launch_split(const AttnCall &call, cudaStream_t stream)
     long long grid = (long long)sms * MINB;
     if (grid > kMaxGrid / 2 * MINB) grid = kMaxGrid / 2 * MINB;
     if (grid > (units * steps + kWarps - 1) / kWarps) grid = (units * steps + kWarps - 1) / kWarps;
+    // Few keys: whole units, joined in their CTA, and no second kernel.  Up
+    // to about 1024 keys that is worth more than the SMs that it leaves
+    // empty.  us of units cut / whole, replayed and (called one by one), 32
+    // over 8 heads of 128, group 128:
+    //   a tree of 15 behind 300   16.5 / 14.3  (25.2 / 22.6)   behind 700   18.4 / 16.4  (25.0 / 22.9)
+    //   40 trees of 7, up to 300  32.5 / 30.2  (31.1 / 30.0)   up to 700    44.6 / 40.9  (44.6 / 38.2)
+    //   32 tokens, window 300     16.4 / 16.5  (24.2 / 21.2)   window 700   18.6 / 20.6  (24.4 / 21.5)
+    // and beyond it, a tree behind 1200 18.5 / 18.0, behind 2000 21.8 / 22.6,
+    // 32 tokens with a window of 1200 23.5 / 25.8 (24.1 / 24.8).
+    p.whole = MASKS && call.n_apart == 0 && call.B <= kThreads && steps <= kWholeUnit;
+    if (p.whole && grid > units) grid = units;
     if (grid < 1) grid = 1;
     p.grid = (int)grid;
     p.R = R;
@@ -1313,7 +1340,7 @@ cudaError_t launch_split(const AttnCall &call, cudaStream_t stream)
     p.part = reinterpret_cast<float *>(static_cast<char *>(call.workspace) + 2 * kMaxGrid * sizeof(int4));
     p.head = p.part + (size_t)grid * 2 * 4 * NB * (32 * J + 2);
     kern<<<(unsigned)grid, kThreads, smem, stream>>>(p);
-    if ((err = cudaGetLastError()) != cudaSuccess || ((steps <= kWholeStages || grid <= 1) && call.n_apart == 0))
+    if ((err = cudaGetLastError()) != cudaSuccess || ((steps <= kWholeStages || grid <= 1 || p.whole) && call.n_apart == 0))
         return err;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];

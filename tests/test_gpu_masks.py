@@ -156,6 +156,22 @@ def test_trees_of_many_rows(gq4, H, KH, D, gs, page, window, sinks):
     assert gq4.device_error() == 0
 
 
+@pytest.mark.parametrize("room", [0, 32768])
+@pytest.mark.parametrize("requests", [1, 40, 255, 256, 257])
+@pytest.mark.parametrize("H,KH,D,gs", [(8, 2, 128, 128), (14, 2, 64, 32), (5, 5, 96, 96)])
+@pytest.mark.parametrize("words,window,sinks", [(1, 0, 0), (0, 100, 40), (1, 600, 4)])
+def test_units_whole_and_cut(gq4, H, KH, D, gs, requests, room, words, window, sinks):
+    """Bounds on the keys that let a unit of work be one block's, and ones that have it cut between blocks."""
+    g = I.rng(2405, requests, H)
+    news = [int(n) for n in g.integers(0, 4, requests)]
+    news[0] = 9
+    lens = [n + int(x) for n, x in zip(news, g.integers(0, 120, requests))]
+    lens[0] = 1023
+    s = Setup(news, lens, H, KH, D, gs, 16, window, sinks, words=words, room=room or max(1024, *lens))
+    s.check(s.run(gq4))
+    assert gq4.device_error() == 0
+
+
 @pytest.mark.parametrize("H,KH", [(4, 2), (64, 2)])
 def test_the_largest_trees(gq4, H, KH):
     s = Setup([256, 250], [256 + 19, 250 + 700], H, KH, 64, 32, 16, words=8)
