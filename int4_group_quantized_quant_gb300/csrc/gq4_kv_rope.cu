@@ -37,6 +37,7 @@
 #include "gq4_kv_internal.h"
 #include "gq4_kv_write.cuh"
 #include "gq4_rope.cuh"
+#include "gq4_two.cuh"
 
 namespace gq4 {
 namespace {
@@ -123,12 +124,37 @@ __device__ __forceinline__ void sin_cos_series(F x, int n, F &s, F &c)
     if ((n + 1) & 2) c = -c;
 }
 
-__device__ __forceinline__ float2 sin_cos_at(int pos, float inv_freq)
+// The same in twice 24 bits, off by 2^-46: the terms from 2^-25 of the first on
+// in f32.
+__device__ __forceinline__ void sin_cos_two(Two x, int n, Two &s, Two &c)
 {
-    const Quarter turn(pos, inv_freq);
-    float2 sc;
-    sin_cos_series<5, float>((float)turn.r, turn.n, sc.x, sc.y);
-    return sc;
+    Two y = mul(x, x);
+    y = {-y.hi, -y.lo};
+    constexpr float tail_a[] = {(float)(1.0 / 39916800), (float)(1.0 / 6227020800.0), (float)(1.0 / 1307674368000.0)};
+    constexpr float tail_b[] = {(float)(1.0 / 3628800), (float)(1.0 / 479001600), (float)(1.0 / 87178291200.0)};
+    constexpr Two terms_a[] = {two_of(1), two_of(1.0 / 6), two_of(1.0 / 120), two_of(1.0 / 5040), two_of(1.0 / 362880)};
+    constexpr Two terms_b[] = {two_of(1), two_of(0.5), two_of(1.0 / 24), two_of(1.0 / 720), two_of(1.0 / 40320)};
+    Two a = {__fmaf_rn(__fmaf_rn(tail_a[2], y.hi, tail_a[1]), y.hi, tail_a[0]), 0.0f};
+    Two b = {__fmaf_rn(__fmaf_rn(tail_b[2], y.hi, tail_b[1]), y.hi, tail_b[0]), 0.0f};
+#pragma unroll
+    for (int i = 4; i >= 0; --i) {
+        a = add_smaller(terms_a[i], mul(a, y));
+        b = add_smaller(terms_b[i], mul(b, y));
+    }
+    a = mul(a, x);
+    s = n & 1 ? b : a;
+    c = n & 1 ? a : b;
+    if (n & 2) s = {-s.hi, -s.lo};
+    if ((n + 1) & 2) c = {-c.hi, -c.lo};
+}
+
+// 1 / sqrt(x): f32's, and its series in the rest.
+__device__ __forceinline__ Two inv_sqrt_two(Two x)
+{
+    const float r = inv_sqrt(x.hi);
+    const Two q = mul(mul(x, Two{r, 0.0f}), Two{r, 0.0f});
+    const float e = __fsub_rn(__fsub_rn(1.0f, q.hi), q.lo);
+    return {r, r * __fmaf_rn(0.375f * e, e, 0.5f * e)};
 }
 
 // The partner of value d (a multiple of 4) of a half-split rotation.
@@ -154,11 +180,24 @@ struct alignas(16) Turn {
     float A[32 * J], B[32 * J];
 };
 
-// Pair i of a token's table.  gain: NULL for ones.
+// Its angles, for exact_values.
 template <int J>
-__device__ __forceinline__ void make_turn(const RopeAppendParams &p, int pos, int i, const float *gain, Turn<J> &t)
+struct Angles {
+    double r[16 * J];
+    uint8_t n[16 * J];
+};
+
+// Pair i of a token's table.  gain: NULL for ones; angles: NULL for none.
+template <int J>
+__device__ __forceinline__ void make_turn(const RopeAppendParams &p, int pos, int i, const float *gain, Turn<J> &t, Angles<J> *angles)
 {
-    const float2 sc = sin_cos_at(pos, __ldg(p.inv_freq + i));
+    const Quarter turn(pos, __ldg(p.inv_freq + i));
+    if (angles) {
+        angles->r[i] = turn.r;
+        angles->n[i] = (uint8_t)turn.n;
+    }
+    float2 sc;
+    sin_cos_series<5, float>((float)turn.r, turn.n, sc.x, sc.y);
     const int a = p.interleaved ? 2 * i : i, b = p.interleaved ? 2 * i + 1 : i + (p.rot >> 1);
     const float ga = gain ? __ldg(gain + a) : 1.0f, gb = gain ? __ldg(gain + b) : 1.0f;
     t.A[a] = ga * sc.y;
@@ -255,20 +294,31 @@ __device__ __forceinline__ void query_rows(const RopeAppendParams &p, int t, int
 // Keys and values
 // ---------------------------------------------------------------------------
 
+__device__ __forceinline__ Two shuffled(Two a, int from)
+{
+    return {__shfl_sync(0xffffffffu, a.hi, from), __shfl_sync(0xffffffffu, a.lo, from)};
+}
+
+template <typename V>
+__device__ __forceinline__ V shuffled(V a, int from)
+{
+    return __shfl_sync(0xffffffffu, a, from);
+}
+
 // Sum over a row's lanes, in each of them (lanes of no row: anything).
 template <int WPR, typename V>
 __device__ __forceinline__ V row_sum(V s, int w, int lane)
 {
     if constexpr ((WPR & (WPR - 1)) == 0) {
 #pragma unroll
-        for (int o = WPR >> 1; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        for (int o = WPR >> 1; o > 0; o >>= 1) s += shuffled(s, lane ^ o);
     } else {
 #pragma unroll
         for (int o = 1; o < WPR; o <<= 1) {
-            const V t = __shfl_down_sync(0xffffffffu, s, o);
+            const V t = shuffled(s, min(lane + o, 31));
             if (w % (2 * o) == 0 && w + o < WPR) s += t;
         }
-        s = __shfl_sync(0xffffffffu, s, lane - w);
+        s = shuffled(s, lane - w);
     }
     return s;
 }
@@ -365,88 +415,101 @@ struct KvRow {
     }
 };
 
-// The scratch of a warp for exact_values: its 256 values, and which are needed.
-struct ExactShared {
-    float v[256];
-    uint8_t list[256];
-};
-
-// Of a unit of key rows, whose values are in s.v, those next to a border of two
-// codes and to their group's ends, in 64 bits.  lo, hi, r32, slack, near: of the
-// lane's group, its ends, its factor and how far its arguments and values may be
-// off; wanted: it has codes.  By the whole warp.
+// Of a unit of key rows, whose values are in v, a lane's 8 in place, those next
+// to a border of two codes and to their group's ends, in twice 24 bits; in 64
+// where the row's size would cost the former bits.  lo, hi, r32, slack, near: of
+// the lane's group, its ends, its factor and how far its arguments and values may
+// be off; largest: of its row; wanted: it has codes.  By the whole warp.
 template <int J>
 __device__ __noinline__ void exact_values(const RopeAppendParams &p, int t, int unit, bool wanted, float lo, float hi, float r32,
-                                          float slack, float near, ExactShared &s)
+                                          float slack, float near, float largest, const Angles<J> &angles, float *v)
 {
     constexpr int D = 32 * J, WPR = 4 * J;
     const int lane = threadIdx.x & 31, in_warp = lane / WPR, w = lane - in_warp * WPR;
     const KvRow<J> row(p, t, unit, false, in_warp);
     const bool norm = p.k_gain != nullptr;
-    // the values needed as a list, of which each lane takes one at a time: most
-    // often there are fewer than lanes
+    v += 8 * lane;
     uint32_t need = 0;
     if (wanted) {
-#pragma unroll 2
+#pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float v = s.v[8 * lane + i], x = __fmul_rn(__fsub_rn(v, lo), r32);
-            if (!(fabsf(x - rintf(x)) <= 0.5f - slack) || v <= lo + near || v >= hi - near) need |= 1u << i;
+            const float x = __fmul_rn(__fsub_rn(v[i], lo), r32);
+            if (!(fabsf(x - rintf(x)) <= 0.5f - slack) || v[i] <= lo + near || v[i] >= hi - near) need |= 1u << i;
         }
     }
-    int at = __popc(need);
-    const int mine = at;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int n = __shfl_up_sync(0xffffffffu, at, o);
-        if (lane >= o) at += n;
-    }
-    const int all = __shfl_sync(0xffffffffu, at, 31);
-    at -= mine;
-#pragma unroll 1
-    for (; need; need &= need - 1) s.list[at++] = (uint8_t)(8 * lane + __ffs(need) - 1);
-    double r = 1.0;
+    bool sized = largest >= 0x1p-50f && largest <= 0x1p50f;
+    Two r = {1.0f, 0.0f};
     if (norm) {
-        double sum = 0.0;
+        Two sum = {0.0f, 0.0f};
         if (row.live) {
 #pragma unroll 2
             for (int i = 0; i < 8; ++i) {
-                const double x = row.at[8 * w + i];
-                sum = fma(x, x, sum);
+                const float x = row.at[8 * w + i];
+                sum += two_product(x, x);
             }
         }
-        sum = fma(row_sum<WPR>(sum, w, lane), 1.0 / D, (double)p.eps);
-        r = inv_sqrt((float)sum);
-        if (r > 0.0 && r < 1e30) {         // and two Newton steps
-            r = fma(fma(-0.5 * sum * r, r, 0.5), r, r);
-            r = fma(fma(-0.5 * sum * r, r, 0.5), r, r);
-        }
+        sum = row_sum<WPR>(sum, w, lane);
+        sum = add(mul(sum, two_of(1.0 / D)), Two{p.eps, 0.0f});
+        sized &= sum.hi >= 0x1p-50f && sum.hi <= 0x1p50f;
+        r = inv_sqrt_two(sum);
     }
-    __syncwarp();
-    const int half = p.rot >> 1, pos = p.rot > 0 ? __ldg(p.positions + t) : 0;
-    for (int n0 = 0; n0 < all; n0 += 32) {
-        const int e = n0 + lane < all ? s.list[n0 + lane] : 0, from = e >> 3;   // value e & 7 of lane `from`
-        const double factor = __shfl_sync(0xffffffffu, r, from);
-        if (n0 + lane < all) {
-            const int d = 8 * (from % WPR) + (e & 7);
-            const float *x = KvRow<J>(p, t, unit, false, from / WPR).at;
-            auto value = [&](int m) { return (double)x[m] * (norm ? (double)__ldg(p.k_gain + m) : 1.0); };
+    const int half = p.rot >> 1;
+    auto other_of = [&](int d) { return p.interleaved ? d ^ 1 : partner_of(d, half); };
+    auto pair_of = [&](int d) { return p.interleaved ? d >> 1 : min(d, partner_of(d, half)); };
+    auto is_first = [&](int d) { return p.interleaved ? !(d & 1) : d < half; };
+    if (__all_sync(0xffffffffu, sized || !wanted)) {
+#pragma unroll 1
+        for (; need; need &= need - 1) {
+            const int i = __ffs(need) - 1, d = 8 * w + i;
+            auto value = [&](int m) { return norm ? two_product(row.at[m], __ldg(p.k_gain + m)) : Two{row.at[m], 0.0f}; };
+            Two y = value(d);
+            if (d < p.rot) {
+                const double x = angles.r[pair_of(d)];
+                const float x_hi = (float)x;
+                Two sine, cosine;
+                sin_cos_two(Two{x_hi, (float)(x - (double)x_hi)}, angles.n[pair_of(d)], sine, cosine);
+                if (is_first(d)) sine = {-sine.hi, -sine.lo};
+                y = add(mul(y, cosine), mul(sine, value(other_of(d))));
+            }
+            y = mul(y, r);
+            v[i] = __fadd_rn(y.hi, y.lo);
+        }
+    } else {
+        double factor = 1.0;
+        if (norm) {
+            double sum = 0.0;
+            if (row.live) {
+#pragma unroll 1
+                for (int i = 0; i < 8; ++i) {
+                    const double x = row.at[8 * w + i];
+                    sum = fma(x, x, sum);
+                }
+            }
+            sum = fma(row_sum<WPR>(sum, w, lane), 1.0 / D, (double)p.eps);
+            factor = inv_sqrt((float)sum);
+            if (factor > 0.0 && factor < 1e30) {         // and two Newton steps
+                factor = fma(fma(-0.5 * sum * factor, factor, 0.5), factor, factor);
+                factor = fma(fma(-0.5 * sum * factor, factor, 0.5), factor, factor);
+            }
+        }
+#pragma unroll 1
+        for (; need; need &= need - 1) {
+            const int i = __ffs(need) - 1, d = 8 * w + i;
+            auto value = [&](int m) { return (double)row.at[m] * (norm ? (double)__ldg(p.k_gain + m) : 1.0); };
             double y = value(d);
             if (d < p.rot) {
-                const bool first = p.interleaved ? !(d & 1) : d < half;
-                const int other = p.interleaved ? d ^ 1 : partner_of(d, half);
                 double sine, cosine;
-                const Quarter turn(pos, __ldg(p.inv_freq + (p.interleaved ? d >> 1 : min(d, other))));
-                sin_cos_series<9, double>(turn.r, turn.n, sine, cosine);
-                y = y * cosine + (first ? -sine : sine) * value(other);
+                sin_cos_series<9, double>(angles.r[pair_of(d)], angles.n[pair_of(d)], sine, cosine);
+                y = y * cosine + (is_first(d) ? -sine : sine) * value(other_of(d));
             }
-            s.v[e] = (float)(y * factor);
+            v[i] = (float)(y * factor);
         }
     }
     __syncwarp();
 }
 
 template <int J, int L>
-__device__ __forceinline__ void kv_rows(const RopeAppendParams &p, int t0, int part, const Turn<J> *turns, ExactShared *scratch)
+__device__ __forceinline__ void kv_rows(const RopeAppendParams &p, int t0, int part, const Turn<J> *turns, const Angles<J> *angles, float (*scratch)[256])
 {
     constexpr int WPR = 4 * J;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -498,15 +561,13 @@ __device__ __forceinline__ void kv_rows(const RopeAppendParams &p, int t0, int p
                 const float largest = g.largest(w, lane), slack = code_slack(largest, g.m, p.k_gain != nullptr);
                 if (__any_sync(0xffffffffu, !(far <= 0.5f - slack) && row.live && !g.bad)) {
                     // once more with the values that count in 64 bits (a group that is not finite stays so)
-                    float4 *at = reinterpret_cast<float4 *>(scratch[warp].v + 8 * lane);
+                    float4 *at = reinterpret_cast<float4 *>(scratch[warp] + 8 * lane);
                     at[0] = a[0];
                     at[1] = a[1];
-                    __syncwarp();
                     exact_values<J>(p, t, unit, row.live && !g.bad, g.lo, g.hi, g.m.r, slack,
-                                    4.0f * key_error(p.k_gain != nullptr) * largest, scratch[warp]);
+                                    4.0f * key_error(p.k_gain != nullptr) * largest, largest, angles[n], scratch[warp]);
                     a[0] = at[0];
                     a[1] = at[1];
-                    __syncwarp();
                     exact = true;
                     continue;
                 }
@@ -523,7 +584,8 @@ template <int J, int L>
 __global__ void __launch_bounds__(kRopeAppendThreads, 8) rope_append_kernel(const __grid_constant__ RopeAppendParams p)
 {
     __shared__ Turn<J> turns[kRopeTokens];
-    __shared__ alignas(16) ExactShared scratch[kRopeAppendWarps];
+    __shared__ Angles<J> angles[kRopeTokens];
+    __shared__ alignas(16) float scratch[kRopeAppendWarps][256];
     const int turn = blockIdx.x / (p.turn + 1), place = blockIdx.x - turn * (p.turn + 1);
     const bool kv = place == 0;
     const int cta = kv ? turn : turn * p.turn + place - 1;
@@ -534,9 +596,10 @@ __global__ void __launch_bounds__(kRopeAppendThreads, 8) rope_append_kernel(cons
     const int half = p.rot >> 1, tokens = min(per, p.T - t0);
     for (int i = threadIdx.x; i < tokens * half; i += kRopeAppendThreads) {
         const int n = i >= half;
-        make_turn<J>(p, __ldg(p.positions + t0 + n), i - n * half, kv ? p.k_gain : p.q_gain, turns[n]);
+        make_turn<J>(p, __ldg(p.positions + t0 + n), i - n * half, kv ? p.k_gain : p.q_gain, turns[n],
+                     kv ? &angles[n] : nullptr);
     }
-    if (kv) kv_rows<J, L>(p, t0, part, turns, scratch);
+    if (kv) kv_rows<J, L>(p, t0, part, turns, angles, scratch);
     else query_rows<J>(p, t0, part, turns[0]);
 }
 
@@ -572,12 +635,21 @@ cudaError_t launch_kv_rope_append(const RopeCall &call, const gq4_kv_cache &c, c
     p.page_sz = (uint32_t)(c.page_size * (c.head_dim / c.group_size) * 8);
     const int per = 32 / (c.head_dim / 8);
     p.units = (c.kv_heads + per - 1) / per;
-    // few tokens: their rows over several CTAs, until the GPU has two each
-    const bool few = call.T < 2 * 152;
-    auto parts = [&](int rows) { return few ? (rows + kRopeAppendWarps - 1) / kRopeAppendWarps : 1; };
-    p.q_parts = parts(c.head_dim == 64 ? (p.q_heads + 1) / 2 : p.q_heads);
-    p.kv_tokens = few ? 1 : kRopeTokens;
-    p.kv_parts = parts(2 * p.units);
+    // Few tokens: a token's rows of keys and values, and of queries, over several
+    // CTAs, until there are 8 of them, and one, per SM.  One token per CTA where
+    // that is a unit for each warp, up to 32 per SM; beyond, the table's making is
+    // shared.  us, group 64 (tokens per CTA / CTAs per such): 32 over 8 heads, 1000
+    // tokens 11.3 (1/1) and 12.0 (2/1), 16381 122.1 and 118.7; 32 over 32, 500
+    // tokens 14.3 (1/3), 16.0 (1/1) and 16.7 (2/1), 4000 65.1 (1/1) and 67.9 (2/1);
+    // 14 over 2, 1000 tokens 7.9 (1/1) and 7.5 (2/1).
+    auto parts = [](int rows, int ctas, int enough) {
+        int n = 1;
+        while (n * kRopeAppendWarps < rows && (long long)n * ctas < enough) ++n;
+        return n;
+    };
+    p.kv_tokens = 2 * p.units >= kRopeAppendWarps && call.T <= 32 * 152 ? 1 : kRopeTokens;
+    p.kv_parts = parts(2 * p.units * p.kv_tokens, (call.T + p.kv_tokens - 1) / p.kv_tokens, 8 * 152);
+    p.q_parts = parts(c.head_dim == 64 ? (p.q_heads + 1) / 2 : p.q_heads, call.T, 152);
     if ((long long)call.T * (p.q_parts + p.kv_parts) > 0x3fffffffll) return cudaErrorInvalidValue;
     p.q_ctas = call.heads[0] > 0 ? call.T * p.q_parts : 0;
     p.kv_ctas = (call.T + p.kv_tokens - 1) / p.kv_tokens * p.kv_parts;

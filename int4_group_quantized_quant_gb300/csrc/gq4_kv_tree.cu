@@ -186,7 +186,8 @@ __global__ void __launch_bounds__(kBookThreads) accept_book_kernel(const __grid_
         }
 #pragma unroll 1
         for (int i = 0; i < back; ++i) {
-            if (top + at + i < p.n_free) p.free_pages[top + at + i] = __ldg(p.page_table + (size_t)b * p.max_pages + had + i);
+            // (unsigned: counts that overflow, of tables that name pages over and over, lead nowhere)
+            if ((unsigned long long)(top + at + i) < (unsigned long long)p.n_free) p.free_pages[top + at + i] = __ldg(p.page_table + (size_t)b * p.max_pages + had + i);
             else atomicOr(&g_tree_error, kAcceptRefused);
         }
         before += all;

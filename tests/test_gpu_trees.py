@@ -64,6 +64,7 @@ APPENDS = [
     (50, 2, 2, 128, 32, 16, 0, False, True, True), (31, 1, 7, 96, 32, 16, 88, False, False, False),
     (401, 3, 2, 64, 64, 16, 64, False, True, True), (307, 0, 1, 256, 128, 32, 128, True, False, False),
     (305, 33, 17, 96, 96, 16, 48, False, False, True), (3, 200, 65, 64, 32, 16, 64, False, True, True),
+    (4999, 2, 8, 128, 64, 16, 128, True, False, True),
 ]
 
 
@@ -89,12 +90,25 @@ def test_rope_append(gq4, T, H, KH, D, gs, page, rot, inter, qn, kn):
     check_rows(gq4, q, k, v, pos, inv, slots, cache, gs, page, qg, kg, inter, host(qr) if H else None)
 
 
-@pytest.mark.parametrize("D,gs,rot,inter,norm", [(128, 128, 128, False, False), (128, 32, 128, False, True), (64, 64, 32, True, False),
-                                            (96, 96, 96, False, False), (256, 64, 128, True, True)])
+BORDER = [(128, 128, 128, False, False), (128, 32, 128, False, True), (64, 64, 32, True, False), (96, 96, 96, False, False),
+          (256, 64, 128, True, True)]
+
+
+@pytest.mark.parametrize("D,gs,rot,inter,norm", BORDER)
 def test_keys_next_to_a_border(gq4, D, gs, rot, inter, norm):
     """Keys whose rotated values lie on the borders of two codes but for the roundings of their inputs: each code is
     that of the value in 64 bits."""
-    T, KH, page = 200, 2, 16
+    keys_next_to_a_border(gq4, D, gs, rot, inter, norm, 0, 2)
+
+
+@pytest.mark.parametrize("power", [-100, -51, -49, 49, 51, 100])
+@pytest.mark.parametrize("D,gs,rot,inter,norm", [c for c in BORDER if not c[4]])
+def test_keys_next_to_a_border_of_any_size(gq4, D, gs, rot, inter, norm, power):
+    keys_next_to_a_border(gq4, D, gs, rot, inter, norm, power, 5)
+
+
+def keys_next_to_a_border(gq4, D, gs, rot, inter, norm, power, KH):
+    T, page = 200, 16
     g = I.rng(2501, D, gs, rot)
     inv = inv_freq(rot)
     pos = g.integers(0, 50000, T).astype(np.int32)
@@ -108,7 +122,7 @@ def test_keys_next_to_a_border(gq4, D, gs, rot, inter, norm):
     c, s = np.cos(ang)[:, None], np.sin(ang)[:, None]
     a, b = (slice(0, rot, 2), slice(1, rot, 2)) if inter else (slice(0, half), slice(half, rot))
     x[..., a], x[..., b] = y[..., a] * c + y[..., b] * s, y[..., b] * c - y[..., a] * s
-    k = (x / (gain if norm else 1.0)).astype(np.float32)
+    k = (x / (gain if norm else 1.0) * 2.0 ** power).astype(np.float32)
     v = g.standard_normal((T, KH, D)).astype(np.float32)
     slots = g.permutation(T + 8)[:T].astype(np.int32)
     cache = gq4.kv_cache((T + 8) // page, KH, page, D, gs)
