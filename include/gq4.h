@@ -464,8 +464,8 @@ GQ4_API gq4_status gq4_kv_append(int T, const gq4_kv_cache *cache, const float *
  * it.  rope, positions, q and q_out as there (q_heads 0: no queries; q_out may
  * be q with the same ld; rows of skipped slots are rotated all the same; any
  * number of query heads goes with any of the cache's), k, v and slots as here.
- * A code is that of the key's value in 64 bits (the angle's 64-bit product
- * among them) rounded once to f32, whatever the order of its f32 operations;
+ * A code is that of the key's value (the angle a 64-bit product; exact to 2^-44
+ * of its pair) rounded once to f32, whatever the order of its f32 operations;
  * scales and zeros are f32's.  So of the two calls' results some codes next to a
  * border and scales' last bits may differ. */
 GQ4_API gq4_status gq4_kv_rope_append(int T, int q_heads, const gq4_kv_cache *cache,

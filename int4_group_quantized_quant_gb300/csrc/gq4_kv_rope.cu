@@ -9,8 +9,9 @@
 // rotated keys' way to HBM and back (8 bytes per value of k).  Floor: 8 bytes
 // per value of q, 4 read and 0.5 + 8/gs written per value of k and v.  16381
 // tokens, 32 + 8 heads of 128: 118 us, 692 MB at 5.9 TB/s (0.86 of a copy's;
-// normalised 128; the two calls 138 and 147), of which exact_values is 10; 61
-// tokens 5.7 us, of which it is 2.
+// normalised 127; the two calls 138 and 146), of which the codes' check and
+// exact_values are 10; 61 tokens 5.1 us (5.4), of which they are 1.5.  Where the
+// queries are few the two calls are as fast: 8 + 8 heads 81 (80), 14 + 2 65 (60).
 //
 // Two kinds of CTAs take turns in the grid, so that the queries', which wait for
 // HBM, and the keys', which are bound by instructions, share an SM.  A CTA of
@@ -24,14 +25,15 @@
 // registers a thread and 8 CTAs per SM, at the price of a few spills: 5 CTAs take
 // 134 us.
 //
-// Codes next to a border.  A key's code is that of its value in 64 bits rounded
-// once to f32: so it does not depend on the order of sums and products.  The
+// Codes next to a border.  A key's code is that of its value (of the angle in 64
+// bits) rounded once to f32: so it does not depend on the order of sums and products.  The
 // rotation itself is f32; what it leaves of a key is off by at most key_error
 // (|a| + |b|) for the pair (a, b) before the rotation.  Where that could turn a
 // code's rounding -- a value so near to the border of two codes -- the warp
 // computes its rows again, the values next to a border and next to the group's
-// two ends in 64 bits (exact_values).  With groups of 128 normal values that is
-// one warp's 256 values in 100.
+// two ends in twice 24 bits (exact_values).  With groups of 128 normal values that
+// is one warp's 256 values in 100.  (All of it in 64 bits: 61 tokens 5.7 us.  Set
+// aside until the CTA's other rows are written: 120 and 6.9 us.)
 #include <cstdint>
 
 #include "gq4_kv_internal.h"
@@ -48,7 +50,7 @@ constexpr int kRopeTokens = 2;         // tokens of a CTA of keys and values, at
 
 // A rotated value's error relative to |a| + |b|, in units of 2^-24 (a rounding):
 // the angle's rounding 1, the sine and cosine 2, the products and their sum 2,
-// and 1 that the value in 64 bits is rounded by; with a norm the gain 1 and the
+// and 1 that the exact value is rounded by; with a norm the gain 1 and the
 // factor that the row shares 1 (its own error is the same for all of the row and
 // moves no code).
 __device__ __forceinline__ float key_error(bool norm)
@@ -560,7 +562,7 @@ __device__ __forceinline__ void kv_rows(const RopeAppendParams &p, int t0, int p
             if (!exact) {
                 const float largest = g.largest(w, lane), slack = code_slack(largest, g.m, p.k_gain != nullptr);
                 if (__any_sync(0xffffffffu, !(far <= 0.5f - slack) && row.live && !g.bad)) {
-                    // once more with the values that count in 64 bits (a group that is not finite stays so)
+                    // once more with the values that count as they are (a group that is not finite stays so)
                     float4 *at = reinterpret_cast<float4 *>(scratch[warp] + 8 * lane);
                     at[0] = a[0];
                     at[1] = a[1];
