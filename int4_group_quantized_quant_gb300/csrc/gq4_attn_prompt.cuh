@@ -798,9 +798,10 @@ __device__ __noinline__ void walk_on(const AttnCall &a)
     walk.more = 0;
     if (walk.pos >= walk.end) return;
     TreeWork w = tree_work<EXACT>(a, walk.at_req);
-    while (walk.unit >= w.units) {          // the next request with work (there is one)
+    while (walk.unit >= w.units) {          // the next request with work
         walk.unit = 0;
-        w = tree_work<EXACT>(a, ++walk.at_req);
+        if (++walk.at_req >= a.B) return;   // (there is one, unless lengths were written meanwhile)
+        w = tree_work<EXACT>(a, walk.at_req);
     }
     const int off = walk.off, upto = (int)min((long long)w.length, off + (walk.end - walk.pos));
     const int from = max(off - kStart, 0);
@@ -834,6 +835,7 @@ template <bool EXACT>
 __device__ __noinline__ bool walk_start(const AttnCall &a)
 {
     if (threadIdx.x == 0) {
+        walk.pos = walk.end = 0;
         a.cut[blockIdx.x] = make_int4(0, 0, 0, -1);
         no_marks(a.apart[a.n_units + 2 * blockIdx.x]);
         no_marks(a.apart[a.n_units + 2 * blockIdx.x + 1]);
