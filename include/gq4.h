@@ -619,11 +619,23 @@ GQ4_API gq4_status gq4_kv_attention_masked(int B, int T, int q_heads, int max_pa
  * request with a parent that is none, more than 32 * tree_words nodes, more
  * nodes than seq_len or rows not within T is refused: its rows inside T get
  * position 0 and no bits, and device error bit 10 is set.  Rows of no request
- * are left as they were. */
+ * are left as they were.
+ *
+ * A request that gq4_kv_plan refused keeps its length, which counts none of its
+ * rows: gq4_kv_tree, which does not know, takes its last tokens for them.
+ * gq4_kv_tree_planned is the call for steps in which that may happen (a pool
+ * that runs dry): slots [T] as gq4_kv_plan wrote them, where a request whose
+ * first row has a negative slot has no new tokens.  Its rows get position 0 and
+ * no bits, its parents are not looked at and no bit is set (bit 7 is). */
 GQ4_API gq4_status gq4_kv_tree(int B, int T, int tree_words, int window, int sinks,
                                const int32_t *parents, const int32_t *query_start,
                                const int32_t *seq_lens, int32_t *positions, uint32_t *tree,
                                cudaStream_t stream);
+
+GQ4_API gq4_status gq4_kv_tree_planned(int B, int T, int tree_words, int window, int sinks,
+                                       const int32_t *parents, const int32_t *slots,
+                                       const int32_t *query_start, const int32_t *seq_lens,
+                                       int32_t *positions, uint32_t *tree, cudaStream_t stream);
 
 /* After the verification: of request b's n new tokens, counts[b] are accepted,
  * the nodes path[b][0 .. counts[b] - 1] (int32 [B][max_path], rising).  The
@@ -645,6 +657,14 @@ GQ4_API gq4_status gq4_kv_tree(int B, int T, int tree_words, int window, int sin
  * is set; free_count is cut to 0 .. n_free.  No two requests of a call may have
  * new tokens in the same page.
  *
+ * Requests that gq4_kv_plan refused: gq4_kv_accept does not know of them, and
+ * would take the last n of such a request's own tokens for its new ones, and
+ * take all but counts[b] of them away.  So it is for steps of which none was
+ * refused (bit 7 is not set); gq4_kv_accept_planned is for all: slots [T] as
+ * gq4_kv_plan wrote them, where a request whose first row has a negative slot
+ * has no new tokens.  Its length, rows and pages stay, its count and path are
+ * not looked at, and no bit is set.  (Rows that are not within T: refused.)
+ *
  * workspace: gq4_kv_accept_workspace_bytes(B) bytes of device memory, 256-byte
  * aligned, as in gq4_kv_attention. */
 GQ4_API size_t gq4_kv_accept_workspace_bytes(int B);
@@ -656,6 +676,15 @@ GQ4_API gq4_status gq4_kv_accept(int B, int max_path, int max_pages, int n_free,
                                  int32_t *free_pages, const int32_t *free_count,
                                  int32_t *free_count_out, int32_t *seq_lens_out, void *workspace,
                                  size_t workspace_bytes, cudaStream_t stream);
+
+GQ4_API gq4_status gq4_kv_accept_planned(int B, int T, int max_path, int max_pages, int n_free,
+                                         const gq4_kv_cache *cache, const int32_t *path,
+                                         const int32_t *counts, const int32_t *slots,
+                                         const int32_t *query_start, const int32_t *seq_lens,
+                                         const int32_t *page_table, int32_t *free_pages,
+                                         const int32_t *free_count, int32_t *free_count_out,
+                                         int32_t *seq_lens_out, void *workspace,
+                                         size_t workspace_bytes, cudaStream_t stream);
 
 /* Integer unpack test kernel: q[n*K + k] = q(n,k) as u8 [N][K].
  * Uses the same in-register extraction as the matvec kernels.

@@ -132,6 +132,98 @@ gq4_status attention(int B, int T, int q_heads, int max_pages, int max_query, in
     return status_of(gq4::launch_attn(c, stream));
 }
 
+// Both forms of the tree's bits and of accepting a path; slots: as planned
+// (gq4_kv_tree_planned, gq4_kv_accept_planned).
+gq4_status kv_tree(bool planned, int B, int T, int tree_words, int window, int sinks, const int32_t *parents,
+                   const int32_t *slots, const int32_t *query_start, const int32_t *seq_lens, int32_t *positions,
+                   uint32_t *tree, cudaStream_t stream)
+{
+    if (B < 1 || B > GQ4_MAX_REQUESTS || T < 0 || tree_words < 1 || tree_words > GQ4_MAX_TREE_WORDS ||
+        window < 0 || sinks < 0)
+        return GQ4_ERR_INVALID_ARG;
+    if (T == 0) return GQ4_OK;
+    if (!parents || !query_start || !seq_lens || !positions || !tree || (planned && !slots)) return GQ4_ERR_INVALID_ARG;
+    const void *all[] = {parents, slots, query_start, seq_lens, positions, tree};
+    for (const void *p : all)
+        if (!aligned(p, 4)) return GQ4_ERR_MISALIGNED;
+    RangeSet rs;
+    rs.input(parents, (size_t)T * 4);
+    rs.input(slots, (size_t)T * 4);
+    rs.input(query_start, ((size_t)B + 1) * 4);
+    rs.input(seq_lens, (size_t)B * 4);
+    rs.output(positions, (size_t)T * 4);
+    rs.output(tree, (size_t)T * tree_words * 4);
+    if (!rs.disjoint()) return GQ4_ERR_ALIAS;
+    gq4::TreeCall c{};
+    c.B = B;
+    c.T = T;
+    c.words = tree_words;
+    c.window = window;
+    c.sinks = sinks;
+    c.parents = parents;
+    c.slots = slots;
+    c.query_start = query_start;
+    c.seq_lens = seq_lens;
+    c.positions = positions;
+    c.bits = tree;
+    return status_of(gq4::launch_kv_tree(c, stream));
+}
+
+// (T < 0: without slots)
+gq4_status kv_accept(int B, int T, int max_path, int max_pages, int n_free, const gq4_kv_cache *cache, const int32_t *path,
+                     const int32_t *counts, const int32_t *slots, const int32_t *query_start, const int32_t *seq_lens,
+                     const int32_t *page_table, int32_t *free_pages, const int32_t *free_count, int32_t *free_count_out,
+                     int32_t *seq_lens_out, void *workspace, size_t workspace_bytes, cudaStream_t stream)
+{
+    if (B < 1 || B > GQ4_MAX_REQUESTS || max_path < 0 || max_pages < 1 || n_free < 0)
+        return GQ4_ERR_INVALID_ARG;
+    GQ4_TRY(check_cache(cache));
+    if ((long long)max_pages * cache->page_size > kMaxKeys) return GQ4_ERR_INVALID_ARG;
+    if (!counts || !query_start || !seq_lens || !page_table || !free_count || !free_count_out || !seq_lens_out ||
+        (n_free > 0 && !free_pages) || (T > 0 && !slots))
+        return GQ4_ERR_INVALID_ARG;
+    const void *all[] = {path, counts, slots, query_start, seq_lens, page_table, free_pages, free_count, free_count_out,
+                         seq_lens_out};
+    for (const void *p : all)
+        if (!aligned(p, 4)) return GQ4_ERR_MISALIGNED;
+    const size_t need = gq4_kv_accept_workspace_bytes(B), b = (size_t)B * 4;
+    if (!workspace || workspace_bytes < need) return GQ4_ERR_INVALID_ARG;
+    if (!aligned(workspace, 256)) return GQ4_ERR_MISALIGNED;
+    RangeSet rs;
+    cache_ranges(cache, true, rs);
+    rs.input(path, b * (size_t)max_path);
+    rs.input(counts, b);
+    if (T > 0) rs.input(slots, (size_t)T * 4);
+    rs.input(query_start, b + 4);
+    if (seq_lens_out != seq_lens) rs.input(seq_lens, b);
+    rs.input(page_table, b * (size_t)max_pages);
+    if (free_count_out != free_count) rs.input(free_count, 4);
+    rs.output(free_pages, (size_t)n_free * 4);
+    rs.output(free_count_out, 4);
+    rs.output(seq_lens_out, b);
+    rs.output(workspace, need);
+    if (!rs.disjoint()) return GQ4_ERR_ALIAS;
+    gq4::AcceptCall c{};
+    c.B = B;
+    c.T = T;
+    c.max_path = max_path;
+    c.max_pages = max_pages;
+    c.n_free = n_free;
+    c.c = *cache;
+    c.path = path;
+    c.counts = counts;
+    c.slots = slots;
+    c.query_start = query_start;
+    c.seq_lens = seq_lens;
+    c.page_table = page_table;
+    c.free_count = free_count;
+    c.free_pages = free_pages;
+    c.free_count_out = free_count_out;
+    c.seq_lens_out = seq_lens_out;
+    c.verdict = static_cast<int32_t *>(workspace);
+    return status_of(gq4::launch_kv_accept(c, stream));
+}
+
 }  // namespace
 
 extern "C" {
@@ -342,33 +434,14 @@ gq4_status gq4_kv_tree(int B, int T, int tree_words, int window, int sinks, cons
                        const int32_t *query_start, const int32_t *seq_lens, int32_t *positions,
                        uint32_t *tree, cudaStream_t stream)
 {
-    if (B < 1 || B > GQ4_MAX_REQUESTS || T < 0 || tree_words < 1 || tree_words > GQ4_MAX_TREE_WORDS ||
-        window < 0 || sinks < 0)
-        return GQ4_ERR_INVALID_ARG;
-    if (T == 0) return GQ4_OK;
-    if (!parents || !query_start || !seq_lens || !positions || !tree) return GQ4_ERR_INVALID_ARG;
-    const void *all[] = {parents, query_start, seq_lens, positions, tree};
-    for (const void *p : all)
-        if (!aligned(p, 4)) return GQ4_ERR_MISALIGNED;
-    RangeSet rs;
-    rs.input(parents, (size_t)T * 4);
-    rs.input(query_start, ((size_t)B + 1) * 4);
-    rs.input(seq_lens, (size_t)B * 4);
-    rs.output(positions, (size_t)T * 4);
-    rs.output(tree, (size_t)T * tree_words * 4);
-    if (!rs.disjoint()) return GQ4_ERR_ALIAS;
-    gq4::TreeCall c{};
-    c.B = B;
-    c.T = T;
-    c.words = tree_words;
-    c.window = window;
-    c.sinks = sinks;
-    c.parents = parents;
-    c.query_start = query_start;
-    c.seq_lens = seq_lens;
-    c.positions = positions;
-    c.bits = tree;
-    return status_of(gq4::launch_kv_tree(c, stream));
+    return kv_tree(false, B, T, tree_words, window, sinks, parents, nullptr, query_start, seq_lens, positions, tree, stream);
+}
+
+gq4_status gq4_kv_tree_planned(int B, int T, int tree_words, int window, int sinks, const int32_t *parents,
+                               const int32_t *slots, const int32_t *query_start, const int32_t *seq_lens,
+                               int32_t *positions, uint32_t *tree, cudaStream_t stream)
+{
+    return kv_tree(true, B, T, tree_words, window, sinks, parents, slots, query_start, seq_lens, positions, tree, stream);
 }
 
 size_t gq4_kv_accept_workspace_bytes(int B)
@@ -382,50 +455,19 @@ gq4_status gq4_kv_accept(int B, int max_path, int max_pages, int n_free, const g
                          const int32_t *free_count, int32_t *free_count_out, int32_t *seq_lens_out,
                          void *workspace, size_t workspace_bytes, cudaStream_t stream)
 {
-    if (B < 1 || B > GQ4_MAX_REQUESTS || max_path < 0 || max_pages < 1 || n_free < 0)
-        return GQ4_ERR_INVALID_ARG;
-    GQ4_TRY(check_cache(cache));
-    if ((long long)max_pages * cache->page_size > kMaxKeys) return GQ4_ERR_INVALID_ARG;
-    if (!counts || !query_start || !seq_lens || !page_table || !free_count || !free_count_out || !seq_lens_out ||
-        (n_free > 0 && !free_pages))
-        return GQ4_ERR_INVALID_ARG;
-    const void *all[] = {path, counts, query_start, seq_lens, page_table, free_pages, free_count, free_count_out,
-                         seq_lens_out};
-    for (const void *p : all)
-        if (!aligned(p, 4)) return GQ4_ERR_MISALIGNED;
-    const size_t need = gq4_kv_accept_workspace_bytes(B), b = (size_t)B * 4;
-    if (!workspace || workspace_bytes < need) return GQ4_ERR_INVALID_ARG;
-    if (!aligned(workspace, 256)) return GQ4_ERR_MISALIGNED;
-    RangeSet rs;
-    cache_ranges(cache, true, rs);
-    rs.input(path, b * (size_t)max_path);
-    rs.input(counts, b);
-    rs.input(query_start, b + 4);
-    if (seq_lens_out != seq_lens) rs.input(seq_lens, b);
-    rs.input(page_table, b * (size_t)max_pages);
-    if (free_count_out != free_count) rs.input(free_count, 4);
-    rs.output(free_pages, (size_t)n_free * 4);
-    rs.output(free_count_out, 4);
-    rs.output(seq_lens_out, b);
-    rs.output(workspace, need);
-    if (!rs.disjoint()) return GQ4_ERR_ALIAS;
-    gq4::AcceptCall c{};
-    c.B = B;
-    c.max_path = max_path;
-    c.max_pages = max_pages;
-    c.n_free = n_free;
-    c.c = *cache;
-    c.path = path;
-    c.counts = counts;
-    c.query_start = query_start;
-    c.seq_lens = seq_lens;
-    c.page_table = page_table;
-    c.free_count = free_count;
-    c.free_pages = free_pages;
-    c.free_count_out = free_count_out;
-    c.seq_lens_out = seq_lens_out;
-    c.verdict = static_cast<int32_t *>(workspace);
-    return status_of(gq4::launch_kv_accept(c, stream));
+    return kv_accept(B, -1, max_path, max_pages, n_free, cache, path, counts, nullptr, query_start, seq_lens, page_table,
+                     free_pages, free_count, free_count_out, seq_lens_out, workspace, workspace_bytes, stream);
+}
+
+gq4_status gq4_kv_accept_planned(int B, int T, int max_path, int max_pages, int n_free, const gq4_kv_cache *cache,
+                                 const int32_t *path, const int32_t *counts, const int32_t *slots,
+                                 const int32_t *query_start, const int32_t *seq_lens, const int32_t *page_table,
+                                 int32_t *free_pages, const int32_t *free_count, int32_t *free_count_out,
+                                 int32_t *seq_lens_out, void *workspace, size_t workspace_bytes, cudaStream_t stream)
+{
+    if (T < 0) return GQ4_ERR_INVALID_ARG;
+    return kv_accept(B, T, max_path, max_pages, n_free, cache, path, counts, slots, query_start, seq_lens, page_table,
+                     free_pages, free_count, free_count_out, seq_lens_out, workspace, workspace_bytes, stream);
 }
 
 size_t gq4_kv_attention_workspace_bytes(int T, int q_heads, int kv_heads, int head_dim)

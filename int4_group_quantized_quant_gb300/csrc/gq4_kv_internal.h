@@ -42,15 +42,15 @@ cudaError_t read_kv_rope_device_error(unsigned int *bits, bool clear);
 // Drafted trees: their bits, and accepting a path.
 struct TreeCall {
     int B, T, words, window, sinks;
-    const int32_t *parents, *query_start, *seq_lens;
+    const int32_t *parents, *slots, *query_start, *seq_lens;   // slots: as planned, or NULL
     int32_t *positions;
     uint32_t *bits;
 };
 cudaError_t launch_kv_tree(const TreeCall &call, cudaStream_t stream);
 struct AcceptCall {
-    int B, max_path, max_pages, n_free;
+    int B, T, max_path, max_pages, n_free;   // T: of slots, -1: there are none
     gq4_kv_cache c;
-    const int32_t *path, *counts, *query_start, *seq_lens, *page_table, *free_count;
+    const int32_t *path, *counts, *slots, *query_start, *seq_lens, *page_table, *free_count;
     int32_t *free_pages, *free_count_out, *seq_lens_out;
     int32_t *verdict;   // [B] of the workspace: how many rows, -1: refused
 };

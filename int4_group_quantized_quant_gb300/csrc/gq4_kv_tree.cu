@@ -14,6 +14,14 @@ __device__ unsigned int g_tree_error = 0;
 constexpr unsigned int kTreeRefused = 1u << 10, kAcceptRefused = 1u << 11;
 constexpr int kMaxNodes = 32 * GQ4_MAX_TREE_WORDS;
 
+// Whether the planning refused a request: its rows from q0 on, if there are any,
+// got no slots, and it has no new tokens though its length counts none.  slots:
+// as planned, or NULL (none was refused).
+__device__ __forceinline__ bool plan_refused(const int32_t *slots, int T, int q0, long long rows)
+{
+    return slots && rows > 0 && q0 >= 0 && q0 < T && __ldg(slots + q0) < 0;
+}
+
 // ---------------------------------------------------------------------------
 // A CTA per request, its parents in shared memory, a thread per node that walks
 // up to its root twice: for its depth, and for the bits.  A parent comes before
@@ -27,14 +35,15 @@ __global__ void __launch_bounds__(kMaxNodes) tree_kernel(const __grid_constant__
     const int b = blockIdx.x, i = threadIdx.x;
     const int q0 = __ldg(p.query_start + b), q1 = __ldg(p.query_start + b + 1), len = __ldg(p.seq_lens + b);
     const long long n = (long long)q1 - q0, past = len - n;
-    bool bad = n < 0 || n > 32 * p.words || q0 < 0 || q1 > p.T || len < 0 || past < 0;
+    const bool none = plan_refused(p.slots, p.T, q0, n);
+    bool bad = none || n < 0 || n > 32 * p.words || q0 < 0 || q1 > p.T || len < 0 || past < 0;
     if (!bad && i < n) {
         const int parent = __ldg(p.parents + q0 + i);
         bad = parent < -1 || parent >= i;
         up[i] = (int16_t)parent;
     }
     if (__syncthreads_or(bad)) {
-        if (i == 0 && n != 0) atomicOr(&g_tree_error, kTreeRefused);
+        if (i == 0 && n != 0 && !none) atomicOr(&g_tree_error, kTreeRefused);
         for (long long row = max(q0, 0) + i; row < min(q1, p.T); row += blockDim.x) {
             p.positions[row] = 0;
             for (int w = 0; w < p.words; ++w) p.bits[row * p.words + w] = 0u;
@@ -73,14 +82,17 @@ constexpr int kPathTile = 256;
 // A request's rows, and whether they can be (before its path is looked at).
 struct Drafted {
     int past, n, len;
-    bool bad;
+    bool none, bad;        // none: the planning refused it, all of its tokens stay
 
     __device__ __forceinline__ Drafted(const AcceptCall &p, int b, int shift)
     {
-        const long long rows = (long long)__ldg(p.query_start + b + 1) - __ldg(p.query_start + b);
+        const int q0 = __ldg(p.query_start + b), q1 = __ldg(p.query_start + b + 1);
+        const long long rows = (long long)q1 - q0;
         len = __ldg(p.seq_lens + b);
-        bad = rows < 0 || rows > len || (long long)len > ((long long)p.max_pages << shift);
-        n = bad ? 0 : (int)rows;
+        none = plan_refused(p.slots, p.T, q0, rows);
+        bad = !none && (rows < 0 || rows > len || (long long)len > ((long long)p.max_pages << shift) ||
+                        (p.T >= 0 && rows > 0 && (q0 < 0 || q1 > p.T)));
+        n = none || bad ? 0 : (int)rows;
         past = len - n;
     }
 };
@@ -91,7 +103,7 @@ __global__ void __launch_bounds__(kMoveThreads) accept_move_kernel(const __grid_
     const int b = blockIdx.x;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const Drafted r(p, b, shift);
-    const int count = __ldg(p.counts + b);
+    const int count = r.none ? 0 : __ldg(p.counts + b);
     const int32_t *path = p.path ? p.path + (size_t)b * p.max_path : nullptr;
     const int32_t *table = p.page_table + (size_t)b * p.max_pages;
     bool bad = r.bad || count < 0 || count > r.n || (path && count > p.max_path);

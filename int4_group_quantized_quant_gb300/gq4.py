@@ -98,8 +98,11 @@ _SIGS = {
     "gq4_kv_append": [_i, _CacheP, _vp, _i, _vp, _i, _vp, _vp],
     "gq4_kv_rope_append": [_i, _i, _CacheP, _RopeP, _vp, _vp, _i, _vp, _i, _vp, _i, _vp, _i, _vp, _vp],
     "gq4_kv_tree": [_i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp],
+    "gq4_kv_tree_planned": [_i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp],
     "gq4_kv_accept": [_i, _i, _i, _i, _CacheP, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t,
                       _vp],
+    "gq4_kv_accept_planned": [_i, _i, _i, _i, _i, _CacheP, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                              ctypes.c_size_t, _vp],
     "gq4_kv_gather": [_i, _CacheP, _vp, _vp, _vp, _vp],
     "gq4_kv_plan": [_i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp],
     "gq4_kv_attention": [_i, _i, _i, _i, _i, _i, _CacheP, _vp, _i, _vp, _vp, _vp, ctypes.c_float, _i,
@@ -719,10 +722,11 @@ def kv_attention(q, query_start, seq_lens, page_table, Kq, K_sz, Vq, V_sz, group
     return out
 
 
-def kv_tree(parents, query_start, seq_lens, words, window=0, sinks=0, positions=None, tree=None, stream=None):
+def kv_tree(parents, query_start, seq_lens, words, window=0, sinks=0, positions=None, tree=None, stream=None, slots=None):
     """(positions int32 [T], tree int32 [T, words]) of drafted trees from their parents int32 [T], the node of
     its request that each follows, -1 the request's last token (gq4_kv_tree), as kv_attention takes them.
-    Rows of no request are left as they were."""
+    Rows of no request are left as they were.  ``slots`` int32 [T], as kv_plan gave them: a request that it
+    refused has no nodes (gq4_kv_tree_planned); without them no request may have been refused."""
     index = _device(parents, "parents")
     T = parents.numel()
     _device(seq_lens, "seq_lens")
@@ -740,17 +744,24 @@ def kv_tree(parents, query_start, seq_lens, words, window=0, sinks=0, positions=
         made.append(tree)
     if stream is not None:
         _lend(stream, index, *made)
-    _call(lib.gq4_kv_tree, "gq4_kv_tree", index, stream, B, T, words, window, sinks, at_parents, at_start, at_lens,
-          _at(positions, "positions", _i32, (T,), index), _at(tree, "tree", _i32, (T, words), index))
+    at_out = _at(positions, "positions", _i32, (T,), index), _at(tree, "tree", _i32, (T, words), index)
+    if slots is None:
+        _call(lib.gq4_kv_tree, "gq4_kv_tree", index, stream, B, T, words, window, sinks, at_parents, at_start, at_lens,
+              *at_out)
+    else:
+        _call(lib.gq4_kv_tree_planned, "gq4_kv_tree_planned", index, stream, B, T, words, window, sinks, at_parents,
+              _at(slots, "slots", _i32, (T,), index), at_start, at_lens, *at_out)
     return positions, tree
 
 
 def kv_accept(path, counts, query_start, seq_lens, page_table, free_pages, free_count, Kq, K_sz, Vq, V_sz, group_size,
-              seq_lens_out=None, free_count_out=None, workspace=None, stream=None):
+              seq_lens_out=None, free_count_out=None, workspace=None, stream=None, slots=None):
     """After a verification (gq4_kv_accept): the cache's rows of the accepted nodes path int32 [B, max_path] (the
     first counts int32 [B] of each row; None: the first new tokens) move to the end of their request, and pages
     left over go back on free_pages.  Returns (seq_lens_out, free_count_out); pass seq_lens_out=seq_lens and
-    free_count_out=free_count to advance them in place."""
+    free_count_out=free_count to advance them in place.  ``slots`` int32 [T], as kv_plan gave them: a request that
+    it refused stays as it is (gq4_kv_accept_planned).  Without them no request of the step may have been refused:
+    one that was would lose tokens that it had before."""
     c, index = _cache(Kq, K_sz, Vq, V_sz, group_size)
     _device(seq_lens, "seq_lens")
     B, width, n_free = seq_lens.numel(), _width(page_table), free_pages.numel()
@@ -766,6 +777,11 @@ def kv_accept(path, counts, query_start, seq_lens, page_table, free_pages, free_
         at_path = _at(path, "path", _i32, (B, most), index)
         if most == 0:
             raise ValueError("path has no columns")
+    T, at_slots = 0, None
+    if slots is not None:
+        _device(slots, "slots")
+        T = slots.numel()
+        at_slots = _at(slots, "slots", _i32, (T,), index)
     need = lib.gq4_kv_accept_workspace_bytes(B)
     # what is not given is a stretch of one allocation, the workspace first
     at_len_out = None if seq_lens_out is None else _at(seq_lens_out, "seq_lens_out", _i32, (B,), index)
@@ -786,8 +802,12 @@ def kv_accept(path, counts, query_start, seq_lens, page_table, free_pages, free_
         if not (isinstance(workspace, torch.Tensor) and workspace.get_device() == index and workspace.is_contiguous()):
             raise ValueError("workspace must be a contiguous CUDA tensor on the others' device")
         at_work, work = workspace.data_ptr(), workspace.nbytes
-    _call(lib.gq4_kv_accept, "gq4_kv_accept", index, stream, B, most, width, n_free, c, at_path, at_counts, at_start,
-          at_lens, at_table, at_free, at_count, at_count_out, at_len_out, at_work, work)
+    if slots is None:
+        _call(lib.gq4_kv_accept, "gq4_kv_accept", index, stream, B, most, width, n_free, c, at_path, at_counts, at_start,
+              at_lens, at_table, at_free, at_count, at_count_out, at_len_out, at_work, work)
+    else:
+        _call(lib.gq4_kv_accept_planned, "gq4_kv_accept_planned", index, stream, B, T, most, width, n_free, c, at_path,
+              at_counts, at_slots, at_start, at_lens, at_table, at_free, at_count, at_count_out, at_len_out, at_work, work)
     return seq_lens_out, free_count_out
 
 
