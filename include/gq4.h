@@ -467,7 +467,9 @@ GQ4_API gq4_status gq4_kv_append(int T, const gq4_kv_cache *cache, const float *
  * A code is that of the key's value (the angle a 64-bit product; exact to 2^-44
  * of its pair) rounded once to f32, whatever the order of its f32 operations;
  * scales and zeros are f32's.  So of the two calls' results some codes next to a
- * border and scales' last bits may differ. */
+ * border and scales' last bits may differ.  A key's norm is that of 64 bits where
+ * its mean square is not one of f32's (above 2^128; below 2^-100, without eps);
+ * queries there are as gq4_head_norm_rope's, 0 or not finite. */
 GQ4_API gq4_status gq4_kv_rope_append(int T, int q_heads, const gq4_kv_cache *cache,
                                       const gq4_rope *rope, const int32_t *positions, const float *q,
                                       int ldq, float *q_out, int ldq_out, const float *k, int ldk,

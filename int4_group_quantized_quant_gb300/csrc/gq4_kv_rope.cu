@@ -57,6 +57,9 @@ __device__ __forceinline__ float key_error(bool norm)
 {
     return norm ? 8 * 0x1p-24f : 6 * 0x1p-24f;
 }
+// Mean squares from here on, and with them the factor, are as exact as f32 sums
+// are: the squares that it rounds to multiples of 2^-149 are 2^-42 of the sum.
+constexpr float kLeastSquare = 0x1p-100f;
 // Of a code's argument (v - lo) r, up to 15, on either side: two roundings and r's two.
 constexpr float kCodeError = 8 * 15 * 0x1p-24f;
 
@@ -421,7 +424,8 @@ struct KvRow {
 // to a border of two codes and to their group's ends, in twice 24 bits; in 64
 // where the row's size would cost the former bits.  lo, hi, r32, slack, near: of
 // the lane's group, its ends, its factor and how far its arguments and values may
-// be off; largest: of its row; wanted: it has codes.  By the whole warp.
+// be off; largest: of its row; wanted: it has codes.  All values of a normalised
+// row whose squares f32 does not hold: it comes as NaN.  By the whole warp.
 template <int J>
 __device__ __noinline__ void exact_values(const RopeAppendParams &p, int t, int unit, bool wanted, float lo, float hi, float r32,
                                           float slack, float near, float largest, const Angles<J> &angles, float *v)
@@ -488,10 +492,15 @@ __device__ __noinline__ void exact_values(const RopeAppendParams &p, int t, int 
                 }
             }
             sum = fma(row_sum<WPR>(sum, w, lane), 1.0 / D, (double)p.eps);
-            factor = inv_sqrt((float)sum);
-            if (factor > 0.0 && factor < 1e30) {         // and two Newton steps
+            factor = inv_sqrt((float)sum);               // (of 0, infinite, NaN)
+            if (sum > 0.0 && sum < INFINITY) {
+                // of 1 .. 4, which f32 holds, with two Newton steps; the even power of two apart
+                const int e = (((__double2hiint(sum) >> 20) & 2047) - 1023) & ~1;
+                sum *= __hiloint2double((1023 - e) << 20, 0);
+                factor = inv_sqrt((float)sum);
                 factor = fma(fma(-0.5 * sum * factor, factor, 0.5), factor, factor);
                 factor = fma(fma(-0.5 * sum * factor, factor, 0.5), factor, factor);
+                factor *= __hiloint2double((1023 - e / 2) << 20, 0);
             }
         }
 #pragma unroll 1
@@ -543,7 +552,11 @@ __device__ __forceinline__ void kv_rows(const RopeAppendParams &p, int t0, int p
         if (slot < 0) continue;            // uniform in the warp
         if (!value) {
             float r = 1.0f;
-            if (p.k_gain) r = inv_sqrt(fmaf(row_sum<WPR>(square_sum(a[0]) + square_sum(a[1]), w, lane), p.inv_d, p.eps));
+            if (p.k_gain) {
+                // (squares that f32 does not hold: no number, which exact_values takes)
+                const float m = fmaf(row_sum<WPR>(square_sum(a[0]) + square_sum(a[1]), w, lane), p.inv_d, p.eps);
+                r = m >= kLeastSquare && m < INFINITY ? inv_sqrt(m) : __int_as_float(0x7fc00000);
+            }
 #pragma unroll
             for (int f = 0; f < 2; ++f) {
                 const int d = 8 * w + 4 * f;
@@ -561,12 +574,12 @@ __device__ __forceinline__ void kv_rows(const RopeAppendParams &p, int t0, int p
             const uint32_t code = code_word<true>(v, g.m, far);
             if (!exact) {
                 const float largest = g.largest(w, lane), slack = code_slack(largest, g.m, p.k_gain != nullptr);
-                if (__any_sync(0xffffffffu, !(far <= 0.5f - slack) && row.live && !g.bad)) {
-                    // once more with the values that count as they are (a group that is not finite stays so)
+                if (__any_sync(0xffffffffu, !(far <= 0.5f - slack) && row.live)) {
+                    // once more with the values that count as they are (without a norm a group that is not finite stays so)
                     float4 *at = reinterpret_cast<float4 *>(scratch[warp] + 8 * lane);
                     at[0] = a[0];
                     at[1] = a[1];
-                    exact_values<J>(p, t, unit, row.live && !g.bad, g.lo, g.hi, g.m.r, slack,
+                    exact_values<J>(p, t, unit, row.live && (p.k_gain || !g.bad), g.lo, g.hi, g.m.r, slack,
                                     4.0f * key_error(p.k_gain != nullptr) * largest, largest, angles[n], scratch[warp]);
                     a[0] = at[0];
                     a[1] = at[1];
