@@ -422,7 +422,7 @@ struct KvRow {
 
 // Of a unit of key rows, whose values are in v, a lane's 8 in place, those next
 // to a border of two codes and to their group's ends, in twice 24 bits; in 64
-// where the row's size would cost the former bits.  lo, hi, r32, slack, near: of
+// where the row's or the group's size would cost the former bits.  lo, hi, r32, slack, near: of
 // the lane's group, its ends, its factor and how far its arguments and values may
 // be off; largest: of its row; wanted: it has codes.  All values of a normalised
 // row whose squares f32 does not hold: it comes as NaN.  By the whole warp.
@@ -443,7 +443,9 @@ __device__ __noinline__ void exact_values(const RopeAppendParams &p, int t, int 
             if (!(fabsf(x - rintf(x)) <= 0.5f - slack) || v[i] <= lo + near || v[i] >= hi - near) need |= 1u << i;
         }
     }
-    bool sized = largest >= 0x1p-50f && largest <= 0x1p50f;
+    // (a small group beside larger ones loses its own second parts; one of zeros has none)
+    const float size = fmaxf(fabsf(lo), fabsf(hi));
+    bool sized = (size >= 0x1p-50f || size == 0.0f) && largest <= 0x1p50f;
     Two r = {1.0f, 0.0f};
     if (norm) {
         Two sum = {0.0f, 0.0f};

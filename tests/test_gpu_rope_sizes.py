@@ -103,3 +103,22 @@ def test_normalised_rows_of_huge_and_not_finite_values(gq4):
     y, size = R.norm_rope(k[[0, 4]], gain, 1e-6, pos[[0, 4]], inv, False)
     check(codes, sz, y, size, gs)
     assert np.array_equal(sz[1, 0], [[1, 0], [1, 0]]) and gq4.device_error(clear=True) == 0
+
+
+@pytest.mark.parametrize("norm", [False, True])
+def test_small_groups_next_to_a_border(gq4, norm):
+    """Groups of some 2^-60 to 2^-118 beside one of ordinary size: their codes are those of 64 bits as well."""
+    T, KH, D, gs = 400, 4, 128, 32
+    g = I.rng(2602, norm)
+    inv, pos = inv_freq(D), g.integers(0, 50000, T).astype(np.int32)
+    small = np.exp2([0.0, -60.0, -100.0, -118.0]).repeat(gs).astype(np.float32)
+    y = border_rows(g, T, KH, D, gs)
+    x = turned_back(y, pos, inv, True)     # (pairs of neighbours: of one group)
+    # by the row or by the gains
+    k, gain = (x.astype(np.float32), small) if norm else ((x * small).astype(np.float32), None)
+    codes, sz = append(gq4, k, pos, inv, True, gain, 1e-6, gs)
+    assert gq4.device_error(clear=True) == 0
+    y, _ = R.norm_rope(k, gain, 1e-6, pos, inv, True)
+    want, _ = R.quantise(y.astype(np.float32), gs)
+    wrong = (codes != want).reshape(T * KH, D // gs, gs).sum((0, 2))
+    assert wrong.tolist() == [0, 0, 0, 0]
