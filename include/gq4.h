@@ -715,7 +715,7 @@ GQ4_API gq4_status gq4_dequant(int K, int N, int group_size, const uint32_t *Bq,
  * gq4_kv_gather met a slot outside the pool, bit 7 when gq4_kv_plan refused
  * a request, bit 8 when gq4_kv_attention met a request outside its bounds or
  * a page outside the pool, bit 9 when its prompt kernel gave up waiting for
- * its own copies or MMAs, bit 10 when gq4_kv_tree and bit 11 when gq4_kv_accept
+ * its own copies or MMAs (rows that it does not vouch for are NaN), bit 10 when gq4_kv_tree and bit 11 when gq4_kv_accept
  * refused a request (or lost pages for want of room); bits 3 and 6 also cover
  * gq4_kv_rope_append, bits 8 and 9 gq4_kv_attention_masked.  Copies the word to
  * *bits (synchronous, device-wide) and clears it when clear != 0.  Not for

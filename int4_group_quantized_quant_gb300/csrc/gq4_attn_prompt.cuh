@@ -1604,6 +1604,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
     if (warp == W::kMma) tmem_dealloc(cta.tmem, kTmemCols);
     // (the request is read again: in registers for so long it costs the roles)
     if constexpr (MODE != kTree) write_marks(a.apart[blockIdx.x], cta.req, cta.tile);
+    else if (cta.abort && threadIdx.x == 0) a.cut[blockIdx.x].w = kUndone;   // (whatever is left of its share)
 }
 
 template <int J, int G, int DP, int MODE>

@@ -1116,8 +1116,37 @@ __global__ void __launch_bounds__(kThreads, MINB) attn_split_kernel(const __grid
 // CTAs of the last kernel for each row tile that the prompt kernel's CTAs share.
 constexpr int kPieceParts = 16;
 
+// A CTA of the prompt kernel gave up, and which row tiles it has left is not known
+// here: rows of all row tiles become NaN that are not joined (join_pieces looks at
+// each of those itself).  A part of the row tiles, by the whole CTA.
+__device__ __noinline__ void spoil_rows(const AttnCall &a, int part)
+{
+    const int R = a.heads / a.c.kv_heads, D = a.c.head_dim;
+    int at = 0;
+    for (int b = 0; b < a.B; ++b) {
+        const AttnRequest r = attn_request<true>(a, b);
+        if (!prompt_takes(a, r)) continue;
+        const int units = (r.n * R + kPromptTile - 1) / kPromptTile * a.c.kv_heads;
+        for (int u = 0; u < units; ++u) {
+            if (at++ % kPieceParts != part) continue;
+            const int tile = u / a.c.kv_heads, h = u - tile * a.c.kv_heads;
+            bool joined = false;
+            for (int c = threadIdx.x; c < a.tree_ctas; c += kJoinThreads) {
+                const int4 v = __ldcg(a.cut + c);
+                joined |= v.w >= 0 && v.x == b && v.y == tile && v.z == h;
+            }
+            if (__syncthreads_or(joined)) continue;
+            for (int i = threadIdx.x; i < min(kPromptTile, r.n * R - tile * kPromptTile) * D; i += kJoinThreads) {
+                const int rho = tile * kPromptTile + i / D, j = rho / R;
+                a.out[(size_t)(r.row0 + j) * a.ldo + (size_t)(h * R + rho - j * R) * D + i % D] = quiet_nan();
+            }
+        }
+    }
+}
+
 // Joins the sums of row tiles that are cut, a part of the rows at a time, and
-// then computes those of them that are marked.
+// then computes those of them that are marked.  Sums of a CTA that gave up may be
+// another call's: they spoil the row.
 template <int J, int G>
 __device__ __forceinline__ void join_pieces(const AttnCall &a, ApartShared<J> &s)
 {
@@ -1126,6 +1155,10 @@ __device__ __forceinline__ void join_pieces(const AttnCall &a, ApartShared<J> &s
     for (int x = blockIdx.x; x < a.tree_ctas * kPieceParts; x += gridDim.x) {
         const int c = x / kPieceParts, lo = (x - c * kPieceParts) * PER;
         const int4 u = __ldcg(a.cut + c);              // request, tile, kv head, last CTA
+        if (u.w == kUndone) {
+            spoil_rows(a, x - c * kPieceParts);
+            continue;
+        }
         // (uniform; what another call wrote over must not lead out of bounds)
         if (u.w < c || u.w >= a.tree_ctas || (uint32_t)u.x >= (uint32_t)a.B || (uint32_t)u.z >= (uint32_t)a.c.kv_heads) continue;
         const AttnRequest rq = attn_request<true>(a, u.x);
@@ -1141,19 +1174,25 @@ __device__ __forceinline__ void join_pieces(const AttnCall &a, ApartShared<J> &s
             for (int k0 = c; k0 <= u.w; k0 += kAhead) {
                 float2 ml[kAhead];
                 float4 t[kAhead];
+                int last[kAhead];
                 float mn = m;
 #pragma unroll
                 for (int k = 0; k < kAhead; ++k) {
                     ml[k] = make_float2(-INFINITY, 0.0f);
                     t[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    last[k] = -1;
                     if (k0 + k <= u.w) {
                         const float *from = piece_of(k0 + k);
+                        last[k] = __ldcg(&a.cut[k0 + k].w);
                         ml[k] = __ldcg(reinterpret_cast<const float2 *>(from + kPromptTile * D) + row);
                         t[k] = __ldcg(reinterpret_cast<const float4 *>(from + row * D + d));
                     }
                 }
 #pragma unroll
-                for (int k = 0; k < kAhead; ++k) mn = fmaxf(mn, ml[k].x);
+                for (int k = 0; k < kAhead; ++k) {
+                    if (last[k] == kUndone) ml[k] = make_float2(0.0f, quiet_nan());
+                    mn = fmaxf(mn, ml[k].x);
+                }
                 const float ref = mn == -INFINITY ? 0.0f : mn, fo = exp2_approx(m - ref);
                 l *= fo;
                 v.x *= fo;

@@ -65,6 +65,7 @@ struct ApartTile {
     uint32_t rows[kPromptTile / 32];
     int request, tile, uneven, unused;
 };
+constexpr int kUndone = -2;
 struct AttnCall {
     int B, T, heads, max_pages, max_query, max_len;
     gq4_kv_cache c;
@@ -90,6 +91,7 @@ struct AttnCall {
     long long n_units;
     float *pieces;     // [tree_ctas][2][kPromptTile][D + 2] sums: the rows', then the maximum and the weights' sum of each
     int4 *cut;         // [tree_ctas] the row tile that starts in the CTA and is cut: request, tile, kv head, last CTA or -1
+                       // (kUndone: the CTA gave up before it had done its share)
 };
 size_t attn_workspace_bytes(int T, int heads, int kv_heads, int D, bool masks);
 cudaError_t launch_attn(const AttnCall &call, cudaStream_t stream);
