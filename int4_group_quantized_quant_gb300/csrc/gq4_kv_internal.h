@@ -48,11 +48,13 @@ struct TreeCall {
 };
 cudaError_t launch_kv_tree(const TreeCall &call, cudaStream_t stream);
 struct AcceptCall {
-    int B, T, max_path, max_pages, n_free;   // T: of slots, -1: there are none
+    int B, max_path, max_pages, n_free;
     gq4_kv_cache c;
-    const int32_t *path, *counts, *slots, *query_start, *seq_lens, *page_table, *free_count;
+    const int32_t *path, *counts, *query_start, *seq_lens, *page_table, *free_count;
     int32_t *free_pages, *free_count_out, *seq_lens_out;
     int32_t *verdict;   // [B] of the workspace: how many rows, -1: refused
+    const int32_t *slots;   // [T] as planned
+    int T;              // -1: there are none
 };
 cudaError_t launch_kv_accept(const AcceptCall &call, cudaStream_t stream);
 cudaError_t read_tree_device_error(unsigned int *bits, bool clear);

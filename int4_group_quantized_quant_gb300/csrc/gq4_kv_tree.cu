@@ -80,6 +80,9 @@ constexpr int kMoveThreads = 128, kBookThreads = 1024;
 constexpr int kPathTile = 256;
 
 // A request's rows, and whether they can be (before its path is looked at).
+// PLANNED: with slots (a form of its own: their load, and the branch around it,
+// cost the other 0.4 us).
+template <bool PLANNED>
 struct Drafted {
     int past, n, len;
     bool none, bad;        // none: the planning refused it, all of its tokens stay
@@ -89,20 +92,21 @@ struct Drafted {
         const int q0 = __ldg(p.query_start + b), q1 = __ldg(p.query_start + b + 1);
         const long long rows = (long long)q1 - q0;
         len = __ldg(p.seq_lens + b);
-        none = plan_refused(p.slots, p.T, q0, rows);
+        none = PLANNED && plan_refused(p.slots, p.T, q0, rows);
         bad = !none && (rows < 0 || rows > len || (long long)len > ((long long)p.max_pages << shift) ||
-                        (p.T >= 0 && rows > 0 && (q0 < 0 || q1 > p.T)));
+                        (PLANNED && rows > 0 && (q0 < 0 || q1 > p.T)));
         n = none || bad ? 0 : (int)rows;
         past = len - n;
     }
 };
 
+template <bool PLANNED>
 __global__ void __launch_bounds__(kMoveThreads) accept_move_kernel(const __grid_constant__ AcceptCall p, int shift)
 {
     __shared__ int s_from[kPathTile], s_to[kPathTile];   // stretches of a page's rows: page id and row of the page
     const int b = blockIdx.x;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const Drafted r(p, b, shift);
+    const Drafted<PLANNED> r(p, b, shift);
     const int count = r.none ? 0 : __ldg(p.counts + b);
     const int32_t *path = p.path ? p.path + (size_t)b * p.max_path : nullptr;
     const int32_t *table = p.page_table + (size_t)b * p.max_pages;
@@ -164,6 +168,7 @@ __global__ void __launch_bounds__(kMoveThreads) accept_move_kernel(const __grid_
     }
 }
 
+template <bool PLANNED>
 __global__ void __launch_bounds__(kBookThreads) accept_book_kernel(const __grid_constant__ AcceptCall p, int shift)
 {
     __shared__ int s_sums[kBookThreads / 32];
@@ -175,7 +180,7 @@ __global__ void __launch_bounds__(kBookThreads) accept_book_kernel(const __grid_
         const int b = b0 + (int)threadIdx.x;
         int back = 0, had = 0;
         if (b < p.B) {
-            const Drafted r(p, b, shift);
+            const Drafted<PLANNED> r(p, b, shift);
             const int verdict = __ldcg(p.verdict + b), len = verdict < 0 ? r.len : r.past + verdict;
             had = (int)(((long long)len + (1 << shift) - 1) >> shift);
             if (verdict < 0) atomicOr(&g_tree_error, kAcceptRefused);
@@ -216,7 +221,8 @@ cudaError_t launch_kv_tree(const TreeCall &call, cudaStream_t stream)
     return cudaGetLastError();
 }
 
-cudaError_t launch_kv_accept(const AcceptCall &call, cudaStream_t stream)
+template <bool PLANNED>
+static cudaError_t launch_accept(const AcceptCall &call, cudaStream_t stream)
 {
     const int shift = log2_of(call.c.page_size);
     // few requests: their columns over several CTAs, until the GPU has one each
@@ -224,7 +230,7 @@ cudaError_t launch_kv_accept(const AcceptCall &call, cudaStream_t stream)
     int splits = 1;
     if (call.path)
         while (splits * kMoveThreads < pieces && (long long)call.B * splits < 152) ++splits;
-    accept_move_kernel<<<dim3((unsigned)call.B, (unsigned)splits), kMoveThreads, 0, stream>>>(call, shift);
+    accept_move_kernel<PLANNED><<<dim3((unsigned)call.B, (unsigned)splits), kMoveThreads, 0, stream>>>(call, shift);
     cudaError_t err = cudaGetLastError();
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
@@ -236,7 +242,12 @@ cudaError_t launch_kv_accept(const AcceptCall &call, cudaStream_t stream)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, accept_book_kernel, call, shift);
+    return cudaLaunchKernelEx(&cfg, accept_book_kernel<PLANNED>, call, shift);
+}
+
+cudaError_t launch_kv_accept(const AcceptCall &call, cudaStream_t stream)
+{
+    return call.T >= 0 ? launch_accept<true>(call, stream) : launch_accept<false>(call, stream);
 }
 
 cudaError_t read_tree_device_error(unsigned int *bits, bool clear)
