@@ -51,9 +51,9 @@
 // with ancestor bits of drafted trees (gq4_attn.cuh says what a row sees): the
 // tiles between the first tokens and the window are left out, and a tile where
 // not every row sees every key is masked by 64 bits per row.  The same three
-// chunks behind 1000 to 16000 with 64 first tokens: 473 us.  Trees: the CTAs
+// chunks behind 1000 to 16000 with 64 first tokens: 477 us.  Trees: the CTAs
 // stay and share all tiles (see kUnitStart); 32 of 26 nodes behind 500 to 4096
-// keys, one group, 138 us (29 GFLOP; a tile takes 2400 cycles, a row tile's
+// keys, one group, 140 us (29 GFLOP; a tile takes 2400 cycles, a row tile's
 // start and end 17 thousand), 4 of 64 behind 8000 to 16000, two groups, 188.
 #pragma once
 
@@ -1193,7 +1193,7 @@ __device__ __forceinline__ void row_tile(const AttnCall &a, int h)
         const uint32_t bad_at = smem_s + M::offBad;
         // Several groups: the blocks of 32 values in small loops, a word at a time.  Instructions that
         // are fetched anew hold up all roles: the trees above 205 -> 188 us (unrolled by 2: 195), the
-        // chunks 494 -> 473 (by 1: 488).  (One group, whose blocks are short: 5 to 10 % slower that way.)
+        // chunks 494 -> 477 (by 1: 488).  (One group, whose blocks are short: 5 to 10 % slower that way.)
         constexpr int kBlocks = UG == 1 ? 2 : 1;
         auto scale_of = [](const float2 (&z)[G], int u) {
             float2 x = z[0];
