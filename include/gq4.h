@@ -510,7 +510,10 @@ GQ4_API gq4_status gq4_kv_gather(int T, const gq4_kv_cache *cache, const int32_t
  * when a length is negative (taken as 0), when past + new passes
  * max_pages * page_size, when its rows end past T (query_start is then cut
  * at T), or when the free list runs out: from the first request on whose
- * pages it cannot cover, no request that needs a page gets one.
+ * pages it cannot cover, no request that needs a page gets one.  query_start
+ * counts its rows all the same: its slots tell the calls that follow (appending
+ * skips them; gq4_kv_tree_planned and gq4_kv_accept_planned take them, and
+ * attention gives its rows values that mean nothing).
  * free_count is cut to 0..n_free.  1 <= B <= GQ4_MAX_REQUESTS; T may be 0;
  * max_pages * page_size is at most 2^30 (as in gq4_kv_attention). */
 #define GQ4_MAX_REQUESTS 65536

@@ -9,7 +9,7 @@ from int4_group_quantized_quant_gb300 import inputs as I
 from tests import kv_ref as R
 from tests import mask_ref as M
 from tests.gpu_util import dev, gq4_module, host, requires_cuda
-from tests.test_gpu_trees import check_rows, inv_freq
+from tests.test_gpu_trees import Accept, check_rows, inv_freq
 
 pytestmark = [pytest.mark.gpu, requires_cuda]
 
@@ -75,6 +75,48 @@ def test_rows_out_of_the_slots(gq4):
         n = np.diff(starts)
         assert host(out).tolist() == [x if bad else x - int(m) for x, m, bad in zip(lens, n, refused)]
         assert gq4.device_error(clear=True) == (1 << 11 if any(refused) else 0) and host(left).tolist() == [0]
+
+
+@pytest.mark.parametrize("sizes,kw", [([int(n) for n in np.arange(2500) % 9], dict(KH=1)),
+                                      ([33, 7, 0, 60, 12, 5], dict(KH=8, D=128, gs=64)), ([256, 3, 250, 17], dict(KH=2))])
+@pytest.mark.parametrize("line", [False, True])
+def test_many_requests_some_refused(gq4, sizes, kw, line):
+    """Every third request without slots, of any count and path: it stays, the others are as without it."""
+    a = Accept(sizes, **kw)
+    B, starts = len(sizes), a.starts
+    lost = np.arange(B) % 3 == 1
+    slots = np.arange(100, 100 + starts[-1], dtype=np.int32)
+    for b in np.nonzero(lost)[0]:
+        slots[starts[b]:starts[b + 1]] = -1
+    # the rule on the others alone: a lost request has no rows there, and nothing is accepted of it
+    sizes_left = np.where(lost & (np.array(sizes) > 0), 0, sizes)
+    counts = np.where(sizes_left > 0, a.counts, 0)
+    path = None if line else a.path
+    lens, free, count, moves, refused = M.accept(path, counts, np.concatenate([[0], np.cumsum(sizes_left)]), a.lens, a.table,
+                                                 a.free, a.count_free, a.pages, a.page)
+    assert not refused
+    arrays, old = [x.copy() for x in a.cache.arrays()], a.cache.arrays()
+    for b, src, dst in moves:
+        (ps, s), (pd, d) = ((a.table[b, t // a.page], t % a.page) for t in (src, dst))
+        for x, o in zip(arrays, old):
+            x[pd, :, d] = o[ps, :, s]
+    given = np.where(lost & (np.array(sizes) > 0), np.arange(B) % 7 - 2, a.counts).astype(np.int32)
+    cache, free_dev = [dev(x) for x in a.cache.arrays()], dev(a.free)
+    got = gq4.kv_accept(None if line else dev(path), dev(given), dev(starts), dev(a.lens), dev(a.table), free_dev,
+                        ints(a.count_free), *cache, a.gs, slots=dev(slots))
+    torch.cuda.synchronize()
+    assert gq4.device_error(clear=True) == 0
+    assert np.array_equal(host(got[0]), lens) and host(got[1]).tolist() == [count] and np.array_equal(host(free_dev), free)
+    for x, c in zip(arrays, cache):
+        assert np.array_equal(host(c).view(np.uint32), x.view(np.uint32))
+    # and the bits of the same trees
+    parents = np.concatenate([M.random_parents(I.rng(5, b), n) for b, n in enumerate(sizes)]).astype(np.int32)
+    want_pos, want, refused = M.tree(parents, starts, a.lens, 8, 5, 9)
+    assert not refused
+    pos, tree = gq4.kv_tree(dev(parents), dev(starts), dev(a.lens), 8, window=5, sinks=9, slots=dev(slots))
+    want_pos[slots < 0], want[slots < 0] = 0, 0
+    assert np.array_equal(host(pos), want_pos) and np.array_equal(host(tree).view(np.uint32), want)
+    assert gq4.device_error() == 0
 
 
 @pytest.mark.parametrize("window,sinks", [(0, 0), (24, 4)])
